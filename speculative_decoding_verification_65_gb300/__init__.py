@@ -1,8 +1,9 @@
 """GB300-native batched speculative-sampling verification.
 
 Thin Python binding over the C ABI of ``libspecverify.so`` (declared in
-``include/spec_verify.h``, ``include/spec_sample.h`` and
-``include/spec_lmhead.h``, ``include/spec_tree.h``).  Every function here only checks and marshals
+``include/spec_verify.h``, ``include/spec_sample.h``,
+``include/spec_lmhead.h``, ``include/spec_tree.h``, ``include/spec_attn.h``
+and ``include/spec_logits.h``).  Every function here only checks and marshals
 arguments (shapes, dtypes, device pointers, the current CUDA stream) and calls
 the function of the same name in the library; all arithmetic runs in the CUDA
 kernels.  PyTorch is used for device memory and streams only.
@@ -19,6 +20,7 @@ import threading
 
 SPEC_F32 = 0
 SPEC_BF16 = 1
+SPEC_F16 = 2  # tree attention and cache commit only
 SPEC_OK = 0
 SPEC_EINVAL = 1
 SPEC_ECUDA = 2
@@ -32,6 +34,11 @@ SPEC_SAMPLE_STAGES = 3
 SPEC_FILTERED_STAGES = 6
 SPEC_LMHEAD_STAGES = 5
 SPEC_TREE_MAX_NODES = 1024
+SPEC_ATTN_MAX_NODES = 1024
+SPEC_ATTN_MAX_HEAD_DIM = 128
+SPEC_PLAN_POSITIONS, SPEC_PLAN_STATUS, SPEC_PLAN_MASK = 0, 1, 2
+SPEC_LOGITS_MAX_ROWS = 1024
+SPEC_LOGITS_MAX_BIAS = 4096
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libspecverify.so")
@@ -41,6 +48,39 @@ _lock = threading.Lock()
 
 class SpecVerifyError(RuntimeError):
     pass
+
+
+class _AttentionArgs(ctypes.Structure):
+    """spec_tree_attention_args (include/spec_attn.h)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k_new", "v_new", "k_cache", "v_cache")]
+                + [(n + "_stride", ctypes.c_int64 * 3)
+                   for n in ("q", "k_new", "v_new", "k_cache", "v_cache")]
+                + [(n, ctypes.c_void_p) for n in ("page_table", "plan", "out", "out_lse")]
+                + [("scale", ctypes.c_float)]
+                + [(n, ctypes.c_int32) for n in ("B", "N", "Hq", "Hkv", "D", "page_size",
+                                                 "pages_per_seq", "num_pages", "dtype")])
+
+
+class _CommitArgs(ctypes.Structure):
+    """spec_tree_commit_args (include/spec_attn.h)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_new", "v_new", "k_cache", "v_cache")]
+                + [(n + "_stride", ctypes.c_int64 * 4)
+                   for n in ("k_new", "v_new", "k_cache", "v_cache")]
+                + [(n, ctypes.c_void_p) for n in ("cache_len", "out_num_accepted", "out_nodes",
+                                                  "page_table", "out_len")]
+                + [(n, ctypes.c_int32) for n in ("layers", "B", "N", "Hkv", "D", "page_size",
+                                                 "pages_per_seq", "num_pages", "elem_size")])
+
+
+class _LogitsArgs(ctypes.Structure):
+    """spec_process_logits_args (include/spec_logits.h)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in (
+                    "logits", "out", "history", "history_len", "prompt_len", "draft_tokens",
+                    "parent", "n_nodes", "repetition", "frequency", "presence", "bias_tokens",
+                    "bias_values", "allowed")]
+                + [(n, ctypes.c_int64) for n in ("allowed_stride_b", "allowed_stride_r")]
+                + [(n, ctypes.c_int32) for n in ("B", "R", "V", "H", "draft_cols", "bias_cols",
+                                                 "dtype")])
 
 
 def library():
@@ -117,6 +157,20 @@ def library():
         lib.spec_verify_filtered_workspace_size.argtypes = [i32, i32, i32, i32]
         lib.spec_verify_tree.restype = i32
         lib.spec_verify_tree.argtypes = [vp] * 11 + [i32] * 4 + [vp]
+        lib.spec_tree_plan_size.restype = sz
+        lib.spec_tree_plan_size.argtypes = [i32, i32]
+        lib.spec_tree_plan_offset.restype = sz
+        lib.spec_tree_plan_offset.argtypes = [i32] * 3
+        lib.spec_tree_plan.restype = i32
+        lib.spec_tree_plan.argtypes = [vp] * 4 + [i32] * 5 + [vp, sz, vp]
+        lib.spec_tree_attention_workspace_size.restype = sz
+        lib.spec_tree_attention_workspace_size.argtypes = [i32] * 4
+        lib.spec_tree_attention.restype = i32
+        lib.spec_tree_attention.argtypes = [ctypes.POINTER(_AttentionArgs), vp, sz, vp]
+        lib.spec_tree_commit.restype = i32
+        lib.spec_tree_commit.argtypes = [ctypes.POINTER(_CommitArgs), vp]
+        lib.spec_process_logits.restype = i32
+        lib.spec_process_logits.argtypes = [ctypes.POINTER(_LogitsArgs), vp]
         _lib = lib
         return lib
 
@@ -896,3 +950,360 @@ def tree_to_device(tc, device="cuda"):
                 u_accept=torch.from_numpy(tc.u_accept).to(device),
                 u_resample=torch.from_numpy(tc.u_resample).to(device),
                 temperature=torch.from_numpy(tc.temperature).to(device))
+
+
+# ------------------------------------------- tree attention and cache commit
+
+def _call_stream(stream, dev, tensors):
+    """The stream a call runs on.  Where that is not the current one, the
+    tensors' memory is kept from reuse until the stream has passed the call."""
+    torch = _torch()
+    current = torch.cuda.current_stream(dev)
+    if stream is None or stream.cuda_stream == current.cuda_stream:
+        return current
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return stream
+
+
+def _empty_on(s, shape, dtype, dev):
+    """An output allocated for use on stream `s`."""
+    torch = _torch()
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _int32(name, t, shape, dev):
+    torch = _torch()
+    if tuple(t.shape) != shape or t.dtype != torch.int32:
+        raise ValueError(f"{name} must be int32 {shape}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous() or t.device != dev:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
+
+
+def _head_strides(name, t, dev, step):
+    """The strides of all dimensions but the last, which must be contiguous;
+    each a multiple of `step` elements (a dimension of one entry has none)."""
+    if not t.is_cuda or t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    out = tuple(0 if n == 1 else s for n, s in zip(t.shape[:-1], st))
+    if step > 1 and (any(s % step for s in out) or t.data_ptr() % (2 * step)):
+        raise ValueError(f"{name}: strides must be multiples of {step} elements and the data "
+                         f"{2 * step}-byte aligned")
+    return out
+
+
+def _geometry(k_cache, page_table, B, dev):
+    """(page_size, pages_per_seq, num_pages) of a cache [.., pages, slots, heads, D]."""
+    P, S = k_cache.shape[-4], k_cache.shape[-3]
+    if page_table is None:
+        if P < B:
+            raise ValueError(f"a contiguous cache needs a page for each of {B} sequences, got {P}")
+        return S, 1, P
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, pages_per_seq]")
+    M = page_table.shape[1]
+    _int32("page_table", page_table, (B, M), dev)
+    return S, M, P
+
+
+class TreePlan:
+    """What spec_tree_plan made: `positions` int32 [B, N], `status` int32 [B] and
+    `mask` int32 [B, N, W] (bits of ancestors, include/spec_attn.h) are views
+    of `data`, which every layer's spec_tree_attention reads."""
+
+    def __init__(self, B, N, geometry, data):
+        torch = _torch()
+        self.B, self.N, self.geometry, self.data = B, N, geometry, data
+        lib, W = library(), 4 * ((N + 127) // 128)
+
+        def part(which, *shape):
+            at = lib.spec_tree_plan_offset(B, N, which)
+            n = 4
+            for x in shape:
+                n *= x
+            return data[at:at + n].view(torch.int32).view(*shape)
+        self.positions = part(SPEC_PLAN_POSITIONS, B, N)
+        self.status = part(SPEC_PLAN_STATUS, B)
+        self.mask = part(SPEC_PLAN_MASK, B, N, W)
+
+
+def spec_tree_plan(parent, n_nodes, cache_len, k_cache, page_table=None, plan=None, stream=None):
+    """The plan of a step (include/spec_attn.h): ancestors, positions and schedule of
+    B trees of up to N nodes over their caches, made once for all layers.
+
+    parent int32 [B, N] (a chain: parent[n] = n - 1); n_nodes, cache_len int32
+    [B]; k_cache [pages, slots, Hkv, D], one layer's cache, asked for its
+    geometry only; page_table int32 [B, pages_per_seq], or None for a
+    contiguous cache (sequence b owns page b).  `plan` refills a TreePlan of
+    the same sizes.  Returns a TreePlan; asynchronous like any CUDA op."""
+    torch = _torch()
+    if parent.dim() != 2 or k_cache.dim() != 4:
+        raise ValueError("parent must be [B, N] and k_cache [pages, slots, Hkv, D]")
+    B, N = parent.shape
+    dev = parent.device
+    _int32("parent", parent, (B, N), dev)
+    _int32("n_nodes", n_nodes, (B,), dev)
+    _int32("cache_len", cache_len, (B,), dev)
+    geometry = _geometry(k_cache, page_table, B, dev)
+    lib = library()
+    need = lib.spec_tree_plan_size(B, N)
+    if need == 0:
+        raise ValueError(f"sizes out of range: B={B} N={N}")
+    s = _call_stream(stream, dev, (parent, n_nodes, cache_len, page_table,
+                                   plan.data if plan is not None else None))
+    if plan is None:
+        plan = TreePlan(B, N, geometry, _empty_on(s, (need,), torch.uint8, dev))
+    elif (plan.B, plan.N) != (B, N) or plan.data.device != dev:
+        raise ValueError(f"plan is for B={plan.B} N={plan.N} on {plan.data.device}")
+    plan.geometry = geometry
+    with _on(dev):
+        rc = lib.spec_tree_plan(_ptr(parent), _ptr(n_nodes), _ptr(cache_len), _ptr(page_table),
+                                B, N, *geometry, _ptr(plan.data), need,
+                                ctypes.c_void_p(s.cuda_stream))
+    _check(rc, "spec_tree_plan")
+    return plan
+
+
+def spec_tree_attention_workspace_size(N: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(library().spec_tree_attention_workspace_size(N, Hq, Hkv, D))
+
+
+_attention_ws = {}
+
+
+def attention_workspace(N: int, Hq: int, Hkv: int, D: int, device=None, stream=None):
+    """A zeroed workspace for spec_tree_attention, cached per (device, stream)
+    and apart from spec_verify's.  While the stream is being captured into a
+    graph it is a new one, in the graph's own memory: a replay may overlap
+    later calls on the stream."""
+    torch = _torch()
+    device = torch.device(device if device is not None else "cuda")
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    need = spec_tree_attention_workspace_size(N, Hq, Hkv, D)
+    if need == 0:
+        raise ValueError(f"sizes out of range: N={N} Hq={Hq} Hkv={Hkv} D={D}")
+    key = (device.index, s.cuda_stream)
+    ws = _attention_ws.get(key)
+    with torch.cuda.stream(s):
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros(need, dtype=torch.uint8, device=device)
+        if ws is None or ws.numel() < need:
+            ws = _attention_ws[key] = torch.zeros(need, dtype=torch.uint8, device=device)
+    return ws
+
+
+def spec_tree_attention(q, k_new, v_new, k_cache, v_cache, plan, page_table=None, scale=None,
+                        out=None, want_lse=False, ws=None, stream=None):
+    """Attention of B trees of drafted tokens over a cache (include/spec_attn.h).
+
+    q [B, N, Hq, D]; k_new, v_new [B, N, Hkv, D]: the new tokens' keys and
+    values; k_cache, v_cache [pages, slots, Hkv, D], bfloat16 or float16, any
+    strides with a contiguous last dimension; plan from spec_tree_plan;
+    page_table int32 [B, pages_per_seq] or None; scale 1 / sqrt(D) by default.
+    Returns out [B, N, Hq, D] and, with want_lse, the rows' log-sum-exp
+    float32 [B, N, Hq]; asynchronous like any CUDA op."""
+    torch = _torch()
+    if any(t.dim() != 4 for t in (q, k_new, v_new, k_cache, v_cache)):
+        raise ValueError("q, k_new, v_new, k_cache and v_cache must have 4 dimensions")
+    B, N, Hq, D = q.shape
+    Hkv = k_new.shape[2]
+    P, S = k_cache.shape[:2]
+    if tuple(k_new.shape) != (B, N, Hkv, D) or v_new.shape != k_new.shape:
+        raise ValueError(f"k_new and v_new must be {(B, N, Hkv, D)}")
+    if tuple(k_cache.shape) != (P, S, Hkv, D) or v_cache.shape != k_cache.shape:
+        raise ValueError(f"k_cache and v_cache must be [pages, slots, {Hkv}, {D}]")
+    if q.dtype == torch.bfloat16:
+        dt = SPEC_BF16
+    elif q.dtype == torch.float16:
+        dt = SPEC_F16
+    else:
+        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
+    if any(t.dtype != q.dtype for t in (k_new, v_new, k_cache, v_cache)):
+        raise TypeError("q, k_new, v_new, k_cache and v_cache must share a dtype")
+    dev = q.device
+    geometry = _geometry(k_cache, page_table, B, dev)
+    if (plan.B, plan.N) != (B, N) or plan.geometry != geometry or plan.data.device != dev:
+        raise ValueError(f"plan is for B={plan.B} N={plan.N}, cache {plan.geometry} on "
+                         f"{plan.data.device}; the call is for B={B} N={N}, {geometry} on {dev}")
+    a = _AttentionArgs()
+    for name, t in (("q", q), ("k_new", k_new), ("v_new", v_new), ("k_cache", k_cache),
+                    ("v_cache", v_cache)):
+        getattr(a, name + "_stride")[:] = _head_strides(name, t, dev, 8)
+        setattr(a, name, t.data_ptr())
+    scale = D ** -0.5 if scale is None else float(scale)
+    if not 0.0 < scale < float("inf"):
+        raise ValueError(f"scale must be finite and positive, got {scale}")
+    if page_table is not None and S % 128 and (S < 8 or S & (S - 1)):
+        raise ValueError(f"page size {S}: a multiple of 128, or a power of two from 8")
+    s = _call_stream(stream, dev, (q, k_new, v_new, k_cache, v_cache, plan.data, page_table, out))
+    if out is None:
+        out = _empty_on(s, (B, N, Hq, D), q.dtype, dev)
+    _dev_out("out", out, (B, N, Hq, D), q.dtype, dev)
+    lse = _empty_on(s, (B, N, Hq), torch.float32, dev) if want_lse else None
+    if ws is None:
+        ws = attention_workspace(N, Hq, Hkv, D, dev, s)
+    _check_ws(ws, dev)
+    a.page_table = page_table.data_ptr() if page_table is not None else None
+    a.plan, a.out = plan.data.data_ptr(), out.data_ptr()
+    a.out_lse = lse.data_ptr() if want_lse else None
+    a.scale, a.B, a.N, a.Hq, a.Hkv, a.D, a.dtype = scale, B, N, Hq, Hkv, D, dt
+    a.page_size, a.pages_per_seq, a.num_pages = geometry
+    with _on(dev):
+        rc = library().spec_tree_attention(ctypes.byref(a), _ptr(ws), ws.numel(),
+                                           ctypes.c_void_p(s.cuda_stream))
+    _check(rc, "spec_tree_attention")
+    return (out, lse) if want_lse else out
+
+
+def spec_tree_commit(k_new, v_new, k_cache, v_cache, cache_len, out_num_accepted, out_nodes=None,
+                     page_table=None, out_len=None, stream=None):
+    """Append the accepted path's keys and values to the cache
+    (include/spec_attn.h), after spec_verify_tree (out_nodes: its path) or
+    spec_verify (out_nodes None: a chain).
+
+    k_new, v_new [B, N, Hkv, D] with caches [pages, slots, Hkv, D], or with a
+    leading dimension of layers; bfloat16, float16 or float32, any strides
+    with a contiguous last dimension.  Returns the new cache_len int32 [B]
+    (-1 for a sequence error, whose cache is left alone)."""
+    torch = _torch()
+    if k_new.dim() not in (4, 5) or k_cache.dim() != k_new.dim():
+        raise ValueError("k_new [.., B, N, Hkv, D] and k_cache [.., pages, slots, Hkv, D] expected")
+    *lead, B, N, Hkv, D = k_new.shape
+    P, S = k_cache.shape[-4:-2]
+    if v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must have one shape")
+    if tuple(k_cache.shape) != (*lead, P, S, Hkv, D) or v_cache.shape != k_cache.shape:
+        raise ValueError(f"k_cache and v_cache must be {(*lead, 'pages', 'slots', Hkv, D)}")
+    if k_new.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+        raise TypeError(f"k_new must be bfloat16, float16 or float32, got {k_new.dtype}")
+    if any(t.dtype != k_new.dtype for t in (v_new, k_cache, v_cache)):
+        raise TypeError("k_new, v_new, k_cache and v_cache must share a dtype")
+    dev = k_new.device
+    _int32("cache_len", cache_len, (B,), dev)
+    _int32("out_num_accepted", out_num_accepted, (B,), dev)
+    if out_nodes is not None:
+        _int32("out_nodes", out_nodes, (B, N), dev)
+    geometry = _geometry(k_cache, page_table, B, dev)
+    a = _CommitArgs()
+    for name, t in (("k_new", k_new), ("v_new", v_new), ("k_cache", k_cache),
+                    ("v_cache", v_cache)):
+        st = _head_strides(name, t, dev, 1)
+        getattr(a, name + "_stride")[:] = st if lead else (0, *st)
+        setattr(a, name, t.data_ptr())
+    s = _call_stream(stream, dev, (k_new, v_new, k_cache, v_cache, cache_len, out_num_accepted,
+                                   out_nodes, page_table, out_len))
+    if out_len is None:
+        out_len = _empty_on(s, (B,), torch.int32, dev)
+    _dev_out("out_len", out_len, (B,), torch.int32, dev)
+    if B > 0 and out_len.data_ptr() == cache_len.data_ptr():
+        raise ValueError("out_len must not be cache_len itself")
+    a.cache_len, a.out_num_accepted = cache_len.data_ptr(), out_num_accepted.data_ptr()
+    a.out_nodes = out_nodes.data_ptr() if out_nodes is not None else None
+    a.page_table = page_table.data_ptr() if page_table is not None else None
+    a.out_len = out_len.data_ptr()
+    a.layers, a.B, a.N, a.Hkv, a.D = lead[0] if lead else 1, B, N, Hkv, D
+    a.page_size, a.pages_per_seq, a.num_pages = geometry
+    a.elem_size = k_new.element_size()
+    with _on(dev):
+        rc = library().spec_tree_commit(ctypes.byref(a), ctypes.c_void_p(s.cuda_stream))
+    _check(rc, "spec_tree_commit")
+    return out_len
+
+
+# --------------------------------------------------------- logits processing
+
+def spec_process_logits(logits, history=None, history_len=None, prompt_len=None,
+                        draft_tokens=None, parent=None, n_nodes=None, repetition=None,
+                        frequency=None, presence=None, bias_tokens=None, bias_values=None,
+                        allowed=None, out=None, stream=None):
+    """Penalties for repeated tokens, biases and grammar masks on the rows that a
+    verification reads next (include/spec_logits.h states the formula).
+
+    logits [B, R, V] float32 or bfloat16; history int32 [B, H] with
+    history_len and prompt_len int32 [B]; draft_tokens int32 [B, R - 1] or
+    [B, R] (chain: row r follows the first r of them), or with parent int32
+    [B, R] the tokens of a tree's nodes; n_nodes int32 [B]: rows past it are
+    left alone; repetition, frequency, presence float32 [B]; bias_tokens int32
+    and bias_values float32 [B, M] (token -1: unused); allowed int32 words
+    [B, R, ceil(V / 32)] (or [B, 1, ..], [1, 1, ..]), bit x % 32 of word
+    x / 32 for token x.  Anything may be None.  `out` may be logits itself.
+    Returns out; asynchronous like any CUDA op."""
+    torch = _torch()
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B, R, V]")
+    B, R, V = logits.shape
+    dt = _dtype_code(logits)
+    dev = logits.device
+    if not logits.is_cuda or not logits.is_contiguous():
+        raise ValueError("logits must be a contiguous CUDA tensor")
+    a = _LogitsArgs()
+    if history is not None:
+        if history.dim() != 2 or history_len is None or prompt_len is None:
+            raise ValueError("history [B, H] comes with history_len and prompt_len [B]")
+        _int32("history", history, (B, history.shape[1]), dev)
+        _int32("history_len", history_len, (B,), dev)
+        _int32("prompt_len", prompt_len, (B,), dev)
+        a.H = history.shape[1]
+        a.history, a.history_len = history.data_ptr(), history_len.data_ptr()
+        a.prompt_len = prompt_len.data_ptr()
+    elif history_len is not None or prompt_len is not None:
+        raise ValueError("history_len and prompt_len come with history")
+    if draft_tokens is not None:
+        cols = draft_tokens.shape[1] if draft_tokens.dim() == 2 else -1
+        if parent is not None and cols != R or parent is None and cols not in (R - 1, R):
+            raise ValueError(f"draft_tokens must be [B, {R}]" +
+                             ("" if parent is not None else f" or [B, {R - 1}]"))
+        _int32("draft_tokens", draft_tokens, (B, cols), dev)
+        a.draft_tokens, a.draft_cols = draft_tokens.data_ptr(), cols
+    if parent is not None:
+        if draft_tokens is None:
+            raise ValueError("parent comes with draft_tokens")
+        _int32("parent", parent, (B, R), dev)
+        a.parent = parent.data_ptr()
+    if n_nodes is not None:
+        _int32("n_nodes", n_nodes, (B,), dev)
+        a.n_nodes = n_nodes.data_ptr()
+    for name, t in (("repetition", repetition), ("frequency", frequency),
+                    ("presence", presence)):
+        if t is not None:
+            _dev_out(name, t, (B,), torch.float32, dev)
+            setattr(a, name, t.data_ptr())
+    if (bias_tokens is None) != (bias_values is None):
+        raise ValueError("bias_tokens and bias_values come together")
+    if bias_tokens is not None:
+        if bias_tokens.dim() != 2 or bias_tokens.shape[1] > SPEC_LOGITS_MAX_BIAS:
+            raise ValueError(f"bias_tokens must be [B, M], M <= {SPEC_LOGITS_MAX_BIAS}")
+        shape = (B, bias_tokens.shape[1])
+        _int32("bias_tokens", bias_tokens, shape, dev)
+        _dev_out("bias_values", bias_values, shape, torch.float32, dev)
+        a.bias_tokens, a.bias_values = bias_tokens.data_ptr(), bias_values.data_ptr()
+        a.bias_cols = shape[1]
+    if allowed is not None:
+        W = (V + 31) // 32
+        if (allowed.dim() != 3 or allowed.shape[0] not in (1, B) or allowed.shape[1] not in (1, R)
+                or allowed.shape[2] != W or allowed.dtype != torch.int32 or not allowed.is_cuda
+                or allowed.device != dev or allowed.stride(2) != 1 and W > 1):
+            raise ValueError(f"allowed must be int32 [{B} or 1, {R} or 1, {W}] on {dev}, its last "
+                             "dimension contiguous")
+        a.allowed = allowed.data_ptr()
+        a.allowed_stride_b = allowed.stride(0) if allowed.shape[0] > 1 else 0
+        a.allowed_stride_r = allowed.stride(1) if allowed.shape[1] > 1 else 0
+    s = _call_stream(stream, dev, (logits, history, history_len, prompt_len, draft_tokens, parent,
+                                   n_nodes, repetition, frequency, presence, bias_tokens,
+                                   bias_values, allowed, out))
+    if out is None:
+        out = _empty_on(s, (B, R, V), logits.dtype, dev)
+    _dev_out("out", out, (B, R, V), logits.dtype, dev)
+    a.logits, a.out = logits.data_ptr(), out.data_ptr()
+    a.B, a.R, a.V, a.dtype = B, R, V, dt
+    with _on(dev):
+        rc = library().spec_process_logits(ctypes.byref(a), ctypes.c_void_p(s.cuda_stream))
+    _check(rc, "spec_process_logits")
+    return out

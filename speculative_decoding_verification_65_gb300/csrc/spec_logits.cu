@@ -1,0 +1,361 @@
+// spec_logits.cu -- penalties for repeated tokens, biases and grammar masks on
+// logits (include/spec_logits.h): one pass that reads each row once and
+// writes it once.
+//
+// A CTA owns one tile of the vocabulary for (some of) the rows of one
+// sequence.  It first counts, in shared memory, the tokens of the sequence's
+// history that fall in its tile (integer adds: any order gives the same
+// count), marks the drafted ones and sums the biases, and keeps one bit per
+// column that any of these touched.  The history is read once per tile from
+// L2, which costs H * 4 bytes against the tile's 2 * R * C * size from HBM, so
+// no table of V counters per sequence has to exist between calls.  Then the
+// rows stream through: a 16-byte vector whose touched bits are 0 and whose
+// mask bits are 1 is stored as it was loaded, and only touched elements take
+// the penalty arithmetic.  A drafted token's own count differs from row to
+// row; it is found by walking the row's path, for columns marked as drafted.
+//
+// Bound by HBM: 2 * V * size bytes a row.  Rows start anywhere (V odd):
+// vectors are the array's 16-byte ones, as in the other kernels, and the
+// elements of a vector that reach over the tile's ends are moved one by one.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <limits.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "spec_logits.h"
+#include "spec_verify.h"
+#include "device_common.cuh"
+
+namespace {
+
+using namespace spec_dev;
+
+constexpr int LTH = 256;      // threads per CTA
+constexpr int LUN = 4;        // vectors in flight per thread
+constexpr uint32_t IN_PROMPT = 0x80000000u;  // flags of a column's word; the rest is its count
+constexpr uint32_t DRAFTED = 0x40000000u;    // in the generated part of the history
+constexpr uint32_t COUNT = 0x3fffffffu;
+
+struct LParams {
+    spec_process_logits_args a;
+    int C;             // columns per tile, a multiple of 32
+    int rows_per_cta;
+};
+
+// shared memory: count words [C] | touched bits [C / 32 + 1] | bias [C] (when
+// there are biases) | drafted tokens [R] | parents [R] (tree)
+struct LSmem {
+    uint32_t *cnt, *touched;
+    float *bias;
+    int *tok, *par;
+};
+
+// bits [c, c + 32) of a bit array; the words past `words` read as 0
+__device__ __forceinline__ uint32_t bits_from(const uint32_t *w, int c)
+{
+    return __funnelshift_r(w[c >> 5], w[(c >> 5) + 1], c & 31);
+}
+
+// bits [c, c + n) of a mask in global memory whose last word is `last`
+__device__ __forceinline__ uint32_t mask_from(const uint32_t *w, int c, int n, int last)
+{
+    const int i = c >> 5, s = c & 31;
+    const uint32_t lo = __ldg(w + i);
+    const uint32_t hi = (s + n > 32 && i < last) ? __ldg(w + i + 1) : 0u;
+    return __funnelshift_r(lo, hi, s);
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t round_bits(float y)
+{
+    if (DT == SPEC_F32)
+        return __float_as_uint(y);
+    return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y));
+}
+
+struct Penalty {
+    float rep, freq, pres;
+};
+
+// the value of one touched logit x in row r at column c of the tile
+__device__ float touched_value(const spec_process_logits_args &A, const LSmem &S, int t0, int c,
+                               int r, float x, const Penalty &pen)
+{
+    const uint32_t w = S.cnt[c];
+    int n = (int)(w & COUNT);
+    if (w & DRAFTED) {
+        const int token = t0 + c;
+        if (A.parent) {
+            for (int i = r; i > 0; i = S.par[i])
+                n += S.tok[i] == token;
+        } else {
+            for (int i = 0; i < r; ++i)
+                n += S.tok[i] == token;
+        }
+    }
+    if (n > 0 || (w & IN_PROMPT))
+        x = x > 0.0f ? x / pen.rep : x * pen.rep;
+    if (n > 0) {
+        x -= pen.freq * (float)n;
+        x -= pen.pres;
+    }
+    if (S.bias)
+        x += S.bias[c];
+    return x;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(LTH) logits_kernel(const LParams P)
+{
+    using L = Lg<DT>;
+    extern __shared__ uint32_t lsm[];
+    const spec_process_logits_args &A = P.a;
+    const int tid = (int)threadIdx.x;
+    const int b = (int)blockIdx.y;
+    const int t0 = (int)blockIdx.x * P.C;
+    const int cols = min(P.C, A.V - t0);
+    LSmem S;
+    S.cnt = lsm;
+    S.touched = S.cnt + P.C;
+    float *fb = reinterpret_cast<float *>(S.touched + P.C / 32 + 1);
+    S.bias = A.bias_cols > 0 ? fb : nullptr;
+    S.tok = reinterpret_cast<int *>(fb + (A.bias_cols > 0 ? P.C : 0));
+    S.par = S.tok + A.R;
+
+    wait_previous_kernel();
+    for (int i = tid; i < P.C + P.C / 32 + 1; i += LTH)
+        lsm[i] = 0;
+    if (S.bias)
+        for (int i = tid; i < P.C; i += LTH)
+            S.bias[i] = 0.0f;
+
+    Penalty pen;
+    pen.rep = A.repetition ? A.repetition[b] : 1.0f;
+    pen.freq = A.frequency ? A.frequency[b] : 0.0f;
+    pen.pres = A.presence ? A.presence[b] : 0.0f;
+    const int hl = A.H > 0 ? A.history_len[b] : 0;
+    const int pl = A.H > 0 ? A.prompt_len[b] : 0;
+    int nn = A.n_nodes ? A.n_nodes[b] : A.R;
+    bool bad = !(pen.rep > 0.0f) || isinf(pen.rep) || !isfinite(pen.freq) ||
+               !isfinite(pen.pres) || pl < 0 || hl < pl || hl > A.H || nn < 1 || nn > A.R;
+    if (nn < 1 || nn > A.R)
+        nn = A.R;
+    __syncthreads();
+
+    // the history's tokens of this tile
+    if (!bad) {
+        const int32_t *hist = A.history + (size_t)b * A.H;
+        for (int i = tid; i < hl; i += LTH) {
+            const int t = __ldg(hist + i);
+            bad |= t < 0 || t >= A.V;
+            const int c = t - t0;
+            if (c >= 0 && c < cols) {
+                if (i < pl)
+                    atomicOr(&S.cnt[c], IN_PROMPT);
+                else
+                    atomicAdd(&S.cnt[c], 1u);
+                atomicOr(&S.touched[c >> 5], 1u << (c & 31));
+            }
+        }
+        // drafted tokens: a chain's token i follows row i, a tree's belongs to node i
+        const int first = A.parent ? 1 : 0;
+        const int last = A.parent ? nn : min(nn - 1, A.draft_cols);
+        if (A.draft_cols > 0)
+            for (int i = first + tid; i < last; i += LTH) {
+                const int t = A.draft_tokens[(size_t)b * A.draft_cols + i];
+                bad |= t < 0 || t >= A.V;
+                S.tok[i] = t;
+                if (A.parent) {
+                    const int p = A.parent[(size_t)b * A.R + i];
+                    bad |= p < 0 || p >= i;
+                    S.par[i] = p;
+                }
+                const int c = t - t0;
+                if (c >= 0 && c < cols) {
+                    atomicOr(&S.cnt[c], DRAFTED);
+                    atomicOr(&S.touched[c >> 5], 1u << (c & 31));
+                }
+            }
+        // biases: the first entry of a token sums all of its entries in order
+        const int32_t *bt = A.bias_tokens + (size_t)b * A.bias_cols;
+        const float *bv = A.bias_values + (size_t)b * A.bias_cols;
+        for (int i = tid; i < A.bias_cols; i += LTH) {
+            const int t = bt[i];
+            bad |= t < -1 || t >= A.V;
+            const int c = t - t0;
+            if (t < 0 || c < 0 || c >= cols)
+                continue;
+            bool first_of = true;
+            for (int j = 0; j < i && first_of; ++j)
+                first_of = bt[j] != t;
+            if (!first_of)
+                continue;
+            float sum = bv[i];
+            for (int j = i + 1; j < A.bias_cols; ++j)
+                if (bt[j] == t)
+                    sum += bv[j];
+            S.bias[c] = sum;
+            atomicOr(&S.touched[c >> 5], 1u << (c & 31));
+        }
+    }
+    bad = __syncthreads_or(bad ? 1 : 0) != 0;
+
+    const int r0 = (int)blockIdx.z * P.rows_per_cta;
+    const int rows = min(nn, r0 + P.rows_per_cta) - r0;
+    if (rows <= 0)
+        return;
+    const int last_word = (A.V - 1) >> 5;
+    const int NV = P.C / L::VEC + 1;  // vectors a row can have, its ends included
+    const int total = rows * NV;
+    for (int i0 = tid; i0 < total; i0 += LUN * LTH) {
+        uint4 raw[LUN];
+        size_t e0[LUN];  // the vector's first element in the array
+        int col[LUN];    // its column in the tile (negative: it starts before the tile)
+        int row[LUN];    // -1: no vector
+#pragma unroll
+        for (int u = 0; u < LUN; ++u) {
+            const int i = i0 + u * LTH;
+            const int rr = i / NV, v = i - rr * NV;
+            const size_t off = ((size_t)b * A.R + (r0 + rr)) * A.V + t0;
+            const int mis = (int)(off % L::VEC);
+            row[u] = (i < total && v * L::VEC - mis < cols) ? r0 + rr : -1;
+            col[u] = v * L::VEC - mis;
+            e0[u] = off - mis + (size_t)v * L::VEC;
+            if (row[u] >= 0) {
+                if (col[u] >= 0 && col[u] + L::VEC <= cols) {
+                    raw[u] = __ldcs(reinterpret_cast<const uint4 *>(A.logits) + e0[u] / L::VEC);
+                } else {
+                    raw[u] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int j = 0; j < L::VEC; ++j)
+                        if (col[u] + j >= 0 && col[u] + j < cols) {
+                            if (DT == SPEC_F32)
+                                L::put(raw[u], j, reinterpret_cast<const uint32_t *>(A.logits)[e0[u] + j]);
+                            else
+                                L::put(raw[u], j, reinterpret_cast<const unsigned short *>(A.logits)[e0[u] + j]);
+                        }
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < LUN; ++u) {
+            if (row[u] < 0)
+                continue;
+            const int c = col[u], lo = max(c, 0), skip = lo - c;  // skip: elements before the tile
+            constexpr uint32_t ALL = (1u << L::VEC) - 1u;
+            const int n = min(cols - lo, L::VEC - skip);
+            const uint32_t have = ((n >= 32 ? 0u : (1u << n)) - 1u) << skip;
+            if (bad) {
+                raw[u] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+            } else {
+                uint32_t t = (bits_from(S.touched, lo) << skip) & have;
+                uint32_t ok = ALL;
+                if (A.allowed) {
+                    const uint32_t *m = A.allowed + b * A.allowed_stride_b +
+                                        row[u] * A.allowed_stride_r;
+                    ok = (mask_from(m, t0 + lo, n, last_word) << skip) & have;
+                    t &= ok;
+                }
+                while (t) {
+                    const int j = __ffs((int)t) - 1;
+                    t &= t - 1;
+                    const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+                    float x;
+                    if (DT == SPEC_F32) {
+                        x = __uint_as_float(j == 0 ? w[0] : j == 1 ? w[1] : j == 2 ? w[2] : w[3]);
+                    } else {
+                        const int h = j >> 1;
+                        const uint32_t word = h == 0 ? w[0] : h == 1 ? w[1] : h == 2 ? w[2] : w[3];
+                        x = __uint_as_float((j & 1) ? (word & 0xffff0000u) : (word << 16));
+                    }
+                    x = touched_value(A, S, t0, c + j, row[u], x, pen);
+                    L::put(raw[u], j, round_bits<DT>(x));
+                }
+                if (ok != ALL) {
+#pragma unroll
+                    for (int j = 0; j < L::VEC; ++j)
+                        if (!((ok >> j) & 1u))
+                            L::put(raw[u], j, L::NEG_INF_WORD & (L::ES == 4 ? 0xffffffffu : 0xffffu));
+                }
+            }
+            if (have == ALL) {
+                reinterpret_cast<uint4 *>(A.out)[e0[u] / L::VEC] = raw[u];
+            } else {
+                const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+#pragma unroll
+                for (int j = 0; j < L::VEC; ++j)
+                    if ((have >> j) & 1u) {
+                        if (DT == SPEC_F32)
+                            reinterpret_cast<uint32_t *>(A.out)[e0[u] + j] = w[j & 3];
+                        else
+                            reinterpret_cast<unsigned short *>(A.out)[e0[u] + j] =
+                                (unsigned short)(w[(j >> 1) & 3] >> ((j & 1) * 16));
+                    }
+            }
+        }
+    }
+}
+
+bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+size_t smem_bytes(const spec_process_logits_args &a, int C)
+{
+    return 4 * ((size_t)C + C / 32 + 1 + (a.bias_cols > 0 ? C : 0) + 2 * (size_t)a.R);
+}
+
+}  // namespace
+
+extern "C" int32_t spec_process_logits(const spec_process_logits_args *args, void *stream)
+{
+    if (!args)
+        return SPEC_EINVAL;
+    const spec_process_logits_args &a = *args;
+    if (a.B < 0 || a.B > 65535 || a.R < 1 || a.R > SPEC_LOGITS_MAX_ROWS || a.V < 2 ||
+        a.V > SPEC_MAX_V || a.H < 0 || a.H > (1 << 24) || a.bias_cols < 0 ||
+        a.bias_cols > SPEC_LOGITS_MAX_BIAS || (a.dtype != SPEC_F32 && a.dtype != SPEC_BF16) ||
+        a.allowed_stride_b < 0 || a.allowed_stride_r < 0)
+        return SPEC_EINVAL;
+    if (a.B == 0)
+        return SPEC_OK;
+    if (!a.logits || !a.out || !aligned(a.logits, 16) || !aligned(a.out, 16))
+        return SPEC_EINVAL;
+    const void *words[] = {a.history, a.history_len, a.prompt_len, a.draft_tokens, a.parent,
+                           a.n_nodes, a.repetition, a.frequency, a.presence, a.bias_tokens,
+                           a.bias_values, a.allowed};
+    for (const void *p : words)
+        if (!aligned(p, 4))
+            return SPEC_EINVAL;
+    if ((a.H > 0 && (!a.history || !a.history_len || !a.prompt_len)) ||
+        (a.bias_cols > 0 && (!a.bias_tokens || !a.bias_values)))
+        return SPEC_EINVAL;
+    if (a.parent ? (a.draft_cols != a.R)
+                 : (a.draft_cols != 0 && a.draft_cols != a.R && a.draft_cols != a.R - 1))
+        return SPEC_EINVAL;
+    if (a.draft_cols > 0 && !a.draft_tokens)
+        return SPEC_EINVAL;
+
+    LParams P;
+    P.a = a;
+    P.C = 4096;
+    auto tiles = [&] { return (long long)a.B * ((a.V + P.C - 1) / P.C); };
+    while (P.C > 1024 && tiles() < 304)
+        P.C /= 2;
+    int splits = 1;
+    while (tiles() * splits < 304 && splits < a.R)
+        splits *= 2;
+    P.rows_per_cta = (a.R + splits - 1) / splits;
+    const size_t smem = smem_bytes(a, P.C);  // at most 41 KB: no opt-in needed
+    const dim3 grid((unsigned int)((a.V + P.C - 1) / P.C), (unsigned int)a.B,
+                    (unsigned int)((a.R + P.rows_per_cta - 1) / P.rows_per_cta));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (a.dtype == SPEC_F32)
+        logits_kernel<SPEC_F32><<<grid, LTH, smem, st>>>(P);
+    else
+        logits_kernel<SPEC_BF16><<<grid, LTH, smem, st>>>(P);
+    if (cudaPeekAtLastError() != cudaSuccess) {
+        (void)cudaGetLastError();
+        return SPEC_ECUDA;
+    }
+    return SPEC_OK;
+}
