@@ -1,15 +1,62 @@
-// spec_attn.cu -- tree attention over a key/value cache (include/spec_attn.h).
+// spec_attn.cu -- tree attention over a key/value cache on the tcgen05 tensor
+// cores (include/spec_attn.h).
 //
-// One CTA of 128 threads per (tree node, query head).  Keys go by in tiles of
-// 128, one per thread: the thread's score, the tile's maximum and the running
-// (maximum, sum, weighted sum) of the softmax; then thread d adds the tile's
-// weighted values of element d.
+// For one sequence and one key/value head all query rows that share the head
+// (every node of the tree times the Hq / Hkv heads of the group) form the
+// rows of a tile of 128: S = Q K^T over 128 keys at a time, a running softmax
+// per row, O += P V.  Keys and values are then read once for all rows, which
+// is what bounds the kernel: D * 4 bytes per key and head from HBM against
+// 4 * D * 128 operations at any number of rows up to 128.  A tile of 64 KB
+// takes an SM's share of the HBM rate about 2850 clocks, its two products
+// about 1030 and its exponentials 512, so up to 128 rows the products' cost is
+// covered whatever part of the rows is in use, and single tokens use the same
+// kernel.  More rows are several row tiles (whole nodes each); the CTAs of
+// one key range run next to each other, so the second one finds the keys in L2.
+//
+// Roles in a CTA (one per SM, 10 warps):
+//   warps 0-3, 4-7  two softmax groups, one thread per row.  Group s takes the
+//                   tiles of its parity with scores, weights and sums of its
+//                   own (S_s, O_s in TMEM), so that one group's exponentials
+//                   run under the other's products.  The weights go back to
+//                   TMEM in the place of the scores, as the A operand of P V.
+//                   The two halves are joined when the piece ends.
+//   warp 8          TMA: Q of an item, then its K and V tiles, each a ring of
+//                   stages; pages smaller than a tile are boxes of one tile
+//   warp 9          issues the products in order: S(i) first two, then
+//                   O(i), S(i + 2), ...; a commit behind S(i + 2) so also
+//                   says that O(i) is done
+// TMEM: S_0, S_1 (128 columns each), O_0, O_1 (up to 128 each).
+//
+// A row's sums are rescaled only when its maximum has grown by more than 2^8
+// since the last time (all of the statistics are fp32, so the larger weights
+// in between lose nothing); most tiles then leave O in TMEM alone.
+//
+// Work: the key tiles of all sequences and heads in a line (the plan's
+// prefix sums) are dealt to the CTAs in equal runs, whatever the lengths.  An
+// item (sequence, head) that lies in one CTA's run is written by it; of a
+// split item each CTA leaves its unnormalised sums with their maximum and
+// total in the workspace, and a second kernel joins them in order, so repeats
+// are bit-equal.  No CTA waits for another.
+//
+// What a row must not see: scores of masked keys are replaced, not added to,
+// so NaN keys have no effect.  A value of a masked key does enter P V with
+// weight 0, and 0 * NaN is NaN: rows of V past the length are zeroed in shared
+// memory, and non-finite elements of new values (which other rows may see)
+// are taken out there and added back row by row, where the mask has them.
+//
+// Every mbarrier wait is bounded; one that gives up sets
+// SPEC_DEV_WAIT_TIMEOUT and the CTA's abort flag, after which no role waits
+// or issues any more, the loads and products in flight land (bounded again),
+// and TMEM is freed.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <limits.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "spec_attn.h"
 #include "spec_verify.h"
@@ -21,134 +68,1068 @@ namespace {
 using namespace spec_dev;
 using namespace spec_attn;
 
-struct AParams {
-    spec_tree_attention_args a;
-    PlanLayout lay;
-    int G;
+constexpr int BM = 128;           // rows of a tile (TMEM lanes)
+constexpr int PANEL = 64;         // elements of a 128-byte swizzled row
+constexpr int PANEL_BYTES = 128 * 128;  // 128 rows (or keys) of one panel
+constexpr int SOFT_THREADS = 256;
+constexpr int THREADS = SOFT_THREADS + 64;
+constexpr int MAX_CTAS = 192;     // the grid's and the workspace's bound while row tiles allow it
+constexpr float GROWTH = 8.0f;    // log2 of how far a maximum may run ahead of the sums' scale
+
+template <int NP>
+struct Cfg {
+    // 128 KB to 192 KB of K and V in flight or in use: an SM's share of HBM
+    // needs about 35 KB in flight
+    static constexpr int STAGES = NP == 2 ? 3 : 6;
+    static constexpr int TILE = NP * PANEL_BYTES;
+    static constexpr int DP = NP * PANEL;  // columns of O
 };
 
-template <int DT>
-__device__ __forceinline__ float elem(const void *p, int64_t i)
+struct Tail {
+    unsigned long long kfull[6], kempty[6], vfull[6], vempty[6];
+    unsigned long long qfull, qempty, sfull[2], pready[2], pvdone[2], drain;
+    uint32_t tmem_base;
+    int abort_flag;
+    uint32_t bad[2][2][4];  // keys of a group's tile (alternating) whose values are not all finite
+    float m[2][BM], l[2][BM];
+};
+
+template <int NP>
+constexpr size_t smem_bytes()
 {
-    if (DT == SPEC_BF16)
-        return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[i]);
-    return __half2float(reinterpret_cast<const __half *>(p)[i]);
+    return (size_t)Cfg<NP>::TILE * (1 + 2 * Cfg<NP>::STAGES) + sizeof(Tail);
+}
+static_assert(smem_bytes<2>() <= 232448 && smem_bytes<1>() <= 232448, "227 KB per CTA");
+
+struct AParams {
+    const uint8_t *plan;
+    PlanLayout lay;
+    const int32_t *page_table;
+    const void *v_new;
+    int64_t v_new_stride[3];
+    void *out;
+    float *lse;
+    int *status;
+    float *part;     // [ctas][2][BM][DP] unnormalised sums of split items
+    float2 *part_ml; // [ctas][2][BM] (maximum in log2 units, total)
+    float c;         // scale * log2(e)
+    int B, N, Hq, Hkv, D, G;
+    int nodes_per_tile, row_tiles, slots;
+    int page_size, pages_per_seq;
+    int page_rows;   // rows of a cache box: min(128, page_size) (contiguous: 128)
+    int new_rows;    // rows of a box of new tokens
+    int q_rows;      // rows of the Q box
+};
+
+// ------------------------------------------------------------ PTX wrappers
+
+// 32 consecutive columns of this warp's 32 TMEM lanes, one lane per thread; they have
+// arrived when it returns
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32])
+{
+    __syncwarp();  // .sync.aligned: the whole warp, converged
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, "
+        "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31 "
+        "}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr) : "memory");
+}
+
+// 64 consecutive columns of this warp's 32 TMEM lanes, one lane per thread; they have
+// arrived when it returns
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[64])
+{
+    __syncwarp();  // .sync.aligned: the whole warp, converged
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, "
+        "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, "
+        "%36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, "
+        "%53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63 "
+        "}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]),
+          "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
+          "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+          "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]),
+          "=r"(r[63])
+        : "r"(taddr) : "memory");
+}
+
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32])
+{
+    __syncwarp();
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
+        "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, "
+        "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32 "
+        "};"
+        :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+          "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+          "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+          "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st()
+{
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_before()
+{
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after()
+{
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async_shared()
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void group_sync(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                            int z, int w, unsigned long long *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];"
+        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w),
+           "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                            int z, int w, int v, unsigned long long *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w),
+           "r"(v), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// D[tmem] (+)= A[smem] B[smem]
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem]
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void mma_commit(unsigned long long *bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+        :: "r"(smem_addr(bar)) : "memory");
+}
+
+// Shared-memory matrix descriptors, 128-byte swizzle (version 1, mode 2).
+// K-major (Q and K): rows of 128 bytes, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr)
+{
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// MN-major (V: its 64-element panels run along N, its keys along K): panels
+// PANEL_BYTES apart (leading offset), groups of 8 keys 1024 bytes apart (stride).
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr)
+{
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(PANEL_BYTES >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// Instruction descriptor, kind::f16: fp32 accumulator, A and B both bf16 (1)
+// or both fp16 (0), M = 128.
+template <int DT>
+__device__ __forceinline__ uint32_t idesc(int n, bool b_mn_major)
+{
+    constexpr uint32_t T = DT == SPEC_BF16 ? 1u : 0u;
+    return (1u << 4) | (T << 7) | (T << 10) | ((b_mn_major ? 1u : 0u) << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+}
+
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b,
+                                                   unsigned long long c)
+{
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
 }
 
 template <int DT>
-__device__ __forceinline__ void store(void *p, int64_t i, float x)
+__device__ __forceinline__ uint32_t pack(float lo, float hi)
 {
-    if (DT == SPEC_BF16)
-        reinterpret_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
-    else
-        reinterpret_cast<__half *>(p)[i] = __float2half_rn(x);
-}
-
-template <int DT>
-__global__ void __launch_bounds__(KT) attention_kernel(const AParams P)
-{
-    const spec_tree_attention_args &A = P.a;
-    __shared__ float qs[SPEC_ATTN_MAX_HEAD_DIM];
-    __shared__ float w[KT];
-    __shared__ float red[4];
-    const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = (int)(blockIdx.x / A.N), n = (int)(blockIdx.x % A.N);
-    const int h = (int)blockIdx.y, kvh = h / P.G;
-    wait_previous_kernel();
-    const uint8_t *plan = static_cast<const uint8_t *>(A.plan);
-    const PlanSeq S = reinterpret_cast<const PlanSeq *>(plan + P.lay.seq)[b];
-    const uint32_t *mask = reinterpret_cast<const uint32_t *>(plan + P.lay.mask) +
-                           ((size_t)b * A.N + n) * P.lay.W;
-    const int64_t orow = ((int64_t)b * A.N + n) * A.Hq + h;
-    if (n >= S.n_nodes) {
-        if (tid < A.D)
-            store<DT>(A.out, orow * A.D + tid, S.status ? NAN : 0.0f);
-        if (tid == 0 && A.out_lse)
-            A.out_lse[orow] = S.status ? NAN : -INFINITY;
-        return;
+    if (DT == SPEC_BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
     }
-    if (tid < A.D)
-        qs[tid] = elem<DT>(A.q, b * A.q_stride[0] + n * A.q_stride[1] + h * A.q_stride[2] + tid);
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+template <int DT>
+__device__ __forceinline__ float unpack1(uint32_t half)
+{
+    if (DT == SPEC_BF16)
+        return __uint_as_float(half << 16);
+    return __half2float(__ushort_as_half((unsigned short)half));
+}
+
+// which halves of a word are NaN or infinite, as masks of 16 bits
+template <int DT>
+__device__ __forceinline__ uint32_t nonfinite(uint32_t w)
+{
+    constexpr uint32_t E = DT == SPEC_BF16 ? 0x7f80u : 0x7c00u;
+    return ((w & E) == E ? 0xffffu : 0u) | (((w >> 16) & E) == E ? 0xffff0000u : 0u);
+}
+
+// Scores of columns past `keys` or with a 0 bit in w1:w0 become -inf.
+template <int N>
+__device__ __forceinline__ void hide(uint32_t (&x)[N], int keys, uint32_t w0, uint32_t w1)
+{
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (j >= keys || !(((j < 32 ? w0 : w1) >> (j & 31)) & 1u))
+            x[j] = 0xff800000u;
+}
+
+// ------------------------------------------------------------------- work
+
+// A run of one item's key tiles inside a CTA's share.
+struct Piece {
+    int b, h;
+    int tile0, n;    // first tile and number of tiles
+    int tiles;       // of the whole item
+    int len, nn;     // cache length and nodes
+    int status;
+    bool idle;       // nothing to compute: no live row in this row tile
+    long long u0;    // the item's first unit
+};
+
+// Sequence of unit u: the last b with cum[b] * Hkv <= u.
+__device__ __forceinline__ int find_seq(const long long *cum, int B, int Hkv, long long u)
+{
+    int lo = 0, hi = B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (__ldg(cum + mid) * Hkv <= u)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ void set_piece(const AParams &P, const long long *cum, int b,
+                                          long long u, long long u1, int rt, Piece &p)
+{
+    const long long c0 = __ldg(cum + b), c1 = __ldg(cum + b + 1);
+    const uint4 s = __ldg(reinterpret_cast<const uint4 *>(P.plan + P.lay.seq) + b);
+    p.b = b;
+    p.tiles = (int)(c1 - c0);
+    const long long rel = u - c0 * P.Hkv;
+    p.h = (int)(rel / p.tiles);
+    p.tile0 = (int)(rel - (long long)p.h * p.tiles);
+    p.u0 = u - p.tile0;
+    const long long left = u1 - u;
+    p.n = p.tiles - p.tile0 < left ? p.tiles - p.tile0 : (int)left;
+    p.len = (int)s.x;
+    p.nn = (int)s.y;
+    p.status = (int)s.z;
+    p.idle = p.nn <= rt * P.nodes_per_tile;
+}
+
+// Calls fn(piece) for each item's run in units [u, u1).
+template <typename F>
+__device__ __forceinline__ void for_pieces(const AParams &P, const long long *cum, long long u,
+                                           long long u1, int rt, F fn)
+{
+    if (u >= u1)
+        return;
+    int b = find_seq(cum, P.B, P.Hkv, u);
+    while (u < u1) {
+        while (b + 1 < P.B && __ldg(cum + b + 1) * P.Hkv <= u)
+            ++b;
+        Piece p;
+        set_piece(P, cum, b, u, u1, rt, p);
+        fn(p);
+        u += p.n;
+    }
+}
+
+// Keys of tile `jt` of an item: how many, and whether they are the cache's.
+__device__ __forceinline__ int tile_keys(const Piece &p, int jt, bool &cached)
+{
+    const int cache_tiles = (p.len + KT - 1) / KT;
+    cached = jt < cache_tiles;
+    const int left = cached ? p.len - jt * KT : p.nn - (jt - cache_tiles) * KT;
+    return left < KT ? left : KT;
+}
+
+// A CTA's share: `per` units for each of the slots that have any.  A share
+// is at least 2 tiles, one for each softmax group.
+__device__ __forceinline__ long long share(const AParams &P, long long total)
+{
+    const long long per = (total + P.slots - 1) / P.slots;
+    return per < 2 ? 2 : per;
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(const AParams &P, int64_t elem, const float (&v)[8])
+{
+    uint4 w;
+    w.x = pack<DT>(v[0], v[1]);
+    w.y = pack<DT>(v[2], v[3]);
+    w.z = pack<DT>(v[4], v[5]);
+    w.w = pack<DT>(v[6], v[7]);
+    *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(P.out) + elem) = w;
+}
+
+// ln of a total of weights in units of 2^m; -inf for none
+__device__ __forceinline__ float lse_of(float m, float l)
+{
+    return l == 0.0f ? -INFINITY : (m + log2f(l)) * (1.0f / LOG2E);
+}
+
+template <int NP, int DT>
+__global__ void __launch_bounds__(THREADS, 1)
+    attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkn,
+                     const __grid_constant__ CUtensorMap mvn, const __grid_constant__ CUtensorMap mkc,
+                     const __grid_constant__ CUtensorMap mvc, const __grid_constant__ AParams P)
+{
+    using C = Cfg<NP>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t q_s = smem_addr(smem);
+    const uint32_t k_s = q_s + C::TILE, v_s = k_s + C::STAGES * C::TILE;
+    uint8_t *v_p = smem + (size_t)C::TILE * (1 + C::STAGES);
+    Tail &S = *reinterpret_cast<Tail *>(smem + (size_t)C::TILE * (1 + 2 * C::STAGES));
+    volatile int *abort_flag = &S.abort_flag;
+    const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int slot = (int)blockIdx.x / P.row_tiles, rt = (int)blockIdx.x - slot * P.row_tiles;
+
+    if (tid == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(&S.kfull[i], 1);
+            mbar_init(&S.kempty[i], 1);
+            mbar_init(&S.vfull[i], 1);
+            mbar_init(&S.vempty[i], 1);
+        }
+        mbar_init(&S.qfull, 1);
+        mbar_init(&S.qempty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.sfull[i], 1);
+            mbar_init(&S.pready[i], 4);
+            mbar_init(&S.pvdone[i], 1);
+        }
+        mbar_init(&S.drain, 1);
+        S.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_shared();
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
+                     :: "r"(smem_addr(&S.tmem_base)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
     __syncthreads();
-    auto row_of = [&](int j, const int64_t *cs, const int64_t *ns, bool &cached) -> int64_t {
-        cached = j < S.cache_len;
-        if (cached) {
-            const int pg = A.page_table
-                ? A.page_table[(size_t)b * A.pages_per_seq + j / A.page_size] : b;
-            return pg * cs[0] + (j % A.page_size) * cs[1] + kvh * cs[2];
-        }
-        return b * ns[0] + (j - S.cache_len) * ns[1] + kvh * ns[2];
+    tc_fence_after();
+    const uint32_t tmem = S.tmem_base;
+    allow_next_kernel();
+    wait_previous_kernel();
+    const long long *cum = reinterpret_cast<const long long *>(P.plan + P.lay.cum);
+    const long long total = __ldg(cum + P.B) * P.Hkv;
+    const long long per = share(P, total);
+    const long long u0 = slot * per, u1 = u0 + per < total ? u0 + per : total;
+
+    // a wait of this thread: false once the CTA has given up
+    auto wait = [&](unsigned long long *bar, uint32_t parity) -> bool {
+        if (mbar_try_wait(bar, parity))
+            return true;
+        if (*abort_flag)
+            return false;
+        if (mbar_wait(bar, parity))
+            return true;
+        atomicExch(P.status, SPEC_DEV_WAIT_TIMEOUT);
+        *abort_flag = 1;
+        return false;
     };
-    float m = -INFINITY, l = 0.0f, o = 0.0f;
-    const int total = S.cache_len + S.n_nodes;
-    const float c = A.scale * LOG2E;
-    for (int j0 = 0; j0 < total; j0 += KT) {
-        const int j = j0 + tid, t = j - S.cache_len;
-        const bool on = j < total && (t < 0 || ((mask[t >> 5] >> (t & 31)) & 1u));
-        float s = -INFINITY;
-        if (on) {
-            bool cached;
-            const int64_t r = row_of(j, A.k_cache_stride, A.k_new_stride, cached);
-            const void *base = cached ? A.k_cache : A.k_new;
-            s = 0.0f;
-            for (int d = 0; d < A.D; ++d)
-                s = fmaf(qs[d], elem<DT>(base, r + d), s);
-            s *= c;
-        }
-        float mx = s;
-        for (int d = 16; d; d >>= 1)
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        if (lane == 0)
-            red[warp] = mx;
-        __syncthreads();
-        const float mn = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-        const float ms = mn == -INFINITY ? 0.0f : mn;
-        w[tid] = on ? ex2(s - ms) : -1.0f;  // -1: not seen
-        const float f = m == -INFINITY ? 0.0f : ex2(m - ms);
-        l *= f;
-        if (f != 1.0f)
-            o = m == -INFINITY ? 0.0f : o * f;
-        m = mn;
-        __syncthreads();
-        const int cnt = min(KT, total - j0);
-        for (int i = 0; i < cnt; ++i) {
-            const float p = w[i];
-            if (p == -1.0f)
-                continue;
-            l += p;
-            if (tid < A.D) {
+
+    if (warp == 8) {
+        // ---------------------------------------------------- TMA producer
+        uint32_t t = 0, items = 0;           // tiles and items so far
+        uint32_t issued[2] = {0, 0};         // tiles of K and of V whose loads were issued
+        bool ok = true;
+        for_pieces(P, cum, u0, u1, rt, [&](const Piece &p) {
+            if (p.idle || !ok)
+                return;
+            ok = __all_sync(0xffffffffu, wait(&S.qempty, (items & 1u) ^ 1u));
+            if (!ok)
+                return;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&S.qfull, (uint32_t)(P.q_rows * 128 * NP));
+                for (int i = 0; i < NP; ++i)
+                    tma_load_5d(q_s + i * PANEL_BYTES, &mq, i * PANEL, 0, rt * P.nodes_per_tile,
+                                p.h, p.b, &S.qfull);
+            }
+            ++items;
+            for (int i = 0; i < p.n && ok; ++i, ++t) {
                 bool cached;
-                const int64_t r = row_of(j0 + i, A.v_cache_stride, A.v_new_stride, cached);
-                o = fmaf(p, elem<DT>(cached ? A.v_cache : A.v_new, r + tid), o);
+                const int jt = p.tile0 + i;
+                const int keys = tile_keys(p, jt, cached);
+                // box of this lane: its rows of the tile and its page
+                const int rows = cached ? P.page_rows : P.new_rows;
+                const int at = lane * rows;
+                const bool mine = at < keys;
+                int y, w;
+                if (cached) {
+                    const int pos = jt * KT + at;
+                    y = pos;
+                    w = p.b;
+                    if (P.page_table && mine) {
+                        const int e = pos / P.page_size;
+                        w = e < P.pages_per_seq
+                            ? __ldg(P.page_table + (size_t)p.b * P.pages_per_seq + e) : -1;
+                        y = pos - e * P.page_size;
+                    }
+                } else {
+                    y = (jt - (p.len + KT - 1) / KT) * KT + at;
+                    w = p.b;
+                }
+                const uint32_t bytes = (uint32_t)(((keys + rows - 1) / rows) * rows * 128 * NP);
+                const int st = (int)(t % C::STAGES);
+                const uint32_t ph = (t / C::STAGES) & 1u;
+#pragma unroll
+                for (int side = 0; side < 2; ++side) {
+                    unsigned long long *empty = side ? &S.vempty[st] : &S.kempty[st];
+                    unsigned long long *full = side ? &S.vfull[st] : &S.kfull[st];
+                    const CUtensorMap *map = cached ? (side ? &mvc : &mkc) : (side ? &mvn : &mkn);
+                    ok = __all_sync(0xffffffffu, wait(empty, ph ^ 1u));
+                    if (!ok)
+                        break;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(full, bytes);
+                    __syncwarp();
+                    issued[side] = t + 1;
+                    if (mine) {
+                        const uint32_t dst = (side ? v_s : k_s) + st * C::TILE + at * 128;
+#pragma unroll
+                        for (int d = 0; d < NP; ++d)
+                            tma_load_4d(dst + d * PANEL_BYTES, map, d * PANEL, y, p.h, w, full);
+                    }
+                }
+            }
+        });
+        if (!ok) {
+            // the loads in flight land first: each barrier's last phase that has a load
+            for (int side = 0; side < 2; ++side) {
+                const uint32_t n = issued[side];
+                for (uint32_t j = n > C::STAGES ? n - C::STAGES : 0; j < n; ++j)
+                    (void)mbar_wait(side ? &S.vfull[j % C::STAGES] : &S.kfull[j % C::STAGES],
+                                    (j / C::STAGES) & 1u);
+            }
+            if (items)
+                (void)mbar_wait(&S.qfull, (items - 1) & 1u);
+        }
+    } else if (warp == 9) {
+        // ------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            uint32_t tk = 0, tv = 0, items = 0, cnt[2] = {0, 0};
+            bool ok = true, issued = false;
+            const int ksteps = (P.D + 15) / 16;
+            const int dcols = ksteps * 16;
+            auto scores = [&](const Piece &p, int i) {  // S(i) = Q K(i)^T
+                bool cached;
+                const int keys = tile_keys(p, p.tile0 + i, cached);
+                const int st = (int)(tk % C::STAGES);
+                ok = ok && wait(&S.kfull[st], (tk / C::STAGES) & 1u);
+                if (!ok)
+                    return;
+                tc_fence_after();
+                const uint32_t id = idesc<DT>((keys + 15) & ~15, false);
+                const uint32_t d = tmem + (uint32_t)((i & 1) * KT);
+                const uint32_t kb = k_s + st * C::TILE;
+                for (int s = 0; s < ksteps; ++s) {
+                    const uint32_t off = (uint32_t)((s >> 2) * PANEL_BYTES + (s & 3) * 32);
+                    mma_ss(d, desc_k(q_s + off), desc_k(kb + off), id, s ? 1u : 0u);
+                }
+                issued = true;
+                mma_commit(&S.kempty[st]);
+                mma_commit(&S.sfull[i & 1]);
+                if (i == p.n - 1)
+                    mma_commit(&S.qempty);
+                ++tk;
+            };
+            for_pieces(P, cum, u0, u1, rt, [&](const Piece &p) {
+                if (p.idle || !ok)
+                    return;
+                ok = wait(&S.qfull, items & 1u);
+                ++items;
+                for (int i = 0; i < 2 && i < p.n && ok; ++i)
+                    scores(p, i);
+                for (int i = 0; i < p.n && ok; ++i) {
+                    bool cached;
+                    const int keys = tile_keys(p, p.tile0 + i, cached);
+                    const int s = i & 1, st = (int)(tv % C::STAGES);
+                    ok = wait(&S.vfull[st], (tv / C::STAGES) & 1u) &&
+                         wait(&S.pready[s], cnt[s] & 1u);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint32_t id = idesc<DT>(dcols, true);
+                    const uint32_t d = tmem + (uint32_t)(2 * KT + s * C::DP);
+                    const uint32_t a = tmem + (uint32_t)(s * KT);
+                    const uint32_t vb = v_s + st * C::TILE;
+                    const int steps = (keys + 15) / 16;
+                    for (int x = 0; x < steps; ++x)  // 16 keys: 8 columns of P, 2 KB of V
+                        mma_ts(d, a + (uint32_t)(x * 8), desc_mn(vb + x * 2048), id,
+                               (i >= 2 || x) ? 1u : 0u);
+                    mma_commit(&S.vempty[st]);
+                    mma_commit(&S.pvdone[s]);
+                    ++tv;
+                    ++cnt[s];
+                    if (i + 2 < p.n)
+                        scores(p, i + 2);
+                }
+            });
+            if (!ok && issued) {  // the products in flight complete (bounded)
+                mma_commit(&S.drain);
+                (void)mbar_wait(&S.drain, 0u);
             }
         }
-        __syncthreads();
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------- softmax groups
+        const int s = warp >> 2;                 // the group
+        const int quarter = warp & 3;
+        const int r = quarter * 32 + lane;       // row of the tile
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const uint32_t t_s = tmem + lanes + (uint32_t)(s * KT);
+        const uint32_t t_o = tmem + lanes + (uint32_t)(2 * KT + s * C::DP);
+        const int local = r / P.G;               // node of the row, counted in the tile
+        const int g = r - local * P.G;
+        const int node = rt * P.nodes_per_tile + local;
+        const bool row = local < P.nodes_per_tile && node < P.N;
+        const uint32_t *masks = reinterpret_cast<const uint32_t *>(P.plan + P.lay.mask);
+        uint32_t cnt = 0, tv = 0;                // the group's tiles, all V tiles
+        const unsigned long long c2 = f2(P.c, P.c);
+
+        for_pieces(P, cum, u0, u1, rt, [&](const Piece &p) {
+            const int64_t orow = ((int64_t)p.b * P.N + node) * P.Hq + (int64_t)p.h * P.G + g;
+            if (p.idle) {
+                // rows past n_nodes are 0, of a bad sequence NaN; once per item
+                if (s == 0 && p.tile0 == 0 && row) {
+                    const float x = p.status ? NAN : 0.0f;
+                    const float v[8] = {x, x, x, x, x, x, x, x};
+                    for (int d = 0; d < P.D; d += 8)
+                        store8<DT>(P, orow * P.D + d, v);
+                    if (P.lse)
+                        P.lse[orow] = p.status ? NAN : -INFINITY;
+                }
+                return;
+            }
+            const bool live = row && node < p.nn;
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            float m = -INFINITY, l = 0.0f;       // maximum of the raw scores, total
+            const int cache_tiles = (p.len + KT - 1) / KT;
+            for (int i = s; i < p.n; i += 2) {
+                bool cached;
+                const int jt = p.tile0 + i;
+                const int keys = tile_keys(p, jt, cached);
+                // what this row sees of the tile
+                uint4 see = make_uint4(~0u, ~0u, ~0u, ~0u);
+                if (!cached) {
+                    see = make_uint4(0, 0, 0, 0);
+                    if (live)
+                        see = __ldg(reinterpret_cast<const uint4 *>(
+                                        masks + ((size_t)p.b * P.N + node) * P.lay.W) +
+                                    (jt - cache_tiles));
+                }
+                uint32_t any_bad = 0;
+                const bool masked = keys < KT || !cached;
+                if (masked) {
+                    // V: rows past the keys (up to the last product's 16) are zeroed; in new
+                    // values, non-finite elements are noted and zeroed
+                    const uint32_t vt = tv + (uint32_t)i;
+                    const int st = (int)(vt % C::STAGES);
+                    wait(&S.vfull[st], (vt / C::STAGES) & 1u);
+                    uint8_t *vrow = v_p + (size_t)st * C::TILE + r * 128;
+                    bool bad = false;
+                    if (r >= keys && r < ((keys + 15) & ~15)) {
+#pragma unroll
+                        for (int x = 0; x < NP * 8; ++x)
+                            *reinterpret_cast<uint4 *>(vrow + (x >> 3) * PANEL_BYTES +
+                                                       (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    } else if (!cached && r < keys) {
+#pragma unroll
+                        for (int x = 0; x < NP * 8; ++x) {
+                            uint4 *q = reinterpret_cast<uint4 *>(vrow + (x >> 3) * PANEL_BYTES +
+                                                                 (x & 7) * 16);
+                            uint4 w = *q;
+                            const uint4 f = make_uint4(nonfinite<DT>(w.x), nonfinite<DT>(w.y),
+                                                       nonfinite<DT>(w.z), nonfinite<DT>(w.w));
+                            if (f.x | f.y | f.z | f.w) {
+                                bad = true;
+                                w.x &= ~f.x;
+                                w.y &= ~f.y;
+                                w.z &= ~f.z;
+                                w.w &= ~f.w;
+                                *q = w;
+                            }
+                        }
+                    }
+                    fence_async_shared();
+                    if (!cached) {
+                        const uint32_t ballot = __ballot_sync(0xffffffffu, bad);
+                        if (lane == 0)
+                            S.bad[s][cnt & 1u][quarter] = ballot;
+                        group_sync(2 + s, 128);
+                        const uint32_t *f = S.bad[s][cnt & 1u];
+                        any_bad = f[0] | f[1] | f[2] | f[3];
+                    }
+                }
+                wait(&S.sfull[s], cnt & 1u);
+                __syncwarp();
+                tc_fence_after();
+                uint32_t zero_w[4] = {0, 0, 0, 0};  // keys whose weight is 0 (with any_bad only)
+                if (warp_live) {
+                    // two passes over the scores, 64 columns at a time: they stay in TMEM, where a
+                    // second read costs less than the registers to keep 128 of them
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t x[64];
+                        tmem_ld(t_s + h * 64, x);
+                        if (masked)
+                            hide<64>(x, keys - h * 64, h ? see.z : see.x, h ? see.w : see.y);
+#pragma unroll
+                        for (int j = 0; j < 64; j += 8) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(x[j + 2 * k]),
+                                                           __uint_as_float(x[j + 2 * k + 1])));
+                        }
+                    }
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    if (i == s) {
+                        m = top;
+                    } else {
+                        const bool grown = (top - m) * P.c > GROWTH;  // -inf to finite too
+                        if (__any_sync(0xffffffffu, grown)) {
+                            const float f = grown ? ex2((m - top) * P.c) : 1.0f;
+                            l *= f;
+                            if (grown)
+                                m = top;
+#pragma unroll
+                            for (int d = 0; d < C::DP; d += 32) {
+                                uint32_t o[32];
+                                tmem_ld(t_o + d, o);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                tmem_st(t_o + d, o);
+                            }
+                        }
+                    }
+                    const float shift = m == -INFINITY ? 0.0f : -m * P.c;
+                    const unsigned long long shift2 = f2(shift, shift);
+                    unsigned long long sum[2] = {0ull, 0ull};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t x[64], pk[32];
+                        tmem_ld(t_s + h * 64, x);
+                        if (masked)
+                            hide<64>(x, keys - h * 64, h ? see.z : see.x, h ? see.w : see.y);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            float a0, a1;
+                            f2_split(fma2(f2_bits(x[2 * j], x[2 * j + 1]), c2, shift2), a0, a1);
+                            a0 = ex2(a0);
+                            a1 = ex2(a1);
+                            sum[j & 1] = add2(sum[j & 1], f2(a0, a1));
+                            pk[j] = pack<DT>(a0, a1);
+                        }
+                        if (any_bad) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                zero_w[h * 2 + (j >> 4)] |=
+                                    ((pk[j] & 0x7fffu) == 0 ? 1u : 0u) << ((2 * j) & 31) |
+                                    ((pk[j] & 0x7fff0000u) == 0 ? 2u : 0u) << ((2 * j) & 31);
+                            }
+                        }
+                        // weights 64 h on lie in columns 32 h on: over scores that were read
+                        tmem_st(t_s + h * 32, pk);
+                    }
+                    float s0, s1;
+                    f2_split(add2(sum[0], sum[1]), s0, s1);
+                    l += s0 + s1;
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&S.pready[s]);
+                if (any_bad) {
+                    // what the zeroed elements give the rows that see them, once O(i) is done
+                    wait(&S.pvdone[s], cnt & 1u);
+                    __syncwarp();
+                    tc_fence_after();
+                    const uint32_t w[4] = {see.x, see.y, see.z, see.w};
+                    const int first = (jt - cache_tiles) * KT;
+#pragma unroll 1
+                    for (int d = 0; d < C::DP; d += 32) {
+                        uint32_t o[32];
+                        tmem_ld(t_o + d, o);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t left = S.bad[s][cnt & 1u][q];
+                            while (left) {
+                                const int bit = __ffs((int)left) - 1;
+                                left &= left - 1;
+                                if (!((w[q] >> bit) & 1u))
+                                    continue;
+                                const uint16_t *src = reinterpret_cast<const uint16_t *>(P.v_new) +
+                                    p.b * P.v_new_stride[0] +
+                                    (first + q * 32 + bit) * P.v_new_stride[1] +
+                                    p.h * P.v_new_stride[2];
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    if (d + j < P.D) {
+                                        const uint32_t e = src[d + j];
+                                        if (nonfinite<DT>(e) & 0xffffu) {
+                                            const float z = (zero_w[q] >> bit) & 1u ? 0.0f : 1.0f;
+                                            o[j] = __float_as_uint(__uint_as_float(o[j]) +
+                                                                   z * unpack1<DT>(e));
+                                        }
+                                    }
+                            }
+                        }
+                        __syncwarp();
+                        tmem_st(t_o + d, o);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    // the next tile's notes come after every thread has read these
+                    group_sync(2 + s, 128);
+                }
+                ++cnt;
+            }
+            tv += (uint32_t)p.n;
+
+            // join the two groups' halves: each group writes one half of the columns
+            const bool mine = p.n > s;           // this group had a tile
+            if (mine)
+                wait(&S.pvdone[s], (cnt - 1) & 1u);
+            __syncwarp();
+            tc_fence_after();
+            S.m[s][r] = mine ? (m == -INFINITY ? -INFINITY : m * P.c) : -INFINITY;
+            S.l[s][r] = mine ? l : 0.0f;
+            tc_fence_before();
+            group_sync(1, SOFT_THREADS);
+            tc_fence_after();
+            const bool whole = p.n == p.tiles;
+            const bool two = p.n > 1;
+            if (__any_sync(0xffffffffu, row && (whole || live))) {
+                const float m0 = S.m[0][r], m1 = S.m[1][r], l0 = S.l[0][r], l1 = S.l[1][r];
+                const float top = fmaxf(m0, m1);
+                const float base = top == -INFINITY ? 0.0f : top;
+                // a half that saw no key has no weight, whatever its O holds
+                const bool some0 = !(m0 == -INFINITY && l0 == 0.0f);
+                const bool some1 = !(m1 == -INFINITY && l1 == 0.0f);
+                const float w0 = some0 ? ex2(m0 - base) : 0.0f;
+                const float w1 = some1 ? ex2(m1 - base) : 0.0f;
+                const float sum = l0 * w0 + l1 * w1;
+                const bool first_of_slot = u0 >= p.u0;  // the CTA's run starts inside the item
+                const size_t at = ((size_t)blockIdx.x * 2 + (first_of_slot ? 0 : 1)) * BM + r;
+                const float norm = whole ? (live && sum != 0.0f ? 1.0f / sum : 0.0f) : 1.0f;
+                constexpr int HALF = C::DP / 2;
+#pragma unroll
+                for (int d0 = 0; d0 < HALF; d0 += 32) {
+                    const int d = s * HALF + d0;
+                    uint32_t a[32], b[32];
+                    tmem_ld(tmem + lanes + (uint32_t)(2 * KT + d), a);
+                    if (two)
+                        tmem_ld(tmem + lanes + (uint32_t)(2 * KT + C::DP + d), b);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        if (d + j >= P.D || !row || !(whole || live))
+                            continue;
+                        float v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            float x = some0 ? __uint_as_float(a[j + k]) * w0 : 0.0f;
+                            if (some1)
+                                x = fmaf(__uint_as_float(b[j + k]), w1, x);
+                            v[k] = (!whole || (live && sum != 0.0f)) ? x * norm : 0.0f;
+                        }
+                        if (whole) {
+                            store8<DT>(P, orow * P.D + d + j, v);
+                        } else {
+                            float4 *o = reinterpret_cast<float4 *>(P.part + at * C::DP + d + j);
+                            o[0] = make_float4(v[0], v[1], v[2], v[3]);
+                            o[1] = make_float4(v[4], v[5], v[6], v[7]);
+                        }
+                    }
+                }
+                if (s == 0 && row) {
+                    if (whole && P.lse)
+                        P.lse[orow] = live ? lse_of(base, sum) : -INFINITY;
+                    if (!whole && live)
+                        P.part_ml[at] = make_float2(top, sum);
+                }
+            }
+            tc_fence_before();
+            group_sync(1, SOFT_THREADS);  // O and the exchanged statistics are free again
+        });
     }
-    if (tid < A.D)
-        store<DT>(A.out, orow * A.D + tid, l == 0.0f ? 0.0f : o / l);
-    if (tid == 0 && A.out_lse)
-        A.out_lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) / LOG2E;
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
+    }
 }
+
+// ---------------------------------------------------------------- joining
+
+constexpr int JOIN_WARPS = 8;
+
+// Joins the pieces of the items that lie across a share's end.  CTA x takes
+// the item that the end of share x cuts (when no earlier end cuts it), one row
+// of one row tile per warp.
+template <int NP, int DT>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_constant__ AParams P)
+{
+    using C = Cfg<NP>;
+    const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
+    const int rt = (int)blockIdx.y;
+    const int r = (int)blockIdx.z * JOIN_WARPS + warp;
+    allow_next_kernel();
+    wait_previous_kernel();
+    const long long *cum = reinterpret_cast<const long long *>(P.plan + P.lay.cum);
+    const long long total = __ldg(cum + P.B) * P.Hkv;
+    const long long per = share(P, total);
+    const long long end = ((long long)blockIdx.x + 1) * per;
+    if (end >= total)
+        return;
+    const int b = find_seq(cum, P.B, P.Hkv, end);
+    Piece p;
+    set_piece(P, cum, b, end, total, rt, p);
+    if (p.tile0 == 0 || p.u0 < end - per || p.idle)
+        return;  // not cut here, or the previous end has it, or no rows
+    const int local = r / P.G, g = r - local * P.G;
+    const int node = rt * P.nodes_per_tile + local;
+    if (r >= BM || local >= P.nodes_per_tile || node >= P.N)
+        return;
+    const int64_t orow = ((int64_t)p.b * P.N + node) * P.Hq + (int64_t)p.h * P.G + g;
+    const bool live = node < p.nn;
+    const int s0 = (int)blockIdx.x, s1 = (int)((p.u0 + p.tiles - 1) / per);
+    // a share that starts with the item, or inside it, left its first piece; one that the item
+    // starts inside of left its second
+    auto at = [&](int s) -> size_t {
+        const int which = (long long)s * per >= p.u0 ? 0 : 1;
+        return (((size_t)s * P.row_tiles + rt) * 2 + which) * BM + r;
+    };
+    float top = -INFINITY;
+    if (live)
+        for (int s = s0 + lane; s <= s1; s += 32)
+            top = fmaxf(top, P.part_ml[at(s)].x);
+    for (int d = 16; d; d >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float base = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int d = lane * 4;
+    if (live) {
+        for (int s = s0; s <= s1; ++s) {
+            const float2 ml = P.part_ml[at(s)];
+            if (ml.x == -INFINITY && ml.y == 0.0f)
+                continue;  // no key seen there
+            const float w = ex2(ml.x - base);
+            sum = fmaf(ml.y, w, sum);
+            if (d < P.D) {
+                const float4 v = *reinterpret_cast<const float4 *>(P.part + at(s) * C::DP + d);
+                o.x = fmaf(v.x, w, o.x);
+                o.y = fmaf(v.y, w, o.y);
+                o.z = fmaf(v.z, w, o.z);
+                o.w = fmaf(v.w, w, o.w);
+            }
+        }
+    }
+    if (d < P.D) {
+        const float norm = sum != 0.0f ? 1.0f / sum : 0.0f;
+        uint2 w = make_uint2(0u, 0u);
+        if (sum != 0.0f) {
+            w.x = pack<DT>(o.x * norm, o.y * norm);
+            w.y = pack<DT>(o.z * norm, o.w * norm);
+        }
+        *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(P.out) + orow * P.D + d) = w;
+    }
+    if (lane == 0 && P.lse)
+        P.lse[orow] = live ? lse_of(base, sum) : -INFINITY;
+}
+
+// ------------------------------------------------------------------- host
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 bool heads_ok(int32_t N, int32_t Hq, int32_t Hkv, int32_t D)
 {
     return N >= 1 && N <= SPEC_ATTN_MAX_NODES && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 &&
-           Hq / Hkv <= 128 && Hq <= 65535 && D >= 8 && D % 8 == 0 && D <= SPEC_ATTN_MAX_HEAD_DIM;
+           Hq / Hkv <= BM && Hq <= 65535 && D >= 8 && D % 8 == 0 && D <= SPEC_ATTN_MAX_HEAD_DIM;
 }
 
 bool page_size_ok(int32_t s, bool paged)
 {
-    return s >= 1 && (!paged || s % 128 == 0 || (s >= 8 && (s & (s - 1)) == 0));
+    return s >= 1 && (!paged || s % KT == 0 || (s >= 8 && (s & (s - 1)) == 0));
 }
 
 bool strides_ok(const int64_t (&s)[3])
 {
     for (int64_t x : s)
-        if (x < 0 || x % 8 != 0 || x > ((int64_t)1 << 38))
+        if (x < 0 || x % 8 != 0 || x >= ((int64_t)1 << 38))
             return false;
     return true;
+}
+
+int row_tiles(int N, int G)
+{
+    const int per = BM / G;
+    return (N + per - 1) / per;
+}
+
+struct WsLayout {
+    size_t ml, part, total;
+};
+
+WsLayout ws_layout(int N, int G, int D)
+{
+    const int rt = row_tiles(N, G);
+    const size_t ctas = rt > MAX_CTAS ? (size_t)rt : (size_t)MAX_CTAS;
+    const size_t dp = D > PANEL ? 2 * PANEL : PANEL;
+    WsLayout w;
+    w.ml = sizeof(WsHeader);
+    w.part = plan_align(w.ml + ctas * 2 * BM * sizeof(float2));
+    w.total = plan_align(w.part + ctas * 2 * BM * dp * sizeof(float));
+    return w;
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn()
+{
+    static const EncodeTiledFn fn = []() -> EncodeTiledFn {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                             cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<EncodeTiledFn>(p);
+        (void)cudaGetLastError();
+        return nullptr;
+    }();
+    return fn;
+}
+
+// A tensor map of 64-element, 128-byte swizzled boxes; dims[0] is the head
+// dimension, strides (elements) belong to dims 1 on.  What lies outside reads 0.
+bool make_map(CUtensorMap *map, const void *base, int dtype, int rank, const uint64_t *dims,
+              const int64_t *strides, const uint32_t *box)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn)
+        return false;
+    cuuint64_t d[5], s[4];
+    cuuint32_t b[5], e[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        e[i] = 1;
+        if (i > 0)  // a dimension of one entry is never stepped along: any stride will do
+            s[i - 1] = (cuuint64_t)(dims[i] > 1 ? strides[i - 1] : (int64_t)dims[0] + 8) * 2 / 16 * 16;
+    }
+    return fn(map, dtype == SPEC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+              (cuuint32_t)rank, const_cast<void *>(base), d, s, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct DevInfo {
+    std::atomic<int> sms;
+    std::atomic<bool> attr[2][2];
+};
+DevInfo g_dev[64];
+
+template <int NP, int DT>
+int launch(const CUtensorMap (&maps)[5], AParams &P, int sms, DevInfo &di, cudaStream_t st)
+{
+    if (!di.attr[NP - 1][DT - 1].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(attention_kernel<NP, DT>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)smem_bytes<NP>()) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return SPEC_ECUDA;
+        }
+        di.attr[NP - 1][DT - 1].store(true, std::memory_order_release);
+    }
+    const int ctas = sms < MAX_CTAS ? sms : MAX_CTAS;
+    P.slots = ctas / P.row_tiles < 1 ? 1 : ctas / P.row_tiles;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned int)(P.slots * P.row_tiles));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem_bytes<NP>();
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, attention_kernel<NP, DT>, maps[0], maps[1], maps[2], maps[3],
+                           maps[4], P) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return SPEC_ECUDA;
+    }
+    if (P.slots > 1) {
+        const int rows = P.nodes_per_tile * P.G < P.N * P.G ? P.nodes_per_tile * P.G : P.N * P.G;
+        cfg.gridDim = dim3((unsigned int)(P.slots - 1), (unsigned int)P.row_tiles,
+                           (unsigned int)((rows + JOIN_WARPS - 1) / JOIN_WARPS));
+        cfg.blockDim = dim3(JOIN_WARPS * 32);
+        cfg.dynamicSmemBytes = 0;
+        if (cudaLaunchKernelEx(&cfg, join_kernel<NP, DT>, P) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return SPEC_ECUDA;
+        }
+    }
+    return SPEC_OK;
 }
 
 }  // namespace
@@ -157,7 +1138,7 @@ extern "C" {
 
 size_t spec_tree_attention_workspace_size(int32_t N, int32_t Hq, int32_t Hkv, int32_t D)
 {
-    return heads_ok(N, Hq, Hkv, D) ? 256 : 0;
+    return heads_ok(N, Hq, Hkv, D) ? ws_layout(N, Hq / Hkv, D).total : 0;
 }
 
 int32_t spec_tree_attention(const spec_tree_attention_args *args, void *workspace,
@@ -166,9 +1147,9 @@ int32_t spec_tree_attention(const spec_tree_attention_args *args, void *workspac
     if (!args)
         return SPEC_EINVAL;
     const spec_tree_attention_args &a = *args;
+    const bool paged = a.page_table != nullptr;
     if (!heads_ok(a.N, a.Hq, a.Hkv, a.D) || a.B < 0 || a.B > 65535 ||
-        !page_size_ok(a.page_size, a.page_table != nullptr) || a.pages_per_seq < 1 ||
-        a.num_pages < 0 ||
+        !page_size_ok(a.page_size, paged) || a.pages_per_seq < 1 || a.num_pages < 0 ||
         (long long)a.pages_per_seq * a.page_size > INT32_MAX - SPEC_ATTN_MAX_NODES ||
         (a.dtype != SPEC_BF16 && a.dtype != SPEC_F16) || !(a.scale > 0.0f) || isinf(a.scale))
         return SPEC_EINVAL;
@@ -182,25 +1163,93 @@ int32_t spec_tree_attention(const spec_tree_attention_args *args, void *workspac
         !strides_ok(a.k_cache_stride) || !strides_ok(a.v_cache_stride) || !a.plan ||
         !aligned(a.plan, 256) || !workspace || !aligned(workspace, 256) ||
         !aligned(a.page_table, 4) || !aligned(a.out_lse, 4) ||
-        (!a.page_table && (a.pages_per_seq != 1 || a.num_pages < a.B)))
+        (!paged && (a.pages_per_seq != 1 || a.num_pages < a.B)))
         return SPEC_EINVAL;
-    if (workspace_bytes < spec_tree_attention_workspace_size(a.N, a.Hq, a.Hkv, a.D))
+    // TMA steps along a dimension by its stride: none may be 0 where there are two entries
+    const int32_t G = a.Hq / a.Hkv;
+    auto stepped = [](const int64_t (&s)[3], int64_t n0, int64_t n1, int64_t n2) {
+        return (n0 < 2 || s[0] > 0) && (n1 < 2 || s[1] > 0) && (n2 < 2 || s[2] > 0);
+    };
+    if (!stepped(a.q_stride, a.B, a.N, a.Hq) || !stepped(a.k_new_stride, a.B, a.N, a.Hkv) ||
+        !stepped(a.v_new_stride, a.B, a.N, a.Hkv) ||
+        !stepped(a.k_cache_stride, a.num_pages, a.page_size, a.Hkv) ||
+        !stepped(a.v_cache_stride, a.num_pages, a.page_size, a.Hkv))
+        return SPEC_EINVAL;
+    const WsLayout w = ws_layout(a.N, G, a.D);
+    if (workspace_bytes < w.total)
         return SPEC_ENOSPACE;
+
     AParams P;
-    P.a = a;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    P.plan = static_cast<const uint8_t *>(a.plan);
     P.lay = plan_layout(a.B, a.N);
-    P.G = a.Hq / a.Hkv;
-    const dim3 grid((unsigned int)a.B * (unsigned int)a.N, (unsigned int)a.Hq);
+    P.page_table = a.page_table;
+    P.v_new = a.v_new;
+    for (int i = 0; i < 3; ++i)
+        P.v_new_stride[i] = a.v_new_stride[i];
+    P.out = a.out;
+    P.lse = a.out_lse;
+    P.status = &reinterpret_cast<WsHeader *>(ws)->status;
+    P.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
+    P.part = reinterpret_cast<float *>(ws + w.part);
+    P.c = a.scale * LOG2E;
+    P.B = a.B;
+    P.N = a.N;
+    P.Hq = a.Hq;
+    P.Hkv = a.Hkv;
+    P.D = a.D;
+    P.G = G;
+    P.nodes_per_tile = BM / G;
+    P.row_tiles = row_tiles(a.N, G);
+    P.page_size = a.page_size;
+    P.pages_per_seq = a.pages_per_seq;
+    P.page_rows = paged && a.page_size < KT ? a.page_size : KT;
+    P.new_rows = a.N < KT ? (a.N + 7) / 8 * 8 : KT;
+    P.q_rows = P.nodes_per_tile * G;
+
+    CUtensorMap maps[5];
+    const uint64_t qd[5] = {(uint64_t)a.D, (uint64_t)G, (uint64_t)a.N, (uint64_t)a.Hkv,
+                            (uint64_t)a.B};
+    const int64_t qs[4] = {a.q_stride[2], a.q_stride[1], a.q_stride[2] * G, a.q_stride[0]};
+    const uint32_t qb[5] = {PANEL, (uint32_t)G, (uint32_t)P.nodes_per_tile, 1, 1};
+    const uint64_t nd[4] = {(uint64_t)a.D, (uint64_t)a.N, (uint64_t)a.Hkv, (uint64_t)a.B};
+    const uint32_t nb[4] = {PANEL, (uint32_t)P.new_rows, 1, 1};
+    const uint64_t cd[4] = {(uint64_t)a.D, (uint64_t)a.page_size, (uint64_t)a.Hkv,
+                            (uint64_t)(a.num_pages > 0 ? a.num_pages : 1)};
+    const uint32_t cb[4] = {PANEL, (uint32_t)P.page_rows, 1, 1};
+    auto order = [](const int64_t (&s)[3], int64_t (&o)[3]) {  // (slot or node, head, page or sequence)
+        o[0] = s[1];
+        o[1] = s[2];
+        o[2] = s[0];
+    };
+    int64_t kn[3], vn[3], kc[3], vc[3];
+    order(a.k_new_stride, kn);
+    order(a.v_new_stride, vn);
+    order(a.k_cache_stride, kc);
+    order(a.v_cache_stride, vc);
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return SPEC_ECUDA;
+    if (!make_map(&maps[0], a.q, a.dtype, 5, qd, qs, qb) ||
+        !make_map(&maps[1], a.k_new, a.dtype, 4, nd, kn, nb) ||
+        !make_map(&maps[2], a.v_new, a.dtype, 4, nd, vn, nb) ||
+        !make_map(&maps[3], a.k_cache, a.dtype, 4, cd, kc, cb) ||
+        !make_map(&maps[4], a.v_cache, a.dtype, 4, cd, vc, cb))
+        return SPEC_ECUDA;
+    DevInfo &di = g_dev[dev];
+    int sms = di.sms.load(std::memory_order_relaxed);
+    if (!sms) {
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            sms < 1)
+            return SPEC_ECUDA;
+        di.sms.store(sms, std::memory_order_relaxed);
+    }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (a.dtype == SPEC_BF16)
-        attention_kernel<SPEC_BF16><<<grid, KT, 0, st>>>(P);
-    else
-        attention_kernel<SPEC_F16><<<grid, KT, 0, st>>>(P);
-    if (cudaPeekAtLastError() != cudaSuccess) {
-        (void)cudaGetLastError();
-        return SPEC_ECUDA;
-    }
-    return SPEC_OK;
+        return a.D > PANEL ? launch<2, SPEC_BF16>(maps, P, sms, di, st)
+                           : launch<1, SPEC_BF16>(maps, P, sms, di, st);
+    return a.D > PANEL ? launch<2, SPEC_F16>(maps, P, sms, di, st)
+                       : launch<1, SPEC_F16>(maps, P, sms, di, st);
 }
 
 }  // extern "C"
