@@ -15,7 +15,9 @@ fallback.  Build it with ``__graft_entry__.build()`` (or
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 import threading
 
 SPEC_F32 = 0
@@ -81,6 +83,13 @@ class _LogitsArgs(ctypes.Structure):
                 + [(n, ctypes.c_int64) for n in ("allowed_stride_b", "allowed_stride_r")]
                 + [(n, ctypes.c_int32) for n in ("B", "R", "V", "H", "draft_cols", "bias_cols",
                                                  "dtype")])
+
+
+# The same structures packed in one go (the binding's own calls: filling a
+# ctypes structure field by field costs more than the smallest kernels).
+_pack_attention = struct.Struct("@5Q15q4Qf9i").pack
+_pack_commit = struct.Struct("@4Q16q5Q9i4x").pack
+_pack_logits = struct.Struct("@14Q2q7i4x").pack
 
 
 def library():
@@ -166,11 +175,11 @@ def library():
         lib.spec_tree_attention_workspace_size.restype = sz
         lib.spec_tree_attention_workspace_size.argtypes = [i32] * 4
         lib.spec_tree_attention.restype = i32
-        lib.spec_tree_attention.argtypes = [ctypes.POINTER(_AttentionArgs), vp, sz, vp]
+        lib.spec_tree_attention.argtypes = [vp, vp, sz, vp]
         lib.spec_tree_commit.restype = i32
-        lib.spec_tree_commit.argtypes = [ctypes.POINTER(_CommitArgs), vp]
+        lib.spec_tree_commit.argtypes = [vp, vp]
         lib.spec_process_logits.restype = i32
-        lib.spec_process_logits.argtypes = [ctypes.POINTER(_LogitsArgs), vp]
+        lib.spec_process_logits.argtypes = [vp, vp]
         _lib = lib
         return lib
 
@@ -955,81 +964,107 @@ def tree_to_device(tc, device="cuda"):
 # ------------------------------------------- tree attention and cache commit
 
 def _call_stream(stream, dev, tensors):
-    """The stream a call runs on.  Where that is not the current one, the
+    """(stream, whether it is the current one) of a call.  Where it is not, the
     tensors' memory is kept from reuse until the stream has passed the call."""
-    torch = _torch()
-    current = torch.cuda.current_stream(dev)
+    current = _torch().cuda.current_stream(dev)
     if stream is None or stream.cuda_stream == current.cuda_stream:
-        return current
+        return current, True
     for t in tensors:
         if t is not None:
             t.record_stream(stream)
-    return stream
+    return stream, False
 
 
-def _empty_on(s, shape, dtype, dev):
+def _empty_on(s, is_current, shape, dtype, dev):
     """An output allocated for use on stream `s`."""
     torch = _torch()
+    if is_current:
+        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(s):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _int32(name, t, shape, dev):
-    torch = _torch()
-    if tuple(t.shape) != shape or t.dtype != torch.int32:
-        raise ValueError(f"{name} must be int32 {shape}, got {t.dtype} {tuple(t.shape)}")
+def _launch(dev, what, fn, *args):
+    """fn(*args) with `dev` current."""
+    if _torch().cuda.current_device() == dev.index:
+        rc = fn(*args)
+    else:
+        with _on(dev):
+            rc = fn(*args)
+    if rc != SPEC_OK:
+        _check(rc, what)
+
+
+def _array(name, t, shape, dtype, dev):
+    """A contiguous array of the call's shape and dtype on its device."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
     if not t.is_cuda or not t.is_contiguous() or t.device != dev:
         raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
+    return t.data_ptr()
 
 
-def _head_strides(name, t, dev, step):
-    """The strides of all dimensions but the last, which must be contiguous;
-    each a multiple of `step` elements (a dimension of one entry has none)."""
+def _strided(name, t, dev, step):
+    """(address, strides of all dimensions but the last) of a tensor whose last
+    dimension is contiguous.  Strides are multiples of `step` elements; a
+    dimension of one entry has none."""
     if not t.is_cuda or t.device != dev:
         raise ValueError(f"{name} must be on {dev}")
-    st = t.stride()
-    if st[-1] != 1 and t.shape[-1] != 1:
+    shape, st, at = t.shape, t.stride(), t.data_ptr()
+    if st[-1] != 1 and shape[-1] != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    out = tuple(0 if n == 1 else s for n, s in zip(t.shape[:-1], st))
-    if step > 1 and (any(s % step for s in out) or t.data_ptr() % (2 * step)):
+    st = [s if n != 1 else 0 for n, s in zip(shape[:-1], st)]
+    if step > 1 and (at % (2 * step) or any([s % step for s in st])):
         raise ValueError(f"{name}: strides must be multiples of {step} elements and the data "
                          f"{2 * step}-byte aligned")
-    return out
+    return at, st
 
 
 def _geometry(k_cache, page_table, B, dev):
-    """(page_size, pages_per_seq, num_pages) of a cache [.., pages, slots, heads, D]."""
-    P, S = k_cache.shape[-4], k_cache.shape[-3]
+    """((page_size, pages_per_seq, num_pages), the table's address) of a cache
+    [.., pages, slots, heads, D]."""
+    P, S = k_cache.shape[-4:-2]
     if page_table is None:
         if P < B:
             raise ValueError(f"a contiguous cache needs a page for each of {B} sequences, got {P}")
-        return S, 1, P
+        return (S, 1, P), 0
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, pages_per_seq]")
     M = page_table.shape[1]
-    _int32("page_table", page_table, (B, M), dev)
-    return S, M, P
+    return (S, M, P), _array("page_table", page_table, (B, M), _torch().int32, dev)
+
+
+@functools.lru_cache(maxsize=256)
+def _plan_layout(B, N):
+    """Bytes of a plan, and the int32 offsets of its readable parts."""
+    lib = library()
+    return (lib.spec_tree_plan_size(B, N),
+            tuple(lib.spec_tree_plan_offset(B, N, i) // 4 for i in range(3)))
 
 
 class TreePlan:
     """What spec_tree_plan made: `positions` int32 [B, N], `status` int32 [B] and
     `mask` int32 [B, N, W] (bits of ancestors, include/spec_attn.h) are views
-    of `data`, which every layer's spec_tree_attention reads."""
+    of `data` (int32), which every layer's spec_tree_attention reads."""
 
     def __init__(self, B, N, geometry, data):
-        torch = _torch()
         self.B, self.N, self.geometry, self.data = B, N, geometry, data
-        lib, W = library(), 4 * ((N + 127) // 128)
 
-        def part(which, *shape):
-            at = lib.spec_tree_plan_offset(B, N, which)
-            n = 4
-            for x in shape:
-                n *= x
-            return data[at:at + n].view(torch.int32).view(*shape)
-        self.positions = part(SPEC_PLAN_POSITIONS, B, N)
-        self.status = part(SPEC_PLAN_STATUS, B)
-        self.mask = part(SPEC_PLAN_MASK, B, N, W)
+    def _part(self, which, shape, strides):
+        return self.data.as_strided(shape, strides, _plan_layout(self.B, self.N)[1][which])
+
+    @property
+    def positions(self):
+        return self._part(SPEC_PLAN_POSITIONS, (self.B, self.N), (self.N, 1))
+
+    @property
+    def status(self):
+        return self._part(SPEC_PLAN_STATUS, (self.B,), (1,))
+
+    @property
+    def mask(self):
+        W = 4 * ((self.N + 127) // 128)
+        return self._part(SPEC_PLAN_MASK, (self.B, self.N, W), (self.N * W, W, 1))
 
 
 def spec_tree_plan(parent, n_nodes, cache_len, k_cache, page_table=None, plan=None, stream=None):
@@ -1045,30 +1080,27 @@ def spec_tree_plan(parent, n_nodes, cache_len, k_cache, page_table=None, plan=No
     if parent.dim() != 2 or k_cache.dim() != 4:
         raise ValueError("parent must be [B, N] and k_cache [pages, slots, Hkv, D]")
     B, N = parent.shape
-    dev = parent.device
-    _int32("parent", parent, (B, N), dev)
-    _int32("n_nodes", n_nodes, (B,), dev)
-    _int32("cache_len", cache_len, (B,), dev)
-    geometry = _geometry(k_cache, page_table, B, dev)
-    lib = library()
-    need = lib.spec_tree_plan_size(B, N)
+    dev, i32 = parent.device, torch.int32
+    p = _array("parent", parent, (B, N), i32, dev)
+    n = _array("n_nodes", n_nodes, (B,), i32, dev)
+    c = _array("cache_len", cache_len, (B,), i32, dev)
+    geometry, table = _geometry(k_cache, page_table, B, dev)
+    need = _plan_layout(B, N)[0]
     if need == 0:
         raise ValueError(f"sizes out of range: B={B} N={N}")
-    s = _call_stream(stream, dev, (parent, n_nodes, cache_len, page_table,
-                                   plan.data if plan is not None else None))
-    if plan is None:
-        plan = TreePlan(B, N, geometry, _empty_on(s, (need,), torch.uint8, dev))
-    elif (plan.B, plan.N) != (B, N) or plan.data.device != dev:
+    if plan is not None and ((plan.B, plan.N) != (B, N) or plan.data.device != dev):
         raise ValueError(f"plan is for B={plan.B} N={plan.N} on {plan.data.device}")
+    s, cur = _call_stream(stream, dev, (parent, n_nodes, cache_len, page_table,
+                                        plan.data if plan is not None else None))
+    if plan is None:
+        plan = TreePlan(B, N, geometry, _empty_on(s, cur, (need // 4,), i32, dev))
     plan.geometry = geometry
-    with _on(dev):
-        rc = lib.spec_tree_plan(_ptr(parent), _ptr(n_nodes), _ptr(cache_len), _ptr(page_table),
-                                B, N, *geometry, _ptr(plan.data), need,
-                                ctypes.c_void_p(s.cuda_stream))
-    _check(rc, "spec_tree_plan")
+    _launch(dev, "spec_tree_plan", library().spec_tree_plan, p, n, c, table or None, B, N, *geometry,
+            plan.data.data_ptr(), need, s.cuda_stream)
     return plan
 
 
+@functools.lru_cache(maxsize=256)
 def spec_tree_attention_workspace_size(N: int, Hq: int, Hkv: int, D: int) -> int:
     return int(library().spec_tree_attention_workspace_size(N, Hq, Hkv, D))
 
@@ -1085,17 +1117,25 @@ def attention_workspace(N: int, Hq: int, Hkv: int, D: int, device=None, stream=N
     device = torch.device(device if device is not None else "cuda")
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
-    s = stream if stream is not None else torch.cuda.current_stream(device)
+    current = torch.cuda.current_stream(device)
+    s = stream if stream is not None else current
+    return _attention_workspace(N, Hq, Hkv, D, device, s, s.cuda_stream == current.cuda_stream)
+
+
+def _attention_workspace(N, Hq, Hkv, D, device, s, is_current):
+    torch = _torch()
     need = spec_tree_attention_workspace_size(N, Hq, Hkv, D)
     if need == 0:
         raise ValueError(f"sizes out of range: N={N} Hq={Hq} Hkv={Hkv} D={D}")
+    if not is_current:
+        with torch.cuda.stream(s):
+            return _attention_workspace(N, Hq, Hkv, D, device, s, True)
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(need, dtype=torch.uint8, device=device)
     key = (device.index, s.cuda_stream)
     ws = _attention_ws.get(key)
-    with torch.cuda.stream(s):
-        if torch.cuda.is_current_stream_capturing():
-            return torch.zeros(need, dtype=torch.uint8, device=device)
-        if ws is None or ws.numel() < need:
-            ws = _attention_ws[key] = torch.zeros(need, dtype=torch.uint8, device=device)
+    if ws is None or ws.numel() < need:
+        ws = _attention_ws[key] = torch.zeros(need, dtype=torch.uint8, device=device)
     return ws
 
 
@@ -1110,55 +1150,52 @@ def spec_tree_attention(q, k_new, v_new, k_cache, v_cache, plan, page_table=None
     Returns out [B, N, Hq, D] and, with want_lse, the rows' log-sum-exp
     float32 [B, N, Hq]; asynchronous like any CUDA op."""
     torch = _torch()
-    if any(t.dim() != 4 for t in (q, k_new, v_new, k_cache, v_cache)):
+    if not q.dim() == k_new.dim() == v_new.dim() == k_cache.dim() == v_cache.dim() == 4:
         raise ValueError("q, k_new, v_new, k_cache and v_cache must have 4 dimensions")
     B, N, Hq, D = q.shape
     Hkv = k_new.shape[2]
     P, S = k_cache.shape[:2]
-    if tuple(k_new.shape) != (B, N, Hkv, D) or v_new.shape != k_new.shape:
+    if k_new.shape != (B, N, Hkv, D) or v_new.shape != k_new.shape:
         raise ValueError(f"k_new and v_new must be {(B, N, Hkv, D)}")
-    if tuple(k_cache.shape) != (P, S, Hkv, D) or v_cache.shape != k_cache.shape:
+    if k_cache.shape != (P, S, Hkv, D) or v_cache.shape != k_cache.shape:
         raise ValueError(f"k_cache and v_cache must be [pages, slots, {Hkv}, {D}]")
-    if q.dtype == torch.bfloat16:
-        dt = SPEC_BF16
-    elif q.dtype == torch.float16:
-        dt = SPEC_F16
-    else:
-        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
-    if any(t.dtype != q.dtype for t in (k_new, v_new, k_cache, v_cache)):
+    dtype = q.dtype
+    if dtype != torch.bfloat16 and dtype != torch.float16:
+        raise TypeError(f"q must be bfloat16 or float16, got {dtype}")
+    if not dtype == k_new.dtype == v_new.dtype == k_cache.dtype == v_cache.dtype:
         raise TypeError("q, k_new, v_new, k_cache and v_cache must share a dtype")
     dev = q.device
-    geometry = _geometry(k_cache, page_table, B, dev)
-    if (plan.B, plan.N) != (B, N) or plan.geometry != geometry or plan.data.device != dev:
+    geometry, table = _geometry(k_cache, page_table, B, dev)
+    if (plan.B, plan.N, plan.geometry) != (B, N, geometry) or plan.data.device != dev:
         raise ValueError(f"plan is for B={plan.B} N={plan.N}, cache {plan.geometry} on "
                          f"{plan.data.device}; the call is for B={B} N={N}, {geometry} on {dev}")
-    a = _AttentionArgs()
-    for name, t in (("q", q), ("k_new", k_new), ("v_new", v_new), ("k_cache", k_cache),
-                    ("v_cache", v_cache)):
-        getattr(a, name + "_stride")[:] = _head_strides(name, t, dev, 8)
-        setattr(a, name, t.data_ptr())
+    q_at, q_st = _strided("q", q, dev, 8)
+    kn_at, kn_st = _strided("k_new", k_new, dev, 8)
+    vn_at, vn_st = _strided("v_new", v_new, dev, 8)
+    kc_at, kc_st = _strided("k_cache", k_cache, dev, 8)
+    vc_at, vc_st = _strided("v_cache", v_cache, dev, 8)
     scale = D ** -0.5 if scale is None else float(scale)
     if not 0.0 < scale < float("inf"):
         raise ValueError(f"scale must be finite and positive, got {scale}")
-    if page_table is not None and S % 128 and (S < 8 or S & (S - 1)):
+    if table and S % 128 and (S < 8 or S & (S - 1)):
         raise ValueError(f"page size {S}: a multiple of 128, or a power of two from 8")
-    s = _call_stream(stream, dev, (q, k_new, v_new, k_cache, v_cache, plan.data, page_table, out))
+    s, cur = _call_stream(stream, dev, (q, k_new, v_new, k_cache, v_cache, plan.data, page_table,
+                                        out, ws))
     if out is None:
-        out = _empty_on(s, (B, N, Hq, D), q.dtype, dev)
-    _dev_out("out", out, (B, N, Hq, D), q.dtype, dev)
-    lse = _empty_on(s, (B, N, Hq), torch.float32, dev) if want_lse else None
+        out = _empty_on(s, cur, (B, N, Hq, D), dtype, dev)
+    else:
+        _dev_out("out", out, (B, N, Hq, D), dtype, dev)
+    lse = _empty_on(s, cur, (B, N, Hq), torch.float32, dev) if want_lse else None
     if ws is None:
-        ws = attention_workspace(N, Hq, Hkv, D, dev, s)
-    _check_ws(ws, dev)
-    a.page_table = page_table.data_ptr() if page_table is not None else None
-    a.plan, a.out = plan.data.data_ptr(), out.data_ptr()
-    a.out_lse = lse.data_ptr() if want_lse else None
-    a.scale, a.B, a.N, a.Hq, a.Hkv, a.D, a.dtype = scale, B, N, Hq, Hkv, D, dt
-    a.page_size, a.pages_per_seq, a.num_pages = geometry
-    with _on(dev):
-        rc = library().spec_tree_attention(ctypes.byref(a), _ptr(ws), ws.numel(),
-                                           ctypes.c_void_p(s.cuda_stream))
-    _check(rc, "spec_tree_attention")
+        ws = _attention_workspace(N, Hq, Hkv, D, dev, s, cur)
+    else:
+        _check_ws(ws, dev)
+    args = _pack_attention(q_at, kn_at, vn_at, kc_at, vc_at, *q_st, *kn_st, *vn_st, *kc_st, *vc_st,
+                           table, plan.data.data_ptr(), out.data_ptr(),
+                           lse.data_ptr() if want_lse else 0, scale, B, N, Hq, Hkv, D, *geometry,
+                           SPEC_BF16 if dtype == torch.bfloat16 else SPEC_F16)
+    _launch(dev, "spec_tree_attention", library().spec_tree_attention, args, ws.data_ptr(),
+            ws.numel(), s.cuda_stream)
     return (out, lse) if want_lse else out
 
 
@@ -1179,41 +1216,34 @@ def spec_tree_commit(k_new, v_new, k_cache, v_cache, cache_len, out_num_accepted
     P, S = k_cache.shape[-4:-2]
     if v_new.shape != k_new.shape:
         raise ValueError("k_new and v_new must have one shape")
-    if tuple(k_cache.shape) != (*lead, P, S, Hkv, D) or v_cache.shape != k_cache.shape:
+    if k_cache.shape != (*lead, P, S, Hkv, D) or v_cache.shape != k_cache.shape:
         raise ValueError(f"k_cache and v_cache must be {(*lead, 'pages', 'slots', Hkv, D)}")
     if k_new.dtype not in (torch.bfloat16, torch.float16, torch.float32):
         raise TypeError(f"k_new must be bfloat16, float16 or float32, got {k_new.dtype}")
-    if any(t.dtype != k_new.dtype for t in (v_new, k_cache, v_cache)):
+    if not k_new.dtype == v_new.dtype == k_cache.dtype == v_cache.dtype:
         raise TypeError("k_new, v_new, k_cache and v_cache must share a dtype")
-    dev = k_new.device
-    _int32("cache_len", cache_len, (B,), dev)
-    _int32("out_num_accepted", out_num_accepted, (B,), dev)
-    if out_nodes is not None:
-        _int32("out_nodes", out_nodes, (B, N), dev)
-    geometry = _geometry(k_cache, page_table, B, dev)
-    a = _CommitArgs()
+    dev, i32 = k_new.device, torch.int32
+    length = _array("cache_len", cache_len, (B,), i32, dev)
+    accepted = _array("out_num_accepted", out_num_accepted, (B,), i32, dev)
+    nodes = _array("out_nodes", out_nodes, (B, N), i32, dev) if out_nodes is not None else 0
+    geometry, table = _geometry(k_cache, page_table, B, dev)
+    at, strides = [], []
     for name, t in (("k_new", k_new), ("v_new", v_new), ("k_cache", k_cache),
                     ("v_cache", v_cache)):
-        st = _head_strides(name, t, dev, 1)
-        getattr(a, name + "_stride")[:] = st if lead else (0, *st)
-        setattr(a, name, t.data_ptr())
-    s = _call_stream(stream, dev, (k_new, v_new, k_cache, v_cache, cache_len, out_num_accepted,
-                                   out_nodes, page_table, out_len))
+        a, st = _strided(name, t, dev, 1)
+        at.append(a)
+        strides += st if lead else (0, *st)
+    s, cur = _call_stream(stream, dev, (k_new, v_new, k_cache, v_cache, cache_len,
+                                        out_num_accepted, out_nodes, page_table, out_len))
     if out_len is None:
-        out_len = _empty_on(s, (B,), torch.int32, dev)
-    _dev_out("out_len", out_len, (B,), torch.int32, dev)
-    if B > 0 and out_len.data_ptr() == cache_len.data_ptr():
-        raise ValueError("out_len must not be cache_len itself")
-    a.cache_len, a.out_num_accepted = cache_len.data_ptr(), out_num_accepted.data_ptr()
-    a.out_nodes = out_nodes.data_ptr() if out_nodes is not None else None
-    a.page_table = page_table.data_ptr() if page_table is not None else None
-    a.out_len = out_len.data_ptr()
-    a.layers, a.B, a.N, a.Hkv, a.D = lead[0] if lead else 1, B, N, Hkv, D
-    a.page_size, a.pages_per_seq, a.num_pages = geometry
-    a.elem_size = k_new.element_size()
-    with _on(dev):
-        rc = library().spec_tree_commit(ctypes.byref(a), ctypes.c_void_p(s.cuda_stream))
-    _check(rc, "spec_tree_commit")
+        out_len = _empty_on(s, cur, (B,), i32, dev)
+    else:
+        _dev_out("out_len", out_len, (B,), i32, dev)
+        if B > 0 and out_len.data_ptr() == length:
+            raise ValueError("out_len must not be cache_len itself")
+    args = _pack_commit(*at, *strides, length, accepted, nodes, table, out_len.data_ptr(),
+                        lead[0] if lead else 1, B, N, Hkv, D, *geometry, k_new.element_size())
+    _launch(dev, "spec_tree_commit", library().spec_tree_commit, args, s.cuda_stream)
     return out_len
 
 
@@ -1240,19 +1270,18 @@ def spec_process_logits(logits, history=None, history_len=None, prompt_len=None,
         raise ValueError("logits must be [B, R, V]")
     B, R, V = logits.shape
     dt = _dtype_code(logits)
-    dev = logits.device
+    dev, i32, f32 = logits.device, torch.int32, torch.float32
     if not logits.is_cuda or not logits.is_contiguous():
         raise ValueError("logits must be a contiguous CUDA tensor")
-    a = _LogitsArgs()
+    h = hl = pl = dtok = par = nn = rep = freq = pres = bt = bv = al = 0
+    H = cols = M = sb = sr = 0
     if history is not None:
         if history.dim() != 2 or history_len is None or prompt_len is None:
             raise ValueError("history [B, H] comes with history_len and prompt_len [B]")
-        _int32("history", history, (B, history.shape[1]), dev)
-        _int32("history_len", history_len, (B,), dev)
-        _int32("prompt_len", prompt_len, (B,), dev)
-        a.H = history.shape[1]
-        a.history, a.history_len = history.data_ptr(), history_len.data_ptr()
-        a.prompt_len = prompt_len.data_ptr()
+        H = history.shape[1]
+        h = _array("history", history, (B, H), i32, dev)
+        hl = _array("history_len", history_len, (B,), i32, dev)
+        pl = _array("prompt_len", prompt_len, (B,), i32, dev)
     elif history_len is not None or prompt_len is not None:
         raise ValueError("history_len and prompt_len come with history")
     if draft_tokens is not None:
@@ -1260,50 +1289,45 @@ def spec_process_logits(logits, history=None, history_len=None, prompt_len=None,
         if parent is not None and cols != R or parent is None and cols not in (R - 1, R):
             raise ValueError(f"draft_tokens must be [B, {R}]" +
                              ("" if parent is not None else f" or [B, {R - 1}]"))
-        _int32("draft_tokens", draft_tokens, (B, cols), dev)
-        a.draft_tokens, a.draft_cols = draft_tokens.data_ptr(), cols
+        dtok = _array("draft_tokens", draft_tokens, (B, cols), i32, dev)
     if parent is not None:
         if draft_tokens is None:
             raise ValueError("parent comes with draft_tokens")
-        _int32("parent", parent, (B, R), dev)
-        a.parent = parent.data_ptr()
+        par = _array("parent", parent, (B, R), i32, dev)
     if n_nodes is not None:
-        _int32("n_nodes", n_nodes, (B,), dev)
-        a.n_nodes = n_nodes.data_ptr()
-    for name, t in (("repetition", repetition), ("frequency", frequency),
-                    ("presence", presence)):
-        if t is not None:
-            _dev_out(name, t, (B,), torch.float32, dev)
-            setattr(a, name, t.data_ptr())
+        nn = _array("n_nodes", n_nodes, (B,), i32, dev)
+    if repetition is not None:
+        rep = _array("repetition", repetition, (B,), f32, dev)
+    if frequency is not None:
+        freq = _array("frequency", frequency, (B,), f32, dev)
+    if presence is not None:
+        pres = _array("presence", presence, (B,), f32, dev)
     if (bias_tokens is None) != (bias_values is None):
         raise ValueError("bias_tokens and bias_values come together")
     if bias_tokens is not None:
         if bias_tokens.dim() != 2 or bias_tokens.shape[1] > SPEC_LOGITS_MAX_BIAS:
             raise ValueError(f"bias_tokens must be [B, M], M <= {SPEC_LOGITS_MAX_BIAS}")
-        shape = (B, bias_tokens.shape[1])
-        _int32("bias_tokens", bias_tokens, shape, dev)
-        _dev_out("bias_values", bias_values, shape, torch.float32, dev)
-        a.bias_tokens, a.bias_values = bias_tokens.data_ptr(), bias_values.data_ptr()
-        a.bias_cols = shape[1]
+        M = bias_tokens.shape[1]
+        bt = _array("bias_tokens", bias_tokens, (B, M), i32, dev)
+        bv = _array("bias_values", bias_values, (B, M), f32, dev)
     if allowed is not None:
         W = (V + 31) // 32
         if (allowed.dim() != 3 or allowed.shape[0] not in (1, B) or allowed.shape[1] not in (1, R)
-                or allowed.shape[2] != W or allowed.dtype != torch.int32 or not allowed.is_cuda
+                or allowed.shape[2] != W or allowed.dtype != i32 or not allowed.is_cuda
                 or allowed.device != dev or allowed.stride(2) != 1 and W > 1):
             raise ValueError(f"allowed must be int32 [{B} or 1, {R} or 1, {W}] on {dev}, its last "
                              "dimension contiguous")
-        a.allowed = allowed.data_ptr()
-        a.allowed_stride_b = allowed.stride(0) if allowed.shape[0] > 1 else 0
-        a.allowed_stride_r = allowed.stride(1) if allowed.shape[1] > 1 else 0
-    s = _call_stream(stream, dev, (logits, history, history_len, prompt_len, draft_tokens, parent,
-                                   n_nodes, repetition, frequency, presence, bias_tokens,
-                                   bias_values, allowed, out))
+        al = allowed.data_ptr()
+        sb = allowed.stride(0) if allowed.shape[0] > 1 else 0
+        sr = allowed.stride(1) if allowed.shape[1] > 1 else 0
+    s, cur = _call_stream(stream, dev, (logits, history, history_len, prompt_len, draft_tokens,
+                                        parent, n_nodes, repetition, frequency, presence,
+                                        bias_tokens, bias_values, allowed, out))
     if out is None:
-        out = _empty_on(s, (B, R, V), logits.dtype, dev)
-    _dev_out("out", out, (B, R, V), logits.dtype, dev)
-    a.logits, a.out = logits.data_ptr(), out.data_ptr()
-    a.B, a.R, a.V, a.dtype = B, R, V, dt
-    with _on(dev):
-        rc = library().spec_process_logits(ctypes.byref(a), ctypes.c_void_p(s.cuda_stream))
-    _check(rc, "spec_process_logits")
+        out = _empty_on(s, cur, (B, R, V), logits.dtype, dev)
+    else:
+        _dev_out("out", out, (B, R, V), logits.dtype, dev)
+    args = _pack_logits(logits.data_ptr(), out.data_ptr(), h, hl, pl, dtok, par, nn, rep, freq,
+                        pres, bt, bv, al, sb, sr, B, R, V, H, cols, M, dt)
+    _launch(dev, "spec_process_logits", library().spec_process_logits, args, s.cuda_stream)
     return out

@@ -33,6 +33,7 @@ using namespace spec_dev;
 
 constexpr int LTH = 256;      // threads per CTA
 constexpr int LUN = 4;        // vectors in flight per thread
+constexpr int HUN = 8;        // history tokens in flight per thread
 constexpr uint32_t IN_PROMPT = 0x80000000u;  // flags of a column's word; the rest is its count
 constexpr uint32_t DRAFTED = 0x40000000u;    // in the generated part of the history
 constexpr uint32_t COUNT = 0x3fffffffu;
@@ -105,7 +106,45 @@ __device__ float touched_value(const spec_process_logits_args &A, const LSmem &S
     return x;
 }
 
+// the touched elements t (bits) of a vector at column c
 template <int DT>
+__device__ __forceinline__ void touch(const spec_process_logits_args &A, const LSmem &S, int t0,
+                                      int c, int r, uint32_t t, const Penalty &pen, uint4 &raw)
+{
+    while (t) {
+        const int j = __ffs((int)t) - 1;
+        t &= t - 1;
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+        const int h = DT == SPEC_F32 ? j : j >> 1;
+        const uint32_t word = h == 0 ? w[0] : h == 1 ? w[1] : h == 2 ? w[2] : w[3];
+        const float x = __uint_as_float(DT == SPEC_F32 ? word
+                                        : (j & 1) ? (word & 0xffff0000u) : (word << 16));
+        Lg<DT>::put(raw, j, round_bits<DT>(touched_value(A, S, t0, c + j, r, x, pen)));
+    }
+}
+
+// -inf where the bits of `ok` are 0
+template <int DT>
+__device__ __forceinline__ void forbid(uint4 &raw, uint32_t ok)
+{
+    uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (DT == SPEC_F32) {
+            w[i] = (ok >> i) & 1u ? w[i] : 0xff800000u;
+        } else {
+            const uint32_t keep = ((ok >> (2 * i)) & 1u ? 0xffffu : 0u) |
+                                  ((ok >> (2 * i + 1)) & 1u ? 0xffff0000u : 0u);
+            w[i] = (w[i] & keep) | (0xff80ff80u & ~keep);
+        }
+    }
+    raw = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ALIGNED: V is a multiple of the vector, so a thread's vectors lie at the same
+// columns in every row; it keeps their touched bits and steps from row to row.
+// Otherwise each vector's place is worked out by itself.
+template <int DT, bool ALIGNED>
 __global__ void __launch_bounds__(LTH) logits_kernel(const LParams P)
 {
     using L = Lg<DT>;
@@ -146,16 +185,22 @@ __global__ void __launch_bounds__(LTH) logits_kernel(const LParams P)
     // the history's tokens of this tile
     if (!bad) {
         const int32_t *hist = A.history + (size_t)b * A.H;
-        for (int i = tid; i < hl; i += LTH) {
-            const int t = __ldg(hist + i);
-            bad |= t < 0 || t >= A.V;
-            const int c = t - t0;
-            if (c >= 0 && c < cols) {
-                if (i < pl)
-                    atomicOr(&S.cnt[c], IN_PROMPT);
-                else
-                    atomicAdd(&S.cnt[c], 1u);
-                atomicOr(&S.touched[c >> 5], 1u << (c & 31));
+        for (int i0 = tid; i0 < hl; i0 += HUN * LTH) {
+            int tok[HUN];
+#pragma unroll
+            for (int u = 0; u < HUN; ++u)
+                tok[u] = i0 + u * LTH < hl ? __ldg(hist + i0 + u * LTH) : t0 + cols;
+#pragma unroll
+            for (int u = 0; u < HUN; ++u) {
+                const int i = i0 + u * LTH, c = tok[u] - t0;
+                bad |= (tok[u] < 0 || tok[u] >= A.V) && i < hl;
+                if (c >= 0 && c < cols) {
+                    if (i < pl)
+                        atomicOr(&S.cnt[c], IN_PROMPT);
+                    else
+                        atomicAdd(&S.cnt[c], 1u);
+                    atomicOr(&S.touched[c >> 5], 1u << (c & 31));
+                }
             }
         }
         // drafted tokens: a chain's token i follows row i, a tree's belongs to node i
@@ -206,6 +251,45 @@ __global__ void __launch_bounds__(LTH) logits_kernel(const LParams P)
     if (rows <= 0)
         return;
     const int last_word = (A.V - 1) >> 5;
+    if (ALIGNED) {
+        constexpr uint32_t ALL = (1u << L::VEC) - 1u;
+        const size_t stride = (size_t)A.V / L::VEC;
+        for (int c = tid * L::VEC; c < cols; c += LTH * L::VEC) {
+            const size_t at = ((size_t)b * A.R + r0) * stride + (size_t)(t0 + c) / L::VEC;
+            const uint4 *src = reinterpret_cast<const uint4 *>(A.logits) + at;
+            uint4 *dst = reinterpret_cast<uint4 *>(A.out) + at;
+            if (bad) {
+                for (int r = 0; r < rows; ++r)
+                    dst[r * stride] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+                continue;
+            }
+            const uint32_t t = (S.touched[c >> 5] >> (c & 31)) & ALL;
+            const int shift = (t0 + c) & 31;
+            const uint32_t *mask = A.allowed ? A.allowed + b * A.allowed_stride_b +
+                r0 * A.allowed_stride_r + ((t0 + c) >> 5) : nullptr;
+            for (int r = 0; r < rows; r += LUN) {
+                uint4 raw[LUN];
+                uint32_t ok[LUN];
+#pragma unroll
+                for (int u = 0; u < LUN; ++u)
+                    if (r + u < rows) {
+                        raw[u] = __ldcs(src + (r + u) * stride);
+                        ok[u] = mask ? (__ldg(mask + (r + u) * A.allowed_stride_r) >> shift) & ALL
+                                     : ALL;
+                    }
+#pragma unroll
+                for (int u = 0; u < LUN; ++u)
+                    if (r + u < rows) {
+                        if (t & ok[u])
+                            touch<DT>(A, S, t0, c, r0 + r + u, t & ok[u], pen, raw[u]);
+                        if (ok[u] != ALL)
+                            forbid<DT>(raw[u], ok[u]);
+                        dst[(r + u) * stride] = raw[u];
+                    }
+            }
+        }
+        return;
+    }
     const int NV = P.C / L::VEC + 1;  // vectors a row can have, its ends included
     const int total = rows * NV;
     for (int i0 = tid; i0 < total; i0 += LUN * LTH) {
@@ -257,27 +341,9 @@ __global__ void __launch_bounds__(LTH) logits_kernel(const LParams P)
                     ok = (mask_from(m, t0 + lo, n, last_word) << skip) & have;
                     t &= ok;
                 }
-                while (t) {
-                    const int j = __ffs((int)t) - 1;
-                    t &= t - 1;
-                    const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-                    float x;
-                    if (DT == SPEC_F32) {
-                        x = __uint_as_float(j == 0 ? w[0] : j == 1 ? w[1] : j == 2 ? w[2] : w[3]);
-                    } else {
-                        const int h = j >> 1;
-                        const uint32_t word = h == 0 ? w[0] : h == 1 ? w[1] : h == 2 ? w[2] : w[3];
-                        x = __uint_as_float((j & 1) ? (word & 0xffff0000u) : (word << 16));
-                    }
-                    x = touched_value(A, S, t0, c + j, row[u], x, pen);
-                    L::put(raw[u], j, round_bits<DT>(x));
-                }
-                if (ok != ALL) {
-#pragma unroll
-                    for (int j = 0; j < L::VEC; ++j)
-                        if (!((ok >> j) & 1u))
-                            L::put(raw[u], j, L::NEG_INF_WORD & (L::ES == 4 ? 0xffffffffu : 0xffffu));
-                }
+                touch<DT>(A, S, t0, c, row[u], t, pen, raw[u]);
+                if (ok != ALL)
+                    forbid<DT>(raw[u], ok);
             }
             if (have == ALL) {
                 reinterpret_cast<uint4 *>(A.out)[e0[u] / L::VEC] = raw[u];
@@ -349,10 +415,17 @@ extern "C" int32_t spec_process_logits(const spec_process_logits_args *args, voi
     const dim3 grid((unsigned int)((a.V + P.C - 1) / P.C), (unsigned int)a.B,
                     (unsigned int)((a.R + P.rows_per_cta - 1) / P.rows_per_cta));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (a.dtype == SPEC_F32)
-        logits_kernel<SPEC_F32><<<grid, LTH, smem, st>>>(P);
-    else
-        logits_kernel<SPEC_BF16><<<grid, LTH, smem, st>>>(P);
+    if (a.dtype == SPEC_F32) {
+        if (a.V % 4 == 0)
+            logits_kernel<SPEC_F32, true><<<grid, LTH, smem, st>>>(P);
+        else
+            logits_kernel<SPEC_F32, false><<<grid, LTH, smem, st>>>(P);
+    } else {
+        if (a.V % 8 == 0)
+            logits_kernel<SPEC_BF16, true><<<grid, LTH, smem, st>>>(P);
+        else
+            logits_kernel<SPEC_BF16, false><<<grid, LTH, smem, st>>>(P);
+    }
     if (cudaPeekAtLastError() != cudaSuccess) {
         (void)cudaGetLastError();
         return SPEC_ECUDA;
