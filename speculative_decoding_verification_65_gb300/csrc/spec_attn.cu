@@ -13,7 +13,7 @@
 // kernel.  More rows are several row tiles (whole nodes each); the CTAs of
 // one key range run next to each other, so the second one finds the keys in L2.
 //
-// Roles in a CTA (one per SM, 10 warps):
+// Roles in a CTA (one per SM, 3 warpgroups; the third gives registers to the others):
 //   warps 0-3, 4-7  two softmax groups, one thread per row.  Group s takes the
 //                   tiles of its parity with scores, weights and sums of its
 //                   own (S_s, O_s in TMEM), so that one group's exponentials
@@ -72,7 +72,10 @@ constexpr int BM = 128;           // rows of a tile (TMEM lanes)
 constexpr int PANEL = 64;         // elements of a 128-byte swizzled row
 constexpr int PANEL_BYTES = 128 * 128;  // 128 rows (or keys) of one panel
 constexpr int SOFT_THREADS = 256;
-constexpr int THREADS = SOFT_THREADS + 64;
+constexpr int THREADS = SOFT_THREADS + 128;
+// 384 threads launch with 168 registers each, 64512; a softmax thread holds a
+// row's 128 scores: 256 * 224 + 128 * 56 = 64512
+constexpr int SOFT_REGS = 224, HELPER_REGS = 56;
 constexpr int MAX_CTAS = 192;     // the grid's and the workspace's bound while row tiles allow it
 constexpr float GROWTH = 8.0f;    // log2 of how far a maximum may run ahead of the sums' scale
 
@@ -141,29 +144,65 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32])
         : "r"(taddr) : "memory");
 }
 
-// 64 consecutive columns of this warp's 32 TMEM lanes, one lane per thread; they have
-// arrived when it returns
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[64])
+// 128 consecutive columns: four loads, one wait
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&a)[32], uint32_t (&b)[32],
+                                         uint32_t (&c)[32], uint32_t (&d)[32])
 {
-    __syncwarp();  // .sync.aligned: the whole warp, converged
+    __syncwarp();
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
         "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, "
-        "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, "
-        "%36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, "
-        "%53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63 "
-        "}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]),
-          "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
-          "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
-          "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]),
-          "=r"(r[63])
-        : "r"(taddr) : "memory");
+        "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31 "
+        "}, [%128];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, "
+        "%49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63 "
+        "}, [%129];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, "
+        "%81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95 "
+        "}, [%130];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, "
+        "%110, %111, %112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, "
+        "%124, %125, %126, %127 "
+        "}, [%131];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]),
+          "=r"(a[7]), "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]),
+          "=r"(a[14]), "=r"(a[15]), "=r"(a[16]), "=r"(a[17]), "=r"(a[18]), "=r"(a[19]),
+          "=r"(a[20]), "=r"(a[21]), "=r"(a[22]), "=r"(a[23]), "=r"(a[24]), "=r"(a[25]),
+          "=r"(a[26]), "=r"(a[27]), "=r"(a[28]), "=r"(a[29]), "=r"(a[30]), "=r"(a[31]),
+          "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]),
+          "=r"(b[7]), "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]),
+          "=r"(b[14]), "=r"(b[15]), "=r"(b[16]), "=r"(b[17]), "=r"(b[18]), "=r"(b[19]),
+          "=r"(b[20]), "=r"(b[21]), "=r"(b[22]), "=r"(b[23]), "=r"(b[24]), "=r"(b[25]),
+          "=r"(b[26]), "=r"(b[27]), "=r"(b[28]), "=r"(b[29]), "=r"(b[30]), "=r"(b[31]),
+          "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]), "=r"(c[4]), "=r"(c[5]), "=r"(c[6]),
+          "=r"(c[7]), "=r"(c[8]), "=r"(c[9]), "=r"(c[10]), "=r"(c[11]), "=r"(c[12]), "=r"(c[13]),
+          "=r"(c[14]), "=r"(c[15]), "=r"(c[16]), "=r"(c[17]), "=r"(c[18]), "=r"(c[19]),
+          "=r"(c[20]), "=r"(c[21]), "=r"(c[22]), "=r"(c[23]), "=r"(c[24]), "=r"(c[25]),
+          "=r"(c[26]), "=r"(c[27]), "=r"(c[28]), "=r"(c[29]), "=r"(c[30]), "=r"(c[31]),
+          "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]), "=r"(d[4]), "=r"(d[5]), "=r"(d[6]),
+          "=r"(d[7]), "=r"(d[8]), "=r"(d[9]), "=r"(d[10]), "=r"(d[11]), "=r"(d[12]), "=r"(d[13]),
+          "=r"(d[14]), "=r"(d[15]), "=r"(d[16]), "=r"(d[17]), "=r"(d[18]), "=r"(d[19]),
+          "=r"(d[20]), "=r"(d[21]), "=r"(d[22]), "=r"(d[23]), "=r"(d[24]), "=r"(d[25]),
+          "=r"(d[26]), "=r"(d[27]), "=r"(d[28]), "=r"(d[29]), "=r"(d[30]), "=r"(d[31])
+        : "r"(taddr), "r"(taddr + 32), "r"(taddr + 64), "r"(taddr + 96)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16])
+{
+    __syncwarp();
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
+        "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16 "
+        "};"
+        :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+          "r"(r[15])
+        : "memory");
 }
 
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32])
@@ -249,6 +288,16 @@ __device__ __forceinline__ void mma_commit(unsigned long long *bar)
         :: "r"(smem_addr(bar)) : "memory");
 }
 
+// one lane of a converged warp, always the same one
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // Shared-memory matrix descriptors, 128-byte swizzle (version 1, mode 2).
 // K-major (Q and K): rows of 128 bytes, 8-row groups 1024 bytes apart.
 __device__ __forceinline__ uint64_t desc_k(uint32_t saddr)
@@ -308,13 +357,12 @@ __device__ __forceinline__ uint32_t nonfinite(uint32_t w)
     return ((w & E) == E ? 0xffffu : 0u) | (((w >> 16) & E) == E ? 0xffff0000u : 0u);
 }
 
-// Scores of columns past `keys` or with a 0 bit in w1:w0 become -inf.
-template <int N>
-__device__ __forceinline__ void hide(uint32_t (&x)[N], int keys, uint32_t w0, uint32_t w1)
+// Scores of columns past `keys` or with a 0 bit become -inf.
+__device__ __forceinline__ void hide(uint32_t (&x)[32], int keys, uint32_t bits)
 {
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-        if (j >= keys || !(((j < 32 ? w0 : w1) >> (j & 31)) & 1u))
+    for (int j = 0; j < 32; ++j)
+        if (j >= keys || !((bits >> j) & 1u))
             x[j] = 0xff800000u;
 }
 
@@ -480,150 +528,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         return false;
     };
 
-    if (warp == 8) {
-        // ---------------------------------------------------- TMA producer
-        uint32_t t = 0, items = 0;           // tiles and items so far
-        uint32_t issued[2] = {0, 0};         // tiles of K and of V whose loads were issued
-        bool ok = true;
-        for_pieces(P, cum, u0, u1, rt, [&](const Piece &p) {
-            if (p.idle || !ok)
-                return;
-            ok = __all_sync(0xffffffffu, wait(&S.qempty, (items & 1u) ^ 1u));
-            if (!ok)
-                return;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&S.qfull, (uint32_t)(P.q_rows * 128 * NP));
-                for (int i = 0; i < NP; ++i)
-                    tma_load_5d(q_s + i * PANEL_BYTES, &mq, i * PANEL, 0, rt * P.nodes_per_tile,
-                                p.h, p.b, &S.qfull);
-            }
-            ++items;
-            for (int i = 0; i < p.n && ok; ++i, ++t) {
-                bool cached;
-                const int jt = p.tile0 + i;
-                const int keys = tile_keys(p, jt, cached);
-                // box of this lane: its rows of the tile and its page
-                const int rows = cached ? P.page_rows : P.new_rows;
-                const int at = lane * rows;
-                const bool mine = at < keys;
-                int y, w;
-                if (cached) {
-                    const int pos = jt * KT + at;
-                    y = pos;
-                    w = p.b;
-                    if (P.page_table && mine) {
-                        const int e = pos / P.page_size;
-                        w = e < P.pages_per_seq
-                            ? __ldg(P.page_table + (size_t)p.b * P.pages_per_seq + e) : -1;
-                        y = pos - e * P.page_size;
-                    }
-                } else {
-                    y = (jt - (p.len + KT - 1) / KT) * KT + at;
-                    w = p.b;
-                }
-                const uint32_t bytes = (uint32_t)(((keys + rows - 1) / rows) * rows * 128 * NP);
-                const int st = (int)(t % C::STAGES);
-                const uint32_t ph = (t / C::STAGES) & 1u;
-#pragma unroll
-                for (int side = 0; side < 2; ++side) {
-                    unsigned long long *empty = side ? &S.vempty[st] : &S.kempty[st];
-                    unsigned long long *full = side ? &S.vfull[st] : &S.kfull[st];
-                    const CUtensorMap *map = cached ? (side ? &mvc : &mkc) : (side ? &mvn : &mkn);
-                    ok = __all_sync(0xffffffffu, wait(empty, ph ^ 1u));
-                    if (!ok)
-                        break;
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(full, bytes);
-                    __syncwarp();
-                    issued[side] = t + 1;
-                    if (mine) {
-                        const uint32_t dst = (side ? v_s : k_s) + st * C::TILE + at * 128;
-#pragma unroll
-                        for (int d = 0; d < NP; ++d)
-                            tma_load_4d(dst + d * PANEL_BYTES, map, d * PANEL, y, p.h, w, full);
-                    }
-                }
-            }
-        });
-        if (!ok) {
-            // the loads in flight land first: each barrier's last phase that has a load
-            for (int side = 0; side < 2; ++side) {
-                const uint32_t n = issued[side];
-                for (uint32_t j = n > C::STAGES ? n - C::STAGES : 0; j < n; ++j)
-                    (void)mbar_wait(side ? &S.vfull[j % C::STAGES] : &S.kfull[j % C::STAGES],
-                                    (j / C::STAGES) & 1u);
-            }
-            if (items)
-                (void)mbar_wait(&S.qfull, (items - 1) & 1u);
-        }
-    } else if (warp == 9) {
-        // ------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            uint32_t tk = 0, tv = 0, items = 0, cnt[2] = {0, 0};
-            bool ok = true, issued = false;
-            const int ksteps = (P.D + 15) / 16;
-            const int dcols = ksteps * 16;
-            auto scores = [&](const Piece &p, int i) {  // S(i) = Q K(i)^T
-                bool cached;
-                const int keys = tile_keys(p, p.tile0 + i, cached);
-                const int st = (int)(tk % C::STAGES);
-                ok = ok && wait(&S.kfull[st], (tk / C::STAGES) & 1u);
-                if (!ok)
-                    return;
-                tc_fence_after();
-                const uint32_t id = idesc<DT>((keys + 15) & ~15, false);
-                const uint32_t d = tmem + (uint32_t)((i & 1) * KT);
-                const uint32_t kb = k_s + st * C::TILE;
-                for (int s = 0; s < ksteps; ++s) {
-                    const uint32_t off = (uint32_t)((s >> 2) * PANEL_BYTES + (s & 3) * 32);
-                    mma_ss(d, desc_k(q_s + off), desc_k(kb + off), id, s ? 1u : 0u);
-                }
-                issued = true;
-                mma_commit(&S.kempty[st]);
-                mma_commit(&S.sfull[i & 1]);
-                if (i == p.n - 1)
-                    mma_commit(&S.qempty);
-                ++tk;
-            };
-            for_pieces(P, cum, u0, u1, rt, [&](const Piece &p) {
-                if (p.idle || !ok)
-                    return;
-                ok = wait(&S.qfull, items & 1u);
-                ++items;
-                for (int i = 0; i < 2 && i < p.n && ok; ++i)
-                    scores(p, i);
-                for (int i = 0; i < p.n && ok; ++i) {
-                    bool cached;
-                    const int keys = tile_keys(p, p.tile0 + i, cached);
-                    const int s = i & 1, st = (int)(tv % C::STAGES);
-                    ok = wait(&S.vfull[st], (tv / C::STAGES) & 1u) &&
-                         wait(&S.pready[s], cnt[s] & 1u);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    const uint32_t id = idesc<DT>(dcols, true);
-                    const uint32_t d = tmem + (uint32_t)(2 * KT + s * C::DP);
-                    const uint32_t a = tmem + (uint32_t)(s * KT);
-                    const uint32_t vb = v_s + st * C::TILE;
-                    const int steps = (keys + 15) / 16;
-                    for (int x = 0; x < steps; ++x)  // 16 keys: 8 columns of P, 2 KB of V
-                        mma_ts(d, a + (uint32_t)(x * 8), desc_mn(vb + x * 2048), id,
-                               (i >= 2 || x) ? 1u : 0u);
-                    mma_commit(&S.vempty[st]);
-                    mma_commit(&S.pvdone[s]);
-                    ++tv;
-                    ++cnt[s];
-                    if (i + 2 < p.n)
-                        scores(p, i + 2);
-                }
-            });
-            if (!ok && issued) {  // the products in flight complete (bounded)
-                mma_commit(&S.drain);
-                (void)mbar_wait(&S.drain, 0u);
-            }
-        }
-        __syncwarp();
-    } else {
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(SOFT_REGS));
         // ---------------------------------------------------- softmax groups
         const int s = warp >> 2;                 // the group
         const int quarter = warp & 3;
@@ -718,24 +624,26 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc_fence_after();
                 uint32_t zero_w[4] = {0, 0, 0, 0};  // keys whose weight is 0 (with any_bad only)
                 if (warp_live) {
-                    // two passes over the scores, 64 columns at a time: they stay in TMEM, where a
-                    // second read costs less than the registers to keep 128 of them
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t x[64];
-                        tmem_ld(t_s + h * 64, x);
-                        if (masked)
-                            hide<64>(x, keys - h * 64, h ? see.z : see.x, h ? see.w : see.y);
-#pragma unroll
-                        for (int j = 0; j < 64; j += 8) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(x[j + 2 * k]),
-                                                           __uint_as_float(x[j + 2 * k + 1])));
-                        }
+                    uint32_t x[4][32];
+                    tmem_ld4(t_s, x[0], x[1], x[2], x[3]);
+                    if (masked) {
+                        hide(x[0], keys, see.x);
+                        hide(x[1], keys - 32, see.y);
+                        hide(x[2], keys - 64, see.z);
+                        hide(x[3], keys - 96, see.w);
                     }
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    float mx[4];
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        mx[h] = __uint_as_float(x[h][0]);
+#pragma unroll
+                        for (int j = 1; j < 31; j += 2)
+                            mx[h] = fmaxf(fmaxf(mx[h], __uint_as_float(x[h][j])),
+                                          __uint_as_float(x[h][j + 1]));
+                        mx[h] = fmaxf(mx[h], __uint_as_float(x[h][31]));
+                    }
+                    float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    top = fmaxf(top, -INFINITY);  // a row of NaN scores has none
                     if (i == s) {
                         m = top;
                     } else {
@@ -745,7 +653,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             l *= f;
                             if (grown)
                                 m = top;
-#pragma unroll
+#pragma unroll 1
                             for (int d = 0; d < C::DP; d += 32) {
                                 uint32_t o[32];
                                 tmem_ld(t_o + d, o);
@@ -760,15 +668,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const unsigned long long shift2 = f2(shift, shift);
                     unsigned long long sum[2] = {0ull, 0ull};
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t x[64], pk[32];
-                        tmem_ld(t_s + h * 64, x);
-                        if (masked)
-                            hide<64>(x, keys - h * 64, h ? see.z : see.x, h ? see.w : see.y);
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t pk[16];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
+                        for (int j = 0; j < 16; ++j) {
                             float a0, a1;
-                            f2_split(fma2(f2_bits(x[2 * j], x[2 * j + 1]), c2, shift2), a0, a1);
+                            f2_split(fma2(f2_bits(x[h][2 * j], x[h][2 * j + 1]), c2, shift2), a0, a1);
                             a0 = ex2(a0);
                             a1 = ex2(a1);
                             sum[j & 1] = add2(sum[j & 1], f2(a0, a1));
@@ -776,14 +681,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                         if (any_bad) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                zero_w[h * 2 + (j >> 4)] |=
-                                    ((pk[j] & 0x7fffu) == 0 ? 1u : 0u) << ((2 * j) & 31) |
-                                    ((pk[j] & 0x7fff0000u) == 0 ? 2u : 0u) << ((2 * j) & 31);
-                            }
+                            for (int j = 0; j < 16; ++j)
+                                zero_w[h] |= ((pk[j] & 0x7fffu) == 0 ? 1u : 0u) << (2 * j) |
+                                             ((pk[j] & 0x7fff0000u) == 0 ? 2u : 0u) << (2 * j);
                         }
-                        // weights 64 h on lie in columns 32 h on: over scores that were read
-                        tmem_st(t_s + h * 32, pk);
+                        tmem_st(t_s + h * 16, pk);
                     }
                     float s0, s1;
                     f2_split(add2(sum[0], sum[1]), s0, s1);
@@ -906,6 +808,176 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc_fence_before();
             group_sync(1, SOFT_THREADS);  // O and the exchanged statistics are free again
         });
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(HELPER_REGS));
+    if (warp == 8) {
+        // ---------------------------------------------------- TMA producer
+        uint32_t t = 0, items = 0;           // tiles and items so far
+        uint32_t issued[2] = {0, 0};         // tiles of K and of V whose loads were issued
+        bool ok = true;
+        for_pieces(P, cum, u0, u1, rt, [&](const Piece &p) {
+            if (p.idle || !ok)
+                return;
+            ok = __all_sync(0xffffffffu, wait(&S.qempty, (items & 1u) ^ 1u));
+            if (!ok)
+                return;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&S.qfull, (uint32_t)(P.q_rows * 128 * NP));
+                for (int i = 0; i < NP; ++i)
+                    tma_load_5d(q_s + i * PANEL_BYTES, &mq, i * PANEL, 0, rt * P.nodes_per_tile,
+                                p.h, p.b, &S.qfull);
+            }
+            ++items;
+            for (int i = 0; i < p.n && ok; ++i, ++t) {
+                bool cached;
+                const int jt = p.tile0 + i;
+                const int keys = tile_keys(p, jt, cached);
+                // box of this lane: its rows of the tile and its page
+                const int rows = cached ? P.page_rows : P.new_rows;
+                const int at = lane * rows;
+                const bool mine = at < keys;
+                int y, w;
+                if (cached) {
+                    const int pos = jt * KT + at;
+                    y = pos;
+                    w = p.b;
+                    if (P.page_table && mine) {
+                        const int e = pos / P.page_size;
+                        w = e < P.pages_per_seq
+                            ? __ldg(P.page_table + (size_t)p.b * P.pages_per_seq + e) : -1;
+                        y = pos - e * P.page_size;
+                    }
+                } else {
+                    y = (jt - (p.len + KT - 1) / KT) * KT + at;
+                    w = p.b;
+                }
+                const uint32_t bytes = (uint32_t)(((keys + rows - 1) / rows) * rows * 128 * NP);
+                const int st = (int)(t % C::STAGES);
+                const uint32_t ph = (t / C::STAGES) & 1u;
+#pragma unroll
+                for (int side = 0; side < 2; ++side) {
+                    unsigned long long *empty = side ? &S.vempty[st] : &S.kempty[st];
+                    unsigned long long *full = side ? &S.vfull[st] : &S.kfull[st];
+                    const CUtensorMap *map = cached ? (side ? &mvc : &mkc) : (side ? &mvn : &mkn);
+                    ok = __all_sync(0xffffffffu, wait(empty, ph ^ 1u));
+                    if (!ok)
+                        break;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(full, bytes);
+                    __syncwarp();
+                    issued[side] = t + 1;
+                    if (mine) {
+                        const uint32_t dst = (side ? v_s : k_s) + st * C::TILE + at * 128;
+#pragma unroll
+                        for (int d = 0; d < NP; ++d)
+                            tma_load_4d(dst + d * PANEL_BYTES, map, d * PANEL, y, p.h, w, full);
+                    }
+                }
+            }
+        });
+        if (!ok) {
+            // the loads in flight land first: each barrier's last phase that has a load
+            for (int side = 0; side < 2; ++side) {
+                const uint32_t n = issued[side];
+                for (uint32_t j = n > C::STAGES ? n - C::STAGES : 0; j < n; ++j)
+                    (void)mbar_wait(side ? &S.vfull[j % C::STAGES] : &S.kfull[j % C::STAGES],
+                                    (j / C::STAGES) & 1u);
+            }
+            if (items)
+                (void)mbar_wait(&S.qfull, (items - 1) & 1u);
+        }
+    } else if (warp == 9) {
+        // ------------------------------------------------------ MMA issuer
+        // The whole warp runs the loop and one elected lane issues: what the products are
+        // given then stays in uniform registers (issued from under `lane == 0` each product
+        // took about 120 clocks to issue, twice its time in the tensor pipe)
+        uint32_t tk = 0, tv = 0, items = 0, cnt[2] = {0, 0};
+        bool ok = true, issued = false;
+        const int ksteps = (P.D + 15) / 16;
+        const uint32_t id_o = idesc<DT>(ksteps * 16, true);
+        auto all = [](bool x) -> bool { return __all_sync(0xffffffffu, x); };
+        auto scores = [&](const Piece &p, int i) {  // S(i) = Q K(i)^T
+            bool cached;
+            const int keys = tile_keys(p, p.tile0 + i, cached);
+            const int st = (int)(tk % C::STAGES);
+            ok = all(wait(&S.kfull[st], (tk / C::STAGES) & 1u));
+            if (!ok)
+                return;
+            tc_fence_after();
+            const uint32_t id = idesc<DT>((keys + 15) & ~15, false);
+            const uint32_t d = tmem + (uint32_t)((i & 1) * KT);
+            const uint64_t qd = desc_k(q_s), kd = desc_k(k_s + st * C::TILE);
+            if (elect_one()) {
+                if (ksteps == NP * 4) {
+#pragma unroll
+                    for (int x = 0; x < NP * 4; ++x) {
+                        const uint64_t off = (uint64_t)(((x >> 2) * PANEL_BYTES + (x & 3) * 32) >> 4);
+                        mma_ss(d, qd + off, kd + off, id, x ? 1u : 0u);
+                    }
+                } else {
+                    for (int x = 0; x < ksteps; ++x) {
+                        const uint64_t off = (uint64_t)(((x >> 2) * PANEL_BYTES + (x & 3) * 32) >> 4);
+                        mma_ss(d, qd + off, kd + off, id, x ? 1u : 0u);
+                    }
+                }
+                mma_commit(&S.kempty[st]);
+                mma_commit(&S.sfull[i & 1]);
+                if (i == p.n - 1)
+                    mma_commit(&S.qempty);
+            }
+            __syncwarp();
+            issued = true;
+            ++tk;
+        };
+        for_pieces(P, cum, u0, u1, rt, [&](const Piece &p) {
+            if (p.idle || !ok)
+                return;
+            ok = all(wait(&S.qfull, items & 1u));
+            ++items;
+            for (int i = 0; i < 2 && i < p.n && ok; ++i)
+                scores(p, i);
+            for (int i = 0; i < p.n && ok; ++i) {
+                bool cached;
+                const int keys = tile_keys(p, p.tile0 + i, cached);
+                const int s = i & 1, st = (int)(tv % C::STAGES);
+                ok = all(wait(&S.vfull[st], (tv / C::STAGES) & 1u) &&
+                         wait(&S.pready[s], cnt[s] & 1u));
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(2 * KT + s * C::DP);
+                const uint32_t a = tmem + (uint32_t)(s * KT);
+                const uint64_t vd = desc_mn(v_s + st * C::TILE);
+                const uint32_t more = i >= 2 ? 1u : 0u;
+                if (elect_one()) {
+                    // 16 keys a step: 8 columns of P, 2 KB of V
+                    if (keys > KT - 16) {
+#pragma unroll
+                        for (int x = 0; x < KT / 16; ++x)
+                            mma_ts(d, a + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)), id_o,
+                                   x ? 1u : more);
+                    } else {
+                        for (int x = 0; x < (keys + 15) / 16; ++x)
+                            mma_ts(d, a + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)), id_o,
+                                   x ? 1u : more);
+                    }
+                    mma_commit(&S.vempty[st]);
+                    mma_commit(&S.pvdone[s]);
+                }
+                __syncwarp();
+                ++tv;
+                ++cnt[s];
+                if (i + 2 < p.n)
+                    scores(p, i + 2);
+            }
+        });
+        if (!ok && issued) {  // the products in flight complete (bounded)
+            if (elect_one())
+                mma_commit(&S.drain);
+            __syncwarp();
+            (void)mbar_wait(&S.drain, 0u);
+        }
+    }
     }
     tc_fence_before();
     __syncthreads();
