@@ -92,10 +92,11 @@ int32_t spec_tree_plan(const int32_t *parent, const int32_t *n_nodes, const int3
  * Scores, the softmax's statistics and the weighted sum are held in fp32;
  * each weight is rounded to the dtype before its product with v.
  * The workspace has spec_tree_attention_workspace_size bytes (0 for sizes out
- * of range), 256-byte aligned, zeroed once after allocation
- * (spec_verify_workspace_reset); calls in flight must not share it.  Its
- * status reads back through spec_verify_read_status: SPEC_DEV_WAIT_TIMEOUT
- * after a wait inside a kernel gave up, until the next reset.  No allocation.
+ * of range), 256-byte aligned; it need not be cleared, and calls in flight
+ * must not share it.  Up to two kernels on `stream`, no allocation.
+ * A wait inside the kernel that gives up marks the plan:
+ * spec_verify_read_status(plan, ..) reads SPEC_DEV_WAIT_TIMEOUT until the
+ * plan is made again (SPEC_DEV_OK otherwise).
  */
 typedef struct spec_tree_attention_args {
     const void *q, *k_new, *v_new, *k_cache, *v_cache;

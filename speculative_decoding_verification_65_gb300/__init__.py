@@ -1050,6 +1050,11 @@ class TreePlan:
     def __init__(self, B, N, geometry, data):
         self.B, self.N, self.geometry, self.data = B, N, geometry, data
 
+    def read_status(self, stream=None):
+        """SPEC_DEV_OK, or SPEC_DEV_WAIT_TIMEOUT after a wait inside an attention
+        kernel that read this plan gave up.  Synchronises the stream."""
+        return spec_verify_read_status(self.data, stream)
+
     def _part(self, which, shape, strides):
         return self.data.as_strided(shape, strides, _plan_layout(self.B, self.N)[1][which])
 
@@ -1109,8 +1114,8 @@ _attention_ws = {}
 
 
 def attention_workspace(N: int, Hq: int, Hkv: int, D: int, device=None, stream=None):
-    """A zeroed workspace for spec_tree_attention, cached per (device, stream)
-    and apart from spec_verify's.  While the stream is being captured into a
+    """A workspace for spec_tree_attention, cached per (device, stream) and
+    apart from spec_verify's.  While the stream is being captured into a
     graph it is a new one, in the graph's own memory: a replay may overlap
     later calls on the stream."""
     torch = _torch()
@@ -1131,11 +1136,11 @@ def _attention_workspace(N, Hq, Hkv, D, device, s, is_current):
         with torch.cuda.stream(s):
             return _attention_workspace(N, Hq, Hkv, D, device, s, True)
     if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(need, dtype=torch.uint8, device=device)
+        return torch.empty(need, dtype=torch.uint8, device=device)
     key = (device.index, s.cuda_stream)
     ws = _attention_ws.get(key)
     if ws is None or ws.numel() < need:
-        ws = _attention_ws[key] = torch.zeros(need, dtype=torch.uint8, device=device)
+        ws = _attention_ws[key] = torch.empty(need, dtype=torch.uint8, device=device)
     return ws
 
 

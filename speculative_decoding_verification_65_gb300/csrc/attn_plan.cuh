@@ -18,7 +18,8 @@ struct PlanSeq {
     int pad;
 };
 
-// header | sequences [B] | tile prefix sums [B + 1] | positions [B][N] |
+// header (the device status word of the attention calls that read the plan) |
+// sequences [B] | tile prefix sums [B + 1] | positions [B][N] |
 // status [B] | mask [B][N][W]
 struct PlanLayout {
     size_t seq, cum, positions, status, mask, total;

@@ -19,12 +19,16 @@
 //                   own (S_s, O_s in TMEM), so that one group's exponentials
 //                   run under the other's products.  The weights go back to
 //                   TMEM in the place of the scores, as the A operand of P V.
-//                   The two halves are joined when the piece ends.
-//   warp 8          TMA: Q of an item, then its K and V tiles, each a ring of
-//                   stages; pages smaller than a tile are boxes of one tile
+//                   The two groups' sums are joined when the piece ends.
+//   warp 8          TMA of the K and V tiles, each a ring of stages; pages
+//                   smaller than a tile are boxes of one tile
 //   warp 9          issues the products in order: S(i) first two, then
 //                   O(i), S(i + 2), ...; a commit behind S(i + 2) so also
 //                   says that O(i) is done
+//   warp 10         TMA of an item's Q
+//   warp 11         walks the CTA's share and hands the pieces of it out
+//                   through a small ring: what a piece is costs several
+//                   dependent loads, which would stall every role at each item
 // TMEM: S_0, S_1 (128 columns each), O_0, O_1 (up to 128 each).
 //
 // A row's sums are rescaled only when its maximum has grown by more than 2^8
@@ -77,6 +81,7 @@ constexpr int THREADS = SOFT_THREADS + 128;
 // row's 128 scores: 256 * 224 + 128 * 56 = 64512
 constexpr int SOFT_REGS = 224, HELPER_REGS = 56;
 constexpr int MAX_CTAS = 192;     // the grid's and the workspace's bound while row tiles allow it
+constexpr int RING = 4;           // pieces handed out ahead
 constexpr float GROWTH = 8.0f;    // log2 of how far a maximum may run ahead of the sums' scale
 
 template <int NP>
@@ -88,9 +93,22 @@ struct Cfg {
     static constexpr int DP = NP * PANEL;  // columns of O
 };
 
+// A run of one item's key tiles inside a CTA's share.
+struct Piece {
+    int b, h;
+    int tile0, n;    // first tile and number of tiles (0: the share has ended)
+    int tiles;       // of the whole item
+    int len, nn;     // cache length and nodes
+    int status;
+    int idle;        // nothing to compute: no live row in this row tile
+    int first;       // 1 when the share starts inside the item or with it
+};
+
 struct Tail {
     unsigned long long kfull[6], kempty[6], vfull[6], vempty[6];
     unsigned long long qfull, qempty, sfull[2], pready[2], pvdone[2], drain;
+    unsigned long long pfull[RING], pempty[RING], join, noted[2];
+    Piece piece[RING];
     uint32_t tmem_base;
     int abort_flag;
     uint32_t bad[2][2][4];  // keys of a group's tile (alternating) whose values are not all finite
@@ -237,10 +255,6 @@ __device__ __forceinline__ void fence_async_shared()
 {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
-__device__ __forceinline__ void group_sync(int id, int threads)
-{
-    asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
-}
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y,
                                             int z, int w, unsigned long long *bar)
@@ -368,17 +382,6 @@ __device__ __forceinline__ void hide(uint32_t (&x)[32], int keys, uint32_t bits)
 
 // ------------------------------------------------------------------- work
 
-// A run of one item's key tiles inside a CTA's share.
-struct Piece {
-    int b, h;
-    int tile0, n;    // first tile and number of tiles
-    int tiles;       // of the whole item
-    int len, nn;     // cache length and nodes
-    int status;
-    bool idle;       // nothing to compute: no live row in this row tile
-    long long u0;    // the item's first unit
-};
-
 // Sequence of unit u: the last b with cum[b] * Hkv <= u.
 __device__ __forceinline__ int find_seq(const long long *cum, int B, int Hkv, long long u)
 {
@@ -393,42 +396,12 @@ __device__ __forceinline__ int find_seq(const long long *cum, int B, int Hkv, lo
     return lo;
 }
 
-__device__ __forceinline__ void set_piece(const AParams &P, const long long *cum, int b,
-                                          long long u, long long u1, int rt, Piece &p)
-{
-    const long long c0 = __ldg(cum + b), c1 = __ldg(cum + b + 1);
-    const uint4 s = __ldg(reinterpret_cast<const uint4 *>(P.plan + P.lay.seq) + b);
-    p.b = b;
-    p.tiles = (int)(c1 - c0);
-    const long long rel = u - c0 * P.Hkv;
-    p.h = (int)(rel / p.tiles);
-    p.tile0 = (int)(rel - (long long)p.h * p.tiles);
-    p.u0 = u - p.tile0;
-    const long long left = u1 - u;
-    p.n = p.tiles - p.tile0 < left ? p.tiles - p.tile0 : (int)left;
-    p.len = (int)s.x;
-    p.nn = (int)s.y;
-    p.status = (int)s.z;
-    p.idle = p.nn <= rt * P.nodes_per_tile;
-}
-
-// Calls fn(piece) for each item's run in units [u, u1).
-template <typename F>
-__device__ __forceinline__ void for_pieces(const AParams &P, const long long *cum, long long u,
-                                           long long u1, int rt, F fn)
-{
-    if (u >= u1)
-        return;
-    int b = find_seq(cum, P.B, P.Hkv, u);
-    while (u < u1) {
-        while (b + 1 < P.B && __ldg(cum + b + 1) * P.Hkv <= u)
-            ++b;
-        Piece p;
-        set_piece(P, cum, b, u, u1, rt, p);
-        fn(p);
-        u += p.n;
-    }
-}
+struct Whole {
+    static constexpr bool value = false;
+};
+struct Masked {
+    static constexpr bool value = true;
+};
 
 // Keys of tile `jt` of an item: how many, and whether they are the cache's.
 __device__ __forceinline__ int tile_keys(const Piece &p, int jt, bool &cached)
@@ -493,7 +466,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&S.sfull[i], 1);
             mbar_init(&S.pready[i], 4);
             mbar_init(&S.pvdone[i], 1);
+            mbar_init(&S.noted[i], 4);
         }
+        for (int i = 0; i < RING; ++i) {
+            mbar_init(&S.pfull[i], 1);
+            mbar_init(&S.pempty[i], 11);  // every warp but the one that writes
+        }
+        mbar_init(&S.join, 8);
         mbar_init(&S.drain, 1);
         S.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -510,22 +489,46 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tmem = S.tmem_base;
     allow_next_kernel();
     wait_previous_kernel();
-    const long long *cum = reinterpret_cast<const long long *>(P.plan + P.lay.cum);
-    const long long total = __ldg(cum + P.B) * P.Hkv;
-    const long long per = share(P, total);
-    const long long u0 = slot * per, u1 = u0 + per < total ? u0 + per : total;
 
-    // a wait of this thread: false once the CTA has given up
+    // a warp's wait: false on every lane once the CTA has given up
     auto wait = [&](unsigned long long *bar, uint32_t parity) -> bool {
-        if (mbar_try_wait(bar, parity))
-            return true;
-        if (*abort_flag)
+        bool ok = mbar_try_wait(bar, parity);
+        if (!ok && !*abort_flag) {
+            ok = mbar_wait(bar, parity);
+            if (!ok) {
+                atomicExch(P.status, SPEC_DEV_WAIT_TIMEOUT);
+                *abort_flag = 1;
+            }
+        }
+        return __all_sync(0xffffffffu, ok);
+    };
+    // the same for a warp that has time: it sleeps between its tests
+    auto wait_idle = [&](unsigned long long *bar, uint32_t parity) -> bool {
+        const unsigned long long t0 = globaltimer();
+        while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+            const bool late = globaltimer() - t0 > WAIT_NS;
+            if (late) {
+                atomicExch(P.status, SPEC_DEV_WAIT_TIMEOUT);
+                *abort_flag = 1;
+            }
+            if (__any_sync(0xffffffffu, late || *abort_flag))
+                return false;
+            __nanosleep(100);
+        }
+        return true;
+    };
+    // the next piece of the share: false when there is none or the CTA has given up
+    uint32_t taken = 0;
+    auto next = [&](Piece &p) -> bool {
+        const int at = (int)(taken % RING);
+        if (!wait(&S.pfull[at], (taken / RING) & 1u))
             return false;
-        if (mbar_wait(bar, parity))
-            return true;
-        atomicExch(P.status, SPEC_DEV_WAIT_TIMEOUT);
-        *abort_flag = 1;
-        return false;
+        p = S.piece[at];
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&S.pempty[at]);
+        ++taken;
+        return p.n > 0;
     };
 
     if (warp < 8) {
@@ -541,11 +544,28 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int g = r - local * P.G;
         const int node = rt * P.nodes_per_tile + local;
         const bool row = local < P.nodes_per_tile && node < P.N;
-        const uint32_t *masks = reinterpret_cast<const uint32_t *>(P.plan + P.lay.mask);
+        const uint4 *masks = reinterpret_cast<const uint4 *>(P.plan + P.lay.mask);
         uint32_t cnt = 0, tv = 0;                // the group's tiles, all V tiles
+        uint32_t joins = 0, notes = 0;
         const unsigned long long c2 = f2(P.c, P.c);
+        // all softmax warps have come here
+        auto join = [&]() -> bool {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&S.join);
+            return wait(&S.join, joins++ & 1u);
+        };
+        // this group's warps have come here
+        auto group = [&]() -> bool {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&S.noted[s]);
+            return wait(&S.noted[s], notes++ & 1u);
+        };
 
-        for_pieces(P, cum, u0, u1, rt, [&](const Piece &p) {
+        bool ok = true;
+        Piece p;
+        while (ok && next(p)) {
             const int64_t orow = ((int64_t)p.b * P.N + node) * P.Hq + (int64_t)p.h * P.G + g;
             if (p.idle) {
                 // rows past n_nodes are 0, of a bad sequence NaN; once per item
@@ -557,33 +577,38 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (P.lse)
                         P.lse[orow] = p.status ? NAN : -INFINITY;
                 }
-                return;
+                continue;
             }
             const bool live = row && node < p.nn;
             const bool warp_live = __any_sync(0xffffffffu, live);
-            float m = -INFINITY, l = 0.0f;       // maximum of the raw scores, total
             const int cache_tiles = (p.len + KT - 1) / KT;
-            for (int i = s; i < p.n; i += 2) {
-                bool cached;
+            const uint4 *mask = masks + ((size_t)p.b * P.N + node) * (P.lay.W / 4);
+            uint4 see0 = make_uint4(0, 0, 0, 0);  // the first new tile's mask, loaded ahead
+            if (live && p.tile0 <= cache_tiles && cache_tiles < p.tile0 + p.n)
+                see0 = __ldg(mask);
+            float m = -INFINITY, l = 0.0f;       // maximum of the raw scores, total
+            // one tile of this group; `masked` tiles hold fewer than KT keys or new ones
+            auto tile = [&](int i, auto kind) {
+                constexpr bool masked = decltype(kind)::value;
+                bool cached = true;
                 const int jt = p.tile0 + i;
-                const int keys = tile_keys(p, jt, cached);
+                const int keys = masked ? tile_keys(p, jt, cached) : KT;
                 // what this row sees of the tile
                 uint4 see = make_uint4(~0u, ~0u, ~0u, ~0u);
                 if (!cached) {
-                    see = make_uint4(0, 0, 0, 0);
-                    if (live)
-                        see = __ldg(reinterpret_cast<const uint4 *>(
-                                        masks + ((size_t)p.b * P.N + node) * P.lay.W) +
-                                    (jt - cache_tiles));
+                    see = see0;
+                    if (live && jt > cache_tiles)
+                        see = __ldg(mask + (jt - cache_tiles));
                 }
                 uint32_t any_bad = 0;
-                const bool masked = keys < KT || !cached;
                 if (masked) {
                     // V: rows past the keys (up to the last product's 16) are zeroed; in new
                     // values, non-finite elements are noted and zeroed
                     const uint32_t vt = tv + (uint32_t)i;
                     const int st = (int)(vt % C::STAGES);
-                    wait(&S.vfull[st], (vt / C::STAGES) & 1u);
+                    ok = wait(&S.vfull[st], (vt / C::STAGES) & 1u);
+                    if (!ok)
+                        return;
                     uint8_t *vrow = v_p + (size_t)st * C::TILE + r * 128;
                     bool bad = false;
                     if (r >= keys && r < ((keys + 15) & ~15)) {
@@ -614,13 +639,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const uint32_t ballot = __ballot_sync(0xffffffffu, bad);
                         if (lane == 0)
                             S.bad[s][cnt & 1u][quarter] = ballot;
-                        group_sync(2 + s, 128);
-                        const uint32_t *f = S.bad[s][cnt & 1u];
+                        ok = group();
+                        if (!ok)
+                            return;
+                        const volatile uint32_t *f = S.bad[s][cnt & 1u];
                         any_bad = f[0] | f[1] | f[2] | f[3];
                     }
                 }
-                wait(&S.sfull[s], cnt & 1u);
-                __syncwarp();
+                ok = wait(&S.sfull[s], cnt & 1u);
+                if (!ok)
+                    return;
                 tc_fence_after();
                 uint32_t zero_w[4] = {0, 0, 0, 0};  // keys whose weight is 0 (with any_bad only)
                 if (warp_live) {
@@ -698,8 +726,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     mbar_arrive(&S.pready[s]);
                 if (any_bad) {
                     // what the zeroed elements give the rows that see them, once O(i) is done
-                    wait(&S.pvdone[s], cnt & 1u);
-                    __syncwarp();
+                    ok = wait(&S.pvdone[s], cnt & 1u);
+                    if (!ok)
+                        return;
                     tc_fence_after();
                     const uint32_t w[4] = {see.x, see.y, see.z, see.w};
                     const int first = (jt - cache_tiles) * KT;
@@ -709,7 +738,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         tmem_ld(t_o + d, o);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            uint32_t left = S.bad[s][cnt & 1u][q];
+                            uint32_t left = *static_cast<volatile uint32_t *>(
+                                &S.bad[s][cnt & 1u][q]);
                             while (left) {
                                 const int bit = __ffs((int)left) - 1;
                                 left &= left - 1;
@@ -719,44 +749,52 @@ __global__ void __launch_bounds__(THREADS, 1)
                                     p.b * P.v_new_stride[0] +
                                     (first + q * 32 + bit) * P.v_new_stride[1] +
                                     p.h * P.v_new_stride[2];
+                                const float z = (zero_w[q] >> bit) & 1u ? 0.0f : 1.0f;
 #pragma unroll
                                 for (int j = 0; j < 32; ++j)
                                     if (d + j < P.D) {
                                         const uint32_t e = src[d + j];
-                                        if (nonfinite<DT>(e) & 0xffffu) {
-                                            const float z = (zero_w[q] >> bit) & 1u ? 0.0f : 1.0f;
+                                        if (nonfinite<DT>(e) & 0xffffu)
                                             o[j] = __float_as_uint(__uint_as_float(o[j]) +
                                                                    z * unpack1<DT>(e));
-                                        }
                                     }
                             }
                         }
-                        __syncwarp();
                         tmem_st(t_o + d, o);
                     }
                     tmem_wait_st();
                     tc_fence_before();
-                    // the next tile's notes come after every thread has read these
-                    group_sync(2 + s, 128);
+                    // the notes are written over only after every warp has read them
+                    ok = group();
                 }
                 ++cnt;
-            }
+            };
+            // whole tiles of the cache first, in a loop of their own: it stays small
+            const int plain = min(p.n, p.len / KT - p.tile0);
+            int i = s;
+            for (; i < plain && ok; i += 2)
+                tile(i, Whole());
+            for (; i < p.n && ok; i += 2)
+                tile(i, Masked());
+            if (!ok)
+                break;
             tv += (uint32_t)p.n;
 
             // join the two groups' halves: each group writes one half of the columns
             const bool mine = p.n > s;           // this group had a tile
-            if (mine)
-                wait(&S.pvdone[s], (cnt - 1) & 1u);
-            __syncwarp();
+            if (mine && !wait(&S.pvdone[s], (cnt - 1) & 1u))
+                break;
             tc_fence_after();
             S.m[s][r] = mine ? (m == -INFINITY ? -INFINITY : m * P.c) : -INFINITY;
             S.l[s][r] = mine ? l : 0.0f;
             tc_fence_before();
-            group_sync(1, SOFT_THREADS);
+            if (!join())
+                break;
             tc_fence_after();
             const bool whole = p.n == p.tiles;
             const bool two = p.n > 1;
-            if (__any_sync(0xffffffffu, row && (whole || live))) {
+            const bool writes = row && (whole || live);
+            if (__any_sync(0xffffffffu, writes)) {
                 const float m0 = S.m[0][r], m1 = S.m[1][r], l0 = S.l[0][r], l1 = S.l[1][r];
                 const float top = fmaxf(m0, m1);
                 const float base = top == -INFINITY ? 0.0f : top;
@@ -766,8 +804,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const float w0 = some0 ? ex2(m0 - base) : 0.0f;
                 const float w1 = some1 ? ex2(m1 - base) : 0.0f;
                 const float sum = l0 * w0 + l1 * w1;
-                const bool first_of_slot = u0 >= p.u0;  // the CTA's run starts inside the item
-                const size_t at = ((size_t)blockIdx.x * 2 + (first_of_slot ? 0 : 1)) * BM + r;
+                const size_t at = ((size_t)blockIdx.x * 2 + (p.first ? 0 : 1)) * BM + r;
                 const float norm = whole ? (live && sum != 0.0f ? 1.0f / sum : 0.0f) : 1.0f;
                 constexpr int HALF = C::DP / 2;
 #pragma unroll
@@ -779,7 +816,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         tmem_ld(tmem + lanes + (uint32_t)(2 * KT + C::DP + d), b);
 #pragma unroll
                     for (int j = 0; j < 32; j += 8) {
-                        if (d + j >= P.D || !row || !(whole || live))
+                        if (d + j >= P.D || !writes)
                             continue;
                         float v[8];
 #pragma unroll
@@ -806,178 +843,240 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             tc_fence_before();
-            group_sync(1, SOFT_THREADS);  // O and the exchanged statistics are free again
-        });
+            ok = join();  // O and the exchanged statistics are free again
+        }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(HELPER_REGS));
-    if (warp == 8) {
-        // ---------------------------------------------------- TMA producer
-        uint32_t t = 0, items = 0;           // tiles and items so far
-        uint32_t issued[2] = {0, 0};         // tiles of K and of V whose loads were issued
-        bool ok = true;
-        for_pieces(P, cum, u0, u1, rt, [&](const Piece &p) {
-            if (p.idle || !ok)
-                return;
-            ok = __all_sync(0xffffffffu, wait(&S.qempty, (items & 1u) ^ 1u));
-            if (!ok)
-                return;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&S.qfull, (uint32_t)(P.q_rows * 128 * NP));
-                for (int i = 0; i < NP; ++i)
-                    tma_load_5d(q_s + i * PANEL_BYTES, &mq, i * PANEL, 0, rt * P.nodes_per_tile,
-                                p.h, p.b, &S.qfull);
-            }
-            ++items;
-            for (int i = 0; i < p.n && ok; ++i, ++t) {
-                bool cached;
-                const int jt = p.tile0 + i;
-                const int keys = tile_keys(p, jt, cached);
-                // box of this lane: its rows of the tile and its page
-                const int rows = cached ? P.page_rows : P.new_rows;
-                const int at = lane * rows;
-                const bool mine = at < keys;
-                int y, w;
-                if (cached) {
-                    const int pos = jt * KT + at;
-                    y = pos;
-                    w = p.b;
-                    if (P.page_table && mine) {
-                        const int e = pos / P.page_size;
-                        w = e < P.pages_per_seq
-                            ? __ldg(P.page_table + (size_t)p.b * P.pages_per_seq + e) : -1;
-                        y = pos - e * P.page_size;
+        if (warp == 8) {
+            // ------------------------------------------------ TMA of K and V
+            uint32_t t = 0;
+            uint32_t issued[2] = {0, 0};         // tiles of K and of V whose loads were issued
+            bool ok = true;
+            Piece p;
+            while (ok && next(p)) {
+                if (p.idle)
+                    continue;
+                const int cache_tiles = (p.len + KT - 1) / KT;
+                for (int i = 0; i < p.n && ok; ++i, ++t) {
+                    bool cached;
+                    const int jt = p.tile0 + i;
+                    const int keys = tile_keys(p, jt, cached);
+                    // box of this lane: its rows of the tile and its page
+                    const int rows = cached ? P.page_rows : P.new_rows;
+                    const int at = lane * rows;
+                    const bool mine = at < keys;
+                    int y = (jt - cache_tiles) * KT + at, w = p.b;
+                    if (cached) {
+                        y = jt * KT + at;
+                        if (P.page_table && mine) {
+                            const int e = y / P.page_size;
+                            w = e < P.pages_per_seq
+                                ? __ldg(P.page_table + (size_t)p.b * P.pages_per_seq + e) : -1;
+                            y -= e * P.page_size;
+                        }
                     }
-                } else {
-                    y = (jt - (p.len + KT - 1) / KT) * KT + at;
-                    w = p.b;
-                }
-                const uint32_t bytes = (uint32_t)(((keys + rows - 1) / rows) * rows * 128 * NP);
-                const int st = (int)(t % C::STAGES);
-                const uint32_t ph = (t / C::STAGES) & 1u;
+                    const uint32_t bytes = (uint32_t)(((keys + rows - 1) / rows) * rows * 128 * NP);
+                    const int st = (int)(t % C::STAGES);
+                    const uint32_t ph = (t / C::STAGES) & 1u;
 #pragma unroll
+                    for (int side = 0; side < 2; ++side) {
+                        unsigned long long *full = side ? &S.vfull[st] : &S.kfull[st];
+                        const CUtensorMap *map = cached ? (side ? &mvc : &mkc)
+                                                        : (side ? &mvn : &mkn);
+                        ok = ok && wait(side ? &S.vempty[st] : &S.kempty[st], ph ^ 1u);
+                        if (!ok)
+                            break;
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(full, bytes);
+                        __syncwarp();
+                        issued[side] = t + 1;
+                        if (mine) {
+                            const uint32_t dst = (side ? v_s : k_s) + st * C::TILE + at * 128;
+#pragma unroll
+                            for (int d = 0; d < NP; ++d)
+                                tma_load_4d(dst + d * PANEL_BYTES, map, d * PANEL, y, p.h, w, full);
+                        }
+                    }
+                }
+            }
+            if (*abort_flag) {
+                // the loads in flight land first: each barrier's last phase that has a load
                 for (int side = 0; side < 2; ++side) {
-                    unsigned long long *empty = side ? &S.vempty[st] : &S.kempty[st];
-                    unsigned long long *full = side ? &S.vfull[st] : &S.kfull[st];
-                    const CUtensorMap *map = cached ? (side ? &mvc : &mkc) : (side ? &mvn : &mkn);
-                    ok = __all_sync(0xffffffffu, wait(empty, ph ^ 1u));
-                    if (!ok)
-                        break;
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(full, bytes);
-                    __syncwarp();
-                    issued[side] = t + 1;
-                    if (mine) {
-                        const uint32_t dst = (side ? v_s : k_s) + st * C::TILE + at * 128;
-#pragma unroll
-                        for (int d = 0; d < NP; ++d)
-                            tma_load_4d(dst + d * PANEL_BYTES, map, d * PANEL, y, p.h, w, full);
-                    }
+                    const uint32_t n = issued[side];
+                    for (uint32_t j = n > C::STAGES ? n - C::STAGES : 0; j < n; ++j)
+                        (void)mbar_wait(side ? &S.vfull[j % C::STAGES] : &S.kfull[j % C::STAGES],
+                                        (j / C::STAGES) & 1u);
                 }
             }
-        });
-        if (!ok) {
-            // the loads in flight land first: each barrier's last phase that has a load
-            for (int side = 0; side < 2; ++side) {
-                const uint32_t n = issued[side];
-                for (uint32_t j = n > C::STAGES ? n - C::STAGES : 0; j < n; ++j)
-                    (void)mbar_wait(side ? &S.vfull[j % C::STAGES] : &S.kfull[j % C::STAGES],
-                                    (j / C::STAGES) & 1u);
-            }
-            if (items)
-                (void)mbar_wait(&S.qfull, (items - 1) & 1u);
-        }
-    } else if (warp == 9) {
-        // ------------------------------------------------------ MMA issuer
-        // The whole warp runs the loop and one elected lane issues: what the products are
-        // given then stays in uniform registers (issued from under `lane == 0` each product
-        // took about 120 clocks to issue, twice its time in the tensor pipe)
-        uint32_t tk = 0, tv = 0, items = 0, cnt[2] = {0, 0};
-        bool ok = true, issued = false;
-        const int ksteps = (P.D + 15) / 16;
-        const uint32_t id_o = idesc<DT>(ksteps * 16, true);
-        auto all = [](bool x) -> bool { return __all_sync(0xffffffffu, x); };
-        auto scores = [&](const Piece &p, int i) {  // S(i) = Q K(i)^T
-            bool cached;
-            const int keys = tile_keys(p, p.tile0 + i, cached);
-            const int st = (int)(tk % C::STAGES);
-            ok = all(wait(&S.kfull[st], (tk / C::STAGES) & 1u));
-            if (!ok)
-                return;
-            tc_fence_after();
-            const uint32_t id = idesc<DT>((keys + 15) & ~15, false);
-            const uint32_t d = tmem + (uint32_t)((i & 1) * KT);
-            const uint64_t qd = desc_k(q_s), kd = desc_k(k_s + st * C::TILE);
-            if (elect_one()) {
-                if (ksteps == NP * 4) {
-#pragma unroll
-                    for (int x = 0; x < NP * 4; ++x) {
-                        const uint64_t off = (uint64_t)(((x >> 2) * PANEL_BYTES + (x & 3) * 32) >> 4);
-                        mma_ss(d, qd + off, kd + off, id, x ? 1u : 0u);
-                    }
-                } else {
-                    for (int x = 0; x < ksteps; ++x) {
-                        const uint64_t off = (uint64_t)(((x >> 2) * PANEL_BYTES + (x & 3) * 32) >> 4);
-                        mma_ss(d, qd + off, kd + off, id, x ? 1u : 0u);
-                    }
-                }
-                mma_commit(&S.kempty[st]);
-                mma_commit(&S.sfull[i & 1]);
-                if (i == p.n - 1)
-                    mma_commit(&S.qempty);
-            }
-            __syncwarp();
-            issued = true;
-            ++tk;
-        };
-        for_pieces(P, cum, u0, u1, rt, [&](const Piece &p) {
-            if (p.idle || !ok)
-                return;
-            ok = all(wait(&S.qfull, items & 1u));
-            ++items;
-            for (int i = 0; i < 2 && i < p.n && ok; ++i)
-                scores(p, i);
-            for (int i = 0; i < p.n && ok; ++i) {
+        } else if (warp == 9) {
+            // -------------------------------------------------- MMA issuer
+            // The whole warp runs the loop and one elected lane issues: what the products
+            // are given then stays in uniform registers (issued from under `lane == 0` each
+            // product took about 120 clocks to issue, twice its time in the tensor pipe)
+            uint32_t tk = 0, tv = 0, items = 0, cnt[2] = {0, 0};
+            bool ok = true, issued = false;
+            const int ksteps = (P.D + 15) / 16;
+            const uint32_t id_o = idesc<DT>(ksteps * 16, true);
+            Piece p = {};
+            auto scores = [&](int i) {  // S(i) = Q K(i)^T
                 bool cached;
                 const int keys = tile_keys(p, p.tile0 + i, cached);
-                const int s = i & 1, st = (int)(tv % C::STAGES);
-                ok = all(wait(&S.vfull[st], (tv / C::STAGES) & 1u) &&
-                         wait(&S.pready[s], cnt[s] & 1u));
+                const int st = (int)(tk % C::STAGES);
+                ok = wait(&S.kfull[st], (tk / C::STAGES) & 1u);
                 if (!ok)
-                    break;
+                    return;
                 tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(2 * KT + s * C::DP);
-                const uint32_t a = tmem + (uint32_t)(s * KT);
-                const uint64_t vd = desc_mn(v_s + st * C::TILE);
-                const uint32_t more = i >= 2 ? 1u : 0u;
+                const uint32_t id = idesc<DT>((keys + 15) & ~15, false);
+                const uint32_t d = tmem + (uint32_t)((i & 1) * KT);
+                const uint64_t qd = desc_k(q_s), kd = desc_k(k_s + st * C::TILE);
                 if (elect_one()) {
-                    // 16 keys a step: 8 columns of P, 2 KB of V
-                    if (keys > KT - 16) {
+                    if (ksteps == NP * 4) {
 #pragma unroll
-                        for (int x = 0; x < KT / 16; ++x)
-                            mma_ts(d, a + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)), id_o,
-                                   x ? 1u : more);
+                        for (int x = 0; x < NP * 4; ++x) {
+                            const uint64_t off =
+                                (uint64_t)(((x >> 2) * PANEL_BYTES + (x & 3) * 32) >> 4);
+                            mma_ss(d, qd + off, kd + off, id, x ? 1u : 0u);
+                        }
                     } else {
-                        for (int x = 0; x < (keys + 15) / 16; ++x)
-                            mma_ts(d, a + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)), id_o,
-                                   x ? 1u : more);
+                        for (int x = 0; x < ksteps; ++x) {
+                            const uint64_t off =
+                                (uint64_t)(((x >> 2) * PANEL_BYTES + (x & 3) * 32) >> 4);
+                            mma_ss(d, qd + off, kd + off, id, x ? 1u : 0u);
+                        }
                     }
-                    mma_commit(&S.vempty[st]);
-                    mma_commit(&S.pvdone[s]);
+                    mma_commit(&S.kempty[st]);
+                    mma_commit(&S.sfull[i & 1]);
+                    if (i == p.n - 1)
+                        mma_commit(&S.qempty);
                 }
                 __syncwarp();
-                ++tv;
-                ++cnt[s];
-                if (i + 2 < p.n)
-                    scores(p, i + 2);
+                issued = true;
+                ++tk;
+            };
+            while (ok && next(p)) {
+                if (p.idle)
+                    continue;
+                ok = wait(&S.qfull, items & 1u);
+                ++items;
+                for (int i = 0; i < 2 && i < p.n && ok; ++i)
+                    scores(i);
+                for (int i = 0; i < p.n && ok; ++i) {
+                    bool cached;
+                    const int keys = tile_keys(p, p.tile0 + i, cached);
+                    const int s = i & 1, st = (int)(tv % C::STAGES);
+                    ok = wait(&S.vfull[st], (tv / C::STAGES) & 1u) &&
+                         wait(&S.pready[s], cnt[s] & 1u);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint32_t d = tmem + (uint32_t)(2 * KT + s * C::DP);
+                    const uint32_t a = tmem + (uint32_t)(s * KT);
+                    const uint64_t vd = desc_mn(v_s + st * C::TILE);
+                    // 16 keys a step: 8 columns of P, 2 KB of V
+                    const int steps = (keys + 15) / 16;
+                    const uint32_t more = i >= 2 ? 1u : 0u;
+                    if (elect_one()) {
+                        if (steps == KT / 16) {
+#pragma unroll
+                            for (int x = 0; x < KT / 16; ++x)
+                                mma_ts(d, a + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)),
+                                       id_o, x ? 1u : more);
+                        } else {
+                            for (int x = 0; x < steps; ++x)
+                                mma_ts(d, a + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)),
+                                       id_o, x ? 1u : more);
+                        }
+                        mma_commit(&S.vempty[st]);
+                        mma_commit(&S.pvdone[s]);
+                    }
+                    __syncwarp();
+                    issued = true;
+                    ++tv;
+                    ++cnt[s];
+                    if (i + 2 < p.n)
+                        scores(i + 2);
+                }
             }
-        });
-        if (!ok && issued) {  // the products in flight complete (bounded)
-            if (elect_one())
-                mma_commit(&S.drain);
-            __syncwarp();
-            (void)mbar_wait(&S.drain, 0u);
+            if (*abort_flag && issued) {  // the products in flight complete (bounded)
+                if (elect_one())
+                    mma_commit(&S.drain);
+                __syncwarp();
+                (void)mbar_wait(&S.drain, 0u);
+            }
+        } else if (warp == 10) {
+            // ---------------------------------------------------- TMA of Q
+            uint32_t items = 0;
+            Piece p;
+            while (next(p)) {
+                if (p.idle)
+                    continue;
+                if (!wait_idle(&S.qempty, (items & 1u) ^ 1u))
+                    break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&S.qfull, (uint32_t)(P.q_rows * 128 * NP));
+                    for (int i = 0; i < NP; ++i)
+                        tma_load_5d(q_s + i * PANEL_BYTES, &mq, i * PANEL, 0,
+                                    rt * P.nodes_per_tile, p.h, p.b, &S.qfull);
+                }
+                __syncwarp();
+                ++items;
+            }
+            if (*abort_flag && items)
+                (void)mbar_wait(&S.qfull, (items - 1) & 1u);
+        } else {
+            // ------------------------------------------- the share's pieces
+            const long long *cum = reinterpret_cast<const long long *>(P.plan + P.lay.cum);
+            const uint4 *seqs = reinterpret_cast<const uint4 *>(P.plan + P.lay.seq);
+            const long long total = __ldg(cum + P.B) * P.Hkv;
+            const long long per = share(P, total);
+            const long long u0 = slot * per, u1 = u0 + per < total ? u0 + per : total;
+            long long u = u0;
+            int b = 0, h = 0, tile = 0, tiles = 1;
+            uint4 q = make_uint4(0, 0, 0, 0);
+            if (u < u1) {
+                b = find_seq(cum, P.B, P.Hkv, u);
+                const long long c0 = __ldg(cum + b);
+                tiles = (int)(__ldg(cum + b + 1) - c0);
+                q = __ldg(seqs + b);
+                h = (int)((u - c0 * P.Hkv) / tiles);
+                tile = (int)(u - c0 * P.Hkv - (long long)h * tiles);
+            }
+            for (uint32_t k = 0;; ++k) {
+                const int at = (int)(k % RING);
+                if (!wait_idle(&S.pempty[at], ((k / RING) & 1u) ^ 1u))
+                    break;
+                const long long left = u1 - u;
+                const int n = left <= 0 ? 0 : tiles - tile < left ? tiles - tile : (int)left;
+                if (lane == 0) {
+                    Piece p;
+                    p.b = b;
+                    p.h = h;
+                    p.tile0 = tile;
+                    p.n = n;
+                    p.tiles = tiles;
+                    p.len = (int)q.x;
+                    p.nn = (int)q.y;
+                    p.status = (int)q.z;
+                    p.idle = p.nn <= rt * P.nodes_per_tile;
+                    p.first = u - tile <= u0;
+                    S.piece[at] = p;
+                    mbar_arrive(&S.pfull[at]);
+                }
+                __syncwarp();
+                if (n == 0)
+                    break;
+                u += n;
+                tile = 0;
+                if (++h == P.Hkv) {
+                    h = 0;
+                    ++b;
+                    if (u < u1) {
+                        tiles = (int)(__ldg(cum + b + 1) - __ldg(cum + b));
+                        q = __ldg(seqs + b);
+                    }
+                }
+            }
         }
-    }
     }
     tc_fence_before();
     __syncthreads();
@@ -1010,21 +1109,24 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_cons
     if (end >= total)
         return;
     const int b = find_seq(cum, P.B, P.Hkv, end);
-    Piece p;
-    set_piece(P, cum, b, end, total, rt, p);
-    if (p.tile0 == 0 || p.u0 < end - per || p.idle)
+    const long long c0 = __ldg(cum + b);
+    const int tiles = (int)(__ldg(cum + b + 1) - c0);
+    const int h = (int)((end - c0 * P.Hkv) / tiles);
+    const long long item = c0 * P.Hkv + (long long)h * tiles;  // its first unit
+    const int nn = (int)__ldg(reinterpret_cast<const uint4 *>(P.plan + P.lay.seq) + b).y;
+    if (item == end || item < end - per || nn <= rt * P.nodes_per_tile)
         return;  // not cut here, or the previous end has it, or no rows
     const int local = r / P.G, g = r - local * P.G;
     const int node = rt * P.nodes_per_tile + local;
     if (r >= BM || local >= P.nodes_per_tile || node >= P.N)
         return;
-    const int64_t orow = ((int64_t)p.b * P.N + node) * P.Hq + (int64_t)p.h * P.G + g;
-    const bool live = node < p.nn;
-    const int s0 = (int)blockIdx.x, s1 = (int)((p.u0 + p.tiles - 1) / per);
+    const int64_t orow = ((int64_t)b * P.N + node) * P.Hq + (int64_t)h * P.G + g;
+    const bool live = node < nn;
+    const int s0 = (int)blockIdx.x, s1 = (int)((item + tiles - 1) / per);
     // a share that starts with the item, or inside it, left its first piece; one that the item
     // starts inside of left its second
     auto at = [&](int s) -> size_t {
-        const int which = (long long)s * per >= p.u0 ? 0 : 1;
+        const int which = (long long)s * per >= item ? 0 : 1;
         return (((size_t)s * P.row_tiles + rt) * 2 + which) * BM + r;
     };
     float top = -INFINITY;
@@ -1105,7 +1207,7 @@ WsLayout ws_layout(int N, int G, int D)
     const size_t ctas = rt > MAX_CTAS ? (size_t)rt : (size_t)MAX_CTAS;
     const size_t dp = D > PANEL ? 2 * PANEL : PANEL;
     WsLayout w;
-    w.ml = sizeof(WsHeader);
+    w.ml = 0;
     w.part = plan_align(w.ml + ctas * 2 * BM * sizeof(float2));
     w.total = plan_align(w.part + ctas * 2 * BM * dp * sizeof(float));
     return w;
@@ -1261,7 +1363,7 @@ int32_t spec_tree_attention(const spec_tree_attention_args *args, void *workspac
         P.v_new_stride[i] = a.v_new_stride[i];
     P.out = a.out;
     P.lse = a.out_lse;
-    P.status = &reinterpret_cast<WsHeader *>(ws)->status;
+    P.status = &reinterpret_cast<WsHeader *>(const_cast<void *>(a.plan))->status;
     P.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
     P.part = reinterpret_cast<float *>(ws + w.part);
     P.c = a.scale * LOG2E;

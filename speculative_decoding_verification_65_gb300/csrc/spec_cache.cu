@@ -53,10 +53,11 @@ __device__ void plan_scan(const PlanParams &P)
     __shared__ long long part[32];
     __shared__ long long base;
     long long *cum = reinterpret_cast<long long *>(P.plan + P.lay.cum);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         base = 0;
         cum[0] = 0;
+        reinterpret_cast<WsHeader *>(P.plan)->status = SPEC_DEV_OK;
     }
     __syncthreads();
     for (int b0 = 0; b0 < P.B; b0 += (int)blockDim.x) {
@@ -84,7 +85,6 @@ __device__ void plan_scan(const PlanParams &P)
             base = before + v;
         __syncthreads();
     }
-    (void)nw;
 }
 
 __global__ void __launch_bounds__(1024) plan_kernel(const PlanParams P)

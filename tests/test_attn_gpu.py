@@ -227,8 +227,10 @@ def test_repeats_are_bit_equal_and_other_streams_work():
     def once(stream=None):
         plan = sv.spec_tree_plan(d["parent"], d["n_nodes"], d["cache_len"], d["k_cache"],
                                  page_table=d["table"], stream=stream)
-        return sv.spec_tree_attention(d["q"], d["k_new"], d["v_new"], d["k_cache"], d["v_cache"],
-                                      plan, page_table=d["table"], stream=stream)
+        out = sv.spec_tree_attention(d["q"], d["k_new"], d["v_new"], d["k_cache"], d["v_cache"],
+                                     plan, page_table=d["table"], stream=stream)
+        assert plan.read_status(stream) == sv.SPEC_DEV_OK
+        return out
     want = once()
     for _ in range(5):
         assert torch.equal(once(), want)
@@ -237,8 +239,6 @@ def test_repeats_are_bit_equal_and_other_streams_work():
     got = once(s)
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(got, want)
-    ws = sv.attention_workspace(9, 8, 2, 128)
-    assert sv.spec_verify_read_status(ws) == sv.SPEC_DEV_OK
 
 
 def test_graph_capture_follows_new_lengths():
