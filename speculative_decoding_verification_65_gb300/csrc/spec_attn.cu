@@ -131,7 +131,7 @@ struct AParams {
     void *out;
     float *lse;
     int *status;
-    float *part;     // [ctas][2][BM][DP] unnormalised sums of split items
+    float *part;     // [ctas][2][DP][BM] unnormalised sums of split items
     float2 *part_ml; // [ctas][2][BM] (maximum in log2 units, total)
     float c;         // scale * log2(e)
     int B, N, Hq, Hkv, D, G;
@@ -143,6 +143,21 @@ struct AParams {
 };
 
 // ------------------------------------------------------------ PTX wrappers
+
+// 16 consecutive columns of this warp's 32 TMEM lanes, one lane per thread; they have
+// arrived when it returns
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16])
+{
+    __syncwarp();  // .sync.aligned: the whole warp, converged
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15 "
+        "}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr) : "memory");
+}
 
 // 32 consecutive columns of this warp's 32 TMEM lanes, one lane per thread; they have
 // arrived when it returns
@@ -312,6 +327,51 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
+// A converged warp's test of a barrier, by one elected lane and without a branch: a test
+// by all 32 lanes is served one after the other (150 to 250 clocks for a
+// barrier that is ready), and a branch to one lane's test costs about as much.
+__device__ __forceinline__ bool warp_try(unsigned long long *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "setp.ne.u32 q, %2, %2;\n\t"
+        "@p mbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    const bool any = __any_sync(0xffffffffu, ok != 0);
+    __syncwarp();
+    return any;
+}
+
+// The wait for a barrier that was not ready at once; `sleep_ns` between the tests.
+__device__ __forceinline__ bool wait_long(unsigned long long *bar, uint32_t parity,
+                                          volatile int *abort_flag, int *status,
+                                          unsigned int sleep_ns)
+{
+    const unsigned long long t0 = globaltimer();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i) {
+            if (warp_try(bar, parity))
+                return true;
+            if (sleep_ns)
+                __nanosleep(sleep_ns);
+        }
+        bool stop = *abort_flag != 0;
+        if (globaltimer() - t0 > WAIT_NS) {
+            atomicExch(status, SPEC_DEV_WAIT_TIMEOUT);
+            *abort_flag = 1;
+            stop = true;
+        }
+        if (__any_sync(0xffffffffu, stop))
+            return false;
+    }
+}
+
 // Shared-memory matrix descriptors, 128-byte swizzle (version 1, mode 2).
 // K-major (Q and K): rows of 128 bytes, 8-row groups 1024 bytes apart.
 __device__ __forceinline__ uint64_t desc_k(uint32_t saddr)
@@ -371,13 +431,48 @@ __device__ __forceinline__ uint32_t nonfinite(uint32_t w)
     return ((w & E) == E ? 0xffffu : 0u) | (((w >> 16) & E) == E ? 0xffff0000u : 0u);
 }
 
-// Scores of columns past `keys` or with a 0 bit become -inf.
-__device__ __forceinline__ void hide(uint32_t (&x)[32], int keys, uint32_t bits)
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// the largest of 32 scores (two chains); -inf if all are NaN
+__device__ __forceinline__ float max32(const uint32_t (&x)[32])
+{
+    float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        a = max3(a, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+        b = max3(b, __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
+    }
+    return fmaxf(a, b);
+}
+
+// scores with a 0 bit become -inf
+__device__ __forceinline__ void hide(uint32_t (&x)[32], uint32_t bits)
 {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-        if (j >= keys || !((bits >> j) & 1u))
-            x[j] = 0xff800000u;
+        x[j] = (int)(bits << (31 - j)) < 0 ? x[j] : 0xff800000u;
+}
+
+// weights 2^(x c + shift) of 32 scores, packed, and their sum added to `sum`
+template <int DT>
+__device__ __forceinline__ void weigh(const uint32_t (&x)[32], unsigned long long c2,
+                                      unsigned long long shift2, unsigned long long (&sum)[2],
+                                      uint32_t (&pk)[16])
+{
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        float a0, a1;
+        f2_split(fma2(f2_bits(x[2 * j], x[2 * j + 1]), c2, shift2), a0, a1);
+        a0 = ex2(a0);
+        a1 = ex2(a1);
+        sum[j & 1] = add2(sum[j & 1], f2(a0, a1));
+        pk[j] = pack<DT>(a0, a1);
+    }
 }
 
 // ------------------------------------------------------------------- work
@@ -418,6 +513,31 @@ __device__ __forceinline__ long long share(const AParams &P, long long total)
 {
     const long long per = (total + P.slots - 1) / P.slots;
     return per < 2 ? 2 : per;
+}
+
+// Among each 8 lanes, chunk k of lane i and chunk i of lane k change places.
+__device__ __forceinline__ void exchange8(uint4 (&u)[8], int lane)
+{
+#pragma unroll
+    for (int m = 4; m; m >>= 1) {
+        const bool up = (lane & m) != 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i & m)
+                continue;
+            uint4 &lo = u[i], &hi = u[i | m];
+            const uint4 give = up ? lo : hi;
+            uint4 got;
+            got.x = __shfl_xor_sync(0xffffffffu, give.x, m);
+            got.y = __shfl_xor_sync(0xffffffffu, give.y, m);
+            got.z = __shfl_xor_sync(0xffffffffu, give.z, m);
+            got.w = __shfl_xor_sync(0xffffffffu, give.w, m);
+            if (up)
+                lo = got;
+            else
+                hi = got;
+        }
+    }
 }
 
 template <int DT>
@@ -492,30 +612,11 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     // a warp's wait: false on every lane once the CTA has given up
     auto wait = [&](unsigned long long *bar, uint32_t parity) -> bool {
-        bool ok = mbar_try_wait(bar, parity);
-        if (!ok && !*abort_flag) {
-            ok = mbar_wait(bar, parity);
-            if (!ok) {
-                atomicExch(P.status, SPEC_DEV_WAIT_TIMEOUT);
-                *abort_flag = 1;
-            }
-        }
-        return __all_sync(0xffffffffu, ok);
+        return warp_try(bar, parity) || wait_long(bar, parity, abort_flag, P.status, 0);
     };
     // the same for a warp that has time: it sleeps between its tests
     auto wait_idle = [&](unsigned long long *bar, uint32_t parity) -> bool {
-        const unsigned long long t0 = globaltimer();
-        while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
-            const bool late = globaltimer() - t0 > WAIT_NS;
-            if (late) {
-                atomicExch(P.status, SPEC_DEV_WAIT_TIMEOUT);
-                *abort_flag = 1;
-            }
-            if (__any_sync(0xffffffffu, late || *abort_flag))
-                return false;
-            __nanosleep(100);
-        }
-        return true;
+        return warp_try(bar, parity) || wait_long(bar, parity, abort_flag, P.status, 100);
     };
     // the next piece of the share: false when there is none or the CTA has given up
     uint32_t taken = 0;
@@ -566,10 +667,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         bool ok = true;
         Piece p;
         while (ok && next(p)) {
-            const int64_t orow = ((int64_t)p.b * P.N + node) * P.Hq + (int64_t)p.h * P.G + g;
+            auto out_row = [&]() -> int64_t {
+                return ((int64_t)p.b * P.N + node) * P.Hq + (int64_t)p.h * P.G + g;
+            };
             if (p.idle) {
                 // rows past n_nodes are 0, of a bad sequence NaN; once per item
                 if (s == 0 && p.tile0 == 0 && row) {
+                    const int64_t orow = out_row();
                     const float x = p.status ? NAN : 0.0f;
                     const float v[8] = {x, x, x, x, x, x, x, x};
                     for (int d = 0; d < P.D; d += 8)
@@ -651,70 +755,85 @@ __global__ void __launch_bounds__(THREADS, 1)
                     return;
                 tc_fence_after();
                 uint32_t zero_w[4] = {0, 0, 0, 0};  // keys whose weight is 0 (with any_bad only)
-                if (warp_live) {
-                    uint32_t x[4][32];
-                    tmem_ld4(t_s, x[0], x[1], x[2], x[3]);
-                    if (masked) {
-                        hide(x[0], keys, see.x);
-                        hide(x[1], keys - 32, see.y);
-                        hide(x[2], keys - 64, see.z);
-                        hide(x[3], keys - 96, see.w);
-                    }
-                    float mx[4];
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        mx[h] = __uint_as_float(x[h][0]);
-#pragma unroll
-                        for (int j = 1; j < 31; j += 2)
-                            mx[h] = fmaxf(fmaxf(mx[h], __uint_as_float(x[h][j])),
-                                          __uint_as_float(x[h][j + 1]));
-                        mx[h] = fmaxf(mx[h], __uint_as_float(x[h][31]));
-                    }
-                    float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    top = fmaxf(top, -INFINITY);  // a row of NaN scores has none
+                // the row's new maximum `top`; O and l follow where it has grown far
+                auto raise = [&](float top) {
                     if (i == s) {
                         m = top;
-                    } else {
-                        const bool grown = (top - m) * P.c > GROWTH;  // -inf to finite too
-                        if (__any_sync(0xffffffffu, grown)) {
-                            const float f = grown ? ex2((m - top) * P.c) : 1.0f;
-                            l *= f;
-                            if (grown)
-                                m = top;
-#pragma unroll 1
-                            for (int d = 0; d < C::DP; d += 32) {
-                                uint32_t o[32];
-                                tmem_ld(t_o + d, o);
-#pragma unroll
-                                for (int j = 0; j < 32; ++j)
-                                    o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                                tmem_st(t_o + d, o);
-                            }
-                        }
+                        return;
                     }
+                    const bool grown = (top - m) * P.c > GROWTH;  // -inf to finite too
+                    if (!__any_sync(0xffffffffu, grown))
+                        return;
+                    const float f = grown ? ex2((m - top) * P.c) : 1.0f;
+                    l *= f;
+                    if (grown)
+                        m = top;
+#pragma unroll 1
+                    for (int d = 0; d < C::DP; d += 16) {
+                        uint32_t o[16];
+                        tmem_ld(t_o + d, o);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                        tmem_st(t_o + d, o);
+                    }
+                };
+                unsigned long long sum[2] = {0ull, 0ull};
+                if (warp_live && !masked) {
+                    uint32_t x[4][32];
+                    tmem_ld4(t_s, x[0], x[1], x[2], x[3]);
+                    raise(fmaxf(fmaxf(max32(x[0]), max32(x[1])),
+                                fmaxf(max32(x[2]), max32(x[3]))));
                     const float shift = m == -INFINITY ? 0.0f : -m * P.c;
                     const unsigned long long shift2 = f2(shift, shift);
-                    unsigned long long sum[2] = {0ull, 0ull};
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
                         uint32_t pk[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float a0, a1;
-                            f2_split(fma2(f2_bits(x[h][2 * j], x[h][2 * j + 1]), c2, shift2), a0, a1);
-                            a0 = ex2(a0);
-                            a1 = ex2(a1);
-                            sum[j & 1] = add2(sum[j & 1], f2(a0, a1));
-                            pk[j] = pack<DT>(a0, a1);
-                        }
-                        if (any_bad) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                zero_w[h] |= ((pk[j] & 0x7fffu) == 0 ? 1u : 0u) << (2 * j) |
-                                             ((pk[j] & 0x7fff0000u) == 0 ? 2u : 0u) << (2 * j);
-                        }
+                        weigh<DT>(x[h], c2, shift2, sum, pk);
                         tmem_st(t_s + h * 16, pk);
                     }
+                }
+                if (warp_live && masked) {
+                    // 32 keys at a time, and no more of them than the tile has: the scores are
+                    // read again for the weights
+                    const int chunks = (keys + 31) / 32;
+                    auto bits = [&](int h) -> uint32_t {
+                        const uint32_t w = h == 0 ? see.x : h == 1 ? see.y : h == 2 ? see.z : see.w;
+                        return keys - h * 32 >= 32 ? w : w & ((1u << (keys - h * 32)) - 1u);
+                    };
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int h = 0; h < chunks; ++h) {
+                        uint32_t x[32];
+                        tmem_ld(t_s + h * 32, x);
+                        hide(x, bits(h));
+                        top = fmaxf(top, max32(x));
+                    }
+                    raise(top);
+                    const float shift = m == -INFINITY ? 0.0f : -m * P.c;
+                    const unsigned long long shift2 = f2(shift, shift);
+#pragma unroll 1
+                    for (int h = 0; h < chunks; ++h) {
+                        uint32_t x[32], pk[16];
+                        tmem_ld(t_s + h * 32, x);
+                        hide(x, bits(h));
+                        weigh<DT>(x, c2, shift2, sum, pk);
+                        // weights 32 h on lie in columns 16 h on: over scores that were read
+                        tmem_st(t_s + h * 16, pk);
+                        if (any_bad) {
+                            uint32_t z = 0;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                z |= ((pk[j] & 0x7fffu) == 0 ? 1u : 0u) << (2 * j) |
+                                     ((pk[j] & 0x7fff0000u) == 0 ? 2u : 0u) << (2 * j);
+                            zero_w[0] = h == 0 ? z : zero_w[0];
+                            zero_w[1] = h == 1 ? z : zero_w[1];
+                            zero_w[2] = h == 2 ? z : zero_w[2];
+                            zero_w[3] = h == 3 ? z : zero_w[3];
+                        }
+                    }
+                }
+                if (warp_live) {
                     float s0, s1;
                     f2_split(add2(sum[0], sum[1]), s0, s1);
                     l += s0 + s1;
@@ -794,6 +913,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool whole = p.n == p.tiles;
             const bool two = p.n > 1;
             const bool writes = row && (whole || live);
+            const int64_t orow = out_row();
             if (__any_sync(0xffffffffu, writes)) {
                 const float m0 = S.m[0][r], m1 = S.m[1][r], l0 = S.l[0][r], l1 = S.l[1][r];
                 const float top = fmaxf(m0, m1);
@@ -804,34 +924,55 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const float w0 = some0 ? ex2(m0 - base) : 0.0f;
                 const float w1 = some1 ? ex2(m1 - base) : 0.0f;
                 const float sum = l0 * w0 + l1 * w1;
-                const size_t at = ((size_t)blockIdx.x * 2 + (p.first ? 0 : 1)) * BM + r;
-                const float norm = whole ? (live && sum != 0.0f ? 1.0f / sum : 0.0f) : 1.0f;
-                constexpr int HALF = C::DP / 2;
+                const size_t at = ((size_t)blockIdx.x * 2 + (p.first ? 0 : 1)) * BM;
+                if (s < NP) {  // group s has panel s of the columns
+                    const float norm = sum != 0.0f ? 1.0f / sum : 0.0f;
+                    uint4 u[8];
 #pragma unroll
-                for (int d0 = 0; d0 < HALF; d0 += 32) {
-                    const int d = s * HALF + d0;
-                    uint32_t a[32], b[32];
-                    tmem_ld(tmem + lanes + (uint32_t)(2 * KT + d), a);
-                    if (two)
-                        tmem_ld(tmem + lanes + (uint32_t)(2 * KT + C::DP + d), b);
+                    for (int d0 = 0; d0 < PANEL; d0 += 32) {
+                        uint32_t a[32], b[32];
+                        tmem_ld(tmem + lanes + (uint32_t)(2 * KT + s * PANEL + d0), a);
+                        if (two)
+                            tmem_ld(tmem + lanes + (uint32_t)(2 * KT + C::DP + s * PANEL + d0), b);
+                        float v[32];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        if (d + j >= P.D || !writes)
-                            continue;
-                        float v[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            float x = some0 ? __uint_as_float(a[j + k]) * w0 : 0.0f;
+                        for (int j = 0; j < 32; ++j) {
+                            v[j] = some0 ? __uint_as_float(a[j]) * w0 : 0.0f;
                             if (some1)
-                                x = fmaf(__uint_as_float(b[j + k]), w1, x);
-                            v[k] = (!whole || (live && sum != 0.0f)) ? x * norm : 0.0f;
+                                v[j] = fmaf(__uint_as_float(b[j]), w1, v[j]);
                         }
                         if (whole) {
-                            store8<DT>(P, orow * P.D + d + j, v);
-                        } else {
-                            float4 *o = reinterpret_cast<float4 *>(P.part + at * C::DP + d + j);
-                            o[0] = make_float4(v[0], v[1], v[2], v[3]);
-                            o[1] = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+                            for (int j = 0; j < 32; j += 8) {
+                                const bool on = live && sum != 0.0f;
+                                u[(d0 + j) / 8] = make_uint4(
+                                    on ? pack<DT>(v[j] * norm, v[j + 1] * norm) : 0u,
+                                    on ? pack<DT>(v[j + 2] * norm, v[j + 3] * norm) : 0u,
+                                    on ? pack<DT>(v[j + 4] * norm, v[j + 5] * norm) : 0u,
+                                    on ? pack<DT>(v[j + 6] * norm, v[j + 7] * norm) : 0u);
+                            }
+                        } else if (writes) {
+                            // [column][row]: a warp's store is one line
+                            float *o = P.part + at * C::DP + (s * PANEL + d0) * BM + r;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (s * PANEL + d0 + j < P.D)
+                                    o[j * BM] = v[j];
+                        }
+                    }
+                    if (whole) {
+                        // 8 lanes exchange so that each holds one 16-byte chunk of 8 rows: a
+                        // store then covers 128 bytes of 4 rows, not 16 of 32 rows
+                        exchange8(u, lane);
+                        const int d = s * PANEL + (lane & 7) * 8;
+                        const uint32_t rows = __ballot_sync(0xffffffffu, writes);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int from = (lane & ~7) | k;
+                            const int64_t at_row = __shfl_sync(0xffffffffu, orow, from);
+                            if (((rows >> from) & 1u) && d < P.D)
+                                *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(P.out) +
+                                                           at_row * P.D + d) = u[k];
                         }
                     }
                 }
@@ -839,7 +980,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (whole && P.lse)
                         P.lse[orow] = live ? lse_of(base, sum) : -INFINITY;
                     if (!whole && live)
-                        P.part_ml[at] = make_float2(top, sum);
+                        P.part_ml[at + r] = make_float2(top, sum);
                 }
             }
             tc_fence_before();
@@ -1089,17 +1230,20 @@ __global__ void __launch_bounds__(THREADS, 1)
 // ---------------------------------------------------------------- joining
 
 constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_ROWS = 32;
 
 // Joins the pieces of the items that lie across a share's end.  CTA x takes
-// the item that the end of share x cuts (when no earlier end cuts it), one row
-// of one row tile per warp.
+// the item that the end of share x cuts (when no earlier end cuts it), 32 rows
+// of one row tile: a row per lane, an eighth of the columns per warp.
 template <int NP, int DT>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_constant__ AParams P)
 {
     using C = Cfg<NP>;
+    constexpr int COLS = C::DP / JOIN_WARPS;
+    __shared__ __align__(16) uint16_t tile[JOIN_ROWS][C::DP + 8];
     const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
     const int rt = (int)blockIdx.y;
-    const int r = (int)blockIdx.z * JOIN_WARPS + warp;
+    const int r0 = (int)blockIdx.z * JOIN_ROWS, r = r0 + lane;
     allow_next_kernel();
     wait_previous_kernel();
     const long long *cum = reinterpret_cast<const long long *>(P.plan + P.lay.cum);
@@ -1118,54 +1262,59 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_cons
         return;  // not cut here, or the previous end has it, or no rows
     const int local = r / P.G, g = r - local * P.G;
     const int node = rt * P.nodes_per_tile + local;
-    if (r >= BM || local >= P.nodes_per_tile || node >= P.N)
-        return;
+    const bool row = local < P.nodes_per_tile && node < P.N;
+    const bool live = row && node < nn;
     const int64_t orow = ((int64_t)b * P.N + node) * P.Hq + (int64_t)h * P.G + g;
-    const bool live = node < nn;
     const int s0 = (int)blockIdx.x, s1 = (int)((item + tiles - 1) / per);
     // a share that starts with the item, or inside it, left its first piece; one that the item
     // starts inside of left its second
     auto at = [&](int s) -> size_t {
         const int which = (long long)s * per >= item ? 0 : 1;
-        return (((size_t)s * P.row_tiles + rt) * 2 + which) * BM + r;
+        return (((size_t)s * P.row_tiles + rt) * 2 + which) * BM;
     };
     float top = -INFINITY;
     if (live)
-        for (int s = s0 + lane; s <= s1; s += 32)
-            top = fmaxf(top, P.part_ml[at(s)].x);
-    for (int d = 16; d; d >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        for (int s = s0; s <= s1; ++s)
+            top = fmaxf(top, __ldcg(&P.part_ml[at(s) + r].x));
     const float base = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const int d = lane * 4;
-    if (live) {
+    float sum = 0.0f, o[COLS];
+#pragma unroll
+    for (int j = 0; j < COLS; ++j)
+        o[j] = 0.0f;
+    if (live)
         for (int s = s0; s <= s1; ++s) {
-            const float2 ml = P.part_ml[at(s)];
+            const float2 ml = __ldcg(&P.part_ml[at(s) + r]);
+            const float *v = P.part + at(s) * C::DP + (size_t)(warp * COLS) * BM + r;
+            float x[COLS];
+#pragma unroll
+            for (int j = 0; j < COLS; ++j)
+                x[j] = warp * COLS + j < P.D ? __ldcg(v + j * BM) : 0.0f;
             if (ml.x == -INFINITY && ml.y == 0.0f)
                 continue;  // no key seen there
             const float w = ex2(ml.x - base);
             sum = fmaf(ml.y, w, sum);
-            if (d < P.D) {
-                const float4 v = *reinterpret_cast<const float4 *>(P.part + at(s) * C::DP + d);
-                o.x = fmaf(v.x, w, o.x);
-                o.y = fmaf(v.y, w, o.y);
-                o.z = fmaf(v.z, w, o.z);
-                o.w = fmaf(v.w, w, o.w);
-            }
+#pragma unroll
+            for (int j = 0; j < COLS; ++j)
+                o[j] = fmaf(x[j], w, o[j]);
         }
-    }
-    if (d < P.D) {
-        const float norm = sum != 0.0f ? 1.0f / sum : 0.0f;
-        uint2 w = make_uint2(0u, 0u);
-        if (sum != 0.0f) {
-            w.x = pack<DT>(o.x * norm, o.y * norm);
-            w.y = pack<DT>(o.z * norm, o.w * norm);
-        }
-        *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(P.out) + orow * P.D + d) = w;
-    }
-    if (lane == 0 && P.lse)
+    const float norm = sum != 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int j = 0; j < COLS; j += 2)
+        *reinterpret_cast<uint32_t *>(&tile[lane][warp * COLS + j]) =
+            sum != 0.0f ? pack<DT>(o[j] * norm, o[j + 1] * norm) : 0u;
+    if (warp == 0 && row && P.lse)
         P.lse[orow] = live ? lse_of(base, sum) : -INFINITY;
+    __syncthreads();
+    const uint32_t rows = __ballot_sync(0xffffffffu, row);
+#pragma unroll
+    for (int k = 0; k < JOIN_ROWS / JOIN_WARPS; ++k) {
+        const int y = warp * (JOIN_ROWS / JOIN_WARPS) + k;
+        const int64_t to = __shfl_sync(0xffffffffu, orow, y);
+        const int d = lane * 4;
+        if (((rows >> y) & 1u) && d < P.D)
+            *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(P.out) + to * P.D + d) =
+                *reinterpret_cast<const uint2 *>(&tile[y][d]);
+    }
 }
 
 // ------------------------------------------------------------------- host
@@ -1295,7 +1444,7 @@ int launch(const CUtensorMap (&maps)[5], AParams &P, int sms, DevInfo &di, cudaS
     if (P.slots > 1) {
         const int rows = P.nodes_per_tile * P.G < P.N * P.G ? P.nodes_per_tile * P.G : P.N * P.G;
         cfg.gridDim = dim3((unsigned int)(P.slots - 1), (unsigned int)P.row_tiles,
-                           (unsigned int)((rows + JOIN_WARPS - 1) / JOIN_WARPS));
+                           (unsigned int)((rows + JOIN_ROWS - 1) / JOIN_ROWS));
         cfg.blockDim = dim3(JOIN_WARPS * 32);
         cfg.dynamicSmemBytes = 0;
         if (cudaLaunchKernelEx(&cfg, join_kernel<NP, DT>, P) != cudaSuccess) {
