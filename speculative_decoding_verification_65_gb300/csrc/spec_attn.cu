@@ -84,11 +84,14 @@ constexpr int MAX_CTAS = 192;     // the grid's and the workspace's bound while 
 constexpr int RING = 4;           // pieces handed out ahead
 constexpr float GROWTH = 8.0f;    // log2 of how far a maximum may run ahead of the sums' scale
 
-template <int NP>
+// PAIR: a CTA has two row tiles, one for each softmax group, over the same keys.
+template <int NP, bool PAIR>
 struct Cfg {
-    // 128 KB to 192 KB of K and V in flight or in use: an SM's share of HBM
+    // 80 KB to 192 KB of K and V in flight or in use: an SM's share of HBM
     // needs about 35 KB in flight
-    static constexpr int STAGES = NP == 2 ? 3 : 6;
+    static constexpr int Q_TILES = PAIR ? 2 : 1;
+    static constexpr int KST = NP == 2 ? 3 : 6;
+    static constexpr int VST = NP == 2 ? (PAIR ? 2 : 3) : 6;
     static constexpr int TILE = NP * PANEL_BYTES;
     static constexpr int DP = NP * PANEL;  // columns of O
 };
@@ -100,7 +103,7 @@ struct Piece {
     int tiles;       // of the whole item
     int len, nn;     // cache length and nodes
     int status;
-    int idle;        // nothing to compute: no live row in this row tile
+    int idle;        // nothing to compute: no live row in the CTA's row tiles
     int first;       // 1 when the share starts inside the item or with it
 };
 
@@ -115,12 +118,15 @@ struct Tail {
     float m[2][BM], l[2][BM];
 };
 
-template <int NP>
+template <int NP, bool PAIR>
 constexpr size_t smem_bytes()
 {
-    return (size_t)Cfg<NP>::TILE * (1 + 2 * Cfg<NP>::STAGES) + sizeof(Tail);
+    using C = Cfg<NP, PAIR>;
+    return (size_t)C::TILE * (C::Q_TILES + C::KST + C::VST) + sizeof(Tail);
 }
-static_assert(smem_bytes<2>() <= 232448 && smem_bytes<1>() <= 232448, "227 KB per CTA");
+static_assert(smem_bytes<2, false>() <= 232448 && smem_bytes<1, false>() <= 232448 &&
+              smem_bytes<2, true>() <= 232448 && smem_bytes<1, true>() <= 232448,
+              "227 KB per CTA");
 
 struct AParams {
     const uint8_t *plan;
@@ -131,11 +137,12 @@ struct AParams {
     void *out;
     float *lse;
     int *status;
-    float *part;     // [ctas][2][DP][BM] unnormalised sums of split items
-    float2 *part_ml; // [ctas][2][BM] (maximum in log2 units, total)
+    float *part;     // [slots][row_tiles][2][DP][BM] unnormalised sums of split items
+    float2 *part_ml; // [slots][row_tiles][2][BM] (maximum in log2 units, total)
     float c;         // scale * log2(e)
     int B, N, Hq, Hkv, D, G;
     int nodes_per_tile, row_tiles, slots;
+    int row_groups;  // CTAs that share a key range: the row tiles, or pairs of them
     int page_size, pages_per_seq;
     int page_rows;   // rows of a cache box: min(128, page_size) (contiguous: 128)
     int new_rows;    // rows of a box of new tokens
@@ -557,24 +564,25 @@ __device__ __forceinline__ float lse_of(float m, float l)
     return l == 0.0f ? -INFINITY : (m + log2f(l)) * (1.0f / LOG2E);
 }
 
-template <int NP, int DT>
+template <int NP, int DT, bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
     attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkn,
                      const __grid_constant__ CUtensorMap mvn, const __grid_constant__ CUtensorMap mkc,
                      const __grid_constant__ CUtensorMap mvc, const __grid_constant__ AParams P)
 {
-    using C = Cfg<NP>;
+    using C = Cfg<NP, PAIR>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t q_s = smem_addr(smem);
-    const uint32_t k_s = q_s + C::TILE, v_s = k_s + C::STAGES * C::TILE;
-    uint8_t *v_p = smem + (size_t)C::TILE * (1 + C::STAGES);
-    Tail &S = *reinterpret_cast<Tail *>(smem + (size_t)C::TILE * (1 + 2 * C::STAGES));
+    const uint32_t k_s = q_s + C::Q_TILES * C::TILE, v_s = k_s + C::KST * C::TILE;
+    uint8_t *v_p = smem + (size_t)C::TILE * (C::Q_TILES + C::KST);
+    Tail &S = *reinterpret_cast<Tail *>(smem + (size_t)C::TILE * (C::Q_TILES + C::KST + C::VST));
     volatile int *abort_flag = &S.abort_flag;
     const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int slot = (int)blockIdx.x / P.row_tiles, rt = (int)blockIdx.x - slot * P.row_tiles;
+    const int slot = (int)blockIdx.x / P.row_groups;
+    const int rt0 = ((int)blockIdx.x - slot * P.row_groups) * C::Q_TILES;  // first row tile
 
     if (tid == 0) {
-        for (int i = 0; i < C::STAGES; ++i) {
+        for (int i = 0; i < 6; ++i) {
             mbar_init(&S.kfull[i], 1);
             mbar_init(&S.kempty[i], 1);
             mbar_init(&S.vfull[i], 1);
@@ -643,8 +651,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t t_o = tmem + lanes + (uint32_t)(2 * KT + s * C::DP);
         const int local = r / P.G;               // node of the row, counted in the tile
         const int g = r - local * P.G;
+        const int rt = rt0 + (PAIR ? s : 0);
         const int node = rt * P.nodes_per_tile + local;
         const bool row = local < P.nodes_per_tile && node < P.N;
+        constexpr int STEP = PAIR ? 1 : 2;       // a group's next tile
+        const int start = PAIR ? 0 : s;          // and its first
         const uint4 *masks = reinterpret_cast<const uint4 *>(P.plan + P.lay.mask);
         uint32_t cnt = 0, tv = 0;                // the group's tiles, all V tiles
         uint32_t joins = 0, notes = 0;
@@ -663,6 +674,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 mbar_arrive(&S.noted[s]);
             return wait(&S.noted[s], notes++ & 1u);
         };
+        // all warps that work on the group's tile
+        auto tile_sync = [&]() -> bool { return PAIR ? join() : group(); };
 
         bool ok = true;
         Piece p;
@@ -672,7 +685,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             };
             if (p.idle) {
                 // rows past n_nodes are 0, of a bad sequence NaN; once per item
-                if (s == 0 && p.tile0 == 0 && row) {
+                if ((PAIR || s == 0) && p.tile0 == 0 && row) {
                     const int64_t orow = out_row();
                     const float x = p.status ? NAN : 0.0f;
                     const float v[8] = {x, x, x, x, x, x, x, x};
@@ -705,12 +718,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                         see = __ldg(mask + (jt - cache_tiles));
                 }
                 uint32_t any_bad = 0;
+                auto bad_keys = [&](int q) -> uint32_t {  // of keys 32 q on, after tile_sync
+                    const volatile uint32_t(*f)[2][4] = S.bad;
+                    const uint32_t own = f[s][cnt & 1u][q];
+                    return PAIR ? own | f[s ^ 1][cnt & 1u][q] : own;
+                };
                 if (masked) {
                     // V: rows past the keys (up to the last product's 16) are zeroed; in new
                     // values, non-finite elements are noted and zeroed
                     const uint32_t vt = tv + (uint32_t)i;
-                    const int st = (int)(vt % C::STAGES);
-                    ok = wait(&S.vfull[st], (vt / C::STAGES) & 1u);
+                    const int st = (int)(vt % C::VST);
+                    ok = wait(&S.vfull[st], (vt / C::VST) & 1u);
                     if (!ok)
                         return;
                     uint8_t *vrow = v_p + (size_t)st * C::TILE + r * 128;
@@ -721,8 +739,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                             *reinterpret_cast<uint4 *>(vrow + (x >> 3) * PANEL_BYTES +
                                                        (x & 7) * 16) = make_uint4(0, 0, 0, 0);
                     } else if (!cached && r < keys) {
+                        // (two groups on one tile take a panel each)
 #pragma unroll
                         for (int x = 0; x < NP * 8; ++x) {
+                            if (PAIR && (x >> 3) != s)
+                                continue;
                             uint4 *q = reinterpret_cast<uint4 *>(vrow + (x >> 3) * PANEL_BYTES +
                                                                  (x & 7) * 16);
                             uint4 w = *q;
@@ -743,11 +764,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const uint32_t ballot = __ballot_sync(0xffffffffu, bad);
                         if (lane == 0)
                             S.bad[s][cnt & 1u][quarter] = ballot;
-                        ok = group();
+                        ok = tile_sync();
                         if (!ok)
                             return;
-                        const volatile uint32_t *f = S.bad[s][cnt & 1u];
-                        any_bad = f[0] | f[1] | f[2] | f[3];
+                        any_bad = bad_keys(0) | bad_keys(1) | bad_keys(2) | bad_keys(3);
                     }
                 }
                 ok = wait(&S.sfull[s], cnt & 1u);
@@ -757,7 +777,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 uint32_t zero_w[4] = {0, 0, 0, 0};  // keys whose weight is 0 (with any_bad only)
                 // the row's new maximum `top`; O and l follow where it has grown far
                 auto raise = [&](float top) {
-                    if (i == s) {
+                    if (i == start) {
                         m = top;
                         return;
                     }
@@ -857,8 +877,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         tmem_ld(t_o + d, o);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            uint32_t left = *static_cast<volatile uint32_t *>(
-                                &S.bad[s][cnt & 1u][q]);
+                            uint32_t left = bad_keys(q);
                             while (left) {
                                 const int bit = __ffs((int)left) - 1;
                                 left &= left - 1;
@@ -884,56 +903,65 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tmem_wait_st();
                     tc_fence_before();
                     // the notes are written over only after every warp has read them
-                    ok = group();
+                    ok = tile_sync();
                 }
                 ++cnt;
             };
             // whole tiles of the cache first, in a loop of their own: it stays small
             const int plain = min(p.n, p.len / KT - p.tile0);
-            int i = s;
-            for (; i < plain && ok; i += 2)
+            int i = start;
+            for (; i < plain && ok; i += STEP)
                 tile(i, Whole());
-            for (; i < p.n && ok; i += 2)
+            for (; i < p.n && ok; i += STEP)
                 tile(i, Masked());
             if (!ok)
                 break;
             tv += (uint32_t)p.n;
 
-            // join the two groups' halves: each group writes one half of the columns
-            const bool mine = p.n > s;           // this group had a tile
+            // each group writes one panel of the joined halves, or with a row tile of its own
+            // all of it
+            const bool mine = p.n > start;       // this group had a tile
             if (mine && !wait(&S.pvdone[s], (cnt - 1) & 1u))
                 break;
             tc_fence_after();
-            S.m[s][r] = mine ? (m == -INFINITY ? -INFINITY : m * P.c) : -INFINITY;
-            S.l[s][r] = mine ? l : 0.0f;
-            tc_fence_before();
-            if (!join())
-                break;
-            tc_fence_after();
+            float top = mine && m != -INFINITY ? m * P.c : -INFINITY;
+            float sum = mine ? l : 0.0f;
+            // a half that saw no key has no weight, whatever its O holds
+            bool some0 = !(top == -INFINITY && sum == 0.0f), some1 = false;
+            float w0 = 1.0f, w1 = 0.0f, base = top == -INFINITY ? 0.0f : top;
+            if (!PAIR) {
+                S.m[s][r] = top;
+                S.l[s][r] = sum;
+                tc_fence_before();
+                if (!join())
+                    break;
+                tc_fence_after();
+                const float m0 = S.m[0][r], m1 = S.m[1][r], l0 = S.l[0][r], l1 = S.l[1][r];
+                top = fmaxf(m0, m1);
+                base = top == -INFINITY ? 0.0f : top;
+                some0 = !(m0 == -INFINITY && l0 == 0.0f);
+                some1 = !(m1 == -INFINITY && l1 == 0.0f);
+                w0 = some0 ? ex2(m0 - base) : 0.0f;
+                w1 = some1 ? ex2(m1 - base) : 0.0f;
+                sum = l0 * w0 + l1 * w1;
+            }
             const bool whole = p.n == p.tiles;
-            const bool two = p.n > 1;
+            const bool two = !PAIR && p.n > 1;
             const bool writes = row && (whole || live);
             const int64_t orow = out_row();
             if (__any_sync(0xffffffffu, writes)) {
-                const float m0 = S.m[0][r], m1 = S.m[1][r], l0 = S.l[0][r], l1 = S.l[1][r];
-                const float top = fmaxf(m0, m1);
-                const float base = top == -INFINITY ? 0.0f : top;
-                // a half that saw no key has no weight, whatever its O holds
-                const bool some0 = !(m0 == -INFINITY && l0 == 0.0f);
-                const bool some1 = !(m1 == -INFINITY && l1 == 0.0f);
-                const float w0 = some0 ? ex2(m0 - base) : 0.0f;
-                const float w1 = some1 ? ex2(m1 - base) : 0.0f;
-                const float sum = l0 * w0 + l1 * w1;
-                const size_t at = ((size_t)blockIdx.x * 2 + (p.first ? 0 : 1)) * BM;
-                if (s < NP) {  // group s has panel s of the columns
-                    const float norm = sum != 0.0f ? 1.0f / sum : 0.0f;
+                const size_t at = (((size_t)slot * P.row_tiles + rt) * 2 + (p.first ? 0 : 1)) * BM;
+                const float norm = sum != 0.0f ? 1.0f / sum : 0.0f;
+                const uint32_t t_o0 = PAIR ? t_o : tmem + lanes + (uint32_t)(2 * KT);
+#pragma unroll 1
+                for (int panel = PAIR ? 0 : s; panel < NP; panel += STEP) {
                     uint4 u[8];
 #pragma unroll
                     for (int d0 = 0; d0 < PANEL; d0 += 32) {
                         uint32_t a[32], b[32];
-                        tmem_ld(tmem + lanes + (uint32_t)(2 * KT + s * PANEL + d0), a);
+                        tmem_ld(t_o0 + (uint32_t)(panel * PANEL + d0), a);
                         if (two)
-                            tmem_ld(tmem + lanes + (uint32_t)(2 * KT + C::DP + s * PANEL + d0), b);
+                            tmem_ld(t_o0 + (uint32_t)(C::DP + panel * PANEL + d0), b);
                         float v[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
@@ -953,10 +981,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                             }
                         } else if (writes) {
                             // [column][row]: a warp's store is one line
-                            float *o = P.part + at * C::DP + (s * PANEL + d0) * BM + r;
+                            float *o = P.part + at * C::DP + (panel * PANEL + d0) * BM + r;
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
-                                if (s * PANEL + d0 + j < P.D)
+                                if (panel * PANEL + d0 + j < P.D)
                                     o[j * BM] = v[j];
                         }
                     }
@@ -964,7 +992,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         // 8 lanes exchange so that each holds one 16-byte chunk of 8 rows: a
                         // store then covers 128 bytes of 4 rows, not 16 of 32 rows
                         exchange8(u, lane);
-                        const int d = s * PANEL + (lane & 7) * 8;
+                        const int d = panel * PANEL + (lane & 7) * 8;
                         const uint32_t rows = __ballot_sync(0xffffffffu, writes);
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
@@ -976,7 +1004,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                 }
-                if (s == 0 && row) {
+                if ((PAIR || s == 0) && row) {
                     if (whole && P.lse)
                         P.lse[orow] = live ? lse_of(base, sum) : -INFINITY;
                     if (!whole && live)
@@ -984,7 +1012,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             tc_fence_before();
-            ok = join();  // O and the exchanged statistics are free again
+            if (!PAIR)
+                ok = join();  // O and the exchanged statistics are free again
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(HELPER_REGS));
@@ -1017,10 +1046,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                     const uint32_t bytes = (uint32_t)(((keys + rows - 1) / rows) * rows * 128 * NP);
-                    const int st = (int)(t % C::STAGES);
-                    const uint32_t ph = (t / C::STAGES) & 1u;
-#pragma unroll
+                    #pragma unroll
                     for (int side = 0; side < 2; ++side) {
+                        const int stages = side ? C::VST : C::KST;
+                        const int st = (int)(t % stages);
+                        const uint32_t ph = (t / stages) & 1u;
                         unsigned long long *full = side ? &S.vfull[st] : &S.kfull[st];
                         const CUtensorMap *map = cached ? (side ? &mvc : &mkc)
                                                         : (side ? &mvn : &mkn);
@@ -1043,10 +1073,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (*abort_flag) {
                 // the loads in flight land first: each barrier's last phase that has a load
                 for (int side = 0; side < 2; ++side) {
-                    const uint32_t n = issued[side];
-                    for (uint32_t j = n > C::STAGES ? n - C::STAGES : 0; j < n; ++j)
-                        (void)mbar_wait(side ? &S.vfull[j % C::STAGES] : &S.kfull[j % C::STAGES],
-                                        (j / C::STAGES) & 1u);
+                    const uint32_t n = issued[side], stages = side ? C::VST : C::KST;
+                    for (uint32_t j = n > stages ? n - stages : 0; j < n; ++j)
+                        (void)mbar_wait(side ? &S.vfull[j % stages] : &S.kfull[j % stages],
+                                        (j / stages) & 1u);
                 }
             }
         } else if (warp == 9) {
@@ -1054,22 +1084,27 @@ __global__ void __launch_bounds__(THREADS, 1)
             // The whole warp runs the loop and one elected lane issues: what the products
             // are given then stays in uniform registers (issued from under `lane == 0` each
             // product took about 120 clocks to issue, twice its time in the tensor pipe)
-            uint32_t tk = 0, tv = 0, items = 0, cnt[2] = {0, 0};
+            // Job j of a piece: tile j of group j & 1, or of a pair tile j / 2 of group j & 1
+            uint32_t t0 = 0, items = 0, cnt[2] = {0, 0};
             bool ok = true, issued = false;
             const int ksteps = (P.D + 15) / 16;
             const uint32_t id_o = idesc<DT>(ksteps * 16, true);
             Piece p = {};
-            auto scores = [&](int i) {  // S(i) = Q K(i)^T
+            int jobs = 0;
+            auto tile_of = [](int j) -> int { return PAIR ? j >> 1 : j; };
+            auto scores = [&](int j) {  // S(j) = Q K^T
                 bool cached;
-                const int keys = tile_keys(p, p.tile0 + i, cached);
-                const int st = (int)(tk % C::STAGES);
-                ok = wait(&S.kfull[st], (tk / C::STAGES) & 1u);
+                const int keys = tile_keys(p, p.tile0 + tile_of(j), cached);
+                const uint32_t t = t0 + (uint32_t)tile_of(j);
+                const int st = (int)(t % C::KST);
+                ok = wait(&S.kfull[st], (t / C::KST) & 1u);
                 if (!ok)
                     return;
                 tc_fence_after();
                 const uint32_t id = idesc<DT>((keys + 15) & ~15, false);
-                const uint32_t d = tmem + (uint32_t)((i & 1) * KT);
-                const uint64_t qd = desc_k(q_s), kd = desc_k(k_s + st * C::TILE);
+                const uint32_t d = tmem + (uint32_t)((j & 1) * KT);
+                const uint64_t qd = desc_k(q_s + (PAIR ? (j & 1) * C::TILE : 0));
+                const uint64_t kd = desc_k(k_s + st * C::TILE);
                 if (elect_one()) {
                     if (ksteps == NP * 4) {
 #pragma unroll
@@ -1085,27 +1120,29 @@ __global__ void __launch_bounds__(THREADS, 1)
                             mma_ss(d, qd + off, kd + off, id, x ? 1u : 0u);
                         }
                     }
-                    mma_commit(&S.kempty[st]);
-                    mma_commit(&S.sfull[i & 1]);
-                    if (i == p.n - 1)
+                    if (!PAIR || (j & 1))
+                        mma_commit(&S.kempty[st]);
+                    mma_commit(&S.sfull[j & 1]);
+                    if (j == jobs - 1)
                         mma_commit(&S.qempty);
                 }
                 __syncwarp();
                 issued = true;
-                ++tk;
             };
             while (ok && next(p)) {
                 if (p.idle)
                     continue;
+                jobs = PAIR ? 2 * p.n : p.n;
                 ok = wait(&S.qfull, items & 1u);
                 ++items;
-                for (int i = 0; i < 2 && i < p.n && ok; ++i)
-                    scores(i);
-                for (int i = 0; i < p.n && ok; ++i) {
+                for (int j = 0; j < 2 && j < jobs && ok; ++j)
+                    scores(j);
+                for (int j = 0; j < jobs && ok; ++j) {
                     bool cached;
-                    const int keys = tile_keys(p, p.tile0 + i, cached);
-                    const int s = i & 1, st = (int)(tv % C::STAGES);
-                    ok = wait(&S.vfull[st], (tv / C::STAGES) & 1u) &&
+                    const int keys = tile_keys(p, p.tile0 + tile_of(j), cached);
+                    const uint32_t t = t0 + (uint32_t)tile_of(j);
+                    const int s = j & 1, st = (int)(t % C::VST);
+                    ok = wait(&S.vfull[st], (t / C::VST) & 1u) &&
                          wait(&S.pready[s], cnt[s] & 1u);
                     if (!ok)
                         break;
@@ -1115,7 +1152,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const uint64_t vd = desc_mn(v_s + st * C::TILE);
                     // 16 keys a step: 8 columns of P, 2 KB of V
                     const int steps = (keys + 15) / 16;
-                    const uint32_t more = i >= 2 ? 1u : 0u;
+                    const uint32_t more = j >= 2 ? 1u : 0u;
                     if (elect_one()) {
                         if (steps == KT / 16) {
 #pragma unroll
@@ -1127,16 +1164,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 mma_ts(d, a + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)),
                                        id_o, x ? 1u : more);
                         }
-                        mma_commit(&S.vempty[st]);
+                        if (!PAIR || s == 1)
+                            mma_commit(&S.vempty[st]);
                         mma_commit(&S.pvdone[s]);
                     }
                     __syncwarp();
                     issued = true;
-                    ++tv;
                     ++cnt[s];
-                    if (i + 2 < p.n)
-                        scores(i + 2);
+                    if (j + 2 < jobs)
+                        scores(j + 2);
                 }
+                t0 += (uint32_t)p.n;
             }
             if (*abort_flag && issued) {  // the products in flight complete (bounded)
                 if (elect_one())
@@ -1154,10 +1192,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!wait_idle(&S.qempty, (items & 1u) ^ 1u))
                     break;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&S.qfull, (uint32_t)(P.q_rows * 128 * NP));
-                    for (int i = 0; i < NP; ++i)
-                        tma_load_5d(q_s + i * PANEL_BYTES, &mq, i * PANEL, 0,
-                                    rt * P.nodes_per_tile, p.h, p.b, &S.qfull);
+                    mbar_arrive_expect_tx(&S.qfull,
+                                          (uint32_t)(P.q_rows * 128 * NP * C::Q_TILES));
+                    for (int i = 0; i < NP * C::Q_TILES; ++i)
+                        tma_load_5d(q_s + i * PANEL_BYTES, &mq, (i % NP) * PANEL, 0,
+                                    (rt0 + i / NP) * P.nodes_per_tile, p.h, p.b, &S.qfull);
                 }
                 __syncwarp();
                 ++items;
@@ -1198,7 +1237,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     p.len = (int)q.x;
                     p.nn = (int)q.y;
                     p.status = (int)q.z;
-                    p.idle = p.nn <= rt * P.nodes_per_tile;
+                    p.idle = p.nn <= rt0 * P.nodes_per_tile;
                     p.first = u - tile <= u0;
                     S.piece[at] = p;
                     mbar_arrive(&S.pfull[at]);
@@ -1235,10 +1274,10 @@ constexpr int JOIN_ROWS = 32;
 // Joins the pieces of the items that lie across a share's end.  CTA x takes
 // the item that the end of share x cuts (when no earlier end cuts it), 32 rows
 // of one row tile: a row per lane, an eighth of the columns per warp.
-template <int NP, int DT>
+template <int NP, int DT, bool PAIR>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_constant__ AParams P)
 {
-    using C = Cfg<NP>;
+    using C = Cfg<NP, PAIR>;
     constexpr int COLS = C::DP / JOIN_WARPS;
     __shared__ __align__(16) uint16_t tile[JOIN_ROWS][C::DP + 8];
     const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
@@ -1258,8 +1297,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_cons
     const int h = (int)((end - c0 * P.Hkv) / tiles);
     const long long item = c0 * P.Hkv + (long long)h * tiles;  // its first unit
     const int nn = (int)__ldg(reinterpret_cast<const uint4 *>(P.plan + P.lay.seq) + b).y;
-    if (item == end || item < end - per || nn <= rt * P.nodes_per_tile)
-        return;  // not cut here, or the previous end has it, or no rows
+    if (item == end || item < end - per || nn <= rt / C::Q_TILES * C::Q_TILES * P.nodes_per_tile)
+        return;  // not cut here, or the previous end has it, or its CTAs were idle
     const int local = r / P.G, g = r - local * P.G;
     const int node = rt * P.nodes_per_tile + local;
     const bool row = local < P.nodes_per_tile && node < P.N;
@@ -1352,8 +1391,9 @@ struct WsLayout {
 
 WsLayout ws_layout(int N, int G, int D)
 {
-    const int rt = row_tiles(N, G);
-    const size_t ctas = rt > MAX_CTAS ? (size_t)rt : (size_t)MAX_CTAS;
+    // row tiles over all slots: one for each CTA, or two
+    const size_t rt = row_tiles(N, G), most = rt > 1 ? 2 * MAX_CTAS : MAX_CTAS;
+    const size_t ctas = rt + 1 > most ? rt + 1 : most;
     const size_t dp = D > PANEL ? 2 * PANEL : PANEL;
     WsLayout w;
     w.ml = 0;
@@ -1408,35 +1448,36 @@ bool make_map(CUtensorMap *map, const void *base, int dtype, int rank, const uin
 
 struct DevInfo {
     std::atomic<int> sms;
-    std::atomic<bool> attr[2][2];
+    std::atomic<bool> attr[2][2][2];
 };
 DevInfo g_dev[64];
 
-template <int NP, int DT>
+template <int NP, int DT, bool PAIR>
 int launch(const CUtensorMap (&maps)[5], AParams &P, int sms, DevInfo &di, cudaStream_t st)
 {
-    if (!di.attr[NP - 1][DT - 1].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(attention_kernel<NP, DT>,
+    if (!di.attr[NP - 1][DT - 1][PAIR].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(attention_kernel<NP, DT, PAIR>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)smem_bytes<NP>()) != cudaSuccess) {
+                                 (int)smem_bytes<NP, PAIR>()) != cudaSuccess) {
             (void)cudaGetLastError();
             return SPEC_ECUDA;
         }
-        di.attr[NP - 1][DT - 1].store(true, std::memory_order_release);
+        di.attr[NP - 1][DT - 1][PAIR].store(true, std::memory_order_release);
     }
     const int ctas = sms < MAX_CTAS ? sms : MAX_CTAS;
-    P.slots = ctas / P.row_tiles < 1 ? 1 : ctas / P.row_tiles;
+    P.row_groups = PAIR ? (P.row_tiles + 1) / 2 : P.row_tiles;
+    P.slots = ctas / P.row_groups < 1 ? 1 : ctas / P.row_groups;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned int)(P.slots * P.row_tiles));
+    cfg.gridDim = dim3((unsigned int)(P.slots * P.row_groups));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem_bytes<NP>();
+    cfg.dynamicSmemBytes = smem_bytes<NP, PAIR>();
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, attention_kernel<NP, DT>, maps[0], maps[1], maps[2], maps[3],
+    if (cudaLaunchKernelEx(&cfg, attention_kernel<NP, DT, PAIR>, maps[0], maps[1], maps[2], maps[3],
                            maps[4], P) != cudaSuccess) {
         (void)cudaGetLastError();
         return SPEC_ECUDA;
@@ -1447,7 +1488,7 @@ int launch(const CUtensorMap (&maps)[5], AParams &P, int sms, DevInfo &di, cudaS
                            (unsigned int)((rows + JOIN_ROWS - 1) / JOIN_ROWS));
         cfg.blockDim = dim3(JOIN_WARPS * 32);
         cfg.dynamicSmemBytes = 0;
-        if (cudaLaunchKernelEx(&cfg, join_kernel<NP, DT>, P) != cudaSuccess) {
+        if (cudaLaunchKernelEx(&cfg, join_kernel<NP, DT, PAIR>, P) != cudaSuccess) {
             (void)cudaGetLastError();
             return SPEC_ECUDA;
         }
@@ -1568,11 +1609,19 @@ int32_t spec_tree_attention(const spec_tree_attention_args *args, void *workspac
         di.sms.store(sms, std::memory_order_relaxed);
     }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (a.dtype == SPEC_BF16)
-        return a.D > PANEL ? launch<2, SPEC_BF16>(maps, P, sms, di, st)
-                           : launch<1, SPEC_BF16>(maps, P, sms, di, st);
-    return a.D > PANEL ? launch<2, SPEC_F16>(maps, P, sms, di, st)
-                       : launch<1, SPEC_F16>(maps, P, sms, di, st);
+    const bool wide = a.D > PANEL, pair = P.row_tiles > 1;
+    if (a.dtype == SPEC_BF16) {
+        if (wide)
+            return pair ? launch<2, SPEC_BF16, true>(maps, P, sms, di, st)
+                        : launch<2, SPEC_BF16, false>(maps, P, sms, di, st);
+        return pair ? launch<1, SPEC_BF16, true>(maps, P, sms, di, st)
+                    : launch<1, SPEC_BF16, false>(maps, P, sms, di, st);
+    }
+    if (wide)
+        return pair ? launch<2, SPEC_F16, true>(maps, P, sms, di, st)
+                    : launch<2, SPEC_F16, false>(maps, P, sms, di, st);
+    return pair ? launch<1, SPEC_F16, true>(maps, P, sms, di, st)
+                : launch<1, SPEC_F16, false>(maps, P, sms, di, st);
 }
 
 }  // extern "C"
