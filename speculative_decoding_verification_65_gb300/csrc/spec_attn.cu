@@ -90,8 +90,22 @@ struct Cfg {
     // 80 KB to 192 KB of K and V in flight or in use: an SM's share of HBM
     // needs about 35 KB in flight
     static constexpr int Q_TILES = PAIR ? 2 : 1;
-    static constexpr int KST = NP == 2 ? 3 : 6;
-    static constexpr int VST = NP == 2 ? (PAIR ? 2 : 3) : 6;
+    static constexpr int KST = NP == 2 ? (PAIR ? 3 : 4) : 6;
+    static constexpr int VST = NP == 2 ? 2 : 6;
+    // Stage and phase of a group's tile number n.  A wait for a phase tells it from the one
+    // before only if that one is known to be over, so nobody may skip a stage's phases: in
+    // a pair both groups go through all stages, otherwise each group has half of its own.
+    static constexpr int KOWN = PAIR ? KST : KST / 2, VOWN = PAIR ? VST : VST / 2;
+    __device__ static __forceinline__ int kstage(int s, uint32_t n)
+    {
+        return (PAIR ? 0 : s * KOWN) + (int)(n % KOWN);
+    }
+    __device__ static __forceinline__ uint32_t kphase(uint32_t n) { return (n / KOWN) & 1u; }
+    __device__ static __forceinline__ int vstage(int s, uint32_t n)
+    {
+        return (PAIR ? 0 : s * VOWN) + (int)(n % VOWN);
+    }
+    __device__ static __forceinline__ uint32_t vphase(uint32_t n) { return (n / VOWN) & 1u; }
     static constexpr int TILE = NP * PANEL_BYTES;
     static constexpr int DP = NP * PANEL;  // columns of O
 };
@@ -657,7 +671,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         constexpr int STEP = PAIR ? 1 : 2;       // a group's next tile
         const int start = PAIR ? 0 : s;          // and its first
         const uint4 *masks = reinterpret_cast<const uint4 *>(P.plan + P.lay.mask);
-        uint32_t cnt = 0, tv = 0;                // the group's tiles, all V tiles
+        uint32_t cnt = 0;                        // the group's tiles
         uint32_t joins = 0, notes = 0;
         const unsigned long long c2 = f2(P.c, P.c);
         // all softmax warps have come here
@@ -717,6 +731,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (live && jt > cache_tiles)
                         see = __ldg(mask + (jt - cache_tiles));
                 }
+                // the scores are there, and the group's product before is done
+                ok = wait(&S.sfull[s], cnt & 1u);
+                if (!ok)
+                    return;
+                tc_fence_after();
                 uint32_t any_bad = 0;
                 auto bad_keys = [&](int q) -> uint32_t {  // of keys 32 q on, after tile_sync
                     const volatile uint32_t(*f)[2][4] = S.bad;
@@ -726,9 +745,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (masked) {
                     // V: rows past the keys (up to the last product's 16) are zeroed; in new
                     // values, non-finite elements are noted and zeroed
-                    const uint32_t vt = tv + (uint32_t)i;
-                    const int st = (int)(vt % C::VST);
-                    ok = wait(&S.vfull[st], (vt / C::VST) & 1u);
+                    const int st = C::vstage(s, cnt);
+                    ok = wait(&S.vfull[st], C::vphase(cnt));
                     if (!ok)
                         return;
                     uint8_t *vrow = v_p + (size_t)st * C::TILE + r * 128;
@@ -770,10 +788,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                         any_bad = bad_keys(0) | bad_keys(1) | bad_keys(2) | bad_keys(3);
                     }
                 }
-                ok = wait(&S.sfull[s], cnt & 1u);
-                if (!ok)
-                    return;
-                tc_fence_after();
                 uint32_t zero_w[4] = {0, 0, 0, 0};  // keys whose weight is 0 (with any_bad only)
                 // the row's new maximum `top`; O and l follow where it has grown far
                 auto raise = [&](float top) {
@@ -806,10 +820,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 fmaxf(max32(x[2]), max32(x[3]))));
                     const float shift = m == -INFINITY ? 0.0f : -m * P.c;
                     const unsigned long long shift2 = f2(shift, shift);
-#pragma unroll
+                    // the scores are read again, chunk by chunk: a loop that four warps and two
+                    // issuers share an instruction cache with beats a second saved read
+#pragma unroll 1
                     for (int h = 0; h < 4; ++h) {
-                        uint32_t pk[16];
-                        weigh<DT>(x[h], c2, shift2, sum, pk);
+                        uint32_t y[32], pk[16];
+                        tmem_ld(t_s + h * 32, y);
+                        weigh<DT>(y, c2, shift2, sum, pk);
+                        // weights 32 h on lie in columns 16 h on: over scores that were read
                         tmem_st(t_s + h * 16, pk);
                     }
                 }
@@ -838,7 +856,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                         tmem_ld(t_s + h * 32, x);
                         hide(x, bits(h));
                         weigh<DT>(x, c2, shift2, sum, pk);
-                        // weights 32 h on lie in columns 16 h on: over scores that were read
                         tmem_st(t_s + h * 16, pk);
                         if (any_bad) {
                             uint32_t z = 0;
@@ -916,7 +933,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tile(i, Masked());
             if (!ok)
                 break;
-            tv += (uint32_t)p.n;
 
             // each group writes one panel of the joined halves, or with a row tile of its own
             // all of it
@@ -1019,73 +1035,81 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(HELPER_REGS));
         if (warp == 8) {
             // ------------------------------------------------ TMA of K and V
-            uint32_t t = 0;
-            uint32_t issued[2] = {0, 0};         // tiles of K and of V whose loads were issued
+            uint32_t nk[2] = {0, 0}, nv[2] = {0, 0};
+            uint32_t out_k = 0, out_v = 0;       // stages that a load was issued for,
+            uint32_t ph_k = 0, ph_v = 0;         // and the phase of the last one
             bool ok = true;
             Piece p;
+            // one tile's keys (side 0) or values (1): a box of rows per lane
+            auto load = [&](int side, int i) {
+                bool cached;
+                const int jt = p.tile0 + i;
+                const int keys = tile_keys(p, jt, cached);
+                const int rows = cached ? P.page_rows : P.new_rows;
+                const int at = lane * rows;
+                const bool mine = at < keys;
+                int y = (jt - (p.len + KT - 1) / KT) * KT + at, w = p.b;
+                if (cached) {
+                    y = jt * KT + at;
+                    if (P.page_table && mine) {
+                        const int e = y / P.page_size;
+                        w = e < P.pages_per_seq
+                            ? __ldg(P.page_table + (size_t)p.b * P.pages_per_seq + e) : -1;
+                        y -= e * P.page_size;
+                    }
+                }
+                const int g = PAIR ? 0 : i & 1;
+                const uint32_t n = side ? nv[g]++ : nk[g]++;
+                const int st = side ? C::vstage(g, n) : C::kstage(g, n);
+                const uint32_t ph = side ? C::vphase(n) : C::kphase(n);
+                ok = wait(side ? &S.vempty[st] : &S.kempty[st], ph ^ 1u);
+                if (!ok)
+                    return;
+                unsigned long long *full = side ? &S.vfull[st] : &S.kfull[st];
+                if (lane == 0)
+                    mbar_arrive_expect_tx(
+                        full, (uint32_t)(((keys + rows - 1) / rows) * rows * 128 * NP));
+                __syncwarp();
+                uint32_t &out = side ? out_v : out_k, &out_ph = side ? ph_v : ph_k;
+                out |= 1u << st;
+                out_ph = (out_ph & ~(1u << st)) | (ph << st);
+                if (mine) {
+                    const CUtensorMap *map = cached ? (side ? &mvc : &mkc) : (side ? &mvn : &mkn);
+                    const uint32_t dst =
+                        (side ? v_s : k_s) + (uint32_t)(st * C::TILE + at * 128);
+#pragma unroll
+                    for (int d = 0; d < NP; ++d)
+                        tma_load_4d(dst + d * PANEL_BYTES, map, d * PANEL, y, p.h, w, full);
+                }
+                __syncwarp();
+            };
             while (ok && next(p)) {
                 if (p.idle)
                     continue;
-                const int cache_tiles = (p.len + KT - 1) / KT;
-                for (int i = 0; i < p.n && ok; ++i, ++t) {
-                    bool cached;
-                    const int jt = p.tile0 + i;
-                    const int keys = tile_keys(p, jt, cached);
-                    // box of this lane: its rows of the tile and its page
-                    const int rows = cached ? P.page_rows : P.new_rows;
-                    const int at = lane * rows;
-                    const bool mine = at < keys;
-                    int y = (jt - cache_tiles) * KT + at, w = p.b;
-                    if (cached) {
-                        y = jt * KT + at;
-                        if (P.page_table && mine) {
-                            const int e = y / P.page_size;
-                            w = e < P.pages_per_seq
-                                ? __ldg(P.page_table + (size_t)p.b * P.pages_per_seq + e) : -1;
-                            y -= e * P.page_size;
-                        }
-                    }
-                    const uint32_t bytes = (uint32_t)(((keys + rows - 1) / rows) * rows * 128 * NP);
-                    #pragma unroll
-                    for (int side = 0; side < 2; ++side) {
-                        const int stages = side ? C::VST : C::KST;
-                        const int st = (int)(t % stages);
-                        const uint32_t ph = (t / stages) & 1u;
-                        unsigned long long *full = side ? &S.vfull[st] : &S.kfull[st];
-                        const CUtensorMap *map = cached ? (side ? &mvc : &mkc)
-                                                        : (side ? &mvn : &mkn);
-                        ok = ok && wait(side ? &S.vempty[st] : &S.kempty[st], ph ^ 1u);
-                        if (!ok)
-                            break;
-                        if (lane == 0)
-                            mbar_arrive_expect_tx(full, bytes);
-                        __syncwarp();
-                        issued[side] = t + 1;
-                        if (mine) {
-                            const uint32_t dst = (side ? v_s : k_s) + st * C::TILE + at * 128;
-#pragma unroll
-                            for (int d = 0; d < NP; ++d)
-                                tma_load_4d(dst + d * PANEL_BYTES, map, d * PANEL, y, p.h, w, full);
-                        }
-                    }
+                // in the order of need: the scores run two tiles ahead of the products with V
+                for (int i = -2; i < p.n && ok; ++i) {
+                    if (i >= 0)
+                        load(1, i);
+                    if (ok && i + 2 < p.n)
+                        load(0, i + 2);
                 }
             }
             if (*abort_flag) {
                 // the loads in flight land first: each barrier's last phase that has a load
-                for (int side = 0; side < 2; ++side) {
-                    const uint32_t n = issued[side], stages = side ? C::VST : C::KST;
-                    for (uint32_t j = n > stages ? n - stages : 0; j < n; ++j)
-                        (void)mbar_wait(side ? &S.vfull[j % stages] : &S.kfull[j % stages],
-                                        (j / stages) & 1u);
+                for (int st = 0; st < 6; ++st) {
+                    if ((out_k >> st) & 1u)
+                        (void)mbar_wait(&S.kfull[st], (ph_k >> st) & 1u);
+                    if ((out_v >> st) & 1u)
+                        (void)mbar_wait(&S.vfull[st], (ph_v >> st) & 1u);
                 }
             }
         } else if (warp == 9) {
-            // -------------------------------------------------- MMA issuer
+            // -------------------------------------------- issuer of the products
             // The whole warp runs the loop and one elected lane issues: what the products
             // are given then stays in uniform registers (issued from under `lane == 0` each
-            // product took about 120 clocks to issue, twice its time in the tensor pipe)
+            // product took about 120 clocks to issue, twice its time in the tensor pipe).
             // Job j of a piece: tile j of group j & 1, or of a pair tile j / 2 of group j & 1
-            uint32_t t0 = 0, items = 0, cnt[2] = {0, 0};
+            uint32_t items = 0, nk[2] = {0, 0}, cnt[2] = {0, 0};
             bool ok = true, issued = false;
             const int ksteps = (P.D + 15) / 16;
             const uint32_t id_o = idesc<DT>(ksteps * 16, true);
@@ -1095,15 +1119,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             auto scores = [&](int j) {  // S(j) = Q K^T
                 bool cached;
                 const int keys = tile_keys(p, p.tile0 + tile_of(j), cached);
-                const uint32_t t = t0 + (uint32_t)tile_of(j);
-                const int st = (int)(t % C::KST);
-                ok = wait(&S.kfull[st], (t / C::KST) & 1u);
+                const int s = j & 1;
+                const uint32_t n = s ? nk[1] : nk[0];
+                const int st = C::kstage(s, n);
+                ok = wait(&S.kfull[st], C::kphase(n));
                 if (!ok)
                     return;
                 tc_fence_after();
                 const uint32_t id = idesc<DT>((keys + 15) & ~15, false);
-                const uint32_t d = tmem + (uint32_t)((j & 1) * KT);
-                const uint64_t qd = desc_k(q_s + (PAIR ? (j & 1) * C::TILE : 0));
+                const uint32_t d = tmem + (uint32_t)(s * KT);
+                const uint64_t qd = desc_k(q_s + (PAIR ? s * C::TILE : 0));
                 const uint64_t kd = desc_k(k_s + st * C::TILE);
                 if (elect_one()) {
                     if (ksteps == NP * 4) {
@@ -1120,14 +1145,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                             mma_ss(d, qd + off, kd + off, id, x ? 1u : 0u);
                         }
                     }
-                    if (!PAIR || (j & 1))
+                    if (!PAIR || s)
                         mma_commit(&S.kempty[st]);
-                    mma_commit(&S.sfull[j & 1]);
+                    mma_commit(&S.sfull[s]);
                     if (j == jobs - 1)
                         mma_commit(&S.qempty);
                 }
                 __syncwarp();
                 issued = true;
+                if (s)
+                    ++nk[1];
+                else
+                    ++nk[0];
             };
             while (ok && next(p)) {
                 if (p.idle)
@@ -1140,10 +1169,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int j = 0; j < jobs && ok; ++j) {
                     bool cached;
                     const int keys = tile_keys(p, p.tile0 + tile_of(j), cached);
-                    const uint32_t t = t0 + (uint32_t)tile_of(j);
-                    const int s = j & 1, st = (int)(t % C::VST);
-                    ok = wait(&S.vfull[st], (t / C::VST) & 1u) &&
-                         wait(&S.pready[s], cnt[s] & 1u);
+                    const int s = j & 1;
+                    const uint32_t n = s ? cnt[1] : cnt[0];
+                    const int st = C::vstage(s, n);
+                    ok = wait(&S.vfull[st], C::vphase(n)) && wait(&S.pready[s], n & 1u);
                     if (!ok)
                         break;
                     tc_fence_after();
@@ -1164,17 +1193,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 mma_ts(d, a + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)),
                                        id_o, x ? 1u : more);
                         }
-                        if (!PAIR || s == 1)
+                        if (!PAIR || s)
                             mma_commit(&S.vempty[st]);
                         mma_commit(&S.pvdone[s]);
                     }
                     __syncwarp();
                     issued = true;
-                    ++cnt[s];
+                    if (s)
+                        ++cnt[1];
+                    else
+                        ++cnt[0];
                     if (j + 2 < jobs)
                         scores(j + 2);
                 }
-                t0 += (uint32_t)p.n;
             }
             if (*abort_flag && issued) {  // the products in flight complete (bounded)
                 if (elect_one())
