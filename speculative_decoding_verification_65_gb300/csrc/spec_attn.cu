@@ -10,8 +10,7 @@
 // takes an SM's share of the HBM rate about 2850 clocks, its two products
 // about 1030 and its exponentials 512, so up to 128 rows the products' cost is
 // covered whatever part of the rows is in use, and single tokens use the same
-// kernel.  More rows are several row tiles (whole nodes each); the CTAs of
-// one key range run next to each other, so the second one finds the keys in L2.
+// kernel.  More rows are several row tiles (whole nodes each), taken in pairs.
 //
 // Roles in a CTA (one per SM, 3 warpgroups; the third gives registers to the others):
 //   warps 0-3, 4-7  two softmax groups, one thread per row.  Group s takes the
@@ -35,9 +34,10 @@
 // since the last time (all of the statistics are fp32, so the larger weights
 // in between lose nothing); most tiles then leave O in TMEM alone.
 //
-// Work: the key tiles of all sequences and heads in a line (the plan's
-// prefix sums) are dealt to the CTAs in equal runs, whatever the lengths.  An
-// item (sequence, head) that lies in one CTA's run is written by it; of a
+// Work: the key tiles of all sequences, heads and row groups that hold a node (a
+// row tile, or a pair) stand in a line and are dealt to the CTAs in equal runs,
+// whatever the lengths and the numbers of nodes.  An
+// item (sequence, head, row group) that lies in one CTA's run is written by it; of a
 // split item each CTA leaves its unnormalised sums with their maximum and
 // total in the workspace, and a second kernel joins them in order, so repeats
 // are bit-equal.  No CTA waits for another.
@@ -78,9 +78,9 @@ constexpr int PANEL_BYTES = 128 * 128;  // 128 rows (or keys) of one panel
 constexpr int SOFT_THREADS = 256;
 constexpr int THREADS = SOFT_THREADS + 128;
 // 384 threads launch with 168 registers each, 64512; a softmax thread holds a
-// row's 128 scores: 256 * 224 + 128 * 56 = 64512
-constexpr int SOFT_REGS = 224, HELPER_REGS = 56;
-constexpr int MAX_CTAS = 192;     // the grid's and the workspace's bound while row tiles allow it
+// row's 128 scores: 256 * 208 + 128 * 88 = 64512
+constexpr int SOFT_REGS = 208, HELPER_REGS = 88;
+constexpr int MAX_CTAS = 192;     // the grid's and the workspace's bound
 constexpr int RING = 4;           // pieces handed out ahead
 constexpr float GROWTH = 8.0f;    // log2 of how far a maximum may run ahead of the sums' scale
 
@@ -90,34 +90,29 @@ struct Cfg {
     // 80 KB to 192 KB of K and V in flight or in use: an SM's share of HBM
     // needs about 35 KB in flight
     static constexpr int Q_TILES = PAIR ? 2 : 1;
-    static constexpr int KST = NP == 2 ? (PAIR ? 3 : 4) : 6;
-    static constexpr int VST = NP == 2 ? 2 : 6;
-    // Stage and phase of a group's tile number n.  A wait for a phase tells it from the one
-    // before only if that one is known to be over, so nobody may skip a stage's phases: in
-    // a pair both groups go through all stages, otherwise each group has half of its own.
-    static constexpr int KOWN = PAIR ? KST : KST / 2, VOWN = PAIR ? VST : VST / 2;
-    __device__ static __forceinline__ int kstage(int s, uint32_t n)
-    {
-        return (PAIR ? 0 : s * KOWN) + (int)(n % KOWN);
-    }
-    __device__ static __forceinline__ uint32_t kphase(uint32_t n) { return (n / KOWN) & 1u; }
-    __device__ static __forceinline__ int vstage(int s, uint32_t n)
-    {
-        return (PAIR ? 0 : s * VOWN) + (int)(n % VOWN);
-    }
-    __device__ static __forceinline__ uint32_t vphase(uint32_t n) { return (n / VOWN) & 1u; }
+    static constexpr int KST = NP == 2 ? 3 : 6;
+    static constexpr int VST = NP == 2 ? (PAIR ? 2 : 3) : 6;
     static constexpr int TILE = NP * PANEL_BYTES;
     static constexpr int DP = NP * PANEL;  // columns of O
 };
+// Stages are taken in the order of the CTA's tiles.  A wait for a phase of a
+// barrier tells it from the phase before only if that one is known to be over
+// (parity), so whoever waits on a stage has gone through its earlier phases: the
+// loader and the issuer wait for all of them, and a softmax group that looks
+// at V waits for its tile's scores first, which the issuer's products of
+// every earlier tile precede.
+
 
 // A run of one item's key tiles inside a CTA's share.
 struct Piece {
     int b, h;
+    int rt0;         // first row tile
+    int last;        // 1 in the sequence's last row group that holds a node
     int tile0, n;    // first tile and number of tiles (0: the share has ended)
     int tiles;       // of the whole item
     int len, nn;     // cache length and nodes
     int status;
-    int idle;        // nothing to compute: no live row in the CTA's row tiles
+    int idle;        // nothing to compute: no node, or a bad sequence
     int first;       // 1 when the share starts inside the item or with it
 };
 
@@ -151,12 +146,12 @@ struct AParams {
     void *out;
     float *lse;
     int *status;
-    float *part;     // [slots][row_tiles][2][DP][BM] unnormalised sums of split items
-    float2 *part_ml; // [slots][row_tiles][2][BM] (maximum in log2 units, total)
+    float *part;     // [ctas][Q_TILES][2][DP][BM] unnormalised sums of split items
+    float2 *part_ml; // [ctas][Q_TILES][2][BM] (maximum in log2 units, total)
     float c;         // scale * log2(e)
     int B, N, Hq, Hkv, D, G;
-    int nodes_per_tile, row_tiles, slots;
-    int row_groups;  // CTAs that share a key range: the row tiles, or pairs of them
+    int nodes_per_tile;
+    int slots;       // CTAs
     int page_size, pages_per_seq;
     int page_rows;   // rows of a cache box: min(128, page_size) (contiguous: 128)
     int new_rows;    // rows of a box of new tokens
@@ -498,18 +493,80 @@ __device__ __forceinline__ void weigh(const uint32_t (&x)[32], unsigned long lon
 
 // ------------------------------------------------------------------- work
 
-// Sequence of unit u: the last b with cum[b] * Hkv <= u.
-__device__ __forceinline__ int find_seq(const long long *cum, int B, int Hkv, long long u)
+// Where a unit lies: its sequence, that sequence's first unit, its key tiles and
+// row groups.
+struct Place {
+    int b;
+    long long first;
+    int tiles, groups;
+    uint4 seq;       // the plan's PlanSeq
+};
+
+template <bool PAIR>
+__device__ __forceinline__ int row_groups_of(const AParams &P, int nn)
 {
-    int lo = 0, hi = B - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(cum + mid) * Hkv <= u)
-            lo = mid;
-        else
-            hi = mid - 1;
+    const int per = P.nodes_per_tile * 2;
+    return PAIR && nn > per ? (nn + per - 1) / per : 1;
+}
+
+// The place of sequence b whose first unit is `first`.
+template <bool PAIR>
+__device__ __forceinline__ Place place_at(const AParams &P, int b, long long first)
+{
+    const long long *cum = reinterpret_cast<const long long *>(P.plan + P.lay.cum);
+    Place q;
+    q.b = b;
+    q.first = first;
+    q.tiles = (int)(__ldg(cum + b + 1) - __ldg(cum + b));
+    q.seq = __ldg(reinterpret_cast<const uint4 *>(P.plan + P.lay.seq) + b);
+    q.groups = row_groups_of<PAIR>(P, (int)q.seq.y);
+    return q;
+}
+
+// All units (u < 0), or the first unit of the sequence that holds unit u < all, which goes to b.  One row
+// group each: the plan's prefix sums.  Otherwise a warp adds them up, 32 sequences a step.
+template <bool PAIR>
+__device__ __forceinline__ long long units(const AParams &P, long long u, int &b)
+{
+    const long long *cum = reinterpret_cast<const long long *>(P.plan + P.lay.cum);
+    if (!PAIR) {
+        if (u < 0)
+            return __ldg(cum + P.B) * P.Hkv;
+        int lo = 0, hi = P.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (__ldg(cum + mid) * P.Hkv <= u)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        b = lo;
+        return __ldg(cum + lo) * P.Hkv;
     }
-    return lo;
+    const int lane = (int)threadIdx.x & 31;
+    long long before = 0;
+    for (int b0 = 0; b0 < P.B; b0 += 32) {
+        long long v = 0;
+        if (b0 + lane < P.B) {
+            const Place q = place_at<PAIR>(P, b0 + lane, 0);
+            v = (long long)q.tiles * q.groups * P.Hkv;
+        }
+        long long sum = v;
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d)
+                sum += o;
+        }
+        const long long all = __shfl_sync(0xffffffffu, sum, 31);
+        if (u >= 0 && u < before + all) {
+            const uint32_t past = __ballot_sync(0xffffffffu, before + sum > u);
+            const int at = __ffs((int)past) - 1;
+            b = b0 + at;
+            return before + __shfl_sync(0xffffffffu, sum - v, at);
+        }
+        before += all;
+    }
+    return before;
 }
 
 struct Whole {
@@ -592,8 +649,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     Tail &S = *reinterpret_cast<Tail *>(smem + (size_t)C::TILE * (C::Q_TILES + C::KST + C::VST));
     volatile int *abort_flag = &S.abort_flag;
     const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int slot = (int)blockIdx.x / P.row_groups;
-    const int rt0 = ((int)blockIdx.x - slot * P.row_groups) * C::Q_TILES;  // first row tile
+    const int slot = (int)blockIdx.x;
 
     if (tid == 0) {
         for (int i = 0; i < 6; ++i) {
@@ -665,13 +721,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t t_o = tmem + lanes + (uint32_t)(2 * KT + s * C::DP);
         const int local = r / P.G;               // node of the row, counted in the tile
         const int g = r - local * P.G;
-        const int rt = rt0 + (PAIR ? s : 0);
-        const int node = rt * P.nodes_per_tile + local;
-        const bool row = local < P.nodes_per_tile && node < P.N;
         constexpr int STEP = PAIR ? 1 : 2;       // a group's next tile
         const int start = PAIR ? 0 : s;          // and its first
         const uint4 *masks = reinterpret_cast<const uint4 *>(P.plan + P.lay.mask);
-        uint32_t cnt = 0;                        // the group's tiles
+        uint32_t cnt = 0, tv = 0;                // the group's tiles, all tiles
         uint32_t joins = 0, notes = 0;
         const unsigned long long c2 = f2(P.c, P.c);
         // all softmax warps have come here
@@ -692,24 +745,30 @@ __global__ void __launch_bounds__(THREADS, 1)
         auto tile_sync = [&]() -> bool { return PAIR ? join() : group(); };
 
         bool ok = true;
-        Piece p;
+        Piece p = {};
         while (ok && next(p)) {
+            const int node = (p.rt0 + (PAIR ? s : 0)) * P.nodes_per_tile + local;
+            const bool row = local < P.nodes_per_tile && node < P.N;
             auto out_row = [&]() -> int64_t {
                 return ((int64_t)p.b * P.N + node) * P.Hq + (int64_t)p.h * P.G + g;
             };
-            if (p.idle) {
-                // rows past n_nodes are 0, of a bad sequence NaN; once per item
-                if ((PAIR || s == 0) && p.tile0 == 0 && row) {
-                    const int64_t orow = out_row();
-                    const float x = p.status ? NAN : 0.0f;
-                    const float v[8] = {x, x, x, x, x, x, x, x};
+            if ((p.idle || p.last) && p.tile0 == 0) {
+                // the head's rows of nodes that no row group has are 0, a bad sequence's NaN
+                const int from =
+                    p.idle ? 0 : min(P.N, (p.rt0 + C::Q_TILES) * P.nodes_per_tile);
+                const float x = p.status ? NAN : 0.0f;
+                const float v[8] = {x, x, x, x, x, x, x, x};
+                for (int y = tid; y < (P.N - from) * P.G; y += SOFT_THREADS) {
+                    const int64_t to = ((int64_t)p.b * P.N + from + y / P.G) * P.Hq +
+                                       (int64_t)p.h * P.G + y % P.G;
                     for (int d = 0; d < P.D; d += 8)
-                        store8<DT>(P, orow * P.D + d, v);
+                        store8<DT>(P, to * P.D + d, v);
                     if (P.lse)
-                        P.lse[orow] = p.status ? NAN : -INFINITY;
+                        P.lse[to] = p.status ? NAN : -INFINITY;
                 }
-                continue;
             }
+            if (p.idle)
+                continue;
             const bool live = row && node < p.nn;
             const bool warp_live = __any_sync(0xffffffffu, live);
             const int cache_tiles = (p.len + KT - 1) / KT;
@@ -745,8 +804,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (masked) {
                     // V: rows past the keys (up to the last product's 16) are zeroed; in new
                     // values, non-finite elements are noted and zeroed
-                    const int st = C::vstage(s, cnt);
-                    ok = wait(&S.vfull[st], C::vphase(cnt));
+                    const uint32_t t = tv + (uint32_t)i;
+                    const int st = (int)(t % C::VST);
+                    ok = wait(&S.vfull[st], (t / C::VST) & 1u);
                     if (!ok)
                         return;
                     uint8_t *vrow = v_p + (size_t)st * C::TILE + r * 128;
@@ -934,6 +994,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!ok)
                 break;
 
+            tv += (uint32_t)p.n;
+
             // each group writes one panel of the joined halves, or with a row tile of its own
             // all of it
             const bool mine = p.n > start;       // this group had a tile
@@ -966,7 +1028,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool writes = row && (whole || live);
             const int64_t orow = out_row();
             if (__any_sync(0xffffffffu, writes)) {
-                const size_t at = (((size_t)slot * P.row_tiles + rt) * 2 + (p.first ? 0 : 1)) * BM;
+                const size_t at =
+                    (((size_t)slot * C::Q_TILES + (PAIR ? s : 0)) * 2 + (p.first ? 0 : 1)) * BM;
                 const float norm = sum != 0.0f ? 1.0f / sum : 0.0f;
                 const uint32_t t_o0 = PAIR ? t_o : tmem + lanes + (uint32_t)(2 * KT);
 #pragma unroll 1
@@ -1035,11 +1098,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(HELPER_REGS));
         if (warp == 8) {
             // ------------------------------------------------ TMA of K and V
-            uint32_t nk[2] = {0, 0}, nv[2] = {0, 0};
+            uint32_t t0 = 0;                     // tiles of earlier pieces
             uint32_t out_k = 0, out_v = 0;       // stages that a load was issued for,
             uint32_t ph_k = 0, ph_v = 0;         // and the phase of the last one
             bool ok = true;
-            Piece p;
+            Piece p = {};
             // one tile's keys (side 0) or values (1): a box of rows per lane
             auto load = [&](int side, int i) {
                 bool cached;
@@ -1058,10 +1121,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                         y -= e * P.page_size;
                     }
                 }
-                const int g = PAIR ? 0 : i & 1;
-                const uint32_t n = side ? nv[g]++ : nk[g]++;
-                const int st = side ? C::vstage(g, n) : C::kstage(g, n);
-                const uint32_t ph = side ? C::vphase(n) : C::kphase(n);
+                const uint32_t n = t0 + (uint32_t)i, stages = side ? C::VST : C::KST;
+                const int st = (int)(n % stages);
+                const uint32_t ph = (n / stages) & 1u;
                 ok = wait(side ? &S.vempty[st] : &S.kempty[st], ph ^ 1u);
                 if (!ok)
                     return;
@@ -1086,13 +1148,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             while (ok && next(p)) {
                 if (p.idle)
                     continue;
-                // in the order of need: the scores run two tiles ahead of the products with V
-                for (int i = -2; i < p.n && ok; ++i) {
-                    if (i >= 0)
+                for (int i = 0; i < p.n && ok; ++i) {
+                    load(0, i);
+                    if (ok)
                         load(1, i);
-                    if (ok && i + 2 < p.n)
-                        load(0, i + 2);
                 }
+                t0 += (uint32_t)p.n;
             }
             if (*abort_flag) {
                 // the loads in flight land first: each barrier's last phase that has a load
@@ -1109,7 +1170,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // are given then stays in uniform registers (issued from under `lane == 0` each
             // product took about 120 clocks to issue, twice its time in the tensor pipe).
             // Job j of a piece: tile j of group j & 1, or of a pair tile j / 2 of group j & 1
-            uint32_t items = 0, nk[2] = {0, 0}, cnt[2] = {0, 0};
+            uint32_t items = 0, t0 = 0, cnt[2] = {0, 0};
             bool ok = true, issued = false;
             const int ksteps = (P.D + 15) / 16;
             const uint32_t id_o = idesc<DT>(ksteps * 16, true);
@@ -1120,9 +1181,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 bool cached;
                 const int keys = tile_keys(p, p.tile0 + tile_of(j), cached);
                 const int s = j & 1;
-                const uint32_t n = s ? nk[1] : nk[0];
-                const int st = C::kstage(s, n);
-                ok = wait(&S.kfull[st], C::kphase(n));
+                const uint32_t t = t0 + (uint32_t)tile_of(j);
+                const int st = (int)(t % C::KST);
+                ok = wait(&S.kfull[st], (t / C::KST) & 1u);
                 if (!ok)
                     return;
                 tc_fence_after();
@@ -1153,10 +1214,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 __syncwarp();
                 issued = true;
-                if (s)
-                    ++nk[1];
-                else
-                    ++nk[0];
             };
             while (ok && next(p)) {
                 if (p.idle)
@@ -1171,8 +1228,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const int keys = tile_keys(p, p.tile0 + tile_of(j), cached);
                     const int s = j & 1;
                     const uint32_t n = s ? cnt[1] : cnt[0];
-                    const int st = C::vstage(s, n);
-                    ok = wait(&S.vfull[st], C::vphase(n)) && wait(&S.pready[s], n & 1u);
+                    const uint32_t t = t0 + (uint32_t)tile_of(j);
+                    const int st = (int)(t % C::VST);
+                    ok = wait(&S.vfull[st], (t / C::VST) & 1u) && wait(&S.pready[s], n & 1u);
                     if (!ok)
                         break;
                     tc_fence_after();
@@ -1206,6 +1264,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (j + 2 < jobs)
                         scores(j + 2);
                 }
+                t0 += (uint32_t)p.n;
             }
             if (*abort_flag && issued) {  // the products in flight complete (bounded)
                 if (elect_one())
@@ -1216,7 +1275,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else if (warp == 10) {
             // ---------------------------------------------------- TMA of Q
             uint32_t items = 0;
-            Piece p;
+            Piece p = {};
             while (next(p)) {
                 if (p.idle)
                     continue;
@@ -1227,7 +1286,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                           (uint32_t)(P.q_rows * 128 * NP * C::Q_TILES));
                     for (int i = 0; i < NP * C::Q_TILES; ++i)
                         tma_load_5d(q_s + i * PANEL_BYTES, &mq, (i % NP) * PANEL, 0,
-                                    (rt0 + i / NP) * P.nodes_per_tile, p.h, p.b, &S.qfull);
+                                    (p.rt0 + i / NP) * P.nodes_per_tile, p.h, p.b, &S.qfull);
                 }
                 __syncwarp();
                 ++items;
@@ -1236,39 +1295,41 @@ __global__ void __launch_bounds__(THREADS, 1)
                 (void)mbar_wait(&S.qfull, (items - 1) & 1u);
         } else {
             // ------------------------------------------- the share's pieces
-            const long long *cum = reinterpret_cast<const long long *>(P.plan + P.lay.cum);
-            const uint4 *seqs = reinterpret_cast<const uint4 *>(P.plan + P.lay.seq);
-            const long long total = __ldg(cum + P.B) * P.Hkv;
+            int b = 0;
+            const long long total = units<PAIR>(P, -1, b);
             const long long per = share(P, total);
             const long long u0 = slot * per, u1 = u0 + per < total ? u0 + per : total;
             long long u = u0;
-            int b = 0, h = 0, tile = 0, tiles = 1;
-            uint4 q = make_uint4(0, 0, 0, 0);
+            Place q = {};
+            int h = 0, rg = 0, tile = 0;
             if (u < u1) {
-                b = find_seq(cum, P.B, P.Hkv, u);
-                const long long c0 = __ldg(cum + b);
-                tiles = (int)(__ldg(cum + b + 1) - c0);
-                q = __ldg(seqs + b);
-                h = (int)((u - c0 * P.Hkv) / tiles);
-                tile = (int)(u - c0 * P.Hkv - (long long)h * tiles);
+                const long long first = units<PAIR>(P, u, b);
+                q = place_at<PAIR>(P, b, first);
+                const long long at = u - first;
+                const int item = (int)(at / q.tiles);
+                tile = (int)(at - (long long)item * q.tiles);
+                h = item / q.groups;
+                rg = item - h * q.groups;
             }
             for (uint32_t k = 0;; ++k) {
                 const int at = (int)(k % RING);
                 if (!wait_idle(&S.pempty[at], ((k / RING) & 1u) ^ 1u))
                     break;
                 const long long left = u1 - u;
-                const int n = left <= 0 ? 0 : tiles - tile < left ? tiles - tile : (int)left;
+                const int n = left <= 0 ? 0 : q.tiles - tile < left ? q.tiles - tile : (int)left;
                 if (lane == 0) {
                     Piece p;
-                    p.b = b;
+                    p.b = q.b;
                     p.h = h;
+                    p.rt0 = rg * C::Q_TILES;
+                    p.last = rg == q.groups - 1;
                     p.tile0 = tile;
                     p.n = n;
-                    p.tiles = tiles;
-                    p.len = (int)q.x;
-                    p.nn = (int)q.y;
-                    p.status = (int)q.z;
-                    p.idle = p.nn <= rt0 * P.nodes_per_tile;
+                    p.tiles = q.tiles;
+                    p.len = (int)q.seq.x;
+                    p.nn = (int)q.seq.y;
+                    p.status = (int)q.seq.z;
+                    p.idle = p.nn <= 0;
                     p.first = u - tile <= u0;
                     S.piece[at] = p;
                     mbar_arrive(&S.pfull[at]);
@@ -1278,12 +1339,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                     break;
                 u += n;
                 tile = 0;
-                if (++h == P.Hkv) {
-                    h = 0;
-                    ++b;
-                    if (u < u1) {
-                        tiles = (int)(__ldg(cum + b + 1) - __ldg(cum + b));
-                        q = __ldg(seqs + b);
+                if (++rg == q.groups) {
+                    rg = 0;
+                    if (++h == P.Hkv) {
+                        h = 0;
+                        if (u < u1)
+                            q = place_at<PAIR>(P, q.b + 1, u);
                     }
                 }
             }
@@ -1304,7 +1365,7 @@ constexpr int JOIN_ROWS = 32;
 
 // Joins the pieces of the items that lie across a share's end.  CTA x takes
 // the item that the end of share x cuts (when no earlier end cuts it), 32 rows
-// of one row tile: a row per lane, an eighth of the columns per warp.
+// of one of its row tiles: a row per lane, an eighth of the columns per warp.
 template <int NP, int DT, bool PAIR>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_constant__ AParams P)
 {
@@ -1312,24 +1373,23 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_cons
     constexpr int COLS = C::DP / JOIN_WARPS;
     __shared__ __align__(16) uint16_t tile[JOIN_ROWS][C::DP + 8];
     const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
-    const int rt = (int)blockIdx.y;
     const int r0 = (int)blockIdx.z * JOIN_ROWS, r = r0 + lane;
     allow_next_kernel();
     wait_previous_kernel();
-    const long long *cum = reinterpret_cast<const long long *>(P.plan + P.lay.cum);
-    const long long total = __ldg(cum + P.B) * P.Hkv;
+    int b = 0;
+    const long long total = units<PAIR>(P, -1, b);
     const long long per = share(P, total);
     const long long end = ((long long)blockIdx.x + 1) * per;
     if (end >= total)
         return;
-    const int b = find_seq(cum, P.B, P.Hkv, end);
-    const long long c0 = __ldg(cum + b);
-    const int tiles = (int)(__ldg(cum + b + 1) - c0);
-    const int h = (int)((end - c0 * P.Hkv) / tiles);
-    const long long item = c0 * P.Hkv + (long long)h * tiles;  // its first unit
-    const int nn = (int)__ldg(reinterpret_cast<const uint4 *>(P.plan + P.lay.seq) + b).y;
-    if (item == end || item < end - per || nn <= rt / C::Q_TILES * C::Q_TILES * P.nodes_per_tile)
-        return;  // not cut here, or the previous end has it, or its CTAs were idle
+    const long long first = units<PAIR>(P, end, b);
+    const Place q = place_at<PAIR>(P, b, first);
+    const int index = (int)((end - first) / q.tiles);
+    const long long item = first + (long long)index * q.tiles;  // its first unit
+    const int tiles = q.tiles, nn = (int)q.seq.y;
+    const int h = index / q.groups, rt = (index - h * q.groups) * C::Q_TILES + (int)blockIdx.y;
+    if (item == end || item < end - per || nn <= 0)
+        return;  // not cut here, or the previous end has it, or no node
     const int local = r / P.G, g = r - local * P.G;
     const int node = rt * P.nodes_per_tile + local;
     const bool row = local < P.nodes_per_tile && node < P.N;
@@ -1340,7 +1400,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_cons
     // starts inside of left its second
     auto at = [&](int s) -> size_t {
         const int which = (long long)s * per >= item ? 0 : 1;
-        return (((size_t)s * P.row_tiles + rt) * 2 + which) * BM;
+        return (((size_t)s * C::Q_TILES + blockIdx.y) * 2 + which) * BM;
     };
     float top = -INFINITY;
     if (live)
@@ -1422,9 +1482,7 @@ struct WsLayout {
 
 WsLayout ws_layout(int N, int G, int D)
 {
-    // row tiles over all slots: one for each CTA, or two
-    const size_t rt = row_tiles(N, G), most = rt > 1 ? 2 * MAX_CTAS : MAX_CTAS;
-    const size_t ctas = rt + 1 > most ? rt + 1 : most;
+    const size_t ctas = row_tiles(N, G) > 1 ? 2 * MAX_CTAS : MAX_CTAS;  // (row tiles of them)
     const size_t dp = D > PANEL ? 2 * PANEL : PANEL;
     WsLayout w;
     w.ml = 0;
@@ -1496,13 +1554,12 @@ int launch(const CUtensorMap (&maps)[5], AParams &P, int sms, DevInfo &di, cudaS
         di.attr[NP - 1][DT - 1][PAIR].store(true, std::memory_order_release);
     }
     const int ctas = sms < MAX_CTAS ? sms : MAX_CTAS;
-    P.row_groups = PAIR ? (P.row_tiles + 1) / 2 : P.row_tiles;
-    P.slots = ctas / P.row_groups < 1 ? 1 : ctas / P.row_groups;
+    P.slots = ctas;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned int)(P.slots * P.row_groups));
+    cfg.gridDim = dim3((unsigned int)P.slots);
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = smem_bytes<NP, PAIR>();
     cfg.stream = st;
@@ -1515,7 +1572,7 @@ int launch(const CUtensorMap (&maps)[5], AParams &P, int sms, DevInfo &di, cudaS
     }
     if (P.slots > 1) {
         const int rows = P.nodes_per_tile * P.G < P.N * P.G ? P.nodes_per_tile * P.G : P.N * P.G;
-        cfg.gridDim = dim3((unsigned int)(P.slots - 1), (unsigned int)P.row_tiles,
+        cfg.gridDim = dim3((unsigned int)(P.slots - 1), (unsigned int)(PAIR ? 2 : 1),
                            (unsigned int)((rows + JOIN_ROWS - 1) / JOIN_ROWS));
         cfg.blockDim = dim3(JOIN_WARPS * 32);
         cfg.dynamicSmemBytes = 0;
@@ -1595,7 +1652,6 @@ int32_t spec_tree_attention(const spec_tree_attention_args *args, void *workspac
     P.D = a.D;
     P.G = G;
     P.nodes_per_tile = BM / G;
-    P.row_tiles = row_tiles(a.N, G);
     P.page_size = a.page_size;
     P.pages_per_seq = a.pages_per_seq;
     P.page_rows = paged && a.page_size < KT ? a.page_size : KT;
@@ -1640,7 +1696,7 @@ int32_t spec_tree_attention(const spec_tree_attention_args *args, void *workspac
         di.sms.store(sms, std::memory_order_relaxed);
     }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const bool wide = a.D > PANEL, pair = P.row_tiles > 1;
+    const bool wide = a.D > PANEL, pair = row_tiles(a.N, G) > 1;
     if (a.dtype == SPEC_BF16) {
         if (wide)
             return pair ? launch<2, SPEC_BF16, true>(maps, P, sms, di, st)
