@@ -193,52 +193,30 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32])
         : "r"(taddr) : "memory");
 }
 
-// 128 consecutive columns: four loads, one wait
-__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&a)[32], uint32_t (&b)[32],
-                                         uint32_t (&c)[32], uint32_t (&d)[32])
+// 32 columns in two halves: the load runs while the code between them does
+__device__ __forceinline__ void tmem_ld_start(uint32_t taddr, uint32_t (&r)[32])
 {
-    __syncwarp();
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
         "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, "
         "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31 "
-        "}, [%128];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, "
-        "%49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63 "
-        "}, [%129];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-        "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, "
-        "%81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95 "
-        "}, [%130];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-        "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, "
-        "%110, %111, %112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, "
-        "%124, %125, %126, %127 "
-        "}, [%131];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]),
-          "=r"(a[7]), "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]),
-          "=r"(a[14]), "=r"(a[15]), "=r"(a[16]), "=r"(a[17]), "=r"(a[18]), "=r"(a[19]),
-          "=r"(a[20]), "=r"(a[21]), "=r"(a[22]), "=r"(a[23]), "=r"(a[24]), "=r"(a[25]),
-          "=r"(a[26]), "=r"(a[27]), "=r"(a[28]), "=r"(a[29]), "=r"(a[30]), "=r"(a[31]),
-          "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]),
-          "=r"(b[7]), "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]),
-          "=r"(b[14]), "=r"(b[15]), "=r"(b[16]), "=r"(b[17]), "=r"(b[18]), "=r"(b[19]),
-          "=r"(b[20]), "=r"(b[21]), "=r"(b[22]), "=r"(b[23]), "=r"(b[24]), "=r"(b[25]),
-          "=r"(b[26]), "=r"(b[27]), "=r"(b[28]), "=r"(b[29]), "=r"(b[30]), "=r"(b[31]),
-          "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]), "=r"(c[4]), "=r"(c[5]), "=r"(c[6]),
-          "=r"(c[7]), "=r"(c[8]), "=r"(c[9]), "=r"(c[10]), "=r"(c[11]), "=r"(c[12]), "=r"(c[13]),
-          "=r"(c[14]), "=r"(c[15]), "=r"(c[16]), "=r"(c[17]), "=r"(c[18]), "=r"(c[19]),
-          "=r"(c[20]), "=r"(c[21]), "=r"(c[22]), "=r"(c[23]), "=r"(c[24]), "=r"(c[25]),
-          "=r"(c[26]), "=r"(c[27]), "=r"(c[28]), "=r"(c[29]), "=r"(c[30]), "=r"(c[31]),
-          "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]), "=r"(d[4]), "=r"(d[5]), "=r"(d[6]),
-          "=r"(d[7]), "=r"(d[8]), "=r"(d[9]), "=r"(d[10]), "=r"(d[11]), "=r"(d[12]), "=r"(d[13]),
-          "=r"(d[14]), "=r"(d[15]), "=r"(d[16]), "=r"(d[17]), "=r"(d[18]), "=r"(d[19]),
-          "=r"(d[20]), "=r"(d[21]), "=r"(d[22]), "=r"(d[23]), "=r"(d[24]), "=r"(d[25]),
-          "=r"(d[26]), "=r"(d[27]), "=r"(d[28]), "=r"(d[29]), "=r"(d[30]), "=r"(d[31])
-        : "r"(taddr), "r"(taddr + 32), "r"(taddr + 64), "r"(taddr + 96)
-        : "memory");
+        "}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_finish(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+        : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+          "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+          "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),
+          "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
+          "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+        :: "memory");
 }
 
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16])
@@ -363,6 +341,28 @@ __device__ __forceinline__ bool warp_try(unsigned long long *bar, uint32_t parit
     return any;
 }
 
+// The same for two barriers at once.
+__device__ __forceinline__ bool warp_try2(unsigned long long *a, uint32_t pa,
+                                          unsigned long long *b, uint32_t pb)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q, r;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "setp.ne.u32 q, %2, %2;\n\t"
+        "setp.ne.u32 r, %2, %2;\n\t"
+        "@p mbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2;\n\t"
+        "@p mbarrier.try_wait.parity.shared::cta.b64 r, [%3], %4;\n\t"
+        "and.pred q, q, r;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(a)), "r"(pa), "r"(smem_addr(b)), "r"(pb)
+        : "memory");
+    const bool any = __any_sync(0xffffffffu, ok != 0);
+    __syncwarp();
+    return any;
+}
+
 // The wait for a barrier that was not ready at once; `sleep_ns` between the tests.
 __device__ __forceinline__ bool wait_long(unsigned long long *bar, uint32_t parity,
                                           volatile int *abort_flag, int *status,
@@ -405,7 +405,7 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr)
 // Instruction descriptor, kind::f16: fp32 accumulator, A and B both bf16 (1)
 // or both fp16 (0), M = 128.
 template <int DT>
-__device__ __forceinline__ uint32_t idesc(int n, bool b_mn_major)
+__host__ __device__ constexpr uint32_t idesc(int n, bool b_mn_major)
 {
     constexpr uint32_t T = DT == SPEC_BF16 ? 1u : 0u;
     return (1u << 4) | (T << 7) | (T << 10) | ((b_mn_major ? 1u : 0u) << 16) |
@@ -569,6 +569,17 @@ __device__ __forceinline__ long long units(const AParams &P, long long u, int &b
     return before;
 }
 
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+// Whether O(i) is reported as done by itself: where a group may look at it before
+// its next scores, after tiles with new values and at the end of a piece.
+__device__ __forceinline__ bool commits_done(int i, int plain, int step, int n)
+{
+    return i >= plain || i + step >= n;
+}
+
 struct Whole {
     static constexpr bool value = false;
 };
@@ -724,7 +735,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         constexpr int STEP = PAIR ? 1 : 2;       // a group's next tile
         const int start = PAIR ? 0 : s;          // and its first
         const uint4 *masks = reinterpret_cast<const uint4 *>(P.plan + P.lay.mask);
-        uint32_t cnt = 0, tv = 0;                // the group's tiles, all tiles
+        uint32_t cnt = 0, tv = 0, done = 0;      // the group's tiles, all tiles, reports of O
         uint32_t joins = 0, notes = 0;
         const unsigned long long c2 = f2(P.c, P.c);
         // all softmax warps have come here
@@ -777,6 +788,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (live && p.tile0 <= cache_tiles && cache_tiles < p.tile0 + p.n)
                 see0 = __ldg(mask);
             float m = -INFINITY, l = 0.0f;       // maximum of the raw scores, total
+            const int plain = min(p.n, p.len / KT - p.tile0);
             // one tile of this group; `masked` tiles hold fewer than KT keys or new ones
             auto tile = [&](int i, auto kind) {
                 constexpr bool masked = decltype(kind)::value;
@@ -873,27 +885,44 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 };
                 unsigned long long sum[2] = {0ull, 0ull};
-                if (warp_live && !masked) {
-                    uint32_t x[4][32];
-                    tmem_ld4(t_s, x[0], x[1], x[2], x[3]);
-                    raise(fmaxf(fmaxf(max32(x[0]), max32(x[1])),
-                                fmaxf(max32(x[2]), max32(x[3]))));
+                // In a pair, whose products bound it, a tile's weights are made in one pass; the
+                // other kernel is bound by its loads, where the small loop below did better
+                // (2 % on 64 trees of 29 nodes)
+                bool redo = !PAIR || masked || i == start;
+                if (PAIR && warp_live && !redo) {
+                    // in one pass: weights by the maximum so far, which serves as long as no
+                    // score is far above it; the tile's own maximum is found on the way
                     const float shift = m == -INFINITY ? 0.0f : -m * P.c;
                     const unsigned long long shift2 = f2(shift, shift);
-                    // the scores are read again, chunk by chunk: a loop that four warps and two
-                    // issuers share an instruction cache with beats a second saved read
-#pragma unroll 1
-                    for (int h = 0; h < 4; ++h) {
-                        uint32_t y[32], pk[16];
-                        tmem_ld(t_s + h * 32, y);
-                        weigh<DT>(y, c2, shift2, sum, pk);
-                        // weights 32 h on lie in columns 16 h on: over scores that were read
-                        tmem_st(t_s + h * 16, pk);
+                    uint32_t x[32], y[32], pk[4][16];
+                    __syncwarp();
+                    tmem_ld_start(t_s, x);
+                    tmem_ld_finish(x);
+                    tmem_ld_start(t_s + 32, y);
+                    float top = max32(x);
+                    weigh<DT>(x, c2, shift2, sum, pk[0]);
+                    tmem_ld_finish(y);
+                    tmem_ld_start(t_s + 64, x);
+                    top = fmaxf(top, max32(y));
+                    weigh<DT>(y, c2, shift2, sum, pk[1]);
+                    tmem_ld_finish(x);
+                    tmem_ld_start(t_s + 96, y);
+                    top = fmaxf(top, max32(x));
+                    weigh<DT>(x, c2, shift2, sum, pk[2]);
+                    tmem_ld_finish(y);
+                    top = fmaxf(top, max32(y));
+                    weigh<DT>(y, c2, shift2, sum, pk[3]);
+                    redo = __any_sync(0xffffffffu, (top - m) * P.c > GROWTH);  // -inf to finite too
+                    if (!redo) {
+#pragma unroll
+                        for (int h = 0; h < 4; ++h)
+                            tmem_st(t_s + h * 16, pk[h]);
+                    } else {
+                        sum[0] = sum[1] = 0ull;
                     }
                 }
-                if (warp_live && masked) {
-                    // 32 keys at a time, and no more of them than the tile has: the scores are
-                    // read again for the weights
+                if (warp_live && redo) {
+                    // the maximum first: 32 keys at a time, and no more of them than the tile has
                     const int chunks = (keys + 31) / 32;
                     auto bits = [&](int h) -> uint32_t {
                         const uint32_t w = h == 0 ? see.x : h == 1 ? see.y : h == 2 ? see.z : see.w;
@@ -904,7 +933,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int h = 0; h < chunks; ++h) {
                         uint32_t x[32];
                         tmem_ld(t_s + h * 32, x);
-                        hide(x, bits(h));
+                        if (masked)
+                            hide(x, bits(h));
                         top = fmaxf(top, max32(x));
                     }
                     raise(top);
@@ -914,8 +944,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int h = 0; h < chunks; ++h) {
                         uint32_t x[32], pk[16];
                         tmem_ld(t_s + h * 32, x);
-                        hide(x, bits(h));
+                        if (masked)
+                            hide(x, bits(h));
                         weigh<DT>(x, c2, shift2, sum, pk);
+                        // weights 32 h on lie in columns 16 h on: over scores that were read
                         tmem_st(t_s + h * 16, pk);
                         if (any_bad) {
                             uint32_t z = 0;
@@ -942,7 +974,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     mbar_arrive(&S.pready[s]);
                 if (any_bad) {
                     // what the zeroed elements give the rows that see them, once O(i) is done
-                    ok = wait(&S.pvdone[s], cnt & 1u);
+                    ok = wait(&S.pvdone[s], done & 1u);
                     if (!ok)
                         return;
                     tc_fence_after();
@@ -982,10 +1014,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                     // the notes are written over only after every warp has read them
                     ok = tile_sync();
                 }
+                if (commits_done(i, plain, STEP, p.n))
+                    ++done;
                 ++cnt;
             };
             // whole tiles of the cache first, in a loop of their own: it stays small
-            const int plain = min(p.n, p.len / KT - p.tile0);
             int i = start;
             for (; i < plain && ok; i += STEP)
                 tile(i, Whole());
@@ -999,7 +1032,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // each group writes one panel of the joined halves, or with a row tile of its own
             // all of it
             const bool mine = p.n > start;       // this group had a tile
-            if (mine && !wait(&S.pvdone[s], (cnt - 1) & 1u))
+            if (mine && !wait(&S.pvdone[s], (done - 1) & 1u))
                 break;
             tc_fence_after();
             float top = mine && m != -INFINITY ? m * P.c : -INFINITY;
@@ -1169,102 +1202,229 @@ __global__ void __launch_bounds__(THREADS, 1)
             // The whole warp runs the loop and one elected lane issues: what the products
             // are given then stays in uniform registers (issued from under `lane == 0` each
             // product took about 120 clocks to issue, twice its time in the tensor pipe).
-            // Job j of a piece: tile j of group j & 1, or of a pair tile j / 2 of group j & 1
-            uint32_t items = 0, t0 = 0, cnt[2] = {0, 0};
+            uint32_t items = 0;
             bool ok = true, issued = false;
             const int ksteps = (P.D + 15) / 16;
             const uint32_t id_o = idesc<DT>(ksteps * 16, true);
             Piece p = {};
-            int jobs = 0;
-            auto tile_of = [](int j) -> int { return PAIR ? j >> 1 : j; };
-            auto scores = [&](int j) {  // S(j) = Q K^T
-                bool cached;
-                const int keys = tile_keys(p, p.tile0 + tile_of(j), cached);
-                const int s = j & 1;
-                const uint32_t t = t0 + (uint32_t)tile_of(j);
-                const int st = (int)(t % C::KST);
-                ok = wait(&S.kfull[st], (t / C::KST) & 1u);
-                if (!ok)
-                    return;
-                tc_fence_after();
-                const uint32_t id = idesc<DT>((keys + 15) & ~15, false);
-                const uint32_t d = tmem + (uint32_t)(s * KT);
-                const uint64_t qd = desc_k(q_s + (PAIR ? s * C::TILE : 0));
-                const uint64_t kd = desc_k(k_s + st * C::TILE);
-                if (elect_one()) {
-                    if (ksteps == NP * 4) {
-#pragma unroll
-                        for (int x = 0; x < NP * 4; ++x) {
-                            const uint64_t off =
-                                (uint64_t)(((x >> 2) * PANEL_BYTES + (x & 3) * 32) >> 4);
-                            mma_ss(d, qd + off, kd + off, id, x ? 1u : 0u);
-                        }
-                    } else {
+            if constexpr (PAIR) {
+                // A step of group G: O(i) += P V(i), then S = Q K(i + 1)^T.  Its own waits, commits
+                // and addresses are what this warp's time goes into (1200 clocks of a step's 2000
+                // when each was done by itself), so in the usual case one test covers both tiles
+                // and one elected block issues all of it.
+                int kst = 0, vst = 0;                // stages and phases of the next K and V tile
+                uint32_t kph = 0, vph = 0, pph[2] = {0, 0};
+                constexpr uint32_t id_s = idesc<DT>(KT, false);
+                const uint64_t qd0 = desc_k(q_s), kd0 = desc_k(k_s), vd0 = desc_mn(v_s);
+                constexpr uint64_t TILE16 = C::TILE >> 4;
+                int plain = 0;                       // whole tiles of the cache come first
+                auto next_k = [&]() {
+                    kph ^= kst + 1 == C::KST ? 1u : 0u;
+                    kst = kst + 1 == C::KST ? 0 : kst + 1;
+                };
+                auto next_v = [&]() {
+                    vph ^= vst + 1 == C::VST ? 1u : 0u;
+                    vst = vst + 1 == C::VST ? 0 : vst + 1;
+                };
+                // commits behind the scores of tile i
+                auto scored = [&](int s, int i) {
+                    if (s)
+                        mma_commit(&S.kempty[kst]);
+                    mma_commit(&S.sfull[s]);
+                    if (i == p.n - 1 && s)
+                        mma_commit(&S.qempty);
+                };
+                auto scores = [&](int s, int i) {    // S = Q K(i)^T by itself
+                    bool cached;
+                    const int keys = tile_keys(p, p.tile0 + i, cached);
+                    ok = wait(&S.kfull[kst], kph);
+                    if (!ok)
+                        return;
+                    tc_fence_after();
+                    const uint32_t id = idesc<DT>((keys + 15) & ~15, false);
+                    const uint32_t d = tmem + (uint32_t)(s * KT);
+                    const uint64_t qd = qd0 + s * TILE16, kd = kd0 + kst * TILE16;
+                    if (elect_one()) {
+#pragma unroll 1
                         for (int x = 0; x < ksteps; ++x) {
                             const uint64_t off =
                                 (uint64_t)(((x >> 2) * PANEL_BYTES + (x & 3) * 32) >> 4);
                             mma_ss(d, qd + off, kd + off, id, x ? 1u : 0u);
                         }
-                    }
-                    if (!PAIR || s)
-                        mma_commit(&S.kempty[st]);
-                    mma_commit(&S.sfull[s]);
-                    if (j == jobs - 1)
-                        mma_commit(&S.qempty);
-                }
-                __syncwarp();
-                issued = true;
-            };
-            while (ok && next(p)) {
-                if (p.idle)
-                    continue;
-                jobs = PAIR ? 2 * p.n : p.n;
-                ok = wait(&S.qfull, items & 1u);
-                ++items;
-                for (int j = 0; j < 2 && j < jobs && ok; ++j)
-                    scores(j);
-                for (int j = 0; j < jobs && ok; ++j) {
-                    bool cached;
-                    const int keys = tile_keys(p, p.tile0 + tile_of(j), cached);
-                    const int s = j & 1;
-                    const uint32_t n = s ? cnt[1] : cnt[0];
-                    const uint32_t t = t0 + (uint32_t)tile_of(j);
-                    const int st = (int)(t % C::VST);
-                    ok = wait(&S.vfull[st], (t / C::VST) & 1u) && wait(&S.pready[s], n & 1u);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    const uint32_t d = tmem + (uint32_t)(2 * KT + s * C::DP);
-                    const uint32_t a = tmem + (uint32_t)(s * KT);
-                    const uint64_t vd = desc_mn(v_s + st * C::TILE);
-                    // 16 keys a step: 8 columns of P, 2 KB of V
-                    const int steps = (keys + 15) / 16;
-                    const uint32_t more = j >= 2 ? 1u : 0u;
-                    if (elect_one()) {
-                        if (steps == KT / 16) {
-#pragma unroll
-                            for (int x = 0; x < KT / 16; ++x)
-                                mma_ts(d, a + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)),
-                                       id_o, x ? 1u : more);
-                        } else {
-                            for (int x = 0; x < steps; ++x)
-                                mma_ts(d, a + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)),
-                                       id_o, x ? 1u : more);
-                        }
-                        if (!PAIR || s)
-                            mma_commit(&S.vempty[st]);
-                        mma_commit(&S.pvdone[s]);
+                        scored(s, i);
                     }
                     __syncwarp();
                     issued = true;
                     if (s)
-                        ++cnt[1];
-                    else
-                        ++cnt[0];
-                    if (j + 2 < jobs)
-                        scores(j + 2);
+                        next_k();
+                };
+                auto step = [&](auto group, int i) {
+                    constexpr int G = decltype(group)::value;
+                    const uint32_t t_s = tmem + (uint32_t)(G * KT);
+                    const uint32_t t_o = tmem + (uint32_t)(2 * KT + G * C::DP);
+                    const uint64_t vd = vd0 + vst * TILE16;
+                    const uint32_t more = i >= 1 ? 1u : 0u;
+                    const bool usual = i + 1 < plain && ksteps == NP * 4;
+                    // (the second group of a pair finds the first one's tiles)
+                    ok = wait(&S.pready[G], pph[G]);
+                    if (!ok)
+                        return;
+                    const bool all = usual && (G ||
+                                               warp_try2(&S.vfull[vst], vph, &S.kfull[kst], kph));
+                    if (all) {
+                        tc_fence_after();
+                        const uint64_t qd = qd0 + G * TILE16, kd = kd0 + kst * TILE16;
+                        if (elect_one()) {
+                            // 16 keys a step: 8 columns of P, 2 KB of V
+#pragma unroll
+                            for (int x = 0; x < KT / 16; ++x)
+                                mma_ts(t_o, t_s + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)),
+                                       id_o, x ? 1u : more);
+                            if (G)
+                                mma_commit(&S.vempty[vst]);
+#pragma unroll
+                            for (int x = 0; x < NP * 4; ++x) {
+                                const uint64_t off =
+                                    (uint64_t)(((x >> 2) * PANEL_BYTES + (x & 3) * 32) >> 4);
+                                mma_ss(t_s, qd + off, kd + off, id_s, x ? 1u : 0u);
+                            }
+                            scored(G, i + 1);
+                        }
+                        __syncwarp();
+                        if (G)
+                            next_k();
+                    } else {
+                        bool cached;
+                        const int keys = tile_keys(p, p.tile0 + i, cached);
+                        ok = wait(&S.vfull[vst], vph);
+                        if (!ok)
+                            return;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const int steps = (keys + 15) / 16;
+#pragma unroll 1
+                            for (int x = 0; x < steps; ++x)
+                                mma_ts(t_o, t_s + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)),
+                                       id_o, x ? 1u : more);
+                            if (G)
+                                mma_commit(&S.vempty[vst]);
+                            if (commits_done(i, plain, 1, p.n))
+                                mma_commit(&S.pvdone[G]);
+                        }
+                        __syncwarp();
+                        if (i + 1 < p.n)
+                            scores(G, i + 1);
+                    }
+                    pph[G] ^= 1u;
+                    if (G)
+                        next_v();
+                };
+                while (ok && next(p)) {
+                    if (p.idle)
+                        continue;
+                    plain = min(p.n, p.len / KT - p.tile0);
+                    ok = wait(&S.qfull, items & 1u);
+                    ++items;
+                    if (ok)
+                        scores(0, 0);
+                    if (ok)
+                        scores(1, 0);
+                    for (int i = 0; i < p.n && ok; ++i) {
+                        step(Int<0>(), i);
+                        if (ok)
+                            step(Int<1>(), i);
+                    }
                 }
-                t0 += (uint32_t)p.n;
+            } else {
+                uint32_t t0 = 0, cnt[2] = {0, 0};
+                auto scores = [&](int j) {  // S = Q K(j)^T of group j & 1
+                    bool cached;
+                    const int keys = tile_keys(p, p.tile0 + j, cached);
+                    const int s = j & 1;
+                    const uint32_t t = t0 + (uint32_t)j;
+                    const int st = (int)(t % C::KST);
+                    ok = wait(&S.kfull[st], (t / C::KST) & 1u);
+                    if (!ok)
+                        return;
+                    tc_fence_after();
+                    const uint32_t id = idesc<DT>((keys + 15) & ~15, false);
+                    const uint32_t d = tmem + (uint32_t)(s * KT);
+                    const uint64_t qd = desc_k(q_s);
+                    const uint64_t kd = desc_k(k_s + st * C::TILE);
+                    if (elect_one()) {
+                        if (ksteps == NP * 4) {
+#pragma unroll
+                            for (int x = 0; x < NP * 4; ++x) {
+                                const uint64_t off =
+                                    (uint64_t)(((x >> 2) * PANEL_BYTES + (x & 3) * 32) >> 4);
+                                mma_ss(d, qd + off, kd + off, id, x ? 1u : 0u);
+                            }
+                        } else {
+                            for (int x = 0; x < ksteps; ++x) {
+                                const uint64_t off =
+                                    (uint64_t)(((x >> 2) * PANEL_BYTES + (x & 3) * 32) >> 4);
+                                mma_ss(d, qd + off, kd + off, id, x ? 1u : 0u);
+                            }
+                        }
+                        mma_commit(&S.kempty[st]);
+                        mma_commit(&S.sfull[s]);
+                        if (j == p.n - 1)
+                            mma_commit(&S.qempty);
+                    }
+                    __syncwarp();
+                    issued = true;
+                };
+                while (ok && next(p)) {
+                    if (p.idle)
+                        continue;
+                    const int plain = min(p.n, p.len / KT - p.tile0);
+                    ok = wait(&S.qfull, items & 1u);
+                    ++items;
+                    for (int j = 0; j < 2 && j < p.n && ok; ++j)
+                        scores(j);
+                    for (int j = 0; j < p.n && ok; ++j) {
+                        bool cached;
+                        const int keys = tile_keys(p, p.tile0 + j, cached);
+                        const int s = j & 1;
+                        const uint32_t n = s ? cnt[1] : cnt[0];
+                        const uint32_t t = t0 + (uint32_t)j;
+                        const int st = (int)(t % C::VST);
+                        ok = wait(&S.vfull[st], (t / C::VST) & 1u) && wait(&S.pready[s], n & 1u);
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        const uint32_t d = tmem + (uint32_t)(2 * KT + s * C::DP);
+                        const uint32_t a = tmem + (uint32_t)(s * KT);
+                        const uint64_t vd = desc_mn(v_s + st * C::TILE);
+                        // 16 keys a step: 8 columns of P, 2 KB of V
+                        const int steps = (keys + 15) / 16;
+                        const uint32_t more = j >= 2 ? 1u : 0u;
+                        if (elect_one()) {
+                            if (steps == KT / 16) {
+#pragma unroll
+                                for (int x = 0; x < KT / 16; ++x)
+                                    mma_ts(d, a + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)),
+                                           id_o, x ? 1u : more);
+                            } else {
+                                for (int x = 0; x < steps; ++x)
+                                    mma_ts(d, a + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)),
+                                           id_o, x ? 1u : more);
+                            }
+                            mma_commit(&S.vempty[st]);
+                            if (commits_done(j, plain, 2, p.n))
+                                mma_commit(&S.pvdone[s]);
+                        }
+                        __syncwarp();
+                        issued = true;
+                        if (s)
+                            ++cnt[1];
+                        else
+                            ++cnt[0];
+                        if (j + 2 < p.n)
+                            scores(j + 2);
+                    }
+                    t0 += (uint32_t)p.n;
+                }
             }
             if (*abort_flag && issued) {  // the products in flight complete (bounded)
                 if (elect_one())
