@@ -523,50 +523,76 @@ __device__ __forceinline__ Place place_at(const AParams &P, int b, long long fir
     return q;
 }
 
-// All units (u < 0), or the first unit of the sequence that holds unit u < all, which goes to b.  One row
-// group each: the plan's prefix sums.  Otherwise a warp adds them up, 32 sequences a step.
-template <bool PAIR>
-__device__ __forceinline__ long long units(const AParams &P, long long u, int &b)
+// A warp looks up one unit: `pick` makes it of the number of all units, and where that lies goes to
+// q (not if it is past the end).  Up to 32 sequences take one round of loads, their units
+// summed over the lanes; more of them a search of the plan's prefix sums with 32 probes a
+// round, or, where row groups make those sums useless, two passes over the sequences.
+template <bool PAIR, typename F>
+__device__ __forceinline__ long long look_up(const AParams &P, F pick, long long &total, Place &q)
 {
     const long long *cum = reinterpret_cast<const long long *>(P.plan + P.lay.cum);
-    if (!PAIR) {
-        if (u < 0)
-            return __ldg(cum + P.B) * P.Hkv;
-        int lo = 0, hi = P.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (__ldg(cum + mid) * P.Hkv <= u)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        b = lo;
-        return __ldg(cum + lo) * P.Hkv;
-    }
     const int lane = (int)threadIdx.x & 31;
-    long long before = 0;
-    for (int b0 = 0; b0 < P.B; b0 += 32) {
-        long long v = 0;
-        if (b0 + lane < P.B) {
-            const Place q = place_at<PAIR>(P, b0 + lane, 0);
-            v = (long long)q.tiles * q.groups * P.Hkv;
+    if (!PAIR && P.B > 32) {
+        total = __ldg(cum + P.B) * P.Hkv;
+        const long long u = pick(total);
+        if (u >= total)
+            return u;
+        int lo = 0, len = P.B;
+        while (len > 1) {
+            const int step = (len + 31) / 32, at = lane * step;
+            const bool below = at < len && __ldg(cum + lo + at) * P.Hkv <= u;
+            const int last = 31 - __clz((int)__ballot_sync(0xffffffffu, below));
+            lo += last * step;
+            len = len - last * step < step ? len - last * step : step;
         }
-        long long sum = v;
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long o = __shfl_up_sync(0xffffffffu, sum, d);
-            if (lane >= d)
-                sum += o;
-        }
-        const long long all = __shfl_sync(0xffffffffu, sum, 31);
-        if (u >= 0 && u < before + all) {
-            const uint32_t past = __ballot_sync(0xffffffffu, before + sum > u);
-            const int at = __ffs((int)past) - 1;
-            b = b0 + at;
-            return before + __shfl_sync(0xffffffffu, sum - v, at);
-        }
-        before += all;
+        q = place_at<PAIR>(P, lo, __ldg(cum + lo) * P.Hkv);
+        return u;
     }
-    return before;
+    long long u = -1;
+    for (int pass = 0; pass < 2; ++pass) {
+        long long before = 0;
+        for (int b0 = 0; b0 < P.B; b0 += 32) {
+            long long v = 0;
+            Place mine = {};
+            if (b0 + lane < P.B) {
+                mine = place_at<PAIR>(P, b0 + lane, 0);
+                v = (long long)mine.tiles * mine.groups * P.Hkv;
+            }
+            long long sum = v;
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long o = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d)
+                    sum += o;
+            }
+            const long long all = __shfl_sync(0xffffffffu, sum, 31);
+            if (P.B <= 32) {
+                total = all;
+                u = pick(total);
+            }
+            if (u >= before && u < before + all) {
+                const uint32_t past = __ballot_sync(0xffffffffu, before + sum > u);
+                const int at = __ffs((int)past) - 1;
+                q.b = b0 + at;
+                q.first = before + __shfl_sync(0xffffffffu, sum - v, at);
+                q.tiles = __shfl_sync(0xffffffffu, mine.tiles, at);
+                q.groups = __shfl_sync(0xffffffffu, mine.groups, at);
+                q.seq.x = __shfl_sync(0xffffffffu, mine.seq.x, at);
+                q.seq.y = __shfl_sync(0xffffffffu, mine.seq.y, at);
+                q.seq.z = __shfl_sync(0xffffffffu, mine.seq.z, at);
+                return u;
+            }
+            before += all;
+        }
+        if (P.B <= 32)
+            return u;
+        if (pass == 0) {
+            total = before;
+            u = pick(total);
+            if (u >= total)
+                return u;
+        }
+    }
+    return u;
 }
 
 template <int N>
@@ -696,8 +722,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = S.tmem_base;
-    allow_next_kernel();
     wait_previous_kernel();
+    allow_next_kernel();
 
     // a warp's wait: false on every lane once the CTA has given up
     auto wait = [&](unsigned long long *bar, uint32_t parity) -> bool {
@@ -1455,17 +1481,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                 (void)mbar_wait(&S.qfull, (items - 1) & 1u);
         } else {
             // ------------------------------------------- the share's pieces
-            int b = 0;
-            const long long total = units<PAIR>(P, -1, b);
-            const long long per = share(P, total);
-            const long long u0 = slot * per, u1 = u0 + per < total ? u0 + per : total;
-            long long u = u0;
+            long long total = 0;
             Place q = {};
+            const long long u0 = look_up<PAIR>(
+                P, [&](long long all) { return slot * share(P, all); }, total, q);
+            const long long per = share(P, total);
+            const long long u1 = u0 + per < total ? u0 + per : total;
+            long long u = u0;
             int h = 0, rg = 0, tile = 0;
             if (u < u1) {
-                const long long first = units<PAIR>(P, u, b);
-                q = place_at<PAIR>(P, b, first);
-                const long long at = u - first;
+                const long long at = u - q.first;
                 const int item = (int)(at / q.tiles);
                 tile = (int)(at - (long long)item * q.tiles);
                 h = item / q.groups;
@@ -1534,16 +1559,18 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_cons
     __shared__ __align__(16) uint16_t tile[JOIN_ROWS][C::DP + 8];
     const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
     const int r0 = (int)blockIdx.z * JOIN_ROWS, r = r0 + lane;
+    // the plan is complete: every CTA of the attention had waited for it before this grid began
+    long long total = 0;
+    Place q = {};
+    const long long end = look_up<PAIR>(
+        P, [&](long long all) { return ((long long)blockIdx.x + 1) * share(P, all); }, total, q);
     allow_next_kernel();
     wait_previous_kernel();
-    int b = 0;
-    const long long total = units<PAIR>(P, -1, b);
     const long long per = share(P, total);
-    const long long end = ((long long)blockIdx.x + 1) * per;
     if (end >= total)
         return;
-    const long long first = units<PAIR>(P, end, b);
-    const Place q = place_at<PAIR>(P, b, first);
+    const int b = q.b;
+    const long long first = q.first;
     const int index = (int)((end - first) / q.tiles);
     const long long item = first + (long long)index * q.tiles;  // its first unit
     const int tiles = q.tiles, nn = (int)q.seq.y;
