@@ -152,6 +152,7 @@ struct AParams {
     int B, N, Hq, Hkv, D, G;
     int nodes_per_tile;
     int slots;       // CTAs
+    int join_rows;   // rows of a join CTA: 32, or the least power of two that holds them
     int page_size, pages_per_seq;
     int page_rows;   // rows of a cache box: min(128, page_size) (contiguous: 128)
     int new_rows;    // rows of a box of new tokens
@@ -1547,18 +1548,38 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 constexpr int JOIN_WARPS = 8;
 constexpr int JOIN_ROWS = 32;
+constexpr int JOIN_UNROLL = 2;    // pieces whose sums a thread has in flight
+
+// The running (maximum in log2 units, total, sums) of some pieces of one row.
+template <int COLS>
+struct Joined {
+    float top = -INFINITY, sum = 0.0f;
+    bool some = false;            // whether any piece saw a key
+    float o[COLS];
+    // scale of these sums under a new maximum `base` (finite)
+    __device__ __forceinline__ float factor(float base) const
+    {
+        return some ? ex2(top - base) : 0.0f;
+    }
+};
 
 // Joins the pieces of the items that lie across a share's end.  CTA x takes
 // the item that the end of share x cuts (when no earlier end cuts it), 32 rows
 // of one of its row tiles: a row per lane, an eighth of the columns per warp.
+// Where there are fewer rows, the lanes left over take pieces of their own (a
+// single token's item over 4096 positions has 17 of them, and one after the
+// other they took most of the call's time).
 template <int NP, int DT, bool PAIR>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_constant__ AParams P)
+__global__ void __launch_bounds__(JOIN_WARPS * 32, 4)
+    join_kernel(const __grid_constant__ AParams P)
 {
     using C = Cfg<NP, PAIR>;
     constexpr int COLS = C::DP / JOIN_WARPS;
     __shared__ __align__(16) uint16_t tile[JOIN_ROWS][C::DP + 8];
     const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
-    const int r0 = (int)blockIdx.z * JOIN_ROWS, r = r0 + lane;
+    const int mine = lane & (P.join_rows - 1), part = lane / P.join_rows;
+    const int parts = 32 / P.join_rows;
+    const int r = (int)blockIdx.z * JOIN_ROWS + mine;
     // the plan is complete: every CTA of the attention had waited for it before this grid began
     long long total = 0;
     Place q = {};
@@ -1569,11 +1590,9 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_cons
     const long long per = share(P, total);
     if (end >= total)
         return;
-    const int b = q.b;
-    const long long first = q.first;
-    const int index = (int)((end - first) / q.tiles);
-    const long long item = first + (long long)index * q.tiles;  // its first unit
-    const int tiles = q.tiles, nn = (int)q.seq.y;
+    const int index = (int)((end - q.first) / q.tiles);
+    const long long item = q.first + (long long)index * q.tiles;  // its first unit
+    const int nn = (int)q.seq.y;
     const int h = index / q.groups, rt = (index - h * q.groups) * C::Q_TILES + (int)blockIdx.y;
     if (item == end || item < end - per || nn <= 0)
         return;  // not cut here, or the previous end has it, or no node
@@ -1581,48 +1600,81 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) join_kernel(const __grid_cons
     const int node = rt * P.nodes_per_tile + local;
     const bool row = local < P.nodes_per_tile && node < P.N;
     const bool live = row && node < nn;
-    const int64_t orow = ((int64_t)b * P.N + node) * P.Hq + (int64_t)h * P.G + g;
-    const int s0 = (int)blockIdx.x, s1 = (int)((item + tiles - 1) / per);
+    const int64_t orow = ((int64_t)q.b * P.N + node) * P.Hq + (int64_t)h * P.G + g;
+    const int s0 = (int)blockIdx.x, n = (int)((item + q.tiles - 1) / per) - s0 + 1;
     // a share that starts with the item, or inside it, left its first piece; one that the item
     // starts inside of left its second
-    auto at = [&](int s) -> size_t {
-        const int which = (long long)s * per >= item ? 0 : 1;
-        return (((size_t)s * C::Q_TILES + blockIdx.y) * 2 + which) * BM;
+    auto at = [&](int k) -> size_t {
+        const int which = (long long)(s0 + k) * per >= item ? 0 : 1;
+        return (((size_t)(s0 + k) * C::Q_TILES + blockIdx.y) * 2 + which) * BM;
     };
-    float top = -INFINITY;
-    if (live)
-        for (int s = s0; s <= s1; ++s)
-            top = fmaxf(top, __ldcg(&P.part_ml[at(s) + r].x));
-    const float base = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f, o[COLS];
+    Joined<COLS> A;
 #pragma unroll
     for (int j = 0; j < COLS; ++j)
-        o[j] = 0.0f;
+        A.o[j] = 0.0f;
     if (live)
-        for (int s = s0; s <= s1; ++s) {
-            const float2 ml = __ldcg(&P.part_ml[at(s) + r]);
-            const float *v = P.part + at(s) * C::DP + (size_t)(warp * COLS) * BM + r;
-            float x[COLS];
+        for (int k0 = part; k0 < n; k0 += JOIN_UNROLL * parts) {
+            float2 ml[JOIN_UNROLL];
+            float x[JOIN_UNROLL][COLS];
+#pragma unroll
+            for (int u = 0; u < JOIN_UNROLL; ++u) {
+                const int k = k0 + u * parts;
+                ml[u] = make_float2(-INFINITY, 0.0f);
+                if (k < n) {
+                    ml[u] = __ldcg(&P.part_ml[at(k) + r]);
+                    const float *v = P.part + at(k) * C::DP + (size_t)(warp * COLS) * BM + r;
+#pragma unroll
+                    for (int j = 0; j < COLS; ++j)
+                        x[u][j] = warp * COLS + j < P.D ? __ldcg(v + j * BM) : 0.0f;
+                }
+            }
+            float top = A.top;
+#pragma unroll
+            for (int u = 0; u < JOIN_UNROLL; ++u)
+                top = fmaxf(top, ml[u].x);
+            const float base = top == -INFINITY ? 0.0f : top;
+            const float f = A.factor(base);
+            A.sum *= f;
 #pragma unroll
             for (int j = 0; j < COLS; ++j)
-                x[j] = warp * COLS + j < P.D ? __ldcg(v + j * BM) : 0.0f;
-            if (ml.x == -INFINITY && ml.y == 0.0f)
-                continue;  // no key seen there
-            const float w = ex2(ml.x - base);
-            sum = fmaf(ml.y, w, sum);
+                A.o[j] *= f;
 #pragma unroll
-            for (int j = 0; j < COLS; ++j)
-                o[j] = fmaf(x[j], w, o[j]);
+            for (int u = 0; u < JOIN_UNROLL; ++u) {
+                if (ml[u].x == -INFINITY && ml[u].y == 0.0f)
+                    continue;  // no key seen there
+                const float w = ex2(ml[u].x - base);
+                A.sum = fmaf(ml[u].y, w, A.sum);
+#pragma unroll
+                for (int j = 0; j < COLS; ++j)
+                    A.o[j] = fmaf(x[u][j], w, A.o[j]);
+                A.some = true;
+            }
+            A.top = top;
         }
-    const float norm = sum != 0.0f ? 1.0f / sum : 0.0f;
+    for (int d = P.join_rows; d < 32; d <<= 1) {
+        const float top2 = __shfl_xor_sync(0xffffffffu, A.top, d);
+        const float sum2 = __shfl_xor_sync(0xffffffffu, A.sum, d);
+        const bool some2 = __shfl_xor_sync(0xffffffffu, A.some ? 1 : 0, d) != 0;
+        const float top = fmaxf(A.top, top2), base = top == -INFINITY ? 0.0f : top;
+        const float f = A.factor(base), f2 = some2 ? ex2(top2 - base) : 0.0f;
+        A.sum = A.sum * f + sum2 * f2;
 #pragma unroll
-    for (int j = 0; j < COLS; j += 2)
-        *reinterpret_cast<uint32_t *>(&tile[lane][warp * COLS + j]) =
-            sum != 0.0f ? pack<DT>(o[j] * norm, o[j + 1] * norm) : 0u;
-    if (warp == 0 && row && P.lse)
-        P.lse[orow] = live ? lse_of(base, sum) : -INFINITY;
+        for (int j = 0; j < COLS; ++j)
+            A.o[j] = A.o[j] * f + __shfl_xor_sync(0xffffffffu, A.o[j], d) * f2;
+        A.top = top;
+        A.some |= some2;
+    }
+    const float norm = A.sum != 0.0f ? 1.0f / A.sum : 0.0f;
+    if (part == 0) {
+#pragma unroll
+        for (int j = 0; j < COLS; j += 2)
+            *reinterpret_cast<uint32_t *>(&tile[mine][warp * COLS + j]) =
+                A.sum != 0.0f ? pack<DT>(A.o[j] * norm, A.o[j + 1] * norm) : 0u;
+        if (warp == 0 && row && P.lse)
+            P.lse[orow] = live ? lse_of(A.top == -INFINITY ? 0.0f : A.top, A.sum) : -INFINITY;
+    }
     __syncthreads();
-    const uint32_t rows = __ballot_sync(0xffffffffu, row);
+    const uint32_t rows = __ballot_sync(0xffffffffu, row && part == 0);
 #pragma unroll
     for (int k = 0; k < JOIN_ROWS / JOIN_WARPS; ++k) {
         const int y = warp * (JOIN_ROWS / JOIN_WARPS) + k;
@@ -1759,6 +1811,9 @@ int launch(const CUtensorMap (&maps)[5], AParams &P, int sms, DevInfo &di, cudaS
     }
     if (P.slots > 1) {
         const int rows = P.nodes_per_tile * P.G < P.N * P.G ? P.nodes_per_tile * P.G : P.N * P.G;
+        P.join_rows = JOIN_ROWS;
+        while (P.join_rows / 2 >= rows)
+            P.join_rows /= 2;
         cfg.gridDim = dim3((unsigned int)(P.slots - 1), (unsigned int)(PAIR ? 2 : 1),
                            (unsigned int)((rows + JOIN_ROWS - 1) / JOIN_ROWS));
         cfg.blockDim = dim3(JOIN_WARPS * 32);
