@@ -963,22 +963,39 @@ def tree_to_device(tc, device="cuda"):
 
 # ------------------------------------------- tree attention and cache commit
 
+def _raw(torch):
+    """(current stream handle of a device index, current device index) getters: the
+    ones that PyTorch's own generated code calls, several times cheaper than
+    torch.cuda.current_stream and torch.cuda.current_device."""
+    c = torch._C
+    return (getattr(c, "_cuda_getCurrentRawStream", None)
+            or (lambda i: torch.cuda.current_stream(i).cuda_stream),
+            getattr(c, "_cuda_getDevice", None) or torch.cuda.current_device)
+
+
+_raw_getters = None
+
+
 def _call_stream(stream, dev, tensors):
-    """(stream, whether it is the current one) of a call.  Where it is not, the
-    tensors' memory is kept from reuse until the stream has passed the call."""
-    current = _torch().cuda.current_stream(dev)
-    if stream is None or stream.cuda_stream == current.cuda_stream:
-        return current, True
+    """(stream handle, the stream to allocate on or None for the current one) of
+    a call.  Where the call's stream is not the current one, the tensors'
+    memory is kept from reuse until the stream has passed the call."""
+    global _raw_getters
+    if _raw_getters is None:
+        _raw_getters = _raw(_torch())
+    current = _raw_getters[0](dev.index)
+    if stream is None or stream.cuda_stream == current:
+        return current, None
     for t in tensors:
         if t is not None:
             t.record_stream(stream)
-    return stream, False
+    return stream.cuda_stream, stream
 
 
-def _empty_on(s, is_current, shape, dtype, dev):
-    """An output allocated for use on stream `s`."""
+def _empty_on(s, shape, dtype, dev):
+    """An output allocated for use on stream `s` (None: the current one)."""
     torch = _torch()
-    if is_current:
+    if s is None:
         return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(s):
         return torch.empty(shape, dtype=dtype, device=dev)
@@ -986,7 +1003,7 @@ def _empty_on(s, is_current, shape, dtype, dev):
 
 def _launch(dev, what, fn, *args):
     """fn(*args) with `dev` current."""
-    if _torch().cuda.current_device() == dev.index:
+    if _raw_getters[1]() == dev.index:
         rc = fn(*args)
     else:
         with _on(dev):
@@ -1095,13 +1112,13 @@ def spec_tree_plan(parent, n_nodes, cache_len, k_cache, page_table=None, plan=No
         raise ValueError(f"sizes out of range: B={B} N={N}")
     if plan is not None and ((plan.B, plan.N) != (B, N) or plan.data.device != dev):
         raise ValueError(f"plan is for B={plan.B} N={plan.N} on {plan.data.device}")
-    s, cur = _call_stream(stream, dev, (parent, n_nodes, cache_len, page_table,
-                                        plan.data if plan is not None else None))
+    h, s = _call_stream(stream, dev, (parent, n_nodes, cache_len, page_table,
+                                      plan.data if plan is not None else None))
     if plan is None:
-        plan = TreePlan(B, N, geometry, _empty_on(s, cur, (need // 4,), i32, dev))
+        plan = TreePlan(B, N, geometry, _empty_on(s, (need // 4,), i32, dev))
     plan.geometry = geometry
-    _launch(dev, "spec_tree_plan", library().spec_tree_plan, p, n, c, table or None, B, N, *geometry,
-            plan.data.data_ptr(), need, s.cuda_stream)
+    _launch(dev, "spec_tree_plan", (_lib or library()).spec_tree_plan, p, n, c, table, B, N,
+            *geometry, plan.data.data_ptr(), need, h)
     return plan
 
 
@@ -1122,22 +1139,21 @@ def attention_workspace(N: int, Hq: int, Hkv: int, D: int, device=None, stream=N
     device = torch.device(device if device is not None else "cuda")
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
-    current = torch.cuda.current_stream(device)
-    s = stream if stream is not None else current
-    return _attention_workspace(N, Hq, Hkv, D, device, s, s.cuda_stream == current.cuda_stream)
+    h, s = _call_stream(stream, device, ())
+    return _attention_workspace(N, Hq, Hkv, D, device, h, s)
 
 
-def _attention_workspace(N, Hq, Hkv, D, device, s, is_current):
+def _attention_workspace(N, Hq, Hkv, D, device, h, s):
     torch = _torch()
     need = spec_tree_attention_workspace_size(N, Hq, Hkv, D)
     if need == 0:
         raise ValueError(f"sizes out of range: N={N} Hq={Hq} Hkv={Hkv} D={D}")
-    if not is_current:
+    if s is not None:
         with torch.cuda.stream(s):
-            return _attention_workspace(N, Hq, Hkv, D, device, s, True)
+            return _attention_workspace(N, Hq, Hkv, D, device, h, None)
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(need, dtype=torch.uint8, device=device)
-    key = (device.index, s.cuda_stream)
+    key = (device.index, h)
     ws = _attention_ws.get(key)
     if ws is None or ws.numel() < need:
         ws = _attention_ws[key] = torch.empty(need, dtype=torch.uint8, device=device)
@@ -1184,23 +1200,23 @@ def spec_tree_attention(q, k_new, v_new, k_cache, v_cache, plan, page_table=None
         raise ValueError(f"scale must be finite and positive, got {scale}")
     if table and S % 128 and (S < 8 or S & (S - 1)):
         raise ValueError(f"page size {S}: a multiple of 128, or a power of two from 8")
-    s, cur = _call_stream(stream, dev, (q, k_new, v_new, k_cache, v_cache, plan.data, page_table,
-                                        out, ws))
+    h, s = _call_stream(stream, dev, (q, k_new, v_new, k_cache, v_cache, plan.data, page_table,
+                                      out, ws))
     if out is None:
-        out = _empty_on(s, cur, (B, N, Hq, D), dtype, dev)
+        out = _empty_on(s, (B, N, Hq, D), dtype, dev)
     else:
         _dev_out("out", out, (B, N, Hq, D), dtype, dev)
-    lse = _empty_on(s, cur, (B, N, Hq), torch.float32, dev) if want_lse else None
+    lse = _empty_on(s, (B, N, Hq), torch.float32, dev) if want_lse else None
     if ws is None:
-        ws = _attention_workspace(N, Hq, Hkv, D, dev, s, cur)
+        ws = _attention_workspace(N, Hq, Hkv, D, dev, h, s)
     else:
         _check_ws(ws, dev)
     args = _pack_attention(q_at, kn_at, vn_at, kc_at, vc_at, *q_st, *kn_st, *vn_st, *kc_st, *vc_st,
                            table, plan.data.data_ptr(), out.data_ptr(),
                            lse.data_ptr() if want_lse else 0, scale, B, N, Hq, Hkv, D, *geometry,
                            SPEC_BF16 if dtype == torch.bfloat16 else SPEC_F16)
-    _launch(dev, "spec_tree_attention", library().spec_tree_attention, args, ws.data_ptr(),
-            ws.numel(), s.cuda_stream)
+    _launch(dev, "spec_tree_attention", (_lib or library()).spec_tree_attention, args,
+            ws.data_ptr(), ws.numel(), h)
     return (out, lse) if want_lse else out
 
 
@@ -1238,17 +1254,17 @@ def spec_tree_commit(k_new, v_new, k_cache, v_cache, cache_len, out_num_accepted
         a, st = _strided(name, t, dev, 1)
         at.append(a)
         strides += st if lead else (0, *st)
-    s, cur = _call_stream(stream, dev, (k_new, v_new, k_cache, v_cache, cache_len,
-                                        out_num_accepted, out_nodes, page_table, out_len))
+    h, s = _call_stream(stream, dev, (k_new, v_new, k_cache, v_cache, cache_len,
+                                      out_num_accepted, out_nodes, page_table, out_len))
     if out_len is None:
-        out_len = _empty_on(s, cur, (B,), i32, dev)
+        out_len = _empty_on(s, (B,), i32, dev)
     else:
         _dev_out("out_len", out_len, (B,), i32, dev)
         if B > 0 and out_len.data_ptr() == length:
             raise ValueError("out_len must not be cache_len itself")
     args = _pack_commit(*at, *strides, length, accepted, nodes, table, out_len.data_ptr(),
                         lead[0] if lead else 1, B, N, Hkv, D, *geometry, k_new.element_size())
-    _launch(dev, "spec_tree_commit", library().spec_tree_commit, args, s.cuda_stream)
+    _launch(dev, "spec_tree_commit", (_lib or library()).spec_tree_commit, args, h)
     return out_len
 
 
@@ -1278,13 +1294,13 @@ def spec_process_logits(logits, history=None, history_len=None, prompt_len=None,
     dev, i32, f32 = logits.device, torch.int32, torch.float32
     if not logits.is_cuda or not logits.is_contiguous():
         raise ValueError("logits must be a contiguous CUDA tensor")
-    h = hl = pl = dtok = par = nn = rep = freq = pres = bt = bv = al = 0
+    hi = hl = pl = dtok = par = nn = rep = freq = pres = bt = bv = al = 0
     H = cols = M = sb = sr = 0
     if history is not None:
         if history.dim() != 2 or history_len is None or prompt_len is None:
             raise ValueError("history [B, H] comes with history_len and prompt_len [B]")
         H = history.shape[1]
-        h = _array("history", history, (B, H), i32, dev)
+        hi = _array("history", history, (B, H), i32, dev)
         hl = _array("history_len", history_len, (B,), i32, dev)
         pl = _array("prompt_len", prompt_len, (B,), i32, dev)
     elif history_len is not None or prompt_len is not None:
@@ -1325,14 +1341,14 @@ def spec_process_logits(logits, history=None, history_len=None, prompt_len=None,
         al = allowed.data_ptr()
         sb = allowed.stride(0) if allowed.shape[0] > 1 else 0
         sr = allowed.stride(1) if allowed.shape[1] > 1 else 0
-    s, cur = _call_stream(stream, dev, (logits, history, history_len, prompt_len, draft_tokens,
+    h, s = _call_stream(stream, dev, (logits, history, history_len, prompt_len, draft_tokens,
                                         parent, n_nodes, repetition, frequency, presence,
                                         bias_tokens, bias_values, allowed, out))
     if out is None:
-        out = _empty_on(s, cur, (B, R, V), logits.dtype, dev)
+        out = _empty_on(s, (B, R, V), logits.dtype, dev)
     else:
         _dev_out("out", out, (B, R, V), logits.dtype, dev)
-    args = _pack_logits(logits.data_ptr(), out.data_ptr(), h, hl, pl, dtok, par, nn, rep, freq,
+    args = _pack_logits(logits.data_ptr(), out.data_ptr(), hi, hl, pl, dtok, par, nn, rep, freq,
                         pres, bt, bv, al, sb, sr, B, R, V, H, cols, M, dt)
-    _launch(dev, "spec_process_logits", library().spec_process_logits, args, s.cuda_stream)
+    _launch(dev, "spec_process_logits", (_lib or library()).spec_process_logits, args, h)
     return out
