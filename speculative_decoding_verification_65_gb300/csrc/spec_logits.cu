@@ -8,20 +8,24 @@
 // count), marks the drafted ones and sums the biases, and keeps one bit per
 // column that any of these touched.  The history is read once per tile from
 // L2, which costs H * 4 bytes against the tile's 2 * R * C * size from HBM, so
-// no table of V counters per sequence has to exist between calls.  Then the
-// rows stream through: a 16-byte vector whose touched bits are 0 and whose
-// mask bits are 1 is stored as it was loaded, and only touched elements take
-// the penalty arithmetic.  A drafted token's own count differs from row to
-// row; it is found by walking the row's path, for columns marked as drafted.
+// no table of V counters per sequence has to exist between calls.  A drafted
+// token's own count differs from row to row; it is found by walking the row's
+// path, for columns marked as drafted.
 //
-// Bound by HBM: 2 * V * size bytes a row.  Rows start anywhere (V odd):
-// vectors are the array's 16-byte ones, as in the other kernels, and the
-// elements of a vector that reach over the tile's ends are moved one by one.
+// Bound by HBM: 2 * V * size bytes a row, nearly all of them copied as they are.
+// Where rows start on 16 bytes (V a multiple of the vector), the copy is bulk
+// copies through a ring of shared-memory stages, one tile of one row each: a
+// thread looks at its columns' touched and mask bits and touches a stage only where they
+// ask for it, then the stage is stored.  Other rows start anywhere: their
+// 16-byte vectors go through registers, and the elements of a vector that reach
+// over the tile's ends are moved one by one.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <limits.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "spec_logits.h"
 #include "spec_verify.h"
@@ -32,7 +36,9 @@ namespace {
 using namespace spec_dev;
 
 constexpr int LTH = 256;      // threads per CTA
-constexpr int LUN = 4;        // vectors in flight per thread
+constexpr int LUN = 4;        // vectors in flight per thread (rows that start anywhere)
+constexpr int STAGES = 3;     // tiles of a row in flight per CTA (the others)
+constexpr int MOST_C = 2048;  // columns of a tile, fewer where there would be few CTAs
 constexpr int HUN = 8;        // history tokens in flight per thread
 constexpr uint32_t IN_PROMPT = 0x80000000u;  // flags of a column's word; the rest is its count
 constexpr uint32_t DRAFTED = 0x40000000u;    // in the generated part of the history
@@ -42,10 +48,11 @@ struct LParams {
     spec_process_logits_args a;
     int C;             // columns per tile, a multiple of 32
     int rows_per_cta;
+    uint32_t ring_at;  // byte offset of the ring in shared memory, a multiple of 16
 };
 
 // shared memory: count words [C] | touched bits [C / 32 + 1] | bias [C] (when
-// there are biases) | drafted tokens [R] | parents [R] (tree)
+// there are biases) | drafted tokens [R] | parents [R] (tree) | stages [STAGES][C]
 struct LSmem {
     uint32_t *cnt, *touched;
     float *bias;
@@ -75,6 +82,13 @@ __device__ __forceinline__ uint32_t round_bits(float y)
     return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y));
 }
 
+__device__ __forceinline__ void bulk_copy_s2g(void *dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\t"
+                 "cp.async.bulk.commit_group;"
+                 :: "l"(dst), "r"(smem_addr(src)), "r"(bytes) : "memory");
+}
+
 struct Penalty {
     float rep, freq, pres;
 };
@@ -88,7 +102,8 @@ __device__ float touched_value(const spec_process_logits_args &A, const LSmem &S
     if (w & DRAFTED) {
         const int token = t0 + c;
         if (A.parent) {
-            for (int i = r; i > 0; i = S.par[i])
+            // (every parent has been found below its node, so at most r steps)
+            for (int i = r, left = r; i > 0 && left > 0; i = S.par[i], --left)
                 n += S.tok[i] == token;
         } else {
             for (int i = 0; i < r; ++i)
@@ -141,14 +156,11 @@ __device__ __forceinline__ void forbid(uint4 &raw, uint32_t ok)
     raw = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// ALIGNED: V is a multiple of the vector, so a thread's vectors lie at the same
-// columns in every row; it keeps their touched bits and steps from row to row.
-// Otherwise each vector's place is worked out by itself.
-template <int DT, bool ALIGNED>
-__global__ void __launch_bounds__(LTH) logits_kernel(const LParams P)
+template <int DT, bool RING>
+__global__ void __launch_bounds__(LTH) logits_kernel(const __grid_constant__ LParams P)
 {
     using L = Lg<DT>;
-    extern __shared__ uint32_t lsm[];
+    extern __shared__ __align__(16) uint32_t lsm[];
     const spec_process_logits_args &A = P.a;
     const int tid = (int)threadIdx.x;
     const int b = (int)blockIdx.y;
@@ -180,6 +192,26 @@ __global__ void __launch_bounds__(LTH) logits_kernel(const LParams P)
                !isfinite(pen.pres) || pl < 0 || hl < pl || hl > A.H || nn < 1 || nn > A.R;
     if (nn < 1 || nn > A.R)
         nn = A.R;
+    const int r0 = (int)blockIdx.z * P.rows_per_cta;
+    const int rows = min(nn, r0 + P.rows_per_cta) - r0;
+    if (rows <= 0)
+        return;
+    __shared__ __align__(8) unsigned long long full[STAGES];
+    uint8_t *ring = reinterpret_cast<uint8_t *>(lsm) + P.ring_at;
+    if (RING && tid == 0) {
+        for (int st = 0; st < STAGES; ++st)
+            mbar_init(&full[st], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        const uint32_t bytes = (uint32_t)(cols * L::ES);
+        for (int st = 0; st < STAGES && st < rows; ++st) {
+            mbar_arrive_expect_tx(&full[st], bytes);
+            bulk_copy_g2s(ring + (size_t)st * P.C * L::ES,
+                          static_cast<const uint8_t *>(A.logits) +
+                              (((size_t)b * A.R + r0 + st) * A.V + t0) * L::ES,
+                          bytes, &full[st]);
+        }
+    }
     __syncthreads();
 
     // the history's tokens of this tile
@@ -246,50 +278,93 @@ __global__ void __launch_bounds__(LTH) logits_kernel(const LParams P)
     }
     bad = __syncthreads_or(bad ? 1 : 0) != 0;
 
-    const int r0 = (int)blockIdx.z * P.rows_per_cta;
-    const int rows = min(nn, r0 + P.rows_per_cta) - r0;
-    if (rows <= 0)
-        return;
-    const int last_word = (A.V - 1) >> 5;
-    if (ALIGNED) {
+    if (RING) {
         constexpr uint32_t ALL = (1u << L::VEC) - 1u;
-        const size_t stride = (size_t)A.V / L::VEC;
-        for (int c = tid * L::VEC; c < cols; c += LTH * L::VEC) {
-            const size_t at = ((size_t)b * A.R + r0) * stride + (size_t)(t0 + c) / L::VEC;
-            const uint4 *src = reinterpret_cast<const uint4 *>(A.logits) + at;
-            uint4 *dst = reinterpret_cast<uint4 *>(A.out) + at;
-            if (bad) {
-                for (int r = 0; r < rows; ++r)
-                    dst[r * stride] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-                continue;
-            }
-            const uint32_t t = (S.touched[c >> 5] >> (c & 31)) & ALL;
-            const int shift = (t0 + c) & 31;
-            const uint32_t *mask = A.allowed ? A.allowed + b * A.allowed_stride_b +
-                r0 * A.allowed_stride_r + ((t0 + c) >> 5) : nullptr;
-            for (int r = 0; r < rows; r += LUN) {
-                uint4 raw[LUN];
-                uint32_t ok[LUN];
+        const uint32_t bytes = (uint32_t)(cols * L::ES);
+        bool stuck = false;
+        constexpr int VPT = MOST_C / L::VEC / LTH;  // a thread's vectors of a row
+        uint32_t next_ok[VPT];                      // their mask words, loaded a row ahead
+        auto load_mask = [&](int r) {
+            const uint32_t *mask = A.allowed + b * A.allowed_stride_b +
+                                   (r0 + r) * A.allowed_stride_r;
 #pragma unroll
-                for (int u = 0; u < LUN; ++u)
-                    if (r + u < rows) {
-                        raw[u] = __ldcs(src + (r + u) * stride);
-                        ok[u] = mask ? (__ldg(mask + (r + u) * A.allowed_stride_r) >> shift) & ALL
-                                     : ALL;
-                    }
-#pragma unroll
-                for (int u = 0; u < LUN; ++u)
-                    if (r + u < rows) {
-                        if (t & ok[u])
-                            touch<DT>(A, S, t0, c, r0 + r + u, t & ok[u], pen, raw[u]);
-                        if (ok[u] != ALL)
-                            forbid<DT>(raw[u], ok[u]);
-                        dst[(r + u) * stride] = raw[u];
-                    }
+            for (int k = 0; k < VPT; ++k) {
+                const int c = (tid + k * LTH) * L::VEC;
+                next_ok[k] = A.allowed && c < cols ? __ldg(mask + ((t0 + c) >> 5)) : ~0u;
             }
+        };
+        load_mask(0);
+        for (int r = 0; r < rows; ++r) {
+            const int st = r % STAGES;
+            if (!stuck && !mbar_wait(&full[st], (uint32_t)(r / STAGES) & 1u))
+                stuck = true;
+            stuck = __syncthreads_or(stuck ? 1 : 0) != 0;
+            if (stuck) {
+                // a copy never came: the rest is marked like a bad sequence's
+                for (int c = tid; c < cols; c += LTH)
+                    for (int y = r; y < rows; ++y) {
+                        const size_t e = ((size_t)b * A.R + r0 + y) * A.V + t0 + c;
+                        if (DT == SPEC_F32)
+                            reinterpret_cast<uint32_t *>(A.out)[e] = 0x7fff7fffu;
+                        else
+                            reinterpret_cast<unsigned short *>(A.out)[e] = 0x7fffu;
+                    }
+                break;
+            }
+            uint8_t *stage = ring + (size_t)st * P.C * L::ES;
+            uint32_t ok[VPT];
+#pragma unroll
+            for (int k = 0; k < VPT; ++k)
+                ok[k] = next_ok[k];
+            if (r + 1 < rows)
+                load_mask(r + 1);
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int c = (tid + k * LTH) * L::VEC;
+                if (c >= cols)
+                    continue;
+                uint4 *at = reinterpret_cast<uint4 *>(stage + (size_t)c * L::ES);
+                if (bad) {  // (its drafts and parents are not to be looked at)
+                    *at = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+                    continue;
+                }
+                const uint32_t allow = (ok[k] >> ((t0 + c) & 31)) & ALL;
+                const uint32_t t = (S.touched[c >> 5] >> (c & 31)) & allow;
+                if (t == 0 && allow == ALL)
+                    continue;
+                uint4 raw = *at;
+                if (t)
+                    touch<DT>(A, S, t0, c, r0 + r, t, pen, raw);
+                if (allow != ALL)
+                    forbid<DT>(raw, allow);
+                *at = raw;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncthreads();
+            if (tid == 0) {
+                const size_t e = ((size_t)b * A.R + r0 + r) * A.V + t0;
+                bulk_copy_s2g(static_cast<uint8_t *>(A.out) + e * L::ES, stage, bytes);
+                // the stage of the row before is free once its store has read it
+                if (r > 0 && r - 1 + STAGES < rows) {
+                    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                    const int n = r - 1 + STAGES;
+                    mbar_arrive_expect_tx(&full[n % STAGES], bytes);
+                    bulk_copy_g2s(ring + (size_t)(n % STAGES) * P.C * L::ES,
+                                  static_cast<const uint8_t *>(A.logits) +
+                                      (e + (size_t)(STAGES - 1) * A.V) * L::ES,
+                                  bytes, &full[n % STAGES]);
+                }
+            }
+        }
+        if (tid == 0) {
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            if (stuck)  // copies still in flight end first (bounded)
+                for (int st = 0; st < STAGES; ++st)
+                    (void)mbar_wait(&full[st], 0u), (void)mbar_wait(&full[st], 1u);
         }
         return;
     }
+    const int last_word = (A.V - 1) >> 5;
     const int NV = P.C / L::VEC + 1;  // vectors a row can have, its ends included
     const int total = rows * NV;
     for (int i0 = tid; i0 < total; i0 += LUN * LTH) {
@@ -367,7 +442,36 @@ bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) &
 
 size_t smem_bytes(const spec_process_logits_args &a, int C)
 {
-    return 4 * ((size_t)C + C / 32 + 1 + (a.bias_cols > 0 ? C : 0) + 2 * (size_t)a.R);
+    return (4 * ((size_t)C + C / 32 + 1 + (a.bias_cols > 0 ? C : 0) + 2 * (size_t)a.R) + 15) / 16 * 16;
+}
+
+// the largest tile's words, bits, biases, drafts and fp32 stages
+constexpr size_t MOST_SMEM =
+    4 * (MOST_C + MOST_C / 32 + 1 + MOST_C + 2 * SPEC_LOGITS_MAX_ROWS) + 16 +
+    (size_t)STAGES * MOST_C * 4;
+static_assert(MOST_SMEM <= 232448 - 64, "227 KB per CTA");
+std::atomic<bool> g_attr[64][2];  // opted in, per device and dtype
+
+template <int DT>
+int launch(const LParams &P, bool ring, dim3 grid, size_t smem, cudaStream_t st)
+{
+    if (!ring) {
+        logits_kernel<DT, false><<<grid, LTH, smem, st>>>(P);
+        return SPEC_OK;
+    }
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return SPEC_ECUDA;
+    if (!g_attr[dev][DT].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(logits_kernel<DT, true>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)MOST_SMEM) != cudaSuccess)
+            return SPEC_ECUDA;
+        g_attr[dev][DT].store(true, std::memory_order_release);
+    }
+    logits_kernel<DT, true>
+        <<<grid, LTH, smem + (size_t)STAGES * P.C * Lg<DT>::ES, st>>>(P);
+    return SPEC_OK;
 }
 
 }  // namespace
@@ -403,7 +507,7 @@ extern "C" int32_t spec_process_logits(const spec_process_logits_args *args, voi
 
     LParams P;
     P.a = a;
-    P.C = 4096;
+    P.C = MOST_C;
     auto tiles = [&] { return (long long)a.B * ((a.V + P.C - 1) / P.C); };
     while (P.C > 1024 && tiles() < 304)
         P.C /= 2;
@@ -411,20 +515,16 @@ extern "C" int32_t spec_process_logits(const spec_process_logits_args *args, voi
     while (tiles() * splits < 304 && splits < a.R)
         splits *= 2;
     P.rows_per_cta = (a.R + splits - 1) / splits;
-    const size_t smem = smem_bytes(a, P.C);  // at most 41 KB: no opt-in needed
+    const size_t smem = smem_bytes(a, P.C);  // at most 41 KB, and a ring of up to 64 KB
+    P.ring_at = (uint32_t)smem;
     const dim3 grid((unsigned int)((a.V + P.C - 1) / P.C), (unsigned int)a.B,
                     (unsigned int)((a.R + P.rows_per_cta - 1) / P.rows_per_cta));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (a.dtype == SPEC_F32) {
-        if (a.V % 4 == 0)
-            logits_kernel<SPEC_F32, true><<<grid, LTH, smem, st>>>(P);
-        else
-            logits_kernel<SPEC_F32, false><<<grid, LTH, smem, st>>>(P);
-    } else {
-        if (a.V % 8 == 0)
-            logits_kernel<SPEC_BF16, true><<<grid, LTH, smem, st>>>(P);
-        else
-            logits_kernel<SPEC_BF16, false><<<grid, LTH, smem, st>>>(P);
+    const int rc = a.dtype == SPEC_F32 ? launch<SPEC_F32>(P, a.V % 4 == 0, grid, smem, st)
+                                       : launch<SPEC_BF16>(P, a.V % 8 == 0, grid, smem, st);
+    if (rc != SPEC_OK) {
+        (void)cudaGetLastError();
+        return rc;
     }
     if (cudaPeekAtLastError() != cudaSuccess) {
         (void)cudaGetLastError();
