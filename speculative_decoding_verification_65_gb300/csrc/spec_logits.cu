@@ -14,9 +14,11 @@
 //
 // Bound by HBM: 2 * V * size bytes a row, nearly all of them copied as they are.
 // Where rows start on 16 bytes (V a multiple of the vector), the copy is bulk
-// copies through a ring of shared-memory stages, one tile of one row each: a
-// thread looks at its columns' touched and mask bits and touches a stage only where they
-// ask for it, then the stage is stored.  Other rows start anywhere: their
+// copies through a ring of shared-memory stages, one tile of one row each.  In
+// the stage the tile's touched columns, listed once, are shared out among the
+// threads (found by their vectors' bits instead, the few touched ones of a
+// warp took its time one by one, 40 % of the call under trees and masks), then
+// a mask forbids what it does, and the stage is stored.  Other rows start anywhere: their
 // 16-byte vectors go through registers, and the elements of a vector that reach
 // over the tile's ends are moved one by one.
 #include <cuda_bf16.h>
@@ -37,7 +39,7 @@ using namespace spec_dev;
 
 constexpr int LTH = 256;      // threads per CTA
 constexpr int LUN = 4;        // vectors in flight per thread (rows that start anywhere)
-constexpr int STAGES = 3;     // tiles of a row in flight per CTA (the others)
+constexpr int STAGES = 4;     // tiles of a row in flight per CTA (the others)
 constexpr int MOST_C = 2048;  // columns of a tile, fewer where there would be few CTAs
 constexpr int HUN = 8;        // history tokens in flight per thread
 constexpr uint32_t IN_PROMPT = 0x80000000u;  // flags of a column's word; the rest is its count
@@ -48,11 +50,12 @@ struct LParams {
     spec_process_logits_args a;
     int C;             // columns per tile, a multiple of 32
     int rows_per_cta;
-    uint32_t ring_at;  // byte offset of the ring in shared memory, a multiple of 16
+    uint32_t list_at, ring_at;  // byte offsets in shared memory, multiples of 16
 };
 
 // shared memory: count words [C] | touched bits [C / 32 + 1] | bias [C] (when
-// there are biases) | drafted tokens [R] | parents [R] (tree) | stages [STAGES][C]
+// there are biases) | drafted tokens [R] | parents [R] (tree) | touched columns [C] |
+// stages [STAGES][C]
 struct LSmem {
     uint32_t *cnt, *touched;
     float *bias;
@@ -197,8 +200,12 @@ __global__ void __launch_bounds__(LTH) logits_kernel(const __grid_constant__ LPa
     if (rows <= 0)
         return;
     __shared__ __align__(8) unsigned long long full[STAGES];
+    __shared__ int listed;          // touched columns
+    __shared__ volatile int stuck;  // a copy's wait gave up
     uint8_t *ring = reinterpret_cast<uint8_t *>(lsm) + P.ring_at;
     if (RING && tid == 0) {
+        listed = 0;
+        stuck = 0;
         for (int st = 0; st < STAGES; ++st)
             mbar_init(&full[st], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -281,7 +288,11 @@ __global__ void __launch_bounds__(LTH) logits_kernel(const __grid_constant__ LPa
     if (RING) {
         constexpr uint32_t ALL = (1u << L::VEC) - 1u;
         const uint32_t bytes = (uint32_t)(cols * L::ES);
-        bool stuck = false;
+        // the touched columns, in any order: each is worked out by itself
+        uint16_t *list = reinterpret_cast<uint16_t *>(reinterpret_cast<uint8_t *>(lsm) + P.list_at);
+        for (int c = tid; c < cols; c += LTH)
+            if ((S.touched[c >> 5] >> (c & 31)) & 1u)
+                list[atomicAdd(&listed, 1)] = (uint16_t)c;
         constexpr int VPT = MOST_C / L::VEC / LTH;  // a thread's vectors of a row
         uint32_t next_ok[VPT];                      // their mask words, loaded a row ahead
         auto load_mask = [&](int r) {
@@ -294,11 +305,51 @@ __global__ void __launch_bounds__(LTH) logits_kernel(const __grid_constant__ LPa
             }
         };
         load_mask(0);
+        __syncthreads();
+        const int n_listed = bad ? 0 : listed;
         for (int r = 0; r < rows; ++r) {
             const int st = r % STAGES;
-            if (!stuck && !mbar_wait(&full[st], (uint32_t)(r / STAGES) & 1u))
-                stuck = true;
-            stuck = __syncthreads_or(stuck ? 1 : 0) != 0;
+            if (!mbar_wait(&full[st], (uint32_t)(r / STAGES) & 1u))
+                stuck = 1;
+            uint8_t *stage = ring + (size_t)st * P.C * L::ES;
+            uint32_t ok[VPT];
+#pragma unroll
+            for (int k = 0; k < VPT; ++k)
+                ok[k] = next_ok[k];
+            if (r + 1 < rows)
+                load_mask(r + 1);
+            for (int i = tid; i < n_listed; i += LTH) {
+                const int c = list[i];
+                if (DT == SPEC_F32) {
+                    float *x = reinterpret_cast<float *>(stage) + c;
+                    *x = touched_value(A, S, t0, c, r0 + r, *x, pen);
+                } else {
+                    unsigned short *x = reinterpret_cast<unsigned short *>(stage) + c;
+                    *x = (unsigned short)round_bits<DT>(touched_value(
+                        A, S, t0, c, r0 + r, __uint_as_float((uint32_t)*x << 16), pen));
+                }
+            }
+            if (A.allowed || bad) {
+                if (n_listed > 0)
+                    __syncthreads();
+#pragma unroll
+                for (int k = 0; k < VPT; ++k) {
+                    const int c = (tid + k * LTH) * L::VEC;
+                    const uint32_t allow = (ok[k] >> ((t0 + c) & 31)) & ALL;
+                    if (c >= cols || (allow == ALL && !bad))
+                        continue;
+                    uint4 *at = reinterpret_cast<uint4 *>(stage + (size_t)c * L::ES);
+                    if (bad) {
+                        *at = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+                    } else {
+                        uint4 raw = *at;
+                        forbid<DT>(raw, allow);
+                        *at = raw;
+                    }
+                }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncthreads();
             if (stuck) {
                 // a copy never came: the rest is marked like a bad sequence's
                 for (int c = tid; c < cols; c += LTH)
@@ -311,36 +362,6 @@ __global__ void __launch_bounds__(LTH) logits_kernel(const __grid_constant__ LPa
                     }
                 break;
             }
-            uint8_t *stage = ring + (size_t)st * P.C * L::ES;
-            uint32_t ok[VPT];
-#pragma unroll
-            for (int k = 0; k < VPT; ++k)
-                ok[k] = next_ok[k];
-            if (r + 1 < rows)
-                load_mask(r + 1);
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int c = (tid + k * LTH) * L::VEC;
-                if (c >= cols)
-                    continue;
-                uint4 *at = reinterpret_cast<uint4 *>(stage + (size_t)c * L::ES);
-                if (bad) {  // (its drafts and parents are not to be looked at)
-                    *at = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-                    continue;
-                }
-                const uint32_t allow = (ok[k] >> ((t0 + c) & 31)) & ALL;
-                const uint32_t t = (S.touched[c >> 5] >> (c & 31)) & allow;
-                if (t == 0 && allow == ALL)
-                    continue;
-                uint4 raw = *at;
-                if (t)
-                    touch<DT>(A, S, t0, c, r0 + r, t, pen, raw);
-                if (allow != ALL)
-                    forbid<DT>(raw, allow);
-                *at = raw;
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncthreads();
             if (tid == 0) {
                 const size_t e = ((size_t)b * A.R + r0 + r) * A.V + t0;
                 bulk_copy_s2g(static_cast<uint8_t *>(A.out) + e * L::ES, stage, bytes);
@@ -445,9 +466,9 @@ size_t smem_bytes(const spec_process_logits_args &a, int C)
     return (4 * ((size_t)C + C / 32 + 1 + (a.bias_cols > 0 ? C : 0) + 2 * (size_t)a.R) + 15) / 16 * 16;
 }
 
-// the largest tile's words, bits, biases, drafts and fp32 stages
+// the largest tile's words, bits, biases, drafts, list and fp32 stages
 constexpr size_t MOST_SMEM =
-    4 * (MOST_C + MOST_C / 32 + 1 + MOST_C + 2 * SPEC_LOGITS_MAX_ROWS) + 16 +
+    4 * (MOST_C + MOST_C / 32 + 1 + MOST_C + 2 * SPEC_LOGITS_MAX_ROWS) + 16 + MOST_C * 2 +
     (size_t)STAGES * MOST_C * 4;
 static_assert(MOST_SMEM <= 232448 - 64, "227 KB per CTA");
 std::atomic<bool> g_attr[64][2];  // opted in, per device and dtype
@@ -470,7 +491,7 @@ int launch(const LParams &P, bool ring, dim3 grid, size_t smem, cudaStream_t st)
         g_attr[dev][DT].store(true, std::memory_order_release);
     }
     logits_kernel<DT, true>
-        <<<grid, LTH, smem + (size_t)STAGES * P.C * Lg<DT>::ES, st>>>(P);
+        <<<grid, LTH, P.ring_at + (size_t)STAGES * P.C * Lg<DT>::ES, st>>>(P);
     return SPEC_OK;
 }
 
@@ -515,8 +536,9 @@ extern "C" int32_t spec_process_logits(const spec_process_logits_args *args, voi
     while (tiles() * splits < 304 && splits < a.R)
         splits *= 2;
     P.rows_per_cta = (a.R + splits - 1) / splits;
-    const size_t smem = smem_bytes(a, P.C);  // at most 41 KB, and a ring of up to 64 KB
-    P.ring_at = (uint32_t)smem;
+    const size_t smem = smem_bytes(a, P.C);  // at most 25 KB, a list of 4 and a ring of 24
+    P.list_at = (uint32_t)smem;
+    P.ring_at = P.list_at + (uint32_t)P.C * 2;
     const dim3 grid((unsigned int)((a.V + P.C - 1) / P.C), (unsigned int)a.B,
                     (unsigned int)((a.R + P.rows_per_cta - 1) / P.rows_per_cta));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
