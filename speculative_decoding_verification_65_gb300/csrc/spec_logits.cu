@@ -13,14 +13,15 @@
 // path, for columns marked as drafted.
 //
 // Bound by HBM: 2 * V * size bytes a row, nearly all of them copied as they are.
-// Where rows start on 16 bytes (V a multiple of the vector), the copy is bulk
-// copies through a ring of shared-memory stages, one tile of one row each.  In
-// the stage the tile's touched columns, listed once, are shared out among the
-// threads (found by their vectors' bits instead, the few touched ones of a
-// warp took its time one by one, 40 % of the call under trees and masks), then
-// a mask forbids what it does, and the stage is stored.  Other rows start anywhere: their
-// 16-byte vectors go through registers, and the elements of a vector that reach
-// over the tile's ends are moved one by one.
+// So the copy is bulk copies through a ring of shared-memory stages, one tile of
+// one row each.  In the stage the tile's touched columns, listed once, are
+// shared out among the threads (found by their vectors' bits instead, the few
+// touched ones of a warp took its time one by one, 40 % of the call under
+// trees and masks), then a mask forbids what it does, and the stage is stored.
+// A bulk copy moves whole 16-byte vectors of the array.  Where V is a multiple
+// of the vector that is the tile; other rows start anywhere, their stages hold
+// the vectors that the tile reaches into, and the tile's elements in the first
+// and last of them are stored one by one.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <limits.h>
@@ -38,8 +39,13 @@ namespace {
 using namespace spec_dev;
 
 constexpr int LTH = 256;      // threads per CTA
-constexpr int LUN = 4;        // vectors in flight per thread (rows that start anywhere)
-constexpr int STAGES = 4;     // tiles of a row in flight per CTA (the others)
+// Tiles of a row in flight per CTA: 24 KB of fp32, 16 of bf16.  A fourth fp32 stage takes
+// more from the number of CTAs than it gives (256 x 9 x 151936: 403 us with
+// three, 425 with four); bf16 gains by it (64 x 29 x 128256 under masks: 171 us
+// with four, 178 with three).
+template <int DT>
+__host__ __device__ constexpr int stages() { return DT == SPEC_F32 ? 3 : 4; }
+constexpr int MOST_STAGES = 4;
 constexpr int MOST_C = 2048;  // columns of a tile, fewer where there would be few CTAs
 constexpr int HUN = 8;        // history tokens in flight per thread
 constexpr uint32_t IN_PROMPT = 0x80000000u;  // flags of a column's word; the rest is its count
@@ -53,29 +59,15 @@ struct LParams {
     uint32_t list_at, ring_at;  // byte offsets in shared memory, multiples of 16
 };
 
-// shared memory: count words [C] | touched bits [C / 32 + 1] | bias [C] (when
+// shared memory: count words [C] | touched bits [C / 32] | bits of columns with several
+// biases [C / 32] | bias [C] (when
 // there are biases) | drafted tokens [R] | parents [R] (tree) | touched columns [C] |
-// stages [STAGES][C]
+// stages [stages][C + a vector]
 struct LSmem {
-    uint32_t *cnt, *touched;
+    uint32_t *cnt, *touched, *again;
     float *bias;
     int *tok, *par;
 };
-
-// bits [c, c + 32) of a bit array; the words past `words` read as 0
-__device__ __forceinline__ uint32_t bits_from(const uint32_t *w, int c)
-{
-    return __funnelshift_r(w[c >> 5], w[(c >> 5) + 1], c & 31);
-}
-
-// bits [c, c + n) of a mask in global memory whose last word is `last`
-__device__ __forceinline__ uint32_t mask_from(const uint32_t *w, int c, int n, int last)
-{
-    const int i = c >> 5, s = c & 31;
-    const uint32_t lo = __ldg(w + i);
-    const uint32_t hi = (s + n > 32 && i < last) ? __ldg(w + i + 1) : 0u;
-    return __funnelshift_r(lo, hi, s);
-}
 
 template <int DT>
 __device__ __forceinline__ uint32_t round_bits(float y)
@@ -124,23 +116,6 @@ __device__ float touched_value(const spec_process_logits_args &A, const LSmem &S
     return x;
 }
 
-// the touched elements t (bits) of a vector at column c
-template <int DT>
-__device__ __forceinline__ void touch(const spec_process_logits_args &A, const LSmem &S, int t0,
-                                      int c, int r, uint32_t t, const Penalty &pen, uint4 &raw)
-{
-    while (t) {
-        const int j = __ffs((int)t) - 1;
-        t &= t - 1;
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-        const int h = DT == SPEC_F32 ? j : j >> 1;
-        const uint32_t word = h == 0 ? w[0] : h == 1 ? w[1] : h == 2 ? w[2] : w[3];
-        const float x = __uint_as_float(DT == SPEC_F32 ? word
-                                        : (j & 1) ? (word & 0xffff0000u) : (word << 16));
-        Lg<DT>::put(raw, j, round_bits<DT>(touched_value(A, S, t0, c + j, r, x, pen)));
-    }
-}
-
 // -inf where the bits of `ok` are 0
 template <int DT>
 __device__ __forceinline__ void forbid(uint4 &raw, uint32_t ok)
@@ -159,10 +134,12 @@ __device__ __forceinline__ void forbid(uint4 &raw, uint32_t ok)
     raw = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int DT, bool RING>
+// ALIGNED: V is a multiple of the vector.
+template <int DT, bool ALIGNED>
 __global__ void __launch_bounds__(LTH) logits_kernel(const __grid_constant__ LParams P)
 {
     using L = Lg<DT>;
+    constexpr int STAGES = stages<DT>();
     extern __shared__ __align__(16) uint32_t lsm[];
     const spec_process_logits_args &A = P.a;
     const int tid = (int)threadIdx.x;
@@ -172,13 +149,14 @@ __global__ void __launch_bounds__(LTH) logits_kernel(const __grid_constant__ LPa
     LSmem S;
     S.cnt = lsm;
     S.touched = S.cnt + P.C;
-    float *fb = reinterpret_cast<float *>(S.touched + P.C / 32 + 1);
+    S.again = S.touched + P.C / 32;
+    float *fb = reinterpret_cast<float *>(S.again + P.C / 32);
     S.bias = A.bias_cols > 0 ? fb : nullptr;
     S.tok = reinterpret_cast<int *>(fb + (A.bias_cols > 0 ? P.C : 0));
     S.par = S.tok + A.R;
 
     wait_previous_kernel();
-    for (int i = tid; i < P.C + P.C / 32 + 1; i += LTH)
+    for (int i = tid; i < P.C + 2 * (P.C / 32); i += LTH)
         lsm[i] = 0;
     if (S.bias)
         for (int i = tid; i < P.C; i += LTH)
@@ -202,25 +180,42 @@ __global__ void __launch_bounds__(LTH) logits_kernel(const __grid_constant__ LPa
     __shared__ __align__(8) unsigned long long full[STAGES];
     __shared__ int listed;          // touched columns
     __shared__ volatile int stuck;  // a copy's wait gave up
+    // Row r of the CTA: its tile's first element in the array, how far into a vector it
+    // lies, and the tile's whole vectors of the array (the array's last, broken one is not)
     uint8_t *ring = reinterpret_cast<uint8_t *>(lsm) + P.ring_at;
-    if (RING && tid == 0) {
+    const uint32_t stage_bytes = (uint32_t)(P.C + L::VEC) * L::ES;
+    auto first_of = [&](int r) -> size_t { return ((size_t)b * A.R + r0 + r) * A.V + t0; };
+    auto shift_of = [&](int r) -> int { return ALIGNED ? 0 : (int)(first_of(r) % L::VEC); };
+    auto vectors_of = [&](int r) -> int {
+        if (ALIGNED)
+            return cols / L::VEC;
+        const size_t v0 = first_of(r) / L::VEC, all = (size_t)A.B * A.R * A.V / L::VEC;
+        const int want = (shift_of(r) + cols + L::VEC - 1) / L::VEC;
+        return v0 + want <= all ? want : (int)(all - v0);
+    };
+    auto load_row = [&](int r) {  // one thread
+        const int st = r % STAGES;
+        const uint32_t bytes = (uint32_t)vectors_of(r) * 16;
+        mbar_arrive_expect_tx(&full[st], bytes);
+        if (bytes > 0)
+            bulk_copy_g2s(ring + st * stage_bytes,
+                          static_cast<const uint8_t *>(A.logits) + first_of(r) / L::VEC * 16,
+                          bytes, &full[st]);
+    };
+    if (tid == 0) {
         listed = 0;
         stuck = 0;
         for (int st = 0; st < STAGES; ++st)
             mbar_init(&full[st], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        const uint32_t bytes = (uint32_t)(cols * L::ES);
-        for (int st = 0; st < STAGES && st < rows; ++st) {
-            mbar_arrive_expect_tx(&full[st], bytes);
-            bulk_copy_g2s(ring + (size_t)st * P.C * L::ES,
-                          static_cast<const uint8_t *>(A.logits) +
-                              (((size_t)b * A.R + r0 + st) * A.V + t0) * L::ES,
-                          bytes, &full[st]);
-        }
+        for (int r = 0; r < STAGES && r < rows; ++r)
+            load_row(r);
     }
     __syncthreads();
 
+    const int32_t *bt = A.bias_tokens + (size_t)b * A.bias_cols;
+    const float *bv = A.bias_values + (size_t)b * A.bias_cols;
     // the history's tokens of this tile
     if (!bad) {
         const int32_t *hist = A.history + (size_t)b * A.H;
@@ -261,201 +256,172 @@ __global__ void __launch_bounds__(LTH) logits_kernel(const __grid_constant__ LPa
                     atomicOr(&S.touched[c >> 5], 1u << (c & 31));
                 }
             }
-        // biases: the first entry of a token sums all of its entries in order
-        const int32_t *bt = A.bias_tokens + (size_t)b * A.bias_cols;
-        const float *bv = A.bias_values + (size_t)b * A.bias_cols;
+        // biases: entry i bids bias_cols - i for its column, so the first one wins
         for (int i = tid; i < A.bias_cols; i += LTH) {
             const int t = bt[i];
             bad |= t < -1 || t >= A.V;
             const int c = t - t0;
             if (t < 0 || c < 0 || c >= cols)
                 continue;
-            bool first_of = true;
-            for (int j = 0; j < i && first_of; ++j)
-                first_of = bt[j] != t;
-            if (!first_of)
-                continue;
-            float sum = bv[i];
-            for (int j = i + 1; j < A.bias_cols; ++j)
-                if (bt[j] == t)
-                    sum += bv[j];
-            S.bias[c] = sum;
+            if (atomicMax(reinterpret_cast<int *>(&S.bias[c]), A.bias_cols - i) != 0)
+                atomicOr(&S.again[c >> 5], 1u << (c & 31));
             atomicOr(&S.touched[c >> 5], 1u << (c & 31));
         }
     }
     bad = __syncthreads_or(bad ? 1 : 0) != 0;
+    if (A.bias_cols > 0) {
+        uint32_t won = 0;  // which of the thread's entries
+        if (!bad)
+            for (int i = tid, k = 0; i < A.bias_cols; i += LTH, ++k) {
+                const int c = bt[i] - t0;
+                if (bt[i] >= 0 && c >= 0 && c < cols &&
+                    __float_as_int(S.bias[c]) == A.bias_cols - i)
+                    won |= 1u << k;
+            }
+        __syncthreads();
+        // the first entry of a token sums all of its entries in order
+        for (int i = tid; won; i += LTH, won >>= 1) {
+            if (!(won & 1u))
+                continue;
+            const int t = bt[i], c = t - t0;
+            float sum = bv[i];
+            if ((S.again[c >> 5] >> (c & 31)) & 1u)
+                for (int j = i + 1; j < A.bias_cols; ++j)
+                    if (bt[j] == t)
+                        sum += bv[j];
+            S.bias[c] = sum;
+        }
+    }
 
-    if (RING) {
-        constexpr uint32_t ALL = (1u << L::VEC) - 1u;
-        const uint32_t bytes = (uint32_t)(cols * L::ES);
-        // the touched columns, in any order: each is worked out by itself
-        uint16_t *list = reinterpret_cast<uint16_t *>(reinterpret_cast<uint8_t *>(lsm) + P.list_at);
-        for (int c = tid; c < cols; c += LTH)
-            if ((S.touched[c >> 5] >> (c & 31)) & 1u)
-                list[atomicAdd(&listed, 1)] = (uint16_t)c;
-        constexpr int VPT = MOST_C / L::VEC / LTH;  // a thread's vectors of a row
-        uint32_t next_ok[VPT];                      // their mask words, loaded a row ahead
-        auto load_mask = [&](int r) {
-            const uint32_t *mask = A.allowed + b * A.allowed_stride_b +
-                                   (r0 + r) * A.allowed_stride_r;
+    // the touched columns, in any order: each is worked out by itself
+    uint16_t *list = reinterpret_cast<uint16_t *>(reinterpret_cast<uint8_t *>(lsm) + P.list_at);
+    for (int c = tid; c < cols; c += LTH)
+        if ((S.touched[c >> 5] >> (c & 31)) & 1u)
+            list[atomicAdd(&listed, 1)] = (uint16_t)c;
+    constexpr uint32_t ALL = (1u << L::VEC) - 1u;
+    constexpr int VPT = MOST_C / L::VEC / LTH + (ALIGNED ? 0 : 1);  // a thread's vectors of a row
+    // The mask words that their elements' bits lie in, loaded a row ahead and not looked at
+    // before (a second word where vectors lie anywhere).
+    uint32_t next_lo[VPT], next_hi[VPT];
+    auto load_mask = [&](int r) {
+        const uint32_t *mask = A.allowed + b * A.allowed_stride_b + (r0 + r) * A.allowed_stride_r;
+        const int mis = shift_of(r);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = (tid + k * LTH) * L::VEC - mis, w = (t0 + max(c, 0)) >> 5;
+            next_lo[k] = c < cols ? __ldg(mask + w) : ~0u;
+            if (!ALIGNED)
+                next_hi[k] = c < cols && w < (A.V - 1) >> 5 ? __ldg(mask + w + 1) : ~0u;
+        }
+    };
+    if (A.allowed)
+        load_mask(0);
+    __syncthreads();
+    const int n_listed = bad ? 0 : listed;
+    for (int r = 0; r < rows; ++r) {
+        const int st = r % STAGES;
+        if (!mbar_wait(&full[st], (uint32_t)(r / STAGES) & 1u))
+            stuck = 1;
+        uint8_t *stage = ring + st * stage_bytes;
+        const int mis = shift_of(r), have = vectors_of(r) * L::VEC - mis;
+        if (!ALIGNED && have < cols) {
+            // the array's last elements, past its last whole vector
+            for (int c = max(have, 0) + tid; c < cols; c += LTH) {
+                if (DT == SPEC_F32)
+                    reinterpret_cast<uint32_t *>(stage)[c + mis] =
+                        reinterpret_cast<const uint32_t *>(A.logits)[first_of(r) + c];
+                else
+                    reinterpret_cast<unsigned short *>(stage)[c + mis] =
+                        reinterpret_cast<const unsigned short *>(A.logits)[first_of(r) + c];
+            }
+            __syncthreads();
+        }
+        for (int i = tid; i < n_listed; i += LTH) {
+            const int c = list[i];
+            if (DT == SPEC_F32) {
+                float *x = reinterpret_cast<float *>(stage) + c + mis;
+                *x = touched_value(A, S, t0, c, r0 + r, *x, pen);
+            } else {
+                unsigned short *x = reinterpret_cast<unsigned short *>(stage) + c + mis;
+                *x = (unsigned short)round_bits<DT>(touched_value(
+                    A, S, t0, c, r0 + r, __uint_as_float((uint32_t)*x << 16), pen));
+            }
+        }
+        if (bad) {
+            for (int v = tid; v * L::VEC - mis < cols; v += LTH)
+                reinterpret_cast<uint4 *>(stage)[v] =
+                    make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+        } else if (A.allowed) {
+            uint32_t ok[VPT];  // (elements outside the tile are not stored, whatever becomes of them)
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int c = (tid + k * LTH) * L::VEC;
-                next_ok[k] = A.allowed && c < cols ? __ldg(mask + ((t0 + c) >> 5)) : ~0u;
+                const int c = (tid + k * LTH) * L::VEC - mis, lo = max(c, 0);
+                if (ALIGNED)
+                    ok[k] = (next_lo[k] >> ((t0 + c) & 31)) & ALL;
+                else
+                    ok[k] = (__funnelshift_r(next_lo[k], next_hi[k], (t0 + lo) & 31) << (lo - c)) &
+                            ALL;
             }
-        };
-        load_mask(0);
-        __syncthreads();
-        const int n_listed = bad ? 0 : listed;
-        for (int r = 0; r < rows; ++r) {
-            const int st = r % STAGES;
-            if (!mbar_wait(&full[st], (uint32_t)(r / STAGES) & 1u))
-                stuck = 1;
-            uint8_t *stage = ring + (size_t)st * P.C * L::ES;
-            uint32_t ok[VPT];
-#pragma unroll
-            for (int k = 0; k < VPT; ++k)
-                ok[k] = next_ok[k];
             if (r + 1 < rows)
                 load_mask(r + 1);
-            for (int i = tid; i < n_listed; i += LTH) {
-                const int c = list[i];
-                if (DT == SPEC_F32) {
-                    float *x = reinterpret_cast<float *>(stage) + c;
-                    *x = touched_value(A, S, t0, c, r0 + r, *x, pen);
-                } else {
-                    unsigned short *x = reinterpret_cast<unsigned short *>(stage) + c;
-                    *x = (unsigned short)round_bits<DT>(touched_value(
-                        A, S, t0, c, r0 + r, __uint_as_float((uint32_t)*x << 16), pen));
-                }
-            }
-            if (A.allowed || bad) {
-                if (n_listed > 0)
-                    __syncthreads();
+            if (n_listed > 0)
+                __syncthreads();
 #pragma unroll
-                for (int k = 0; k < VPT; ++k) {
-                    const int c = (tid + k * LTH) * L::VEC;
-                    const uint32_t allow = (ok[k] >> ((t0 + c) & 31)) & ALL;
-                    if (c >= cols || (allow == ALL && !bad))
-                        continue;
-                    uint4 *at = reinterpret_cast<uint4 *>(stage + (size_t)c * L::ES);
-                    if (bad) {
-                        *at = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-                    } else {
-                        uint4 raw = *at;
-                        forbid<DT>(raw, allow);
-                        *at = raw;
-                    }
-                }
+            for (int k = 0; k < VPT; ++k) {
+                const int v = tid + k * LTH;
+                if (v * L::VEC - mis >= cols || ok[k] == ALL)
+                    continue;
+                uint4 *at = reinterpret_cast<uint4 *>(stage) + v;
+                uint4 raw = *at;
+                forbid<DT>(raw, ok[k]);
+                *at = raw;
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncthreads();
-            if (stuck) {
-                // a copy never came: the rest is marked like a bad sequence's
-                for (int c = tid; c < cols; c += LTH)
-                    for (int y = r; y < rows; ++y) {
-                        const size_t e = ((size_t)b * A.R + r0 + y) * A.V + t0 + c;
-                        if (DT == SPEC_F32)
-                            reinterpret_cast<uint32_t *>(A.out)[e] = 0x7fff7fffu;
-                        else
-                            reinterpret_cast<unsigned short *>(A.out)[e] = 0x7fffu;
-                    }
-                break;
-            }
-            if (tid == 0) {
-                const size_t e = ((size_t)b * A.R + r0 + r) * A.V + t0;
-                bulk_copy_s2g(static_cast<uint8_t *>(A.out) + e * L::ES, stage, bytes);
-                // the stage of the row before is free once its store has read it
-                if (r > 0 && r - 1 + STAGES < rows) {
-                    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                    const int n = r - 1 + STAGES;
-                    mbar_arrive_expect_tx(&full[n % STAGES], bytes);
-                    bulk_copy_g2s(ring + (size_t)(n % STAGES) * P.C * L::ES,
-                                  static_cast<const uint8_t *>(A.logits) +
-                                      (e + (size_t)(STAGES - 1) * A.V) * L::ES,
-                                  bytes, &full[n % STAGES]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();
+        if (stuck) {
+            // a copy never came: the rest is marked like a bad sequence's
+            for (int c = tid; c < cols; c += LTH)
+                for (int y = r; y < rows; ++y) {
+                    if (DT == SPEC_F32)
+                        reinterpret_cast<uint32_t *>(A.out)[first_of(y) + c] = 0x7fff7fffu;
+                    else
+                        reinterpret_cast<unsigned short *>(A.out)[first_of(y) + c] = 0x7fffu;
                 }
+            break;
+        }
+        // the vectors that are the tile's alone, and its elements in the others
+        const int v0 = mis ? 1 : 0, v1 = (mis + cols) / L::VEC;
+        if (!ALIGNED && tid < 2 * L::VEC) {
+            const int c = tid < L::VEC ? tid : cols - 1 - (tid - L::VEC);
+            if (c >= 0 && c < cols && (c + mis < v0 * L::VEC || c + mis >= v1 * L::VEC)) {
+                if (DT == SPEC_F32)
+                    reinterpret_cast<uint32_t *>(A.out)[first_of(r) + c] =
+                        reinterpret_cast<const uint32_t *>(stage)[c + mis];
+                else
+                    reinterpret_cast<unsigned short *>(A.out)[first_of(r) + c] =
+                        reinterpret_cast<const unsigned short *>(stage)[c + mis];
             }
         }
         if (tid == 0) {
-            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-            if (stuck)  // copies still in flight end first (bounded)
-                for (int st = 0; st < STAGES; ++st)
-                    (void)mbar_wait(&full[st], 0u), (void)mbar_wait(&full[st], 1u);
+            if (v1 > v0)
+                bulk_copy_s2g(static_cast<uint8_t *>(A.out) +
+                                  (first_of(r) / L::VEC + (size_t)v0) * 16,
+                              stage + v0 * 16, (uint32_t)(v1 - v0) * 16);
+            else  // (a group all the same: they are counted)
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            // the stage of the row before is free once its store has read it
+            if (r > 0 && r - 1 + STAGES < rows) {
+                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                load_row(r - 1 + STAGES);
+            }
         }
-        return;
     }
-    const int last_word = (A.V - 1) >> 5;
-    const int NV = P.C / L::VEC + 1;  // vectors a row can have, its ends included
-    const int total = rows * NV;
-    for (int i0 = tid; i0 < total; i0 += LUN * LTH) {
-        uint4 raw[LUN];
-        size_t e0[LUN];  // the vector's first element in the array
-        int col[LUN];    // its column in the tile (negative: it starts before the tile)
-        int row[LUN];    // -1: no vector
-#pragma unroll
-        for (int u = 0; u < LUN; ++u) {
-            const int i = i0 + u * LTH;
-            const int rr = i / NV, v = i - rr * NV;
-            const size_t off = ((size_t)b * A.R + (r0 + rr)) * A.V + t0;
-            const int mis = (int)(off % L::VEC);
-            row[u] = (i < total && v * L::VEC - mis < cols) ? r0 + rr : -1;
-            col[u] = v * L::VEC - mis;
-            e0[u] = off - mis + (size_t)v * L::VEC;
-            if (row[u] >= 0) {
-                if (col[u] >= 0 && col[u] + L::VEC <= cols) {
-                    raw[u] = __ldcs(reinterpret_cast<const uint4 *>(A.logits) + e0[u] / L::VEC);
-                } else {
-                    raw[u] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int j = 0; j < L::VEC; ++j)
-                        if (col[u] + j >= 0 && col[u] + j < cols) {
-                            if (DT == SPEC_F32)
-                                L::put(raw[u], j, reinterpret_cast<const uint32_t *>(A.logits)[e0[u] + j]);
-                            else
-                                L::put(raw[u], j, reinterpret_cast<const unsigned short *>(A.logits)[e0[u] + j]);
-                        }
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < LUN; ++u) {
-            if (row[u] < 0)
-                continue;
-            const int c = col[u], lo = max(c, 0), skip = lo - c;  // skip: elements before the tile
-            constexpr uint32_t ALL = (1u << L::VEC) - 1u;
-            const int n = min(cols - lo, L::VEC - skip);
-            const uint32_t have = ((n >= 32 ? 0u : (1u << n)) - 1u) << skip;
-            if (bad) {
-                raw[u] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-            } else {
-                uint32_t t = (bits_from(S.touched, lo) << skip) & have;
-                uint32_t ok = ALL;
-                if (A.allowed) {
-                    const uint32_t *m = A.allowed + b * A.allowed_stride_b +
-                                        row[u] * A.allowed_stride_r;
-                    ok = (mask_from(m, t0 + lo, n, last_word) << skip) & have;
-                    t &= ok;
-                }
-                touch<DT>(A, S, t0, c, row[u], t, pen, raw[u]);
-                if (ok != ALL)
-                    forbid<DT>(raw[u], ok);
-            }
-            if (have == ALL) {
-                reinterpret_cast<uint4 *>(A.out)[e0[u] / L::VEC] = raw[u];
-            } else {
-                const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-#pragma unroll
-                for (int j = 0; j < L::VEC; ++j)
-                    if ((have >> j) & 1u) {
-                        if (DT == SPEC_F32)
-                            reinterpret_cast<uint32_t *>(A.out)[e0[u] + j] = w[j & 3];
-                        else
-                            reinterpret_cast<unsigned short *>(A.out)[e0[u] + j] =
-                                (unsigned short)(w[(j >> 1) & 3] >> ((j & 1) * 16));
-                    }
-            }
-        }
+    if (tid == 0) {
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (stuck)  // copies still in flight end first (bounded)
+            for (int st = 0; st < STAGES; ++st)
+                (void)mbar_wait(&full[st], 0u), (void)mbar_wait(&full[st], 1u);
     }
 }
 
@@ -463,35 +429,32 @@ bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) &
 
 size_t smem_bytes(const spec_process_logits_args &a, int C)
 {
-    return (4 * ((size_t)C + C / 32 + 1 + (a.bias_cols > 0 ? C : 0) + 2 * (size_t)a.R) + 15) / 16 * 16;
+    return (4 * ((size_t)C + 2 * (C / 32) + (a.bias_cols > 0 ? C : 0) + 2 * (size_t)a.R) + 15) / 16 * 16;
 }
 
 // the largest tile's words, bits, biases, drafts, list and fp32 stages
 constexpr size_t MOST_SMEM =
-    4 * (MOST_C + MOST_C / 32 + 1 + MOST_C + 2 * SPEC_LOGITS_MAX_ROWS) + 16 + MOST_C * 2 +
-    (size_t)STAGES * MOST_C * 4;
+    4 * (MOST_C + 2 * (MOST_C / 32) + MOST_C + 2 * SPEC_LOGITS_MAX_ROWS) + 16 + MOST_C * 2 +
+    (size_t)MOST_STAGES * (MOST_C * 4 + 16);
 static_assert(MOST_SMEM <= 232448 - 64, "227 KB per CTA");
-std::atomic<bool> g_attr[64][2];  // opted in, per device and dtype
+static_assert(SPEC_LOGITS_MAX_BIAS <= 32 * LTH, "a thread's bias entries in one word");
+std::atomic<bool> g_attr[64][2][2];  // opted in, per device, dtype and alignment
 
-template <int DT>
-int launch(const LParams &P, bool ring, dim3 grid, size_t smem, cudaStream_t st)
+template <int DT, bool ALIGNED>
+int launch(const LParams &P, dim3 grid, cudaStream_t st)
 {
-    if (!ring) {
-        logits_kernel<DT, false><<<grid, LTH, smem, st>>>(P);
-        return SPEC_OK;
-    }
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
         return SPEC_ECUDA;
-    if (!g_attr[dev][DT].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(logits_kernel<DT, true>,
+    if (!g_attr[dev][DT][ALIGNED].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(logits_kernel<DT, ALIGNED>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)MOST_SMEM) != cudaSuccess)
             return SPEC_ECUDA;
-        g_attr[dev][DT].store(true, std::memory_order_release);
+        g_attr[dev][DT][ALIGNED].store(true, std::memory_order_release);
     }
-    logits_kernel<DT, true>
-        <<<grid, LTH, P.ring_at + (size_t)STAGES * P.C * Lg<DT>::ES, st>>>(P);
+    const size_t stage = (size_t)(P.C + Lg<DT>::VEC) * Lg<DT>::ES;
+    logits_kernel<DT, ALIGNED><<<grid, LTH, P.ring_at + stages<DT>() * stage, st>>>(P);
     return SPEC_OK;
 }
 
@@ -542,8 +505,11 @@ extern "C" int32_t spec_process_logits(const spec_process_logits_args *args, voi
     const dim3 grid((unsigned int)((a.V + P.C - 1) / P.C), (unsigned int)a.B,
                     (unsigned int)((a.R + P.rows_per_cta - 1) / P.rows_per_cta));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const int rc = a.dtype == SPEC_F32 ? launch<SPEC_F32>(P, a.V % 4 == 0, grid, smem, st)
-                                       : launch<SPEC_BF16>(P, a.V % 8 == 0, grid, smem, st);
+    int rc;
+    if (a.dtype == SPEC_F32)
+        rc = a.V % 4 == 0 ? launch<SPEC_F32, true>(P, grid, st) : launch<SPEC_F32, false>(P, grid, st);
+    else
+        rc = a.V % 8 == 0 ? launch<SPEC_BF16, true>(P, grid, st) : launch<SPEC_BF16, false>(P, grid, st);
     if (rc != SPEC_OK) {
         (void)cudaGetLastError();
         return rc;
