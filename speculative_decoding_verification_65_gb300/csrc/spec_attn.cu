@@ -364,29 +364,14 @@ __device__ __forceinline__ bool warp_try2(unsigned long long *a, uint32_t pa,
     return any;
 }
 
-// The wait for a barrier that was not ready at once; `sleep_ns` between the tests.
-__device__ __forceinline__ bool wait_long(unsigned long long *bar, uint32_t parity,
-                                          volatile int *abort_flag, int *status,
-                                          unsigned int sleep_ns)
+// Tests of a barrier before a wait gives up.  A test that fails takes 50 ns at least (the
+// hardware holds it a while), so this is 0.2 s at least and seconds at most.
+constexpr int WAIT_TRIES = 1 << 22;
+
+__device__ __forceinline__ void give_up(volatile int *abort_flag, int *status)
 {
-    const unsigned long long t0 = globaltimer();
-    while (true) {
-#pragma unroll 1
-        for (int i = 0; i < 32; ++i) {
-            if (warp_try(bar, parity))
-                return true;
-            if (sleep_ns)
-                __nanosleep(sleep_ns);
-        }
-        bool stop = *abort_flag != 0;
-        if (globaltimer() - t0 > WAIT_NS) {
-            atomicExch(status, SPEC_DEV_WAIT_TIMEOUT);
-            *abort_flag = 1;
-            stop = true;
-        }
-        if (__any_sync(0xffffffffu, stop))
-            return false;
-    }
+    atomicExch(status, SPEC_DEV_WAIT_TIMEOUT);
+    *abort_flag = 1;
 }
 
 // Shared-memory matrix descriptors, 128-byte swizzle (version 1, mode 2).
@@ -726,13 +711,31 @@ __global__ void __launch_bounds__(THREADS, 1)
     wait_previous_kernel();
     allow_next_kernel();
 
-    // a warp's wait: false on every lane once the CTA has given up
+    // A warp's wait: false on every lane once the CTA has given up.  (Kept this small: the
+    // waits stand in every role's loop, and the loops share an instruction cache.)
     auto wait = [&](unsigned long long *bar, uint32_t parity) -> bool {
-        return warp_try(bar, parity) || wait_long(bar, parity, abort_flag, P.status, 0);
+#pragma unroll 1
+        for (int i = 0; i < WAIT_TRIES; ++i) {
+            if (warp_try(bar, parity))
+                return true;
+            if (*abort_flag)
+                return false;
+        }
+        give_up(abort_flag, P.status);
+        return false;
     };
     // the same for a warp that has time: it sleeps between its tests
     auto wait_idle = [&](unsigned long long *bar, uint32_t parity) -> bool {
-        return warp_try(bar, parity) || wait_long(bar, parity, abort_flag, P.status, 100);
+#pragma unroll 1
+        for (int i = 0; i < WAIT_TRIES; ++i) {
+            if (warp_try(bar, parity))
+                return true;
+            if (*abort_flag)
+                return false;
+            __nanosleep(100);
+        }
+        give_up(abort_flag, P.status);
+        return false;
     };
     // the next piece of the share: false when there is none or the CTA has given up
     uint32_t taken = 0;
