@@ -21,23 +21,24 @@ PROMPTS = [[5, 17, 3, 40], [9], [1, 2, 3, 4, 5, 6, 7], [60, 61]]
 
 
 def plain_logits(model, text):
-    """The model over one text in 64 bits."""
+    """The model over one text in 64 bits, on the CPU."""
+    text = text.cpu()
     wide = ts.Model.__new__(ts.Model)
     wide.__dict__.update(model.__dict__)
     for name in ("embed", "place", "head"):
-        setattr(wide, name, getattr(model, name).double())
-    wide.layers = [{k: v.double() for k, v in layer.items()} for layer in model.layers]
+        setattr(wide, name, getattr(model, name).cpu().double())
+    wide.layers = [{k: v.cpu().double() for k, v in layer.items()} for layer in model.layers]
     wide.norm = lambda x: x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-6)
     n = len(text)
     G = model.heads // model.kv_heads
-    mask = torch.ones((n, n), dtype=torch.bool, device="cuda").triu(1)
+    mask = torch.ones((n, n), dtype=torch.bool).triu(1)
 
     def attend(i, q, k, v):
         k, v = k.repeat_interleave(G, 1), v.repeat_interleave(G, 1)
         s = torch.einsum("ihd,jhd->hij", q, k) / model.head_dim ** 0.5
         p = torch.softmax(s.masked_fill(mask, float("-inf")), -1)
         return torch.einsum("hij,jhd->ihd", p, v)
-    x = wide.embed[text] + wide.place[torch.arange(n, device="cuda")]
+    x = wide.embed[text] + wide.place[torch.arange(n)]
     for i, layer in enumerate(wide.layers):
         qkv = (wide.norm(x) @ layer["qkv"].T).unflatten(-1, (model.heads + 2 * model.kv_heads, 64))
         h, kv = model.heads, model.kv_heads
@@ -56,7 +57,7 @@ def test_greedy_trees_emit_the_targets_own_tokens(parent):
         assert int(n.min()) >= 1
     assert torch.equal(dec.length, dec.text_len - 1)
     for b, prompt in enumerate(PROMPTS):
-        text = dec.history[b, :int(dec.text_len[b])].long()
+        text = dec.history[b, :int(dec.text_len[b])].long().cpu()
         logits = plain_logits(model, text)
         for i in range(len(prompt), len(text)):
             row = logits[i - 1]
