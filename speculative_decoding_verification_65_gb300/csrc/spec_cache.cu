@@ -23,6 +23,8 @@
 #include <limits.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "spec_attn.h"
 #include "spec_verify.h"
 #include "attn_plan.cuh"
@@ -179,6 +181,11 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PlanParams P)
     }
 }
 
+constexpr size_t plan_smem(int N) { return (size_t)N * ((N + 31) / 32) * 4; }
+static_assert(plan_smem(SPEC_ATTN_MAX_NODES) <= 232448 - 1024, "227 KB per CTA");
+
+std::atomic<bool> g_plan_attr[64];  // opted in, per device
+
 // ----------------------------------------------------------------- commit
 
 struct CommitParams {
@@ -302,14 +309,21 @@ int32_t spec_tree_plan(const int32_t *parent, const int32_t *n_nodes, const int3
     P.plan = static_cast<uint8_t *>(plan);
     const int NW = (N + 31) / 32;
     const int threads = NW < 4 ? 128 : NW * 32;
-    const size_t smem = (size_t)N * NW * 4;  // 128 KB at 1024 nodes
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem) != cudaSuccess) {
-        (void)cudaGetLastError();
+    // The limit belongs to the function, so one for every size: another thread's call may
+    // come between a call's own and its launch.  (48 KB without it hold the static part too.)
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
         return SPEC_ECUDA;
+    if (!g_plan_attr[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)plan_smem(SPEC_ATTN_MAX_NODES)) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return SPEC_ECUDA;
+        }
+        g_plan_attr[dev].store(true, std::memory_order_release);
     }
-    plan_kernel<<<(unsigned int)B + 1, threads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(P);
+    plan_kernel<<<(unsigned int)B + 1, threads, plan_smem(N),
+                  reinterpret_cast<cudaStream_t>(stream)>>>(P);
     if (cudaPeekAtLastError() != cudaSuccess) {
         (void)cudaGetLastError();
         return SPEC_ECUDA;
