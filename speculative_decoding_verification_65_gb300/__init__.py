@@ -1127,12 +1127,20 @@ def spec_tree_attention_workspace_size(N: int, Hq: int, Hkv: int, D: int) -> int
     return int(library().spec_tree_attention_workspace_size(N, Hq, Hkv, D))
 
 
-_attention_ws = {}
+class _Workspaces(threading.local):
+    """One host thread's workspaces by (device, stream).  Calls on a stream run in
+    order, but a call is several kernels, and another thread's may come between them."""
+
+    def __init__(self):
+        self.of = {}
+
+
+_attention_ws = _Workspaces()
 
 
 def attention_workspace(N: int, Hq: int, Hkv: int, D: int, device=None, stream=None):
-    """A workspace for spec_tree_attention, cached per (device, stream) and
-    apart from spec_verify's.  While the stream is being captured into a
+    """A workspace for spec_tree_attention, cached per (host thread, device, stream)
+    and apart from spec_verify's.  While the stream is being captured into a
     graph it is a new one, in the graph's own memory: a replay may overlap
     later calls on the stream."""
     torch = _torch()
@@ -1154,9 +1162,9 @@ def _attention_workspace(N, Hq, Hkv, D, device, h, s):
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(need, dtype=torch.uint8, device=device)
     key = (device.index, h)
-    ws = _attention_ws.get(key)
+    ws = _attention_ws.of.get(key)
     if ws is None or ws.numel() < need:
-        ws = _attention_ws[key] = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = _attention_ws.of[key] = torch.empty(need, dtype=torch.uint8, device=device)
     return ws
 
 
@@ -1167,7 +1175,8 @@ def spec_tree_attention(q, k_new, v_new, k_cache, v_cache, plan, page_table=None
     q [B, N, Hq, D]; k_new, v_new [B, N, Hkv, D]: the new tokens' keys and
     values; k_cache, v_cache [pages, slots, Hkv, D], bfloat16 or float16, any
     strides with a contiguous last dimension; plan from spec_tree_plan;
-    page_table int32 [B, pages_per_seq] or None; scale 1 / sqrt(D) by default.
+    page_table int32 [B, pages_per_seq] or None; scale 1 / sqrt(D) by default;
+    ws of one call at a time, by default this thread's (attention_workspace).
     Returns out [B, N, Hq, D] and, with want_lse, the rows' log-sum-exp
     float32 [B, N, Hq]; asynchronous like any CUDA op."""
     torch = _torch()

@@ -1,8 +1,10 @@
 """Refusals of the serving operators (tree attention, its plan, the cache
 commit, logits processing), in the library and in the binding, on the CPU:
 every call here returns before any CUDA runtime call."""
+import contextlib
 import ctypes
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -274,3 +276,45 @@ def test_restatements_on_worked_examples():
     pos, status, mask = su.plan_ref(np.array([[-1, 0, 0, 1], [-1, 1, 0, 0]]), [4, 2], [10, 0], 20)
     assert pos.tolist() == [[10, 11, 11, 12], [-1] * 4] and status.tolist() == [0, -1]
     assert mask[0, :, 0].tolist() == [1, 3, 5, 11]
+
+
+# ------------------------------------------- workspaces, lengths, empty plans
+
+class _FakeTorch:
+    """What the workspace caches use of torch, without a GPU."""
+    uint8 = torch.uint8
+
+    class cuda:
+        @staticmethod
+        def is_current_stream_capturing():
+            return False
+
+        @staticmethod
+        def stream(s):
+            return contextlib.nullcontext()
+
+    @staticmethod
+    def empty(n, dtype, device):
+        return torch.empty(n, dtype=dtype)
+
+    zeros = empty
+
+
+def _by_threads(call):
+    """call() twice in this thread and twice in another one."""
+    other = []
+    t = threading.Thread(target=lambda: other.extend([call(), call()]))
+    t.start()
+    t.join()
+    return [call(), call()], other
+
+
+def test_attention_workspace_belongs_to_one_thread(lib, monkeypatch):
+    """A call's two kernels hand partial sums over in it, and another thread's call on the same
+    stream may come between them."""
+    monkeypatch.setattr(sv, "_torch", lambda: _FakeTorch)
+    dev = torch.device("cuda:0")
+    (a, b), (c, d) = _by_threads(lambda: sv._attention_workspace(4, 8, 2, 64, dev, 7, None))
+    assert a is b and c is d and a is not c
+    assert sv._attention_workspace(4, 8, 2, 64, dev, 8, None) is not a
+    assert sv._attention_workspace(4, 8, 2, 64, dev, 7, None) is a

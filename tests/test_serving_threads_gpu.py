@@ -59,3 +59,35 @@ def test_plans_of_any_size_in_a_fresh_process(sizes, repeats):
     run = subprocess.run([sys.executable, "-c", CHILD, sizes, str(repeats)], cwd=ROOT, env=env,
                          capture_output=True, text=True, timeout=300)
     assert run.returncode == 0, run.stdout[-1000:] + run.stderr[-2000:]
+
+
+def test_attention_from_threads_on_one_stream():
+    """Threads, each with its own inputs, call on the same stream; what a call's first kernel
+    leaves for its second is not the other thread's."""
+    jobs = []
+    for seed in range(4):
+        c = make(2, 5, 2, 4, 64, 16, 4000, BF16, seed=seed, lens=[4000, 3000], nodes=[5])
+        d = {k: dev(v) for k, v in c.items()}
+        plan = sv.spec_tree_plan(d["parent"], d["n_nodes"], d["cache_len"], d["k_cache"],
+                                 page_table=d["table"])
+        args = (d["q"], d["k_new"], d["v_new"], d["k_cache"], d["v_cache"], plan, d["table"])
+        jobs.append((args, sv.spec_tree_attention(*args)))
+    torch.cuda.synchronize()
+    gate, wrong = threading.Barrier(len(jobs)), []
+
+    def work(i):
+        args, want = jobs[i]
+        gate.wait()
+        outs = [sv.spec_tree_attention(*args) for _ in range(2000)]
+        wrong.append(sum(not torch.equal(out, want) for out in outs))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    interval = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(interval)
+    assert wrong == [0] * len(jobs)
