@@ -233,13 +233,21 @@ def spec_verify_host_arena_size(B: int, k: int, V: int, dtype: int) -> int:
     return int(library().spec_verify_host_arena_size(B, k, V, dtype))
 
 
-_ws_cache = {}
+class _Workspaces(threading.local):
+    """One host thread's workspaces by (device, stream).  Calls on a stream run in
+    order, but a call is several kernels, and another thread's may come between them."""
+
+    def __init__(self):
+        self.of = {}
+
+
+_ws_cache = _Workspaces()
 
 
 def workspace(B: int, k: int, V: int, dtype: int, device=None, stream=None):
     """A zeroed workspace tensor big enough for these sizes, cached per
-    (device, stream): calls in flight on one stream run in order, so they can
-    share it."""
+    (host thread, device, stream): a thread's calls in flight on one stream run
+    in order, so they can share it."""
     torch = _torch()
     device = torch.device(device if device is not None else "cuda")
     if device.index is None:
@@ -272,11 +280,11 @@ def filtered_workspace(B: int, k: int, V: int, dtype: int, device=None, stream=N
 def _cached_workspace(need: int, device, s):
     torch = _torch()
     key = (device.index, s.cuda_stream)
-    ws = _ws_cache.get(key)
+    ws = _ws_cache.of.get(key)
     if ws is None or ws.numel() < need:
         with torch.cuda.stream(s):
             ws = torch.zeros(max(need, 1 << 20), dtype=torch.uint8, device=device)
-        _ws_cache[key] = ws
+        _ws_cache.of[key] = ws
     return ws
 
 
@@ -1125,14 +1133,6 @@ def spec_tree_plan(parent, n_nodes, cache_len, k_cache, page_table=None, plan=No
 @functools.lru_cache(maxsize=256)
 def spec_tree_attention_workspace_size(N: int, Hq: int, Hkv: int, D: int) -> int:
     return int(library().spec_tree_attention_workspace_size(N, Hq, Hkv, D))
-
-
-class _Workspaces(threading.local):
-    """One host thread's workspaces by (device, stream).  Calls on a stream run in
-    order, but a call is several kernels, and another thread's may come between them."""
-
-    def __init__(self):
-        self.of = {}
 
 
 _attention_ws = _Workspaces()

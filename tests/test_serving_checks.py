@@ -318,3 +318,10 @@ def test_attention_workspace_belongs_to_one_thread(lib, monkeypatch):
     assert a is b and c is d and a is not c
     assert sv._attention_workspace(4, 8, 2, 64, dev, 8, None) is not a
     assert sv._attention_workspace(4, 8, 2, 64, dev, 7, None) is a
+
+
+def test_verification_workspace_belongs_to_one_thread(lib, monkeypatch):
+    monkeypatch.setattr(sv, "_torch", lambda: _FakeTorch)
+    dev, stream = torch.device("cuda:0"), type("Stream", (), {"cuda_stream": 7})()
+    (a, b), (c, d) = _by_threads(lambda: sv._cached_workspace(1000, dev, stream))
+    assert a is b and c is d and a is not c
