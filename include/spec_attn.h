@@ -90,7 +90,9 @@ int32_t spec_tree_plan(const int32_t *parent, const int32_t *n_nodes, const int3
  * and positive; page_size a multiple of 128, or a power of two from 8, or, without a page
  * table, anything.  Base addresses 16-byte aligned, strides multiples of 8 elements.
  * Scores, the softmax's statistics and the weighted sum are held in fp32;
- * each weight is rounded to the dtype before its product with v.
+ * each weight is rounded to the dtype before its product with v (SPEC_F16: in
+ * units of 2^-11 of the row's largest weight or less, so weights down to 2^-25
+ * of it keep all of their bits).
  * The workspace has spec_tree_attention_workspace_size bytes (0 for sizes out
  * of range), 256-byte aligned; it need not be cleared, and calls in flight
  * must not share it.  Up to two kernels on `stream`, no allocation.

@@ -31,8 +31,9 @@
 // TMEM: S_0, S_1 (128 columns each), O_0, O_1 (up to 128 each).
 //
 // A row's sums are rescaled only when its maximum has grown by more than 2^8
-// since the last time (all of the statistics are fp32, so the larger weights
-// in between lose nothing); most tiles then leave O in TMEM alone.
+// (2^4 with fp16 weights) since the last time (all of the statistics are fp32,
+// so the larger weights in between lose nothing); most tiles then leave O in
+// TMEM alone.
 //
 // Work: the key tiles of all sequences, heads and row groups that hold a node (a
 // row tile, or a pair) stand in a line and are dealt to the CTAs in equal runs,
@@ -82,7 +83,16 @@ constexpr int THREADS = SOFT_THREADS + 128;
 constexpr int SOFT_REGS = 208, HELPER_REGS = 88;
 constexpr int MAX_CTAS = 192;     // the grid's and the workspace's bound
 constexpr int RING = 4;           // pieces handed out ahead
-constexpr float GROWTH = 8.0f;    // log2 of how far a maximum may run ahead of the sums' scale
+// log2 of how far a maximum may run ahead of the sums' scale, and of the weight that the scale gives
+// it.  bf16 weights have fp32's exponents.  fp16 ones lose bits below 2^-14 and vanish below
+// 2^-25, so their scale puts the maximum at 2^11 (2^15 ahead of the scale): weights keep all of
+// their bits down to 2^-25 of it, where with 2^0 they had vanished while the total
+// counted them.  The constant cancels in the division; it and the earlier rescaling cost nothing
+// to speak of (4 trees of up to 256 nodes over up to 16384 positions in fp16: 279 to 280 us).
+template <int DT>
+__host__ __device__ constexpr float growth() { return DT == SPEC_BF16 ? 8.0f : 4.0f; }
+template <int DT>
+__host__ __device__ constexpr float lift() { return DT == SPEC_BF16 ? 0.0f : 11.0f; }
 
 // PAIR: a CTA has two row tiles, one for each softmax group, over the same keys.
 template <int NP, bool PAIR>
@@ -147,7 +157,7 @@ struct AParams {
     float *lse;
     int *status;
     float *part;     // [ctas][Q_TILES][2][DP][BM] unnormalised sums of split items
-    float2 *part_ml; // [ctas][Q_TILES][2][BM] (maximum in log2 units, total)
+    float2 *part_ml; // [ctas][Q_TILES][2][BM] (log2 of the weights' unit, total)
     float c;         // scale * log2(e)
     int B, N, Hq, Hkv, D, G;
     int nodes_per_tile;
@@ -768,6 +778,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t cnt = 0, tv = 0, done = 0;      // the group's tiles, all tiles, reports of O
         uint32_t joins = 0, notes = 0;
         const unsigned long long c2 = f2(P.c, P.c);
+        // a score x has weight 2^(x c + shift) under the maximum m
+        auto shift_of = [&](float m) -> float {
+            return m == -INFINITY ? 0.0f : fmaf(-m, P.c, lift<DT>());
+        };
         // all softmax warps have come here
         auto join = [&]() -> bool {
             __syncwarp();
@@ -897,7 +911,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         m = top;
                         return;
                     }
-                    const bool grown = (top - m) * P.c > GROWTH;  // -inf to finite too
+                    const bool grown = (top - m) * P.c > growth<DT>();  // -inf to finite too
                     if (!__any_sync(0xffffffffu, grown))
                         return;
                     const float f = grown ? ex2((m - top) * P.c) : 1.0f;
@@ -922,7 +936,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (PAIR && warp_live && !redo) {
                     // in one pass: weights by the maximum so far, which serves as long as no
                     // score is far above it; the tile's own maximum is found on the way
-                    const float shift = m == -INFINITY ? 0.0f : -m * P.c;
+                    const float shift = shift_of(m);
                     const unsigned long long shift2 = f2(shift, shift);
                     uint32_t x[32], y[32], pk[4][16];
                     __syncwarp();
@@ -942,7 +956,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tmem_ld_finish(y);
                     top = fmaxf(top, max32(y));
                     weigh<DT>(y, c2, shift2, sum, pk[3]);
-                    redo = __any_sync(0xffffffffu, (top - m) * P.c > GROWTH);  // -inf to finite too
+                    redo = __any_sync(0xffffffffu,
+                                      (top - m) * P.c > growth<DT>());  // -inf to finite too
                     if (!redo) {
 #pragma unroll
                         for (int h = 0; h < 4; ++h)
@@ -968,7 +983,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         top = fmaxf(top, max32(x));
                     }
                     raise(top);
-                    const float shift = m == -INFINITY ? 0.0f : -m * P.c;
+                    const float shift = shift_of(m);
                     const unsigned long long shift2 = f2(shift, shift);
 #pragma unroll 1
                     for (int h = 0; h < chunks; ++h) {
@@ -1065,7 +1080,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (mine && !wait(&S.pvdone[s], (done - 1) & 1u))
                 break;
             tc_fence_after();
-            float top = mine && m != -INFINITY ? m * P.c : -INFINITY;
+            float top = mine && m != -INFINITY ? -shift_of(m) : -INFINITY;
             float sum = mine ? l : 0.0f;
             // a half that saw no key has no weight, whatever its O holds
             bool some0 = !(top == -INFINITY && sum == 0.0f), some1 = false;
@@ -1553,7 +1568,7 @@ constexpr int JOIN_WARPS = 8;
 constexpr int JOIN_ROWS = 32;
 constexpr int JOIN_UNROLL = 2;    // pieces whose sums a thread has in flight
 
-// The running (maximum in log2 units, total, sums) of some pieces of one row.
+// The running (log2 of the weights' unit, total, sums) of some pieces of one row.
 template <int COLS>
 struct Joined {
     float top = -INFINITY, sum = 0.0f;
