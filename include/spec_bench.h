@@ -10,6 +10,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "spec_attn.h"
+
 #ifdef __cplusplus
 extern "C" {
 #endif
@@ -47,6 +49,18 @@ int32_t spec_selftest_wait_timeout(void *workspace, uint64_t limit_ns, void *str
  * scratch's address cannot be looked up.
  */
 int32_t spec_selftest_wait_timeout_noalloc(uint64_t limit_ns, void *stream);
+
+/*
+ * Self-test of tree attention's failure detection: spec_tree_attention, but the warp of
+ * CTA `cta` that hands out its pieces of work waits, once it has handed out `after` of them,
+ * on an mbarrier that nothing arrives at, with a limit of 64 tests, and gives
+ * up.  The CTA's other warps then end their waits, and the plan's status word
+ * reads SPEC_DEV_WAIT_TIMEOUT (OK if the CTA has no such piece).  No fault and
+ * no hang.  `cta` and `after` from 0; results otherwise as spec_tree_attention's.
+ */
+int32_t spec_selftest_attention_timeout(const spec_tree_attention_args *args, void *workspace,
+                                        size_t workspace_bytes, int32_t cta, int32_t after,
+                                        void *stream);
 
 #ifdef __cplusplus
 }

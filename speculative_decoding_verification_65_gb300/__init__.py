@@ -176,6 +176,8 @@ def library():
         lib.spec_tree_attention_workspace_size.argtypes = [i32] * 4
         lib.spec_tree_attention.restype = i32
         lib.spec_tree_attention.argtypes = [vp, vp, sz, vp]
+        lib.spec_selftest_attention_timeout.restype = i32
+        lib.spec_selftest_attention_timeout.argtypes = [vp, vp, sz, i32, i32, vp]
         lib.spec_tree_commit.restype = i32
         lib.spec_tree_commit.argtypes = [vp, vp]
         lib.spec_process_logits.restype = i32

@@ -64,6 +64,7 @@
 #include <atomic>
 
 #include "spec_attn.h"
+#include "spec_bench.h"
 #include "spec_verify.h"
 #include "attn_plan.cuh"
 #include "device_common.cuh"
@@ -167,6 +168,7 @@ struct AParams {
     int page_rows;   // rows of a cache box: min(128, page_size) (contiguous: 128)
     int new_rows;    // rows of a box of new tokens
     int q_rows;      // rows of the Q box
+    int lose, lose_after;  // the self-test's CTA (-1: none) and the pieces that it hands out first
 };
 
 // ------------------------------------------------------------ PTX wrappers
@@ -377,6 +379,7 @@ __device__ __forceinline__ bool warp_try2(unsigned long long *a, uint32_t pa,
 // Tests of a barrier before a wait gives up.  A test that fails takes 50 ns at least (the
 // hardware holds it a while), so this is 0.2 s at least and seconds at most.
 constexpr int WAIT_TRIES = 1 << 22;
+constexpr int LOSE_TRIES = 1 << 6;  // the self-test's
 
 __device__ __forceinline__ void give_up(volatile int *abort_flag, int *status)
 {
@@ -721,6 +724,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     wait_previous_kernel();
     allow_next_kernel();
 
+    // Whether the CTA has given up, the same on every lane: lanes that each looked for
+    // themselves could part, and wait for each other in the next test for good.  (The vote costs 1 %
+    // of 32 chains of 5, 0.6 % of 4 trees of 256 nodes; one vote for flag and barrier, or
+    // one sum, in the same instruction cost 1.5 and 4 % there.)
+    auto given_up = [&]() -> bool { return __any_sync(0xffffffffu, *abort_flag != 0); };
     // A warp's wait: false on every lane once the CTA has given up.  (Kept this small: the
     // waits stand in every role's loop, and the loops share an instruction cache.)
     auto wait = [&](unsigned long long *bar, uint32_t parity) -> bool {
@@ -728,19 +736,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < WAIT_TRIES; ++i) {
             if (warp_try(bar, parity))
                 return true;
-            if (*abort_flag)
+            if (given_up())
                 return false;
         }
         give_up(abort_flag, P.status);
         return false;
     };
-    // the same for a warp that has time: it sleeps between its tests
-    auto wait_idle = [&](unsigned long long *bar, uint32_t parity) -> bool {
+    // the same for a warp that has time, with a limit of its own: it sleeps between its tests
+    auto wait_idle = [&](unsigned long long *bar, uint32_t parity, int tries) -> bool {
 #pragma unroll 1
-        for (int i = 0; i < WAIT_TRIES; ++i) {
+        for (int i = 0; i < tries; ++i) {
             if (warp_try(bar, parity))
                 return true;
-            if (*abort_flag)
+            if (given_up())
                 return false;
             __nanosleep(100);
         }
@@ -1471,7 +1479,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     t0 += (uint32_t)p.n;
                 }
             }
-            if (*abort_flag && issued) {  // the products in flight complete (bounded)
+            if (issued && given_up()) {  // the products in flight complete (bounded)
                 if (elect_one())
                     mma_commit(&S.drain);
                 __syncwarp();
@@ -1484,7 +1492,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             while (next(p)) {
                 if (p.idle)
                     continue;
-                if (!wait_idle(&S.qempty, (items & 1u) ^ 1u))
+                if (!wait_idle(&S.qempty, (items & 1u) ^ 1u, WAIT_TRIES))
                     break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&S.qfull,
@@ -1517,7 +1525,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             for (uint32_t k = 0;; ++k) {
                 const int at = (int)(k % RING);
-                if (!wait_idle(&S.pempty[at], ((k / RING) & 1u) ^ 1u))
+                // (the self-test: a wait for what nothing brings, with a small limit)
+                const bool lose = slot == P.lose && (int)k == P.lose_after;
+                if (!wait_idle(lose ? &S.drain : &S.pempty[at], lose ? 0u : ((k / RING) & 1u) ^ 1u,
+                               lose ? LOSE_TRIES : WAIT_TRIES))
                     break;
                 const long long left = u1 - u;
                 const int n = left <= 0 ? 0 : q.tiles - tile < left ? q.tiles - tile : (int)left;
@@ -1853,8 +1864,8 @@ size_t spec_tree_attention_workspace_size(int32_t N, int32_t Hq, int32_t Hkv, in
     return heads_ok(N, Hq, Hkv, D) ? ws_layout(N, Hq / Hkv, D).total : 0;
 }
 
-int32_t spec_tree_attention(const spec_tree_attention_args *args, void *workspace,
-                            size_t workspace_bytes, void *stream)
+static int32_t attend(const spec_tree_attention_args *args, void *workspace,
+                      size_t workspace_bytes, int lose, int lose_after, void *stream)
 {
     if (!args)
         return SPEC_EINVAL;
@@ -1917,6 +1928,8 @@ int32_t spec_tree_attention(const spec_tree_attention_args *args, void *workspac
     P.page_rows = paged && a.page_size < KT ? a.page_size : KT;
     P.new_rows = a.N < KT ? (a.N + 7) / 8 * 8 : KT;
     P.q_rows = P.nodes_per_tile * G;
+    P.lose = lose;
+    P.lose_after = lose_after;
 
     CUtensorMap maps[5];
     const uint64_t qd[5] = {(uint64_t)a.D, (uint64_t)G, (uint64_t)a.N, (uint64_t)a.Hkv,
@@ -1969,6 +1982,21 @@ int32_t spec_tree_attention(const spec_tree_attention_args *args, void *workspac
                     : launch<2, SPEC_F16, false>(maps, P, sms, di, st);
     return pair ? launch<1, SPEC_F16, true>(maps, P, sms, di, st)
                 : launch<1, SPEC_F16, false>(maps, P, sms, di, st);
+}
+
+int32_t spec_tree_attention(const spec_tree_attention_args *args, void *workspace,
+                            size_t workspace_bytes, void *stream)
+{
+    return attend(args, workspace, workspace_bytes, -1, 0, stream);
+}
+
+int32_t spec_selftest_attention_timeout(const spec_tree_attention_args *args, void *workspace,
+                                        size_t workspace_bytes, int32_t cta, int32_t after,
+                                        void *stream)
+{
+    if (cta < 0 || after < 0)
+        return SPEC_EINVAL;
+    return attend(args, workspace, workspace_bytes, cta, after, stream);
 }
 
 }  // extern "C"

@@ -5,8 +5,9 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+import speculative_decoding_verification_65_gb300 as sv  # noqa: E402
 from tests import attn_ref as ar  # noqa: E402
-from tests.test_attn_gpu import FP16, make, run  # noqa: E402
+from tests.test_attn_gpu import BF16, FP16, dev, make, run  # noqa: E402
 
 gpu = pytest.mark.gpu
 
@@ -38,3 +39,52 @@ def test_small_weights_of_fp16_count(N, G, at):
     c["v_cache"] = (64 + 64 * torch.rand(c["v_cache"].shape, generator=gen)).to(FP16)
     c["k_cache"][0, at::ar.KT], c["v_cache"][0, at::ar.KT] = 0.0, 0.0
     check(c, scale=1.0)
+
+
+class Losing:
+    """The library, its tree attention with a CTA whose wait gives up (include/spec_bench.h)."""
+
+    def __init__(self, lib, cta, after):
+        self.lib, self.lose = lib, (cta, after)
+
+    def __getattr__(self, name):
+        return getattr(self.lib, name)
+
+    def spec_tree_attention(self, args, ws, size, stream):
+        return self.lib.spec_selftest_attention_timeout(args, ws, size, *self.lose, stream)
+
+
+def giving_up(monkeypatch, c, cta, after):
+    """(results without and with the lost wait, plan, results of a new plan afterwards)"""
+    d = {k: dev(v) for k, v in c.items()}
+
+    def call():
+        plan = sv.spec_tree_plan(d["parent"], d["n_nodes"], d["cache_len"], d["k_cache"],
+                                 page_table=d["table"])
+        got = sv.spec_tree_attention(d["q"], d["k_new"], d["v_new"], d["k_cache"], d["v_cache"],
+                                     plan, page_table=d["table"], want_lse=True)
+        torch.cuda.synchronize()
+        return got, plan
+    want, plan = call()
+    assert plan.read_status() == sv.SPEC_DEV_OK
+    with monkeypatch.context() as m:
+        m.setattr(sv, "_lib", Losing(sv.library(), cta, after))
+        got, lost = call()
+    again, plan = call()
+    assert plan.read_status() == sv.SPEC_DEV_OK
+    return want, got, lost, again
+
+
+# B = 6 of 1 or 2 row groups over up to 24 tiles and 2 heads: every CTA has a share
+LOSING = dict(B=6, Hkv=2, G=5, D=64, S=16, cap=3000, dtype=BF16, lens=[3000, 2222, 0, 2777])
+
+
+@gpu
+@pytest.mark.parametrize("N", [5, 60])
+@pytest.mark.parametrize("cta,after", [(0, 0), (7, 0)])
+def test_a_wait_that_gives_up_is_reported(monkeypatch, N, cta, after):
+    """The status is read, the GPU answers, and the next step is right again."""
+    c = make(N=N, seed=N, nodes=[N, 3, 0], **LOSING)
+    want, _, lost, again = giving_up(monkeypatch, c, cta, after)
+    assert lost.read_status() == sv.SPEC_DEV_WAIT_TIMEOUT
+    assert all(torch.equal(a, b) for a, b in zip(again, want))

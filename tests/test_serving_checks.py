@@ -325,3 +325,11 @@ def test_verification_workspace_belongs_to_one_thread(lib, monkeypatch):
     dev, stream = torch.device("cuda:0"), type("Stream", (), {"cuda_stream": 7})()
     (a, b), (c, d) = _by_threads(lambda: sv._cached_workspace(1000, dev, stream))
     assert a is b and c is d and a is not c
+
+
+def test_attention_selftest_refusals(lib):
+    ws = lib.spec_tree_attention_workspace_size(4, 8, 2, 64)
+    vp = ctypes.c_void_p
+    for cta, after, a in ((-1, 0, attention()), (0, -1, attention()), (0, 0, attention(q=0))):
+        assert lib.spec_selftest_attention_timeout(ctypes.byref(a), vp(A), ws, cta, after,
+                                                   None) == sv.SPEC_EINVAL
