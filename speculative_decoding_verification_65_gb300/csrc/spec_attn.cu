@@ -51,8 +51,8 @@
 //
 // Every mbarrier wait is bounded; one that gives up sets
 // SPEC_DEV_WAIT_TIMEOUT and the CTA's abort flag, after which no role waits
-// or issues any more, the loads and products in flight land (bounded again),
-// and TMEM is freed.
+// or issues any more.  When all have ended, the loads and products in flight
+// land (bounded again), and TMEM is freed.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -134,6 +134,7 @@ struct Tail {
     Piece piece[RING];
     uint32_t tmem_base;
     int abort_flag;
+    uint32_t loaded[3];  // loads that were issued when their warp ended: tiles of K, of V, and Qs
     uint32_t bad[2][2][4];  // keys of a group's tile (alternating) whose values are not all finite
     float m[2][BM], l[2][BM];
 };
@@ -1185,8 +1186,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (warp == 8) {
             // ------------------------------------------------ TMA of K and V
             uint32_t t0 = 0;                     // tiles of earlier pieces
-            uint32_t out_k = 0, out_v = 0;       // stages that a load was issued for,
-            uint32_t ph_k = 0, ph_v = 0;         // and the phase of the last one
+            uint32_t loaded_k = 0, loaded_v = 0; // tiles that a load was issued for
             bool ok = true;
             Piece p = {};
             // one tile's keys (side 0) or values (1): a box of rows per lane
@@ -1209,8 +1209,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 const uint32_t n = t0 + (uint32_t)i, stages = side ? C::VST : C::KST;
                 const int st = (int)(n % stages);
-                const uint32_t ph = (n / stages) & 1u;
-                ok = wait(side ? &S.vempty[st] : &S.kempty[st], ph ^ 1u);
+                ok = wait(side ? &S.vempty[st] : &S.kempty[st], ((n / stages) & 1u) ^ 1u);
                 if (!ok)
                     return;
                 unsigned long long *full = side ? &S.vfull[st] : &S.kfull[st];
@@ -1218,9 +1217,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     mbar_arrive_expect_tx(
                         full, (uint32_t)(((keys + rows - 1) / rows) * rows * 128 * NP));
                 __syncwarp();
-                uint32_t &out = side ? out_v : out_k, &out_ph = side ? ph_v : ph_k;
-                out |= 1u << st;
-                out_ph = (out_ph & ~(1u << st)) | (ph << st);
+                (side ? loaded_v : loaded_k) = n + 1;
                 if (mine) {
                     const CUtensorMap *map = cached ? (side ? &mvc : &mkc) : (side ? &mvn : &mkn);
                     const uint32_t dst =
@@ -1241,14 +1238,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 t0 += (uint32_t)p.n;
             }
-            if (*abort_flag) {
-                // the loads in flight land first: each barrier's last phase that has a load
-                for (int st = 0; st < 6; ++st) {
-                    if ((out_k >> st) & 1u)
-                        (void)mbar_wait(&S.kfull[st], (ph_k >> st) & 1u);
-                    if ((out_v >> st) & 1u)
-                        (void)mbar_wait(&S.vfull[st], (ph_v >> st) & 1u);
-                }
+            if (lane == 0) {
+                S.loaded[0] = loaded_k;
+                S.loaded[1] = loaded_v;
             }
         } else if (warp == 9) {
             // -------------------------------------------- issuer of the products
@@ -1256,7 +1248,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // are given then stays in uniform registers (issued from under `lane == 0` each
             // product took about 120 clocks to issue, twice its time in the tensor pipe).
             uint32_t items = 0;
-            bool ok = true, issued = false;
+            bool ok = true;
             const int ksteps = (P.D + 15) / 16;
             const uint32_t id_o = idesc<DT>(ksteps * 16, true);
             Piece p = {};
@@ -1307,7 +1299,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                         scored(s, i);
                     }
                     __syncwarp();
-                    issued = true;
                     if (s)
                         next_k();
                 };
@@ -1425,7 +1416,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                             mma_commit(&S.qempty);
                     }
                     __syncwarp();
-                    issued = true;
                 };
                 while (ok && next(p)) {
                     if (p.idle)
@@ -1468,7 +1458,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 mma_commit(&S.pvdone[s]);
                         }
                         __syncwarp();
-                        issued = true;
                         if (s)
                             ++cnt[1];
                         else
@@ -1478,12 +1467,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                     t0 += (uint32_t)p.n;
                 }
-            }
-            if (issued && given_up()) {  // the products in flight complete (bounded)
-                if (elect_one())
-                    mma_commit(&S.drain);
-                __syncwarp();
-                (void)mbar_wait(&S.drain, 0u);
             }
         } else if (warp == 10) {
             // ---------------------------------------------------- TMA of Q
@@ -1504,8 +1487,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 ++items;
             }
-            if (*abort_flag && items)
-                (void)mbar_wait(&S.qfull, (items - 1) & 1u);
+            if (lane == 0)
+                S.loaded[2] = items;
         } else {
             // ------------------------------------------- the share's pieces
             long long total = 0;
@@ -1567,6 +1550,25 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag) {
+        // Every role has ended, some perhaps before the one that gave up: what they left in flight
+        // lands first (bounded).  Each barrier's last phase that has a load, and the products.
+        if (warp == 8) {
+            for (int side = 0; side < 2; ++side) {
+                const uint32_t stages = side ? C::VST : C::KST, n = S.loaded[side];
+                for (uint32_t st = 0; st < stages && st < n; ++st)
+                    (void)mbar_wait(side ? &S.vfull[st] : &S.kfull[st], ((n - 1 - st) / stages) & 1u);
+            }
+        } else if (warp == 9) {
+            if (elect_one())
+                mma_commit(&S.drain);
+            __syncwarp();
+            (void)mbar_wait(&S.drain, 0u);
+        } else if (warp == 10 && S.loaded[2] > 0) {
+            (void)mbar_wait(&S.qfull, (S.loaded[2] - 1) & 1u);
+        }
+        __syncthreads();
+    }
     if (warp == 9) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");

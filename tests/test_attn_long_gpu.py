@@ -75,16 +75,17 @@ def giving_up(monkeypatch, c, cta, after):
     return want, got, lost, again
 
 
-# B = 6 of 1 or 2 row groups over up to 24 tiles and 2 heads: every CTA has a share
-LOSING = dict(B=6, Hkv=2, G=5, D=64, S=16, cap=3000, dtype=BF16, lens=[3000, 2222, 0, 2777])
+# 6 sequences of 1 or 2 row groups over up to 235 tiles and 2 heads: shares of a dozen tiles and more
+LOSING = dict(B=6, Hkv=2, G=5, S=16, cap=30000, dtype=BF16, lens=[30000, 22222, 0, 27777])
 
 
 @gpu
-@pytest.mark.parametrize("N", [5, 60])
-@pytest.mark.parametrize("cta,after", [(0, 0), (7, 0)])
-def test_a_wait_that_gives_up_is_reported(monkeypatch, N, cta, after):
-    """The status is read, the GPU answers, and the next step is right again."""
-    c = make(N=N, seed=N, nodes=[N, 3, 0], **LOSING)
+@pytest.mark.parametrize("N,D", [(5, 64), (60, 64), (60, 128)])
+@pytest.mark.parametrize("cta,after", [(0, 0), (7, 0), (0, 1), (9, 1)])
+def test_a_wait_that_gives_up_is_reported(monkeypatch, N, D, cta, after):
+    """The status is read, the GPU answers, and the next step is right again, whether the CTA has
+    nothing in flight (after 0) or loads and products of its first piece (after 1)."""
+    c = make(N=N, D=D, seed=N, nodes=[N, 3, 0], **LOSING)
     want, _, lost, again = giving_up(monkeypatch, c, cta, after)
     assert lost.read_status() == sv.SPEC_DEV_WAIT_TIMEOUT
     assert all(torch.equal(a, b) for a, b in zip(again, want))
