@@ -98,7 +98,8 @@ int32_t spec_tree_plan(const int32_t *parent, const int32_t *n_nodes, const int3
  * must not share it.  Up to two kernels on `stream`, no allocation.
  * A wait inside the kernel that gives up marks the plan:
  * spec_verify_read_status(plan, ..) reads SPEC_DEV_WAIT_TIMEOUT until the
- * plan is made again (SPEC_DEV_OK otherwise).
+ * plan is made again (SPEC_DEV_OK otherwise).  Rows that the CTA of that wait
+ * had a part in are then NaN, the other rows what they always are.
  */
 typedef struct spec_tree_attention_args {
     const void *q, *k_new, *v_new, *k_cache, *v_cache;

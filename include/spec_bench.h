@@ -54,9 +54,9 @@ int32_t spec_selftest_wait_timeout_noalloc(uint64_t limit_ns, void *stream);
  * Self-test of tree attention's failure detection: spec_tree_attention, but the warp of
  * CTA `cta` that hands out its pieces of work waits, once it has handed out `after` of them,
  * on an mbarrier that nothing arrives at, with a limit of 64 tests, and gives
- * up.  The CTA's other warps then end their waits, and the plan's status word
- * reads SPEC_DEV_WAIT_TIMEOUT (OK if the CTA has no such piece).  No fault and
- * no hang.  `cta` and `after` from 0; results otherwise as spec_tree_attention's.
+ * up.  The CTA's other warps then end their waits, the rows that it has a part
+ * in become NaN, and the plan's status word reads SPEC_DEV_WAIT_TIMEOUT (OK if
+ * the CTA has no such piece).  No fault and no hang.  `cta` and `after` from 0.
  */
 int32_t spec_selftest_attention_timeout(const spec_tree_attention_args *args, void *workspace,
                                         size_t workspace_bytes, int32_t cta, int32_t after,

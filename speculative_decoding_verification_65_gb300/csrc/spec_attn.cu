@@ -52,7 +52,8 @@
 // Every mbarrier wait is bounded; one that gives up sets
 // SPEC_DEV_WAIT_TIMEOUT and the CTA's abort flag, after which no role waits
 // or issues any more.  When all have ended, the loads and products in flight
-// land (bounded again), and TMEM is freed.
+// land (bounded again), the rows of the CTA's share become NaN, which the
+// verification reports, and TMEM is freed.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -628,6 +629,92 @@ __device__ __forceinline__ long long share(const AParams &P, long long total)
 {
     const long long per = (total + P.slots - 1) / P.slots;
     return per < 2 ? 2 : per;
+}
+
+// The pieces of a CTA's share, one after the other (a warp's walk, all lanes alike).
+template <bool PAIR>
+struct Walk {
+    Place q = {};
+    long long u0, u1, u;
+    int h = 0, rg = 0, tile = 0;
+
+    __device__ __forceinline__ Walk(const AParams &P, int slot)
+    {
+        long long total = 0;
+        u0 = look_up<PAIR>(P, [&](long long all) { return slot * share(P, all); }, total, q);
+        const long long per = share(P, total);
+        u1 = u0 + per < total ? u0 + per : total;
+        u = u0;
+        if (u < u1) {
+            const long long at = u - q.first;
+            const int item = (int)(at / q.tiles);
+            tile = (int)(at - (long long)item * q.tiles);
+            h = item / q.groups;
+            rg = item - h * q.groups;
+        }
+    }
+    __device__ __forceinline__ Piece piece() const
+    {
+        const long long left = u1 - u;
+        Piece p;
+        p.b = q.b;
+        p.h = h;
+        p.rt0 = rg * (PAIR ? 2 : 1);
+        p.last = rg == q.groups - 1;
+        p.tile0 = tile;
+        p.n = left <= 0 ? 0 : q.tiles - tile < left ? q.tiles - tile : (int)left;
+        p.tiles = q.tiles;
+        p.len = (int)q.seq.x;
+        p.nn = (int)q.seq.y;
+        p.status = (int)q.seq.z;
+        p.idle = p.nn <= 0;
+        p.first = u - tile <= u0;
+        return p;
+    }
+    __device__ __forceinline__ void go_on(const AParams &P, int n)
+    {
+        u += n;
+        tile = 0;
+        if (++rg == q.groups) {
+            rg = 0;
+            if (++h == P.Hkv) {
+                h = 0;
+                if (u < u1)
+                    q = place_at<PAIR>(P, q.b + 1, u);
+            }
+        }
+    }
+};
+
+// A CTA that has given up leaves NaN, not what memory held before: in the statistics of its
+// pieces of split items, whose rows the join then makes NaN, and in the rows that it was to
+// write itself.  By the softmax warps.
+template <int NP, bool PAIR>
+__device__ __noinline__ void void_share(const AParams &P, int slot, int tid)
+{
+    constexpr int TILES = Cfg<NP, PAIR>::Q_TILES;
+    for (int i = tid; i < TILES * 2 * BM; i += SOFT_THREADS)
+        P.part_ml[(size_t)slot * TILES * 2 * BM + i] = make_float2(NAN, NAN);
+    Walk<PAIR> walk(P, slot);
+    while (true) {
+        const Piece p = walk.piece();
+        if (p.n == 0)
+            break;
+        if (p.tile0 == 0) {
+            const int from = p.idle ? 0 : p.rt0 * P.nodes_per_tile;
+            const int to = p.idle || p.last ? P.N : min(P.N, (p.rt0 + TILES) * P.nodes_per_tile);
+            for (int y = tid; y < (to - from) * P.G; y += SOFT_THREADS) {
+                const int64_t row = ((int64_t)p.b * P.N + from + y / P.G) * P.Hq +
+                                    (int64_t)p.h * P.G + y % P.G;
+                for (int d = 0; d < P.D; d += 8)
+                    *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(P.out) + row * P.D + d) =
+                        make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+                if (P.lse)
+                    P.lse[row] = NAN;
+            }
+        }
+        walk.go_on(P, p.n);
+    }
 }
 
 // Among each 8 lanes, chunk k of lane i and chunk i of lane k change places.
@@ -1491,21 +1578,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 S.loaded[2] = items;
         } else {
             // ------------------------------------------- the share's pieces
-            long long total = 0;
-            Place q = {};
-            const long long u0 = look_up<PAIR>(
-                P, [&](long long all) { return slot * share(P, all); }, total, q);
-            const long long per = share(P, total);
-            const long long u1 = u0 + per < total ? u0 + per : total;
-            long long u = u0;
-            int h = 0, rg = 0, tile = 0;
-            if (u < u1) {
-                const long long at = u - q.first;
-                const int item = (int)(at / q.tiles);
-                tile = (int)(at - (long long)item * q.tiles);
-                h = item / q.groups;
-                rg = item - h * q.groups;
-            }
+            Walk<PAIR> walk(P, slot);
             for (uint32_t k = 0;; ++k) {
                 const int at = (int)(k % RING);
                 // (the self-test: a wait for what nothing brings, with a small limit)
@@ -1513,38 +1586,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!wait_idle(lose ? &S.drain : &S.pempty[at], lose ? 0u : ((k / RING) & 1u) ^ 1u,
                                lose ? LOSE_TRIES : WAIT_TRIES))
                     break;
-                const long long left = u1 - u;
-                const int n = left <= 0 ? 0 : q.tiles - tile < left ? q.tiles - tile : (int)left;
+                const Piece p = walk.piece();
                 if (lane == 0) {
-                    Piece p;
-                    p.b = q.b;
-                    p.h = h;
-                    p.rt0 = rg * C::Q_TILES;
-                    p.last = rg == q.groups - 1;
-                    p.tile0 = tile;
-                    p.n = n;
-                    p.tiles = q.tiles;
-                    p.len = (int)q.seq.x;
-                    p.nn = (int)q.seq.y;
-                    p.status = (int)q.seq.z;
-                    p.idle = p.nn <= 0;
-                    p.first = u - tile <= u0;
                     S.piece[at] = p;
                     mbar_arrive(&S.pfull[at]);
                 }
                 __syncwarp();
-                if (n == 0)
+                if (p.n == 0)
                     break;
-                u += n;
-                tile = 0;
-                if (++rg == q.groups) {
-                    rg = 0;
-                    if (++h == P.Hkv) {
-                        h = 0;
-                        if (u < u1)
-                            q = place_at<PAIR>(P, q.b + 1, u);
-                    }
-                }
+                walk.go_on(P, p.n);
             }
         }
     }
@@ -1566,6 +1616,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             (void)mbar_wait(&S.drain, 0u);
         } else if (warp == 10 && S.loaded[2] > 0) {
             (void)mbar_wait(&S.qfull, (S.loaded[2] - 1) & 1u);
+        } else if (warp < 8) {
+            void_share<NP, PAIR>(P, slot, tid);
         }
         __syncthreads();
     }

@@ -89,3 +89,25 @@ def test_a_wait_that_gives_up_is_reported(monkeypatch, N, D, cta, after):
     want, _, lost, again = giving_up(monkeypatch, c, cta, after)
     assert lost.read_status() == sv.SPEC_DEV_WAIT_TIMEOUT
     assert all(torch.equal(a, b) for a, b in zip(again, want))
+
+
+# shares of several whole items, idle ones among them
+SHORT = dict(B=200, Hkv=2, G=5, S=16, cap=300, dtype=BF16,
+             lens=[0, 3, 128, 300, 1, 64, 0, 129, 257, 17])
+
+
+@gpu
+@pytest.mark.parametrize("N,D", [(5, 64), (60, 64), (60, 128)])
+@pytest.mark.parametrize("shape,cta,after", [(LOSING, 0, 0), (LOSING, 9, 1), (LOSING, 30, 1),
+                                             (SHORT, 0, 0), (SHORT, 70, 1), (SHORT, 101, 2)])
+def test_rows_of_a_wait_that_gives_up_are_nan(monkeypatch, N, D, shape, cta, after):
+    """A row is what it is without the lost wait, or NaN throughout with its log-sum-exp;
+    none is left unwritten or joined from an earlier call's sums."""
+    c = make(N=N, D=D, seed=N, nodes=[N, 3, 0], **shape)
+    (want, want_lse), (out, lse), lost, _ = giving_up(monkeypatch, c, cta, after)
+    assert lost.read_status() == sv.SPEC_DEV_WAIT_TIMEOUT
+    nan = torch.isnan(out)
+    assert torch.equal(nan.all(-1), nan.any(-1)) and torch.equal(nan.all(-1), torch.isnan(lse))
+    assert bool(nan.any()) and not bool(nan.all())
+    keep = ~nan.all(-1)
+    assert torch.equal(out[keep], want[keep]) and torch.equal(lse[keep], want_lse[keep])
