@@ -51,6 +51,7 @@ constexpr int HUN = 8;        // history tokens in flight per thread
 constexpr uint32_t IN_PROMPT = 0x80000000u;  // flags of a column's word; the rest is its count
 constexpr uint32_t DRAFTED = 0x40000000u;    // in the generated part of the history
 constexpr uint32_t COUNT = 0x3fffffffu;
+constexpr uint32_t NO_BIAS = 0x80000000u;    // a column's bias without an entry: -0, which adds nothing
 
 struct LParams {
     spec_process_logits_args a;
@@ -88,9 +89,10 @@ struct Penalty {
     float rep, freq, pres;
 };
 
-// the value of one touched logit x in row r at column c of the tile
-__device__ float touched_value(const spec_process_logits_args &A, const LSmem &S, int t0, int c,
-                               int r, float x, const Penalty &pen)
+// Changes logit x of row r at a touched column c of the tile; false where only other rows
+// touch it (a token drafted on their paths), and it keeps its bits.
+__device__ bool touch(const spec_process_logits_args &A, const LSmem &S, int t0, int c, int r,
+                      float &x, const Penalty &pen)
 {
     const uint32_t w = S.cnt[c];
     int n = (int)(w & COUNT);
@@ -105,15 +107,16 @@ __device__ float touched_value(const spec_process_logits_args &A, const LSmem &S
                 n += S.tok[i] == token;
         }
     }
-    if (n > 0 || (w & IN_PROMPT))
+    const float bias = S.bias ? S.bias[c] : __uint_as_float(NO_BIAS);
+    const bool seen = n > 0 || (w & IN_PROMPT);
+    if (seen)
         x = x > 0.0f ? x / pen.rep : x * pen.rep;
     if (n > 0) {
         x -= pen.freq * (float)n;
         x -= pen.pres;
     }
-    if (S.bias)
-        x += S.bias[c];
-    return x;
+    x += bias;
+    return seen || __float_as_uint(bias) != NO_BIAS;
 }
 
 // -inf where the bits of `ok` are 0
@@ -160,7 +163,7 @@ __global__ void __launch_bounds__(LTH) logits_kernel(const __grid_constant__ LPa
         lsm[i] = 0;
     if (S.bias)
         for (int i = tid; i < P.C; i += LTH)
-            S.bias[i] = 0.0f;
+            S.bias[i] = __uint_as_float(NO_BIAS);
 
     Penalty pen;
     pen.rep = A.repetition ? A.repetition[b] : 1.0f;
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(LTH) logits_kernel(const __grid_constant__ LPa
             const int c = t - t0;
             if (t < 0 || c < 0 || c >= cols)
                 continue;
-            if (atomicMax(reinterpret_cast<int *>(&S.bias[c]), A.bias_cols - i) != 0)
+            if (atomicMax(reinterpret_cast<int *>(&S.bias[c]), A.bias_cols - i) > 0)
                 atomicOr(&S.again[c >> 5], 1u << (c & 31));
             atomicOr(&S.touched[c >> 5], 1u << (c & 31));
         }
@@ -339,12 +342,15 @@ __global__ void __launch_bounds__(LTH) logits_kernel(const __grid_constant__ LPa
         for (int i = tid; i < n_listed; i += LTH) {
             const int c = list[i];
             if (DT == SPEC_F32) {
-                float *x = reinterpret_cast<float *>(stage) + c + mis;
-                *x = touched_value(A, S, t0, c, r0 + r, *x, pen);
+                float *at = reinterpret_cast<float *>(stage) + c + mis, x = *at;
+                if (touch(A, S, t0, c, r0 + r, x, pen))
+                    *at = x;
             } else {
-                unsigned short *x = reinterpret_cast<unsigned short *>(stage) + c + mis;
-                *x = (unsigned short)round_bits<DT>(touched_value(
-                    A, S, t0, c, r0 + r, __uint_as_float((uint32_t)*x << 16), pen));
+                unsigned short *at = reinterpret_cast<unsigned short *>(stage) + c + mis;
+                float x = __uint_as_float((uint32_t)*at << 16);
+                const unsigned short was = *at;  // (stored back: to skip the store took 1 % more)
+                const bool on = touch(A, S, t0, c, r0 + r, x, pen);
+                *at = on ? (unsigned short)round_bits<DT>(x) : was;
             }
         }
         if (bad) {

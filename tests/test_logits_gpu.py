@@ -197,3 +197,27 @@ def test_many_sequences_on_another_stream():
     got = sv.spec_process_logits(x, stream=s, **c)
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [64, 61])
+def test_columns_of_other_rows_keep_their_bits(V, dtype):
+    """A token drafted on another row's path only, and no bias for it: -0 and the bits of a NaN
+    stay, beside columns that do change."""
+    word, ints = {F32: (torch.int32, (-2 ** 31, 0x7fc12345)),
+                  BF16: (torch.int16, (-2 ** 15, 0x7fc5))}[dtype]
+    for value in ints:
+        x = inputs(1, 4, V, dtype, seed=18)
+        for token in (5, 9, 60):
+            x[0, :, token] = torch.tensor(value, dtype=word).view(dtype)
+        i32 = lambda *a: torch.tensor([a], dtype=torch.int32, device="cuda")  # noqa: E731
+        one = lambda v: torch.tensor([v], device="cuda")  # noqa: E731
+        got = sv.spec_process_logits(
+            x.cuda(), draft_tokens=i32(-1, 5, 9, 60), parent=i32(-1, 0, 0, 2), repetition=one(1.5),
+            frequency=one(0.25), presence=one(0.5), bias_tokens=i32(7, -1), bias_values=i32(1, 1).float())
+        bits, was = got.cpu().view(word)[0], x.view(word)[0]
+        path = [[], [5], [9], [9, 60]]
+        for r in range(4):
+            keep = [t for t in range(V) if t != 7 and t not in path[r]]
+            assert torch.equal(bits[r, keep], was[r, keep]), (value, r)
+            assert not torch.equal(got.cpu()[0, r, 7], x[0, r, 7])
