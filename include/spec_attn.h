@@ -128,7 +128,7 @@ int32_t spec_tree_attention(const spec_tree_attention_args *args, void *workspac
  * sequence's cache as it is and writes out_len[b] = -1.
  *   k_new   [layers, B, N, Hkv, D], strides (layer, sequence, node, head) in elements
  *   k_cache [layers, num_pages, page_size, Hkv, D], strides (layer, page, slot, head)
- *   out_len device int32 [B], not cache_len itself
+ *   out_len device int32 [B], no word of it in cache_len or another int32 input
  * elem_size 2 or 4 bytes; any D >= 1, page_size >= 1; base addresses aligned
  * to the element.  One kernel on `stream`, no allocation.
  */

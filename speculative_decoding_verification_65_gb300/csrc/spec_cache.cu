@@ -252,6 +252,13 @@ __global__ void __launch_bounds__(CTH) commit_kernel(const __grid_constant__ Com
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// whether the int32 arrays p [n] and q [m] have a word in common (a null one has none)
+bool overlap(const int32_t *p, uint64_t n, const int32_t *q, uint64_t m)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && a < b + m * 4 && b < a + n * 4;
+}
+
 bool plan_sizes_ok(int32_t B, int32_t N)
 {
     return B >= 0 && B <= 65535 && N >= 1 && N <= SPEC_ATTN_MAX_NODES;
@@ -344,7 +351,13 @@ int32_t spec_tree_commit(const spec_tree_commit_args *args, void *stream)
     if (a.B == 0)
         return SPEC_OK;
     const size_t es = (size_t)a.elem_size;
-    if (!a.cache_len || !a.out_num_accepted || !a.out_len || a.out_len == a.cache_len ||
+    // CTAs read a sequence's inputs while one of them writes its length
+    const uint64_t B = (uint64_t)a.B;
+    if (overlap(a.out_len, B, a.cache_len, B) || overlap(a.out_len, B, a.out_num_accepted, B) ||
+        overlap(a.out_len, B, a.out_nodes, B * a.N) ||
+        overlap(a.out_len, B, a.page_table, B * a.pages_per_seq))
+        return SPEC_EINVAL;
+    if (!a.cache_len || !a.out_num_accepted || !a.out_len ||
         !aligned(a.cache_len, 4) || !aligned(a.out_num_accepted, 4) || !aligned(a.out_len, 4) ||
         !aligned(a.out_nodes, 4) || !aligned(a.page_table, 4) ||
         (!a.page_table && (a.pages_per_seq != 1 || a.num_pages < a.B)))

@@ -333,3 +333,15 @@ def test_attention_selftest_refusals(lib):
     for cta, after, a in ((-1, 0, attention()), (0, -1, attention()), (0, 0, attention(q=0))):
         assert lib.spec_selftest_attention_timeout(ctypes.byref(a), vp(A), ws, cta, after,
                                                    None) == sv.SPEC_EINVAL
+
+
+def test_commit_refuses_lengths_over_its_inputs(lib):
+    """CTAs of a sequence read its inputs while one of them writes its length."""
+    def call(**kw):
+        a = _set(sv._CommitArgs(), k_new=A, v_new=A, k_cache=A, v_cache=A, cache_len=4 * A,
+                 out_num_accepted=5 * A, out_nodes=6 * A, page_table=7 * A, out_len=2 * A, layers=1,
+                 B=2, N=4, Hkv=2, D=64, page_size=16, pages_per_seq=4, num_pages=9, elem_size=2)
+        return lib.spec_tree_commit(ctypes.byref(_set(a, **kw)), None)
+    for at in (4 * A, 4 * A + 4, 4 * A - 4, 5 * A, 5 * A + 4, 6 * A - 4, 6 * A + 28, 7 * A + 28,
+               7 * A - 4):
+        assert call(out_len=at) == sv.SPEC_EINVAL, hex(at)
