@@ -62,7 +62,7 @@ size_t spec_tree_plan_offset(int32_t B, int32_t N, int32_t part);
  * [0, n), or a page that a position below cache_len needs outside
  * [0, num_pages).  Returns SPEC_OK once launched, SPEC_EINVAL for a size,
  * pointer or alignment error, SPEC_ENOSPACE for a short plan, SPEC_ECUDA if
- * the launch failed.  B = 0 is a no-op.
+ * the launch failed.  B = 0 is a no-op, which writes no status word either.
  */
 int32_t spec_tree_plan(const int32_t *parent, const int32_t *n_nodes, const int32_t *cache_len,
                        const int32_t *page_table, int32_t B, int32_t N, int32_t page_size,

@@ -345,3 +345,8 @@ def test_commit_refuses_lengths_over_its_inputs(lib):
     for at in (4 * A, 4 * A + 4, 4 * A - 4, 5 * A, 5 * A + 4, 6 * A - 4, 6 * A + 28, 7 * A + 28,
                7 * A - 4):
         assert call(out_len=at) == sv.SPEC_EINVAL, hex(at)
+
+
+def test_status_of_an_empty_batch(lib):
+    """Nothing ran, and nothing was written to read."""
+    assert sv.TreePlan(0, 5, (16, 4, 9), None).read_status() == sv.SPEC_DEV_OK
