@@ -1,5 +1,6 @@
 """Tree attention in 64 bits, a sequence and a key head at a time, with the bound of its
-outputs.  CPU only; no code shared with the library."""
+outputs, and inputs whose every tile of keys some row depends on.  CPU only; no
+code shared with the library."""
 import math
 
 import numpy as np
@@ -81,3 +82,60 @@ def lse_tolerance(c, r):
     keys = int(np.max(c["cache_len"])) + c["q"].shape[1]
     return ((c["q"].shape[3] + 8) * 2.0 ** -23 * r["big"] + (KT + keys / KT) * 2.0 ** -24
             + 2.0 ** -20 + 2.0 ** -22 * r["lse"].abs().nan_to_num(0, 0, 0))
+
+
+SHARP = 18.0
+
+
+def directed(c, ends, seed=0):
+    """Sets q, k and v of `c` so that row y (node and head of the group) has score SHARP (use scale
+    1) with the keys of every D-th tile, from tile y % D on, and 0 with all others: each
+    tile carries a large part of some row.  With `ends` only the first and the last key of
+    a tile, of a page and of the sequence count.  A tile's values share a sign in each column."""
+    gen = torch.Generator().manual_seed(seed)
+    B, N, Hq, D = c["q"].shape
+    H, S = c["k_new"].shape[2], c["k_cache"].shape[1]
+    G, dt = Hq // H, c["q"].dtype
+    rows = (torch.arange(N)[:, None] * G + torch.arange(Hq)[None, :] % G) % D
+    c["q"] = (torch.nn.functional.one_hot(rows, D) * SHARP).to(dt).repeat(B, 1, 1, 1)
+    for name in ("k_cache", "k_new"):
+        c[name] = torch.zeros_like(c[name])
+    c["v_new"] = torch.randn(c["v_new"].shape, generator=gen).to(dt)
+    for b in range(B):
+        L = int(c["cache_len"][b])
+        t = torch.arange(L)
+        page = torch.full((L,), b) if c["table"] is None else torch.from_numpy(
+            c["table"][b][t.numpy() // S].astype(np.int64))
+        on = torch.ones(L, dtype=torch.bool)
+        if ends:
+            on = (t % KT == 0) | (t % KT == KT - 1) | (t == L - 1)
+            if c["table"] is not None and S >= 64:
+                on |= (t % S == 0) | (t % S == S - 1)
+        k = torch.nn.functional.one_hot(t // KT % D, D) * on[:, None]
+        sign = torch.randint(0, 2, (L // KT + 1, H, D), generator=gen) * 2 - 1
+        v = sign[t // KT] * (0.75 + 0.5 * torch.rand((L, H, D), generator=gen))
+        c["k_cache"][page, t % S] = k[:, None, :].to(dt).expand(L, H, D)
+        c["v_cache"][page, t % S] = v.to(dt)
+    return c
+
+
+def parts_of_tiles(c, b, scale=1.0):
+    """What each tile of sequence b's cache gives each output: [tiles, N, Hq, D]."""
+    N, Hq, D = c["q"].shape[1:]
+    H, S, L = c["k_new"].shape[2], c["k_cache"].shape[1], int(c["cache_len"][b])
+    lse = attention(c, scale)["lse"]
+    t = np.arange(L)
+    page = torch.full((L,), b) if c["table"] is None else torch.from_numpy(
+        c["table"][b][t // S].astype(np.int64))
+    tiles = -(-L // KT)
+    out = torch.zeros((tiles, N, Hq, D), dtype=torch.float64)
+    G, n = Hq // H, int(c["n_nodes"][b])
+    for h in range(H):
+        k = c["k_cache"][page, t % S, h].double()
+        v = c["v_cache"][page, t % S, h].double()
+        for x in range(tiles):
+            of = slice(x * KT, min(L, (x + 1) * KT))
+            heads = slice(h * G, (h + 1) * G)
+            s = c["q"][b, :n, heads].double() @ k[of].T * scale
+            out[x, :n, heads] = torch.exp(s - lse[b, :n, heads, None]) @ v[of]
+    return out
