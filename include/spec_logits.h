@@ -41,7 +41,8 @@ extern "C" {
 /*
  *   logits       device, [B, R, V] of dtype (SPEC_F32 or SPEC_BF16), contiguous
  *   out          the same shape; may be `logits` itself
- *   history      device int32 [B, H] or NULL (H = 0); history_len, prompt_len int32 [B]
+ *   history      device int32 [B, H] or NULL (H = 0); history_len, prompt_len int32 [B] (not
+ *                read where H = 0)
  *   draft_tokens device int32 [B, draft_cols] or NULL (draft_cols = 0): chain, draft_cols
  *                R - 1 or R; tree, draft_cols = R
  *   parent       device int32 [B, R] or NULL (a chain)

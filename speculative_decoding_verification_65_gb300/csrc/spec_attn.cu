@@ -23,7 +23,8 @@
 //                   smaller than a tile are boxes of one tile
 //   warp 9          issues the products in order: S(i) first two, then
 //                   O(i), S(i + 2), ...; a commit behind S(i + 2) so also
-//                   says that O(i) is done
+//                   says that O(i) is done.  With two row tiles: S(0) of
+//                   each, then O(i), S(i + 1) of the one and of the other
 //   warp 10         TMA of an item's Q
 //   warp 11         walks the CTA's share and hands the pieces of it out
 //                   through a small ring: what a piece is costs several
@@ -99,8 +100,8 @@ __host__ __device__ constexpr float lift() { return DT == SPEC_BF16 ? 0.0f : 11.
 // PAIR: a CTA has two row tiles, one for each softmax group, over the same keys.
 template <int NP, bool PAIR>
 struct Cfg {
-    // 80 KB to 192 KB of K and V in flight or in use: an SM's share of HBM
-    // needs about 35 KB in flight
+    // 160 KB (D > 64, pairs) or 192 KB of K and V in flight or in use: an SM's share of
+    // HBM needs about 35 KB in flight
     static constexpr int Q_TILES = PAIR ? 2 : 1;
     static constexpr int KST = NP == 2 ? 3 : 6;
     static constexpr int VST = NP == 2 ? (PAIR ? 2 : 3) : 6;
@@ -475,7 +476,10 @@ __device__ __forceinline__ void hide(uint32_t (&x)[32], uint32_t bits)
         x[j] = (int)(bits << (31 - j)) < 0 ? x[j] : 0xff800000u;
 }
 
-// weights 2^(x c + shift) of 32 scores, packed, and their sum added to `sum`
+// weights 2^(x c + shift) of 32 scores, packed, and their sum added to `sum`.  They are rounded
+// to the dtype because the product's two operands have one type, and V's is that; the total keeps
+// fp32.  Outputs are then 2.3e-3 from 64 bits in bf16 and 2.8e-4 in fp16 (2-norm), where fp32
+// weights and one rounding of the result give 1.7e-3 and 2.1e-4.
 template <int DT>
 __device__ __forceinline__ void weigh(const uint32_t (&x)[32], unsigned long long c2,
                                       unsigned long long shift2, unsigned long long (&sum)[2],
