@@ -129,7 +129,8 @@ int32_t spec_tree_attention(const spec_tree_attention_args *args, void *workspac
  *   k_new   [layers, B, N, Hkv, D], strides (layer, sequence, node, head) in elements
  *   k_cache [layers, num_pages, page_size, Hkv, D], strides (layer, page, slot, head)
  *   out_len device int32 [B], no word of it in cache_len or another int32 input
- * elem_size 2 or 4 bytes; any D >= 1, page_size >= 1; base addresses aligned
+ * elem_size 2 or 4 bytes; any D >= 1, page_size >= 1, Hkv * D up to 2^24, and up to
+ * 2^29 / N heads that do not lie one after the other; base addresses aligned
  * to the element.  One kernel on `stream`, no allocation.
  */
 typedef struct spec_tree_commit_args {

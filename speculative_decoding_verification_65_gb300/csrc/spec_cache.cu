@@ -380,6 +380,8 @@ int32_t spec_tree_commit(const spec_tree_commit_args *args, void *stream)
     const bool flat = a.k_new_stride[3] == a.D && a.v_new_stride[3] == a.D &&
                       a.k_cache_stride[3] == a.D && a.v_cache_stride[3] == a.D;
     P.runs = flat ? 1 : a.Hkv;
+    if (2ll * a.N * P.runs > INT_MAX / 2)
+        return SPEC_EINVAL;  // a sequence's runs are counted in 32 bits
     P.run = (int)((size_t)a.D * es / vec) * (flat ? a.Hkv : 1);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const unsigned int gy = a.layers < 1 ? 1u : a.layers > 65535 ? 65535u : (unsigned int)a.layers;

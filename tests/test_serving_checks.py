@@ -350,3 +350,13 @@ def test_commit_refuses_lengths_over_its_inputs(lib):
 def test_status_of_an_empty_batch(lib):
     """Nothing ran, and nothing was written to read."""
     assert sv.TreePlan(0, 5, (16, 4, 9), None).read_status() == sv.SPEC_DEV_OK
+
+
+def test_commit_refuses_more_runs_than_it_counts(lib):
+    """A path's runs of strided heads are counted in 32 bits."""
+    a = _set(sv._CommitArgs(), k_new=A, v_new=A, k_cache=A, v_cache=A, cache_len=4 * A,
+             out_num_accepted=5 * A, page_table=7 * A, out_len=2 * A, layers=1, B=2, N=1024,
+             Hkv=1 << 21, D=8, page_size=16, pages_per_seq=400, num_pages=900, elem_size=2,
+             k_new_stride=(0, 0, 1 << 25, 16), v_new_stride=(0, 0, 1 << 25, 16),
+             k_cache_stride=(0, 1 << 29, 1 << 25, 16), v_cache_stride=(0, 1 << 29, 1 << 25, 16))
+    assert lib.spec_tree_commit(ctypes.byref(a), None) == sv.SPEC_EINVAL
