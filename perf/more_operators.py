@@ -303,9 +303,9 @@ def _fork_plain(st):
     first = live & (eldest[pa] == r)
     private = i >= (length // S)[:, None]
     single = ref[rows.clamp(min=0)] == 1
-    keep = live[:, None] & (rows >= 0) & (~private | (first[:, None] & single))
-    need = ((length + reserve + S - 1) // S)[:, None]
-    fresh = live[:, None] & private & (i < need) & ~keep
+    need = live[:, None] & (i < ((length + reserve + S - 1) // S)[:, None])
+    keep = need & (rows >= 0) & (~private | (first[:, None] & single))
+    fresh = need & ~keep
     free = _listed_pages(ref == 0, P, P)
     take = free[(torch.cumsum(fresh.flatten(), 0) - 1).clamp(min=0)].view(R, M)
     new = torch.where(keep, rows, torch.where(fresh, take, -1))
