@@ -202,7 +202,8 @@ def prepare(case, seed):
             parent = first + np.minimum(K - 1, rng.exponential(K / 4, size=R).astype(np.int64))
             parent[np.repeat(rng.random(B) < 0.08, K)] = -1
             st["parent"] = _dev(parent.astype(np.int32))
-            st["reserve"] = _dev(rng.integers(1, c["most"] + 1, size=R).astype(np.int32))
+            reserve = rng.integers(1, c["most"] + 1, size=R) * (parent >= 0)
+            st["reserve"] = _dev(reserve.astype(np.int32))
         st.update(table=_dev(table), length=_dev(length), ref=_dev(ref))
         shape = (c["layers"], len(ref), c["S"], c["Hkv"], c["D"])
         st["k_cache"] = _normal(gen, shape, DTYPES[c["dtype"]])
@@ -303,8 +304,8 @@ def _fork_plain(st):
     first = live & (eldest[pa] == r)
     private = i >= (length // S)[:, None]
     single = ref[rows.clamp(min=0)] == 1
-    need = live[:, None] & (i < ((length + reserve + S - 1) // S)[:, None])
-    keep = need & (rows >= 0) & (~private | (first[:, None] & single))
+    need = i < ((length + reserve + S - 1) // S)[:, None]
+    keep = need & live[:, None] & (rows >= 0) & (~private | (first[:, None] & single))
     fresh = need & ~keep
     free = _listed_pages(ref == 0, P, P)
     take = free[(torch.cumsum(fresh.flatten(), 0) - 1).clamp(min=0)].view(R, M)
