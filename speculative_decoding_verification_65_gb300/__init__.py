@@ -2,8 +2,9 @@
 
 Thin Python binding over the C ABI of ``libspecverify.so`` (declared in
 ``include/spec_verify.h``, ``include/spec_sample.h``,
-``include/spec_lmhead.h``, ``include/spec_tree.h``, ``include/spec_attn.h``
-and ``include/spec_logits.h``).  Every function here only checks and marshals
+``include/spec_lmhead.h``, ``include/spec_tree.h``, ``include/spec_attn.h``,
+``include/spec_logits.h``, ``include/spec_chunk.h``, ``include/spec_beam.h``
+and ``include/spec_pages.h``).  Every function here only checks and marshals
 arguments (shapes, dtypes, device pointers, the current CUDA stream) and calls
 the function of the same name in the library; all arithmetic runs in the CUDA
 kernels.  PyTorch is used for device memory and streams only.
@@ -16,13 +17,14 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 import struct
 import threading
 
 SPEC_F32 = 0
 SPEC_BF16 = 1
-SPEC_F16 = 2  # tree attention and cache commit only
+SPEC_F16 = 2  # attention and appends to the cache only
 SPEC_OK = 0
 SPEC_EINVAL = 1
 SPEC_ECUDA = 2
@@ -41,6 +43,9 @@ SPEC_ATTN_MAX_HEAD_DIM = 128
 SPEC_PLAN_POSITIONS, SPEC_PLAN_STATUS, SPEC_PLAN_MASK = 0, 1, 2
 SPEC_LOGITS_MAX_ROWS = 1024
 SPEC_LOGITS_MAX_BIAS = 4096
+SPEC_CHUNK_MAX_ROWS = 1 << 24
+SPEC_BEAM_MAX = 64
+SPEC_PAGES_MAX = 1 << 24
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libspecverify.so")
@@ -85,11 +90,72 @@ class _LogitsArgs(ctypes.Structure):
                                                  "dtype")])
 
 
+class _AppendArgs(ctypes.Structure):
+    """spec_chunk_append_args (include/spec_chunk.h)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_new", "v_new", "k_cache", "v_cache")]
+                + [(n + "_stride", ctypes.c_int64 * 3) for n in ("k_new", "v_new")]
+                + [(n + "_stride", ctypes.c_int64 * 4) for n in ("k_cache", "v_cache")]
+                + [(n, ctypes.c_void_p) for n in ("row_start", "cache_len", "page_table",
+                                                  "out_len")]
+                + [(n, ctypes.c_int32) for n in ("layers", "B", "rows", "Hkv", "D", "page_size",
+                                                 "pages_per_seq", "num_pages", "elem_size")])
+
+
+class _ChunkArgs(ctypes.Structure):
+    """spec_chunk_attention_args (include/spec_chunk.h)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k_cache", "v_cache")]
+                + [("q_stride", ctypes.c_int64 * 2)]
+                + [(n + "_stride", ctypes.c_int64 * 3) for n in ("k_cache", "v_cache")]
+                + [(n, ctypes.c_void_p) for n in ("page_table", "plan", "out", "out_lse")]
+                + [("scale", ctypes.c_float)]
+                + [(n, ctypes.c_int32) for n in ("B", "rows", "Hq", "Hkv", "D", "page_size",
+                                                 "pages_per_seq", "num_pages", "dtype")])
+
+
+class _BeamArgs(ctypes.Structure):
+    """spec_beam_select_args (include/spec_beam.h)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("logits", "scores", "norm", "finished",
+                                                "out_tokens", "out_beams", "out_scores")]
+                + [(n, ctypes.c_int32) for n in ("B", "K", "V", "n", "end_token", "dtype")])
+
+
+class _ForkArgs(ctypes.Structure):
+    """spec_pages_fork_args (include/spec_pages.h)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in (
+                    "table_in", "length_in", "parent", "reserve", "ref_in", "table_out",
+                    "length_out", "ref_out", "copies")]
+                + [(n, ctypes.c_int32) for n in ("rows_in", "rows_out", "pages_per_seq",
+                                                 "page_size", "num_pages")])
+
+
+class _CompactArgs(ctypes.Structure):
+    """spec_pages_compact_args (include/spec_pages.h)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("table_in", "ref_in", "table_out", "ref_out",
+                                                "copies", "used")]
+                + [(n, ctypes.c_int32) for n in ("rows", "pages_per_seq", "page_size",
+                                                 "num_pages")])
+
+
+class _CopyArgs(ctypes.Structure):
+    """spec_pages_copy_args (include/spec_pages.h)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_cache", "v_cache")]
+                + [(n + "_stride", ctypes.c_int64 * 4) for n in ("k_cache", "v_cache")]
+                + [("copies", ctypes.c_void_p)]
+                + [(n, ctypes.c_int32) for n in ("n", "layers", "Hkv", "D", "page_size",
+                                                 "num_pages", "elem_size")])
+
+
 # The same structures packed in one go (the binding's own calls: filling a
 # ctypes structure field by field costs more than the smallest kernels).
 _pack_attention = struct.Struct("@5Q15q4Qf9i").pack
 _pack_commit = struct.Struct("@4Q16q5Q9i4x").pack
 _pack_logits = struct.Struct("@14Q2q7i4x").pack
+_pack_append = struct.Struct("@4Q14q4Q9i4x").pack
+_pack_chunk = struct.Struct("@3Q8q4Qf9i").pack
+_pack_beam = struct.Struct("@7Q6i").pack
+_pack_fork = struct.Struct("@9Q5i4x").pack
+_pack_compact = struct.Struct("@6Q4i").pack
+_pack_copy = struct.Struct("@2Q8qQ7i4x").pack
 
 
 def library():
@@ -182,6 +248,26 @@ def library():
         lib.spec_tree_commit.argtypes = [vp, vp]
         lib.spec_process_logits.restype = i32
         lib.spec_process_logits.argtypes = [vp, vp]
+        lib.spec_chunk_append.restype = i32
+        lib.spec_chunk_append.argtypes = [vp, vp]
+        for name in ("spec_chunk_plan_size", "spec_chunk_plan_status",
+                     "spec_chunk_attention_workspace_size"):
+            getattr(lib, name).restype = sz
+            getattr(lib, name).argtypes = [i32] * 3
+        lib.spec_chunk_plan.restype = i32
+        lib.spec_chunk_plan.argtypes = [vp] * 3 + [i32] * 6 + [vp, sz, vp]
+        lib.spec_beam_workspace_size.restype = sz
+        lib.spec_beam_workspace_size.argtypes = [i32] * 5
+        lib.spec_pages_workspace_size.restype = sz
+        lib.spec_pages_workspace_size.argtypes = [i32] * 2
+        for name in ("spec_chunk_attention", "spec_beam_select", "spec_pages_fork",
+                     "spec_pages_compact"):
+            getattr(lib, name).restype = i32
+            getattr(lib, name).argtypes = [vp, vp, sz, vp]
+        lib.spec_beam_reorder.restype = i32
+        lib.spec_beam_reorder.argtypes = [vp] * 3 + [i32] * 4 + [ctypes.c_int64, vp]
+        lib.spec_pages_copy.restype = i32
+        lib.spec_pages_copy.argtypes = [vp, vp]
         _lib = lib
         return lib
 
@@ -1365,3 +1451,391 @@ def spec_process_logits(logits, history=None, history_len=None, prompt_len=None,
                         pres, bt, bv, al, sb, sr, B, R, V, H, cols, M, dt)
     _launch(dev, "spec_process_logits", (_lib or library()).spec_process_logits, args, h)
     return out
+
+
+# --------------------------------------------------- chunks of new tokens
+
+def _scratch(cache, need, device, h, s, zeroed=False):
+    """A workspace of `need` bytes from `cache`, one per (host thread, device, stream).
+    While the stream is being captured into a graph it is a new one, in the
+    graph's own memory: a replay may overlap later calls on the stream."""
+    torch = _torch()
+    if s is not None:
+        with torch.cuda.stream(s):
+            return _scratch(cache, need, device, h, None, zeroed)
+    make = torch.zeros if zeroed else torch.empty
+    if torch.cuda.is_current_stream_capturing():
+        return make(need, dtype=torch.uint8, device=device)
+    key = (device.index, h)
+    ws = cache.of.get(key)
+    if ws is None or ws.numel() < need:
+        ws = cache.of[key] = make(need, dtype=torch.uint8, device=device)
+    return ws
+
+
+_chunk_ws, _beam_ws, _pages_ws = _Workspaces(), _Workspaces(), _Workspaces()
+
+
+def _caches(k_cache, v_cache, lead, Hkv, D, dtype):
+    """Checks the caches [*lead, pages, slots, Hkv, D]; (pages, slots)."""
+    P, S = k_cache.shape[-4:-2]
+    if k_cache.shape != (*lead, P, S, Hkv, D) or v_cache.shape != k_cache.shape:
+        raise ValueError(f"k_cache and v_cache must be {(*lead, 'pages', 'slots', Hkv, D)}")
+    if not dtype == k_cache.dtype == v_cache.dtype:
+        raise TypeError("keys, values and their caches must share a dtype")
+    return P, S
+
+
+def spec_chunk_append(k_new, v_new, k_cache, v_cache, row_start, cache_len, page_table=None,
+                      out_len=None, stream=None):
+    """Append new tokens' keys and values to the cache (include/spec_chunk.h).
+
+    k_new, v_new [rows, Hkv, D] with caches [pages, slots, Hkv, D], or both with
+    a leading dimension of layers; bfloat16, float16 or float32, any strides
+    with a contiguous last dimension; row_start int32 [B + 1]: sequence b's
+    tokens are rows row_start[b] .. row_start[b + 1] - 1; cache_len int32 [B].
+    Returns the new lengths int32 [B] (-1 for a sequence error, whose cache is
+    left alone); asynchronous like any CUDA op."""
+    torch = _torch()
+    if k_new.dim() not in (3, 4) or k_cache.dim() != k_new.dim() + 1:
+        raise ValueError("k_new [.., rows, Hkv, D] and k_cache [.., pages, slots, Hkv, D] expected")
+    *lead, T, Hkv, D = k_new.shape
+    if v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must have one shape")
+    if k_new.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+        raise TypeError(f"k_new must be bfloat16, float16 or float32, got {k_new.dtype}")
+    if v_new.dtype != k_new.dtype:
+        raise TypeError("k_new and v_new must share a dtype")
+    _caches(k_cache, v_cache, lead, Hkv, D, k_new.dtype)
+    if cache_len.dim() != 1:
+        raise ValueError("cache_len must be [B]")
+    dev, i32, B = k_new.device, torch.int32, cache_len.shape[0]
+    start = _array("row_start", row_start, (B + 1,), i32, dev)
+    length = _array("cache_len", cache_len, (B,), i32, dev)
+    geometry, table = _geometry(k_cache, page_table, B, dev)
+    at, strides = [], []
+    for name, t in (("k_new", k_new), ("v_new", v_new), ("k_cache", k_cache),
+                    ("v_cache", v_cache)):
+        a, st = _strided(name, t, dev, 1)
+        at.append(a)
+        strides += st if lead else (0, *st)
+    h, s = _call_stream(stream, dev, (k_new, v_new, k_cache, v_cache, row_start, cache_len,
+                                      page_table, out_len))
+    if out_len is None:
+        out_len = _empty_on(s, (B,), i32, dev)
+    else:
+        _dev_out("out_len", out_len, (B,), i32, dev)
+    args = _pack_append(*at, *strides, start, length, table, out_len.data_ptr(),
+                        lead[0] if lead else 1, B, T, Hkv, D, *geometry, k_new.element_size())
+    _launch(dev, "spec_chunk_append", (_lib or library()).spec_chunk_append, args, h)
+    return out_len
+
+
+@functools.lru_cache(maxsize=256)
+def _chunk_layout(B, T, G):
+    """Bytes of a plan, and the int32 offset of its statuses."""
+    lib = library()
+    return lib.spec_chunk_plan_size(B, T, G), lib.spec_chunk_plan_status(B, T, G) // 4
+
+
+class ChunkPlan:
+    """What spec_chunk_plan made: `status` int32 [B] is a view of `data` (int32),
+    which every layer's spec_chunk_attention reads."""
+
+    def __init__(self, B, rows, group, geometry, data):
+        self.B, self.rows, self.group, self.geometry, self.data = B, rows, group, geometry, data
+
+    def read_status(self, stream=None):
+        """SPEC_DEV_OK, or SPEC_DEV_WAIT_TIMEOUT after a wait inside an attention
+        kernel that read this plan gave up.  Synchronises the stream."""
+        if self.B == 0:  # no kernel ran, and nothing was written
+            return SPEC_DEV_OK
+        return spec_verify_read_status(self.data, stream)
+
+    @property
+    def status(self):
+        at = _chunk_layout(self.B, self.rows, self.group)[1]
+        return self.data[at:at + self.B]
+
+
+def spec_chunk_plan(row_start, kv_len, q, k_cache, page_table=None, plan=None, stream=None):
+    """The plan of a step over chunks of new tokens (include/spec_chunk.h), made
+    once for all layers.
+
+    row_start int32 [B + 1]; kv_len int32 [B]: positions in the cache, the new
+    tokens' included (what spec_chunk_append returned); q [rows, Hq, D] and
+    k_cache [pages, slots, Hkv, D], one layer's, asked for their sizes only;
+    page_table int32 [B, pages_per_seq], or None for a contiguous cache.
+    `plan` refills a ChunkPlan of the same sizes.  Returns a ChunkPlan;
+    asynchronous like any CUDA op."""
+    torch = _torch()
+    if kv_len.dim() != 1 or q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("kv_len must be [B], q [rows, Hq, D] and k_cache [pages, slots, Hkv, D]")
+    B, (T, Hq), Hkv = kv_len.shape[0], q.shape[:2], k_cache.shape[2]
+    if Hkv < 1 or Hq % Hkv:
+        raise ValueError(f"{Hq} query heads do not divide among {Hkv} key heads")
+    G = Hq // Hkv
+    dev, i32 = kv_len.device, torch.int32
+    r = _array("row_start", row_start, (B + 1,), i32, dev)
+    n = _array("kv_len", kv_len, (B,), i32, dev)
+    geometry, table = _geometry(k_cache, page_table, B, dev)
+    need = _chunk_layout(B, T, G)[0]
+    if need == 0:
+        raise ValueError(f"sizes out of range: B={B} rows={T} Hq/Hkv={G}")
+    if plan is not None and ((plan.B, plan.rows, plan.group) != (B, T, G)
+                             or plan.data.device != dev):
+        raise ValueError(f"plan is for B={plan.B} rows={plan.rows} Hq/Hkv={plan.group} on "
+                         f"{plan.data.device}")
+    h, s = _call_stream(stream, dev, (row_start, kv_len, page_table,
+                                      plan.data if plan is not None else None))
+    if plan is None:
+        plan = ChunkPlan(B, T, G, geometry, _empty_on(s, (need // 4,), i32, dev))
+    plan.geometry = geometry
+    _launch(dev, "spec_chunk_plan", (_lib or library()).spec_chunk_plan, r, n, table, B, T, G,
+            *geometry, plan.data.data_ptr(), need, h)
+    return plan
+
+
+@functools.lru_cache(maxsize=256)
+def spec_chunk_attention_workspace_size(Hq: int, Hkv: int, D: int) -> int:
+    return int(library().spec_chunk_attention_workspace_size(Hq, Hkv, D))
+
+
+def spec_chunk_attention(q, k_cache, v_cache, plan, page_table=None, scale=None, out=None,
+                         want_lse=False, ws=None, stream=None):
+    """Causal attention of chunks of new tokens over a cache that holds their keys
+    and values already (include/spec_chunk.h).
+
+    q [rows, Hq, D]; k_cache, v_cache [pages, slots, Hkv, D], bfloat16 or
+    float16, any strides with a contiguous last dimension; plan from
+    spec_chunk_plan; page_table int32 [B, pages_per_seq] or None; scale
+    1 / sqrt(D) by default; ws of one call at a time, by default this thread's.
+    Returns out [rows, Hq, D] and, with want_lse, the rows' log-sum-exp float32
+    [rows, Hq]; rows of no sequence are left as they are.  Asynchronous like
+    any CUDA op."""
+    torch = _torch()
+    if q.dim() != 3 or not k_cache.dim() == v_cache.dim() == 4:
+        raise ValueError("q must be [rows, Hq, D], k_cache and v_cache [pages, slots, Hkv, D]")
+    T, Hq, D = q.shape
+    Hkv, dtype, dev = k_cache.shape[2], q.dtype, q.device
+    if dtype != torch.bfloat16 and dtype != torch.float16:
+        raise TypeError(f"q must be bfloat16 or float16, got {dtype}")
+    S = _caches(k_cache, v_cache, (), Hkv, D, dtype)[1]
+    geometry, table = _geometry(k_cache, page_table, plan.B, dev)
+    if ((plan.rows, plan.group * Hkv, plan.geometry) != (T, Hq, geometry)
+            or plan.data.device != dev):
+        raise ValueError(f"plan is for rows={plan.rows} Hq/Hkv={plan.group}, cache {plan.geometry} "
+                         f"on {plan.data.device}; the call is for rows={T} Hq={Hq} Hkv={Hkv}, "
+                         f"{geometry} on {dev}")
+    q_at, q_st = _strided("q", q, dev, 8)
+    kc_at, kc_st = _strided("k_cache", k_cache, dev, 8)
+    vc_at, vc_st = _strided("v_cache", v_cache, dev, 8)
+    scale = D ** -0.5 if scale is None else float(scale)
+    if not 0.0 < scale < float("inf"):
+        raise ValueError(f"scale must be finite and positive, got {scale}")
+    if table and S % 128 and (S < 8 or S & (S - 1)):
+        raise ValueError(f"page size {S}: a multiple of 128, or a power of two from 8")
+    need = spec_chunk_attention_workspace_size(Hq, Hkv, D)
+    if need == 0:
+        raise ValueError(f"sizes out of range: Hq={Hq} Hkv={Hkv} D={D}")
+    h, s = _call_stream(stream, dev, (q, k_cache, v_cache, plan.data, page_table, out, ws))
+    if out is None:
+        out = _empty_on(s, (T, Hq, D), dtype, dev)
+    else:
+        _dev_out("out", out, (T, Hq, D), dtype, dev)
+    lse = _empty_on(s, (T, Hq), torch.float32, dev) if want_lse else None
+    if ws is None:
+        ws = _scratch(_chunk_ws, need, dev, h, s)
+    else:
+        _check_ws(ws, dev)
+    args = _pack_chunk(q_at, kc_at, vc_at, *q_st, *kc_st, *vc_st, table, plan.data.data_ptr(),
+                       out.data_ptr(), lse.data_ptr() if want_lse else 0, scale, plan.B, T, Hq, Hkv,
+                       D, *geometry, SPEC_BF16 if dtype == torch.bfloat16 else SPEC_F16)
+    _launch(dev, "spec_chunk_attention", (_lib or library()).spec_chunk_attention, args,
+            ws.data_ptr(), ws.numel(), h)
+    return (out, lse) if want_lse else out
+
+
+# ------------------------------------------------------------ beam search
+
+@functools.lru_cache(maxsize=256)
+def spec_beam_workspace_size(B: int, K: int, V: int, n: int, dtype: int) -> int:
+    return int(library().spec_beam_workspace_size(B, K, V, n, dtype))
+
+
+def spec_beam_select(logits, scores, n, finished=None, norm=None, end_token=0, ws=None,
+                     stream=None):
+    """The n best continuations of each sequence's beams (include/spec_beam.h).
+
+    logits [B, K, V] float32 or bfloat16; scores float32 [B, K]: the beams'
+    log-probabilities so far; finished int32 [B, K]: beams that have ended, with
+    end_token as their only candidate; norm float32 [B, K]: what a beam's
+    candidates are divided by where they are compared.  ws: zeroed once, of one
+    call at a time, by default this thread's.  Returns tokens, beams int32
+    [B, n] and scores float32 [B, n], best first (-1, -1 and -inf where there
+    are fewer); asynchronous like any CUDA op."""
+    torch = _torch()
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B, K, V]")
+    B, K, V = logits.shape
+    dt = _dtype_code(logits)
+    dev, i32, f32 = logits.device, torch.int32, torch.float32
+    if not logits.is_cuda or not logits.is_contiguous():
+        raise ValueError("logits must be a contiguous CUDA tensor")
+    need = spec_beam_workspace_size(B, K, V, n, dt)
+    if need == 0:
+        raise ValueError(f"sizes out of range: B={B} K={K} V={V} n={n}")
+    if not 0 <= end_token < V:
+        raise ValueError(f"end_token must be in [0, {V}), got {end_token}")
+    sc = _array("scores", scores, (B, K), f32, dev)
+    fin = _array("finished", finished, (B, K), i32, dev) if finished is not None else 0
+    no = _array("norm", norm, (B, K), f32, dev) if norm is not None else 0
+    h, s = _call_stream(stream, dev, (logits, scores, finished, norm, ws))
+    tokens, beams = _empty_on(s, (B, n), i32, dev), _empty_on(s, (B, n), i32, dev)
+    best = _empty_on(s, (B, n), f32, dev)
+    if ws is None:
+        ws = _scratch(_beam_ws, need, dev, h, s, zeroed=True)
+    else:
+        _check_ws(ws, dev)
+    args = _pack_beam(logits.data_ptr(), sc, no, fin, tokens.data_ptr(), beams.data_ptr(),
+                      best.data_ptr(), B, K, V, n, end_token, dt)
+    _launch(dev, "spec_beam_select", (_lib or library()).spec_beam_select, args, ws.data_ptr(),
+            ws.numel(), h)
+    return tokens, beams, best
+
+
+def spec_beam_reorder(state, beams, dim=0, out=None, stream=None):
+    """The beams' states in the order of the selected (include/spec_beam.h).
+
+    state [.., B, K, ..] contiguous, of any dtype, B its dimension `dim`; beams
+    int32 [B, n] from spec_beam_select.  Returns [.., B, n, ..], where the place
+    of a beam -1 is 0; asynchronous like any CUDA op."""
+    torch = _torch()
+    if not 0 <= dim <= state.dim() - 2 or beams.dim() != 2:
+        raise ValueError("state must be [.., B, K, ..] with B at `dim`, and beams [B, n]")
+    B, K = state.shape[dim:dim + 2]
+    n, dev = beams.shape[1], state.device
+    if not state.is_cuda or not state.is_contiguous():
+        raise ValueError("state must be a contiguous CUDA tensor")
+    at = _array("beams", beams, (B, n), torch.int32, dev)
+    shape = (*state.shape[:dim], B, n, *state.shape[dim + 2:])
+    h, s = _call_stream(stream, dev, (state, beams, out))
+    if out is None:
+        out = _empty_on(s, shape, state.dtype, dev)
+    else:
+        _dev_out("out", out, shape, state.dtype, dev)
+    _launch(dev, "spec_beam_reorder", (_lib or library()).spec_beam_reorder, state.data_ptr(), at,
+            out.data_ptr(), math.prod(state.shape[:dim]), B, K, n,
+            math.prod(state.shape[dim + 2:]) * state.element_size(), h)
+    return out
+
+
+# --------------------------------------------------------- pages of a cache
+
+@functools.lru_cache(maxsize=256)
+def spec_pages_workspace_size(rows_out: int, num_pages: int) -> int:
+    return int(library().spec_pages_workspace_size(rows_out, num_pages))
+
+
+def _pages_workspace(ws, rows, pages, dev, h, s):
+    need = spec_pages_workspace_size(rows, pages)
+    if need == 0:
+        raise ValueError(f"sizes out of range: rows={rows} pages={pages}")
+    if ws is None:
+        return _scratch(_pages_ws, need, dev, h, s)
+    _check_ws(ws, dev)
+    return ws
+
+
+def _outs(given, shapes, dev, s):
+    """The int32 outputs of a call: the caller's, or new ones."""
+    i32 = _torch().int32
+    if given is None:
+        return [_empty_on(s, shape, i32, dev) for shape in shapes]
+    if len(given) != len(shapes):
+        raise ValueError(f"out must be {len(shapes)} tensors")
+    for i, (t, shape) in enumerate(zip(given, shapes)):
+        _dev_out(f"out[{i}]", t, shape, i32, dev)
+    return list(given)
+
+
+def spec_pages_fork(table, length, parent, ref_count, page_size, reserve=None, out=None, ws=None,
+                    stream=None):
+    """New rows of a page table from old ones (include/spec_pages.h): row r takes
+    over row parent[r], sharing its whole pages, or starts empty (-1).
+
+    table int32 [rows, pages_per_seq], length int32 [rows], parent int32
+    [rows_out], ref_count int32 [num_pages] (0: free); reserve int32
+    [rows_out]: tokens to have pages for besides.  Returns the new table,
+    lengths, reference counts and copies int32 [3, rows_out] for spec_pages_copy
+    (before the next call that takes pages).  `out`: those four, none of them an
+    input.  Asynchronous like any CUDA op."""
+    torch = _torch()
+    if table.dim() != 2 or parent.dim() != 1 or ref_count.dim() != 1:
+        raise ValueError("table must be [rows, pages_per_seq], parent [rows_out], ref_count [pages]")
+    (R0, M), R, P = table.shape, parent.shape[0], ref_count.shape[0]
+    dev, i32 = table.device, torch.int32
+    t = _array("table", table, (R0, M), i32, dev)
+    n = _array("length", length, (R0,), i32, dev)
+    p = _array("parent", parent, (R,), i32, dev)
+    rc = _array("ref_count", ref_count, (P,), i32, dev)
+    rs = _array("reserve", reserve, (R,), i32, dev) if reserve is not None else 0
+    h, s = _call_stream(stream, dev, (table, length, parent, ref_count, reserve, ws,
+                                      *(out if out is not None else ())))
+    out = _outs(out, ((R, M), (R,), (P,), (3, R)), dev, s)
+    ws = _pages_workspace(ws, R, P, dev, h, s)
+    args = _pack_fork(t, n, p, rs, rc, *(o.data_ptr() for o in out), R0, R, M, page_size, P)
+    _launch(dev, "spec_pages_fork", (_lib or library()).spec_pages_fork, args, ws.data_ptr(),
+            ws.numel(), h)
+    return tuple(out)
+
+
+def spec_pages_compact(table, ref_count, page_size, out=None, ws=None, stream=None):
+    """The pages in use to the front of the pool (include/spec_pages.h).
+
+    table int32 [rows, pages_per_seq]: all tables over the pool; ref_count
+    int32 [num_pages].  Returns the new table, reference counts, copies int32
+    [3, num_pages // 2] for spec_pages_copy and the number of pages in use
+    int32 [1].  `out`: those four, none of them an input.  Asynchronous like any
+    CUDA op."""
+    torch = _torch()
+    if table.dim() != 2 or ref_count.dim() != 1:
+        raise ValueError("table must be [rows, pages_per_seq], ref_count [pages]")
+    (R, M), P = table.shape, ref_count.shape[0]
+    dev, i32 = table.device, torch.int32
+    t = _array("table", table, (R, M), i32, dev)
+    rc = _array("ref_count", ref_count, (P,), i32, dev)
+    h, s = _call_stream(stream, dev, (table, ref_count, ws, *(out if out is not None else ())))
+    out = _outs(out, ((R, M), (P,), (3, P // 2), (1,)), dev, s)
+    ws = _pages_workspace(ws, R, P, dev, h, s)
+    args = _pack_compact(t, rc, *(o.data_ptr() for o in out), R, M, page_size, P)
+    _launch(dev, "spec_pages_compact", (_lib or library()).spec_pages_compact, args,
+            ws.data_ptr(), ws.numel(), h)
+    return tuple(out)
+
+
+def spec_pages_copy(k_cache, v_cache, copies, stream=None):
+    """Copy pages within the caches, in every layer (include/spec_pages.h).
+
+    k_cache, v_cache [pages, slots, Hkv, D] or with a leading dimension of
+    layers, 2 or 4 bytes an element, any strides with a contiguous last
+    dimension; copies int32 [3, n]: sources, destinations and numbers of slots
+    (-1, -1, 0: nothing).  Asynchronous like any CUDA op."""
+    torch = _torch()
+    if k_cache.dim() not in (4, 5) or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must be [.., pages, slots, Hkv, D]")
+    if v_cache.dtype != k_cache.dtype or k_cache.element_size() not in (2, 4):
+        raise TypeError("k_cache and v_cache must share a dtype of 2 or 4 bytes")
+    if copies.dim() != 2 or copies.shape[0] != 3:
+        raise ValueError("copies must be [3, n]")
+    *lead, P, S, Hkv, D = k_cache.shape
+    dev, n = k_cache.device, copies.shape[1]
+    c = _array("copies", copies, (3, n), torch.int32, dev)
+    k_at, k_st = _strided("k_cache", k_cache, dev, 1)
+    v_at, v_st = _strided("v_cache", v_cache, dev, 1)
+    if not lead:
+        k_st, v_st = (0, *k_st), (0, *v_st)
+    h, _ = _call_stream(stream, dev, (k_cache, v_cache, copies))
+    args = _pack_copy(k_at, v_at, *k_st, *v_st, c, n, lead[0] if lead else 1, Hkv, D, S, P,
+                      k_cache.element_size())
+    _launch(dev, "spec_pages_copy", (_lib or library()).spec_pages_copy, args, h)

@@ -1,8 +1,9 @@
 """Build libspecverify.so in-tree with nvcc for sm_103a (GB300).
 
-Eight translation units (verification, sampling, the LM-head-fused
+Twelve translation units (verification, sampling, the LM-head-fused
 verification, tree verification, tree attention, its plan and cache commit,
-logits processing, the benchmark's read probe), one -gencode, no cmake: each
+logits processing, chunk attention, its plan and append, beam selection, the
+cache's pages, the benchmark's read probe), one -gencode, no cmake: each
 is compiled by its own nvcc process in parallel, then one nvcc call links the
 shared library.  The library links the CUDA runtime statically so it only
 needs the driver at run time; PyTorch's own runtime is not involved.
@@ -20,8 +21,11 @@ CSRC = os.path.join(PKG, "csrc")
 SRCS = [os.path.join(CSRC, "spec_verify.cu"), os.path.join(CSRC, "spec_sample.cu"),
         os.path.join(CSRC, "spec_lmhead.cu"), os.path.join(CSRC, "spec_tree.cu"),
         os.path.join(CSRC, "spec_attn.cu"), os.path.join(CSRC, "spec_cache.cu"),
-        os.path.join(CSRC, "spec_logits.cu"), os.path.join(CSRC, "bench_read.cu")]
-DEPS = [os.path.join(CSRC, "device_common.cuh"), os.path.join(CSRC, "attn_plan.cuh"), os.path.join(CSRC, "internal.h"),
+        os.path.join(CSRC, "spec_logits.cu"), os.path.join(CSRC, "spec_chunk.cu"),
+        os.path.join(CSRC, "spec_append.cu"), os.path.join(CSRC, "spec_beam.cu"),
+        os.path.join(CSRC, "spec_pages.cu"), os.path.join(CSRC, "bench_read.cu")]
+DEPS = [os.path.join(CSRC, "device_common.cuh"), os.path.join(CSRC, "attn_plan.cuh"),
+        os.path.join(CSRC, "attn_common.cuh"), os.path.join(CSRC, "chunk_plan.cuh"), os.path.join(CSRC, "internal.h"),
         os.path.join(CSRC, "resolve.cuh"), os.path.join(CSRC, "exp2_table.h"),
         os.path.join(ROOT, "include", "spec_lmhead.h"),
         os.path.join(ROOT, "include", "spec_verify.h"),
@@ -29,7 +33,10 @@ DEPS = [os.path.join(CSRC, "device_common.cuh"), os.path.join(CSRC, "attn_plan.c
         os.path.join(ROOT, "include", "spec_bench.h"),
         os.path.join(ROOT, "include", "spec_tree.h"),
         os.path.join(ROOT, "include", "spec_attn.h"),
-        os.path.join(ROOT, "include", "spec_logits.h")]
+        os.path.join(ROOT, "include", "spec_logits.h"),
+        os.path.join(ROOT, "include", "spec_chunk.h"),
+        os.path.join(ROOT, "include", "spec_beam.h"),
+        os.path.join(ROOT, "include", "spec_pages.h")]
 SRC = SRCS[0]
 LIB = os.path.join(PKG, "libspecverify.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

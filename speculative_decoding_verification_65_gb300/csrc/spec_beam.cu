@@ -1,0 +1,801 @@
+// spec_beam.cu -- beam search's selection over beams and vocabulary, and the beams' states in the
+// order of the selected (include/spec_beam.h).
+//
+// Selection, first kernel: one pass over the logits of the live beams.  A row is cut into segments,
+// one per CTA; each keeps the running sum of exponentials and the segment's n largest logits.
+// Within a beam candidates are ordered by their logits alone (one constant per beam makes scores of
+// them), so no candidate needs the row's total.  A logit joins the CTA's candidates when it is above
+// the n-th best so far; the first tile starts from the n-th largest of its threads' own maxima (of 8 threads per warp), so
+// few do.
+// The last CTA of a sequence joins its rows' totals and merges the sorted lists of all segments:
+// n rounds of the best head.  Bound by the bytes of the logits.
+//
+// Orders between beams hang on the difference of two logarithms of sums, which fp32 gives to a few
+// 1e-6.  Where two neighbours of different beams lie nearer than that, the sequence is listed,
+// and the second kernel takes the sums of its beams again in exact integers (units of 2^-51 of the row's
+// largest weight, resolve.cuh) and merges once more, so the order is that of 64 bits.
+//
+// Reorder: a gather of rows, 8 KB of a row per warp, in the widest vectors that the
+// addresses allow.  Bound by bytes.
+#include <cuda_runtime.h>
+#include <limits.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "spec_beam.h"
+#include "spec_verify.h"
+#include "device_common.cuh"
+#include "resolve.cuh"
+
+namespace {
+
+using namespace spec_dev;
+
+typedef unsigned long long u64;
+
+constexpr int TH = 256;            // threads of a CTA
+constexpr int WARPS = TH / 32;
+static_assert(8 * WARPS >= SPEC_BEAM_MAX, "the first bound comes from 8 threads of a warp");
+constexpr int UN = 4;              // vectors of a thread in a tile
+constexpr int CAP = 1024;          // candidates of a segment before they are cut
+constexpr int MAX_LISTS = 2 * TH;  // segments of a sequence's beams
+constexpr int EXACT_CTAS = 304;
+constexpr size_t MAX_B = 65536;    // sequences that the counters have room for
+// How far a row's logarithm of its total may be off, in nats: exponents' rounding (2^-23 of up to
+// 24 binary digits, and the constant's 2^-25: 2.5e-6), ex2 three times (2^-22 each), some 19 fp32
+// additions of 2^-24
+constexpr double LSE_OFF = 5e-6;
+constexpr float SLACK = 5.0f;      // nats that a maximum may run ahead of its sum's scale
+
+struct BeamParams {
+    spec_beam_select_args a;
+    int segs;        // of a row
+    int chunks;      // of a row in the exact sums
+    WsHeader *hdr;   // n_flag: sequences listed; next_item: CTAs of the exact kernel that are done
+    int *arrived;    // [B] CTAs of the first kernel
+    int *summed;     // [B] items of the exact kernel, by place in the list
+    int *listed;     // [B]
+    float2 *stats;   // [B K segs] (largest logit, sum of exp(x - largest)); NaN: an error
+    u64 *lists;      // [B K segs n] candidates, best first; 0: none
+    long long *sums; // [B K chunks] by place in the list
+};
+
+// Floats in an order of unsigned numbers (-0 is 0), and a candidate: larger is better, of equal
+// logits the lower token.
+constexpr uint32_t NONE = 0x007fffffu;  // of -inf: no candidate
+__device__ __forceinline__ uint32_t ordered(float x)
+{
+    const uint32_t b = __float_as_uint(x + 0.0f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(u64 key)
+{
+    const uint32_t o = (uint32_t)(key >> 32);
+    return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ u64 candidate(uint32_t order, int col)
+{
+    return (u64)order << 32 | (uint32_t)~col;
+}
+__device__ __forceinline__ int token_of(u64 key) { return (int)~(uint32_t)key; }
+__device__ __forceinline__ u64 ordered(double x)
+{
+    const u64 b = (u64)__double_as_longlong(x + 0.0);
+    return b >> 63 ? ~b : b | 1ull << 63;
+}
+__device__ __forceinline__ double rank_of(u64 o)
+{
+    return __longlong_as_double((long long)(o >> 63 ? o & ~(1ull << 63) : ~o));
+}
+
+struct ScanSmem {
+    u64 cand[CAP];
+    u64 best[8 * WARPS];
+    float part[WARPS][2];
+    u64 most[WARPS];
+    uint32_t bound;
+    int count;
+    int last;
+};
+
+struct PickSmem {
+    double lse[SPEC_BEAM_MAX], score[SPEC_BEAM_MAX], inv[SPEC_BEAM_MAX];
+    float top[SPEC_BEAM_MAX];
+    u64 rank[2][WARPS];
+    int flat[2][WARPS], list[2][WARPS];
+};
+
+// The candidates' best n, sorted, to S.cand; returns the order that a later one has to exceed.
+// The whole CTA; S.count candidates (at most CAP).
+__device__ uint32_t cut(ScanSmem &S, int n)
+{
+    const int tid = (int)threadIdx.x;
+    __syncthreads();
+    const int m = S.count;
+    if (tid < n)
+        S.best[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < m; i += TH) {
+        const u64 key = S.cand[i];
+        int rank = 0;
+        for (int j = 0; j < m && rank < n; ++j)
+            rank += S.cand[j] > key ? 1 : 0;
+        if (rank < n)
+            S.best[rank] = key;
+    }
+    __syncthreads();
+    if (tid < n)
+        S.cand[tid] = S.best[tid];
+    if (tid == 0)
+        S.count = m < n ? m : n;
+    __syncthreads();
+    return m < n ? NONE : (uint32_t)(S.best[n - 1] >> 32);
+}
+
+// A whole CTA merges the lists of sequence b.  `exact`: S.lse holds the beams' logarithms;
+// otherwise they come from the segments' totals, and the answer says whether the order stands.
+template <bool EXACT>
+__device__ bool pick(const BeamParams &P, int b, PickSmem &S)
+{
+    const spec_beam_select_args &A = P.a;
+    const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    bool bad = false;
+    for (int k = warp; k < A.K; k += WARPS) {
+        const int row = b * A.K + k;
+        const float s = A.scores[row], norm = A.norm ? A.norm[row] : 1.0f;
+        const bool fin = A.finished && A.finished[row] != 0;
+        bad |= isnan(s) || s == INFINITY;
+        if (s == -INFINITY)
+            continue;
+        bad |= !(norm > 0.0f) || isinf(norm);
+        double lse = 0.0;
+        if (!fin && !EXACT) {
+            float top = -INFINITY;
+            for (int g = lane; g < P.segs; g += 32) {
+                const float2 x = __ldcg(&P.stats[(size_t)row * P.segs + g]);
+                bad |= isnan(x.x);
+                top = fmaxf(top, x.x);
+            }
+            for (int d = 16; d; d >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            double z = 0.0;
+            for (int g = lane; g < P.segs; g += 32) {
+                const float2 x = __ldcg(&P.stats[(size_t)row * P.segs + g]);
+                if (x.x > -INFINITY)
+                    z += (double)x.y * (double)ex2((x.x - top) * LOG2E);
+            }
+            for (int d = 16; d; d >>= 1)
+                z += __shfl_xor_sync(0xffffffffu, z, d);
+            lse = top > -INFINITY ? (double)top + log(z) : 0.0;
+        }
+        if (lane == 0) {
+            S.score[k] = (double)s;
+            S.inv[k] = 1.0 / (double)norm;
+            if (!EXACT)
+                S.lse[k] = lse;
+        }
+    }
+    bad = __syncthreads_or(bad ? 1 : 0) != 0;
+    const size_t out = (size_t)b * A.n;
+    if (bad) {
+        for (int i = tid; i < A.n; i += TH) {
+            A.out_tokens[out + i] = -1;
+            A.out_beams[out + i] = -1;
+            A.out_scores[out + i] = NAN;
+        }
+        return true;
+    }
+    // a thread's lists: two heads at most
+    const int lists = A.K * P.segs;
+    u64 rank[2];
+    int flat[2], at[2] = {0, 0};
+    auto load = [&](int c) {
+        rank[c] = 0;
+        flat[c] = INT_MAX;
+        const int l = tid + c * TH;
+        if (l >= lists || at[c] >= A.n)
+            return;
+        const int k = l / P.segs, row = b * A.K + k;
+        if (A.scores[row] == -INFINITY)
+            return;
+        if (A.finished && A.finished[row] != 0) {
+            if (at[c] == 0 && l == k * P.segs) {
+                rank[c] = ordered(S.score[k] * S.inv[k]);
+                flat[c] = k * A.V + A.end_token;
+            }
+            return;
+        }
+        const u64 key = __ldcg(&P.lists[((size_t)row * P.segs + (l - k * P.segs)) * A.n + at[c]]);
+        if (key) {
+            rank[c] = ordered((S.score[k] + ((double)value_of(key) - S.lse[k])) * S.inv[k]);
+            flat[c] = k * A.V + token_of(key);
+        }
+    };
+    load(0);
+    load(1);
+    auto better = [](u64 r1, int f1, u64 r2, int f2) { return r1 > r2 || (r1 == r2 && f1 < f2); };
+    u64 r_before = 0;
+    int k_before = -1;
+    bool open = false;
+    // one round more than is written: the next one may lie too near
+    for (int i = 0; i <= A.n; ++i) {
+        const int c = better(rank[1], flat[1], rank[0], flat[0]) ? 1 : 0;
+        u64 r = c ? rank[1] : rank[0];
+        int f = c ? flat[1] : flat[0], l = tid + c * TH;
+        for (int d = 16; d; d >>= 1) {
+            const u64 r2 = __shfl_xor_sync(0xffffffffu, r, d);
+            const int f2 = __shfl_xor_sync(0xffffffffu, f, d);
+            const int l2 = __shfl_xor_sync(0xffffffffu, l, d);
+            if (better(r2, f2, r, f)) {
+                r = r2;
+                f = f2;
+                l = l2;
+            }
+        }
+        if (lane == 0) {
+            S.rank[i & 1][warp] = r;
+            S.flat[i & 1][warp] = f;
+            S.list[i & 1][warp] = l;
+        }
+        __syncthreads();
+        r = 0;
+        f = INT_MAX;
+        l = -1;
+        for (int w = 0; w < WARPS; ++w)
+            if (better(S.rank[i & 1][w], S.flat[i & 1][w], r, f)) {
+                r = S.rank[i & 1][w];
+                f = S.flat[i & 1][w];
+                l = S.list[i & 1][w];
+            }
+        if (r == 0) {  // none left
+            for (int j = i + tid; j < A.n; j += TH) {
+                A.out_tokens[out + j] = -1;
+                A.out_beams[out + j] = -1;
+                A.out_scores[out + j] = -INFINITY;
+            }
+            break;
+        }
+        const int k = f / A.V;
+        if (!EXACT && k_before >= 0 && k != k_before) {
+            const double off = LSE_OFF * (S.inv[k] + S.inv[k_before]);
+            open |= !(rank_of(r_before) - rank_of(r) > off);
+        }
+        r_before = r;
+        k_before = k;
+        if (i == A.n)
+            break;
+        if (l == tid || l == tid + TH) {
+            const int c = l == tid ? 0 : 1;
+            const bool fin = A.finished && A.finished[b * A.K + k] != 0;
+            float score = (float)S.score[k];
+            if (!fin) {
+                const u64 key = __ldcg(&P.lists[((size_t)b * lists + l) * A.n + (c ? at[1] : at[0])]);
+                score = (float)(S.score[k] + ((double)value_of(key) - S.lse[k]));
+            }
+            A.out_tokens[out + i] = f - k * A.V;
+            A.out_beams[out + i] = k;
+            A.out_scores[out + i] = score;
+            if (c == 0) {
+                ++at[0];
+                load(0);
+            } else {
+                ++at[1];
+                load(1);
+            }
+        }
+    }
+    return !open;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(TH) beam_kernel(const __grid_constant__ BeamParams P)
+{
+    using L = Lg<DT>;
+    const spec_beam_select_args &A = P.a;
+    __shared__ ScanSmem S;
+    __shared__ PickSmem K;
+    const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int row = (int)(blockIdx.x / P.segs), seg = (int)(blockIdx.x - row * P.segs);
+    const int b = row / A.K, n = A.n;
+    allow_next_kernel();
+    wait_previous_kernel();
+    const bool counts = A.scores[row] > -INFINITY && !(A.finished && A.finished[row] != 0);
+    if (tid == 0)
+        S.count = 0;
+    __syncthreads();
+    if (counts) {
+        const size_t e0 = (size_t)row * A.V, all = (size_t)A.B * A.K * A.V;
+        const int mis = (int)(e0 % L::VEC);  // elements of the row's first vector before it
+        const size_t vbase = e0 / L::VEC;
+        const int nvec = (mis + A.V + L::VEC - 1) / L::VEC;
+        const int per = (nvec + P.segs - 1) / P.segs;
+        const int v0 = seg * per, v1 = min(nvec, v0 + per);
+        const uint4 *src = reinterpret_cast<const uint4 *>(A.logits) + vbase;
+        auto fetch = [&](int v) -> uint4 {
+            uint4 r = make_uint4(L::NEG_INF_WORD, L::NEG_INF_WORD, L::NEG_INF_WORD, L::NEG_INF_WORD);
+            if (v >= v1)
+                return r;
+            const bool edge = (v == 0 && mis > 0) || v == nvec - 1;
+            if (!edge)
+                return __ldg(src + v);
+            const uint8_t *p = static_cast<const uint8_t *>(A.logits);
+            for (int j = 0; j < L::VEC; ++j) {
+                const int col = v * L::VEC + j - mis;
+                const size_t e = (vbase + v) * L::VEC + j;
+                if (col >= 0 && col < A.V && e < all)
+                    L::put(r, j, L::bits_at(p + e * L::ES));
+            }
+            return r;
+        };
+        uint4 raw[UN], ahead[UN];
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+            raw[u] = fetch(v0 + u * TH + tid);
+        float m = -INFINITY, top = -INFINITY, sum = 0.0f, low = 0.0f;  // sum + low in units of e^m
+        bool bad = false;
+        uint32_t above = NONE;
+        int held = 0;  // candidates before the tile
+        const u64 c2 = f2(LOG2E, LOG2E);
+        for (int t = v0; t < v1; t += TH * UN) {
+#pragma unroll
+            for (int u = 0; u < UN; ++u)
+                ahead[u] = fetch(t + TH * UN + u * TH + tid);
+            const float tm = L::tile_max(raw);
+            bad |= !(tm < INFINITY);
+            top = fmaxf(top, tm);
+            if (tm > m + SLACK || m == -INFINITY) {
+                const float f = m == -INFINITY ? 0.0f : ex2((m - tm) * LOG2E);
+                sum *= f;
+                low *= f;
+                m = tm;
+            }
+            if (m > -INFINITY) {
+                u64 acc = L::expsum2(raw[0], -m, c2);
+#pragma unroll
+                for (int u = 1; u < UN; ++u)
+                    acc = add2(acc, L::expsum2(raw[u], -m, c2));
+                float x, y;
+                f2_split(acc, x, y);
+                x += y;
+                // sum + x exactly, as a float and what it leaves (Knuth's two-sum)
+                const float s = __fadd_rn(sum, x), back = __fsub_rn(s, sum);
+                low += __fadd_rn(__fsub_rn(sum, __fsub_rn(s, back)), __fsub_rn(x, back));
+                sum = s;
+            }
+            if (t == v0) {
+                // a bound that n of the tile's elements reach: the n-th of the warps' 8 best threads
+                float mine = tm;
+                for (int i = 0; i < 8; ++i) {
+                    float most = mine;
+                    for (int d = 16; d; d >>= 1)
+                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+                    const uint32_t who = __ballot_sync(0xffffffffu, mine == most);
+                    if (lane == __ffs((int)who) - 1) {
+                        S.best[warp * 8 + i] = candidate(ordered(mine), warp * 8 + i);
+                        mine = -INFINITY;
+                    }
+                }
+                __syncthreads();
+                if (tid < 8 * WARPS) {
+                    const u64 key = S.best[tid];
+                    int rank = 0;
+                    for (int j = 0; j < 8 * WARPS; ++j)
+                        rank += S.best[j] > key ? 1 : 0;
+                    if (rank == n - 1)
+                        S.bound = (uint32_t)(key >> 32);
+                }
+                __syncthreads();
+                above = max(S.bound, NONE + 1) - 1;  // the bound itself included
+            }
+            if (!bad && ordered(tm) > above) {
+#pragma unroll
+                for (int u = 0; u < UN; ++u) {
+                    if (ordered(L::vmax(raw[u])) <= above)
+                        continue;
+                    float x[L::VEC];
+                    L::unpack(raw[u], x);
+#pragma unroll
+                    for (int j = 0; j < L::VEC; ++j) {
+                        const uint32_t o = ordered(x[j]);
+                        if (o > above) {
+                            const int i = atomicAdd(&S.count, 1);
+                            if (i < CAP)
+                                S.cand[i] = candidate(o, (t + u * TH + tid) * L::VEC + j - mis);
+                        }
+                    }
+                }
+            }
+            bad = __syncthreads_or(bad ? 1 : 0) != 0;
+            if (bad)
+                break;
+            int now = S.count;
+            if (now > CAP) {
+                // too many at once (equal logits, rising ones): the tile's n best one by one
+                __syncthreads();
+                u64 lower = ~0ull;
+                int got = 0;
+                for (; got < n; ++got) {
+                    u64 most = 0;
+#pragma unroll
+                    for (int u = 0; u < UN; ++u) {
+                        float x[L::VEC];
+                        L::unpack(raw[u], x);
+#pragma unroll
+                        for (int j = 0; j < L::VEC; ++j) {
+                            const uint32_t o = ordered(x[j]);
+                            const u64 key = candidate(o, (t + u * TH + tid) * L::VEC + j - mis);
+                            if (o > above && key < lower && key > most)
+                                most = key;
+                        }
+                    }
+                    for (int d = 16; d; d >>= 1) {
+                        const u64 other = __shfl_xor_sync(0xffffffffu, most, d);
+                        most = other > most ? other : most;
+                    }
+                    if (lane == 0)
+                        S.most[warp] = most;
+                    __syncthreads();
+                    for (int w = 0; w < WARPS; ++w)
+                        most = S.most[w] > most ? S.most[w] : most;
+                    __syncthreads();
+                    if (most == 0)
+                        break;
+                    if (tid == 0)
+                        S.cand[held + got] = most;
+                    lower = most;
+                }
+                if (tid == 0)
+                    S.count = held + got;
+                now = held + got;
+            }
+            held = now;
+            if (t == v0 || now >= 2 * n + 32) {
+                above = cut(S, n);
+                held = min(now, n);
+            }
+            __syncthreads();  // S.count has been read by all
+#pragma unroll
+            for (int u = 0; u < UN; ++u)
+                raw[u] = ahead[u];
+        }
+        if (!bad)
+            (void)cut(S, n);
+        u64 *list = P.lists + ((size_t)row * P.segs + seg) * n;
+        for (int i = tid; i < n; i += TH)
+            list[i] = !bad && i < S.count ? S.cand[i] : 0;
+        // the segment's total
+        float most = top;
+        for (int d = 16; d; d >>= 1)
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+        if (lane == 0)
+            S.part[warp][0] = most;
+        __syncthreads();
+        for (int w = 0; w < WARPS; ++w)
+            most = fmaxf(most, S.part[w][0]);
+        float z = m > -INFINITY ? (sum + low) * ex2((m - most) * LOG2E) : 0.0f;
+        for (int d = 16; d; d >>= 1)
+            z += __shfl_xor_sync(0xffffffffu, z, d);
+        if (lane == 0)
+            S.part[warp][1] = z;
+        __syncthreads();
+        if (tid == 0) {
+            z = 0.0f;
+            for (int w = 0; w < WARPS; ++w)
+                z += S.part[w][1];
+            P.stats[(size_t)row * P.segs + seg] =
+                bad ? make_float2(NAN, NAN) : make_float2(most, z);
+        }
+    }
+    // the sequence's last CTA merges
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+        S.last = atomicAdd(&P.arrived[b], 1) == A.K * P.segs - 1;
+        if (S.last)
+            P.arrived[b] = 0;
+    }
+    __syncthreads();
+    if (!S.last)
+        return;
+    __threadfence();
+    if (!pick<false>(P, b, K) && tid == 0)
+        P.listed[atomicAdd(&P.hdr->n_flag, 1u)] = b;
+}
+
+struct ExactSmem {
+    float2 tab[256];
+    long long part[WARPS];
+    int last;
+};
+
+// The exact sums of the listed sequences' beams, 2048 logits at a time, and their merge.
+template <int DT>
+__global__ void __launch_bounds__(TH) beam_exact_kernel(const __grid_constant__ BeamParams P)
+{
+    using L = Lg<DT>;
+    const spec_beam_select_args &A = P.a;
+    __shared__ ExactSmem S;
+    __shared__ PickSmem K;
+    const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    allow_next_kernel();
+    wait_previous_kernel();
+    const int listed = (int)*reinterpret_cast<volatile unsigned int *>(&P.hdr->n_flag);
+    if (listed == 0)
+        return;
+    load_exp2_table(S.tab);
+    __syncthreads();
+    auto counts = [&](int row) {
+        return A.scores[row] > -INFINITY && !(A.finished && A.finished[row] != 0);
+    };
+    auto top_of = [&](int row) -> float {
+        float top = -INFINITY;
+        for (int g = 0; g < P.segs; ++g)
+            top = fmaxf(top, __ldcg(&P.stats[(size_t)row * P.segs + g]).x);
+        return top;
+    };
+    const long long per = (long long)A.K * P.chunks, items = per * listed;
+    for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+        const int i = (int)(item / per), k = (int)(item - i * per) / P.chunks;
+        const int chunk = (int)(item - i * per) - k * P.chunks;
+        const int b = __ldcg(&P.listed[i]), row = b * A.K + k;
+        const float top = counts(row) ? top_of(row) : -INFINITY;
+        if (top > -INFINITY) {
+            long long sum = 0;
+            for (int c = chunk * RCH + 2 * tid; c < min(A.V, (chunk + 1) * RCH); c += 2 * TH) {
+                const bool two = c + 1 < A.V;
+                const float x0 = L::load1(A.logits, (size_t)row * A.V + c);
+                const float x1 = two ? L::load1(A.logits, (size_t)row * A.V + c + 1) : -INFINITY;
+                long long E0, E1;
+                float a0, a1;
+                efix2(x0, x1, top, top, true, two, LOG2E_HI, LOG2E_LO, S.tab, E0, E1, a0, a1);
+                sum += E0 + E1;
+            }
+            for (int d = 16; d; d >>= 1)
+                sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            if (lane == 0)
+                S.part[warp] = sum;
+            __syncthreads();
+            if (tid == 0) {
+                for (int w = 1; w < WARPS; ++w)
+                    sum += S.part[w];
+                P.sums[((size_t)i * A.K + k) * P.chunks + chunk] = sum;
+            }
+        }
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+            S.last = atomicAdd(&P.summed[i], 1) == (int)per - 1;
+            if (S.last)
+                P.summed[i] = 0;
+        }
+        __syncthreads();
+        if (!S.last)
+            continue;
+        __threadfence();
+        for (int q = warp; q < A.K; q += WARPS) {
+            const int r = b * A.K + q;
+            const float high = counts(r) ? top_of(r) : -INFINITY;
+            double z = 0.0;
+            if (high > -INFINITY)
+                for (int c = lane; c < P.chunks; c += 32)
+                    z += (double)__ldcg(&P.sums[((size_t)i * A.K + q) * P.chunks + c]);
+            for (int d = 16; d; d >>= 1)
+                z += __shfl_xor_sync(0xffffffffu, z, d);
+            if (lane == 0)
+                K.lse[q] = high > -INFINITY ? (double)high + log(z * 0x1p-51) : 0.0;
+        }
+        __syncthreads();
+        (void)pick<true>(P, b, K);
+        __syncthreads();
+    }
+    // the list is empty again once every CTA has been through it
+    if (tid == 0) {
+        __threadfence();
+        if (atomicAdd(&P.hdr->next_item, 1u) == gridDim.x - 1) {
+            P.hdr->next_item = 0;
+            P.hdr->n_flag = 0;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- reorder
+
+struct ReorderParams {
+    const void *in;
+    void *out;
+    const int32_t *beams;
+    long long rows;      // of out: lead * B * n
+    int per, K, n;       // B * n, beams in and out
+    long long vecs;      // of a row
+    int parts;           // pieces of a row, PIECE vectors each
+};
+
+constexpr int PIECE = 512;
+
+template <typename V>
+__global__ void __launch_bounds__(TH) reorder_kernel(const __grid_constant__ ReorderParams P)
+{
+    const int lane = (int)threadIdx.x & 31;
+    allow_next_kernel();
+    wait_previous_kernel();
+    const long long jobs = P.rows * P.parts;
+    for (long long j = (long long)blockIdx.x * WARPS + (threadIdx.x >> 5); j < jobs;
+         j += (long long)gridDim.x * WARPS) {
+        const long long row = j / P.parts;
+        const long long first = (j - row * P.parts) * PIECE;
+        const long long l = row / P.per;
+        const int at = (int)(row - l * P.per), b = at / P.n, beam = __ldg(P.beams + at);
+        const bool some = beam >= 0 && beam < P.K;
+        const V *src = static_cast<const V *>(P.in) +
+                       ((l * (P.per / P.n) + b) * P.K + (some ? beam : 0)) * P.vecs;
+        V *dst = static_cast<V *>(P.out) + row * P.vecs;
+        const long long end = min(P.vecs, first + PIECE);
+        for (long long v = first + lane; v < end; v += 4 * 32) {
+            V x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                x[u] = V{};
+                if (some && v + u * 32 < end)
+                    x[u] = __ldg(src + v + u * 32);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (v + u * 32 < end)
+                    dst[v + u * 32] = x[u];
+        }
+    }
+}
+
+// ------------------------------------------------------------------- host
+
+bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+
+bool sizes_ok(int32_t B, int32_t K, int32_t V, int32_t n, int32_t dtype)
+{
+    return B >= 0 && B <= 65535 && K >= 1 && K <= SPEC_BEAM_MAX && n >= 1 && n <= SPEC_BEAM_MAX &&
+           V >= 2 && V <= SPEC_MAX_V && (dtype == SPEC_F32 || dtype == SPEC_BF16);
+}
+
+// Segments of a row: about eight CTAs per SM in all, each with a tile at least.
+int segments(int32_t B, int32_t K, int32_t V, int32_t dtype)
+{
+    const long long rows = (long long)B * K;
+    const int vecs = V / (dtype == SPEC_F32 ? 4 : 8) + 1;
+    long long s = rows > 0 ? (1216 + rows - 1) / rows : 1;
+    const int tiles = (vecs + TH * UN - 1) / (TH * UN);
+    s = s < tiles ? s : tiles;
+    s = s < MAX_LISTS / K ? s : MAX_LISTS / K;
+    return s < 1 ? 1 : (int)s;
+}
+
+struct BeamLayout {
+    size_t arrived, summed, listed, stats, lists, sums, total;
+};
+
+BeamLayout beam_layout(int32_t B, int32_t K, int32_t V, int32_t n, int32_t dtype)
+{
+    const size_t rows = (size_t)B * K, segs = (size_t)segments(B, K, V, dtype);
+    const size_t chunks = (size_t)(V + RCH - 1) / RCH;
+    BeamLayout w;
+    // the counters, zero between calls, lie where calls of any sizes have them
+    w.arrived = sizeof(WsHeader);
+    w.summed = w.arrived + MAX_B * 4;
+    w.listed = w.summed + MAX_B * 4;
+    w.stats = up(w.listed + (size_t)B * 4);
+    w.lists = up(w.stats + rows * segs * sizeof(float2));
+    w.sums = up(w.lists + rows * segs * n * sizeof(u64));
+    w.total = up(w.sums + rows * chunks * sizeof(long long));
+    return w;
+}
+
+template <typename K, typename P>
+int launch(K kernel, unsigned int grid, const P &params, void *stream)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(TH);
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, params) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return SPEC_ECUDA;
+    }
+    return SPEC_OK;
+}
+
+template <int DT>
+int select_beams(const BeamParams &P, void *stream)
+{
+    const int rc = launch(beam_kernel<DT>, (unsigned int)(P.a.B * P.a.K * P.segs), P, stream);
+    return rc != SPEC_OK ? rc : launch(beam_exact_kernel<DT>, EXACT_CTAS, P, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t spec_beam_workspace_size(int32_t B, int32_t K, int32_t V, int32_t n, int32_t dtype)
+{
+    return sizes_ok(B, K, V, n, dtype) ? beam_layout(B, K, V, n, dtype).total : 0;
+}
+
+int32_t spec_beam_select(const spec_beam_select_args *args, void *workspace,
+                         size_t workspace_bytes, void *stream)
+{
+    if (!args)
+        return SPEC_EINVAL;
+    const spec_beam_select_args &a = *args;
+    if (!sizes_ok(a.B, a.K, a.V, a.n, a.dtype) || a.end_token < 0 || a.end_token >= a.V)
+        return SPEC_EINVAL;
+    if (a.B == 0)
+        return SPEC_OK;
+    if (!a.logits || !aligned(a.logits, 16) || !a.scores || !aligned(a.scores, 4) ||
+        !aligned(a.finished, 4) || !aligned(a.norm, 4) || !a.out_tokens ||
+        !aligned(a.out_tokens, 4) || !a.out_beams || !aligned(a.out_beams, 4) || !a.out_scores ||
+        !aligned(a.out_scores, 4) || !workspace || !aligned(workspace, 256))
+        return SPEC_EINVAL;
+    const BeamLayout w = beam_layout(a.B, a.K, a.V, a.n, a.dtype);
+    if (workspace_bytes < w.total)
+        return SPEC_ENOSPACE;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    BeamParams P;
+    P.a = a;
+    P.segs = segments(a.B, a.K, a.V, a.dtype);
+    P.chunks = (a.V + RCH - 1) / RCH;
+    P.hdr = reinterpret_cast<WsHeader *>(ws);
+    P.arrived = reinterpret_cast<int *>(ws + w.arrived);
+    P.summed = reinterpret_cast<int *>(ws + w.summed);
+    P.listed = reinterpret_cast<int *>(ws + w.listed);
+    P.stats = reinterpret_cast<float2 *>(ws + w.stats);
+    P.lists = reinterpret_cast<u64 *>(ws + w.lists);
+    P.sums = reinterpret_cast<long long *>(ws + w.sums);
+    return a.dtype == SPEC_F32 ? select_beams<SPEC_F32>(P, stream)
+                               : select_beams<SPEC_BF16>(P, stream);
+}
+
+int32_t spec_beam_reorder(const void *in, const int32_t *beams, void *out, int32_t lead,
+                          int32_t B, int32_t K, int32_t n, int64_t row_bytes, void *stream)
+{
+    if (lead < 0 || B < 0 || K < 0 || n < 0 || row_bytes < 0 ||
+        (long long)B * n > INT_MAX || (long long)lead * B > INT_MAX ||
+        (long long)lead * B * n > INT_MAX || row_bytes > 1ll << 40)
+        return SPEC_EINVAL;
+    if (lead == 0 || B == 0 || n == 0 || row_bytes == 0)
+        return SPEC_OK;
+    if (!beams || !aligned(beams, 4) || !out || (K > 0 && !in))
+        return SPEC_EINVAL;
+    const uintptr_t i0 = reinterpret_cast<uintptr_t>(in), o0 = reinterpret_cast<uintptr_t>(out);
+    const uint64_t in_bytes = (uint64_t)lead * B * K * (uint64_t)row_bytes;
+    const uint64_t out_bytes = (uint64_t)lead * B * n * (uint64_t)row_bytes;
+    if (in && i0 < o0 + out_bytes && o0 < i0 + in_bytes)
+        return SPEC_EINVAL;
+    const uint64_t bits = i0 | o0 | (uint64_t)row_bytes;
+    const int vec = (bits & 15) == 0 ? 16 : (bits & 3) == 0 ? 4 : 1;
+    ReorderParams P;
+    P.in = in;
+    P.out = out;
+    P.beams = beams;
+    P.rows = (long long)lead * B * n;
+    P.per = B * n;
+    P.K = K;
+    P.n = n;
+    P.vecs = row_bytes / vec;
+    const long long parts = (P.vecs + PIECE - 1) / PIECE;
+    if (parts > INT_MAX)
+        return SPEC_EINVAL;
+    P.parts = (int)parts;
+    const long long ctas = (P.rows * parts + WARPS - 1) / WARPS;
+    const unsigned int grid = ctas < 1216 ? (unsigned int)ctas : 1216u;
+    if (vec == 16)
+        return launch(reorder_kernel<uint4>, grid, P, stream);
+    if (vec == 4)
+        return launch(reorder_kernel<uint32_t>, grid, P, stream);
+    return launch(reorder_kernel<unsigned char>, grid, P, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,1255 @@
+// spec_chunk.cu -- causal attention of chunks of new tokens over a key/value cache on the
+// tcgen05 tensor cores (include/spec_chunk.h).
+//
+// For one sequence and one key/value head the query rows are the new tokens times the G = Hq / Hkv
+// heads of the group.  A CTA works on a row group: the 2 * floor(128 / G) tokens that fill two row
+// tiles of 128, over the keys that any of them sees, 128 at a time: S = Q K^T, a running softmax
+// per row, O += P V.  A step over 128 keys is four products of 128 x 128 x D, 2048 clocks of the
+// tensor pipe at D = 128, for 64 KB of K and V from L2; that, and the 32768 exponentials beside it,
+// is what bounds the kernel.
+//
+// Roles in a CTA (one per SM, 3 warpgroups; the third gives registers to the others):
+//   warps 0-3, 4-7  a row tile each, one thread per row: while one tile's scores become weights
+//                   (in TMEM, in the place of the scores, as the A operand of P V) the tensor
+//                   cores work on the other's products
+//   warp 8          TMA of the K and V tiles, each a ring of stages; pages
+//                   smaller than a tile are boxes of one tile
+//   warp 9          issues the products: S(0) of each tile, then O(i), S(i + 1) of the one and of
+//                   the other; a commit behind S(i + 1) so also says that O(i) is done
+//   warp 10         TMA of an item's Q
+//   warp 11         walks the CTA's share and hands the pieces of it out through a small ring
+// TMEM: S_0, S_1 (128 columns each), O_0, O_1 (up to 128 each).
+//
+// A row's sums are rescaled only when its maximum has grown by more than 2^8 (2^4 with fp16
+// weights) since the last time, so most tiles leave O in TMEM alone.
+//
+// Work: the key tiles of all row groups and heads stand in a line and are dealt to the CTAs in
+// equal runs.  An item (head, row group) that lies in one CTA's run is written by it; of a split
+// item each CTA leaves its unnormalised sums with their maximum and total in the workspace, and a
+// second kernel joins them in order, so repeats are bit-equal.  No CTA waits for another.
+//
+// What a row must not see: tiles that every row of the group sees whole come first and are not
+// masked.  In the others, scores of hidden keys are replaced, not added to, so NaN keys have no
+// effect.  A hidden key's value does enter P V with weight 0, and 0 * NaN is NaN: rows of V past
+// the group's last position are zeroed in shared memory, and non-finite elements of values that
+// only some of its rows see are taken out there and added back row by row.
+//
+// Every mbarrier wait is bounded; one that gives up sets SPEC_DEV_WAIT_TIMEOUT and the CTA's abort
+// flag, after which no role waits or issues any more.  When all have ended, the loads and products
+// in flight land (bounded again), the rows of the CTA's share become NaN, and TMEM is freed.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <limits.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "spec_chunk.h"
+#include "spec_verify.h"
+#include "attn_common.cuh"
+#include "chunk_plan.cuh"
+#include "device_common.cuh"
+
+namespace {
+
+using namespace spec_dev;
+using namespace spec_attn;
+
+constexpr int SOFT_THREADS = 256;
+constexpr int THREADS = SOFT_THREADS + 128;
+// 384 threads launch with 168 registers each, 64512; a softmax thread holds a
+// row's 128 scores: 256 * 208 + 128 * 88 = 64512
+constexpr int SOFT_REGS = 208, HELPER_REGS = 88;
+constexpr int MAX_CTAS = 192;     // the grid's and the workspace's bound
+constexpr int RING = 4;           // pieces handed out ahead
+
+template <int NP>
+struct Cfg {
+    static constexpr int KST = NP == 2 ? 3 : 6;
+    static constexpr int VST = NP == 2 ? 2 : 6;
+    static constexpr int TILE = NP * PANEL_BYTES;
+    static constexpr int DP = NP * PANEL;  // columns of O
+};
+// Stages are taken in the order of the CTA's tiles.  A wait for a phase of a barrier tells it from
+// the phase before only if that one is known to be over (parity), so whoever waits on a stage has
+// gone through its earlier phases: the loader and the issuer wait for all of them, and a softmax
+// group that looks at V waits for its tile's scores first, which the issuer's products of every
+// earlier tile precede.
+
+// A run of one item's key tiles inside a CTA's share.
+struct Piece {
+    int b, h;
+    int row0, ntok;  // the group's rows
+    int pos0;        // its first token's position
+    int tile0, n;    // first tile and number of tiles (0: the share has ended)
+    int tiles;       // of the whole item
+    int idle;        // nothing to compute: a sequence in error
+    int first;       // 1 when the share starts inside the item or with it
+};
+
+struct Tail {
+    unsigned long long kfull[6], kempty[6], vfull[6], vempty[6];
+    unsigned long long qfull, qempty, sfull[2], pready[2], pvdone[2], drain;
+    unsigned long long pfull[RING], pempty[RING], join;
+    Piece piece[RING];
+    uint32_t tmem_base;
+    int abort_flag;
+    uint32_t loaded[3];  // loads that were issued when their warp ended: tiles of K, of V, and Qs
+    uint32_t bad[2][2][4];  // keys of a tile (alternating) with non-finite values, by the group that looked
+};
+
+template <int NP>
+constexpr size_t smem_bytes()
+{
+    using C = Cfg<NP>;
+    return (size_t)C::TILE * (2 + C::KST + C::VST) + sizeof(Tail);
+}
+static_assert(smem_bytes<2>() <= 232448 && smem_bytes<1>() <= 232448, "227 KB per CTA");
+
+struct KParams {
+    const uint8_t *plan;
+    ChunkLayout lay;
+    const int32_t *page_table;
+    const void *v_cache;
+    int64_t v_cache_stride[3];
+    void *out;
+    float *lse;
+    int *status;
+    float *part;     // [ctas][2 tiles][2][DP][BM] unnormalised sums of split items
+    float2 *part_ml; // [ctas][2 tiles][2][BM] (log2 of the weights' unit, total)
+    float c;         // scale * log2(e)
+    int Hq, Hkv, D, G;
+    int tokens_per_tile;
+    int slots;       // CTAs
+    int join_rows;   // rows of a join CTA: 32, or the least power of two that holds them
+    int page_size, pages_per_seq;
+    int page_rows;   // rows of a cache box: min(128, page_size) (contiguous: 128)
+};
+
+// ------------------------------------------------------------------- work
+
+// Where a unit (a key tile of an item) lies: its head, its row group, and the tile in it.
+struct Place {
+    int h, g, tile;
+    int groups;
+    long long total;  // units of one head
+    ChunkGroup x;
+    int status;
+};
+
+__device__ __forceinline__ void load_group(const KParams &P, Place &q)
+{
+    const int4 *at = reinterpret_cast<const int4 *>(P.plan + P.lay.group) + 2 * (size_t)q.g;
+    const int4 a = __ldg(at), b = __ldg(at + 1);
+    q.x.b = a.x;
+    q.x.row0 = a.y;
+    q.x.ntok = a.z;
+    q.x.tiles = a.w;
+    q.x.pos0 = b.x;
+    q.x.bad = b.y;
+    q.status = __ldg(reinterpret_cast<const int *>(P.plan + P.lay.status) + a.x);
+}
+
+__device__ __forceinline__ Place empty_place(const KParams &P)
+{
+    Place q = {};
+    q.groups = __ldg(&reinterpret_cast<const ChunkHeader *>(P.plan)->groups);
+    q.total = __ldg(reinterpret_cast<const long long *>(P.plan + P.lay.cum) + q.groups);
+    return q;
+}
+
+// A warp looks up unit u < total * Hkv: 32 probes of the plan's running sums a round.
+__device__ __forceinline__ void look_up(const KParams &P, long long u, Place &q)
+{
+    const long long *cum = reinterpret_cast<const long long *>(P.plan + P.lay.cum);
+    const int lane = (int)threadIdx.x & 31;
+    q.h = (int)(u / q.total);
+    const long long at = u - q.h * q.total;
+    int lo = 0, len = q.groups;
+    while (len > 1) {
+        const int step = (len + 31) / 32, i = lane * step;
+        const bool below = i < len && __ldg(cum + lo + i) <= at;
+        const int last = 31 - __clz((int)__ballot_sync(0xffffffffu, below));
+        lo += last * step;
+        len = len - last * step < step ? len - last * step : step;
+    }
+    q.g = lo;
+    q.tile = (int)(at - __ldg(cum + lo));
+    load_group(P, q);
+}
+
+// A CTA's share: `per` units for each of the slots that have any.
+__device__ __forceinline__ long long share(const KParams &P, long long all)
+{
+    const long long per = (all + P.slots - 1) / P.slots;
+    return per < 2 ? 2 : per;
+}
+
+// The pieces of a CTA's share, one after the other (a warp's walk, all lanes alike).
+struct Walk {
+    Place q;
+    long long u0, u1, u;
+
+    __device__ __forceinline__ Walk(const KParams &P, int slot) : q(empty_place(P))
+    {
+        const long long all = q.total * P.Hkv, per = share(P, all);
+        u0 = slot * per;
+        u1 = u0 + per < all ? u0 + per : all;
+        u = u0;
+        if (u < u1)
+            look_up(P, u, q);
+    }
+    __device__ __forceinline__ Piece piece() const
+    {
+        const long long left = u1 - u;
+        Piece p;
+        p.b = q.x.b;
+        p.h = q.h;
+        p.row0 = q.x.row0;
+        p.ntok = q.x.ntok;
+        p.pos0 = q.x.pos0;
+        p.tile0 = q.tile;
+        p.tiles = q.x.tiles;
+        p.n = left <= 0 ? 0 : p.tiles - q.tile < left ? p.tiles - q.tile : (int)left;
+        p.idle = q.x.bad | (q.status != 0);
+        p.first = u - q.tile <= u0;
+        return p;
+    }
+    // to the piece behind this one of n tiles
+    __device__ __forceinline__ void go_on(const KParams &P, int n)
+    {
+        u += n;
+        q.tile = 0;
+        if (++q.g == q.groups) {
+            q.g = 0;
+            ++q.h;
+        }
+        if (u < u1)
+            load_group(P, q);
+    }
+};
+
+// The group's rows of one head become NaN, by the softmax warps.
+__device__ __forceinline__ void void_rows(const KParams &P, int h, int row0, int ntok, int tid)
+{
+    for (int y = tid; y < ntok * P.G; y += SOFT_THREADS) {
+        const int64_t row = ((int64_t)row0 + y / P.G) * P.Hq + (int64_t)h * P.G + y % P.G;
+        for (int d = 0; d < P.D; d += 8)
+            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(P.out) + row * P.D + d) =
+                make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+        if (P.lse)
+            P.lse[row] = NAN;
+    }
+}
+
+// A CTA that has given up leaves NaN, not what memory held before: in the statistics of its
+// pieces of split items, whose rows the join then makes NaN, and in the rows that it was to
+// write itself.
+__device__ __noinline__ void void_share(const KParams &P, int slot, int tid)
+{
+    for (int i = tid; i < 2 * 2 * BM; i += SOFT_THREADS)
+        P.part_ml[(size_t)slot * 2 * 2 * BM + i] = make_float2(NAN, NAN);
+    Walk walk(P, slot);
+    while (true) {
+        const Piece p = walk.piece();
+        if (p.n == 0)
+            break;
+        if (p.tile0 == 0)
+            void_rows(P, p.h, p.row0, p.ntok, tid);
+        walk.go_on(P, p.n);
+    }
+}
+
+// Keys of tile `jt` of a group: those up to its last token's position.
+__device__ __forceinline__ int tile_keys(const Piece &p, int jt)
+{
+    const int left = p.pos0 + p.ntok - jt * KT;
+    return left < KT ? left : KT;
+}
+
+template <int NP, int DT>
+__global__ void __launch_bounds__(THREADS, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkc,
+                 const __grid_constant__ CUtensorMap mvc, const __grid_constant__ KParams P)
+{
+    using C = Cfg<NP>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t q_s = smem_addr(smem);
+    const uint32_t k_s = q_s + 2 * C::TILE, v_s = k_s + C::KST * C::TILE;
+    uint8_t *v_p = smem + (size_t)C::TILE * (2 + C::KST);
+    Tail &S = *reinterpret_cast<Tail *>(smem + (size_t)C::TILE * (2 + C::KST + C::VST));
+    volatile int *abort_flag = &S.abort_flag;
+    const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int slot = (int)blockIdx.x;
+
+    if (tid == 0) {
+        for (int i = 0; i < 6; ++i) {
+            mbar_init(&S.kfull[i], 1);
+            mbar_init(&S.kempty[i], 1);
+            mbar_init(&S.vfull[i], 1);
+            mbar_init(&S.vempty[i], 1);
+        }
+        mbar_init(&S.qfull, 1);
+        mbar_init(&S.qempty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.sfull[i], 1);
+            mbar_init(&S.pready[i], 4);
+            mbar_init(&S.pvdone[i], 1);
+        }
+        for (int i = 0; i < RING; ++i) {
+            mbar_init(&S.pfull[i], 1);
+            mbar_init(&S.pempty[i], 11);  // every warp but the one that writes
+        }
+        mbar_init(&S.join, 8);
+        mbar_init(&S.drain, 1);
+        S.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_shared();
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
+                     :: "r"(smem_addr(&S.tmem_base)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem_base;
+    wait_previous_kernel();
+    allow_next_kernel();
+
+    // Whether the CTA has given up, the same on every lane: lanes that each looked for
+    // themselves could part, and wait for each other in the next test for good.
+    auto given_up = [&]() -> bool { return __any_sync(0xffffffffu, *abort_flag != 0); };
+    // A warp's wait: false on every lane once the CTA has given up.
+    auto wait = [&](unsigned long long *bar, uint32_t parity) -> bool {
+#pragma unroll 1
+        for (int i = 0; i < WAIT_TRIES; ++i) {
+            if (warp_try(bar, parity))
+                return true;
+            if (given_up())
+                return false;
+        }
+        give_up(abort_flag, P.status);
+        return false;
+    };
+    // the same for a warp that has time: it sleeps between its tests
+    auto wait_idle = [&](unsigned long long *bar, uint32_t parity) -> bool {
+#pragma unroll 1
+        for (int i = 0; i < WAIT_TRIES; ++i) {
+            if (warp_try(bar, parity))
+                return true;
+            if (given_up())
+                return false;
+            __nanosleep(100);
+        }
+        give_up(abort_flag, P.status);
+        return false;
+    };
+    // the next piece of the share: false when there is none or the CTA has given up
+    uint32_t taken = 0;
+    auto next = [&](Piece &p) -> bool {
+        const int at = (int)(taken % RING);
+        if (!wait(&S.pfull[at], (taken / RING) & 1u))
+            return false;
+        p = S.piece[at];
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&S.pempty[at]);
+        ++taken;
+        return p.n > 0;
+    };
+    // tiles of a piece that every row of the group sees whole
+    auto plain_tiles = [](const Piece &p) -> int {
+        const int whole = (p.pos0 + 1) / KT - p.tile0;
+        return whole < 0 ? 0 : whole < p.n ? whole : p.n;
+    };
+
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(SOFT_REGS));
+        // ---------------------------------------------------- softmax groups
+        const int s = warp >> 2;                 // the group, and its row tile
+        const int quarter = warp & 3;
+        const int r = quarter * 32 + lane;       // row of the tile
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const uint32_t t_s = tmem + lanes + (uint32_t)(s * KT);
+        const uint32_t t_o = tmem + lanes + (uint32_t)(2 * KT + s * C::DP);
+        const int local = r / P.G;               // token of the row, counted in the tile
+        const int g = r - local * P.G;
+        const int tok = s * P.tokens_per_tile + local;  // and in the group
+        uint32_t cnt = 0, tv = 0, done = 0;      // tiles, tiles of earlier pieces, reports of O
+        uint32_t joins = 0;
+        const unsigned long long c2 = f2(P.c, P.c);
+        // a score x has weight 2^(x c + shift) under the maximum m
+        auto shift_of = [&](float m) -> float {
+            return m == -INFINITY ? 0.0f : fmaf(-m, P.c, lift<DT>());
+        };
+        // all softmax warps have come here
+        auto join = [&]() -> bool {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&S.join);
+            return wait(&S.join, joins++ & 1u);
+        };
+
+        bool ok = true;
+        Piece p = {};
+        while (ok && next(p)) {
+            if (p.idle) {
+                if (p.tile0 == 0)
+                    void_rows(P, p.h, p.row0, p.ntok, tid);
+                continue;
+            }
+            const bool live = local < P.tokens_per_tile && tok < p.ntok;
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            const int64_t orow =
+                ((int64_t)p.row0 + tok) * P.Hq + (int64_t)p.h * P.G + g;
+            float m = -INFINITY, l = 0.0f;       // maximum of the raw scores, total
+            const int plain = plain_tiles(p);
+            // one tile; in a `masked` one some keys are hidden from some rows
+            auto tile = [&](int i, auto kind) {
+                constexpr bool masked = decltype(kind)::value;
+                const int jt = p.tile0 + i;
+                const int keys = masked ? tile_keys(p, jt) : KT;
+                // keys of the tile that this row sees
+                const int sees = masked ? min(keys, p.pos0 + tok + 1 - jt * KT) : KT;
+                // the scores are there, and the group's product before is done
+                ok = wait(&S.sfull[s], cnt & 1u);
+                if (!ok)
+                    return;
+                tc_fence_after();
+                uint32_t any_bad = 0;
+                auto bad_keys = [&](int q) -> uint32_t {  // of keys 32 q on, after join
+                    const volatile uint32_t(*f)[2][4] = S.bad;
+                    return f[0][cnt & 1u][q] | f[1][cnt & 1u][q];
+                };
+                if (masked) {
+                    // V: rows past the keys (up to the last product's 16) are zeroed; of keys that
+                    // some row does not see, non-finite elements are noted and zeroed.  Each group
+                    // looks at a panel (with one panel the second only zeroes)
+                    const uint32_t t = tv + (uint32_t)i;
+                    const int st = (int)(t % C::VST);
+                    ok = wait(&S.vfull[st], (t / C::VST) & 1u);
+                    if (!ok)
+                        return;
+                    uint8_t *vrow = v_p + (size_t)st * C::TILE + r * 128;
+                    bool bad = false;
+                    if (s < NP) {
+                        vrow += s * PANEL_BYTES;
+                        if (r >= keys && r < ((keys + 15) & ~15)) {
+#pragma unroll
+                            for (int x = 0; x < 8; ++x)
+                                *reinterpret_cast<uint4 *>(vrow + x * 16) = make_uint4(0, 0, 0, 0);
+                        } else if (r < keys && jt * KT + r > p.pos0) {
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) {
+                                uint4 *q = reinterpret_cast<uint4 *>(vrow + x * 16);
+                                uint4 w = *q;
+                                const uint4 f = make_uint4(nonfinite<DT>(w.x), nonfinite<DT>(w.y),
+                                                           nonfinite<DT>(w.z), nonfinite<DT>(w.w));
+                                if (f.x | f.y | f.z | f.w) {
+                                    bad = true;
+                                    w.x &= ~f.x;
+                                    w.y &= ~f.y;
+                                    w.z &= ~f.z;
+                                    w.w &= ~f.w;
+                                    *q = w;
+                                }
+                            }
+                        }
+                        fence_async_shared();
+                    }
+                    const uint32_t ballot = __ballot_sync(0xffffffffu, bad);
+                    if (lane == 0)
+                        S.bad[s][cnt & 1u][quarter] = ballot;
+                    ok = join();
+                    if (!ok)
+                        return;
+                    any_bad = bad_keys(0) | bad_keys(1) | bad_keys(2) | bad_keys(3);
+                }
+                auto bits = [&](int h) -> uint32_t {  // of keys 32 h on, those that the row sees
+                    const int left = sees - h * 32;
+                    return left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u;
+                };
+                uint32_t zero_w[4] = {0, 0, 0, 0};  // keys whose weight is 0 (with any_bad only)
+                // the row's new maximum `top`; O and l follow where it has grown far
+                auto raise = [&](float top) {
+                    if (i == 0) {
+                        m = top;
+                        return;
+                    }
+                    const bool grown = (top - m) * P.c > growth<DT>();  // -inf to finite too
+                    if (!__any_sync(0xffffffffu, grown))
+                        return;
+                    const float f = grown ? ex2((m - top) * P.c) : 1.0f;
+                    l *= f;
+                    if (grown)
+                        m = top;
+#pragma unroll 1
+                    for (int d = 0; d < C::DP; d += 16) {
+                        uint32_t o[16];
+                        tmem_ld(t_o + d, o);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                        tmem_st(t_o + d, o);
+                    }
+                };
+                unsigned long long sum[2] = {0ull, 0ull};
+                bool redo = masked || i == 0;
+                if (warp_live && !redo) {
+                    // in one pass: weights by the maximum so far, which serves as long as no
+                    // score is far above it; the tile's own maximum is found on the way
+                    const float shift = shift_of(m);
+                    const unsigned long long shift2 = f2(shift, shift);
+                    uint32_t x[32], y[32], pk[4][16];
+                    __syncwarp();
+                    tmem_ld_start(t_s, x);
+                    tmem_ld_finish(x);
+                    tmem_ld_start(t_s + 32, y);
+                    float top = max32(x);
+                    weigh<DT>(x, c2, shift2, sum, pk[0]);
+                    tmem_ld_finish(y);
+                    tmem_ld_start(t_s + 64, x);
+                    top = fmaxf(top, max32(y));
+                    weigh<DT>(y, c2, shift2, sum, pk[1]);
+                    tmem_ld_finish(x);
+                    tmem_ld_start(t_s + 96, y);
+                    top = fmaxf(top, max32(x));
+                    weigh<DT>(x, c2, shift2, sum, pk[2]);
+                    tmem_ld_finish(y);
+                    top = fmaxf(top, max32(y));
+                    weigh<DT>(y, c2, shift2, sum, pk[3]);
+                    redo = __any_sync(0xffffffffu,
+                                      (top - m) * P.c > growth<DT>());  // -inf to finite too
+                    if (!redo) {
+#pragma unroll
+                        for (int h = 0; h < 4; ++h)
+                            tmem_st(t_s + h * 16, pk[h]);
+                    } else {
+                        sum[0] = sum[1] = 0ull;
+                    }
+                }
+                if (warp_live && redo) {
+                    // the maximum first: 32 keys at a time, and no more of them than the tile has
+                    const int chunks = (keys + 31) / 32;
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int h = 0; h < chunks; ++h) {
+                        uint32_t x[32];
+                        tmem_ld(t_s + h * 32, x);
+                        if (masked)
+                            hide(x, bits(h));
+                        top = fmaxf(top, max32(x));
+                    }
+                    raise(top);
+                    const float shift = shift_of(m);
+                    const unsigned long long shift2 = f2(shift, shift);
+#pragma unroll 1
+                    for (int h = 0; h < chunks; ++h) {
+                        uint32_t x[32], pk[16];
+                        tmem_ld(t_s + h * 32, x);
+                        if (masked)
+                            hide(x, bits(h));
+                        weigh<DT>(x, c2, shift2, sum, pk);
+                        // weights 32 h on lie in columns 16 h on: over scores that were read
+                        tmem_st(t_s + h * 16, pk);
+                        if (any_bad) {
+                            uint32_t z = 0;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                z |= ((pk[j] & 0x7fffu) == 0 ? 1u : 0u) << (2 * j) |
+                                     ((pk[j] & 0x7fff0000u) == 0 ? 2u : 0u) << (2 * j);
+                            zero_w[0] = h == 0 ? z : zero_w[0];
+                            zero_w[1] = h == 1 ? z : zero_w[1];
+                            zero_w[2] = h == 2 ? z : zero_w[2];
+                            zero_w[3] = h == 3 ? z : zero_w[3];
+                        }
+                    }
+                }
+                if (warp_live) {
+                    float s0, s1;
+                    f2_split(add2(sum[0], sum[1]), s0, s1);
+                    l += s0 + s1;
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&S.pready[s]);
+                if (any_bad) {
+                    // what the zeroed elements give the rows that see them, once O(i) is done
+                    ok = wait(&S.pvdone[s], done & 1u);
+                    if (!ok)
+                        return;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int d = 0; d < C::DP; d += 32) {
+                        uint32_t o[32];
+                        tmem_ld(t_o + d, o);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t left = bad_keys(q) & bits(q);
+                            while (live && left) {
+                                const int bit = __ffs((int)left) - 1;
+                                left &= left - 1;
+                                const int key = jt * KT + q * 32 + bit;
+                                const int e = key / P.page_size;
+                                const int64_t page = P.page_table
+                                    ? __ldg(P.page_table + (size_t)p.b * P.pages_per_seq + e) : p.b;
+                                const uint16_t *src = reinterpret_cast<const uint16_t *>(P.v_cache) +
+                                    page * P.v_cache_stride[0] +
+                                    (key - e * P.page_size) * P.v_cache_stride[1] +
+                                    p.h * P.v_cache_stride[2];
+                                const float z = (zero_w[q] >> bit) & 1u ? 0.0f : 1.0f;
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    if (d + j < P.D) {
+                                        const uint32_t v = src[d + j];
+                                        if (nonfinite<DT>(v) & 0xffffu)
+                                            o[j] = __float_as_uint(__uint_as_float(o[j]) +
+                                                                   z * unpack1<DT>(v));
+                                    }
+                            }
+                        }
+                        tmem_st(t_o + d, o);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    // the notes are written over only after every warp has read them
+                    ok = join();
+                }
+                if (commits_done(i, plain, 1, p.n))
+                    ++done;
+                ++cnt;
+            };
+            // tiles without a mask first, in a loop of their own: it stays small
+            int i = 0;
+            for (; i < plain && ok; ++i)
+                tile(i, Whole());
+            for (; i < p.n && ok; ++i)
+                tile(i, Masked());
+            if (!ok)
+                break;
+            tv += (uint32_t)p.n;
+
+            if (!wait(&S.pvdone[s], (done - 1) & 1u))
+                break;
+            tc_fence_after();
+            const float top = m != -INFINITY ? -shift_of(m) : -INFINITY;
+            const float sum = l, base = top == -INFINITY ? 0.0f : top;
+            // a row that saw no key has no weight, whatever its O holds
+            const bool some = !(top == -INFINITY && sum == 0.0f);
+            const bool whole = p.n == p.tiles;
+            if (warp_live) {
+                const size_t at = (((size_t)slot * 2 + s) * 2 + (p.first ? 0 : 1)) * BM;
+                const float norm = sum != 0.0f ? 1.0f / sum : 0.0f;
+                const bool on = live && some && sum != 0.0f;
+#pragma unroll 1
+                for (int panel = 0; panel < NP; ++panel) {
+                    uint4 u[8];
+#pragma unroll
+                    for (int d0 = 0; d0 < PANEL; d0 += 32) {
+                        uint32_t a[32];
+                        tmem_ld(t_o + (uint32_t)(panel * PANEL + d0), a);
+                        if (whole) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 8) {
+                                float v[8];
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    v[k] = __uint_as_float(a[j + k]) * norm;
+                                u[(d0 + j) / 8] = make_uint4(
+                                    on ? pack<DT>(v[0], v[1]) : 0u, on ? pack<DT>(v[2], v[3]) : 0u,
+                                    on ? pack<DT>(v[4], v[5]) : 0u, on ? pack<DT>(v[6], v[7]) : 0u);
+                            }
+                        } else if (live) {
+                            // [column][row]: a warp's store is one line
+                            float *o = P.part + at * C::DP + (panel * PANEL + d0) * BM + r;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (panel * PANEL + d0 + j < P.D)
+                                    o[j * BM] = some ? __uint_as_float(a[j]) : 0.0f;
+                        }
+                    }
+                    if (whole) {
+                        // 8 lanes exchange so that each holds one 16-byte chunk of 8 rows: a
+                        // store then covers 128 bytes of 4 rows, not 16 of 32 rows
+                        exchange8(u, lane);
+                        const int d = panel * PANEL + (lane & 7) * 8;
+                        const uint32_t rows = __ballot_sync(0xffffffffu, live);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int from = (lane & ~7) | k;
+                            const int64_t at_row = __shfl_sync(0xffffffffu, orow, from);
+                            if (((rows >> from) & 1u) && d < P.D)
+                                *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(P.out) +
+                                                           at_row * P.D + d) = u[k];
+                        }
+                    }
+                }
+                if (live) {
+                    if (!whole)
+                        P.part_ml[at + r] = make_float2(top, sum);
+                    else if (P.lse)
+                        P.lse[orow] = lse_of(base, sum);
+                }
+            }
+            tc_fence_before();
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(HELPER_REGS));
+        if (warp == 8) {
+            // ------------------------------------------------ TMA of K and V
+            uint32_t t0 = 0;                     // tiles of earlier pieces
+            uint32_t loaded_k = 0, loaded_v = 0; // tiles that a load was issued for
+            bool ok = true;
+            Piece p = {};
+            // one tile's keys (side 0) or values (1): a box of rows per lane
+            auto load = [&](int side, int i) {
+                const int jt = p.tile0 + i;
+                const int keys = tile_keys(p, jt);
+                const int rows = P.page_rows, at = lane * rows;
+                const bool mine = at < keys;
+                int y = jt * KT + at, w = p.b;
+                if (P.page_table && mine) {
+                    const int e = y / P.page_size;
+                    w = __ldg(P.page_table + (size_t)p.b * P.pages_per_seq + e);
+                    y -= e * P.page_size;
+                }
+                const uint32_t n = t0 + (uint32_t)i, stages = side ? C::VST : C::KST;
+                const int st = (int)(n % stages);
+                ok = wait(side ? &S.vempty[st] : &S.kempty[st], ((n / stages) & 1u) ^ 1u);
+                if (!ok)
+                    return;
+                unsigned long long *full = side ? &S.vfull[st] : &S.kfull[st];
+                if (lane == 0)
+                    mbar_arrive_expect_tx(
+                        full, (uint32_t)(((keys + rows - 1) / rows) * rows * 128 * NP));
+                __syncwarp();
+                (side ? loaded_v : loaded_k) = n + 1;
+                if (mine) {
+                    const CUtensorMap *map = side ? &mvc : &mkc;
+                    const uint32_t dst =
+                        (side ? v_s : k_s) + (uint32_t)(st * C::TILE + at * 128);
+#pragma unroll
+                    for (int d = 0; d < NP; ++d)
+                        tma_load_4d(dst + d * PANEL_BYTES, map, d * PANEL, y, p.h, w, full);
+                }
+                __syncwarp();
+            };
+            while (ok && next(p)) {
+                if (p.idle)
+                    continue;
+                for (int i = 0; i < p.n && ok; ++i) {
+                    load(0, i);
+                    if (ok)
+                        load(1, i);
+                }
+                t0 += (uint32_t)p.n;
+            }
+            if (lane == 0) {
+                S.loaded[0] = loaded_k;
+                S.loaded[1] = loaded_v;
+            }
+        } else if (warp == 9) {
+            // -------------------------------------------- issuer of the products
+            // The whole warp runs the loop and one elected lane issues: what the products are
+            // given then stays in uniform registers.  A step of group G: O(i) += P V(i), then
+            // S = Q K(i + 1)^T; in the usual case one test covers both tiles and one elected
+            // block issues all of it.
+            uint32_t items = 0;
+            bool ok = true;
+            const int ksteps = (P.D + 15) / 16;
+            const uint32_t id_o = idesc<DT>(ksteps * 16, true);
+            Piece p = {};
+            int kst = 0, vst = 0;                // stages and phases of the next K and V tile
+            uint32_t kph = 0, vph = 0, pph[2] = {0, 0};
+            constexpr uint32_t id_s = idesc<DT>(KT, false);
+            const uint64_t qd0 = desc_k(q_s), kd0 = desc_k(k_s), vd0 = desc_mn(v_s);
+            constexpr uint64_t TILE16 = C::TILE >> 4;
+            int plain = 0;
+            auto next_k = [&]() {
+                kph ^= kst + 1 == C::KST ? 1u : 0u;
+                kst = kst + 1 == C::KST ? 0 : kst + 1;
+            };
+            auto next_v = [&]() {
+                vph ^= vst + 1 == C::VST ? 1u : 0u;
+                vst = vst + 1 == C::VST ? 0 : vst + 1;
+            };
+            // commits behind the scores of tile i
+            auto scored = [&](int s, int i) {
+                if (s)
+                    mma_commit(&S.kempty[kst]);
+                mma_commit(&S.sfull[s]);
+                if (i == p.n - 1 && s)
+                    mma_commit(&S.qempty);
+            };
+            auto scores = [&](int s, int i) {    // S = Q K(i)^T by itself
+                const int keys = tile_keys(p, p.tile0 + i);
+                ok = wait(&S.kfull[kst], kph);
+                if (!ok)
+                    return;
+                tc_fence_after();
+                const uint32_t id = idesc<DT>((keys + 15) & ~15, false);
+                const uint32_t d = tmem + (uint32_t)(s * KT);
+                const uint64_t qd = qd0 + s * TILE16, kd = kd0 + kst * TILE16;
+                if (elect_one()) {
+#pragma unroll 1
+                    for (int x = 0; x < ksteps; ++x) {
+                        const uint64_t off =
+                            (uint64_t)(((x >> 2) * PANEL_BYTES + (x & 3) * 32) >> 4);
+                        mma_ss(d, qd + off, kd + off, id, x ? 1u : 0u);
+                    }
+                    scored(s, i);
+                }
+                __syncwarp();
+                if (s)
+                    next_k();
+            };
+            auto step = [&](auto group, int i) {
+                constexpr int G = decltype(group)::value;
+                const uint32_t t_s = tmem + (uint32_t)(G * KT);
+                const uint32_t t_o = tmem + (uint32_t)(2 * KT + G * C::DP);
+                const uint64_t vd = vd0 + vst * TILE16;
+                const uint32_t more = i >= 1 ? 1u : 0u;
+                const bool usual = i + 1 < plain && ksteps == NP * 4;
+                // (the second group finds the first one's tiles)
+                ok = wait(&S.pready[G], pph[G]);
+                if (!ok)
+                    return;
+                const bool all = usual && (G ||
+                                           warp_try2(&S.vfull[vst], vph, &S.kfull[kst], kph));
+                if (all) {
+                    tc_fence_after();
+                    const uint64_t qd = qd0 + G * TILE16, kd = kd0 + kst * TILE16;
+                    if (elect_one()) {
+                        // 16 keys a step: 8 columns of P, 2 KB of V
+#pragma unroll
+                        for (int x = 0; x < KT / 16; ++x)
+                            mma_ts(t_o, t_s + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)),
+                                   id_o, x ? 1u : more);
+                        if (G)
+                            mma_commit(&S.vempty[vst]);
+#pragma unroll
+                        for (int x = 0; x < NP * 4; ++x) {
+                            const uint64_t off =
+                                (uint64_t)(((x >> 2) * PANEL_BYTES + (x & 3) * 32) >> 4);
+                            mma_ss(t_s, qd + off, kd + off, id_s, x ? 1u : 0u);
+                        }
+                        scored(G, i + 1);
+                    }
+                    __syncwarp();
+                    if (G)
+                        next_k();
+                } else {
+                    const int keys = tile_keys(p, p.tile0 + i);
+                    ok = wait(&S.vfull[vst], vph);
+                    if (!ok)
+                        return;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const int steps = (keys + 15) / 16;
+#pragma unroll 1
+                        for (int x = 0; x < steps; ++x)
+                            mma_ts(t_o, t_s + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)),
+                                   id_o, x ? 1u : more);
+                        if (G)
+                            mma_commit(&S.vempty[vst]);
+                        if (commits_done(i, plain, 1, p.n))
+                            mma_commit(&S.pvdone[G]);
+                    }
+                    __syncwarp();
+                    if (i + 1 < p.n)
+                        scores(G, i + 1);
+                }
+                pph[G] ^= 1u;
+                if (G)
+                    next_v();
+            };
+            while (ok && next(p)) {
+                if (p.idle)
+                    continue;
+                plain = plain_tiles(p);
+                ok = wait(&S.qfull, items & 1u);
+                ++items;
+                if (ok)
+                    scores(0, 0);
+                if (ok)
+                    scores(1, 0);
+                for (int i = 0; i < p.n && ok; ++i) {
+                    step(Int<0>(), i);
+                    if (ok)
+                        step(Int<1>(), i);
+                }
+            }
+        } else if (warp == 10) {
+            // ---------------------------------------------------- TMA of Q
+            uint32_t items = 0;
+            Piece p = {};
+            while (next(p)) {
+                if (p.idle)
+                    continue;
+                if (!wait_idle(&S.qempty, (items & 1u) ^ 1u))
+                    break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(
+                        &S.qfull, (uint32_t)(P.tokens_per_tile * P.G * 128 * NP * 2));
+                    for (int i = 0; i < NP * 2; ++i)
+                        tma_load_4d(q_s + i * PANEL_BYTES, &mq, (i % NP) * PANEL, 0,
+                                    p.row0 + (i / NP) * P.tokens_per_tile, p.h, &S.qfull);
+                }
+                __syncwarp();
+                ++items;
+            }
+            if (lane == 0)
+                S.loaded[2] = items;
+        } else {
+            // ------------------------------------------- the share's pieces
+            Walk walk(P, slot);
+            for (uint32_t k = 0;; ++k) {
+                const int at = (int)(k % RING);
+                if (!wait_idle(&S.pempty[at], ((k / RING) & 1u) ^ 1u))
+                    break;
+                const Piece p = walk.piece();
+                if (lane == 0) {
+                    S.piece[at] = p;
+                    mbar_arrive(&S.pfull[at]);
+                }
+                __syncwarp();
+                if (p.n == 0)
+                    break;
+                walk.go_on(P, p.n);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag) {
+        // Every role has ended, some perhaps before the one that gave up: what they left in flight
+        // lands first (bounded).  Each barrier's last phase that has a load, and the products.
+        if (warp == 8) {
+            for (int side = 0; side < 2; ++side) {
+                const uint32_t stages = side ? C::VST : C::KST, n = S.loaded[side];
+                for (uint32_t st = 0; st < stages && st < n; ++st)
+                    (void)mbar_wait(side ? &S.vfull[st] : &S.kfull[st], ((n - 1 - st) / stages) & 1u);
+            }
+        } else if (warp == 9) {
+            if (elect_one())
+                mma_commit(&S.drain);
+            __syncwarp();
+            (void)mbar_wait(&S.drain, 0u);
+        } else if (warp == 10 && S.loaded[2] > 0) {
+            (void)mbar_wait(&S.qfull, (S.loaded[2] - 1) & 1u);
+        } else if (warp < 8) {
+            void_share(P, slot, tid);
+        }
+        __syncthreads();
+    }
+    if (warp == 9) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------- joining
+
+constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_ROWS = 32;
+constexpr int JOIN_UNROLL = 2;    // pieces whose sums a thread has in flight
+
+// Joins the pieces of the items that lie across a share's end.  CTA x takes the item that the end
+// of share x cuts (when no earlier end cuts it), 32 rows of one of its row tiles: a row per lane,
+// an eighth of the columns per warp.  Where there are fewer rows, the lanes left over take pieces
+// of their own.
+template <int NP, int DT>
+__global__ void __launch_bounds__(JOIN_WARPS * 32, 4)
+    chunk_join_kernel(const __grid_constant__ KParams P)
+{
+    using C = Cfg<NP>;
+    constexpr int COLS = C::DP / JOIN_WARPS;
+    __shared__ __align__(16) uint16_t tile[JOIN_ROWS][C::DP + 8];
+    const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
+    const int mine = lane & (P.join_rows - 1), part = lane / P.join_rows;
+    const int parts = 32 / P.join_rows;
+    const int r = (int)blockIdx.z * JOIN_ROWS + mine, s = (int)blockIdx.y;
+    allow_next_kernel();
+    // (the plan is complete: every CTA of the attention had waited for it before this grid began)
+    Place q = empty_place(P);
+    const long long all = q.total * P.Hkv, per = share(P, all);
+    const long long end = ((long long)blockIdx.x + 1) * per;
+    if (end < all)
+        look_up(P, end, q);
+    wait_previous_kernel();
+    if (end >= all)
+        return;
+    const long long item = end - q.tile;  // its first unit
+    if (item == end || item < end - per || q.x.bad || q.status != 0)
+        return;  // not cut here, or the previous end has it, or a sequence in error
+    const int local = r / P.G, g = r - local * P.G;
+    const int tok = s * P.tokens_per_tile + local;
+    const bool live = local < P.tokens_per_tile && tok < q.x.ntok;
+    const int64_t orow = ((int64_t)q.x.row0 + tok) * P.Hq + (int64_t)q.h * P.G + g;
+    const int s0 = (int)blockIdx.x, n = (int)((item + q.x.tiles - 1) / per) - s0 + 1;
+    // a share that starts with the item, or inside it, left its first piece; one that the item
+    // starts inside of left its second
+    auto at = [&](int k) -> size_t {
+        const int which = (long long)(s0 + k) * per >= item ? 0 : 1;
+        return (((size_t)(s0 + k) * 2 + s) * 2 + which) * BM;
+    };
+    float a_top = -INFINITY, a_sum = 0.0f, a_o[COLS];
+    bool a_some = false;
+#pragma unroll
+    for (int j = 0; j < COLS; ++j)
+        a_o[j] = 0.0f;
+    if (live)
+        for (int k0 = part; k0 < n; k0 += JOIN_UNROLL * parts) {
+            float2 ml[JOIN_UNROLL];
+            float x[JOIN_UNROLL][COLS];
+#pragma unroll
+            for (int u = 0; u < JOIN_UNROLL; ++u) {
+                const int k = k0 + u * parts;
+                ml[u] = make_float2(-INFINITY, 0.0f);
+                if (k < n) {
+                    ml[u] = __ldcg(&P.part_ml[at(k) + r]);
+                    const float *v = P.part + at(k) * C::DP + (size_t)(warp * COLS) * BM + r;
+#pragma unroll
+                    for (int j = 0; j < COLS; ++j)
+                        x[u][j] = warp * COLS + j < P.D ? __ldcg(v + j * BM) : 0.0f;
+                }
+            }
+            float top = a_top;
+#pragma unroll
+            for (int u = 0; u < JOIN_UNROLL; ++u)
+                top = fmaxf(top, ml[u].x);
+            const float base = top == -INFINITY ? 0.0f : top;
+            const float f = a_some ? ex2(a_top - base) : 0.0f;
+            a_sum *= f;
+#pragma unroll
+            for (int j = 0; j < COLS; ++j)
+                a_o[j] *= f;
+#pragma unroll
+            for (int u = 0; u < JOIN_UNROLL; ++u) {
+                if (ml[u].x == -INFINITY && ml[u].y == 0.0f)
+                    continue;  // no key seen there
+                const float w = ex2(ml[u].x - base);
+                a_sum = fmaf(ml[u].y, w, a_sum);
+#pragma unroll
+                for (int j = 0; j < COLS; ++j)
+                    a_o[j] = fmaf(x[u][j], w, a_o[j]);
+                a_some = true;
+            }
+            a_top = top;
+        }
+    for (int d = P.join_rows; d < 32; d <<= 1) {
+        const float top2 = __shfl_xor_sync(0xffffffffu, a_top, d);
+        const float sum2 = __shfl_xor_sync(0xffffffffu, a_sum, d);
+        const bool some2 = __shfl_xor_sync(0xffffffffu, a_some ? 1 : 0, d) != 0;
+        const float top = fmaxf(a_top, top2), base = top == -INFINITY ? 0.0f : top;
+        const float f = a_some ? ex2(a_top - base) : 0.0f, f2 = some2 ? ex2(top2 - base) : 0.0f;
+        a_sum = a_sum * f + sum2 * f2;
+#pragma unroll
+        for (int j = 0; j < COLS; ++j)
+            a_o[j] = a_o[j] * f + __shfl_xor_sync(0xffffffffu, a_o[j], d) * f2;
+        a_top = top;
+        a_some |= some2;
+    }
+    const float norm = a_sum != 0.0f ? 1.0f / a_sum : 0.0f;
+    if (part == 0) {
+#pragma unroll
+        for (int j = 0; j < COLS; j += 2)
+            *reinterpret_cast<uint32_t *>(&tile[mine][warp * COLS + j]) =
+                a_sum != 0.0f ? pack<DT>(a_o[j] * norm, a_o[j + 1] * norm) : 0u;
+        if (warp == 0 && live && P.lse)
+            P.lse[orow] = lse_of(a_top == -INFINITY ? 0.0f : a_top, a_sum);
+    }
+    __syncthreads();
+    const uint32_t rows = __ballot_sync(0xffffffffu, live && part == 0);
+#pragma unroll
+    for (int k = 0; k < JOIN_ROWS / JOIN_WARPS; ++k) {
+        const int y = warp * (JOIN_ROWS / JOIN_WARPS) + k;
+        const int64_t to = __shfl_sync(0xffffffffu, orow, y);
+        const int d = lane * 4;
+        if (((rows >> y) & 1u) && d < P.D)
+            *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(P.out) + to * P.D + d) =
+                *reinterpret_cast<const uint2 *>(&tile[y][d]);
+    }
+}
+
+// ------------------------------------------------------------------- host
+
+bool heads_ok(int32_t Hq, int32_t Hkv, int32_t D)
+{
+    return Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hq / Hkv <= BM && Hq <= 65535 && D >= 8 &&
+           D % 8 == 0 && D <= SPEC_ATTN_MAX_HEAD_DIM;
+}
+
+struct WsLayout {
+    size_t ml, part, total;
+};
+
+WsLayout ws_layout(int D)
+{
+    const size_t dp = D > PANEL ? 2 * PANEL : PANEL;
+    WsLayout w;
+    w.ml = 0;
+    w.part = plan_align(w.ml + (size_t)MAX_CTAS * 2 * 2 * BM * sizeof(float2));
+    w.total = plan_align(w.part + (size_t)MAX_CTAS * 2 * 2 * BM * dp * sizeof(float));
+    return w;
+}
+
+struct DevInfo {
+    std::atomic<int> sms;
+    std::atomic<bool> attr[2][2];
+};
+DevInfo g_dev[64];
+
+template <int NP, int DT>
+int launch(const CUtensorMap (&maps)[3], KParams &P, int rows, int sms, DevInfo &di,
+           cudaStream_t st)
+{
+    if (!di.attr[NP - 1][DT - 1].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(chunk_kernel<NP, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)smem_bytes<NP>()) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return SPEC_ECUDA;
+        }
+        di.attr[NP - 1][DT - 1].store(true, std::memory_order_release);
+    }
+    P.slots = sms < MAX_CTAS ? sms : MAX_CTAS;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned int)P.slots);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem_bytes<NP>();
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, chunk_kernel<NP, DT>, maps[0], maps[1], maps[2], P) !=
+        cudaSuccess) {
+        (void)cudaGetLastError();
+        return SPEC_ECUDA;
+    }
+    if (P.slots > 1) {
+        const int most = P.tokens_per_tile < rows ? P.tokens_per_tile * P.G : rows * P.G;
+        P.join_rows = JOIN_ROWS;
+        while (P.join_rows / 2 >= most)
+            P.join_rows /= 2;
+        cfg.gridDim = dim3((unsigned int)(P.slots - 1), rows > P.tokens_per_tile ? 2u : 1u,
+                           (unsigned int)((most + JOIN_ROWS - 1) / JOIN_ROWS));
+        cfg.blockDim = dim3(JOIN_WARPS * 32);
+        cfg.dynamicSmemBytes = 0;
+        if (cudaLaunchKernelEx(&cfg, chunk_join_kernel<NP, DT>, P) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return SPEC_ECUDA;
+        }
+    }
+    return SPEC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t spec_chunk_attention_workspace_size(int32_t Hq, int32_t Hkv, int32_t D)
+{
+    return heads_ok(Hq, Hkv, D) ? ws_layout(D).total : 0;
+}
+
+int32_t spec_chunk_attention(const spec_chunk_attention_args *args, void *workspace,
+                             size_t workspace_bytes, void *stream)
+{
+    if (!args)
+        return SPEC_EINVAL;
+    const spec_chunk_attention_args &a = *args;
+    const bool paged = a.page_table != nullptr;
+    if (!heads_ok(a.Hq, a.Hkv, a.D) || a.B < 0 || a.B > 65535 || a.rows < 0 ||
+        a.rows > SPEC_CHUNK_MAX_ROWS || !page_size_ok(a.page_size, paged) || a.pages_per_seq < 1 ||
+        a.num_pages < 0 ||
+        (long long)a.pages_per_seq * a.page_size > INT32_MAX - SPEC_CHUNK_MAX_ROWS ||
+        (a.dtype != SPEC_BF16 && a.dtype != SPEC_F16) || !(a.scale > 0.0f) || isinf(a.scale))
+        return SPEC_EINVAL;
+    if (a.B == 0 || a.rows == 0)
+        return SPEC_OK;
+    const void *bases[] = {a.q, a.k_cache, a.v_cache, a.out};
+    for (const void *p : bases)
+        if (!p || !aligned(p, 16))
+            return SPEC_EINVAL;
+    const int64_t qs3[3] = {a.q_stride[0], a.q_stride[1], 0};
+    if (!strides_ok(qs3) || !strides_ok(a.k_cache_stride) || !strides_ok(a.v_cache_stride) ||
+        !a.plan || !aligned(a.plan, 256) || !workspace || !aligned(workspace, 256) ||
+        !aligned(a.page_table, 4) || !aligned(a.out_lse, 4) ||
+        (!paged && (a.pages_per_seq != 1 || a.num_pages < a.B)))
+        return SPEC_EINVAL;
+    // TMA steps along a dimension by its stride: none may be 0 where there are two entries
+    auto stepped = [&](const int64_t (&s)[3]) {
+        return (a.num_pages < 2 || s[0] > 0) && (a.page_size < 2 || s[1] > 0) &&
+               (a.Hkv < 2 || s[2] > 0);
+    };
+    if (!stepped(a.k_cache_stride) || !stepped(a.v_cache_stride) ||
+        (a.rows > 1 && a.q_stride[0] == 0) || (a.Hq > 1 && a.q_stride[1] == 0))
+        return SPEC_EINVAL;
+    const WsLayout w = ws_layout(a.D);
+    if (workspace_bytes < w.total)
+        return SPEC_ENOSPACE;
+
+    KParams P;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const int32_t G = a.Hq / a.Hkv;
+    P.plan = static_cast<const uint8_t *>(a.plan);
+    P.lay = chunk_layout(a.B, a.rows, G);
+    P.page_table = a.page_table;
+    P.v_cache = a.v_cache;
+    for (int i = 0; i < 3; ++i)
+        P.v_cache_stride[i] = a.v_cache_stride[i];
+    P.out = a.out;
+    P.lse = a.out_lse;
+    P.status = &reinterpret_cast<ChunkHeader *>(const_cast<void *>(a.plan))->status;
+    P.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
+    P.part = reinterpret_cast<float *>(ws + w.part);
+    P.c = a.scale * LOG2E;
+    P.Hq = a.Hq;
+    P.Hkv = a.Hkv;
+    P.D = a.D;
+    P.G = G;
+    P.tokens_per_tile = BM / G;
+    P.page_size = a.page_size;
+    P.pages_per_seq = a.pages_per_seq;
+    P.page_rows = paged && a.page_size < KT ? a.page_size : KT;
+
+    CUtensorMap maps[3];
+    const uint64_t qd[4] = {(uint64_t)a.D, (uint64_t)G, (uint64_t)a.rows, (uint64_t)a.Hkv};
+    const int64_t qs[3] = {a.q_stride[1], a.q_stride[0], a.q_stride[1] * G};
+    const uint32_t qb[4] = {PANEL, (uint32_t)G, (uint32_t)P.tokens_per_tile, 1};
+    const uint64_t cd[4] = {(uint64_t)a.D, (uint64_t)a.page_size, (uint64_t)a.Hkv,
+                            (uint64_t)(a.num_pages > 0 ? a.num_pages : 1)};
+    const uint32_t cb[4] = {PANEL, (uint32_t)P.page_rows, 1, 1};
+    const int64_t kc[3] = {a.k_cache_stride[1], a.k_cache_stride[2], a.k_cache_stride[0]};
+    const int64_t vc[3] = {a.v_cache_stride[1], a.v_cache_stride[2], a.v_cache_stride[0]};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return SPEC_ECUDA;
+    if (!make_map(&maps[0], a.q, a.dtype, 4, qd, qs, qb) ||
+        !make_map(&maps[1], a.k_cache, a.dtype, 4, cd, kc, cb) ||
+        !make_map(&maps[2], a.v_cache, a.dtype, 4, cd, vc, cb))
+        return SPEC_ECUDA;
+    DevInfo &di = g_dev[dev];
+    int sms = di.sms.load(std::memory_order_relaxed);
+    if (!sms) {
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            sms < 1)
+            return SPEC_ECUDA;
+        di.sms.store(sms, std::memory_order_relaxed);
+    }
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (a.dtype == SPEC_BF16)
+        return a.D > PANEL ? launch<2, SPEC_BF16>(maps, P, a.rows, sms, di, st)
+                           : launch<1, SPEC_BF16>(maps, P, a.rows, sms, di, st);
+    return a.D > PANEL ? launch<2, SPEC_F16>(maps, P, a.rows, sms, di, st)
+                       : launch<1, SPEC_F16>(maps, P, a.rows, sms, di, st);
+}
+
+}  // extern "C"
