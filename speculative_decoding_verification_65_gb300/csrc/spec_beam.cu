@@ -2,13 +2,15 @@
 // order of the selected (include/spec_beam.h).
 //
 // Selection, first kernel: one pass over the logits of the live beams.  A row is cut into segments,
-// one per CTA; each keeps the running sum of exponentials and the segment's n largest logits.
-// Within a beam candidates are ordered by their logits alone (one constant per beam makes scores of
-// them), so no candidate needs the row's total.  A logit joins the CTA's candidates when it is above
-// the n-th best so far; the first tile starts from the n-th largest of its threads' own maxima (of 8 threads per warp), so
-// few do.
-// The last CTA of a sequence joins its rows' totals and merges the sorted lists of all segments:
-// n rounds of the best head.  Bound by the bytes of the logits.
+// one per CTA.  A thread reads 4 vectors at a time (a group), adds to its running sum of exponentials
+// and notes the group's maximum; no thread waits for another.  Within a beam candidates are ordered by
+// their logits alone (one constant per beam makes scores of them), so no candidate needs the row's
+// total: when the segment has been read, the n-th largest of the threads' own maxima (of 8 threads per
+// warp) bounds its n best logits from below, the few groups that reach the bound are
+// read again, and their elements that do are sorted.
+// The last CTA of a sequence joins its rows' totals and merges the sorted lists of all segments: the
+// n-th best head bounds the result, so at most n lists have entries in it; those are sorted.
+// Bound by the bytes of the logits.
 //
 // Orders between beams hang on the difference of two logarithms of sums, which fp32 gives to a few
 // 1e-6.  Where two neighbours of different beams lie nearer than that, the sequence is listed,
@@ -21,6 +23,8 @@
 #include <limits.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "spec_beam.h"
 #include "spec_verify.h"
@@ -36,9 +40,10 @@ typedef unsigned long long u64;
 constexpr int TH = 256;            // threads of a CTA
 constexpr int WARPS = TH / 32;
 static_assert(8 * WARPS >= SPEC_BEAM_MAX, "the first bound comes from 8 threads of a warp");
-constexpr int UN = 4;              // vectors of a thread in a tile
+constexpr int UN = 4;              // vectors of a group
+constexpr int GROUPS = 16;         // most groups of a thread, in a segment
 constexpr int CAP = 1024;          // candidates of a segment before they are cut
-constexpr int MAX_LISTS = 2 * TH;  // segments of a sequence's beams
+constexpr int MAX_LISTS = 2048;    // segments of a sequence's beams: 1216 / K + 1, or 19 for the longest rows
 constexpr int EXACT_CTAS = 304;
 constexpr size_t MAX_B = 65536;    // sequences that the counters have room for
 // How far a row's logarithm of its total may be off, in nats: exponents' rounding (2^-23 of up to
@@ -95,15 +100,31 @@ struct ScanSmem {
     u64 most[WARPS];
     uint32_t bound;
     int count;
-    int last;
 };
 
 struct PickSmem {
     double lse[SPEC_BEAM_MAX], score[SPEC_BEAM_MAX], inv[SPEC_BEAM_MAX];
-    float top[SPEC_BEAM_MAX];
-    u64 rank[2][WARPS];
-    int flat[2][WARPS], list[2][WARPS];
+    u64 rank[SPEC_BEAM_MAX + 1];  // the best n and the next, sorted
+    int flat[SPEC_BEAM_MAX + 1], entry[SPEC_BEAM_MAX + 1];
+    u64 least;
+    int least_flat;
+    int count;
 };
+
+// Shared memory that a kernel is launched with: the groups' maxima of the scan, or a merge's heads
+// of lists (order, k V + x) and then what it has to sort, up to n entries of n lists (a place too).
+constexpr size_t larger(size_t a, size_t b) { return a > b ? a : b; }
+constexpr size_t merge_bytes(int n, int lists)
+{
+    return larger((size_t)n * n * 16, (size_t)lists * 12);
+}
+constexpr size_t SCAN_BYTES = (size_t)GROUPS * TH * 4;
+extern __shared__ __align__(16) uint8_t dyn[];
+
+__device__ __forceinline__ bool better(u64 r1, int f1, u64 r2, int f2)
+{
+    return r1 > r2 || (r1 == r2 && f1 < f2);
+}
 
 // The candidates' best n, sorted, to S.cand; returns the order that a later one has to exceed.
 // The whole CTA; S.count candidates (at most CAP).
@@ -185,162 +206,265 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
         }
         return true;
     }
-    // a thread's lists: two heads at most
-    const int lists = A.K * P.segs;
-    u64 rank[2];
-    int flat[2], at[2] = {0, 0};
-    auto load = [&](int c) {
-        rank[c] = 0;
-        flat[c] = INT_MAX;
-        const int l = tid + c * TH;
-        if (l >= lists || at[c] >= A.n)
-            return;
+    // candidate `at` of list l: its order (0: none) and k V + x
+    const int lists = A.K * P.segs, n = A.n;
+    auto load = [&](int l, int at, int &flat) -> u64 {
         const int k = l / P.segs, row = b * A.K + k;
+        flat = INT_MAX;
         if (A.scores[row] == -INFINITY)
-            return;
+            return 0;
         if (A.finished && A.finished[row] != 0) {
-            if (at[c] == 0 && l == k * P.segs) {
-                rank[c] = ordered(S.score[k] * S.inv[k]);
-                flat[c] = k * A.V + A.end_token;
-            }
-            return;
+            if (at > 0 || l != k * P.segs)
+                return 0;
+            flat = k * A.V + A.end_token;
+            return ordered(S.score[k] * S.inv[k]);
         }
-        const u64 key = __ldcg(&P.lists[((size_t)row * P.segs + (l - k * P.segs)) * A.n + at[c]]);
-        if (key) {
-            rank[c] = ordered((S.score[k] + ((double)value_of(key) - S.lse[k])) * S.inv[k]);
-            flat[c] = k * A.V + token_of(key);
-        }
+        const u64 key = __ldcg(&P.lists[((size_t)row * P.segs + (l - k * P.segs)) * n + at]);
+        if (key == 0)
+            return 0;
+        flat = k * A.V + token_of(key);
+        return ordered((S.score[k] + ((double)value_of(key) - S.lse[k])) * S.inv[k]);
     };
-    load(0);
-    load(1);
-    auto better = [](u64 r1, int f1, u64 r2, int f2) { return r1 > r2 || (r1 == r2 && f1 < f2); };
-    u64 r_before = 0;
-    int k_before = -1;
-    bool open = false;
-    // one round more than is written: the next one may lie too near
-    for (int i = 0; i <= A.n; ++i) {
-        const int c = better(rank[1], flat[1], rank[0], flat[0]) ? 1 : 0;
-        u64 r = c ? rank[1] : rank[0];
-        int f = c ? flat[1] : flat[0], l = tid + c * TH;
-        for (int d = 16; d; d >>= 1) {
-            const u64 r2 = __shfl_xor_sync(0xffffffffu, r, d);
-            const int f2 = __shfl_xor_sync(0xffffffffu, f, d);
-            const int l2 = __shfl_xor_sync(0xffffffffu, l, d);
-            if (better(r2, f2, r, f)) {
-                r = r2;
-                f = f2;
-                l = l2;
-            }
+    // the n-th best head: no more than n lists reach it
+    u64 *rank = reinterpret_cast<u64 *>(dyn);
+    int *flat = reinterpret_cast<int *>(rank + lists);
+    for (int l = tid; l < lists; l += TH)
+        rank[l] = load(l, 0, flat[l]);
+    if (tid == 0) {
+        S.least = 0;
+        S.least_flat = INT_MAX;
+        S.count = 0;
+    }
+    if (tid <= n)
+        S.rank[tid] = 0;
+    __syncthreads();
+    for (int l = tid; l < lists; l += TH) {
+        const u64 r = rank[l];
+        const int f = flat[l];
+        int place = 0;
+        for (int j = 0; j < lists && place < n; ++j)
+            place += better(rank[j], flat[j], r, f) ? 1 : 0;
+        if (r != 0 && place == n - 1) {
+            S.least = r;
+            S.least_flat = f;
         }
-        if (lane == 0) {
-            S.rank[i & 1][warp] = r;
-            S.flat[i & 1][warp] = f;
-            S.list[i & 1][warp] = l;
-        }
-        __syncthreads();
-        r = 0;
-        f = INT_MAX;
-        l = -1;
-        for (int w = 0; w < WARPS; ++w)
-            if (better(S.rank[i & 1][w], S.flat[i & 1][w], r, f)) {
-                r = S.rank[i & 1][w];
-                f = S.flat[i & 1][w];
-                l = S.list[i & 1][w];
-            }
-        if (r == 0) {  // none left
-            for (int j = i + tid; j < A.n; j += TH) {
-                A.out_tokens[out + j] = -1;
-                A.out_beams[out + j] = -1;
-                A.out_scores[out + j] = -INFINITY;
-            }
-            break;
-        }
-        const int k = f / A.V;
-        if (!EXACT && k_before >= 0 && k != k_before) {
-            const double off = LSE_OFF * (S.inv[k] + S.inv[k_before]);
-            open |= !(rank_of(r_before) - rank_of(r) > off);
-        }
-        r_before = r;
-        k_before = k;
-        if (i == A.n)
-            break;
-        if (l == tid || l == tid + TH) {
-            const int c = l == tid ? 0 : 1;
-            const bool fin = A.finished && A.finished[b * A.K + k] != 0;
-            float score = (float)S.score[k];
-            if (!fin) {
-                const u64 key = __ldcg(&P.lists[((size_t)b * lists + l) * A.n + (c ? at[1] : at[0])]);
-                score = (float)(S.score[k] + ((double)value_of(key) - S.lse[k]));
-            }
-            A.out_tokens[out + i] = f - k * A.V;
-            A.out_beams[out + i] = k;
-            A.out_scores[out + i] = score;
-            if (c == 0) {
-                ++at[0];
-                load(0);
-            } else {
-                ++at[1];
-                load(1);
+    }
+    __syncthreads();
+    // the entries that reach it (n n of them at most, in the place of the heads)
+    flat = reinterpret_cast<int *>(rank + n * n);
+    int *entry = flat + n * n;
+    const u64 least = S.least;
+    const int least_flat = S.least_flat;
+    for (int e = tid; e < lists * n; e += TH) {
+        int f;
+        const u64 r = load(e / n, e % n, f);
+        if (r != 0 && !better(least, least_flat, r, f)) {
+            const int i = atomicAdd(&S.count, 1);
+            if (i < n * n) {
+                rank[i] = r;
+                flat[i] = f;
+                entry[i] = e;
             }
         }
     }
-    return !open;
+    __syncthreads();
+    const int m = min(S.count, n * n);
+    for (int i = tid; i < m; i += TH) {
+        const u64 r = rank[i];
+        const int f = flat[i];
+        int place = 0;
+        for (int j = 0; j < m && place <= n; ++j)
+            place += better(rank[j], flat[j], r, f) ? 1 : 0;
+        if (place <= n) {
+            S.rank[place] = r;
+            S.flat[place] = f;
+            S.entry[place] = entry[i];
+        }
+    }
+    __syncthreads();
+    bool open = false;
+    if (tid < n) {
+        int token = -1, beam = -1;
+        float score = -INFINITY;
+        if (S.rank[tid] != 0) {
+            const int k = S.flat[tid] / A.V, e = S.entry[tid];
+            beam = k;
+            token = S.flat[tid] - k * A.V;
+            score = (float)S.score[k];
+            if (!(A.finished && A.finished[b * A.K + k] != 0))
+                score = (float)(S.score[k] +
+                                ((double)value_of(__ldcg(&P.lists[(size_t)b * lists * n + e])) -
+                                 S.lse[k]));
+            // the next one may lie too near
+            if (!EXACT && S.rank[tid + 1] != 0 && S.flat[tid + 1] / A.V != k) {
+                const double off = LSE_OFF * (S.inv[k] + S.inv[S.flat[tid + 1] / A.V]);
+                open = !(rank_of(S.rank[tid]) - rank_of(S.rank[tid + 1]) > off);
+            }
+        }
+        A.out_tokens[out + tid] = token;
+        A.out_beams[out + tid] = beam;
+        A.out_scores[out + tid] = score;
+    }
+    return __syncthreads_or(open ? 1 : 0) == 0;
+}
+
+// A row's segment: whole vectors of the array.  The row's elements before its first one and behind
+// its last (fewer than two vectors) belong to the first segment, one for each of its first threads.
+template <int DT>
+struct Segment {
+    using L = Lg<DT>;
+    const uint4 *src;
+    int mis, v0, v1;
+    int head, tail, edges;  // elements before the vectors, the first one behind, and how many in all
+    const void *base;
+    size_t e0;
+
+    __device__ __forceinline__ Segment(const BeamParams &P, int row, int seg)
+    {
+        const int V = P.a.V;
+        base = P.a.logits;
+        e0 = (size_t)row * V;
+        mis = (int)(e0 % L::VEC);  // elements of the row's first vector before it
+        src = reinterpret_cast<const uint4 *>(base) + e0 / L::VEC;
+        const int f0 = mis > 0 ? 1 : 0, f1 = max(f0, (mis + V) / L::VEC);
+        const int per = (f1 - f0 + P.segs - 1) / P.segs;
+        v0 = f0 + seg * per;
+        v1 = min(f1, v0 + per);
+        head = mis > 0 ? min(V, L::VEC - mis) : 0;
+        tail = max(head, f1 * L::VEC - mis);
+        edges = seg == 0 ? head + V - tail : 0;
+    }
+    __device__ __forceinline__ uint4 fetch(int v) const
+    {
+        return v < v1 ? __ldg(src + v) : neg_inf_vec(L::NEG_INF_WORD);
+    }
+    __device__ __forceinline__ int col(int v, int j) const { return v * L::VEC + j - mis; }
+    __device__ __forceinline__ int edge_col(int i) const { return i < head ? i : tail + i - head; }
+    __device__ __forceinline__ float edge(int i) const
+    {
+        return i < edges ? L::load1(base, e0 + edge_col(i)) : -INFINITY;
+    }
+};
+
+// The segment's n best where too many reach the bound (equal logits): tile by tile in order, each
+// tile's best one by one where there are too many of them too.  The whole CTA; to S.cand.
+template <int DT>
+__device__ __noinline__ void scan_again(const Segment<DT> &G, int n, ScanSmem &S)
+{
+    using L = Lg<DT>;
+    const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint32_t above = NONE;
+    int held = 0;  // candidates before the tile
+    auto push_edge = [&](bool head) {
+        const float x = G.edge(tid);
+        if (tid < G.edges && (tid < G.head) == head && ordered(x) > above)
+            S.cand[atomicAdd(&S.count, 1)] = candidate(ordered(x), G.edge_col(tid));
+    };
+    __syncthreads();
+    if (tid == 0)
+        S.count = 0;
+    __syncthreads();
+    push_edge(true);
+    __syncthreads();
+    held = S.count;
+    __syncthreads();
+    for (int t = G.v0; t < G.v1; t += TH * UN) {
+        u64 lower = ~0ull;
+        for (int u = 0; u < UN; ++u) {
+            float x[L::VEC];
+            L::unpack(G.fetch(t + u * TH + tid), x);
+            for (int j = 0; j < L::VEC; ++j) {
+                const uint32_t o = ordered(x[j]);
+                if (o > above) {
+                    const int i = atomicAdd(&S.count, 1);
+                    if (i < CAP)
+                        S.cand[i] = candidate(o, G.col(t + u * TH + tid, j));
+                }
+            }
+        }
+        __syncthreads();
+        int now = S.count;
+        __syncthreads();
+        for (int got = 0; now > CAP; ++got) {
+            u64 most = 0;
+            if (got < n)
+                for (int u = 0; u < UN; ++u) {
+                    float x[L::VEC];
+                    L::unpack(G.fetch(t + u * TH + tid), x);
+                    for (int j = 0; j < L::VEC; ++j) {
+                        const uint32_t o = ordered(x[j]);
+                        const u64 key = candidate(o, G.col(t + u * TH + tid, j));
+                        if (o > above && key < lower && key > most)
+                            most = key;
+                    }
+                }
+            for (int d = 16; d; d >>= 1) {
+                const u64 other = __shfl_xor_sync(0xffffffffu, most, d);
+                most = other > most ? other : most;
+            }
+            if (lane == 0)
+                S.most[warp] = most;
+            __syncthreads();
+            for (int w = 0; w < WARPS; ++w)
+                most = S.most[w] > most ? S.most[w] : most;
+            __syncthreads();
+            if (most == 0) {
+                now = held + got;
+                if (tid == 0)
+                    S.count = now;
+            } else {
+                if (tid == 0)
+                    S.cand[held + got] = most;
+                lower = most;
+            }
+        }
+        above = cut(S, n);
+        held = min(now, n);
+    }
+    push_edge(false);
+    (void)cut(S, n);
 }
 
 template <int DT>
-__global__ void __launch_bounds__(TH) beam_kernel(const __grid_constant__ BeamParams P)
+__global__ void __launch_bounds__(TH, 4) beam_kernel(const __grid_constant__ BeamParams P)
 {
     using L = Lg<DT>;
     const spec_beam_select_args &A = P.a;
-    __shared__ ScanSmem S;
-    __shared__ PickSmem K;
+    __shared__ union {
+        ScanSmem scan;
+        PickSmem pick;
+    } U;
+    __shared__ int last;
+    ScanSmem &S = U.scan;
     const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row = (int)(blockIdx.x / P.segs), seg = (int)(blockIdx.x - row * P.segs);
     const int b = row / A.K, n = A.n;
     allow_next_kernel();
     wait_previous_kernel();
     const bool counts = A.scores[row] > -INFINITY && !(A.finished && A.finished[row] != 0);
-    if (tid == 0)
-        S.count = 0;
-    __syncthreads();
     if (counts) {
-        const size_t e0 = (size_t)row * A.V, all = (size_t)A.B * A.K * A.V;
-        const int mis = (int)(e0 % L::VEC);  // elements of the row's first vector before it
-        const size_t vbase = e0 / L::VEC;
-        const int nvec = (mis + A.V + L::VEC - 1) / L::VEC;
-        const int per = (nvec + P.segs - 1) / P.segs;
-        const int v0 = seg * per, v1 = min(nvec, v0 + per);
-        const uint4 *src = reinterpret_cast<const uint4 *>(A.logits) + vbase;
-        auto fetch = [&](int v) -> uint4 {
-            uint4 r = make_uint4(L::NEG_INF_WORD, L::NEG_INF_WORD, L::NEG_INF_WORD, L::NEG_INF_WORD);
-            if (v >= v1)
-                return r;
-            const bool edge = (v == 0 && mis > 0) || v == nvec - 1;
-            if (!edge)
-                return __ldg(src + v);
-            const uint8_t *p = static_cast<const uint8_t *>(A.logits);
-            for (int j = 0; j < L::VEC; ++j) {
-                const int col = v * L::VEC + j - mis;
-                const size_t e = (vbase + v) * L::VEC + j;
-                if (col >= 0 && col < A.V && e < all)
-                    L::put(r, j, L::bits_at(p + e * L::ES));
-            }
-            return r;
-        };
+        const Segment<DT> G(P, row, seg);
+        float *maxima = reinterpret_cast<float *>(dyn) + tid;  // of the thread's groups
         uint4 raw[UN], ahead[UN];
 #pragma unroll
         for (int u = 0; u < UN; ++u)
-            raw[u] = fetch(v0 + u * TH + tid);
+            raw[u] = G.fetch(G.v0 + u * TH + tid);
         float m = -INFINITY, top = -INFINITY, sum = 0.0f, low = 0.0f;  // sum + low in units of e^m
         bool bad = false;
-        uint32_t above = NONE;
-        int held = 0;  // candidates before the tile
         const u64 c2 = f2(LOG2E, LOG2E);
-        for (int t = v0; t < v1; t += TH * UN) {
+        const float lone = G.edge(tid);
+        if (G.edges > 0) {
+            bad = !(lone < INFINITY);
+            m = top = lone;
+            sum = lone > -INFINITY ? 1.0f : 0.0f;
+        }
+        int groups = 0;
+        for (int t = G.v0; t < G.v1; t += TH * UN) {
 #pragma unroll
             for (int u = 0; u < UN; ++u)
-                ahead[u] = fetch(t + TH * UN + u * TH + tid);
+                ahead[u] = G.fetch(t + TH * UN + u * TH + tid);
             const float tm = L::tile_max(raw);
+            maxima[groups++ * TH] = tm;
             bad |= !(tm < INFINITY);
             top = fmaxf(top, tm);
             if (tm > m + SLACK || m == -INFINITY) {
@@ -362,114 +486,37 @@ __global__ void __launch_bounds__(TH) beam_kernel(const __grid_constant__ BeamPa
                 low += __fadd_rn(__fsub_rn(sum, __fsub_rn(s, back)), __fsub_rn(x, back));
                 sum = s;
             }
-            if (t == v0) {
-                // a bound that n of the tile's elements reach: the n-th of the warps' 8 best threads
-                float mine = tm;
-                for (int i = 0; i < 8; ++i) {
-                    float most = mine;
-                    for (int d = 16; d; d >>= 1)
-                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-                    const uint32_t who = __ballot_sync(0xffffffffu, mine == most);
-                    if (lane == __ffs((int)who) - 1) {
-                        S.best[warp * 8 + i] = candidate(ordered(mine), warp * 8 + i);
-                        mine = -INFINITY;
-                    }
-                }
-                __syncthreads();
-                if (tid < 8 * WARPS) {
-                    const u64 key = S.best[tid];
-                    int rank = 0;
-                    for (int j = 0; j < 8 * WARPS; ++j)
-                        rank += S.best[j] > key ? 1 : 0;
-                    if (rank == n - 1)
-                        S.bound = (uint32_t)(key >> 32);
-                }
-                __syncthreads();
-                above = max(S.bound, NONE + 1) - 1;  // the bound itself included
-            }
-            if (!bad && ordered(tm) > above) {
-#pragma unroll
-                for (int u = 0; u < UN; ++u) {
-                    if (ordered(L::vmax(raw[u])) <= above)
-                        continue;
-                    float x[L::VEC];
-                    L::unpack(raw[u], x);
-#pragma unroll
-                    for (int j = 0; j < L::VEC; ++j) {
-                        const uint32_t o = ordered(x[j]);
-                        if (o > above) {
-                            const int i = atomicAdd(&S.count, 1);
-                            if (i < CAP)
-                                S.cand[i] = candidate(o, (t + u * TH + tid) * L::VEC + j - mis);
-                        }
-                    }
-                }
-            }
-            bad = __syncthreads_or(bad ? 1 : 0) != 0;
-            if (bad)
-                break;
-            int now = S.count;
-            if (now > CAP) {
-                // too many at once (equal logits, rising ones): the tile's n best one by one
-                __syncthreads();
-                u64 lower = ~0ull;
-                int got = 0;
-                for (; got < n; ++got) {
-                    u64 most = 0;
-#pragma unroll
-                    for (int u = 0; u < UN; ++u) {
-                        float x[L::VEC];
-                        L::unpack(raw[u], x);
-#pragma unroll
-                        for (int j = 0; j < L::VEC; ++j) {
-                            const uint32_t o = ordered(x[j]);
-                            const u64 key = candidate(o, (t + u * TH + tid) * L::VEC + j - mis);
-                            if (o > above && key < lower && key > most)
-                                most = key;
-                        }
-                    }
-                    for (int d = 16; d; d >>= 1) {
-                        const u64 other = __shfl_xor_sync(0xffffffffu, most, d);
-                        most = other > most ? other : most;
-                    }
-                    if (lane == 0)
-                        S.most[warp] = most;
-                    __syncthreads();
-                    for (int w = 0; w < WARPS; ++w)
-                        most = S.most[w] > most ? S.most[w] : most;
-                    __syncthreads();
-                    if (most == 0)
-                        break;
-                    if (tid == 0)
-                        S.cand[held + got] = most;
-                    lower = most;
-                }
-                if (tid == 0)
-                    S.count = held + got;
-                now = held + got;
-            }
-            held = now;
-            if (t == v0 || now >= 2 * n + 32) {
-                above = cut(S, n);
-                held = min(now, n);
-            }
-            __syncthreads();  // S.count has been read by all
 #pragma unroll
             for (int u = 0; u < UN; ++u)
                 raw[u] = ahead[u];
         }
-        if (!bad)
-            (void)cut(S, n);
-        u64 *list = P.lists + ((size_t)row * P.segs + seg) * n;
-        for (int i = tid; i < n; i += TH)
-            list[i] = !bad && i < S.count ? S.cand[i] : 0;
-        // the segment's total
-        float most = top;
-        for (int d = 16; d; d >>= 1)
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+        // the bound: the n-th of the warps' 8 best threads
+        float mine = bad ? -INFINITY : top, most = top;
+        for (int i = 0; i < 8; ++i) {
+            float x = mine;
+            for (int d = 16; d; d >>= 1)
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+            most = i == 0 ? x : most;
+            const uint32_t who = __ballot_sync(0xffffffffu, mine == x);
+            if (lane == __ffs((int)who) - 1) {
+                S.best[warp * 8 + i] = candidate(ordered(mine), warp * 8 + i);
+                mine = -INFINITY;
+            }
+        }
         if (lane == 0)
             S.part[warp][0] = most;
-        __syncthreads();
+        if (tid == 0)
+            S.count = 0;
+        bad = __syncthreads_or(bad ? 1 : 0) != 0;
+        if (tid < 8 * WARPS) {
+            const u64 key = S.best[tid];
+            int place = 0;
+            for (int j = 0; j < 8 * WARPS; ++j)
+                place += S.best[j] > key ? 1 : 0;
+            if (place == n - 1)
+                S.bound = (uint32_t)(key >> 32);
+        }
+        // the segment's total
         for (int w = 0; w < WARPS; ++w)
             most = fmaxf(most, S.part[w][0]);
         float z = m > -INFINITY ? (sum + low) * ex2((m - most) * LOG2E) : 0.0f;
@@ -485,20 +532,53 @@ __global__ void __launch_bounds__(TH) beam_kernel(const __grid_constant__ BeamPa
             P.stats[(size_t)row * P.segs + seg] =
                 bad ? make_float2(NAN, NAN) : make_float2(most, z);
         }
+        if (!bad) {
+            const uint32_t above = max(S.bound, NONE + 1) - 1;  // the bound itself included
+            if (ordered(lone) > above)
+                S.cand[atomicAdd(&S.count, 1)] = candidate(ordered(lone), G.edge_col(tid));
+            for (int g = 0; g < groups; ++g) {
+                if (ordered(maxima[g * TH]) <= above)
+                    continue;
+                const int v = G.v0 + g * TH * UN + tid;
+                for (int u = 0; u < UN; ++u) {
+                    const uint4 r = G.fetch(v + u * TH);
+                    if (ordered(L::vmax(r)) <= above)
+                        continue;
+                    float x[L::VEC];
+                    L::unpack(r, x);
+                    for (int j = 0; j < L::VEC; ++j) {
+                        const uint32_t o = ordered(x[j]);
+                        if (o > above) {
+                            const int i = atomicAdd(&S.count, 1);
+                            if (i < CAP)
+                                S.cand[i] = candidate(o, G.col(v + u * TH, j));
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+            if (S.count > CAP)
+                scan_again(G, n, S);
+            else
+                (void)cut(S, n);
+            u64 *list = P.lists + ((size_t)row * P.segs + seg) * n;
+            for (int i = tid; i < n; i += TH)
+                list[i] = i < S.count ? S.cand[i] : 0;
+        }
     }
     // the sequence's last CTA merges
     __threadfence();
     __syncthreads();
     if (tid == 0) {
-        S.last = atomicAdd(&P.arrived[b], 1) == A.K * P.segs - 1;
-        if (S.last)
+        last = atomicAdd(&P.arrived[b], 1) == A.K * P.segs - 1;
+        if (last)
             P.arrived[b] = 0;
     }
     __syncthreads();
-    if (!S.last)
+    if (!last)
         return;
     __threadfence();
-    if (!pick<false>(P, b, K) && tid == 0)
+    if (!pick<false>(P, b, U.pick) && tid == 0)
         P.listed[atomicAdd(&P.hdr->n_flag, 1u)] = b;
 }
 
@@ -657,16 +737,16 @@ bool sizes_ok(int32_t B, int32_t K, int32_t V, int32_t n, int32_t dtype)
            V >= 2 && V <= SPEC_MAX_V && (dtype == SPEC_F32 || dtype == SPEC_BF16);
 }
 
-// Segments of a row: about eight CTAs per SM in all, each with a tile at least.
+// Segments of a row: eight CTAs per SM in all, no more groups than a thread has room for, and no
+// fewer than one.
 int segments(int32_t B, int32_t K, int32_t V, int32_t dtype)
 {
     const long long rows = (long long)B * K;
-    const int vecs = V / (dtype == SPEC_F32 ? 4 : 8) + 1;
+    const int vecs = V / (dtype == SPEC_F32 ? 4 : 8) + 2;
+    const int tiles = (vecs + TH * UN - 1) / (TH * UN), least = (tiles + GROUPS - 2) / (GROUPS - 1);
     long long s = rows > 0 ? (1216 + rows - 1) / rows : 1;
-    const int tiles = (vecs + TH * UN - 1) / (TH * UN);
     s = s < tiles ? s : tiles;
-    s = s < MAX_LISTS / K ? s : MAX_LISTS / K;
-    return s < 1 ? 1 : (int)s;
+    return s < least ? least : (int)s;
 }
 
 struct BeamLayout {
@@ -690,7 +770,7 @@ BeamLayout beam_layout(int32_t B, int32_t K, int32_t V, int32_t n, int32_t dtype
 }
 
 template <typename K, typename P>
-int launch(K kernel, unsigned int grid, const P &params, void *stream)
+int launch(K kernel, unsigned int grid, size_t smem, const P &params, void *stream)
 {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -698,6 +778,7 @@ int launch(K kernel, unsigned int grid, const P &params, void *stream)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(TH);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -708,11 +789,29 @@ int launch(K kernel, unsigned int grid, const P &params, void *stream)
     return SPEC_OK;
 }
 
+std::atomic<bool> g_attr[64][2];  // opted in to a merge's shared memory, per device and dtype
+
 template <int DT>
 int select_beams(const BeamParams &P, void *stream)
 {
-    const int rc = launch(beam_kernel<DT>, (unsigned int)(P.a.B * P.a.K * P.segs), P, stream);
-    return rc != SPEC_OK ? rc : launch(beam_exact_kernel<DT>, EXACT_CTAS, P, stream);
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return SPEC_ECUDA;
+    if (!g_attr[dev][DT].load(std::memory_order_acquire)) {
+        constexpr int most = (int)merge_bytes(SPEC_BEAM_MAX, MAX_LISTS);
+        if (cudaFuncSetAttribute(beam_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 most) != cudaSuccess ||
+            cudaFuncSetAttribute(beam_exact_kernel<DT>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return SPEC_ECUDA;
+        }
+        g_attr[dev][DT].store(true, std::memory_order_release);
+    }
+    const size_t merge = merge_bytes(P.a.n, P.a.K * P.segs);
+    const int rc = launch(beam_kernel<DT>, (unsigned int)(P.a.B * P.a.K * P.segs),
+                          larger(merge, SCAN_BYTES), P, stream);
+    return rc != SPEC_OK ? rc : launch(beam_exact_kernel<DT>, EXACT_CTAS, merge, P, stream);
 }
 
 }  // namespace
@@ -792,10 +891,10 @@ int32_t spec_beam_reorder(const void *in, const int32_t *beams, void *out, int32
     const long long ctas = (P.rows * parts + WARPS - 1) / WARPS;
     const unsigned int grid = ctas < 1216 ? (unsigned int)ctas : 1216u;
     if (vec == 16)
-        return launch(reorder_kernel<uint4>, grid, P, stream);
+        return launch(reorder_kernel<uint4>, grid, 0, P, stream);
     if (vec == 4)
-        return launch(reorder_kernel<uint32_t>, grid, P, stream);
-    return launch(reorder_kernel<unsigned char>, grid, P, stream);
+        return launch(reorder_kernel<uint32_t>, grid, 0, P, stream);
+    return launch(reorder_kernel<unsigned char>, grid, 0, P, stream);
 }
 
 }  // extern "C"
