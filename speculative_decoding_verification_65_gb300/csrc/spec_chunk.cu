@@ -16,8 +16,9 @@
 //                   smaller than a tile are boxes of one tile
 //   warp 9          issues the products: S(0) of each tile, then O(i), S(i + 1) of the one and of
 //                   the other; a commit behind S(i + 1) so also says that O(i) is done
-//   warp 10         TMA of an item's Q
-//   warp 11         walks the CTA's share and hands the pieces of it out through a small ring
+//   warp 10         waits for the issuer's tiles
+//   warp 11         walks the CTA's share, hands the pieces of it out through a small ring and loads
+//                   their Q
 // TMEM: S_0, S_1 (128 columns each), O_0, O_1 (up to 128 each).
 //
 // A row's sums are rescaled only when its maximum has grown by more than 2^8 (2^4 with fp16
@@ -66,8 +67,8 @@ constexpr int RING = 4;           // pieces handed out ahead
 
 template <int NP>
 struct Cfg {
-    static constexpr int KST = NP == 2 ? 3 : 6;
-    static constexpr int VST = NP == 2 ? 2 : 6;
+    static constexpr int KST = NP == 2 ? 3 : 4;
+    static constexpr int VST = NP == 2 ? 2 : 4;
     static constexpr int TILE = NP * PANEL_BYTES;
     static constexpr int DP = NP * PANEL;  // columns of O
 };
@@ -89,14 +90,16 @@ struct Piece {
 };
 
 struct Tail {
-    unsigned long long kfull[6], kempty[6], vfull[6], vempty[6];
-    unsigned long long qfull, qempty, sfull[2], pready[2], pvdone[2], drain;
-    unsigned long long pfull[RING], pempty[RING], join;
+    unsigned long long kfull[4], kempty[4], vfull[4], vempty[4];
+    unsigned long long qfull, qempty, sfull[2], pvdone[2], vclean[2], drain;
+    unsigned long long pfull[RING], pempty[RING];
     Piece piece[RING];
     uint32_t tmem_base;
     int abort_flag;
     uint32_t loaded[3];  // loads that were issued when their warp ended: tiles of K, of V, and Qs
-    uint32_t bad[2][2][4];  // keys of a tile (alternating) with non-finite values, by the group that looked
+    int issuer_out;      // the issuer has left
+    int go[2][2];        // what the waits of a group came to, alternating
+    uint16_t bad[4][8];     // keys of a masked tile with non-finite values, 16 for each warp that looked
 };
 
 template <int NP>
@@ -125,6 +128,7 @@ struct KParams {
     int join_rows;   // rows of a join CTA: 32, or the least power of two that holds them
     int page_size, pages_per_seq;
     int page_rows;   // rows of a cache box: min(128, page_size) (contiguous: 128)
+    int wide_rows;   // 1 where rows of out start on 32 bytes
 };
 
 // ------------------------------------------------------------------- work
@@ -268,6 +272,29 @@ __device__ __forceinline__ int tile_keys(const Piece &p, int jt)
     return left < KT ? left : KT;
 }
 
+// Named barriers: a softmax group among itself; its weights, for the issuer; the tiles of a step, for
+// the issuer, one for each stage of V; a piece's first tiles.
+enum { GROUP = 1, WEIGHTS = 3, TILES = 5, FIRST = 9 };
+
+__device__ __forceinline__ void named_sync(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void named_arrive(int id, int threads)
+{
+    __syncwarp();
+    asm volatile("bar.arrive %0, %1;" :: "r"(id), "r"(threads) : "memory");
+}
+
+// 32 bytes to an address that they divide
+__device__ __forceinline__ void store32(void *p, const uint32_t *w)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]),
+                    "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 template <int NP, int DT>
 __global__ void __launch_bounds__(THREADS, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkc,
@@ -284,7 +311,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int slot = (int)blockIdx.x;
 
     if (tid == 0) {
-        for (int i = 0; i < 6; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&S.kfull[i], 1);
             mbar_init(&S.kempty[i], 1);
             mbar_init(&S.vfull[i], 1);
@@ -294,16 +321,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(&S.qempty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.sfull[i], 1);
-            mbar_init(&S.pready[i], 4);
             mbar_init(&S.pvdone[i], 1);
+            mbar_init(&S.vclean[i], 8);
         }
         for (int i = 0; i < RING; ++i) {
             mbar_init(&S.pfull[i], 1);
             mbar_init(&S.pempty[i], 11);  // every warp but the one that writes
         }
-        mbar_init(&S.join, 8);
         mbar_init(&S.drain, 1);
         S.abort_flag = 0;
+        S.issuer_out = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_shared();
     }
@@ -328,7 +355,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < WAIT_TRIES; ++i) {
             if (warp_try(bar, parity))
                 return true;
-            if (given_up())
+            if ((i & 15) == 15 && given_up())
                 return false;
         }
         give_up(abort_flag, P.status);
@@ -342,23 +369,25 @@ __global__ void __launch_bounds__(THREADS, 1)
                 return true;
             if (given_up())
                 return false;
-            __nanosleep(100);
+            __nanosleep(40);
         }
         give_up(abort_flag, P.status);
         return false;
     };
-    // the next piece of the share: false when there is none or the CTA has given up
+    // The next piece of the share, where it lies (the one before is given back with that): false
+    // when there is none or the CTA has given up.
     uint32_t taken = 0;
-    auto next = [&](Piece &p) -> bool {
-        const int at = (int)(taken % RING);
-        if (!wait(&S.pfull[at], (taken / RING) & 1u))
-            return false;
-        p = S.piece[at];
+    const Piece *piece = S.piece;
+    auto next = [&](auto wait_for) -> bool {
+        if (taken > 0 && lane == 0)
+            mbar_arrive(&S.pempty[(taken - 1) % RING]);
         __syncwarp();
-        if (lane == 0)
-            mbar_arrive(&S.pempty[at]);
+        const int at = (int)(taken % RING);
+        if (!wait_for(&S.pfull[at], (taken / RING) & 1u))
+            return false;
+        piece = &S.piece[at];
         ++taken;
-        return p.n > 0;
+        return piece->n > 0;
     };
     // tiles of a piece that every row of the group sees whole
     auto plain_tiles = [](const Piece &p) -> int {
@@ -378,24 +407,33 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int local = r / P.G;               // token of the row, counted in the tile
         const int g = r - local * P.G;
         const int tok = s * P.tokens_per_tile + local;  // and in the group
-        uint32_t cnt = 0, tv = 0, done = 0;      // tiles, tiles of earlier pieces, reports of O
-        uint32_t joins = 0;
+        uint32_t cnt = 0, hid = 0, pieces = 0;   // tiles, masked ones among them, pieces
+        int vst = 0;                             // stage and phase of the next V tile
+        uint32_t vph = 0;
         const unsigned long long c2 = f2(P.c, P.c);
         // a score x has weight 2^(x c + shift) under the maximum m
         auto shift_of = [&](float m) -> float {
             return m == -INFINITY ? 0.0f : fmaf(-m, P.c, lift<DT>());
         };
-        // all softmax warps have come here
-        auto join = [&]() -> bool {
+        // A group's wait: its first warp tests the barrier, the others are held without a
+        // test at a named one (tests by all of them took half of the kernel's instructions, and
+        // of the issue slots of the warps that had work).  The group leaves as one where the wait
+        // has given up, so none is left at the named barrier.
+        uint32_t waits = 0;
+        auto wait_group = [&](unsigned long long *bar, uint32_t parity) -> bool {
+            volatile int *go = &S.go[s][waits++ & 1u];
+            if (quarter == 0) {
+                const bool there = wait(bar, parity);
+                if (lane == 0)
+                    *go = there;
+            }
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&S.join);
-            return wait(&S.join, joins++ & 1u);
+            named_sync(GROUP + s, 128);
+            return *go != 0;
         };
-
         bool ok = true;
-        Piece p = {};
-        while (ok && next(p)) {
+        while (ok && next(wait_group)) {
+            const Piece &p = *piece;
             if (p.idle) {
                 if (p.tile0 == 0)
                     void_rows(P, p.h, p.row0, p.ntok, tid);
@@ -403,82 +441,106 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             const bool live = local < P.tokens_per_tile && tok < p.ntok;
             const bool warp_live = __any_sync(0xffffffffu, live);
-            const int64_t orow =
-                ((int64_t)p.row0 + tok) * P.Hq + (int64_t)p.h * P.G + g;
             float m = -INFINITY, l = 0.0f;       // maximum of the raw scores, total
             const int plain = plain_tiles(p);
+            // keys 32 h on of tile jt that this row sees, as bits
+            auto bits = [&](int jt, int h) -> uint32_t {
+                const int left = min(tile_keys(p, jt), p.pos0 + tok + 1 - jt * KT) - h * 32;
+                return left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u;
+            };
+            // What the zeroed elements of a masked tile's values give the rows that see them, once
+            // its O is done.
+            auto add_back = [&](int jt, uint32_t slot) {
+                const volatile uint32_t *notes = reinterpret_cast<const uint32_t *>(S.bad[slot & 3u]);
+                if ((notes[0] | notes[1] | notes[2] | notes[3]) == 0 || !warp_live)
+                    return;
+#pragma unroll 1
+                for (int d = 0; d < C::DP; d += 32) {
+                    uint32_t o[32];
+                    tmem_ld(t_o + d, o);
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t left = live ? notes[q] & bits(jt, q) : 0u;
+                        while (left) {
+                            const int key = jt * KT + q * 32 + __ffs((int)left) - 1;
+                            left &= left - 1;
+                            const int e = key / P.page_size;
+                            const int64_t page = P.page_table
+                                ? __ldg(P.page_table + (size_t)p.b * P.pages_per_seq + e) : p.b;
+                            const uint16_t *src = reinterpret_cast<const uint16_t *>(P.v_cache) +
+                                page * P.v_cache_stride[0] +
+                                (key - e * P.page_size) * P.v_cache_stride[1] +
+                                p.h * P.v_cache_stride[2];
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (d + j < P.D) {
+                                    const uint32_t v = src[d + j];
+                                    if (nonfinite<DT>(v) & 0xffffu)
+                                        o[j] = __float_as_uint(__uint_as_float(o[j]) + unpack1<DT>(v));
+                                }
+                        }
+                    }
+                    tmem_st(t_o + d, o);
+                }
+                tmem_wait_st();
+            };
             // one tile; in a `masked` one some keys are hidden from some rows
             auto tile = [&](int i, auto kind) {
                 constexpr bool masked = decltype(kind)::value;
                 const int jt = p.tile0 + i;
-                const int keys = masked ? tile_keys(p, jt) : KT;
-                // keys of the tile that this row sees
-                const int sees = masked ? min(keys, p.pos0 + tok + 1 - jt * KT) : KT;
+                if (masked) {
+                    // V, while the scores are on their way: rows past the keys (up to the last
+                    // product's 16) are zeroed; of keys that some row does not see, non-finite
+                    // elements are noted and zeroed.  16 rows for each warp of both groups
+                    ok = wait_group(&S.vfull[vst], vph);
+                    if (!ok)
+                        return;
+                    const int keys = tile_keys(p, jt), r0 = warp * 16;
+                    uint32_t found = 0;
+#pragma unroll
+                    for (int x = 0; x < NP * 4; ++x) {  // 4 rows of a panel, 8 lanes each
+                        const int row = r0 + (x & 3) * 4 + (lane >> 3);
+                        uint4 *q = reinterpret_cast<uint4 *>(v_p + (size_t)vst * C::TILE +
+                                                             (x >> 2) * PANEL_BYTES + row * 128 +
+                                                             (lane & 7) * 16);
+                        bool bad = false;
+                        if (row >= keys) {
+                            if (row < ((keys + 15) & ~15))
+                                *q = make_uint4(0, 0, 0, 0);
+                        } else if (jt * KT + row > p.pos0) {
+                            uint4 w = *q;
+                            const uint4 f = make_uint4(nonfinite<DT>(w.x), nonfinite<DT>(w.y),
+                                                       nonfinite<DT>(w.z), nonfinite<DT>(w.w));
+                            bad = (f.x | f.y | f.z | f.w) != 0;
+                            if (bad) {
+                                w.x &= ~f.x;
+                                w.y &= ~f.y;
+                                w.z &= ~f.z;
+                                w.w &= ~f.w;
+                                *q = w;
+                            }
+                        }
+                        const uint32_t who = __ballot_sync(0xffffffffu, bad);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            found |= ((who >> (8 * y)) & 0xffu ? 1u : 0u) << ((x & 3) * 4 + y);
+                    }
+                    if (lane == 0)
+                        S.bad[hid & 3u][warp] = (uint16_t)found;
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&S.vclean[hid & 1u]);
+                }
                 // the scores are there, and the group's product before is done
-                ok = wait(&S.sfull[s], cnt & 1u);
+                ok = wait_group(&S.sfull[s], cnt & 1u);
                 if (!ok)
                     return;
                 tc_fence_after();
-                uint32_t any_bad = 0;
-                auto bad_keys = [&](int q) -> uint32_t {  // of keys 32 q on, after join
-                    const volatile uint32_t(*f)[2][4] = S.bad;
-                    return f[0][cnt & 1u][q] | f[1][cnt & 1u][q];
-                };
-                if (masked) {
-                    // V: rows past the keys (up to the last product's 16) are zeroed; of keys that
-                    // some row does not see, non-finite elements are noted and zeroed.  Each group
-                    // looks at a panel (with one panel the second only zeroes)
-                    const uint32_t t = tv + (uint32_t)i;
-                    const int st = (int)(t % C::VST);
-                    ok = wait(&S.vfull[st], (t / C::VST) & 1u);
-                    if (!ok)
-                        return;
-                    uint8_t *vrow = v_p + (size_t)st * C::TILE + r * 128;
-                    bool bad = false;
-                    if (s < NP) {
-                        vrow += s * PANEL_BYTES;
-                        if (r >= keys && r < ((keys + 15) & ~15)) {
-#pragma unroll
-                            for (int x = 0; x < 8; ++x)
-                                *reinterpret_cast<uint4 *>(vrow + x * 16) = make_uint4(0, 0, 0, 0);
-                        } else if (r < keys && jt * KT + r > p.pos0) {
-#pragma unroll
-                            for (int x = 0; x < 8; ++x) {
-                                uint4 *q = reinterpret_cast<uint4 *>(vrow + x * 16);
-                                uint4 w = *q;
-                                const uint4 f = make_uint4(nonfinite<DT>(w.x), nonfinite<DT>(w.y),
-                                                           nonfinite<DT>(w.z), nonfinite<DT>(w.w));
-                                if (f.x | f.y | f.z | f.w) {
-                                    bad = true;
-                                    w.x &= ~f.x;
-                                    w.y &= ~f.y;
-                                    w.z &= ~f.z;
-                                    w.w &= ~f.w;
-                                    *q = w;
-                                }
-                            }
-                        }
-                        fence_async_shared();
-                    }
-                    const uint32_t ballot = __ballot_sync(0xffffffffu, bad);
-                    if (lane == 0)
-                        S.bad[s][cnt & 1u][quarter] = ballot;
-                    ok = join();
-                    if (!ok)
-                        return;
-                    any_bad = bad_keys(0) | bad_keys(1) | bad_keys(2) | bad_keys(3);
-                }
-                auto bits = [&](int h) -> uint32_t {  // of keys 32 h on, those that the row sees
-                    const int left = sees - h * 32;
-                    return left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u;
-                };
-                uint32_t zero_w[4] = {0, 0, 0, 0};  // keys whose weight is 0 (with any_bad only)
+                if (masked && i > plain)
+                    add_back(jt - 1, hid - 1);
                 // the row's new maximum `top`; O and l follow where it has grown far
                 auto raise = [&](float top) {
-                    if (i == 0) {
-                        m = top;
-                        return;
-                    }
                     const bool grown = (top - m) * P.c > growth<DT>();  // -inf to finite too
                     if (!__any_sync(0xffffffffu, grown))
                         return;
@@ -497,8 +559,32 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 };
                 unsigned long long sum[2] = {0ull, 0ull};
-                bool redo = masked || i == 0;
-                if (warp_live && !redo) {
+                if (warp_live && i == 0) {
+                    // a piece's first tile: all scores in registers, the maximum, the weights (32 h on
+                    // lie in columns 16 h on)
+                    uint32_t x[4][32];
+                    float top = -INFINITY;
+                    __syncwarp();
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+                        tmem_ld_start(t_s + h * 32, x[h]);
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        tmem_ld_finish(x[h]);
+                        if (masked)
+                            hide(x[h], bits(jt, h));
+                        top = fmaxf(top, max32(x[h]));
+                    }
+                    m = top;
+                    const float shift = shift_of(m);
+                    const unsigned long long shift2 = f2(shift, shift);
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t pk[16];
+                        weigh<DT>(x[h], c2, shift2, sum, pk);
+                        tmem_st(t_s + h * 16, pk);
+                    }
+                } else if (warp_live) {
                     // in one pass: weights by the maximum so far, which serves as long as no
                     // score is far above it; the tile's own maximum is found on the way
                     const float shift = shift_of(m);
@@ -508,63 +594,44 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tmem_ld_start(t_s, x);
                     tmem_ld_finish(x);
                     tmem_ld_start(t_s + 32, y);
+                    if (masked)
+                        hide(x, bits(jt, 0));
                     float top = max32(x);
                     weigh<DT>(x, c2, shift2, sum, pk[0]);
                     tmem_ld_finish(y);
                     tmem_ld_start(t_s + 64, x);
+                    if (masked)
+                        hide(y, bits(jt, 1));
                     top = fmaxf(top, max32(y));
                     weigh<DT>(y, c2, shift2, sum, pk[1]);
                     tmem_ld_finish(x);
                     tmem_ld_start(t_s + 96, y);
+                    if (masked)
+                        hide(x, bits(jt, 2));
                     top = fmaxf(top, max32(x));
                     weigh<DT>(x, c2, shift2, sum, pk[2]);
                     tmem_ld_finish(y);
+                    if (masked)
+                        hide(y, bits(jt, 3));
                     top = fmaxf(top, max32(y));
                     weigh<DT>(y, c2, shift2, sum, pk[3]);
-                    redo = __any_sync(0xffffffffu,
-                                      (top - m) * P.c > growth<DT>());  // -inf to finite too
-                    if (!redo) {
+                    if (!__any_sync(0xffffffffu, (top - m) * P.c > growth<DT>())) {
 #pragma unroll
                         for (int h = 0; h < 4; ++h)
                             tmem_st(t_s + h * 16, pk[h]);
                     } else {
+                        // again, by the new maximum
+                        raise(top);
                         sum[0] = sum[1] = 0ull;
-                    }
-                }
-                if (warp_live && redo) {
-                    // the maximum first: 32 keys at a time, and no more of them than the tile has
-                    const int chunks = (keys + 31) / 32;
-                    float top = -INFINITY;
+                        const float shift = shift_of(m);
+                        const unsigned long long shift2 = f2(shift, shift);
 #pragma unroll 1
-                    for (int h = 0; h < chunks; ++h) {
-                        uint32_t x[32];
-                        tmem_ld(t_s + h * 32, x);
-                        if (masked)
-                            hide(x, bits(h));
-                        top = fmaxf(top, max32(x));
-                    }
-                    raise(top);
-                    const float shift = shift_of(m);
-                    const unsigned long long shift2 = f2(shift, shift);
-#pragma unroll 1
-                    for (int h = 0; h < chunks; ++h) {
-                        uint32_t x[32], pk[16];
-                        tmem_ld(t_s + h * 32, x);
-                        if (masked)
-                            hide(x, bits(h));
-                        weigh<DT>(x, c2, shift2, sum, pk);
-                        // weights 32 h on lie in columns 16 h on: over scores that were read
-                        tmem_st(t_s + h * 16, pk);
-                        if (any_bad) {
-                            uint32_t z = 0;
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                z |= ((pk[j] & 0x7fffu) == 0 ? 1u : 0u) << (2 * j) |
-                                     ((pk[j] & 0x7fff0000u) == 0 ? 2u : 0u) << (2 * j);
-                            zero_w[0] = h == 0 ? z : zero_w[0];
-                            zero_w[1] = h == 1 ? z : zero_w[1];
-                            zero_w[2] = h == 2 ? z : zero_w[2];
-                            zero_w[3] = h == 3 ? z : zero_w[3];
+                        for (int h = 0; h < 4; ++h) {
+                            tmem_ld(t_s + h * 32, x);
+                            if (masked)
+                                hide(x, bits(jt, h));
+                            weigh<DT>(x, c2, shift2, sum, pk[0]);
+                            tmem_st(t_s + h * 16, pk[0]);
                         }
                     }
                 }
@@ -575,54 +642,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tmem_wait_st();
                 }
                 tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&S.pready[s]);
-                if (any_bad) {
-                    // what the zeroed elements give the rows that see them, once O(i) is done
-                    ok = wait(&S.pvdone[s], done & 1u);
-                    if (!ok)
-                        return;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int d = 0; d < C::DP; d += 32) {
-                        uint32_t o[32];
-                        tmem_ld(t_o + d, o);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t left = bad_keys(q) & bits(q);
-                            while (live && left) {
-                                const int bit = __ffs((int)left) - 1;
-                                left &= left - 1;
-                                const int key = jt * KT + q * 32 + bit;
-                                const int e = key / P.page_size;
-                                const int64_t page = P.page_table
-                                    ? __ldg(P.page_table + (size_t)p.b * P.pages_per_seq + e) : p.b;
-                                const uint16_t *src = reinterpret_cast<const uint16_t *>(P.v_cache) +
-                                    page * P.v_cache_stride[0] +
-                                    (key - e * P.page_size) * P.v_cache_stride[1] +
-                                    p.h * P.v_cache_stride[2];
-                                const float z = (zero_w[q] >> bit) & 1u ? 0.0f : 1.0f;
-#pragma unroll
-                                for (int j = 0; j < 32; ++j)
-                                    if (d + j < P.D) {
-                                        const uint32_t v = src[d + j];
-                                        if (nonfinite<DT>(v) & 0xffffu)
-                                            o[j] = __float_as_uint(__uint_as_float(o[j]) +
-                                                                   z * unpack1<DT>(v));
-                                    }
-                            }
-                        }
-                        tmem_st(t_o + d, o);
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    // the notes are written over only after every warp has read them
-                    ok = join();
-                }
-                if (commits_done(i, plain, 1, p.n))
-                    ++done;
+                named_arrive(WEIGHTS + s, 160);
                 ++cnt;
+                vph ^= vst + 1 == C::VST ? 1u : 0u;
+                vst = vst + 1 == C::VST ? 0 : vst + 1;
+                if (masked)
+                    ++hid;
             };
             // tiles without a mask first, in a loop of their own: it stays small
             int i = 0;
@@ -630,63 +655,54 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tile(i, Whole());
             for (; i < p.n && ok; ++i)
                 tile(i, Masked());
+            ok = ok && wait_group(&S.pvdone[s], pieces++ & 1u);
             if (!ok)
                 break;
-            tv += (uint32_t)p.n;
-
-            if (!wait(&S.pvdone[s], (done - 1) & 1u))
-                break;
             tc_fence_after();
+            if (p.n > plain)
+                add_back(p.tile0 + p.n - 1, hid - 1);
             const float top = m != -INFINITY ? -shift_of(m) : -INFINITY;
             const float sum = l, base = top == -INFINITY ? 0.0f : top;
             // a row that saw no key has no weight, whatever its O holds
             const bool some = !(top == -INFINITY && sum == 0.0f);
-            const bool whole = p.n == p.tiles;
             if (warp_live) {
+                const bool whole = p.n == p.tiles;
+                const int64_t orow = ((int64_t)p.row0 + tok) * P.Hq + (int64_t)p.h * P.G + g;
                 const size_t at = (((size_t)slot * 2 + s) * 2 + (p.first ? 0 : 1)) * BM;
-                const float norm = sum != 0.0f ? 1.0f / sum : 0.0f;
-                const bool on = live && some && sum != 0.0f;
+                const float norm = sum != 0.0f && some ? 1.0f / sum : 0.0f;
+                uint16_t *to = reinterpret_cast<uint16_t *>(P.out) + orow * P.D;
 #pragma unroll 1
-                for (int panel = 0; panel < NP; ++panel) {
-                    uint4 u[8];
+                for (int d0 = 0; d0 < C::DP; d0 += 32) {
+                    uint32_t a[32];
+                    tmem_ld(t_o + (uint32_t)d0, a);
+                    if (!live)
+                        continue;
+                    if (!whole) {
+                        // [column][row]: a warp's store is one line
+                        float *o = P.part + at * C::DP + d0 * BM + r;
 #pragma unroll
-                    for (int d0 = 0; d0 < PANEL; d0 += 32) {
-                        uint32_t a[32];
-                        tmem_ld(t_o + (uint32_t)(panel * PANEL + d0), a);
-                        if (whole) {
-#pragma unroll
-                            for (int j = 0; j < 32; j += 8) {
-                                float v[8];
-#pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    v[k] = __uint_as_float(a[j + k]) * norm;
-                                u[(d0 + j) / 8] = make_uint4(
-                                    on ? pack<DT>(v[0], v[1]) : 0u, on ? pack<DT>(v[2], v[3]) : 0u,
-                                    on ? pack<DT>(v[4], v[5]) : 0u, on ? pack<DT>(v[6], v[7]) : 0u);
-                            }
-                        } else if (live) {
-                            // [column][row]: a warp's store is one line
-                            float *o = P.part + at * C::DP + (panel * PANEL + d0) * BM + r;
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (panel * PANEL + d0 + j < P.D)
-                                    o[j * BM] = some ? __uint_as_float(a[j]) : 0.0f;
-                        }
+                        for (int j = 0; j < 32; ++j)
+                            if (d0 + j < P.D)
+                                o[j * BM] = some ? __uint_as_float(a[j]) : 0.0f;
+                        continue;
                     }
-                    if (whole) {
-                        // 8 lanes exchange so that each holds one 16-byte chunk of 8 rows: a
-                        // store then covers 128 bytes of 4 rows, not 16 of 32 rows
-                        exchange8(u, lane);
-                        const int d = panel * PANEL + (lane & 7) * 8;
-                        const uint32_t rows = __ballot_sync(0xffffffffu, live);
+                    uint32_t u[16];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int from = (lane & ~7) | k;
-                            const int64_t at_row = __shfl_sync(0xffffffffu, orow, from);
-                            if (((rows >> from) & 1u) && d < P.D)
-                                *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(P.out) +
-                                                           at_row * P.D + d) = u[k];
-                        }
+                    for (int j = 0; j < 16; ++j)
+                        u[j] = norm != 0.0f ? pack<DT>(__uint_as_float(a[2 * j]) * norm,
+                                                       __uint_as_float(a[2 * j + 1]) * norm) : 0u;
+                    if (P.wide_rows) {
+                        // a lane's store is a whole sector of its row
+#pragma unroll
+                        for (int j = 0; j < 32; j += 16)
+                            if (d0 + j < P.D)
+                                store32(to + d0 + j, u + j / 2);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8)
+                            if (d0 + j < P.D)
+                                *reinterpret_cast<uint4 *>(to + d0 + j) =
+                                    make_uint4(u[j / 2], u[j / 2 + 1], u[j / 2 + 2], u[j / 2 + 3]);
                     }
                 }
                 if (live) {
@@ -702,212 +718,213 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(HELPER_REGS));
         if (warp == 8) {
             // ------------------------------------------------ TMA of K and V
-            uint32_t t0 = 0;                     // tiles of earlier pieces
-            uint32_t loaded_k = 0, loaded_v = 0; // tiles that a load was issued for
+            // tiles that a load was issued for, and the next one's stage and phase: of K and of V
+            uint32_t loaded[2] = {0, 0}, phase[2] = {1, 1};
+            int stage[2] = {0, 0};
             bool ok = true;
-            Piece p = {};
-            // one tile's keys (side 0) or values (1): a box of rows per lane
-            auto load = [&](int side, int i) {
-                const int jt = p.tile0 + i;
-                const int keys = tile_keys(p, jt);
-                const int rows = P.page_rows, at = lane * rows;
-                const bool mine = at < keys;
-                int y = jt * KT + at, w = p.b;
-                if (P.page_table && mine) {
-                    const int e = y / P.page_size;
-                    w = __ldg(P.page_table + (size_t)p.b * P.pages_per_seq + e);
-                    y -= e * P.page_size;
-                }
-                const uint32_t n = t0 + (uint32_t)i, stages = side ? C::VST : C::KST;
-                const int st = (int)(n % stages);
-                ok = wait(side ? &S.vempty[st] : &S.kempty[st], ((n / stages) & 1u) ^ 1u);
-                if (!ok)
-                    return;
-                unsigned long long *full = side ? &S.vfull[st] : &S.kfull[st];
-                if (lane == 0)
-                    mbar_arrive_expect_tx(
-                        full, (uint32_t)(((keys + rows - 1) / rows) * rows * 128 * NP));
-                __syncwarp();
-                (side ? loaded_v : loaded_k) = n + 1;
-                if (mine) {
-                    const CUtensorMap *map = side ? &mvc : &mkc;
-                    const uint32_t dst =
-                        (side ? v_s : k_s) + (uint32_t)(st * C::TILE + at * 128);
-#pragma unroll
-                    for (int d = 0; d < NP; ++d)
-                        tma_load_4d(dst + d * PANEL_BYTES, map, d * PANEL, y, p.h, w, full);
-                }
-                __syncwarp();
-            };
-            while (ok && next(p)) {
+            while (ok && next(wait_idle)) {
+                const Piece &p = *piece;
                 if (p.idle)
                     continue;
+                const int rows = P.page_rows, at = lane * rows;  // a box of rows per lane
                 for (int i = 0; i < p.n && ok; ++i) {
-                    load(0, i);
-                    if (ok)
-                        load(1, i);
+                    const int jt = p.tile0 + i, keys = tile_keys(p, jt);
+                    const bool mine = at < keys;
+                    int y = jt * KT + at, w = p.b;
+                    if (P.page_table && mine) {
+                        const int e = y / P.page_size;
+                        w = __ldg(P.page_table + (size_t)p.b * P.pages_per_seq + e);
+                        y -= e * P.page_size;
+                    }
+                    const uint32_t bytes = (uint32_t)(((keys + rows - 1) / rows) * rows * 128 * NP);
+#pragma unroll
+                    for (int side = 0; side < 2 && ok; ++side) {
+                        const int st = stage[side];
+                        unsigned long long *full = side ? &S.vfull[st] : &S.kfull[st];
+                        ok = wait_idle(side ? &S.vempty[st] : &S.kempty[st], phase[side]);
+                        if (!ok)
+                            break;
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(full, bytes);
+                        __syncwarp();
+                        if (mine) {
+                            const uint32_t dst =
+                                (side ? v_s : k_s) + (uint32_t)(st * C::TILE + at * 128);
+#pragma unroll
+                            for (int d = 0; d < NP; ++d)
+                                tma_load_4d(dst + d * PANEL_BYTES, side ? &mvc : &mkc, d * PANEL, y,
+                                            p.h, w, full);
+                        }
+                        __syncwarp();
+                        ++loaded[side];
+                        const bool last = st + 1 == (side ? C::VST : C::KST);
+                        stage[side] = last ? 0 : st + 1;
+                        phase[side] ^= last ? 1u : 0u;
+                    }
                 }
-                t0 += (uint32_t)p.n;
             }
             if (lane == 0) {
-                S.loaded[0] = loaded_k;
-                S.loaded[1] = loaded_v;
+                S.loaded[0] = loaded[0];
+                S.loaded[1] = loaded[1];
             }
         } else if (warp == 9) {
             // -------------------------------------------- issuer of the products
             // The whole warp runs the loop and one elected lane issues: what the products are
             // given then stays in uniform registers.  A step of group G: O(i) += P V(i), then
-            // S = Q K(i + 1)^T; in the usual case one test covers both tiles and one elected
-            // block issues all of it.
-            uint32_t items = 0;
+            // S = Q K(i + 1)^T.  It tests no mbarrier in its loop: a test of one that is ready takes
+            // 100 to 200 clocks, in which the tensor pipe runs dry, a named barrier's sync
+            // about 30.  The weights come by one from the softmax groups, the tiles by one from
+            // the next warp, which tests theirs.  Where a CTA has given up that warp frees this one.
             bool ok = true;
             const int ksteps = (P.D + 15) / 16;
+            const bool all_steps = ksteps == NP * 4;
             const uint32_t id_o = idesc<DT>(ksteps * 16, true);
-            Piece p = {};
-            int kst = 0, vst = 0;                // stages and phases of the next K and V tile
-            uint32_t kph = 0, vph = 0, pph[2] = {0, 0};
+            int kst = 0, vst = 0;                // stages of the next K and V tile
             constexpr uint32_t id_s = idesc<DT>(KT, false);
             const uint64_t qd0 = desc_k(q_s), kd0 = desc_k(k_s), vd0 = desc_mn(v_s);
             constexpr uint64_t TILE16 = C::TILE >> 4;
-            int plain = 0;
-            auto next_k = [&]() {
-                kph ^= kst + 1 == C::KST ? 1u : 0u;
-                kst = kst + 1 == C::KST ? 0 : kst + 1;
-            };
-            auto next_v = [&]() {
-                vph ^= vst + 1 == C::VST ? 1u : 0u;
-                vst = vst + 1 == C::VST ? 0 : vst + 1;
-            };
-            // commits behind the scores of tile i
-            auto scored = [&](int s, int i) {
+            // S = Q K^T of group s by the elected lane, and what it commits; `last` of the piece
+            auto scores = [&](int s, uint32_t id, bool last) {
+                const uint32_t d = tmem + (uint32_t)(s * KT);
+                const uint64_t qd = qd0 + s * TILE16, kd = kd0 + kst * TILE16;
+                if (all_steps) {
+#pragma unroll
+                    for (int x = 0; x < NP * 4; ++x) {
+                        const uint64_t off = (uint64_t)(((x >> 2) * PANEL_BYTES + (x & 3) * 32) >> 4);
+                        mma_ss(d, qd + off, kd + off, id, x ? 1u : 0u);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int x = 0; x < ksteps; ++x) {
+                        const uint64_t off = (uint64_t)(((x >> 2) * PANEL_BYTES + (x & 3) * 32) >> 4);
+                        mma_ss(d, qd + off, kd + off, id, x ? 1u : 0u);
+                    }
+                }
                 if (s)
                     mma_commit(&S.kempty[kst]);
                 mma_commit(&S.sfull[s]);
-                if (i == p.n - 1 && s)
+                if (last && s)
                     mma_commit(&S.qempty);
             };
-            auto scores = [&](int s, int i) {    // S = Q K(i)^T by itself
-                const int keys = tile_keys(p, p.tile0 + i);
-                ok = wait(&S.kfull[kst], kph);
+            while (ok && next(wait)) {
+                const Piece &p = *piece;
+                if (p.idle)
+                    continue;
+                const int n = p.n, plain = plain_tiles(p);
+                // only a group's last tile can have fewer than KT keys
+                const int tail = tile_keys(p, p.tile0 + n - 1);
+                const uint32_t id_tail = idesc<DT>((tail + 15) & ~15, false);
+                named_sync(FIRST, 64);
+                ok = !given_up();
                 if (!ok)
-                    return;
+                    break;
                 tc_fence_after();
-                const uint32_t id = idesc<DT>((keys + 15) & ~15, false);
-                const uint32_t d = tmem + (uint32_t)(s * KT);
-                const uint64_t qd = qd0 + s * TILE16, kd = kd0 + kst * TILE16;
                 if (elect_one()) {
-#pragma unroll 1
-                    for (int x = 0; x < ksteps; ++x) {
-                        const uint64_t off =
-                            (uint64_t)(((x >> 2) * PANEL_BYTES + (x & 3) * 32) >> 4);
-                        mma_ss(d, qd + off, kd + off, id, x ? 1u : 0u);
-                    }
-                    scored(s, i);
+                    scores(0, n == 1 ? id_tail : id_s, n == 1);
+                    scores(1, n == 1 ? id_tail : id_s, n == 1);
                 }
                 __syncwarp();
-                if (s)
-                    next_k();
-            };
-            auto step = [&](auto group, int i) {
-                constexpr int G = decltype(group)::value;
-                const uint32_t t_s = tmem + (uint32_t)(G * KT);
-                const uint32_t t_o = tmem + (uint32_t)(2 * KT + G * C::DP);
-                const uint64_t vd = vd0 + vst * TILE16;
-                const uint32_t more = i >= 1 ? 1u : 0u;
-                const bool usual = i + 1 < plain && ksteps == NP * 4;
-                // (the second group finds the first one's tiles)
-                ok = wait(&S.pready[G], pph[G]);
-                if (!ok)
-                    return;
-                const bool all = usual && (G ||
-                                           warp_try2(&S.vfull[vst], vph, &S.kfull[kst], kph));
-                if (all) {
-                    tc_fence_after();
-                    const uint64_t qd = qd0 + G * TILE16, kd = kd0 + kst * TILE16;
-                    if (elect_one()) {
-                        // 16 keys a step: 8 columns of P, 2 KB of V
-#pragma unroll
-                        for (int x = 0; x < KT / 16; ++x)
-                            mma_ts(t_o, t_s + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)),
-                                   id_o, x ? 1u : more);
-                        if (G)
-                            mma_commit(&S.vempty[vst]);
-#pragma unroll
-                        for (int x = 0; x < NP * 4; ++x) {
-                            const uint64_t off =
-                                (uint64_t)(((x >> 2) * PANEL_BYTES + (x & 3) * 32) >> 4);
-                            mma_ss(t_s, qd + off, kd + off, id_s, x ? 1u : 0u);
-                        }
-                        scored(G, i + 1);
-                    }
-                    __syncwarp();
-                    if (G)
-                        next_k();
-                } else {
-                    const int keys = tile_keys(p, p.tile0 + i);
-                    ok = wait(&S.vfull[vst], vph);
+                kst = kst + 1 == C::KST ? 0 : kst + 1;
+                auto step = [&](auto group, int i) {
+                    constexpr int G = decltype(group)::value;
+                    const uint32_t t_s = tmem + (uint32_t)(G * KT);
+                    const uint32_t t_o = tmem + (uint32_t)(2 * KT + G * C::DP);
+                    const uint64_t vd = vd0 + vst * TILE16;
+                    const uint32_t more = i >= 1 ? 1u : 0u;
+                    const bool end = i + 1 == n;
+                    if (G == 0)  // (the second group finds the first one's tiles)
+                        named_sync(TILES + vst, 64);
+                    named_sync(WEIGHTS + G, 160);
+                    ok = !given_up();
                     if (!ok)
                         return;
                     tc_fence_after();
                     if (elect_one()) {
-                        const int steps = (keys + 15) / 16;
+                        // 16 keys a step: 8 columns of P, 2 KB of V
+                        if (!end || tail == KT) {
+#pragma unroll
+                            for (int x = 0; x < KT / 16; ++x)
+                                mma_ts(t_o, t_s + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)),
+                                       id_o, x ? 1u : more);
+                        } else {
 #pragma unroll 1
-                        for (int x = 0; x < steps; ++x)
-                            mma_ts(t_o, t_s + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)),
-                                   id_o, x ? 1u : more);
+                            for (int x = 0; x < (tail + 15) / 16; ++x)
+                                mma_ts(t_o, t_s + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)),
+                                       id_o, x ? 1u : more);
+                        }
                         if (G)
                             mma_commit(&S.vempty[vst]);
-                        if (commits_done(i, plain, 1, p.n))
+                        if (end)
                             mma_commit(&S.pvdone[G]);
+                        else
+                            scores(G, i + 2 == n ? id_tail : id_s, i + 2 == n);
                     }
                     __syncwarp();
-                    if (i + 1 < p.n)
-                        scores(G, i + 1);
-                }
-                pph[G] ^= 1u;
-                if (G)
-                    next_v();
-            };
-            while (ok && next(p)) {
-                if (p.idle)
-                    continue;
-                plain = plain_tiles(p);
-                ok = wait(&S.qfull, items & 1u);
-                ++items;
-                if (ok)
-                    scores(0, 0);
-                if (ok)
-                    scores(1, 0);
-                for (int i = 0; i < p.n && ok; ++i) {
+                    if (G) {
+                        if (!end)
+                            kst = kst + 1 == C::KST ? 0 : kst + 1;
+                        vst = vst + 1 == C::VST ? 0 : vst + 1;
+                    }
+                };
+                for (int i = 0; i < n && ok; ++i) {
                     step(Int<0>(), i);
                     if (ok)
                         step(Int<1>(), i);
                 }
             }
+            if (lane == 0)
+                *(volatile int *)&S.issuer_out = 1;
         } else if (warp == 10) {
-            // ---------------------------------------------------- TMA of Q
-            uint32_t items = 0;
-            Piece p = {};
-            while (next(p)) {
+            // -------------------------------- waits for the issuer's tiles, some steps ahead of it
+            // (A stage's barrier is come to again only when its V has been loaded again, so after the
+            // issuer has been there; the first one when Q has been.)
+            bool ok = true;
+            int kst = 0, vst = 0;
+            uint32_t kph = 0, vph = 0, items = 0, hid = 0;
+            auto wait_k = [&]() -> bool {
+                const bool there = wait(&S.kfull[kst], kph);
+                kph ^= kst + 1 == C::KST ? 1u : 0u;
+                kst = kst + 1 == C::KST ? 0 : kst + 1;
+                return there;
+            };
+            while (ok && next(wait_idle)) {
+                const Piece &p = *piece;
                 if (p.idle)
                     continue;
-                if (!wait_idle(&S.qempty, (items & 1u) ^ 1u))
-                    break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(
-                        &S.qfull, (uint32_t)(P.tokens_per_tile * P.G * 128 * NP * 2));
-                    for (int i = 0; i < NP * 2; ++i)
-                        tma_load_4d(q_s + i * PANEL_BYTES, &mq, (i % NP) * PANEL, 0,
-                                    p.row0 + (i / NP) * P.tokens_per_tile, p.h, &S.qfull);
+                const int plain = plain_tiles(p);
+                ok = wait(&S.qfull, items++ & 1u) && wait_k();
+                if (ok)
+                    named_arrive(FIRST, 64);
+                for (int i = 0; i < p.n && ok; ++i) {
+                    ok = wait(&S.vfull[vst], vph) && (i + 1 == p.n || wait_k());
+                    if (ok && i >= plain) {
+                        ok = wait(&S.vclean[hid & 1u], (hid >> 1) & 1u);
+                        ++hid;
+                    }
+                    if (ok)
+                        named_arrive(TILES + vst, 64);
+                    vph ^= vst + 1 == C::VST ? 1u : 0u;
+                    vst = vst + 1 == C::VST ? 0 : vst + 1;
                 }
-                __syncwarp();
-                ++items;
             }
-            if (lane == 0)
-                S.loaded[2] = items;
+            // The issuer's syncs have no limit of their own.  Once the CTA has given up, this warp comes
+            // to all of them, again and again, until the issuer has left: whatever had come there
+            // before, each fills up while the issuer waits at it.
+            for (int i = 0; i < WAIT_TRIES; ++i) {
+                if (__any_sync(0xffffffffu, *(volatile int *)&S.issuer_out != 0))
+                    break;
+                if (given_up()) {
+                    for (int id = WEIGHTS; id < TILES; ++id)
+                        named_arrive(id, 160);
+                    for (int id = TILES; id <= FIRST; ++id)
+                        named_arrive(id, 64);
+                }
+                __nanosleep(200);
+            }
         } else {
-            // ------------------------------------------- the share's pieces
+            // ------------------------------- the share's pieces, and the TMA of their Q
             Walk walk(P, slot);
+            uint32_t items = 0;
             for (uint32_t k = 0;; ++k) {
                 const int at = (int)(k % RING);
                 if (!wait_idle(&S.pempty[at], ((k / RING) & 1u) ^ 1u))
@@ -920,8 +937,23 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 if (p.n == 0)
                     break;
+                if (!p.idle) {
+                    if (!wait_idle(&S.qempty, (items & 1u) ^ 1u))
+                        break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(
+                            &S.qfull, (uint32_t)(P.tokens_per_tile * P.G * 128 * NP * 2));
+                        for (int i = 0; i < NP * 2; ++i)
+                            tma_load_4d(q_s + i * PANEL_BYTES, &mq, (i % NP) * PANEL, 0,
+                                        p.row0 + (i / NP) * P.tokens_per_tile, p.h, &S.qfull);
+                    }
+                    __syncwarp();
+                    ++items;
+                }
                 walk.go_on(P, p.n);
             }
+            if (lane == 0)
+                S.loaded[2] = items;
         }
     }
     tc_fence_before();
@@ -940,7 +972,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 mma_commit(&S.drain);
             __syncwarp();
             (void)mbar_wait(&S.drain, 0u);
-        } else if (warp == 10 && S.loaded[2] > 0) {
+        } else if (warp == 11 && S.loaded[2] > 0) {
             (void)mbar_wait(&S.qfull, (S.loaded[2] - 1) & 1u);
         } else if (warp < 8) {
             void_share(P, slot, tid);
@@ -1218,6 +1250,7 @@ int32_t spec_chunk_attention(const spec_chunk_attention_args *args, void *worksp
     P.tokens_per_tile = BM / G;
     P.page_size = a.page_size;
     P.pages_per_seq = a.pages_per_seq;
+    P.wide_rows = a.D % 16 == 0 && aligned(a.out, 32);
     P.page_rows = paged && a.page_size < KT ? a.page_size : KT;
 
     CUtensorMap maps[3];
