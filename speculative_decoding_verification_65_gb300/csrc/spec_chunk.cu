@@ -86,6 +86,7 @@ struct Piece {
     int tile0, n;    // first tile and number of tiles (0: the share has ended)
     int tiles;       // of the whole item
     int idle;        // nothing to compute: a sequence in error
+    int turn;        // the whole tiles are taken from this one on, and then from the first
     int first;       // 1 when the share starts inside the item or with it
 };
 
@@ -193,11 +194,12 @@ __device__ __forceinline__ long long share(const KParams &P, long long all)
 // The pieces of a CTA's share, one after the other (a warp's walk, all lanes alike).
 struct Walk {
     Place q;
-    long long u0, u1, u;
+    long long u0, u1, u, per;
 
     __device__ __forceinline__ Walk(const KParams &P, int slot) : q(empty_place(P))
     {
-        const long long all = q.total * P.Hkv, per = share(P, all);
+        const long long all = q.total * P.Hkv;
+        per = share(P, all);
         u0 = slot * per;
         u1 = u0 + per < all ? u0 + per : all;
         u = u0;
@@ -218,6 +220,16 @@ struct Walk {
         p.n = left <= 0 ? 0 : p.tiles - q.tile < left ? p.tiles - q.tile : (int)left;
         p.idle = q.x.bad | (q.status != 0);
         p.first = u - q.tile <= u0;
+        // Where an item's tiles are those of more than one share, whole tiles are taken in an order
+        // by the time: tile t of the item when the CTA has taken t more than a multiple of a share's
+        // tiles.  CTAs that read the same keys for other rows then read them at one time,
+        // once from DRAM: from the first tile on, each at a place of its own, 512 tokens
+        // behind 131072 positions read 11 times the cache, as fast as DRAM gives it.
+        p.turn = 0;
+        if (p.tiles >= per) {
+            const long long turn = (u - u0 - q.tile) % per;
+            p.turn = (int)(turn < 0 ? turn + per : turn);
+        }
         return p;
     }
     // to the piece behind this one of n tiles
@@ -367,7 +379,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < WAIT_TRIES; ++i) {
             if (warp_try(bar, parity))
                 return true;
-            if (given_up())
+            if ((i & 15) == 15 && given_up())
                 return false;
             __nanosleep(40);
         }
@@ -484,9 +496,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 tmem_wait_st();
             };
-            // one tile; in a `masked` one some keys are hidden from some rows
-            auto tile = [&](int i, auto kind) {
-                constexpr bool masked = decltype(kind)::value;
+            // The tiles; in a masked one (the last ones) some keys are hidden from some rows.  What a
+            // few tiles need beside the common way stands in small loops of its own: unrolled
+            // variants of that way, run once in 30 tiles, took three times its time, most of it
+            // for their instructions to arrive.
+            for (int i = 0; i < p.n && ok; ++i) {
+                const bool masked = i >= plain;
                 const int jt = p.tile0 + i;
                 if (masked) {
                     // V, while the scores are on their way: rows past the keys (up to the last
@@ -494,36 +509,33 @@ __global__ void __launch_bounds__(THREADS, 1)
                     // elements are noted and zeroed.  16 rows for each warp of both groups
                     ok = wait_group(&S.vfull[vst], vph);
                     if (!ok)
-                        return;
+                        break;
                     const int keys = tile_keys(p, jt), r0 = warp * 16;
                     uint32_t found = 0;
+                    uint8_t *at = v_p + (size_t)vst * C::TILE + (r0 + (lane >> 3)) * 128 +
+                                  (lane & 7) * 16;
+                    uint4 w[NP * 4];  // 4 rows of a panel, 8 lanes each
 #pragma unroll
-                    for (int x = 0; x < NP * 4; ++x) {  // 4 rows of a panel, 8 lanes each
+                    for (int x = 0; x < NP * 4; ++x)
+                        w[x] = *reinterpret_cast<const uint4 *>(at + (x >> 2) * PANEL_BYTES +
+                                                                (x & 3) * 512);
+#pragma unroll
+                    for (int x = 0; x < NP * 4; ++x) {
                         const int row = r0 + (x & 3) * 4 + (lane >> 3);
-                        uint4 *q = reinterpret_cast<uint4 *>(v_p + (size_t)vst * C::TILE +
-                                                             (x >> 2) * PANEL_BYTES + row * 128 +
-                                                             (lane & 7) * 16);
-                        bool bad = false;
-                        if (row >= keys) {
-                            if (row < ((keys + 15) & ~15))
-                                *q = make_uint4(0, 0, 0, 0);
-                        } else if (jt * KT + row > p.pos0) {
-                            uint4 w = *q;
-                            const uint4 f = make_uint4(nonfinite<DT>(w.x), nonfinite<DT>(w.y),
-                                                       nonfinite<DT>(w.z), nonfinite<DT>(w.w));
-                            bad = (f.x | f.y | f.z | f.w) != 0;
-                            if (bad) {
-                                w.x &= ~f.x;
-                                w.y &= ~f.y;
-                                w.z &= ~f.z;
-                                w.w &= ~f.w;
-                                *q = w;
-                            }
-                        }
+                        const uint4 f = make_uint4(nonfinite<DT>(w[x].x), nonfinite<DT>(w[x].y),
+                                                   nonfinite<DT>(w[x].z), nonfinite<DT>(w[x].w));
+                        const bool past = row >= keys && row < ((keys + 15) & ~15);
+                        const bool bad = row < keys && jt * KT + row > p.pos0 &&
+                                         (f.x | f.y | f.z | f.w) != 0;
+                        if (past || bad)
+                            *reinterpret_cast<uint4 *>(at + (x >> 2) * PANEL_BYTES + (x & 3) * 512) =
+                                past ? make_uint4(0, 0, 0, 0)
+                                     : make_uint4(w[x].x & ~f.x, w[x].y & ~f.y, w[x].z & ~f.z,
+                                                  w[x].w & ~f.w);
                         const uint32_t who = __ballot_sync(0xffffffffu, bad);
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            found |= ((who >> (8 * y)) & 0xffu ? 1u : 0u) << ((x & 3) * 4 + y);
+                        if (who)
+                            for (int y = 0; y < 4; ++y)
+                                found |= ((who >> (8 * y)) & 0xffu ? 1u : 0u) << ((x & 3) * 4 + y);
                     }
                     if (lane == 0)
                         S.bad[hid & 3u][warp] = (uint16_t)found;
@@ -535,107 +547,87 @@ __global__ void __launch_bounds__(THREADS, 1)
                 // the scores are there, and the group's product before is done
                 ok = wait_group(&S.sfull[s], cnt & 1u);
                 if (!ok)
-                    return;
+                    break;
                 tc_fence_after();
                 if (masked && i > plain)
                     add_back(jt - 1, hid - 1);
-                // the row's new maximum `top`; O and l follow where it has grown far
-                auto raise = [&](float top) {
-                    const bool grown = (top - m) * P.c > growth<DT>();  // -inf to finite too
-                    if (!__any_sync(0xffffffffu, grown))
-                        return;
-                    const float f = grown ? ex2((m - top) * P.c) : 1.0f;
-                    l *= f;
-                    if (grown)
-                        m = top;
-#pragma unroll 1
-                    for (int d = 0; d < C::DP; d += 16) {
-                        uint32_t o[16];
-                        tmem_ld(t_o + d, o);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                        tmem_st(t_o + d, o);
-                    }
-                };
                 unsigned long long sum[2] = {0ull, 0ull};
-                if (warp_live && i == 0) {
-                    // a piece's first tile: all scores in registers, the maximum, the weights (32 h on
-                    // lie in columns 16 h on)
-                    uint32_t x[4][32];
-                    float top = -INFINITY;
-                    __syncwarp();
-#pragma unroll
-                    for (int h = 0; h < 4; ++h)
-                        tmem_ld_start(t_s + h * 32, x[h]);
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        tmem_ld_finish(x[h]);
-                        if (masked)
-                            hide(x[h], bits(jt, h));
-                        top = fmaxf(top, max32(x[h]));
+                if (warp_live) {
+                    if (masked) {
+#pragma unroll 1
+                        for (int h = 0; h < 4; ++h) {
+                            const uint32_t see = bits(jt, h);
+                            if (__all_sync(0xffffffffu, see == ~0u))
+                                continue;
+                            uint32_t x[32];
+                            tmem_ld(t_s + h * 32, x);
+                            hide(x, see);
+                            tmem_st(t_s + h * 32, x);
+                        }
+                        tmem_wait_st();
                     }
-                    m = top;
-                    const float shift = shift_of(m);
-                    const unsigned long long shift2 = f2(shift, shift);
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        uint32_t pk[16];
-                        weigh<DT>(x[h], c2, shift2, sum, pk);
-                        tmem_st(t_s + h * 16, pk);
+                    if (i == 0) {
+                        m = -INFINITY;
+#pragma unroll 1
+                        for (int h = 0; h < 4; ++h) {
+                            uint32_t x[32];
+                            tmem_ld(t_s + h * 32, x);
+                            m = fmaxf(m, max32(x));
+                        }
                     }
-                } else if (warp_live) {
                     // in one pass: weights by the maximum so far, which serves as long as no
                     // score is far above it; the tile's own maximum is found on the way
-                    const float shift = shift_of(m);
-                    const unsigned long long shift2 = f2(shift, shift);
+                    float shift = shift_of(m);
+                    unsigned long long shift2 = f2(shift, shift);
                     uint32_t x[32], y[32], pk[4][16];
                     __syncwarp();
                     tmem_ld_start(t_s, x);
                     tmem_ld_finish(x);
                     tmem_ld_start(t_s + 32, y);
-                    if (masked)
-                        hide(x, bits(jt, 0));
                     float top = max32(x);
                     weigh<DT>(x, c2, shift2, sum, pk[0]);
                     tmem_ld_finish(y);
                     tmem_ld_start(t_s + 64, x);
-                    if (masked)
-                        hide(y, bits(jt, 1));
                     top = fmaxf(top, max32(y));
                     weigh<DT>(y, c2, shift2, sum, pk[1]);
                     tmem_ld_finish(x);
                     tmem_ld_start(t_s + 96, y);
-                    if (masked)
-                        hide(x, bits(jt, 2));
                     top = fmaxf(top, max32(x));
                     weigh<DT>(x, c2, shift2, sum, pk[2]);
                     tmem_ld_finish(y);
-                    if (masked)
-                        hide(y, bits(jt, 3));
                     top = fmaxf(top, max32(y));
                     weigh<DT>(y, c2, shift2, sum, pk[3]);
-                    if (!__any_sync(0xffffffffu, (top - m) * P.c > growth<DT>())) {
+                    const bool grown = (top - m) * P.c > growth<DT>();  // -inf to finite too
+                    if (!__any_sync(0xffffffffu, grown)) {
+                        // weights 32 h on lie in columns 16 h on
 #pragma unroll
                         for (int h = 0; h < 4; ++h)
                             tmem_st(t_s + h * 16, pk[h]);
                     } else {
-                        // again, by the new maximum
-                        raise(top);
+                        // again, by the new maximum, which O and l follow
+                        const float f = grown ? ex2((m - top) * P.c) : 1.0f;
+                        l *= f;
+                        if (grown)
+                            m = top;
+#pragma unroll 1
+                        for (int d = 0; d < C::DP; d += 16) {
+                            uint32_t o[16];
+                            tmem_ld(t_o + d, o);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tmem_st(t_o + d, o);
+                        }
                         sum[0] = sum[1] = 0ull;
-                        const float shift = shift_of(m);
-                        const unsigned long long shift2 = f2(shift, shift);
+                        shift = shift_of(m);
+                        shift2 = f2(shift, shift);
 #pragma unroll 1
                         for (int h = 0; h < 4; ++h) {
                             tmem_ld(t_s + h * 32, x);
-                            if (masked)
-                                hide(x, bits(jt, h));
                             weigh<DT>(x, c2, shift2, sum, pk[0]);
                             tmem_st(t_s + h * 16, pk[0]);
                         }
                     }
-                }
-                if (warp_live) {
                     float s0, s1;
                     f2_split(add2(sum[0], sum[1]), s0, s1);
                     l += s0 + s1;
@@ -646,15 +638,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ++cnt;
                 vph ^= vst + 1 == C::VST ? 1u : 0u;
                 vst = vst + 1 == C::VST ? 0 : vst + 1;
-                if (masked)
-                    ++hid;
-            };
-            // tiles without a mask first, in a loop of their own: it stays small
-            int i = 0;
-            for (; i < plain && ok; ++i)
-                tile(i, Whole());
-            for (; i < p.n && ok; ++i)
-                tile(i, Masked());
+                hid += masked ? 1u : 0u;
+            }
             ok = ok && wait_group(&S.pvdone[s], pieces++ & 1u);
             if (!ok)
                 break;
@@ -727,8 +712,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (p.idle)
                     continue;
                 const int rows = P.page_rows, at = lane * rows;  // a box of rows per lane
+                const int plain = plain_tiles(p), turn = p.turn < plain ? p.turn : 0;
                 for (int i = 0; i < p.n && ok; ++i) {
-                    const int jt = p.tile0 + i, keys = tile_keys(p, jt);
+                    int jt = p.tile0 + i;
+                    if (i < plain)
+                        jt += i + turn < plain ? turn : turn - plain;
+                    const int keys = tile_keys(p, jt);
                     const bool mine = at < keys;
                     int y = jt * KT + at, w = p.b;
                     if (P.page_table && mine) {
