@@ -111,12 +111,13 @@ struct PickSmem {
     int count;
 };
 
-// Shared memory that a kernel is launched with: the groups' maxima of the scan, or a merge's heads
-// of lists (order, k V + x) and then what it has to sort, up to n entries of n lists (a place too).
+// Shared memory that a kernel is launched with: the groups' maxima of the scan, or a merge's first
+// entries of lists (order, k V + x; 4 n of them, or one of each list) and then what it has to
+// sort, up to n entries of n lists (a place too).
 constexpr size_t larger(size_t a, size_t b) { return a > b ? a : b; }
 constexpr size_t merge_bytes(int n, int lists)
 {
-    return larger((size_t)n * n * 16, (size_t)lists * 12);
+    return larger((size_t)n * n * 16, larger((size_t)lists, (size_t)4 * n) * 12);
 }
 constexpr size_t SCAN_BYTES = (size_t)GROUPS * TH * 4;
 extern __shared__ __align__(16) uint8_t dyn[];
@@ -126,23 +127,32 @@ __device__ __forceinline__ bool better(u64 r1, int f1, u64 r2, int f2)
     return r1 > r2 || (r1 == r2 && f1 < f2);
 }
 
+// How many of m things are better than this one, by a converged warp: `is_better(j)` asks for one.
+template <typename F>
+__device__ __forceinline__ int place_of(int m, F is_better)
+{
+    const int lane = (int)threadIdx.x & 31;
+    int place = 0;
+    for (int j0 = 0; j0 < m; j0 += 32)
+        place += __popc(__ballot_sync(0xffffffffu, j0 + lane < m && is_better(j0 + lane)));
+    return place;
+}
+
 // The candidates' best n, sorted, to S.cand; returns the order that a later one has to exceed.
 // The whole CTA; S.count candidates (at most CAP).
 __device__ uint32_t cut(ScanSmem &S, int n)
 {
-    const int tid = (int)threadIdx.x;
+    const int tid = (int)threadIdx.x, lane = tid & 31;
     __syncthreads();
     const int m = S.count;
     if (tid < n)
         S.best[tid] = 0;
     __syncthreads();
-    for (int i = tid; i < m; i += TH) {
+    for (int i = tid >> 5; i < m; i += WARPS) {
         const u64 key = S.cand[i];
-        int rank = 0;
-        for (int j = 0; j < m && rank < n; ++j)
-            rank += S.cand[j] > key ? 1 : 0;
-        if (rank < n)
-            S.best[rank] = key;
+        const int place = place_of(m, [&](int j) { return S.cand[j] > key; });
+        if (lane == 0 && place < n)
+            S.best[place] = key;
     }
     __syncthreads();
     if (tid < n)
@@ -225,11 +235,13 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
         flat = k * A.V + token_of(key);
         return ordered((S.score[k] + ((double)value_of(key) - S.lse[k])) * S.inv[k]);
     };
-    // the n-th best head: no more than n lists reach it
+    // the n-th best of the lists' first entries: no more than n lists reach it, and where a few of each
+    // list are looked at, not many more than n entries
+    const int deep = min(n, max(1, 4 * n / lists)), firsts = lists * deep;
     u64 *rank = reinterpret_cast<u64 *>(dyn);
-    int *flat = reinterpret_cast<int *>(rank + lists);
-    for (int l = tid; l < lists; l += TH)
-        rank[l] = load(l, 0, flat[l]);
+    int *flat = reinterpret_cast<int *>(rank + firsts);
+    for (int e = tid; e < firsts; e += TH)
+        rank[e] = load(e / deep, e % deep, flat[e]);
     if (tid == 0) {
         S.least = 0;
         S.least_flat = INT_MAX;
@@ -238,13 +250,11 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
     if (tid <= n)
         S.rank[tid] = 0;
     __syncthreads();
-    for (int l = tid; l < lists; l += TH) {
-        const u64 r = rank[l];
-        const int f = flat[l];
-        int place = 0;
-        for (int j = 0; j < lists && place < n; ++j)
-            place += better(rank[j], flat[j], r, f) ? 1 : 0;
-        if (r != 0 && place == n - 1) {
+    for (int e = warp; e < firsts; e += WARPS) {
+        const u64 r = rank[e];
+        const int f = flat[e];
+        const int place = place_of(firsts, [&](int j) { return better(rank[j], flat[j], r, f); });
+        if (lane == 0 && r != 0 && place == n - 1) {
             S.least = r;
             S.least_flat = f;
         }
@@ -269,13 +279,11 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
     }
     __syncthreads();
     const int m = min(S.count, n * n);
-    for (int i = tid; i < m; i += TH) {
+    for (int i = warp; i < m; i += WARPS) {
         const u64 r = rank[i];
         const int f = flat[i];
-        int place = 0;
-        for (int j = 0; j < m && place <= n; ++j)
-            place += better(rank[j], flat[j], r, f) ? 1 : 0;
-        if (place <= n) {
+        const int place = place_of(m, [&](int j) { return better(rank[j], flat[j], r, f); });
+        if (lane == 0 && place <= n) {
             S.rank[place] = r;
             S.flat[place] = f;
             S.entry[place] = entry[i];
@@ -490,32 +498,32 @@ __global__ void __launch_bounds__(TH, 4) beam_kernel(const __grid_constant__ Bea
             for (int u = 0; u < UN; ++u)
                 raw[u] = ahead[u];
         }
-        // the bound: the n-th of the warps' 8 best threads
-        float mine = bad ? -INFINITY : top, most = top;
-        for (int i = 0; i < 8; ++i) {
-            float x = mine;
-            for (int d = 16; d; d >>= 1)
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-            most = i == 0 ? x : most;
-            const uint32_t who = __ballot_sync(0xffffffffu, mine == x);
-            if (lane == __ffs((int)who) - 1) {
-                S.best[warp * 8 + i] = candidate(ordered(mine), warp * 8 + i);
-                mine = -INFINITY;
+        // the bound: the n-th of the warps' 8 best threads, whose maxima each warp sorts (a bitonic
+        // network over its lanes)
+        uint32_t mine = bad ? NONE : ordered(top);
+#pragma unroll
+        for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+            for (int d = size >> 1; d; d >>= 1) {
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, d);
+                const bool larger_one = ((lane & d) == 0) == ((lane & size) == 0 || size == 32);
+                mine = larger_one ? max(mine, other) : min(mine, other);
             }
-        }
+        if (lane < 8)
+            S.best[warp * 8 + lane] = (u64)mine << 32 | (uint32_t)(warp * 8 + lane);
         if (lane == 0)
-            S.part[warp][0] = most;
+            S.part[warp][0] = mine == NONE ? -INFINITY : value_of((u64)mine << 32);
         if (tid == 0)
             S.count = 0;
         bad = __syncthreads_or(bad ? 1 : 0) != 0;
-        if (tid < 8 * WARPS) {
-            const u64 key = S.best[tid];
-            int place = 0;
-            for (int j = 0; j < 8 * WARPS; ++j)
-                place += S.best[j] > key ? 1 : 0;
-            if (place == n - 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const u64 key = S.best[warp * 8 + i];
+            const int place = place_of(8 * WARPS, [&](int j) { return S.best[j] > key; });
+            if (lane == 0 && place == n - 1)
                 S.bound = (uint32_t)(key >> 32);
         }
+        float most = -INFINITY;
         // the segment's total
         for (int w = 0; w < WARPS; ++w)
             most = fmaxf(most, S.part[w][0]);

@@ -89,11 +89,9 @@ __device__ void list_free(const int32_t *ref, int32_t *ref_out, int num_pages, i
 // Free pages before each block, to smem[0 .. blocks]; the whole CTA.
 __device__ void sum_blocks(const int *free_of, int blocks, int *sums)
 {
-    __shared__ int part[WARPS], base;
+    __shared__ int part[WARPS];
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0)
-        base = 0;
-    __syncthreads();
+    int base = 0;
     for (int i0 = 0; i0 < blocks; i0 += TH) {
         const int own = i0 + tid < blocks ? __ldcg(free_of + i0 + tid) : 0;
         int v = own;
@@ -106,13 +104,12 @@ __device__ void sum_blocks(const int *free_of, int blocks, int *sums)
             part[warp] = v;
         __syncthreads();
         int before = base;
-        for (int w = 0; w < warp; ++w)
-            before += part[w];
+        for (int w = 0; w < WARPS; ++w) {
+            before += w < warp ? part[w] : 0;
+            base += part[w];
+        }
         if (i0 + tid < blocks)
             sums[i0 + tid] = before + v - own;
-        __syncthreads();
-        if (tid == TH - 1)
-            base = before + v;
         __syncthreads();
     }
     if (tid == 0)
@@ -134,24 +131,29 @@ struct Old {
     bool ok;
 };
 
+constexpr int AHEAD = 4;  // 32 entries each that a warp has in flight
+
 __device__ __forceinline__ Old old_row(const spec_pages_fork_args &A, int o)
 {
-    const int lane = (int)threadIdx.x & 31;
+    const int lane = (int)threadIdx.x & 31, M = A.pages_per_seq;
+    const int32_t *row = A.table_in + (size_t)o * M;
     Old r;
     r.length = __ldg(A.length_in + o);
-    r.held = A.pages_per_seq;
+    r.held = M;
     bool bad = false;
-    for (int i0 = 0; i0 < A.pages_per_seq; i0 += 32) {
-        const int i = i0 + lane;
-        const int e = i < A.pages_per_seq
-            ? __ldg(A.table_in + (size_t)o * A.pages_per_seq + i) : -1;
-        bad |= e >= A.num_pages;
-        const uint32_t none = __ballot_sync(0xffffffffu, e < 0);
-        if (none) {
-            const int at = i0 + __ffs((int)none) - 1;
-            r.held = min(at, A.pages_per_seq);
-            bad = bad && i < at;  // entries behind the first -1 are not looked at
-            break;
+    for (int i0 = 0; i0 < M && r.held == M; i0 += 32 * AHEAD) {
+        int e[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+            e[u] = i0 + u * 32 + lane < M ? __ldg(row + i0 + u * 32 + lane) : -1;
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            const int at = i0 + u * 32;
+            const uint32_t none = __ballot_sync(0xffffffffu, e[u] < 0);
+            if (at < r.held && none)
+                r.held = min(at + __ffs((int)none) - 1, M);
+            // (entries behind the first -1 are not looked at)
+            bad |= e[u] >= A.num_pages && at + lane < r.held;
         }
     }
     r.ok = !__any_sync(0xffffffffu, bad) && r.length >= 0 &&
@@ -170,11 +172,18 @@ __device__ __forceinline__ int pages_for(const spec_pages_fork_args &A, int leng
 __device__ bool has_child(const spec_pages_fork_args &A, int o, int length, int end)
 {
     const int lane = (int)threadIdx.x & 31;
-    for (int i0 = 0; i0 < end; i0 += 32) {
-        const int i = i0 + lane;
-        bool hit = i < end && __ldg(A.parent + i) == o;
-        if (hit)
-            hit = pages_for(A, length, A.reserve ? __ldg(A.reserve + i) : 0) >= 0;
+    for (int i0 = 0; i0 < end; i0 += 32 * AHEAD) {
+        int parent[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            const int i = i0 + u * 32 + lane;
+            parent[u] = i < end ? __ldg(A.parent + i) : -1;
+        }
+        bool hit = false;
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+            if (parent[u] == o)
+                hit |= pages_for(A, length, A.reserve ? __ldg(A.reserve + i0 + u * 32 + lane) : 0) >= 0;
         if (__any_sync(0xffffffffu, hit))
             return true;
     }
@@ -234,14 +243,16 @@ __global__ void __launch_bounds__(TH) fork_rows_kernel(const __grid_constant__ F
 {
     extern __shared__ int sums[];  // free pages before each block
     __shared__ long long part[WARPS][2];
+    __shared__ int own[WARPS];      // pages that this CTA's rows take
     const spec_pages_fork_args &A = P.a;
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
     allow_next_kernel();
     wait_previous_kernel();
-    sum_blocks(P.w.free_of, P.blocks, sums);
     // pages that the rows before this CTA's take, and all rows
     const int r0 = (int)blockIdx.x * WARPS;
     long long before = 0, all = 0;
+    if (tid < WARPS)
+        own[tid] = r0 + tid < A.rows_out ? __ldcg(P.w.need + r0 + tid) : 0;
     for (int i = tid; i < A.rows_out; i += TH) {
         const int n = __ldcg(P.w.need + i);
         all += n;
@@ -255,7 +266,7 @@ __global__ void __launch_bounds__(TH) fork_rows_kernel(const __grid_constant__ F
         part[warp][0] = before;
         part[warp][1] = all;
     }
-    __syncthreads();
+    sum_blocks(P.w.free_of, P.blocks, sums);  // (and all have written theirs)
     before = all = 0;
     for (int w = 0; w < WARPS; ++w) {
         before += part[w][0];
@@ -278,8 +289,8 @@ __global__ void __launch_bounds__(TH) fork_rows_kernel(const __grid_constant__ F
             const int32_t *old = A.table_in + (size_t)max(parent, 0) * M;
             length = o.length;
             long long next = before;
-            for (int w = r0; w < r; ++w)
-                next += __ldcg(P.w.need + w);
+            for (int w = 0; w < warp; ++w)
+                next += own[w];
             for (int i0 = 0; i0 < M; i0 += 32) {
                 const int i = i0 + lane;
                 const int e = i < o.held ? __ldg(old + i) : -1;
