@@ -41,14 +41,15 @@ constexpr int TH = 256;            // threads of a CTA
 constexpr int WARPS = TH / 32;
 static_assert(8 * WARPS >= SPEC_BEAM_MAX, "the first bound comes from 8 threads of a warp");
 constexpr int UN = 4;              // vectors of a group
-constexpr int GROUPS = 16;         // most groups of a thread, in a segment
+constexpr int GROUPS = 32;         // most groups of a thread, in a segment
+static_assert(GROUPS <= 32, "a thread's groups are bits of a word");
 constexpr int CAP = 1024;          // candidates of a segment before they are cut
 constexpr int MAX_LISTS = 2048;    // segments of a sequence's beams: 1216 / K + 1, or 19 for the longest rows
 constexpr int EXACT_CTAS = 304;
 constexpr size_t MAX_B = 65536;    // sequences that the counters have room for
 // How far a row's logarithm of its total may be off, in nats: exponents' rounding (2^-23 of up to
-// 24 binary digits, and the constant's 2^-25: 2.5e-6), ex2 three times (2^-22 each), some 19 fp32
-// additions of 2^-24
+// 24 binary digits, and the constant's 2^-25: 2.5e-6), ex2 three times (2^-22 each: 0.7e-6), some 26
+// fp32 additions and products of 2^-24 (1.6e-6)
 constexpr double LSE_OFF = 5e-6;
 constexpr float SLACK = 5.0f;      // nats that a maximum may run ahead of its sum's scale
 
@@ -104,8 +105,10 @@ struct ScanSmem {
 
 struct PickSmem {
     double lse[SPEC_BEAM_MAX], score[SPEC_BEAM_MAX], inv[SPEC_BEAM_MAX];
+    float2 total[SPEC_BEAM_MAX];  // a row's largest logit and sum of exp(x - largest)
     u64 rank[SPEC_BEAM_MAX + 1];  // the best n and the next, sorted
-    int flat[SPEC_BEAM_MAX + 1], entry[SPEC_BEAM_MAX + 1];
+    int flat[SPEC_BEAM_MAX + 1];
+    float value[SPEC_BEAM_MAX + 1];  // logits
     u64 least;
     int least_flat;
     int count;
@@ -171,39 +174,62 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
     const spec_beam_select_args &A = P.a;
     const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
     bool bad = false;
-    for (int k = warp; k < A.K; k += WARPS) {
-        const int row = b * A.K + k;
-        const float s = A.scores[row], norm = A.norm ? A.norm[row] : 1.0f;
-        const bool fin = A.finished && A.finished[row] != 0;
-        bad |= isnan(s) || s == INFINITY;
-        if (s == -INFINITY)
-            continue;
-        bad |= !(norm > 0.0f) || isinf(norm);
-        double lse = 0.0;
-        if (!fin && !EXACT) {
-            float top = -INFINITY;
-            for (int g = lane; g < P.segs; g += 32) {
-                const float2 x = __ldcg(&P.stats[(size_t)row * P.segs + g]);
-                bad |= isnan(x.x);
-                top = fmaxf(top, x.x);
+    // the rows' totals, a row per warp; what takes 64 bits for all rows at once, a row per lane (this
+    // GPU has two 64-bit lanes per SM: by the warps one after the other it took 10 us)
+    if (!EXACT)
+        for (int k = warp; k < A.K; k += WARPS) {
+            const size_t first = ((size_t)b * A.K + k) * P.segs;
+            const float s = A.scores[b * A.K + k];
+            if (!(s > -INFINITY) || (A.finished && A.finished[b * A.K + k] != 0))
+                continue;
+            float2 x = make_float2(-INFINITY, 0.0f), y = x;
+            if (lane < P.segs)
+                x = __ldcg(&P.stats[first + lane]);
+            float top = x.x, z = 0.0f;
+            bad |= isnan(x.x);
+            for (int g = lane + 32; g < P.segs; g += 32) {
+                y = __ldcg(&P.stats[first + g]);
+                bad |= isnan(y.x);
+                top = fmaxf(top, y.x);
             }
             for (int d = 16; d; d >>= 1)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            double z = 0.0;
-            for (int g = lane; g < P.segs; g += 32) {
-                const float2 x = __ldcg(&P.stats[(size_t)row * P.segs + g]);
-                if (x.x > -INFINITY)
-                    z += (double)x.y * (double)ex2((x.x - top) * LOG2E);
+            if (x.x > -INFINITY)
+                z = x.y * ex2((x.x - top) * LOG2E);
+            for (int g = lane + 32; g < P.segs; g += 32) {
+                y = __ldcg(&P.stats[first + g]);
+                if (y.x > -INFINITY)
+                    z += y.y * ex2((y.x - top) * LOG2E);
             }
             for (int d = 16; d; d >>= 1)
                 z += __shfl_xor_sync(0xffffffffu, z, d);
-            lse = top > -INFINITY ? (double)top + log(z) : 0.0;
+            if (lane == 0)
+                S.total[k] = make_float2(top, z);
         }
-        if (lane == 0) {
-            S.score[k] = (double)s;
-            S.inv[k] = 1.0 / (double)norm;
-            if (!EXACT)
-                S.lse[k] = lse;
+    __syncthreads();
+    if (tid < A.K) {
+        const int row = b * A.K + tid;
+        const float s = A.scores[row], norm = A.norm ? A.norm[row] : 1.0f;
+        bad |= isnan(s) || s == INFINITY;
+        if (s > -INFINITY) {
+            bad |= !(norm > 0.0f) || isinf(norm);
+            S.score[tid] = (double)s;
+            // 1 / norm: fp32's, and a step of Newton's iteration
+            const double guess = (double)(1.0f / norm);
+            S.inv[tid] = A.norm ? guess * (2.0 - (double)norm * guess) : 1.0;
+            if (!EXACT) {
+                // ln z = e ln 2 + ln m, m in [2/3, 4/3)
+                const bool fin = A.finished && A.finished[row] != 0;
+                const float2 x = fin ? make_float2(0.0f, 1.0f) : S.total[tid];
+                int e;
+                float m = frexpf(x.y, &e);
+                if (m < 2.0f / 3.0f) {
+                    m *= 2.0f;
+                    --e;
+                }
+                S.lse[tid] = x.x > -INFINITY
+                    ? (double)x.x + ((double)e * 0.693147180559945309 + (double)logf(m)) : 0.0;
+            }
         }
     }
     bad = __syncthreads_or(bad ? 1 : 0) != 0;
@@ -218,7 +244,7 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
     }
     // candidate `at` of list l: its order (0: none) and k V + x
     const int lists = A.K * P.segs, n = A.n;
-    auto load = [&](int l, int at, int &flat) -> u64 {
+    auto load = [&](int l, int at, int &flat, float &value) -> u64 {
         const int k = l / P.segs, row = b * A.K + k;
         flat = INT_MAX;
         if (A.scores[row] == -INFINITY)
@@ -233,15 +259,17 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
         if (key == 0)
             return 0;
         flat = k * A.V + token_of(key);
-        return ordered((S.score[k] + ((double)value_of(key) - S.lse[k])) * S.inv[k]);
+        value = value_of(key);
+        return ordered((S.score[k] + ((double)value - S.lse[k])) * S.inv[k]);
     };
     // the n-th best of the lists' first entries: no more than n lists reach it, and where a few of each
     // list are looked at, not many more than n entries
     const int deep = min(n, max(1, 4 * n / lists)), firsts = lists * deep;
     u64 *rank = reinterpret_cast<u64 *>(dyn);
     int *flat = reinterpret_cast<int *>(rank + firsts);
+    float x = 0.0f;
     for (int e = tid; e < firsts; e += TH)
-        rank[e] = load(e / deep, e % deep, flat[e]);
+        rank[e] = load(e / deep, e % deep, flat[e], x);
     if (tid == 0) {
         S.least = 0;
         S.least_flat = INT_MAX;
@@ -262,18 +290,18 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
     __syncthreads();
     // the entries that reach it (n n of them at most, in the place of the heads)
     flat = reinterpret_cast<int *>(rank + n * n);
-    int *entry = flat + n * n;
+    float *value = reinterpret_cast<float *>(flat + n * n);
     const u64 least = S.least;
     const int least_flat = S.least_flat;
     for (int e = tid; e < lists * n; e += TH) {
         int f;
-        const u64 r = load(e / n, e % n, f);
+        const u64 r = load(e / n, e % n, f, x);
         if (r != 0 && !better(least, least_flat, r, f)) {
             const int i = atomicAdd(&S.count, 1);
             if (i < n * n) {
                 rank[i] = r;
                 flat[i] = f;
-                entry[i] = e;
+                value[i] = x;
             }
         }
     }
@@ -286,7 +314,7 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
         if (lane == 0 && place <= n) {
             S.rank[place] = r;
             S.flat[place] = f;
-            S.entry[place] = entry[i];
+            S.value[place] = value[i];
         }
     }
     __syncthreads();
@@ -295,14 +323,12 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
         int token = -1, beam = -1;
         float score = -INFINITY;
         if (S.rank[tid] != 0) {
-            const int k = S.flat[tid] / A.V, e = S.entry[tid];
+            const int k = S.flat[tid] / A.V;
             beam = k;
             token = S.flat[tid] - k * A.V;
             score = (float)S.score[k];
             if (!(A.finished && A.finished[b * A.K + k] != 0))
-                score = (float)(S.score[k] +
-                                ((double)value_of(__ldcg(&P.lists[(size_t)b * lists * n + e])) -
-                                 S.lse[k]));
+                score = (float)(S.score[k] + ((double)S.value[tid] - S.lse[k]));
             // the next one may lie too near
             if (!EXACT && S.rank[tid + 1] != 0 && S.flat[tid + 1] / A.V != k) {
                 const double off = LSE_OFF * (S.inv[k] + S.inv[S.flat[tid + 1] / A.V]);
@@ -449,14 +475,15 @@ __global__ void __launch_bounds__(TH, 4) beam_kernel(const __grid_constant__ Bea
     const int b = row / A.K, n = A.n;
     allow_next_kernel();
     wait_previous_kernel();
+    // (the first group is on its way before it is known whether the beam counts)
+    const Segment<DT> G(P, row, seg);
+    uint4 raw[UN], ahead[UN];
+#pragma unroll
+    for (int u = 0; u < UN; ++u)
+        raw[u] = G.fetch(G.v0 + u * TH + tid);
     const bool counts = A.scores[row] > -INFINITY && !(A.finished && A.finished[row] != 0);
     if (counts) {
-        const Segment<DT> G(P, row, seg);
         float *maxima = reinterpret_cast<float *>(dyn) + tid;  // of the thread's groups
-        uint4 raw[UN], ahead[UN];
-#pragma unroll
-        for (int u = 0; u < UN; ++u)
-            raw[u] = G.fetch(G.v0 + u * TH + tid);
         float m = -INFINITY, top = -INFINITY, sum = 0.0f, low = 0.0f;  // sum + low in units of e^m
         bool bad = false;
         const u64 c2 = f2(LOG2E, LOG2E);
@@ -544,16 +571,22 @@ __global__ void __launch_bounds__(TH, 4) beam_kernel(const __grid_constant__ Bea
             const uint32_t above = max(S.bound, NONE + 1) - 1;  // the bound itself included
             if (ordered(lone) > above)
                 S.cand[atomicAdd(&S.count, 1)] = candidate(ordered(lone), G.edge_col(tid));
-            for (int g = 0; g < groups; ++g) {
-                if (ordered(maxima[g * TH]) <= above)
-                    continue;
-                const int v = G.v0 + g * TH * UN + tid;
+            uint32_t reach = 0;  // the thread's groups that do, each lane's next one at a time
+#pragma unroll 4
+            for (int g = 0; g < groups; ++g)
+                reach |= (ordered(maxima[g * TH]) > above ? 1u : 0u) << g;
+            for (; reach; reach &= reach - 1) {
+                const int v = G.v0 + (__ffs((int)reach) - 1) * TH * UN + tid;
+#pragma unroll
+                for (int u = 0; u < UN; ++u)
+                    raw[u] = G.fetch(v + u * TH);
+#pragma unroll
                 for (int u = 0; u < UN; ++u) {
-                    const uint4 r = G.fetch(v + u * TH);
-                    if (ordered(L::vmax(r)) <= above)
+                    if (ordered(L::vmax(raw[u])) <= above)
                         continue;
                     float x[L::VEC];
-                    L::unpack(r, x);
+                    L::unpack(raw[u], x);
+#pragma unroll
                     for (int j = 0; j < L::VEC; ++j) {
                         const uint32_t o = ordered(x[j]);
                         if (o > above) {
@@ -575,9 +608,9 @@ __global__ void __launch_bounds__(TH, 4) beam_kernel(const __grid_constant__ Bea
         }
     }
     // the sequence's last CTA merges
-    __threadfence();
     __syncthreads();
     if (tid == 0) {
+        __threadfence();
         last = atomicAdd(&P.arrived[b], 1) == A.K * P.segs - 1;
         if (last)
             P.arrived[b] = 0;
@@ -745,14 +778,15 @@ bool sizes_ok(int32_t B, int32_t K, int32_t V, int32_t n, int32_t dtype)
            V >= 2 && V <= SPEC_MAX_V && (dtype == SPEC_F32 || dtype == SPEC_BF16);
 }
 
-// Segments of a row: eight CTAs per SM in all, no more groups than a thread has room for, and no
-// fewer than one.
+// Segments of a row: as many CTAs in all as run at a time (four per SM), each of which ends with some
+// us of choosing; no more groups than a thread has room for, and no fewer than one.  (64 x 8 rows of
+// 128256: in one segment XX us, in three YY us.)
 int segments(int32_t B, int32_t K, int32_t V, int32_t dtype)
 {
     const long long rows = (long long)B * K;
     const int vecs = V / (dtype == SPEC_F32 ? 4 : 8) + 2;
     const int tiles = (vecs + TH * UN - 1) / (TH * UN), least = (tiles + GROUPS - 2) / (GROUPS - 1);
-    long long s = rows > 0 ? (1216 + rows - 1) / rows : 1;
+    long long s = rows > 0 ? 608 / rows : 1;
     s = s < tiles ? s : tiles;
     return s < least ? least : (int)s;
 }
