@@ -150,12 +150,8 @@ class _CopyArgs(ctypes.Structure):
 _pack_attention = struct.Struct("@5Q15q4Qf9i").pack
 _pack_commit = struct.Struct("@4Q16q5Q9i4x").pack
 _pack_logits = struct.Struct("@14Q2q7i4x").pack
-_pack_append = struct.Struct("@4Q14q4Q9i4x").pack
-_pack_chunk = struct.Struct("@3Q8q4Qf9i").pack
-_pack_beam = struct.Struct("@7Q6i").pack
-_pack_fork = struct.Struct("@9Q5i4x").pack
-_pack_compact = struct.Struct("@6Q4i").pack
-_pack_copy = struct.Struct("@2Q8qQ7i4x").pack
+_pack_chunk = struct.Struct("@4Qf").pack
+_pack_beam = struct.Struct("@7Q").pack
 
 
 def library():
@@ -1454,6 +1450,31 @@ def spec_process_logits(logits, history=None, history_len=None, prompt_len=None,
 
 
 # --------------------------------------------------- chunks of new tokens
+#
+# A call's checks depend on its tensors' shapes, strides, dtypes and devices
+# alone (addresses apart, which the library checks), so each function keeps what
+# they came to by those: with small kernels the checks cost more than the launch.
+
+def _meta(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+
+
+class _Checked(dict):
+    """What a function's checks came to, by what they depend on."""
+
+    def __call__(self, key, check):
+        got = self.get(key)
+        if got is None:
+            if len(self) >= 4096:
+                self.clear()
+            got = self[key] = check()
+        return got
+
+
+_checked_append, _checked_plan, _checked_chunk = _Checked(), _Checked(), _Checked()
+_checked_beam, _checked_reorder = _Checked(), _Checked()
+_checked_fork, _checked_compact, _checked_copy = _Checked(), _Checked(), _Checked()
+
 
 def _scratch(cache, need, device, h, s, zeroed=False):
     """A workspace of `need` bytes from `cache`, one per (host thread, device, stream).
@@ -1477,13 +1498,42 @@ _chunk_ws, _beam_ws, _pages_ws = _Workspaces(), _Workspaces(), _Workspaces()
 
 
 def _caches(k_cache, v_cache, lead, Hkv, D, dtype):
-    """Checks the caches [*lead, pages, slots, Hkv, D]; (pages, slots)."""
+    """Checks the caches [*lead, pages, slots, Hkv, D]."""
     P, S = k_cache.shape[-4:-2]
     if k_cache.shape != (*lead, P, S, Hkv, D) or v_cache.shape != k_cache.shape:
         raise ValueError(f"k_cache and v_cache must be {(*lead, 'pages', 'slots', Hkv, D)}")
     if not dtype == k_cache.dtype == v_cache.dtype:
         raise TypeError("keys, values and their caches must share a dtype")
-    return P, S
+
+
+_plain_empty = None
+
+
+def _new(s, shape, strides, dtype, dev):
+    """A contiguous output, of these strides, for use on stream `s` (None: the current
+    one).  On the current device and stream it is made by the function that PyTorch's own
+    generated code calls, in half of torch.empty's time."""
+    global _plain_empty
+    if _plain_empty is None:
+        guards = getattr(getattr(_torch()._C, "_dynamo", None), "guards", None)
+        _plain_empty = getattr(guards, "_empty_strided_cuda", False)
+    if s is None and _plain_empty and _raw_getters[1]() == dev.index:
+        return _plain_empty(shape, strides, dtype)
+    return _empty_on(s, shape, dtype, dev)
+
+
+def _strides_of(shape):
+    st = [1] * len(shape)
+    for i in range(len(shape) - 2, -1, -1):
+        st[i] = st[i + 1] * max(1, shape[i + 1])
+    return tuple(st)
+
+
+def _ptr_of(t):
+    return 0 if t is None else t.data_ptr()
+
+
+_pack_4q, _pack_5q, _pack_3q = (struct.Struct(f).pack for f in ("@4Q", "@5Q", "@3Q"))
 
 
 def spec_chunk_append(k_new, v_new, k_cache, v_cache, row_start, cache_len, page_table=None,
@@ -1497,36 +1547,46 @@ def spec_chunk_append(k_new, v_new, k_cache, v_cache, row_start, cache_len, page
     Returns the new lengths int32 [B] (-1 for a sequence error, whose cache is
     left alone); asynchronous like any CUDA op."""
     torch = _torch()
-    if k_new.dim() not in (3, 4) or k_cache.dim() != k_new.dim() + 1:
-        raise ValueError("k_new [.., rows, Hkv, D] and k_cache [.., pages, slots, Hkv, D] expected")
-    *lead, T, Hkv, D = k_new.shape
-    if v_new.shape != k_new.shape:
-        raise ValueError("k_new and v_new must have one shape")
-    if k_new.dtype not in (torch.bfloat16, torch.float16, torch.float32):
-        raise TypeError(f"k_new must be bfloat16, float16 or float32, got {k_new.dtype}")
-    if v_new.dtype != k_new.dtype:
-        raise TypeError("k_new and v_new must share a dtype")
-    _caches(k_cache, v_cache, lead, Hkv, D, k_new.dtype)
-    if cache_len.dim() != 1:
-        raise ValueError("cache_len must be [B]")
-    dev, i32, B = k_new.device, torch.int32, cache_len.shape[0]
-    start = _array("row_start", row_start, (B + 1,), i32, dev)
-    length = _array("cache_len", cache_len, (B,), i32, dev)
-    geometry, table = _geometry(k_cache, page_table, B, dev)
-    at, strides = [], []
-    for name, t in (("k_new", k_new), ("v_new", v_new), ("k_cache", k_cache),
-                    ("v_cache", v_cache)):
-        a, st = _strided(name, t, dev, 1)
-        at.append(a)
-        strides += st if lead else (0, *st)
+
+    def check():
+        if k_new.dim() not in (3, 4) or k_cache.dim() != k_new.dim() + 1:
+            raise ValueError("k_new [.., rows, Hkv, D] and k_cache [.., pages, slots, Hkv, D] "
+                             "expected")
+        *lead, T, Hkv, D = k_new.shape
+        if v_new.shape != k_new.shape:
+            raise ValueError("k_new and v_new must have one shape")
+        if k_new.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+            raise TypeError(f"k_new must be bfloat16, float16 or float32, got {k_new.dtype}")
+        if v_new.dtype != k_new.dtype:
+            raise TypeError("k_new and v_new must share a dtype")
+        _caches(k_cache, v_cache, lead, Hkv, D, k_new.dtype)
+        if cache_len.dim() != 1:
+            raise ValueError("cache_len must be [B]")
+        dev, i32, B = k_new.device, torch.int32, cache_len.shape[0]
+        _array("row_start", row_start, (B + 1,), i32, dev)
+        _array("cache_len", cache_len, (B,), i32, dev)
+        geometry, _ = _geometry(k_cache, page_table, B, dev)
+        strides = []
+        for name, t in (("k_new", k_new), ("v_new", v_new), ("k_cache", k_cache),
+                        ("v_cache", v_cache)):
+            st = _strided(name, t, dev, 1)[1]
+            strides += st if lead else (0, *st)
+        if out_len is not None:
+            _dev_out("out_len", out_len, (B,), i32, dev)
+        return (dev, (B,), struct.pack("@14q", *strides),
+                struct.pack("@9i4x", lead[0] if lead else 1, B, T, Hkv, D, *geometry,
+                            k_new.element_size()))
+    dev, shape, strides, sizes = _checked_append(
+        (_meta(k_new), _meta(v_new), _meta(k_cache), _meta(v_cache), _meta(row_start),
+         _meta(cache_len), _meta(page_table), _meta(out_len)), check)
     h, s = _call_stream(stream, dev, (k_new, v_new, k_cache, v_cache, row_start, cache_len,
                                       page_table, out_len))
     if out_len is None:
-        out_len = _empty_on(s, (B,), i32, dev)
-    else:
-        _dev_out("out_len", out_len, (B,), i32, dev)
-    args = _pack_append(*at, *strides, start, length, table, out_len.data_ptr(),
-                        lead[0] if lead else 1, B, T, Hkv, D, *geometry, k_new.element_size())
+        out_len = _new(s, shape, (1,), torch.int32, dev)
+    args = b"".join((_pack_4q(k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(),
+                              v_cache.data_ptr()), strides,
+                     _pack_4q(row_start.data_ptr(), cache_len.data_ptr(), _ptr_of(page_table),
+                              out_len.data_ptr()), sizes))
     _launch(dev, "spec_chunk_append", (_lib or library()).spec_chunk_append, args, h)
     return out_len
 
@@ -1569,19 +1629,25 @@ def spec_chunk_plan(row_start, kv_len, q, k_cache, page_table=None, plan=None, s
     `plan` refills a ChunkPlan of the same sizes.  Returns a ChunkPlan;
     asynchronous like any CUDA op."""
     torch = _torch()
-    if kv_len.dim() != 1 or q.dim() != 3 or k_cache.dim() != 4:
-        raise ValueError("kv_len must be [B], q [rows, Hq, D] and k_cache [pages, slots, Hkv, D]")
-    B, (T, Hq), Hkv = kv_len.shape[0], q.shape[:2], k_cache.shape[2]
-    if Hkv < 1 or Hq % Hkv:
-        raise ValueError(f"{Hq} query heads do not divide among {Hkv} key heads")
-    G = Hq // Hkv
-    dev, i32 = kv_len.device, torch.int32
-    r = _array("row_start", row_start, (B + 1,), i32, dev)
-    n = _array("kv_len", kv_len, (B,), i32, dev)
-    geometry, table = _geometry(k_cache, page_table, B, dev)
-    need = _chunk_layout(B, T, G)[0]
-    if need == 0:
-        raise ValueError(f"sizes out of range: B={B} rows={T} Hq/Hkv={G}")
+
+    def check():
+        if kv_len.dim() != 1 or q.dim() != 3 or k_cache.dim() != 4:
+            raise ValueError("kv_len must be [B], q [rows, Hq, D] and k_cache "
+                             "[pages, slots, Hkv, D]")
+        B, (T, Hq), Hkv = kv_len.shape[0], q.shape[:2], k_cache.shape[2]
+        if Hkv < 1 or Hq % Hkv:
+            raise ValueError(f"{Hq} query heads do not divide among {Hkv} key heads")
+        G = Hq // Hkv
+        dev, i32 = kv_len.device, torch.int32
+        _array("row_start", row_start, (B + 1,), i32, dev)
+        _array("kv_len", kv_len, (B,), i32, dev)
+        geometry, _ = _geometry(k_cache, page_table, B, dev)
+        need = _chunk_layout(B, T, G)[0]
+        if need == 0:
+            raise ValueError(f"sizes out of range: B={B} rows={T} Hq/Hkv={G}")
+        return dev, B, T, G, geometry, need
+    dev, B, T, G, geometry, need = _checked_plan(
+        (_meta(row_start), _meta(kv_len), q.shape, k_cache.shape, _meta(page_table)), check)
     if plan is not None and ((plan.B, plan.rows, plan.group) != (B, T, G)
                              or plan.data.device != dev):
         raise ValueError(f"plan is for B={plan.B} rows={plan.rows} Hq/Hkv={plan.group} on "
@@ -1589,10 +1655,11 @@ def spec_chunk_plan(row_start, kv_len, q, k_cache, page_table=None, plan=None, s
     h, s = _call_stream(stream, dev, (row_start, kv_len, page_table,
                                       plan.data if plan is not None else None))
     if plan is None:
-        plan = ChunkPlan(B, T, G, geometry, _empty_on(s, (need // 4,), i32, dev))
+        plan = ChunkPlan(B, T, G, geometry, _new(s, (need // 4,), (1,), torch.int32, dev))
     plan.geometry = geometry
-    _launch(dev, "spec_chunk_plan", (_lib or library()).spec_chunk_plan, r, n, table, B, T, G,
-            *geometry, plan.data.data_ptr(), need, h)
+    _launch(dev, "spec_chunk_plan", (_lib or library()).spec_chunk_plan, row_start.data_ptr(),
+            kv_len.data_ptr(), _ptr_of(page_table), B, T, G, *geometry, plan.data.data_ptr(), need,
+            h)
     return plan
 
 
@@ -1614,43 +1681,56 @@ def spec_chunk_attention(q, k_cache, v_cache, plan, page_table=None, scale=None,
     [rows, Hq]; rows of no sequence are left as they are.  Asynchronous like
     any CUDA op."""
     torch = _torch()
-    if q.dim() != 3 or not k_cache.dim() == v_cache.dim() == 4:
-        raise ValueError("q must be [rows, Hq, D], k_cache and v_cache [pages, slots, Hkv, D]")
-    T, Hq, D = q.shape
-    Hkv, dtype, dev = k_cache.shape[2], q.dtype, q.device
-    if dtype != torch.bfloat16 and dtype != torch.float16:
-        raise TypeError(f"q must be bfloat16 or float16, got {dtype}")
-    S = _caches(k_cache, v_cache, (), Hkv, D, dtype)[1]
-    geometry, table = _geometry(k_cache, page_table, plan.B, dev)
-    if ((plan.rows, plan.group * Hkv, plan.geometry) != (T, Hq, geometry)
-            or plan.data.device != dev):
-        raise ValueError(f"plan is for rows={plan.rows} Hq/Hkv={plan.group}, cache {plan.geometry} "
-                         f"on {plan.data.device}; the call is for rows={T} Hq={Hq} Hkv={Hkv}, "
-                         f"{geometry} on {dev}")
-    q_at, q_st = _strided("q", q, dev, 8)
-    kc_at, kc_st = _strided("k_cache", k_cache, dev, 8)
-    vc_at, vc_st = _strided("v_cache", v_cache, dev, 8)
-    scale = D ** -0.5 if scale is None else float(scale)
+
+    def check():
+        if q.dim() != 3 or not k_cache.dim() == v_cache.dim() == 4:
+            raise ValueError("q must be [rows, Hq, D], k_cache and v_cache "
+                             "[pages, slots, Hkv, D]")
+        T, Hq, D = q.shape
+        Hkv, dtype, dev = k_cache.shape[2], q.dtype, q.device
+        if dtype != torch.bfloat16 and dtype != torch.float16:
+            raise TypeError(f"q must be bfloat16 or float16, got {dtype}")
+        _caches(k_cache, v_cache, (), Hkv, D, dtype)
+        geometry, _ = _geometry(k_cache, page_table, plan.B, dev)
+        if ((plan.rows, plan.group * Hkv, plan.geometry) != (T, Hq, geometry)
+                or plan.data.device != dev):
+            raise ValueError(f"plan is for rows={plan.rows} Hq/Hkv={plan.group}, cache "
+                             f"{plan.geometry} on {plan.data.device}; the call is for rows={T} "
+                             f"Hq={Hq} Hkv={Hkv}, {geometry} on {dev}")
+        strides = []
+        for name, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache)):
+            strides += _strided(name, t, dev, 8)[1]
+        S = geometry[0]
+        if page_table is not None and S % 128 and (S < 8 or S & (S - 1)):
+            raise ValueError(f"page size {S}: a multiple of 128, or a power of two from 8")
+        need = spec_chunk_attention_workspace_size(Hq, Hkv, D)
+        if need == 0:
+            raise ValueError(f"sizes out of range: Hq={Hq} Hkv={Hkv} D={D}")
+        if out is not None:
+            _dev_out("out", out, (T, Hq, D), dtype, dev)
+        return (dev, (T, Hq, D), (Hq * D, D, 1), dtype, need, struct.pack("@8q", *strides),
+                struct.pack("@9i", plan.B, T, Hq, Hkv, D, *geometry,
+                            SPEC_BF16 if dtype == torch.bfloat16 else SPEC_F16))
+    dev, shape, out_st, dtype, need, strides, sizes = _checked_chunk(
+        (_meta(q), _meta(k_cache), _meta(v_cache), _meta(page_table), _meta(out), plan.B,
+         plan.rows, plan.group, plan.geometry, plan.data.device), check)
+    scale = shape[2] ** -0.5 if scale is None else float(scale)
     if not 0.0 < scale < float("inf"):
         raise ValueError(f"scale must be finite and positive, got {scale}")
-    if table and S % 128 and (S < 8 or S & (S - 1)):
-        raise ValueError(f"page size {S}: a multiple of 128, or a power of two from 8")
-    need = spec_chunk_attention_workspace_size(Hq, Hkv, D)
-    if need == 0:
-        raise ValueError(f"sizes out of range: Hq={Hq} Hkv={Hkv} D={D}")
+    at = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
+    if (at[0] | at[1] | at[2]) & 15:
+        raise ValueError("q, k_cache and v_cache must be 16-byte aligned")
     h, s = _call_stream(stream, dev, (q, k_cache, v_cache, plan.data, page_table, out, ws))
     if out is None:
-        out = _empty_on(s, (T, Hq, D), dtype, dev)
-    else:
-        _dev_out("out", out, (T, Hq, D), dtype, dev)
-    lse = _empty_on(s, (T, Hq), torch.float32, dev) if want_lse else None
+        out = _new(s, shape, out_st, dtype, dev)
+    lse = _empty_on(s, shape[:2], torch.float32, dev) if want_lse else None
     if ws is None:
         ws = _scratch(_chunk_ws, need, dev, h, s)
     else:
         _check_ws(ws, dev)
-    args = _pack_chunk(q_at, kc_at, vc_at, *q_st, *kc_st, *vc_st, table, plan.data.data_ptr(),
-                       out.data_ptr(), lse.data_ptr() if want_lse else 0, scale, plan.B, T, Hq, Hkv,
-                       D, *geometry, SPEC_BF16 if dtype == torch.bfloat16 else SPEC_F16)
+    args = b"".join((_pack_3q(*at), strides,
+                     _pack_chunk(_ptr_of(page_table), plan.data.data_ptr(), out.data_ptr(),
+                                 _ptr_of(lse), scale), sizes))
     _launch(dev, "spec_chunk_attention", (_lib or library()).spec_chunk_attention, args,
             ws.data_ptr(), ws.numel(), h)
     return (out, lse) if want_lse else out
@@ -1675,30 +1755,38 @@ def spec_beam_select(logits, scores, n, finished=None, norm=None, end_token=0, w
     [B, n] and scores float32 [B, n], best first (-1, -1 and -inf where there
     are fewer); asynchronous like any CUDA op."""
     torch = _torch()
-    if logits.dim() != 3:
-        raise ValueError("logits must be [B, K, V]")
-    B, K, V = logits.shape
-    dt = _dtype_code(logits)
-    dev, i32, f32 = logits.device, torch.int32, torch.float32
-    if not logits.is_cuda or not logits.is_contiguous():
-        raise ValueError("logits must be a contiguous CUDA tensor")
-    need = spec_beam_workspace_size(B, K, V, n, dt)
-    if need == 0:
-        raise ValueError(f"sizes out of range: B={B} K={K} V={V} n={n}")
-    if not 0 <= end_token < V:
-        raise ValueError(f"end_token must be in [0, {V}), got {end_token}")
-    sc = _array("scores", scores, (B, K), f32, dev)
-    fin = _array("finished", finished, (B, K), i32, dev) if finished is not None else 0
-    no = _array("norm", norm, (B, K), f32, dev) if norm is not None else 0
+
+    def check():
+        if logits.dim() != 3:
+            raise ValueError("logits must be [B, K, V]")
+        B, K, V = logits.shape
+        dt = _dtype_code(logits)
+        dev, f32 = logits.device, torch.float32
+        if not logits.is_cuda or not logits.is_contiguous():
+            raise ValueError("logits must be a contiguous CUDA tensor")
+        need = spec_beam_workspace_size(B, K, V, n, dt)
+        if need == 0:
+            raise ValueError(f"sizes out of range: B={B} K={K} V={V} n={n}")
+        if not 0 <= end_token < V:
+            raise ValueError(f"end_token must be in [0, {V}), got {end_token}")
+        _array("scores", scores, (B, K), f32, dev)
+        if finished is not None:
+            _array("finished", finished, (B, K), torch.int32, dev)
+        if norm is not None:
+            _array("norm", norm, (B, K), f32, dev)
+        return dev, (B, n), need, struct.pack("@6i", B, K, V, n, end_token, dt)
+    dev, shape, need, sizes = _checked_beam(
+        (_meta(logits), _meta(scores), _meta(finished), _meta(norm), n, end_token), check)
     h, s = _call_stream(stream, dev, (logits, scores, finished, norm, ws))
-    tokens, beams = _empty_on(s, (B, n), i32, dev), _empty_on(s, (B, n), i32, dev)
-    best = _empty_on(s, (B, n), f32, dev)
+    st = (n, 1)
+    tokens, beams = _new(s, shape, st, torch.int32, dev), _new(s, shape, st, torch.int32, dev)
+    best = _new(s, shape, st, torch.float32, dev)
     if ws is None:
         ws = _scratch(_beam_ws, need, dev, h, s, zeroed=True)
     else:
         _check_ws(ws, dev)
-    args = _pack_beam(logits.data_ptr(), sc, no, fin, tokens.data_ptr(), beams.data_ptr(),
-                      best.data_ptr(), B, K, V, n, end_token, dt)
+    args = _pack_beam(logits.data_ptr(), scores.data_ptr(), _ptr_of(norm), _ptr_of(finished),
+                      tokens.data_ptr(), beams.data_ptr(), best.data_ptr()) + sizes
     _launch(dev, "spec_beam_select", (_lib or library()).spec_beam_select, args, ws.data_ptr(),
             ws.numel(), h)
     return tokens, beams, best
@@ -1711,22 +1799,27 @@ def spec_beam_reorder(state, beams, dim=0, out=None, stream=None):
     int32 [B, n] from spec_beam_select.  Returns [.., B, n, ..], where the place
     of a beam -1 is 0; asynchronous like any CUDA op."""
     torch = _torch()
-    if not 0 <= dim <= state.dim() - 2 or beams.dim() != 2:
-        raise ValueError("state must be [.., B, K, ..] with B at `dim`, and beams [B, n]")
-    B, K = state.shape[dim:dim + 2]
-    n, dev = beams.shape[1], state.device
-    if not state.is_cuda or not state.is_contiguous():
-        raise ValueError("state must be a contiguous CUDA tensor")
-    at = _array("beams", beams, (B, n), torch.int32, dev)
-    shape = (*state.shape[:dim], B, n, *state.shape[dim + 2:])
+
+    def check():
+        if not 0 <= dim <= state.dim() - 2 or beams.dim() != 2:
+            raise ValueError("state must be [.., B, K, ..] with B at `dim`, and beams [B, n]")
+        B, K = state.shape[dim:dim + 2]
+        n, dev = beams.shape[1], state.device
+        if not state.is_cuda or not state.is_contiguous():
+            raise ValueError("state must be a contiguous CUDA tensor")
+        _array("beams", beams, (B, n), torch.int32, dev)
+        shape = (*state.shape[:dim], B, n, *state.shape[dim + 2:])
+        if out is not None:
+            _dev_out("out", out, shape, state.dtype, dev)
+        return (dev, shape, _strides_of(shape), state.dtype,
+                (math.prod(state.shape[:dim]), B, K, n,
+                 math.prod(state.shape[dim + 2:]) * state.element_size()))
+    dev, shape, st, dtype, sizes = _checked_reorder((_meta(state), _meta(beams), _meta(out), dim), check)
     h, s = _call_stream(stream, dev, (state, beams, out))
     if out is None:
-        out = _empty_on(s, shape, state.dtype, dev)
-    else:
-        _dev_out("out", out, shape, state.dtype, dev)
-    _launch(dev, "spec_beam_reorder", (_lib or library()).spec_beam_reorder, state.data_ptr(), at,
-            out.data_ptr(), math.prod(state.shape[:dim]), B, K, n,
-            math.prod(state.shape[dim + 2:]) * state.element_size(), h)
+        out = _new(s, shape, st, dtype, dev)
+    _launch(dev, "spec_beam_reorder", (_lib or library()).spec_beam_reorder, state.data_ptr(),
+            beams.data_ptr(), out.data_ptr(), *sizes, h)
     return out
 
 
@@ -1737,26 +1830,34 @@ def spec_pages_workspace_size(rows_out: int, num_pages: int) -> int:
     return int(library().spec_pages_workspace_size(rows_out, num_pages))
 
 
-def _pages_workspace(ws, rows, pages, dev, h, s):
+def _pages_workspace_size(rows, pages):
     need = spec_pages_workspace_size(rows, pages)
     if need == 0:
         raise ValueError(f"sizes out of range: rows={rows} pages={pages}")
-    if ws is None:
-        return _scratch(_pages_ws, need, dev, h, s)
-    _check_ws(ws, dev)
-    return ws
+    return need
 
 
-def _outs(given, shapes, dev, s):
-    """The int32 outputs of a call: the caller's, or new ones."""
-    i32 = _torch().int32
+def _check_outs(given, shapes, dev):
+    """The caller's int32 outputs of a call."""
     if given is None:
-        return [_empty_on(s, shape, i32, dev) for shape in shapes]
+        return
     if len(given) != len(shapes):
         raise ValueError(f"out must be {len(shapes)} tensors")
     for i, (t, shape) in enumerate(zip(given, shapes)):
-        _dev_out(f"out[{i}]", t, shape, i32, dev)
-    return list(given)
+        _dev_out(f"out[{i}]", t, shape, _torch().int32, dev)
+
+
+def _pages_call(name, pointers, sizes, shapes, need, out, ws, dev, h, s):
+    """The outputs and the workspace where the caller gave none, and the launch."""
+    i32 = _torch().int32
+    out = tuple(out) if out is not None else tuple([_new(s, *x, i32, dev) for x in shapes])
+    if ws is None:
+        ws = _scratch(_pages_ws, need, dev, h, s)
+    else:
+        _check_ws(ws, dev)
+    args = b"".join((pointers, _pack_4q(*[t.data_ptr() for t in out]), sizes))
+    _launch(dev, name, getattr(_lib or library(), name), args, ws.data_ptr(), ws.numel(), h)
+    return out
 
 
 def spec_pages_fork(table, length, parent, ref_count, page_size, reserve=None, out=None, ws=None,
@@ -1770,24 +1871,30 @@ def spec_pages_fork(table, length, parent, ref_count, page_size, reserve=None, o
     lengths, reference counts and copies int32 [3, rows_out] for spec_pages_copy
     (before the next call that takes pages).  `out`: those four, none of them an
     input.  Asynchronous like any CUDA op."""
-    torch = _torch()
-    if table.dim() != 2 or parent.dim() != 1 or ref_count.dim() != 1:
-        raise ValueError("table must be [rows, pages_per_seq], parent [rows_out], ref_count [pages]")
-    (R0, M), R, P = table.shape, parent.shape[0], ref_count.shape[0]
-    dev, i32 = table.device, torch.int32
-    t = _array("table", table, (R0, M), i32, dev)
-    n = _array("length", length, (R0,), i32, dev)
-    p = _array("parent", parent, (R,), i32, dev)
-    rc = _array("ref_count", ref_count, (P,), i32, dev)
-    rs = _array("reserve", reserve, (R,), i32, dev) if reserve is not None else 0
+    def check():
+        if table.dim() != 2 or parent.dim() != 1 or ref_count.dim() != 1:
+            raise ValueError("table must be [rows, pages_per_seq], parent [rows_out], "
+                             "ref_count [pages]")
+        (R0, M), R, P = table.shape, parent.shape[0], ref_count.shape[0]
+        dev, i32 = table.device, _torch().int32
+        _array("table", table, (R0, M), i32, dev)
+        _array("length", length, (R0,), i32, dev)
+        _array("parent", parent, (R,), i32, dev)
+        _array("ref_count", ref_count, (P,), i32, dev)
+        if reserve is not None:
+            _array("reserve", reserve, (R,), i32, dev)
+        shapes = ((R, M), (R,), (P,), (3, R))
+        _check_outs(out, shapes, dev)
+        return (dev, tuple((x, _strides_of(x)) for x in shapes), _pages_workspace_size(R, P),
+                struct.pack("@5i4x", R0, R, M, page_size, P))
+    dev, shapes, need, sizes = _checked_fork(
+        (_meta(table), _meta(length), _meta(parent), _meta(ref_count), _meta(reserve), page_size,
+         None if out is None else tuple([_meta(t) for t in out])), check)
     h, s = _call_stream(stream, dev, (table, length, parent, ref_count, reserve, ws,
                                       *(out if out is not None else ())))
-    out = _outs(out, ((R, M), (R,), (P,), (3, R)), dev, s)
-    ws = _pages_workspace(ws, R, P, dev, h, s)
-    args = _pack_fork(t, n, p, rs, rc, *(o.data_ptr() for o in out), R0, R, M, page_size, P)
-    _launch(dev, "spec_pages_fork", (_lib or library()).spec_pages_fork, args, ws.data_ptr(),
-            ws.numel(), h)
-    return tuple(out)
+    pointers = _pack_5q(table.data_ptr(), length.data_ptr(), parent.data_ptr(), _ptr_of(reserve),
+                        ref_count.data_ptr())
+    return _pages_call("spec_pages_fork", pointers, sizes, shapes, need, out, ws, dev, h, s)
 
 
 def spec_pages_compact(table, ref_count, page_size, out=None, ws=None, stream=None):
@@ -1798,20 +1905,23 @@ def spec_pages_compact(table, ref_count, page_size, out=None, ws=None, stream=No
     [3, num_pages // 2] for spec_pages_copy and the number of pages in use
     int32 [1].  `out`: those four, none of them an input.  Asynchronous like any
     CUDA op."""
-    torch = _torch()
-    if table.dim() != 2 or ref_count.dim() != 1:
-        raise ValueError("table must be [rows, pages_per_seq], ref_count [pages]")
-    (R, M), P = table.shape, ref_count.shape[0]
-    dev, i32 = table.device, torch.int32
-    t = _array("table", table, (R, M), i32, dev)
-    rc = _array("ref_count", ref_count, (P,), i32, dev)
+    def check():
+        if table.dim() != 2 or ref_count.dim() != 1:
+            raise ValueError("table must be [rows, pages_per_seq], ref_count [pages]")
+        (R, M), P = table.shape, ref_count.shape[0]
+        dev, i32 = table.device, _torch().int32
+        _array("table", table, (R, M), i32, dev)
+        _array("ref_count", ref_count, (P,), i32, dev)
+        shapes = ((R, M), (P,), (3, P // 2), (1,))
+        _check_outs(out, shapes, dev)
+        return (dev, tuple((x, _strides_of(x)) for x in shapes), _pages_workspace_size(R, P),
+                struct.pack("@4i", R, M, page_size, P))
+    dev, shapes, need, sizes = _checked_compact(
+        (_meta(table), _meta(ref_count), page_size,
+         None if out is None else tuple([_meta(t) for t in out])), check)
     h, s = _call_stream(stream, dev, (table, ref_count, ws, *(out if out is not None else ())))
-    out = _outs(out, ((R, M), (P,), (3, P // 2), (1,)), dev, s)
-    ws = _pages_workspace(ws, R, P, dev, h, s)
-    args = _pack_compact(t, rc, *(o.data_ptr() for o in out), R, M, page_size, P)
-    _launch(dev, "spec_pages_compact", (_lib or library()).spec_pages_compact, args,
-            ws.data_ptr(), ws.numel(), h)
-    return tuple(out)
+    pointers = struct.pack("@2Q", table.data_ptr(), ref_count.data_ptr())
+    return _pages_call("spec_pages_compact", pointers, sizes, shapes, need, out, ws, dev, h, s)
 
 
 def spec_pages_copy(k_cache, v_cache, copies, stream=None):
@@ -1821,21 +1931,25 @@ def spec_pages_copy(k_cache, v_cache, copies, stream=None):
     layers, 2 or 4 bytes an element, any strides with a contiguous last
     dimension; copies int32 [3, n]: sources, destinations and numbers of slots
     (-1, -1, 0: nothing).  Asynchronous like any CUDA op."""
-    torch = _torch()
-    if k_cache.dim() not in (4, 5) or v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must be [.., pages, slots, Hkv, D]")
-    if v_cache.dtype != k_cache.dtype or k_cache.element_size() not in (2, 4):
-        raise TypeError("k_cache and v_cache must share a dtype of 2 or 4 bytes")
-    if copies.dim() != 2 or copies.shape[0] != 3:
-        raise ValueError("copies must be [3, n]")
-    *lead, P, S, Hkv, D = k_cache.shape
-    dev, n = k_cache.device, copies.shape[1]
-    c = _array("copies", copies, (3, n), torch.int32, dev)
-    k_at, k_st = _strided("k_cache", k_cache, dev, 1)
-    v_at, v_st = _strided("v_cache", v_cache, dev, 1)
-    if not lead:
-        k_st, v_st = (0, *k_st), (0, *v_st)
+    def check():
+        if k_cache.dim() not in (4, 5) or v_cache.shape != k_cache.shape:
+            raise ValueError("k_cache and v_cache must be [.., pages, slots, Hkv, D]")
+        if v_cache.dtype != k_cache.dtype or k_cache.element_size() not in (2, 4):
+            raise TypeError("k_cache and v_cache must share a dtype of 2 or 4 bytes")
+        if copies.dim() != 2 or copies.shape[0] != 3:
+            raise ValueError("copies must be [3, n]")
+        *lead, P, S, Hkv, D = k_cache.shape
+        dev, n = k_cache.device, copies.shape[1]
+        _array("copies", copies, (3, n), _torch().int32, dev)
+        strides = []
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+            st = _strided(name, t, dev, 1)[1]
+            strides += st if lead else (0, *st)
+        return (dev, struct.pack("@8q", *strides),
+                struct.pack("@7i4x", n, lead[0] if lead else 1, Hkv, D, S, P,
+                            k_cache.element_size()))
+    dev, strides, sizes = _checked_copy((_meta(k_cache), _meta(v_cache), _meta(copies)), check)
     h, _ = _call_stream(stream, dev, (k_cache, v_cache, copies))
-    args = _pack_copy(k_at, v_at, *k_st, *v_st, c, n, lead[0] if lead else 1, Hkv, D, S, P,
-                      k_cache.element_size())
+    args = b"".join((struct.pack("@2Q", k_cache.data_ptr(), v_cache.data_ptr()), strides,
+                     struct.pack("@Q", copies.data_ptr()), sizes))
     _launch(dev, "spec_pages_copy", (_lib or library()).spec_pages_copy, args, h)

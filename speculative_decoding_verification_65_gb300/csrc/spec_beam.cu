@@ -17,7 +17,7 @@
 // and the second kernel takes the sums of its beams again in exact integers (units of 2^-51 of the row's
 // largest weight, resolve.cuh) and merges once more, so the order is that of 64 bits.
 //
-// Reorder: a gather of rows, 8 KB of a row per warp, in the widest vectors that the
+// Reorder: a gather of rows, 128 vectors of a row per warp, in the widest vectors that the
 // addresses allow.  Bound by bytes.
 #include <cuda_runtime.h>
 #include <limits.h>
@@ -45,7 +45,7 @@ constexpr int GROUPS = 32;         // most groups of a thread, in a segment
 static_assert(GROUPS <= 32, "a thread's groups are bits of a word");
 constexpr int CAP = 1024;          // candidates of a segment before they are cut
 constexpr int MAX_LISTS = 2048;    // segments of a sequence's beams: 1216 / K + 1, or 19 for the longest rows
-constexpr int EXACT_CTAS = 304;
+constexpr int EXACT_CTAS = 152;
 constexpr size_t MAX_B = 65536;    // sequences that the counters have room for
 // How far a row's logarithm of its total may be off, in nats: exponents' rounding (2^-23 of up to
 // 24 binary digits, and the constant's 2^-25: 2.5e-6), ex2 three times (2^-22 each: 0.7e-6), some 26
@@ -731,7 +731,7 @@ struct ReorderParams {
     int parts;           // pieces of a row, PIECE vectors each
 };
 
-constexpr int PIECE = 512;
+constexpr int PIECE = 128;
 
 template <typename V>
 __global__ void __launch_bounds__(TH) reorder_kernel(const __grid_constant__ ReorderParams P)

@@ -92,7 +92,7 @@ struct Piece {
 
 struct Tail {
     unsigned long long kfull[4], kempty[4], vfull[4], vempty[4];
-    unsigned long long qfull, qempty, sfull[2], pvdone[2], vclean[2], drain;
+    unsigned long long qfull, qempty, sfull[2], halfdone[2], pvdone[2], vclean[2], drain;
     unsigned long long pfull[RING], pempty[RING];
     Piece piece[RING];
     uint32_t tmem_base;
@@ -284,9 +284,9 @@ __device__ __forceinline__ int tile_keys(const Piece &p, int jt)
     return left < KT ? left : KT;
 }
 
-// Named barriers: a softmax group among itself; its weights, for the issuer; the tiles of a step, for
-// the issuer, one for each stage of V; a piece's first tiles.
-enum { GROUP = 1, WEIGHTS = 3, TILES = 5, FIRST = 9 };
+// Named barriers: a softmax group among itself; its weights of a tile's first and second half, for the
+// issuer; the tiles of a step, for the issuer, one for each stage of V; a piece's first tiles.
+enum { GROUP = 1, WEIGHTS = 3, TILES = 7, FIRST = 11 };
 
 __device__ __forceinline__ void named_sync(int id, int threads)
 {
@@ -333,6 +333,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(&S.qempty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.sfull[i], 1);
+            mbar_init(&S.halfdone[i], 1);
             mbar_init(&S.pvdone[i], 1);
             mbar_init(&S.vclean[i], 8);
         }
@@ -551,7 +552,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc_fence_after();
                 if (masked && i > plain)
                     add_back(jt - 1, hid - 1);
-                unsigned long long sum[2] = {0ull, 0ull};
                 if (warp_live) {
                     if (masked) {
 #pragma unroll 1
@@ -575,66 +575,67 @@ __global__ void __launch_bounds__(THREADS, 1)
                             m = fmaxf(m, max32(x));
                         }
                     }
-                    // in one pass: weights by the maximum so far, which serves as long as no
-                    // score is far above it; the tile's own maximum is found on the way
-                    float shift = shift_of(m);
-                    unsigned long long shift2 = f2(shift, shift);
-                    uint32_t x[32], y[32], pk[4][16];
-                    __syncwarp();
-                    tmem_ld_start(t_s, x);
-                    tmem_ld_finish(x);
-                    tmem_ld_start(t_s + 32, y);
-                    float top = max32(x);
-                    weigh<DT>(x, c2, shift2, sum, pk[0]);
-                    tmem_ld_finish(y);
-                    tmem_ld_start(t_s + 64, x);
-                    top = fmaxf(top, max32(y));
-                    weigh<DT>(y, c2, shift2, sum, pk[1]);
-                    tmem_ld_finish(x);
-                    tmem_ld_start(t_s + 96, y);
-                    top = fmaxf(top, max32(x));
-                    weigh<DT>(x, c2, shift2, sum, pk[2]);
-                    tmem_ld_finish(y);
-                    top = fmaxf(top, max32(y));
-                    weigh<DT>(y, c2, shift2, sum, pk[3]);
-                    const bool grown = (top - m) * P.c > growth<DT>();  // -inf to finite too
-                    if (!__any_sync(0xffffffffu, grown)) {
-                        // weights 32 h on lie in columns 16 h on
-#pragma unroll
-                        for (int h = 0; h < 4; ++h)
-                            tmem_st(t_s + h * 16, pk[h]);
-                    } else {
-                        // again, by the new maximum, which O and l follow
-                        const float f = grown ? ex2((m - top) * P.c) : 1.0f;
-                        l *= f;
-                        if (grown)
-                            m = top;
-#pragma unroll 1
-                        for (int d = 0; d < C::DP; d += 16) {
-                            uint32_t o[16];
-                            tmem_ld(t_o + d, o);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                            tmem_st(t_o + d, o);
-                        }
-                        sum[0] = sum[1] = 0ull;
-                        shift = shift_of(m);
-                        shift2 = f2(shift, shift);
-#pragma unroll 1
-                        for (int h = 0; h < 4; ++h) {
-                            tmem_ld(t_s + h * 32, x);
-                            weigh<DT>(x, c2, shift2, sum, pk[0]);
-                            tmem_st(t_s + h * 16, pk[0]);
-                        }
-                    }
-                    float s0, s1;
-                    f2_split(add2(sum[0], sum[1]), s0, s1);
-                    l += s0 + s1;
-                    tmem_wait_st();
                 }
-                tc_fence_before();
-                named_arrive(WEIGHTS + s, 160);
+                // The tile in two halves, whose products begin one after the other: the first one's
+                // runs while the second one's weights are made.  Each in one pass: weights by
+                // the maximum so far, which serves as long as no score is far above it; the
+                // half's own maximum is found on the way.  Weights 32 h on lie in columns 16 h on,
+                // over scores that have been read.
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    if (warp_live) {
+                        float shift = shift_of(m);
+                        unsigned long long shift2 = f2(shift, shift);
+                        unsigned long long sum[2] = {0ull, 0ull};
+                        uint32_t x[32], y[32], pk[2][16];
+                        __syncwarp();
+                        tmem_ld_start(t_s + part * 64, x);
+                        tmem_ld_finish(x);
+                        tmem_ld_start(t_s + part * 64 + 32, y);
+                        float top = max32(x);
+                        weigh<DT>(x, c2, shift2, sum, pk[0]);
+                        tmem_ld_finish(y);
+                        top = fmaxf(top, max32(y));
+                        weigh<DT>(y, c2, shift2, sum, pk[1]);
+                        const bool grown = (top - m) * P.c > growth<DT>();  // -inf to finite too
+                        if (__any_sync(0xffffffffu, grown)) {
+                            // again, by the new maximum, which O and l follow (O when it has the
+                            // first half; a wait that gives up ends the group's next one)
+                            if (part) {
+                                (void)wait(&S.halfdone[s], cnt & 1u);
+                                tc_fence_after();
+                            }
+                            const float f = grown ? ex2((m - top) * P.c) : 1.0f;
+                            l *= f;
+                            if (grown)
+                                m = top;
+#pragma unroll 1
+                            for (int d = 0; d < C::DP; d += 16) {
+                                uint32_t o[16];
+                                tmem_ld(t_o + d, o);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                tmem_st(t_o + d, o);
+                            }
+                            sum[0] = sum[1] = 0ull;
+                            shift = shift_of(m);
+                            shift2 = f2(shift, shift);
+                            tmem_ld(t_s + part * 64, x);
+                            weigh<DT>(x, c2, shift2, sum, pk[0]);
+                            tmem_ld(t_s + part * 64 + 32, x);
+                            weigh<DT>(x, c2, shift2, sum, pk[1]);
+                        }
+                        tmem_st(t_s + part * 32, pk[0]);
+                        tmem_st(t_s + part * 32 + 16, pk[1]);
+                        float s0, s1;
+                        f2_split(add2(sum[0], sum[1]), s0, s1);
+                        l += s0 + s1;
+                        tmem_wait_st();
+                    }
+                    tc_fence_before();
+                    named_arrive(WEIGHTS + 2 * part + s, 160);
+                }
                 ++cnt;
                 vph ^= vst + 1 == C::VST ? 1u : 0u;
                 vst = vst + 1 == C::VST ? 0 : vst + 1;
@@ -823,23 +824,42 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const bool end = i + 1 == n;
                     if (G == 0)  // (the second group finds the first one's tiles)
                         named_sync(TILES + vst, 64);
+                    // 16 keys a product: 8 columns of P, 2 KB of V
+                    auto products = [&](int from, int to) {
+#pragma unroll 1
+                        for (int x = from; x < to; ++x)
+                            mma_ts(t_o, t_s + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)),
+                                   id_o, x ? 1u : more);
+                    };
+                    const bool full = !end || tail == KT;
+                    const int some = (tail + 15) / 16;
                     named_sync(WEIGHTS + G, 160);
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (full) {
+#pragma unroll
+                            for (int x = 0; x < KT / 32; ++x)
+                                mma_ts(t_o, t_s + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)),
+                                       id_o, x ? 1u : more);
+                        } else {
+                            products(0, some < KT / 32 ? some : KT / 32);
+                        }
+                        mma_commit(&S.halfdone[G]);
+                    }
+                    __syncwarp();
+                    named_sync(WEIGHTS + 2 + G, 160);
                     ok = !given_up();
                     if (!ok)
                         return;
                     tc_fence_after();
                     if (elect_one()) {
-                        // 16 keys a step: 8 columns of P, 2 KB of V
-                        if (!end || tail == KT) {
+                        if (full) {
 #pragma unroll
-                            for (int x = 0; x < KT / 16; ++x)
+                            for (int x = KT / 32; x < KT / 16; ++x)
                                 mma_ts(t_o, t_s + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)),
-                                       id_o, x ? 1u : more);
+                                       id_o, 1u);
                         } else {
-#pragma unroll 1
-                            for (int x = 0; x < (tail + 15) / 16; ++x)
-                                mma_ts(t_o, t_s + (uint32_t)(x * 8), vd + (uint64_t)(x * (2048 >> 4)),
-                                       id_o, x ? 1u : more);
+                            products(KT / 32, some);
                         }
                         if (G)
                             mma_commit(&S.vempty[vst]);

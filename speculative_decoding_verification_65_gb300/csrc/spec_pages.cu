@@ -8,7 +8,7 @@
 // second sums those of the rows before.  Both are bound by the chain of their loads, not by bytes.
 // Counts change by atomic additions of whole numbers, whose order does not matter.
 //
-// The copy moves whole rows of slots, 8 KB per warp at a time, in the widest vectors that the
+// The copy moves whole rows of slots, 256 vectors per warp at a time, in the widest vectors that the
 // addresses allow.  A warp looks at 32 entries of the list at once and works on those that copy
 // something.  Bound by bytes.
 #include <cuda_runtime.h>
@@ -470,7 +470,7 @@ struct CopyParams {
     int parts;         // pieces of a page, PIECE vectors each
 };
 
-constexpr int PIECE = 512;
+constexpr int PIECE = 256;
 
 // FLAT: a page's slots and heads lie one after the other.
 template <typename V, bool FLAT>
