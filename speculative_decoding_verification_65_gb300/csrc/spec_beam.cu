@@ -44,7 +44,7 @@ constexpr int UN = 4;              // vectors of a group
 constexpr int GROUPS = 32;         // most groups of a thread, in a segment
 static_assert(GROUPS <= 32, "a thread's groups are bits of a word");
 constexpr int CAP = 1024;          // candidates of a segment before they are cut
-constexpr int MAX_LISTS = 2048;    // segments of a sequence's beams: 1216 / K + 1, or 19 for the longest rows
+constexpr int MAX_LISTS = 2048;    // segments of a sequence's beams: 608, or 9 of each of 64 long rows
 constexpr int EXACT_CTAS = 152;
 constexpr size_t MAX_B = 65536;    // sequences that the counters have room for
 // How far a row's logarithm of its total may be off, in nats: exponents' rounding (2^-23 of up to
@@ -106,11 +106,12 @@ struct ScanSmem {
 struct PickSmem {
     double lse[SPEC_BEAM_MAX], score[SPEC_BEAM_MAX], inv[SPEC_BEAM_MAX];
     float2 total[SPEC_BEAM_MAX];  // a row's largest logit and sum of exp(x - largest)
-    u64 rank[SPEC_BEAM_MAX + 1];  // the best n and the next, sorted
-    int flat[SPEC_BEAM_MAX + 1];
-    float value[SPEC_BEAM_MAX + 1];  // logits
+    u64 rank[SPEC_BEAM_MAX];      // the best n, sorted
+    int flat[SPEC_BEAM_MAX];
+    float value[SPEC_BEAM_MAX];   // logits
     u64 least;
     int least_flat;
+    int widest;                   // the largest 1 / norm, as a float's bits
     int count;
 };
 
@@ -174,6 +175,8 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
     const spec_beam_select_args &A = P.a;
     const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
     bool bad = false;
+    if (tid == 0)
+        S.widest = 0;
     // the rows' totals, a row per warp; what takes 64 bits for all rows at once, a row per lane (this
     // GPU has two 64-bit lanes per SM: by the warps one after the other it took 10 us)
     if (!EXACT)
@@ -214,10 +217,15 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
         if (s > -INFINITY) {
             bad |= !(norm > 0.0f) || isinf(norm);
             S.score[tid] = (double)s;
-            // 1 / norm: fp32's, and a step of Newton's iteration
-            const double guess = (double)(1.0f / norm);
-            S.inv[tid] = A.norm ? guess * (2.0 - (double)norm * guess) : 1.0;
             if (!EXACT) {
+                // 1 / norm: fp32's, and a step of Newton's iteration, far from fp32's ends
+                const float to = norm < 0x1p-64f ? 0x1p64f : norm > 0x1p64f ? 0x1p-64f : 1.0f;
+                const double guess = (double)(1.0f / (norm * to));
+                S.inv[tid] =
+                    A.norm ? guess * (2.0 - (double)(norm * to) * guess) * (double)to : 1.0;
+                // (rounded up; infinity where a float has no room)
+                if (norm > 0.0f)
+                    atomicMax(&S.widest, __float_as_int(__double2float_ru(S.inv[tid])));
                 // ln z = e ln 2 + ln m, m in [2/3, 4/3)
                 const bool fin = A.finished && A.finished[row] != 0;
                 const float2 x = fin ? make_float2(0.0f, 1.0f) : S.total[tid];
@@ -242,8 +250,12 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
         }
         return true;
     }
-    // candidate `at` of list l: its order (0: none) and k V + x
     const int lists = A.K * P.segs, n = A.n;
+    auto rank_by = [&](double score, int row) -> u64 {
+        return ordered(EXACT ? score / (A.norm ? (double)A.norm[row] : 1.0)
+                             : score * S.inv[row - b * A.K]);
+    };
+    // candidate `at` of list l: its order (0: none) and k V + x
     auto load = [&](int l, int at, int &flat, float &value) -> u64 {
         const int k = l / P.segs, row = b * A.K + k;
         flat = INT_MAX;
@@ -253,14 +265,14 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
             if (at > 0 || l != k * P.segs)
                 return 0;
             flat = k * A.V + A.end_token;
-            return ordered(S.score[k] * S.inv[k]);
+            return rank_by(S.score[k], row);
         }
         const u64 key = __ldcg(&P.lists[((size_t)row * P.segs + (l - k * P.segs)) * n + at]);
         if (key == 0)
             return 0;
         flat = k * A.V + token_of(key);
         value = value_of(key);
-        return ordered((S.score[k] + ((double)value - S.lse[k])) * S.inv[k]);
+        return rank_by(S.score[k] + ((double)value - S.lse[k]), row);
     };
     // the n-th best of the lists' first entries: no more than n lists reach it, and where a few of each
     // list are looked at, not many more than n entries
@@ -275,7 +287,7 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
         S.least_flat = INT_MAX;
         S.count = 0;
     }
-    if (tid <= n)
+    if (tid < n)
         S.rank[tid] = 0;
     __syncthreads();
     for (int e = warp; e < firsts; e += WARPS) {
@@ -288,15 +300,21 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
         }
     }
     __syncthreads();
-    // the entries that reach it (n n of them at most, in the place of the heads)
+    // the entries that reach it (n n of them at most, in the place of the heads); where the order
+    // may be open, also those that might after all
     flat = reinterpret_cast<int *>(rank + n * n);
     float *value = reinterpret_cast<float *>(flat + n * n);
-    const u64 least = S.least;
     const int least_flat = S.least_flat;
+    u64 least = S.least;
+    if (!EXACT && least != 0) {
+        const double low =
+            rank_of(least) - 2.0 * LSE_OFF * (double)__int_as_float(S.widest);
+        least = low > -INFINITY ? ordered(low) : 0;
+    }
     for (int e = tid; e < lists * n; e += TH) {
         int f;
         const u64 r = load(e / n, e % n, f, x);
-        if (r != 0 && !better(least, least_flat, r, f)) {
+        if (r != 0 && (EXACT ? !better(least, least_flat, r, f) : r >= least)) {
             const int i = atomicAdd(&S.count, 1);
             if (i < n * n) {
                 rank[i] = r;
@@ -311,14 +329,24 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
         const u64 r = rank[i];
         const int f = flat[i];
         const int place = place_of(m, [&](int j) { return better(rank[j], flat[j], r, f); });
-        if (lane == 0 && place <= n) {
+        if (lane == 0 && place < n) {
             S.rank[place] = r;
             S.flat[place] = f;
             S.value[place] = value[i];
         }
     }
     __syncthreads();
-    bool open = false;
+    // two candidates of different beams lie too near: neighbours among the best, or the last of these
+    // and any that is left (no other pair's order can be open then)
+    bool open = !EXACT && S.count > n * n;
+    auto near = [&](u64 r1, int f1, u64 r2, int f2) {
+        const double off = LSE_OFF * (S.inv[f1 / A.V] + S.inv[f2 / A.V]);
+        return f1 / A.V != f2 / A.V && !(rank_of(r1) - rank_of(r2) > off);
+    };
+    if (!EXACT && S.rank[n - 1] != 0)
+        for (int i = tid; i < m; i += TH)
+            open |= better(S.rank[n - 1], S.flat[n - 1], rank[i], flat[i]) &&
+                    near(S.rank[n - 1], S.flat[n - 1], rank[i], flat[i]);
     if (tid < n) {
         int token = -1, beam = -1;
         float score = -INFINITY;
@@ -329,11 +357,8 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
             score = (float)S.score[k];
             if (!(A.finished && A.finished[b * A.K + k] != 0))
                 score = (float)(S.score[k] + ((double)S.value[tid] - S.lse[k]));
-            // the next one may lie too near
-            if (!EXACT && S.rank[tid + 1] != 0 && S.flat[tid + 1] / A.V != k) {
-                const double off = LSE_OFF * (S.inv[k] + S.inv[S.flat[tid + 1] / A.V]);
-                open = !(rank_of(S.rank[tid]) - rank_of(S.rank[tid + 1]) > off);
-            }
+            if (!EXACT && tid + 1 < n && S.rank[tid + 1] != 0)
+                open |= near(S.rank[tid], S.flat[tid], S.rank[tid + 1], S.flat[tid + 1]);
         }
         A.out_tokens[out + tid] = token;
         A.out_beams[out + tid] = beam;
@@ -780,7 +805,7 @@ bool sizes_ok(int32_t B, int32_t K, int32_t V, int32_t n, int32_t dtype)
 
 // Segments of a row: as many CTAs in all as run at a time (four per SM), each of which ends with some
 // us of choosing; no more groups than a thread has room for, and no fewer than one.  (64 x 8 rows of
-// 128256: in one segment XX us, in three YY us.)
+// 128256 bf16: in one segment 50 us, in three 68 us.)
 int segments(int32_t B, int32_t K, int32_t V, int32_t dtype)
 {
     const long long rows = (long long)B * K;

@@ -85,6 +85,37 @@ def test_orders_that_fp32_leaves_open(dtype):
     check(x, torch.full((B, K), -3.0), 12)
 
 
+@pytest.mark.parametrize("n", [1, 2, 3])
+@pytest.mark.parametrize("lengths", [False, True])
+def test_the_last_place_left_open(n, lengths):
+    """The best of one beam against the n-th of another to fp32's last bits, so that fp32 statistics
+    may put the wrong one out, and equal logits behind the n-th."""
+    B, V = 64, 6001
+    x, s = rows(8, B, 2, V, torch.float32)
+    x[:, 0] = torch.where(x[:, 0] > 8, 8.0, x[:, 0])  # many at the top of beam 0, all equal
+    norm = torch.ones(B, 2)
+    if lengths:
+        norm = 1 + torch.arange(2 * B).reshape(B, 2) % 7
+    rank = x.double().amax(2) - torch.logsumexp(x.double(), 2)
+    s[:, 0] = -5.0
+    s[:, 1] = ((s[:, 0] + rank[:, 0]) / norm[:, 0] * norm[:, 1] - rank[:, 1]).float()
+    check(x, s, n, norm=norm.float())
+
+
+def test_equal_ends_and_extreme_norms():
+    """Ended beams whose score / norm is the same number in 64 bits; norms near fp32's ends."""
+    x, s = rows(10, 5, 4, 2003, torch.float32)
+    norm = torch.tensor([3.0, 2, 7, 1]).repeat(5, 1)
+    s[:] = -norm
+    fin = torch.ones(5, 4, dtype=torch.int32)
+    norm[2], norm[3] = 1e-40, 3e38
+    s[3] = -torch.tensor([3e38, 2e38, 1e-3, 1e38])
+    norm[4, :2], s[4] = 1e-44, -1.0
+    fin[4] = 0
+    check(x, s, 3, finished=fin, norm=norm)
+    check(x, s, 9, finished=fin * 0, norm=norm)
+
+
 def test_hidden_logits_and_dead_beams():
     x, s = rows(6, 5, 3, 3001, torch.float32)
     ninf = -math.inf
