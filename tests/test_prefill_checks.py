@@ -406,6 +406,59 @@ def test_workspaces_belong_to_one_thread(monkeypatch, which):
     assert sv._scratch(cache, 1024, dev, 7, None).numel() == 1024
 
 
+def _calls(dev):
+    """A call of every entry point with tensors on `dev`."""
+    f = lambda shape, dtype: _Fake(shape, dtype, dev)  # noqa: E731
+    ws = f((1 << 20,), torch.uint8)
+    cache = f((9, 16, 2, 64), BF16)
+    table, start, length = f((2, 4), I32), f((3,), I32), f((2,), I32)
+    q, new = f((9, 8, 64), BF16), f((9, 2, 64), BF16)
+    plan = sv.ChunkPlan(2, 9, 4, (16, 4, 9), f((4096,), I32))
+    parent, ref = f((3,), I32), f((9,), I32)
+    yield lambda: sv.spec_chunk_append(new, new, cache, cache, start, length, table)
+    yield lambda: sv.spec_chunk_plan(start, length, q, cache, table, plan=plan)
+    yield lambda: sv.spec_chunk_attention(q, cache, cache, plan, table, ws=ws)
+    yield lambda: sv.spec_beam_select(f((2, 4, 100), F32), f((2, 4), F32), 4, ws=ws)
+    yield lambda: sv.spec_beam_reorder(f((2, 4, 9), I32), f((2, 4), I32))
+    yield lambda: sv.spec_pages_fork(table, length, parent, ref, 16, ws=ws)
+    yield lambda: sv.spec_pages_compact(table, ref, 16, ws=ws)
+    yield lambda: sv.spec_pages_copy(cache, cache, f((3, 5), I32))
+
+
+def test_library_calls_run_with_the_tensors_device_current(lib, monkeypatch):
+    """With cuda:0 current, a call on cuda:1 tensors enters that device around the library's call,
+    and one on cuda:0 tensors enters none."""
+    seen = []
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = str(dev)
+
+        def __enter__(self):
+            seen.append(self.dev)
+
+        def __exit__(self, *exc):
+            seen.append("out")
+
+    class Lib:
+        def __getattr__(self, name):
+            if name.endswith(("_size", "_status")):
+                return getattr(lib, name)
+            return lambda *args: seen.append(name) or sv.SPEC_OK
+    monkeypatch.setattr(sv, "_lib", Lib())
+    monkeypatch.setattr(sv, "_on", Device)
+    monkeypatch.setattr(sv, "_raw_getters", (lambda i: 7, lambda: 0))
+    monkeypatch.setattr(sv, "_empty_on", lambda s, shape, dtype, dev: _Fake(shape, dtype, dev))
+    monkeypatch.setattr(sv, "_plain_empty", lambda shape, st, dtype: _Fake(shape, dtype))
+    names = ("spec_chunk_append", "spec_chunk_plan", "spec_chunk_attention", "spec_beam_select",
+             "spec_beam_reorder", "spec_pages_fork", "spec_pages_compact", "spec_pages_copy")
+    for dev in ("cuda:1", "cuda:0"):
+        for name, call in zip(names, _calls(dev)):
+            call()
+            assert seen == (["cuda:1", name, "out"] if dev == "cuda:1" else [name])
+            seen.clear()
+
+
 def test_status_of_an_empty_batch():
     assert sv.ChunkPlan(0, 5, 4, (16, 4, 9), None).read_status() == sv.SPEC_DEV_OK
 
