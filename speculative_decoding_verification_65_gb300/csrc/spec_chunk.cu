@@ -187,8 +187,7 @@ __device__ __forceinline__ void look_up(const KParams &P, long long u, Place &q)
 // A CTA's share: `per` units for each of the slots that have any.
 __device__ __forceinline__ long long share(const KParams &P, long long all)
 {
-    const long long per = (all + P.slots - 1) / P.slots;
-    return per < 2 ? 2 : per;
+    return (all + P.slots - 1) / P.slots;
 }
 
 // The pieces of a CTA's share, one after the other (a warp's walk, all lanes alike).

@@ -30,6 +30,13 @@ constexpr int WARPS = TH / 32;
 constexpr int PB = 4096;           // pages of a block
 constexpr int MAX_BLOCKS = SPEC_PAGES_MAX / PB;
 
+// One CTA does all where it has up to SMALL_ROWS rows or SMALL_ENTRIES entries of a table, and one block
+// of pages: a launch costs the host 2.5 us.  (4 beams of 600 tokens forked, with their copies: 8.3 us of
+// the GPU's time and 24 us of the host's, by two kernels 8.7 and 27; 512 pages compacted and
+// copied: 22 and 22, by three kernels 25 and 28.)
+constexpr int SMALL_ROWS = 16;
+constexpr uint64_t SMALL_ENTRIES = 4096;
+
 struct Work {
     int *free_of;    // [blocks] free pages of a block
     int *free_list;  // [num_pages] a block's free pages in order, from block * PB on
@@ -38,13 +45,21 @@ struct Work {
     int *holes;      // [num_pages] compaction: free pages below the number in use, in order
     int *movers;     // [num_pages] pages in use from it on, in order
     int *rank;       // [num_pages] a mover's place among them
-    int *moves;      // [1] their number
+    int *moves;      // [2] their number, and that of the pages in use
 };
+
+// A word of the work that an earlier kernel wrote, or (SMALL) this CTA, whose work lies in shared
+// memory.
+template <bool SMALL>
+__device__ __forceinline__ int got(const int *p)
+{
+    return SMALL ? *p : __ldcg(p);
+}
 
 enum { ROW_ERROR = -1, ROW_EMPTY = 0, ROW_FIRST = 1, ROW_OTHER = 2 };
 
-// A block of pages: free ones (count 0, or for USED not above 0) counted and listed in order; counts
-// copied where ref_out is not null.  The whole CTA.
+// A block of pages: free ones (count 0, or for USED not above 0) counted, and for a fork listed in
+// order and the counts copied.  The whole CTA.
 template <bool USED>
 __device__ void list_free(const int32_t *ref, int32_t *ref_out, int num_pages, int block,
                           const Work &W)
@@ -61,7 +76,7 @@ __device__ void list_free(const int32_t *ref, int32_t *ref_out, int num_pages, i
         int c = 1;
         if (p < num_pages) {
             c = __ldg(ref + p);
-            if (ref_out)
+            if (!USED)
                 ref_out[p] = c;
         }
         zero[i] = __ballot_sync(0xffffffffu, USED ? c <= 0 : c == 0);
@@ -79,7 +94,7 @@ __device__ void list_free(const int32_t *ref, int32_t *ref_out, int num_pages, i
         W.free_of[block] = all;
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
-        if ((zero[i] >> lane) & 1u)
+        if (!USED && ((zero[i] >> lane) & 1u))
             W.free_list[block * PB + before + __popc(zero[i] & ((1u << lane) - 1u))] =
                 base + i * 32 + lane;
         before += __popc(zero[i]);
@@ -87,13 +102,14 @@ __device__ void list_free(const int32_t *ref, int32_t *ref_out, int num_pages, i
 }
 
 // Free pages before each block, to smem[0 .. blocks]; the whole CTA.
+template <bool SMALL>
 __device__ void sum_blocks(const int *free_of, int blocks, int *sums)
 {
     __shared__ int part[WARPS];
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int base = 0;
     for (int i0 = 0; i0 < blocks; i0 += TH) {
-        const int own = i0 + tid < blocks ? __ldcg(free_of + i0 + tid) : 0;
+        const int own = i0 + tid < blocks ? got<SMALL>(free_of + i0 + tid) : 0;
         int v = own;
         for (int d = 1; d < 32; d <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, v, d);
@@ -190,17 +206,11 @@ __device__ bool has_child(const spec_pages_fork_args &A, int o, int length, int 
     return false;
 }
 
-__global__ void __launch_bounds__(TH) fork_count_kernel(const __grid_constant__ ForkParams P)
+// What a new row is, and the pages that it takes; a warp asks.
+__device__ void count_row(const ForkParams &P, int r)
 {
     const spec_pages_fork_args &A = P.a;
     const int lane = (int)threadIdx.x & 31;
-    allow_next_kernel();
-    wait_previous_kernel();
-    if ((int)blockIdx.x < P.blocks) {
-        list_free<false>(A.ref_in, A.ref_out, A.num_pages, (int)blockIdx.x, P.w);
-        return;
-    }
-    const int r = ((int)blockIdx.x - P.blocks) * WARPS + ((int)threadIdx.x >> 5);
     if (r >= A.rows_out)
         return;
     const int parent = __ldg(A.parent + r);
@@ -239,22 +249,22 @@ __global__ void __launch_bounds__(TH) fork_count_kernel(const __grid_constant__ 
     }
 }
 
-__global__ void __launch_bounds__(TH) fork_rows_kernel(const __grid_constant__ ForkParams P)
+extern __shared__ int sums[];  // free pages before each block
+
+// New rows r0 .. r0 + 7 and old rows of these numbers, by a whole CTA.
+template <bool SMALL>
+__device__ void write_rows(const ForkParams &P, int r0)
 {
-    extern __shared__ int sums[];  // free pages before each block
     __shared__ long long part[WARPS][2];
     __shared__ int own[WARPS];      // pages that this CTA's rows take
     const spec_pages_fork_args &A = P.a;
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    allow_next_kernel();
-    wait_previous_kernel();
     // pages that the rows before this CTA's take, and all rows
-    const int r0 = (int)blockIdx.x * WARPS;
     long long before = 0, all = 0;
     if (tid < WARPS)
-        own[tid] = r0 + tid < A.rows_out ? __ldcg(P.w.need + r0 + tid) : 0;
+        own[tid] = r0 + tid < A.rows_out ? got<SMALL>(P.w.need + r0 + tid) : 0;
     for (int i = tid; i < A.rows_out; i += TH) {
-        const int n = __ldcg(P.w.need + i);
+        const int n = got<SMALL>(P.w.need + i);
         all += n;
         before += i < r0 ? n : 0;
     }
@@ -266,7 +276,7 @@ __global__ void __launch_bounds__(TH) fork_rows_kernel(const __grid_constant__ F
         part[warp][0] = before;
         part[warp][1] = all;
     }
-    sum_blocks(P.w.free_of, P.blocks, sums);  // (and all have written theirs)
+    sum_blocks<SMALL>(P.w.free_of, P.blocks, sums);  // (and all have written theirs)
     before = all = 0;
     for (int w = 0; w < WARPS; ++w) {
         before += part[w][0];
@@ -276,7 +286,7 @@ __global__ void __launch_bounds__(TH) fork_rows_kernel(const __grid_constant__ F
     const int M = A.pages_per_seq, r = r0 + warp;
     if (r < A.rows_out) {
         // -------------------------------------------------- a new row
-        const int state = enough ? __ldcg(P.w.state + r) : ROW_ERROR;
+        const int state = enough ? got<SMALL>(P.w.state + r) : ROW_ERROR;
         int32_t *row = A.table_out + (size_t)r * M;
         int src = -1, dst = -1, slots = 0, length = -1;
         if (state != ROW_ERROR) {
@@ -310,7 +320,7 @@ __global__ void __launch_bounds__(TH) fork_rows_kernel(const __grid_constant__ F
                         else
                             hi = mid;
                     }
-                    page = __ldcg(P.w.free_list + lo * PB + (j - sums[lo]));
+                    page = got<SMALL>(P.w.free_list + lo * PB + (j - sums[lo]));
                 }
                 next += __popc(takes);
                 if (i < M)
@@ -350,6 +360,51 @@ __global__ void __launch_bounds__(TH) fork_rows_kernel(const __grid_constant__ F
     }
 }
 
+__global__ void __launch_bounds__(TH) fork_count_kernel(const __grid_constant__ ForkParams P)
+{
+    allow_next_kernel();
+    wait_previous_kernel();
+    const int x = (int)blockIdx.x - P.blocks;
+    if (x < 0)
+        list_free<false>(P.a.ref_in, P.a.ref_out, P.a.num_pages, (int)blockIdx.x, P.w);
+    else
+        count_row(P, x * WARPS + ((int)threadIdx.x >> 5));
+}
+
+__global__ void __launch_bounds__(TH) fork_rows_kernel(const __grid_constant__ ForkParams P)
+{
+    allow_next_kernel();
+    wait_previous_kernel();
+    write_rows<false>(P, (int)blockIdx.x * WARPS);
+}
+
+// Both by one CTA, where that has little more to do than any CTA: one launch for two, and what the first
+// part leaves for the second in shared memory.
+__global__ void __launch_bounds__(TH) fork_small_kernel(const __grid_constant__ ForkParams given)
+{
+    __shared__ int free_of, free_list[PB], need[SMALL_ROWS], state[SMALL_ROWS];
+    __shared__ ForkParams P;
+    if (threadIdx.x == 0) {
+        P = given;
+        P.w.free_of = &free_of;
+        P.w.free_list = free_list;
+        P.w.need = need;
+        P.w.state = state;
+    }
+    allow_next_kernel();
+    wait_previous_kernel();
+    __syncthreads();
+    if (P.blocks > 0)
+        list_free<false>(P.a.ref_in, P.a.ref_out, P.a.num_pages, 0, P.w);
+    for (int r = (int)threadIdx.x >> 5; r < P.a.rows_out; r += WARPS)
+        count_row(P, r);
+    __syncthreads();
+    for (int r0 = 0; r0 < max(P.a.rows_in, P.a.rows_out); r0 += WARPS) {
+        write_rows<true>(P, r0);
+        __syncthreads();
+    }
+}
+
 // ---------------------------------------------------------------- compact
 
 struct CompactParams {
@@ -358,23 +413,15 @@ struct CompactParams {
     int blocks;
 };
 
-__global__ void __launch_bounds__(TH) compact_count_kernel(const __grid_constant__ CompactParams P)
+// A block's holes below the number in use and its pages in use from it on, with their places; the
+// whole CTA.
+template <bool SMALL>
+__device__ void list_moves(const CompactParams &P, int block)
 {
-    allow_next_kernel();
-    wait_previous_kernel();
-    list_free<true>(P.a.ref_in, nullptr, P.a.num_pages, (int)blockIdx.x, P.w);
-}
-
-// Each block's holes below the number in use and its pages in use from it on, with their places.
-__global__ void __launch_bounds__(TH) compact_list_kernel(const __grid_constant__ CompactParams P)
-{
-    extern __shared__ int sums[];
     __shared__ int part[WARPS];
     const spec_pages_compact_args &A = P.a;
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    allow_next_kernel();
-    wait_previous_kernel();
-    sum_blocks(P.w.free_of, P.blocks, sums);
+    sum_blocks<SMALL>(P.w.free_of, P.blocks, sums);
     const int used = A.num_pages - sums[P.blocks];
     // free pages below `used`: those of the whole blocks before it, and of its own up to it
     const int bu = min(used / PB, P.blocks - 1);
@@ -389,12 +436,13 @@ __global__ void __launch_bounds__(TH) compact_list_kernel(const __grid_constant_
     for (int w = 0; w < WARPS; ++w)
         holes += part[w];
     __syncthreads();
-    if (blockIdx.x == 0 && tid == 0) {
-        *P.w.moves = holes;
+    if (block == 0 && tid == 0) {
+        P.w.moves[0] = holes;
+        P.w.moves[1] = used;
         A.used[0] = used;
     }
     constexpr int EACH = PB / TH;
-    const int base = (int)blockIdx.x * PB + warp * (PB / WARPS);
+    const int base = block * PB + warp * (PB / WARPS);
     uint32_t zero[EACH];
     int count[EACH], mine = 0;
 #pragma unroll
@@ -407,7 +455,7 @@ __global__ void __launch_bounds__(TH) compact_list_kernel(const __grid_constant_
     if (lane == 0)
         part[warp] = mine;
     __syncthreads();
-    int before = sums[blockIdx.x];  // free pages before this one
+    int before = sums[block];  // free pages before this one
     for (int w = 0; w < warp; ++w)
         before += part[w];
 #pragma unroll
@@ -434,19 +482,19 @@ __global__ void __launch_bounds__(TH) compact_list_kernel(const __grid_constant_
     }
 }
 
-__global__ void __launch_bounds__(TH) compact_rows_kernel(const __grid_constant__ CompactParams P)
+// The moves and the table after them, by all CTAs.
+template <bool SMALL>
+__device__ void move_rows(const CompactParams &P)
 {
     const spec_pages_compact_args &A = P.a;
-    allow_next_kernel();
-    wait_previous_kernel();
-    const int moves = __ldcg(P.w.moves), used = __ldcg(A.used), most = A.num_pages / 2;
+    const int moves = got<SMALL>(P.w.moves), used = got<SMALL>(P.w.moves + 1), most = A.num_pages / 2;
     const long long step = (long long)gridDim.x * TH;
     const long long first = (long long)blockIdx.x * TH + threadIdx.x;
     for (long long i = first; i < most; i += step) {
         int src = -1, dst = -1;
         if (i < moves) {
-            src = __ldcg(P.w.movers + i);
-            dst = __ldcg(P.w.holes + i);
+            src = got<SMALL>(P.w.movers + i);
+            dst = got<SMALL>(P.w.holes + i);
             A.ref_out[dst] = __ldg(A.ref_in + src);
         }
         A.copies[i] = src;
@@ -457,9 +505,53 @@ __global__ void __launch_bounds__(TH) compact_rows_kernel(const __grid_constant_
     for (long long i = first; i < entries; i += step) {
         int e = __ldg(A.table_in + i);
         if (e >= used && e < A.num_pages && __ldg(A.ref_in + e) > 0)
-            e = __ldcg(P.w.holes + __ldcg(P.w.rank + e));
+            e = got<SMALL>(P.w.holes + got<SMALL>(P.w.rank + e));
         A.table_out[i] = e;
     }
+}
+
+__global__ void __launch_bounds__(TH) compact_count_kernel(const __grid_constant__ CompactParams P)
+{
+    allow_next_kernel();
+    wait_previous_kernel();
+    list_free<true>(P.a.ref_in, nullptr, P.a.num_pages, (int)blockIdx.x, P.w);
+}
+
+__global__ void __launch_bounds__(TH) compact_list_kernel(const __grid_constant__ CompactParams P)
+{
+    allow_next_kernel();
+    wait_previous_kernel();
+    list_moves<false>(P, (int)blockIdx.x);
+}
+
+__global__ void __launch_bounds__(TH) compact_rows_kernel(const __grid_constant__ CompactParams P)
+{
+    allow_next_kernel();
+    wait_previous_kernel();
+    move_rows<false>(P);
+}
+
+// All three by one CTA, where it has one block of pages and a small table.
+__global__ void __launch_bounds__(TH) compact_small_kernel(const __grid_constant__ CompactParams given)
+{
+    __shared__ int free_of, moves[2], holes[PB / 2], movers[PB / 2], rank[PB];
+    __shared__ CompactParams P;
+    if (threadIdx.x == 0) {
+        P = given;
+        P.w.free_of = &free_of;
+        P.w.moves = moves;
+        P.w.holes = holes;  // no more than there are pages in use behind them
+        P.w.movers = movers;
+        P.w.rank = rank;
+    }
+    allow_next_kernel();
+    wait_previous_kernel();
+    __syncthreads();
+    list_free<true>(P.a.ref_in, nullptr, P.a.num_pages, 0, P.w);
+    __syncthreads();
+    list_moves<true>(P, 0);
+    __syncthreads();
+    move_rows<true>(P);
 }
 
 // ------------------------------------------------------------------- copy
@@ -593,7 +685,7 @@ size_t lay_out(int rows, int pages, uint8_t *at, Work &w)
     w.holes = part((size_t)pages);
     w.movers = part((size_t)pages);
     w.rank = part((size_t)pages);
-    w.moves = part(1);
+    w.moves = part(2);
     return used;
 }
 
@@ -650,6 +742,8 @@ int32_t spec_pages_fork(const spec_pages_fork_args *args, void *workspace, size_
     P.blocks = blocks_of(a.num_pages);
     if (workspace_bytes < lay_out(a.rows_out, a.num_pages, static_cast<uint8_t *>(workspace), P.w))
         return SPEC_ENOSPACE;
+    if (P.blocks <= 1 && std::max(a.rows_in, a.rows_out) <= SMALL_ROWS && a.rows_out > 0)
+        return launch(fork_small_kernel, dim3(1), (P.blocks + 1) * 4, P, stream);
     const unsigned int first = (unsigned int)(P.blocks + (a.rows_out + WARPS - 1) / WARPS);
     const unsigned int second =
         (unsigned int)((std::max(a.rows_in, a.rows_out) + WARPS - 1) / WARPS);
@@ -682,6 +776,8 @@ int32_t spec_pages_compact(const spec_pages_compact_args *args, void *workspace,
     P.blocks = blocks_of(a.num_pages);
     if (workspace_bytes < lay_out(a.rows, a.num_pages, static_cast<uint8_t *>(workspace), P.w))
         return SPEC_ENOSPACE;
+    if (P.blocks == 1 && entries <= SMALL_ENTRIES)
+        return launch(compact_small_kernel, dim3(1), 2 * 4, P, stream);
     int rc = launch(compact_count_kernel, dim3((unsigned int)P.blocks), 0, P, stream);
     if (rc == SPEC_OK)
         rc = launch(compact_list_kernel, dim3((unsigned int)P.blocks), (P.blocks + 1) * 4, P, stream);

@@ -219,3 +219,32 @@ def test_a_life_of_a_pool():
             got = k[0, table[r].long()[at // S], at % S, 0]
             assert got[:, 0].tolist() == texts[r] and got[:, 1].tolist() == [-x for x in texts[r]]
             assert v[0, table[r].long()[at // S], at % S, 0, 0].tolist() == [2 * x for x in texts[r]]
+
+
+@pytest.mark.parametrize("P", [300, 4096, 4097])
+@pytest.mark.parametrize("R0,R1", [(16, 16), (17, 16), (16, 17), (2, 16)])
+def test_fork_by_one_cta_or_several(R0, R1, P):
+    """Around the sizes up to which one CTA does it all."""
+    table, length, ref, rng = pool(R0 + R1, R0, 9, 8, P)
+    for _ in range(3):
+        check_fork(table, length, rng.integers(-1, R0, R1), ref, 8, rng.integers(0, 17, R1))
+
+
+@pytest.mark.parametrize("R,M", [(64, 64), (241, 17)])
+@pytest.mark.parametrize("P", [4096, 4097])
+def test_compact_by_one_cta_or_several(R, M, P):
+    table, _, ref, _ = pool(R, R, M, 4, P)
+    want = pu.compact_ref(table, ref, 4)
+    got = sv.spec_pages_compact(cuda(table), cuda(ref), 4)
+    for x, y in zip(got[:3], want[:3]):
+        assert np.array_equal(x.cpu().numpy(), y)
+    assert int(got[3]) == want[3]
+
+
+def test_fork_without_pages():
+    """A pool of no pages has rows of no tokens only."""
+    none = np.zeros(0, np.int32)
+    got = fork(np.zeros((0, 3)), none, [-1, -1], none, 4)
+    assert (got[0] == -1).all() and got[1].tolist() == [0, 0] and got[3].tolist() == [[-1] * 2] * 2 + [[0] * 2]
+    got = fork(np.zeros((0, 3)), none, [-1, -1], none, 4, reserve=np.array([1, 0]))
+    assert (got[0] == -1).all() and got[1].tolist() == [-1, -1]
