@@ -11,6 +11,7 @@
 #include <stdint.h>
 
 #include "spec_attn.h"
+#include "spec_chunk.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -61,6 +62,14 @@ int32_t spec_selftest_wait_timeout_noalloc(uint64_t limit_ns, void *stream);
 int32_t spec_selftest_attention_timeout(const spec_tree_attention_args *args, void *workspace,
                                         size_t workspace_bytes, int32_t cta, int32_t after,
                                         void *stream);
+
+/*
+ * The same self-test of the chunk attention (spec_chunk_attention's arguments): its CTA `cta` gives up
+ * once it has handed out `after` pieces.
+ */
+int32_t spec_selftest_chunk_timeout(const spec_chunk_attention_args *args, void *workspace,
+                                    size_t workspace_bytes, int32_t cta, int32_t after,
+                                    void *stream);
 
 #ifdef __cplusplus
 }

@@ -240,6 +240,8 @@ def library():
         lib.spec_tree_attention.argtypes = [vp, vp, sz, vp]
         lib.spec_selftest_attention_timeout.restype = i32
         lib.spec_selftest_attention_timeout.argtypes = [vp, vp, sz, i32, i32, vp]
+        lib.spec_selftest_chunk_timeout.restype = i32
+        lib.spec_selftest_chunk_timeout.argtypes = [vp, vp, sz, i32, i32, vp]
         lib.spec_tree_commit.restype = i32
         lib.spec_tree_commit.argtypes = [vp, vp]
         lib.spec_process_logits.restype = i32

@@ -46,6 +46,7 @@
 
 #include <atomic>
 
+#include "spec_bench.h"
 #include "spec_chunk.h"
 #include "spec_verify.h"
 #include "attn_common.cuh"
@@ -130,6 +131,7 @@ struct KParams {
     int page_size, pages_per_seq;
     int page_rows;   // rows of a cache box: min(128, page_size) (contiguous: 128)
     int wide_rows;   // 1 where rows of out start on 32 bytes
+    int lose, lose_after;  // the self-test's CTA (-1: none) and the pieces that it hands out first
 };
 
 // ------------------------------------------------------------------- work
@@ -374,9 +376,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         return false;
     };
     // the same for a warp that has time: it sleeps between its tests
-    auto wait_idle = [&](unsigned long long *bar, uint32_t parity) -> bool {
+    auto wait_idle = [&](unsigned long long *bar, uint32_t parity, int tries = WAIT_TRIES) -> bool {
 #pragma unroll 1
-        for (int i = 0; i < WAIT_TRIES; ++i) {
+        for (int i = 0; i < tries; ++i) {
             if (warp_try(bar, parity))
                 return true;
             if ((i & 15) == 15 && given_up())
@@ -935,7 +937,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             uint32_t items = 0;
             for (uint32_t k = 0;; ++k) {
                 const int at = (int)(k % RING);
-                if (!wait_idle(&S.pempty[at], ((k / RING) & 1u) ^ 1u))
+                // (the self-test: a wait for what nothing brings, with a small limit)
+                const bool lose = slot == P.lose && (int)k == P.lose_after;
+                if (!wait_idle(lose ? &S.drain : &S.pempty[at], lose ? 0u : ((k / RING) & 1u) ^ 1u,
+                               lose ? LOSE_TRIES : WAIT_TRIES))
                     break;
                 const Piece p = walk.piece();
                 if (lane == 0) {
@@ -1199,8 +1204,8 @@ size_t spec_chunk_attention_workspace_size(int32_t Hq, int32_t Hkv, int32_t D)
     return heads_ok(Hq, Hkv, D) ? ws_layout(D).total : 0;
 }
 
-int32_t spec_chunk_attention(const spec_chunk_attention_args *args, void *workspace,
-                             size_t workspace_bytes, void *stream)
+static int32_t attend(const spec_chunk_attention_args *args, void *workspace,
+                      size_t workspace_bytes, int lose, int lose_after, void *stream)
 {
     if (!args)
         return SPEC_EINVAL;
@@ -1259,6 +1264,8 @@ int32_t spec_chunk_attention(const spec_chunk_attention_args *args, void *worksp
     P.page_size = a.page_size;
     P.pages_per_seq = a.pages_per_seq;
     P.wide_rows = a.D % 16 == 0 && aligned(a.out, 32);
+    P.lose = lose;
+    P.lose_after = lose_after;
     P.page_rows = paged && a.page_size < KT ? a.page_size : KT;
 
     CUtensorMap maps[3];
@@ -1291,6 +1298,21 @@ int32_t spec_chunk_attention(const spec_chunk_attention_args *args, void *worksp
                            : launch<1, SPEC_BF16>(maps, P, a.rows, sms, di, st);
     return a.D > PANEL ? launch<2, SPEC_F16>(maps, P, a.rows, sms, di, st)
                        : launch<1, SPEC_F16>(maps, P, a.rows, sms, di, st);
+}
+
+int32_t spec_chunk_attention(const spec_chunk_attention_args *args, void *workspace,
+                             size_t workspace_bytes, void *stream)
+{
+    return attend(args, workspace, workspace_bytes, -1, 0, stream);
+}
+
+int32_t spec_selftest_chunk_timeout(const spec_chunk_attention_args *args, void *workspace,
+                                    size_t workspace_bytes, int32_t cta, int32_t after,
+                                    void *stream)
+{
+    if (cta < 0 || after < 0)
+        return SPEC_EINVAL;
+    return attend(args, workspace, workspace_bytes, cta, after, stream);
 }
 
 }  // extern "C"

@@ -304,3 +304,60 @@ def test_other_streams_and_captured_graphs():
                                   page_table=cases[1]["table"], stream=side)
     side.synchronize()
     assert torch.equal(got, want[1])
+
+
+class Losing:
+    """The library, its chunk attention with a CTA whose wait gives up (include/spec_bench.h)."""
+
+    def __init__(self, lib, cta, after):
+        self.lib, self.lose = lib, (cta, after)
+
+    def __getattr__(self, name):
+        return getattr(self.lib, name)
+
+    def spec_chunk_attention(self, args, ws, size, stream):
+        return self.lib.spec_selftest_chunk_timeout(args, ws, size, *self.lose, stream)
+
+
+# shares inside long items, and of several whole ones with idle ones among them
+LONG = ([70, 5, 0, 200], [20000, 9000, 50, 30000], 2, 5)
+SHORT = ([3, 0, 40, 1] * 50, [0, 9, 100, 128] * 50, 2, 5)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, torch.float16), (128, torch.bfloat16)])
+@pytest.mark.parametrize("shape,cta,after", [(LONG, 0, 0), (LONG, 7, 0), (LONG, 0, 1), (LONG, 30, 1),
+                                             (SHORT, 0, 0), (SHORT, 70, 1), (SHORT, 101, 2)])
+def test_a_wait_that_gives_up(monkeypatch, D, dtype, shape, cta, after):
+    """The status is read, a row is what it is without the lost wait or NaN throughout, none is left
+    unwritten or joined from an earlier call's sums, and the next step is right, whether the CTA has
+    nothing in flight (after 0) or loads and products of its pieces."""
+    new, past, Hkv, G = shape
+    st = pu.make_chunk(8, new, past, Hkv, G, D, 16, dtype)
+    if len(new) > 4:
+        st["length"][2] = -1  # a sequence in error: its item is idle
+
+    def call():
+        plan = sv.spec_chunk_plan(st["start"], st["length"], st["q"], st["k_cache"],
+                                  page_table=st["table"])
+        got = sv.spec_chunk_attention(st["q"], st["k_cache"], st["v_cache"], plan,
+                                      page_table=st["table"], want_lse=True)
+        return *got, plan.read_status()
+    want, want_lse, status = call()
+    assert status == sv.SPEC_DEV_OK
+    with monkeypatch.context() as m:
+        m.setattr(sv, "_lib", Losing(sv.library(), cta, after))
+        out, lse, status = call()
+    assert status == sv.SPEC_DEV_WAIT_TIMEOUT
+    rows = st["start"][-1]
+    bad = torch.isnan(want[:rows]).all(-1)
+    nan = torch.isnan(out[:rows])
+    assert torch.equal(nan.all(-1), nan.any(-1))
+    assert torch.equal(nan.all(-1), torch.isnan(lse[:rows]))
+    assert bool((nan.all(-1) & ~bad).any()) and not bool(nan.all())
+    keep = ~nan.all(-1)
+    assert torch.equal(out[:rows][keep], want[:rows][keep])
+    assert torch.equal(lse[:rows][keep], want_lse[:rows][keep])
+    again, lse, status = call()
+    assert status == sv.SPEC_DEV_OK
+    assert torch.equal(torch.isnan(again), torch.isnan(want))
+    assert torch.equal(again.nan_to_num(), want.nan_to_num())

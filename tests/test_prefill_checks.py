@@ -119,6 +119,16 @@ def test_attention_workspace(lib):
         assert lib.spec_chunk_attention_workspace_size(*bad) == 0
 
 
+def test_selftest_refusals(lib):
+    need = lib.spec_chunk_attention_workspace_size(8, 2, 64)
+    a = _set(sv._ChunkArgs(), q=0, k_cache=A, v_cache=A, page_table=A, plan=A, out=A, scale=0.1, B=2,
+             rows=9, Hq=8, Hkv=2, D=64, page_size=16, pages_per_seq=4, num_pages=9,
+             dtype=sv.SPEC_BF16)
+    for cta, after in ((-1, 0), (0, -1), (0, 0)):
+        assert lib.spec_selftest_chunk_timeout(ctypes.byref(a), vp(A), need, cta, after,
+                                               None) == sv.SPEC_EINVAL
+
+
 # ------------------------------------------------------------------- beams
 
 def select(lib, ws=A, ws_bytes=None, **kw):
