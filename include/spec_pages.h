@@ -35,8 +35,8 @@ extern "C" {
  *   - where the last page in use (length % page_size tokens) is replaced so, it is
  *     listed to be copied: copies[0][r], copies[1][r], copies[2][r] are its old page, its
  *     new page and its tokens; -1, -1, 0 where there is nothing to copy.
- * parent[r] = -1: a row of length 0, with pages for reserve[r] tokens.  Every old row gives up its references, so pages
- * that no new row has taken over lose them and may become free.
+ * parent[r] = -1: a row of length 0, with pages for reserve[r] tokens.  Every old row gives up its
+ * references, so pages that no new row has taken over lose them and may become free.
  *   table_in   device int32 [rows_in, pages_per_seq], length_in [rows_in]
  *   parent     device int32 [rows_out]; reserve likewise or NULL (0)
  *   table_out  [rows_out, pages_per_seq], length_out [rows_out], ref_out [num_pages],
@@ -49,8 +49,8 @@ extern "C" {
  * suffice, every row is in error, and ref_out is ref_in.
  * 0 <= rows_in, rows_out <= 65535, 0 <= num_pages <= SPEC_PAGES_MAX, pages_per_seq * page_size <
  * 2^31.  The workspace has spec_pages_workspace_size bytes (0 for sizes out of range), 256-byte
- * aligned, need not be cleared and belongs to one call at a time.  Two kernels on
- * `stream`, no allocation.
+ * aligned, need not be cleared and belongs to one call at a time.  One or two kernels
+ * on `stream`, no allocation.
  */
 typedef struct spec_pages_fork_args {
     const int32_t *table_in, *length_in, *parent, *reserve, *ref_in;
@@ -72,7 +72,7 @@ int32_t spec_pages_fork(const spec_pages_fork_args *args, void *workspace, size_
  *              move in order; then -1, -1, 0
  *   used       int32 [1]: n
  * Tables of other owners have to be in the same call.  Workspace as
- * spec_pages_fork's (rows_out = rows).  Three kernels on `stream`.
+ * spec_pages_fork's (rows_out = rows).  One to three kernels on `stream`.
  */
 typedef struct spec_pages_compact_args {
     const int32_t *table_in, *ref_in;

