@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib
 import math
 import os
 import struct
@@ -1477,6 +1478,40 @@ _checked_append, _checked_plan, _checked_chunk = _Checked(), _Checked(), _Checke
 _checked_beam, _checked_reorder = _Checked(), _Checked()
 _checked_fork, _checked_compact, _checked_copy = _Checked(), _Checked(), _Checked()
 
+# The short way of a call that is known (csrc/calls.cpp): by the same things, what its checks came to and
+# the words of its arguments but the addresses are kept there, and run(number, a, b, *tensors)
+# makes the outputs and the call, or answers None for the long way.
+_short = _run = None
+_APPEND, _PLAN, _ATTEND, _SELECT, _REORDER, _FORK, _COMPACT, _COPY = range(8)
+_AS_ARGS, _WITH_WORKSPACE, _AS_REORDER, _AS_PLAN = range(4)
+
+
+def _load_calls():
+    """The module; without it every call goes the long way."""
+    global _short, _run
+    if _short is None:
+        try:
+            module = importlib.import_module("._calls", __name__)
+        except ImportError:
+            _short = False
+        else:
+            text = ctypes.cast(library().spec_verify_strerror, ctypes.c_void_p).value
+            module.setup(SpecVerifyError, text)
+            _short, _run = module, module.run
+    return _short
+
+
+def _keep(call, name, style, args, in_at, outs, out_at, dev, kind=-1, need=0, extra=None):
+    """What run(*call) does from now on: call = (number, a, b, *tensors), in_at and out_at the
+    places of the inputs' and outputs' addresses in args."""
+    torch, lib = _torch(), _lib
+    if type(lib) is not ctypes.CDLL or not all([t is None or type(t) is torch.Tensor
+                                                for t in call[3:]]):
+        return
+    if _short or _load_calls():
+        _short.keep(call, name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value, style, args,
+                    in_at, outs, out_at, kind, need, dev.index, extra)
+
 
 def _scratch(cache, need, device, h, s, zeroed=False):
     """A workspace of `need` bytes from `cache`, one per (host thread, device, stream).
@@ -1493,10 +1528,12 @@ def _scratch(cache, need, device, h, s, zeroed=False):
     ws = cache.of.get(key)
     if ws is None or ws.numel() < need:
         ws = cache.of[key] = make(need, dtype=torch.uint8, device=device)
+        if _short or _load_calls():
+            _short.workspace(_kinds.index(cache), device.index, h, ws.data_ptr(), need)
     return ws
 
 
-_chunk_ws, _beam_ws, _pages_ws = _Workspaces(), _Workspaces(), _Workspaces()
+_chunk_ws, _beam_ws, _pages_ws = _kinds = _Workspaces(), _Workspaces(), _Workspaces()
 
 
 def _caches(k_cache, v_cache, lead, Hkv, D, dtype):
@@ -1548,6 +1585,11 @@ def spec_chunk_append(k_new, v_new, k_cache, v_cache, row_start, cache_len, page
     tokens are rows row_start[b] .. row_start[b + 1] - 1; cache_len int32 [B].
     Returns the new lengths int32 [B] (-1 for a sequence error, whose cache is
     left alone); asynchronous like any CUDA op."""
+    plain = out_len is None and stream is None
+    if _run and plain:
+        got = _run(_APPEND, 0, 0, k_new, v_new, k_cache, v_cache, row_start, cache_len, page_table)
+        if got is not None:
+            return got
     torch = _torch()
 
     def check():
@@ -1590,6 +1632,10 @@ def spec_chunk_append(k_new, v_new, k_cache, v_cache, row_start, cache_len, page
                      _pack_4q(row_start.data_ptr(), cache_len.data_ptr(), _ptr_of(page_table),
                               out_len.data_ptr()), sizes))
     _launch(dev, "spec_chunk_append", (_lib or library()).spec_chunk_append, args, h)
+    if plain:
+        _keep((_APPEND, 0, 0, k_new, v_new, k_cache, v_cache, row_start, cache_len, page_table),
+              "spec_chunk_append", _AS_ARGS, args, (0, 8, 16, 24, 144, 152, 160), (out_len,), (168,),
+              dev)
     return out_len
 
 
@@ -1604,8 +1650,13 @@ class ChunkPlan:
     """What spec_chunk_plan made: `status` int32 [B] is a view of `data` (int32),
     which every layer's spec_chunk_attention reads."""
 
-    def __init__(self, B, rows, group, geometry, data):
+    def __init__(self, B, rows, group, geometry, data, code=None):
         self.B, self.rows, self.group, self.geometry, self.data = B, rows, group, geometry, data
+        self.code = code or self.code_of(geometry)
+
+    def code_of(self, geometry):
+        """All that a call's checks depend on of a plan, but its data."""
+        return struct.pack("@6q", self.B, self.rows, self.group, *geometry)
 
     def read_status(self, stream=None):
         """SPEC_DEV_OK, or SPEC_DEV_WAIT_TIMEOUT after a wait inside an attention
@@ -1630,6 +1681,12 @@ def spec_chunk_plan(row_start, kv_len, q, k_cache, page_table=None, plan=None, s
     page_table int32 [B, pages_per_seq], or None for a contiguous cache.
     `plan` refills a ChunkPlan of the same sizes.  Returns a ChunkPlan;
     asynchronous like any CUDA op."""
+    plain = plan is None and stream is None
+    if _run and plain:
+        got = _run(_PLAN, 0, 0, row_start, kv_len, q, k_cache, page_table)
+        if got is not None:
+            data, (B, T, G, geometry, code) = got
+            return ChunkPlan(B, T, G, geometry, data, code)
     torch = _torch()
 
     def check():
@@ -1658,10 +1715,14 @@ def spec_chunk_plan(row_start, kv_len, q, k_cache, page_table=None, plan=None, s
                                       plan.data if plan is not None else None))
     if plan is None:
         plan = ChunkPlan(B, T, G, geometry, _new(s, (need // 4,), (1,), torch.int32, dev))
-    plan.geometry = geometry
+    plan.geometry, plan.code = geometry, plan.code_of(geometry)
     _launch(dev, "spec_chunk_plan", (_lib or library()).spec_chunk_plan, row_start.data_ptr(),
             kv_len.data_ptr(), _ptr_of(page_table), B, T, G, *geometry, plan.data.data_ptr(), need,
             h)
+    if plain:
+        _keep((_PLAN, 0, 0, row_start, kv_len, q, k_cache, page_table), "spec_chunk_plan", _AS_PLAN,
+              struct.pack("@5Q6i", 0, 0, 0, 0, need, B, T, G, *geometry), (0, 8, -1, -1, 16),
+              (plan.data,), (24,), dev, extra=(B, T, G, geometry, plan.code))
     return plan
 
 
@@ -1682,6 +1743,11 @@ def spec_chunk_attention(q, k_cache, v_cache, plan, page_table=None, scale=None,
     Returns out [rows, Hq, D] and, with want_lse, the rows' log-sum-exp float32
     [rows, Hq]; rows of no sequence are left as they are.  Asynchronous like
     any CUDA op."""
+    plain = scale is None and out is None and not want_lse and ws is None and stream is None
+    if _run and plain:
+        got = _run(_ATTEND, plan.code, 0, q, k_cache, v_cache, plan.data, page_table)
+        if got is not None:
+            return got
     torch = _torch()
 
     def check():
@@ -1735,6 +1801,10 @@ def spec_chunk_attention(q, k_cache, v_cache, plan, page_table=None, scale=None,
                                  _ptr_of(lse), scale), sizes))
     _launch(dev, "spec_chunk_attention", (_lib or library()).spec_chunk_attention, args,
             ws.data_ptr(), ws.numel(), h)
+    if plain:
+        _keep((_ATTEND, plan.code, 0, q, k_cache, v_cache, plan.data, page_table),
+              "spec_chunk_attention", _WITH_WORKSPACE, args, (0, 8, 16, 96, 88), (out,), (104,), dev,
+              0, need)
     return (out, lse) if want_lse else out
 
 
@@ -1756,6 +1826,11 @@ def spec_beam_select(logits, scores, n, finished=None, norm=None, end_token=0, w
     call at a time, by default this thread's.  Returns tokens, beams int32
     [B, n] and scores float32 [B, n], best first (-1, -1 and -inf where there
     are fewer); asynchronous like any CUDA op."""
+    plain = ws is None and stream is None
+    if _run and plain:
+        got = _run(_SELECT, n, end_token, logits, scores, finished, norm)
+        if got is not None:
+            return got
     torch = _torch()
 
     def check():
@@ -1791,6 +1866,10 @@ def spec_beam_select(logits, scores, n, finished=None, norm=None, end_token=0, w
                       tokens.data_ptr(), beams.data_ptr(), best.data_ptr()) + sizes
     _launch(dev, "spec_beam_select", (_lib or library()).spec_beam_select, args, ws.data_ptr(),
             ws.numel(), h)
+    if plain:
+        _keep((_SELECT, n, end_token, logits, scores, finished, norm), "spec_beam_select",
+              _WITH_WORKSPACE, args, (0, 8, 24, 16), (tokens, beams, best), (32, 40, 48), dev, 1,
+              need)
     return tokens, beams, best
 
 
@@ -1800,6 +1879,11 @@ def spec_beam_reorder(state, beams, dim=0, out=None, stream=None):
     state [.., B, K, ..] contiguous, of any dtype, B its dimension `dim`; beams
     int32 [B, n] from spec_beam_select.  Returns [.., B, n, ..], where the place
     of a beam -1 is 0; asynchronous like any CUDA op."""
+    plain = out is None and stream is None
+    if _run and plain:
+        got = _run(_REORDER, dim, 0, state, beams)
+        if got is not None:
+            return got
     torch = _torch()
 
     def check():
@@ -1822,6 +1906,9 @@ def spec_beam_reorder(state, beams, dim=0, out=None, stream=None):
         out = _new(s, shape, st, dtype, dev)
     _launch(dev, "spec_beam_reorder", (_lib or library()).spec_beam_reorder, state.data_ptr(),
             beams.data_ptr(), out.data_ptr(), *sizes, h)
+    if plain:
+        _keep((_REORDER, dim, 0, state, beams), "spec_beam_reorder", _AS_REORDER,
+              struct.pack("@3Q4iq", 0, 0, 0, *sizes), (0, 8), (out,), (16,), dev)
     return out
 
 
@@ -1849,8 +1936,9 @@ def _check_outs(given, shapes, dev):
         _dev_out(f"out[{i}]", t, shape, _torch().int32, dev)
 
 
-def _pages_call(name, pointers, sizes, shapes, need, out, ws, dev, h, s):
-    """The outputs and the workspace where the caller gave none, and the launch."""
+def _pages_call(name, call, in_at, pointers, sizes, shapes, need, out, ws, dev, h, s):
+    """The outputs and the workspace where the caller gave none, and the launch; `call` as
+    _keep's, or None."""
     i32 = _torch().int32
     out = tuple(out) if out is not None else tuple([_new(s, *x, i32, dev) for x in shapes])
     if ws is None:
@@ -1859,6 +1947,10 @@ def _pages_call(name, pointers, sizes, shapes, need, out, ws, dev, h, s):
         _check_ws(ws, dev)
     args = b"".join((pointers, _pack_4q(*[t.data_ptr() for t in out]), sizes))
     _launch(dev, name, getattr(_lib or library(), name), args, ws.data_ptr(), ws.numel(), h)
+    if call is not None:
+        at = len(pointers)
+        _keep(call, name, _WITH_WORKSPACE, args, in_at, out, (at, at + 8, at + 16, at + 24), dev, 2,
+              need)
     return out
 
 
@@ -1873,6 +1965,12 @@ def spec_pages_fork(table, length, parent, ref_count, page_size, reserve=None, o
     lengths, reference counts and copies int32 [3, rows_out] for spec_pages_copy
     (before the next call that takes pages).  `out`: those four, none of them an
     input.  Asynchronous like any CUDA op."""
+    plain = out is None and ws is None and stream is None
+    if _run and plain:
+        got = _run(_FORK, page_size, 0, table, length, parent, ref_count, reserve)
+        if got is not None:
+            return got
+
     def check():
         if table.dim() != 2 or parent.dim() != 1 or ref_count.dim() != 1:
             raise ValueError("table must be [rows, pages_per_seq], parent [rows_out], "
@@ -1896,7 +1994,9 @@ def spec_pages_fork(table, length, parent, ref_count, page_size, reserve=None, o
                                       *(out if out is not None else ())))
     pointers = _pack_5q(table.data_ptr(), length.data_ptr(), parent.data_ptr(), _ptr_of(reserve),
                         ref_count.data_ptr())
-    return _pages_call("spec_pages_fork", pointers, sizes, shapes, need, out, ws, dev, h, s)
+    call = (_FORK, page_size, 0, table, length, parent, ref_count, reserve) if plain else None
+    return _pages_call("spec_pages_fork", call, (0, 8, 16, 32, 24), pointers, sizes, shapes, need, out,
+                       ws, dev, h, s)
 
 
 def spec_pages_compact(table, ref_count, page_size, out=None, ws=None, stream=None):
@@ -1907,6 +2007,12 @@ def spec_pages_compact(table, ref_count, page_size, out=None, ws=None, stream=No
     [3, num_pages // 2] for spec_pages_copy and the number of pages in use
     int32 [1].  `out`: those four, none of them an input.  Asynchronous like any
     CUDA op."""
+    plain = out is None and ws is None and stream is None
+    if _run and plain:
+        got = _run(_COMPACT, page_size, 0, table, ref_count)
+        if got is not None:
+            return got
+
     def check():
         if table.dim() != 2 or ref_count.dim() != 1:
             raise ValueError("table must be [rows, pages_per_seq], ref_count [pages]")
@@ -1923,7 +2029,9 @@ def spec_pages_compact(table, ref_count, page_size, out=None, ws=None, stream=No
          None if out is None else tuple([_meta(t) for t in out])), check)
     h, s = _call_stream(stream, dev, (table, ref_count, ws, *(out if out is not None else ())))
     pointers = struct.pack("@2Q", table.data_ptr(), ref_count.data_ptr())
-    return _pages_call("spec_pages_compact", pointers, sizes, shapes, need, out, ws, dev, h, s)
+    call = (_COMPACT, page_size, 0, table, ref_count) if plain else None
+    return _pages_call("spec_pages_compact", call, (0, 8), pointers, sizes, shapes, need, out, ws, dev,
+                       h, s)
 
 
 def spec_pages_copy(k_cache, v_cache, copies, stream=None):
@@ -1933,6 +2041,9 @@ def spec_pages_copy(k_cache, v_cache, copies, stream=None):
     layers, 2 or 4 bytes an element, any strides with a contiguous last
     dimension; copies int32 [3, n]: sources, destinations and numbers of slots
     (-1, -1, 0: nothing).  Asynchronous like any CUDA op."""
+    if _run and stream is None and _run(_COPY, 0, 0, k_cache, v_cache, copies):
+        return
+
     def check():
         if k_cache.dim() not in (4, 5) or v_cache.shape != k_cache.shape:
             raise ValueError("k_cache and v_cache must be [.., pages, slots, Hkv, D]")
@@ -1955,3 +2066,6 @@ def spec_pages_copy(k_cache, v_cache, copies, stream=None):
     args = b"".join((struct.pack("@2Q", k_cache.data_ptr(), v_cache.data_ptr()), strides,
                      struct.pack("@Q", copies.data_ptr()), sizes))
     _launch(dev, "spec_pages_copy", (_lib or library()).spec_pages_copy, args, h)
+    if stream is None:
+        _keep((_COPY, 0, 0, k_cache, v_cache, copies), "spec_pages_copy", _AS_ARGS, args, (0, 8, 80), (),
+              (), dev)

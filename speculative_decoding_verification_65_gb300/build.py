@@ -7,12 +7,17 @@ cache's pages, the benchmark's read probe), one -gencode, no cmake: each
 is compiled by its own nvcc process in parallel, then one nvcc call links the
 shared library.  The library links the CUDA runtime statically so it only
 needs the driver at run time; PyTorch's own runtime is not involved.
+
+Beside them, where PyTorch is installed, g++ compiles the Python binding's short way
+into the library (csrc/calls.cpp) against PyTorch's headers.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -39,6 +44,8 @@ DEPS = [os.path.join(CSRC, "device_common.cuh"), os.path.join(CSRC, "attn_plan.c
         os.path.join(ROOT, "include", "spec_pages.h")]
 SRC = SRCS[0]
 LIB = os.path.join(PKG, "libspecverify.so")
+CALLS_SRC = os.path.join(CSRC, "calls.cpp")
+CALLS = os.path.join(PKG, "_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -62,11 +69,35 @@ def link_command(objs, out: str) -> list:
     return [nvcc_path(), *ARCH, "--shared", "-cudart", "static", "-o", out, *objs]
 
 
+def calls_command(out: str):
+    """None without PyTorch (which is looked for, not imported)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    torch = spec.submodule_search_locations[0]
+    lib = os.path.join(torch, "lib")
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    return ["g++", "-std=c++17", "-O2", "-Wall", "-fPIC", "-shared", "-fvisibility=hidden",
+            "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"],
+            "-isystem", os.path.join(torch, "include"),
+            "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(cuda, "include"), "-o", out, CALLS_SRC, "-L", lib,
+            "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10",
+            f"-Wl,-rpath,{lib}"]
+
+
 def stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(p) > t for p in (*SRCS, *DEPS, __file__))
+    return any(os.path.getmtime(p) > t for p in (*SRCS, *DEPS, __file__)) or calls_stale()
+
+
+def calls_stale() -> bool:
+    if importlib.util.find_spec("torch") is None:
+        return False
+    return not os.path.exists(CALLS) or any(os.path.getmtime(p) > os.path.getmtime(CALLS)
+                                            for p in (CALLS_SRC, __file__))
 
 
 def _run(cmd, verbose):
@@ -83,13 +114,19 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and not stale() and not extra:
         return LIB
     tag = f".tmp{os.getpid()}"
+    calls = calls_command(CALLS + tag)
     objs = [os.path.join(CSRC, os.path.basename(s) + tag + ".o") for s in SRCS]
     try:
-        with ThreadPoolExecutor(len(SRCS)) as ex:
+        with ThreadPoolExecutor(len(SRCS) + 1) as ex:
+            short = ex.submit(_run, calls, verbose) if calls else None
             rcs = list(ex.map(lambda so: _run(compile_command(so[0], so[1], extra), verbose),
                               zip(SRCS, objs)))
         if any(rcs):
             raise RuntimeError("nvcc failed compiling the CUDA sources")
+        if short and short.result():
+            raise RuntimeError("g++ failed compiling csrc/calls.cpp")
+        if short:
+            os.replace(CALLS + tag, CALLS)
         tmp = LIB + tag
         if _run(link_command(objs, tmp), verbose):
             raise RuntimeError("nvcc failed linking libspecverify.so")

@@ -34,8 +34,8 @@ constexpr int MAX_BLOCKS = SPEC_PAGES_MAX / PB;
 
 // One CTA does all where it has up to SMALL_ROWS rows or SMALL_ENTRIES entries of a table, and one block
 // of pages: a launch costs the host 2.5 us.  (4 beams of 600 tokens forked, with their copies: 8.3 us of
-// the GPU's time and 24 us of the host's, by two kernels 8.7 and 27; 512 pages compacted and
-// copied: 22 and 22, by three kernels 25 and 28.)
+// the GPU's time and 10 us of the host's, by two kernels 8.7 and 13; 512 pages compacted and
+// copied: 22 and 10, by three kernels 25 and 16.)
 constexpr int SMALL_ROWS = 16;
 constexpr uint64_t SMALL_ENTRIES = 4096;
 
