@@ -90,7 +90,7 @@ def stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(p) > t for p in (*SRCS, *DEPS, __file__)) or calls_stale()
+    return any(os.path.getmtime(p) > t for p in (*SRCS, *DEPS, __file__))
 
 
 def calls_stale() -> bool:
@@ -109,24 +109,31 @@ def _run(cmd, verbose):
     return res.returncode
 
 
+def build_calls(command, tag, verbose):
+    if _run(command, verbose):
+        raise RuntimeError("g++ failed compiling csrc/calls.cpp")
+    os.replace(CALLS + tag, CALLS)
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    """Compile the CUDA library if it is missing or older than its sources."""
-    if not force and not stale() and not extra:
-        return LIB
+    """Compile the CUDA library if it is missing or older than its sources, and the binding's
+    short way into it likewise."""
     tag = f".tmp{os.getpid()}"
-    calls = calls_command(CALLS + tag)
+    calls = calls_command(CALLS + tag) if force or calls_stale() else None
+    if not force and not stale() and not extra:
+        if calls:
+            build_calls(calls, tag, verbose)
+        return LIB
     objs = [os.path.join(CSRC, os.path.basename(s) + tag + ".o") for s in SRCS]
     try:
         with ThreadPoolExecutor(len(SRCS) + 1) as ex:
-            short = ex.submit(_run, calls, verbose) if calls else None
+            short = ex.submit(build_calls, calls, tag, verbose) if calls else None
             rcs = list(ex.map(lambda so: _run(compile_command(so[0], so[1], extra), verbose),
                               zip(SRCS, objs)))
         if any(rcs):
             raise RuntimeError("nvcc failed compiling the CUDA sources")
-        if short and short.result():
-            raise RuntimeError("g++ failed compiling csrc/calls.cpp")
         if short:
-            os.replace(CALLS + tag, CALLS)
+            short.result()
         tmp = LIB + tag
         if _run(link_command(objs, tmp), verbose):
             raise RuntimeError("nvcc failed linking libspecverify.so")

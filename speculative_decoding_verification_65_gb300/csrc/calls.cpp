@@ -73,9 +73,10 @@ struct Recipe {
 
 constexpr size_t MOST_ARGS = 512, MOST_OUTS = 4, MOST_KEPT = 4096;
 
-// (all under the interpreter's lock)
-std::unordered_map<std::string, std::unique_ptr<Recipe>> kept;
-std::unordered_set<std::string> names;
+// (All under the interpreter's lock.  Never taken down: a process's end comes after the interpreter's,
+// whose objects they hold.)
+auto &kept = *new std::unordered_map<std::string, std::unique_ptr<Recipe>>;
+auto &names = *new std::unordered_set<std::string>;
 PyObject *error_class = nullptr;
 const char *(*error_text)(int32_t) = nullptr;
 

@@ -21,10 +21,11 @@ struct alignas(16) ChunkGroup {
     int pad[2];
 };
 
-struct ChunkHeader {
+struct alignas(16) ChunkHeader {
     int status;       // device status word of the attention calls that read the plan
     int groups;
-    int pad[62];
+    long long tiles;  // key tiles of all groups
+    int pad[60];
 };
 static_assert(sizeof(ChunkHeader) == 256, "header is 256 bytes");
 

@@ -137,6 +137,7 @@ __device__ void list_groups(const PlanParams &P)
         ChunkHeader *h = reinterpret_cast<ChunkHeader *>(P.plan);
         h->status = SPEC_DEV_OK;
         h->groups = (int)done;
+        h->tiles = tiles;
     }
 }
 

@@ -166,32 +166,57 @@ __device__ __forceinline__ void load_group(const KParams &P, Place &q)
     q.status = __ldg(reinterpret_cast<const int *>(P.plan + P.lay.status) + a.x);
 }
 
-__device__ __forceinline__ Place empty_place(const KParams &P)
+// What a look-up begins with: the plan's totals, and, on its way beside them, each lane's first
+// probe of the running sums (by the groups that there may be: how many there are is not known yet).
+__device__ __forceinline__ Place empty_place(const KParams &P, long long &probe)
 {
+    const long long *cum = reinterpret_cast<const long long *>(P.plan + P.lay.cum);
+    const int i = ((int)threadIdx.x & 31) * ((P.lay.most + 31) / 32);
     Place q = {};
-    q.groups = __ldg(&reinterpret_cast<const ChunkHeader *>(P.plan)->groups);
-    q.total = __ldg(reinterpret_cast<const long long *>(P.plan + P.lay.cum) + q.groups);
+    const int4 head = __ldg(reinterpret_cast<const int4 *>(P.plan));
+    probe = i < P.lay.most ? __ldg(cum + i) : 0;
+    q.groups = head.y;
+    q.total = (long long)((unsigned long long)(unsigned int)head.w << 32 | (unsigned int)head.z);
     return q;
 }
 
-// A warp looks up unit u < total * Hkv: 32 probes of the plan's running sums a round.
-__device__ __forceinline__ void look_up(const KParams &P, long long u, Place &q)
+// A warp looks up unit u < total * Hkv: 32 probes of the plan's running sums a round, the last of them
+// with the groups themselves.  (A chain of three loads up to 1024 groups, and the status.)
+__device__ __forceinline__ void look_up(const KParams &P, long long u, long long probe, Place &q)
 {
     const long long *cum = reinterpret_cast<const long long *>(P.plan + P.lay.cum);
     const int lane = (int)threadIdx.x & 31;
     q.h = (int)(u / q.total);
     const long long at = u - q.h * q.total;
-    int lo = 0, len = q.groups;
-    while (len > 1) {
-        const int step = (len + 31) / 32, i = lane * step;
-        const bool below = i < len && __ldg(cum + lo + i) <= at;
+    int step = (P.lay.most + 31) / 32, lo = 0, len = q.groups;
+    bool below = lane * step < len && probe <= at;
+    while (true) {
         const int last = 31 - __clz((int)__ballot_sync(0xffffffffu, below));
         lo += last * step;
         len = len - last * step < step ? len - last * step : step;
+        if (len <= 32)
+            break;
+        step = (len + 31) / 32;
+        below = lane * step < len && __ldg(cum + lo + lane * step) <= at;
     }
-    q.g = lo;
-    q.tile = (int)(at - __ldg(cum + lo));
-    load_group(P, q);
+    long long before = 0;
+    int4 a = {}, b = {};
+    if (lane < len) {
+        const int4 *group = reinterpret_cast<const int4 *>(P.plan + P.lay.group) + 2 * (size_t)(lo + lane);
+        before = __ldg(cum + lo + lane);
+        a = __ldg(group);
+        b = __ldg(group + 1);
+    }
+    const int in = 31 - __clz((int)__ballot_sync(0xffffffffu, lane < len && before <= at));
+    q.g = lo + in;
+    q.tile = (int)(at - __shfl_sync(0xffffffffu, before, in));
+    q.x.b = __shfl_sync(0xffffffffu, a.x, in);
+    q.x.row0 = __shfl_sync(0xffffffffu, a.y, in);
+    q.x.ntok = __shfl_sync(0xffffffffu, a.z, in);
+    q.x.tiles = __shfl_sync(0xffffffffu, a.w, in);
+    q.x.pos0 = __shfl_sync(0xffffffffu, b.x, in);
+    q.x.bad = __shfl_sync(0xffffffffu, b.y, in);
+    q.status = __ldg(reinterpret_cast<const int *>(P.plan + P.lay.status) + q.x.b);
 }
 
 // A CTA's share: `per` units for each of the slots that have any.
@@ -205,15 +230,17 @@ struct Walk {
     Place q;
     long long u0, u1, u, per;
 
-    __device__ __forceinline__ Walk(const KParams &P, int slot) : q(empty_place(P))
+    __device__ __forceinline__ Walk(const KParams &P, int slot)
     {
+        long long probe;
+        q = empty_place(P, probe);
         const long long all = q.total * P.Hkv;
         per = share(P, all);
         u0 = slot * per;
         u1 = u0 + per < all ? u0 + per : all;
         u = u0;
         if (u < u1)
-            look_up(P, u, q);
+            look_up(P, u, probe, q);
     }
     __device__ __forceinline__ Piece piece() const
     {
@@ -1030,11 +1057,12 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, 4)
     const int r = (int)blockIdx.z * JOIN_ROWS + mine, s = (int)blockIdx.y;
     allow_next_kernel();
     // (the plan is complete: every CTA of the attention had waited for it before this grid began)
-    Place q = empty_place(P);
+    long long probe;
+    Place q = empty_place(P, probe);
     const long long all = q.total * P.Hkv, per = share(P, all);
     const long long end = ((long long)blockIdx.x + 1) * per;
     if (end < all)
-        look_up(P, end, q);
+        look_up(P, end, probe, q);
     wait_previous_kernel();
     if (end >= all)
         return;
