@@ -12,7 +12,7 @@
 // n-th best head bounds the result, so at most n lists have entries in it; those are sorted.
 // Bound by the bytes of the logits, and by what comes behind them when all segments end at one
 // time: 64 x 8 rows of 128256 bf16 (440 of them live, 113 MB) are read by 28 us (4.2 TB/s), their best are
-// chosen by 32 and merged by 40; 32 x 5 rows of 151936 fp32 (83 MB) by 20, 25 and 33.  More bytes in
+// chosen by 32 and merged by 39; 32 x 5 rows of 151936 fp32 (83 MB) by 20, 25 and 33.  More bytes in
 // flight (rings in shared memory, prefetches into L2) did not shorten the reading: 42 us
 // became 44 to 46.
 //
@@ -122,10 +122,11 @@ struct PickSmem {
 // Shared memory that a kernel is launched with: the groups' maxima of the scan, or a merge's first
 // entries of lists (order, k V + x; 4 n of them, or one of each list) and then what it has to
 // sort, up to n entries of n lists (a place too).
+constexpr int FEW = 128;
 constexpr size_t larger(size_t a, size_t b) { return a > b ? a : b; }
 constexpr size_t merge_bytes(int n, int lists)
 {
-    return larger(larger((size_t)n * n, (size_t)TH / 2) * 16, larger((size_t)lists, (size_t)4 * n) * 12);
+    return larger(larger((size_t)n * n, (size_t)FEW) * 16, larger((size_t)lists, (size_t)4 * n) * 12);
 }
 constexpr size_t SCAN_BYTES = (size_t)GROUPS * TH * 4;
 extern __shared__ __align__(16) uint8_t dyn[];
@@ -135,33 +136,42 @@ __device__ __forceinline__ bool better(u64 r1, int f1, u64 r2, int f2)
     return r1 > r2 || (r1 == r2 && f1 < f2);
 }
 
-// How many of m things are better than this one, by a converged warp: `is_better(j)` asks for one.
-template <typename F>
-__device__ __forceinline__ int place_of(int m, F is_better)
+// The places of m things in their order, by the whole CTA: `is_better(j, i)` compares two, `found(i, place)`
+// is told once for each.  Four lanes share one thing's comparisons: with a warp for each thing
+// a merge of 128 took 0.6 us more.
+template <typename B, typename F>
+__device__ __forceinline__ void places(int m, B is_better, F found)
 {
-    const int lane = (int)threadIdx.x & 31;
-    int place = 0;
-    for (int j0 = 0; j0 < m; j0 += 32)
-        place += __popc(__ballot_sync(0xffffffffu, j0 + lane < m && is_better(j0 + lane)));
-    return place;
+    const int quarter = (int)threadIdx.x & 3;
+    for (int i0 = 0; i0 < m; i0 += TH / 4) {
+        const int i = i0 + (int)(threadIdx.x >> 2);
+        int place = 0;
+        if (i < m)
+#pragma unroll 4
+            for (int j = quarter; j < m; j += 4)
+                place += is_better(j, i) ? 1 : 0;
+        place += __shfl_xor_sync(0xffffffffu, place, 1);
+        place += __shfl_xor_sync(0xffffffffu, place, 2);
+        if (i < m && quarter == 0)
+            found(i, place);
+    }
 }
 
 // The candidates' best n, sorted, to S.cand; returns the order that a later one has to exceed.
 // The whole CTA; S.count candidates (at most CAP).
 __device__ uint32_t cut(ScanSmem &S, int n)
 {
-    const int tid = (int)threadIdx.x, lane = tid & 31;
+    const int tid = (int)threadIdx.x;
     __syncthreads();
     const int m = S.count;
     if (tid < n)
         S.best[tid] = 0;
     __syncthreads();
-    for (int i = tid >> 5; i < m; i += WARPS) {
-        const u64 key = S.cand[i];
-        const int place = place_of(m, [&](int j) { return S.cand[j] > key; });
-        if (lane == 0 && place < n)
-            S.best[place] = key;
-    }
+    places(m, [&](int j, int i) { return S.cand[j] > S.cand[i]; },
+           [&](int i, int place) {
+               if (place < n)
+                   S.best[place] = S.cand[i];
+           });
     __syncthreads();
     if (tid < n)
         S.cand[tid] = S.best[tid];
@@ -191,9 +201,9 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
         const u64 key = __ldcg(&P.lists[((size_t)row * P.segs + (l - k * P.segs)) * n + at]);
         return !(s > -INFINITY) ? 0 : !fin ? key : at == 0 && l == k * P.segs ? ENDED : 0;
     };
-    // Few candidates in all: each has a thread, whose load is on its way from here on, and is compared
-    // with all of them (128: 1.1 us less than by the bound below; 150: 0.7 us more)
-    const bool few = lists * n <= TH / 2;
+    // Few candidates in all: each has a thread, whose load is on its way from here on, and all are
+    // compared (64: 1.5 us less than by the bound below; 128: 0.25 less; 150: 2.2 more)
+    const bool few = lists * n <= FEW;
     const u64 mine = few && tid < lists * n ? fetch(tid / n, tid % n) : 0;
     // the rows' totals, a row per warp; what takes 64 bits for all rows at once, a row per lane (this
     // GPU has two 64-bit lanes per SM: by the warps one after the other it took 10 us)
@@ -283,6 +293,7 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
     };
     u64 *rank = reinterpret_cast<u64 *>(dyn);
     int *flat;
+    float *value;
     int m;  // candidates among which the n best are
     bool open = false;
     if (tid < n)
@@ -290,25 +301,9 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
     if (few) {
         m = lists * n;
         flat = reinterpret_cast<int *>(rank + m);
-        u64 r = 0;
-        int f = INT_MAX;
-        float x = 0.0f;
-        if (tid < m) {
-            rank[tid] = r = worth(tid / n, mine, f, x);
-            flat[tid] = f;
-        }
-        __syncthreads();
-        if (r != 0) {
-            int place = 0;
-#pragma unroll 8
-            for (int j = 0; j < m; ++j)
-                place += better(rank[j], flat[j], r, f) ? 1 : 0;
-            if (place < n) {
-                S.rank[place] = r;
-                S.flat[place] = f;
-                S.value[place] = x;
-            }
-        }
+        value = reinterpret_cast<float *>(flat + m);
+        if (tid < m)
+            rank[tid] = worth(tid / n, mine, flat[tid], value[tid]);
     } else {
         // the n-th best of the lists' first entries: no more than n lists reach it, and where a few of
         // each list are looked at, not many more than n entries
@@ -323,20 +318,18 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
             S.count = 0;
         }
         __syncthreads();
-        for (int e = warp; e < firsts; e += WARPS) {
-            const u64 r = rank[e];
-            const int f = flat[e];
-            const int place = place_of(firsts, [&](int j) { return better(rank[j], flat[j], r, f); });
-            if (lane == 0 && r != 0 && place == n - 1) {
-                S.least = r;
-                S.least_flat = f;
-            }
-        }
+        places(firsts, [&](int j, int i) { return better(rank[j], flat[j], rank[i], flat[i]); },
+               [&](int i, int place) {
+                   if (rank[i] != 0 && place == n - 1) {
+                       S.least = rank[i];
+                       S.least_flat = flat[i];
+                   }
+               });
         __syncthreads();
         // the entries that reach it (n n of them at most, in the place of the heads); where the order
         // may be open, also those that might after all
         flat = reinterpret_cast<int *>(rank + n * n);
-        float *value = reinterpret_cast<float *>(flat + n * n);
+        value = reinterpret_cast<float *>(flat + n * n);
         const int least_flat = S.least_flat;
         u64 least = S.least;
         if (!EXACT && least != 0) {
@@ -359,17 +352,16 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
         __syncthreads();
         open = !EXACT && S.count > n * n;
         m = min(S.count, n * n);
-        for (int i = warp; i < m; i += WARPS) {
-            const u64 r = rank[i];
-            const int f = flat[i];
-            const int place = place_of(m, [&](int j) { return better(rank[j], flat[j], r, f); });
-            if (lane == 0 && place < n) {
-                S.rank[place] = r;
-                S.flat[place] = f;
-                S.value[place] = value[i];
-            }
-        }
     }
+    __syncthreads();
+    places(m, [&](int j, int i) { return better(rank[j], flat[j], rank[i], flat[i]); },
+           [&](int i, int place) {
+               if (rank[i] != 0 && place < n) {
+                   S.rank[place] = rank[i];
+                   S.flat[place] = flat[i];
+                   S.value[place] = value[i];
+               }
+           });
     __syncthreads();
     // two candidates of different beams lie too near: neighbours among the best, or the last of these
     // and any that is left (no other pair's order can be open then)
@@ -602,13 +594,11 @@ __global__ void __launch_bounds__(TH, 4) beam_kernel(const __grid_constant__ Bea
         if (tid == 0)
             S.count = 0;
         bad = __syncthreads_or(bad ? 1 : 0) != 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const u64 key = S.best[warp * 8 + i];
-            const int place = place_of(8 * WARPS, [&](int j) { return S.best[j] > key; });
-            if (lane == 0 && place == n - 1)
-                S.bound = (uint32_t)(key >> 32);
-        }
+        places(8 * WARPS, [&](int j, int i) { return S.best[j] > S.best[i]; },
+               [&](int i, int place) {
+                   if (place == n - 1)
+                       S.bound = (uint32_t)(S.best[i] >> 32);
+               });
         float most = -INFINITY;
         // the segment's total
         for (int w = 0; w < WARPS; ++w)
@@ -692,7 +682,7 @@ struct ExactSmem {
 
 // The exact sums of the listed sequences' beams, 2048 logits at a time, and their merge.
 template <int DT>
-__global__ void __launch_bounds__(TH) beam_exact_kernel(const __grid_constant__ BeamParams P)
+__global__ void __launch_bounds__(TH, 4) beam_exact_kernel(const __grid_constant__ BeamParams P)
 {
     using L = Lg<DT>;
     const spec_beam_select_args &A = P.a;
