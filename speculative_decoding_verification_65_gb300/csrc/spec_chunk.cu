@@ -343,6 +343,16 @@ __device__ __forceinline__ void store32(void *p, const uint32_t *w)
                  : "memory");
 }
 
+// Not 0 where one of a word's two elements is an infinity or NaN: its exponent, all ones, carries
+// into the sign's place.
+template <int DT>
+__device__ __forceinline__ uint32_t nonfinite_bits(uint32_t w)
+{
+    constexpr uint32_t exponent = DT == SPEC_BF16 ? 0x7f807f80u : 0x7c007c00u;
+    constexpr uint32_t one = DT == SPEC_BF16 ? 0x00800080u : 0x04000400u;
+    return ((w & exponent) + one) & 0x80008000u;
+}
+
 template <int NP, int DT>
 __global__ void __launch_bounds__(THREADS, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkc,
@@ -551,28 +561,37 @@ __global__ void __launch_bounds__(THREADS, 1)
                     uint32_t found = 0;
                     uint8_t *at = v_p + (size_t)vst * C::TILE + (r0 + (lane >> 3)) * 128 +
                                   (lane & 7) * 16;
-                    uint4 w[NP * 4];  // 4 rows of a panel, 8 lanes each
+                    uint32_t any = 0;
 #pragma unroll
-                    for (int x = 0; x < NP * 4; ++x)
-                        w[x] = *reinterpret_cast<const uint4 *>(at + (x >> 2) * PANEL_BYTES +
-                                                                (x & 3) * 512);
-#pragma unroll
-                    for (int x = 0; x < NP * 4; ++x) {
+                    for (int x = 0; x < NP * 4; ++x) {  // 4 rows of a panel, 8 lanes each
                         const int row = r0 + (x & 3) * 4 + (lane >> 3);
-                        const uint4 f = make_uint4(nonfinite<DT>(w[x].x), nonfinite<DT>(w[x].y),
-                                                   nonfinite<DT>(w[x].z), nonfinite<DT>(w[x].w));
-                        const bool past = row >= keys && row < ((keys + 15) & ~15);
-                        const bool bad = row < keys && jt * KT + row > p.pos0 &&
-                                         (f.x | f.y | f.z | f.w) != 0;
-                        if (past || bad)
-                            *reinterpret_cast<uint4 *>(at + (x >> 2) * PANEL_BYTES + (x & 3) * 512) =
-                                past ? make_uint4(0, 0, 0, 0)
-                                     : make_uint4(w[x].x & ~f.x, w[x].y & ~f.y, w[x].z & ~f.z,
-                                                  w[x].w & ~f.w);
-                        const uint32_t who = __ballot_sync(0xffffffffu, bad);
-                        if (who)
+                        const uint4 w = *reinterpret_cast<const uint4 *>(at + (x >> 2) * PANEL_BYTES +
+                                                                         (x & 3) * 512);
+                        const uint32_t f = nonfinite_bits<DT>(w.x) | nonfinite_bits<DT>(w.y) |
+                                           nonfinite_bits<DT>(w.z) | nonfinite_bits<DT>(w.w);
+                        any |= row < keys && jt * KT + row > p.pos0 ? f : 0u;
+                    }
+                    // (seldom: one warp has rows past the keys, if any, and such values are rare)
+                    if (__any_sync(0xffffffffu, any != 0) || (keys > r0 && keys < r0 + 16)) {
+#pragma unroll 1
+                        for (int x = 0; x < NP * 4; ++x) {
+                            const int row = r0 + (x & 3) * 4 + (lane >> 3);
+                            uint4 *v = reinterpret_cast<uint4 *>(at + (x >> 2) * PANEL_BYTES +
+                                                                 (x & 3) * 512);
+                            uint4 w = *v;
+                            const uint4 f = make_uint4(nonfinite<DT>(w.x), nonfinite<DT>(w.y),
+                                                       nonfinite<DT>(w.z), nonfinite<DT>(w.w));
+                            const bool past = row >= keys && row < ((keys + 15) & ~15);
+                            const bool bad = row < keys && jt * KT + row > p.pos0 &&
+                                             (f.x | f.y | f.z | f.w) != 0;
+                            if (past || bad)
+                                *v = past ? make_uint4(0, 0, 0, 0)
+                                          : make_uint4(w.x & ~f.x, w.y & ~f.y, w.z & ~f.z, w.w & ~f.w);
+                            const uint32_t who = __ballot_sync(0xffffffffu, bad);
+#pragma unroll
                             for (int y = 0; y < 4; ++y)
                                 found |= ((who >> (8 * y)) & 0xffu ? 1u : 0u) << ((x & 3) * 4 + y);
+                        }
                     }
                     if (lane == 0)
                         S.bad[hid & 3u][warp] = (uint16_t)found;
