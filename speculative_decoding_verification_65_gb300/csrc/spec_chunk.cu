@@ -639,21 +639,24 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {
                     if (warp_live) {
-                        float shift = shift_of(m);
-                        unsigned long long shift2 = f2(shift, shift);
-                        unsigned long long sum[2] = {0ull, 0ull};
+                        unsigned long long sum[2];
                         uint32_t x[32], y[32], pk[2][16];
-                        __syncwarp();
-                        tmem_ld_start(t_s + part * 64, x);
-                        tmem_ld_finish(x);
-                        tmem_ld_start(t_s + part * 64 + 32, y);
-                        float top = max32(x);
-                        weigh<DT>(x, c2, shift2, sum, pk[0]);
-                        tmem_ld_finish(y);
-                        top = fmaxf(top, max32(y));
-                        weigh<DT>(y, c2, shift2, sum, pk[1]);
-                        const bool grown = (top - m) * P.c > growth<DT>();  // -inf to finite too
-                        if (__any_sync(0xffffffffu, grown)) {
+                        while (true) {  // (twice at most: by the new maximum nothing has grown)
+                            const float shift = shift_of(m);
+                            const unsigned long long shift2 = f2(shift, shift);
+                            sum[0] = sum[1] = 0ull;
+                            __syncwarp();
+                            tmem_ld_start(t_s + part * 64, x);
+                            tmem_ld_finish(x);
+                            tmem_ld_start(t_s + part * 64 + 32, y);
+                            float top = max32(x);
+                            weigh<DT>(x, c2, shift2, sum, pk[0]);
+                            tmem_ld_finish(y);
+                            top = fmaxf(top, max32(y));
+                            weigh<DT>(y, c2, shift2, sum, pk[1]);
+                            const bool grown = (top - m) * P.c > growth<DT>();  // -inf to finite too
+                            if (!__any_sync(0xffffffffu, grown))
+                                break;
                             // again, by the new maximum, which O and l follow (O when it has the
                             // first half; a wait that gives up ends the group's next one)
                             if (part) {
@@ -673,13 +676,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                                     o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
                                 tmem_st(t_o + d, o);
                             }
-                            sum[0] = sum[1] = 0ull;
-                            shift = shift_of(m);
-                            shift2 = f2(shift, shift);
-                            tmem_ld(t_s + part * 64, x);
-                            weigh<DT>(x, c2, shift2, sum, pk[0]);
-                            tmem_ld(t_s + part * 64 + 32, x);
-                            weigh<DT>(x, c2, shift2, sum, pk[1]);
                         }
                         tmem_st(t_s + part * 32, pk[0]);
                         tmem_st(t_s + part * 32 + 16, pk[1]);
@@ -713,37 +709,30 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const float norm = sum != 0.0f && some ? 1.0f / sum : 0.0f;
                 uint16_t *to = reinterpret_cast<uint16_t *>(P.out) + orow * P.D;
 #pragma unroll 1
-                for (int d0 = 0; d0 < C::DP; d0 += 32) {
-                    uint32_t a[32];
+                for (int d0 = 0; d0 < C::DP && d0 < P.D; d0 += 16) {
+                    uint32_t a[16];
                     tmem_ld(t_o + (uint32_t)d0, a);
                     if (!live)
                         continue;
                     if (!whole) {
-                        // [column][row]: a warp's store is one line
+                        // [column][row]: a warp's store is one line (columns past D have their room)
                         float *o = P.part + at * C::DP + d0 * BM + r;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (d0 + j < P.D)
-                                o[j * BM] = some ? __uint_as_float(a[j]) : 0.0f;
+                        for (int j = 0; j < 16; ++j)
+                            o[j * BM] = some ? __uint_as_float(a[j]) : 0.0f;
                         continue;
                     }
-                    uint32_t u[16];
+                    uint32_t u[8];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
+                    for (int j = 0; j < 8; ++j)
                         u[j] = norm != 0.0f ? pack<DT>(__uint_as_float(a[2 * j]) * norm,
                                                        __uint_as_float(a[2 * j + 1]) * norm) : 0u;
                     if (P.wide_rows) {
-                        // a lane's store is a whole sector of its row
-#pragma unroll
-                        for (int j = 0; j < 32; j += 16)
-                            if (d0 + j < P.D)
-                                store32(to + d0 + j, u + j / 2);
+                        store32(to + d0, u);  // a lane's store is a whole sector of its row
                     } else {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 8)
-                            if (d0 + j < P.D)
-                                *reinterpret_cast<uint4 *>(to + d0 + j) =
-                                    make_uint4(u[j / 2], u[j / 2 + 1], u[j / 2 + 2], u[j / 2 + 3]);
+                        *reinterpret_cast<uint4 *>(to + d0) = make_uint4(u[0], u[1], u[2], u[3]);
+                        if (d0 + 8 < P.D)
+                            *reinterpret_cast<uint4 *>(to + d0 + 8) = make_uint4(u[4], u[5], u[6], u[7]);
                     }
                 }
                 if (live) {
