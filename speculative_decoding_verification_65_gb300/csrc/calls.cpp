@@ -353,6 +353,7 @@ PyObject *keep(PyObject *, PyObject *given)
 // workspace(kind, device, stream, address, bytes): this thread's, from now on.
 PyObject *workspace(PyObject *, PyObject *given)
 {
+    HANDLE_TH_ERRORS
     int kind, device;
     unsigned long long stream, at, bytes;
     if (!PyArg_ParseTuple(given, "iiKKK", &kind, &device, &stream, &at, &bytes))
@@ -372,6 +373,7 @@ PyObject *workspace(PyObject *, PyObject *given)
     w->at = reinterpret_cast<void *>((uintptr_t)at);
     w->bytes = (size_t)bytes;
     Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
 }
 
 // setup(error class, address of spec_verify_strerror)
