@@ -11,10 +11,10 @@
 // The last CTA of a sequence joins its rows' totals and merges the sorted lists of all segments: the
 // n-th best head bounds the result, so at most n lists have entries in it; those are sorted.
 // Bound by the bytes of the logits, and by what comes behind them when all segments end at one
-// time: 64 x 8 rows of 128256 bf16 (440 of them live, 113 MB) are read by 28 us (4.2 TB/s), their best are
-// chosen by 32 and merged by 39; 32 x 5 rows of 151936 fp32 (83 MB) by 20, 25 and 33.  More bytes in
-// flight (rings in shared memory, prefetches into L2) did not shorten the reading: 42 us
-// became 44 to 46.
+// time: 64 x 8 rows of 128256 bf16 (440 of them live, 113 MB) are read by 22 us (half of them by 20, 5.6
+// TB/s), their best are chosen by 28 and merged by 34; 32 x 5 rows of 151936 fp32 (83 MB) by 17, 21
+// and 28.  More bytes in flight (rings in shared memory, prefetches into L2) did not shorten the reading,
+// nor did rows that begin at different places.
 //
 // Orders between beams hang on the difference of two logarithms of sums, which fp32 gives to a few
 // 1e-6.  Where two neighbours of different beams lie nearer than that, the sequence is listed,
@@ -837,7 +837,7 @@ bool sizes_ok(int32_t B, int32_t K, int32_t V, int32_t n, int32_t dtype)
 
 // Segments of a row: as many CTAs in all as run at a time (four per SM), each of which ends with some
 // us of choosing; no more groups than a thread has room for, and no fewer than one.  (64 x 8 rows of
-// 128256 bf16: in one segment 50 us, in three 68 us.)
+// 128256 bf16, before the reading was made faster: in one segment 50 us, in three 68 us.)
 int segments(int32_t B, int32_t K, int32_t V, int32_t dtype)
 {
     const long long rows = (long long)B * K;

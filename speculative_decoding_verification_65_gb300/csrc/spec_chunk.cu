@@ -23,11 +23,12 @@
 // TMEM: S_0, S_1 (128 columns each), O_0, O_1 (up to 128 each).
 //
 // Measured, GPU time with plan, append and join, 128 columns bf16: 8 x up to 1024 tokens behind up to 4096
-// positions, 32 heads on 8, 334 us, 1.15 PFLOP/s; 512 behind 96547, 40 on 8, 787 us, 1.45 PFLOP/s; 2 x
-// up to 8192, 64 on 8, 1546 us, 1.27 PFLOP/s.  A step of both row tiles over 128 keys all of whose
+// positions, 32 heads on 8, 329 us, 1.17 PFLOP/s; 512 behind 96547, 40 on 8, 782 us, 1.46 PFLOP/s; 2 x
+// up to 8192, 64 on 8, 1470 us, 1.34 PFLOP/s.  A step of both row tiles over 128 keys all of whose
 // keys are seen takes 2470 to 2740 clocks, of which the tensor pipe is at work 2144; the products of S
 // read 128 bytes of shared memory a clock, as many as there are, while TMA writes the next tiles.
-// A piece's start and end add some 12000 clocks: its first maxima, its masked tile, its stores.
+// A piece's start and end add some 10000 clocks: its first maxima, its masked tile, its stores, and the
+// instructions for them, which have left the caches in between.
 //
 // A row's sums are rescaled only when its maximum has grown by more than 2^8 (2^4 with fp16
 // weights) since the last time, so most tiles leave O in TMEM alone.
