@@ -261,6 +261,22 @@ __device__ void write_rows(const ForkParams &P, int r0)
     __shared__ int own[WARPS];      // pages that this CTA's rows take
     const spec_pages_fork_args &A = P.a;
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int M = A.pages_per_seq, r = r0 + warp;
+    // what does not hang on the sums is looked at before they are there
+    int state = ROW_ERROR, parent = -1, reserve = 0;
+    if (r < A.rows_out) {
+        state = got<SMALL>(P.w.state + r);
+        parent = __ldg(A.parent + r);
+        reserve = A.reserve ? __ldg(A.reserve + r) : 0;
+    }
+    Old o = {0, 0, true};
+    if (state == ROW_FIRST || state == ROW_OTHER)
+        o = old_row(A, parent);
+    Old given_up = {0, 0, false};  // an old row that nobody takes over
+    if (r < A.rows_in) {
+        given_up = old_row(A, r);
+        given_up.ok = given_up.ok && !has_child(A, r, given_up.length, A.rows_out);
+    }
     // pages that the rows before this CTA's take, and all rows
     long long before = 0, all = 0;
     if (tid < WARPS)
@@ -285,18 +301,14 @@ __device__ void write_rows(const ForkParams &P, int r0)
         all += part[w][1];
     }
     const bool enough = all <= sums[P.blocks];
-    const int M = A.pages_per_seq, r = r0 + warp;
     if (r < A.rows_out) {
         // -------------------------------------------------- a new row
-        const int state = enough ? got<SMALL>(P.w.state + r) : ROW_ERROR;
+        if (!enough)
+            state = ROW_ERROR;
         int32_t *row = A.table_out + (size_t)r * M;
         int src = -1, dst = -1, slots = 0, length = -1;
         if (state != ROW_ERROR) {
-            const int parent = __ldg(A.parent + r);
-            Old o = {0, 0, true};
-            if (state != ROW_EMPTY)
-                o = old_row(A, parent);
-            const int pages = pages_for(A, o.length, A.reserve ? __ldg(A.reserve + r) : 0);
+            const int pages = pages_for(A, o.length, reserve);
             const int whole = o.length / A.page_size, tail = o.length - whole * A.page_size;
             const int32_t *old = A.table_in + (size_t)max(parent, 0) * M;
             length = o.length;
@@ -353,13 +365,9 @@ __device__ void write_rows(const ForkParams &P, int r0)
             A.copies[2 * (size_t)A.rows_out + r] = slots;
         }
     }
-    if (r < A.rows_in && enough) {
-        // ------------------------------------ an old row that nobody takes over
-        const Old o = old_row(A, r);
-        if (o.ok && !has_child(A, r, o.length, A.rows_out))
-            for (int i = lane; i < o.held; i += 32)
-                atomicAdd(A.ref_out + __ldg(A.table_in + (size_t)r * M + i), -1);
-    }
+    if (given_up.ok && enough)
+        for (int i = lane; i < given_up.held; i += 32)
+            atomicAdd(A.ref_out + __ldg(A.table_in + (size_t)r * M + i), -1);
 }
 
 __global__ void __launch_bounds__(TH) fork_count_kernel(const __grid_constant__ ForkParams P)
