@@ -205,17 +205,22 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
     // compared (64: 1.5 us less than by the bound below; 128: 0.25 less; 150: 2.2 more)
     const bool few = lists * n <= FEW;
     const u64 mine = few && tid < lists * n ? fetch(tid / n, tid % n) : 0;
+    // (and so is what a row has of its own)
+    const bool own = tid < A.K;
+    const float norm = own && A.norm ? A.norm[b * A.K + tid] : 1.0f;
+    const float s = own ? A.scores[b * A.K + tid] : -INFINITY;
+    const bool fin = own && A.finished && A.finished[b * A.K + tid] != 0;
     // the rows' totals, a row per warp; what takes 64 bits for all rows at once, a row per lane (this
     // GPU has two 64-bit lanes per SM: by the warps one after the other it took 10 us)
     if (!EXACT)
         for (int k = warp; k < A.K; k += WARPS) {
             const size_t first = ((size_t)b * A.K + k) * P.segs;
-            const float s = A.scores[b * A.K + k];
-            if (!(s > -INFINITY) || (A.finished && A.finished[b * A.K + k] != 0))
-                continue;
             float2 x = make_float2(-INFINITY, 0.0f), y = x;
             if (lane < P.segs)
                 x = __ldcg(&P.stats[first + lane]);
+            if (!(A.scores[b * A.K + k] > -INFINITY) ||
+                (A.finished && A.finished[b * A.K + k] != 0))
+                continue;
             float top = x.x, z = 0.0f;
             bad |= isnan(x.x);
             for (int g = lane + 32; g < P.segs; g += 32) {
@@ -238,9 +243,7 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
                 S.total[k] = make_float2(top, z);
         }
     __syncthreads();
-    if (tid < A.K) {
-        const int row = b * A.K + tid;
-        const float s = A.scores[row], norm = A.norm ? A.norm[row] : 1.0f;
+    if (own) {
         bad |= isnan(s) || s == INFINITY;
         if (s > -INFINITY) {
             bad |= !(norm > 0.0f) || isinf(norm);
@@ -255,7 +258,6 @@ __device__ bool pick(const BeamParams &P, int b, PickSmem &S)
                 if (norm > 0.0f)
                     atomicMax(&S.widest, __float_as_int(__double2float_ru(S.inv[tid])));
                 // ln z = e ln 2 + ln m, m in [2/3, 4/3)
-                const bool fin = A.finished && A.finished[row] != 0;
                 const float2 x = fin ? make_float2(0.0f, 1.0f) : S.total[tid];
                 int e;
                 float m = frexpf(x.y, &e);
