@@ -32,6 +32,7 @@ SRCS = [os.path.join(CSRC, "spec_verify.cu"), os.path.join(CSRC, "spec_sample.cu
 DEPS = [os.path.join(CSRC, "device_common.cuh"), os.path.join(CSRC, "attn_plan.cuh"),
         os.path.join(CSRC, "attn_common.cuh"), os.path.join(CSRC, "chunk_plan.cuh"), os.path.join(CSRC, "internal.h"),
         os.path.join(CSRC, "resolve.cuh"), os.path.join(CSRC, "exp2_table.h"),
+        os.path.join(CSRC, "row_cut.h"),
         os.path.join(ROOT, "include", "spec_lmhead.h"),
         os.path.join(ROOT, "include", "spec_verify.h"),
         os.path.join(ROOT, "include", "spec_sample.h"),

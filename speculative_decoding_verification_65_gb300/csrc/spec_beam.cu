@@ -34,6 +34,7 @@
 #include "spec_verify.h"
 #include "device_common.cuh"
 #include "resolve.cuh"
+#include "row_cut.h"
 
 namespace {
 
@@ -411,14 +412,14 @@ struct Segment {
         const int V = P.a.V;
         base = P.a.logits;
         e0 = (size_t)row * V;
-        mis = (int)(e0 % L::VEC);  // elements of the row's first vector before it
         src = reinterpret_cast<const uint4 *>(base) + e0 / L::VEC;
-        const int f0 = mis > 0 ? 1 : 0, f1 = max(f0, (mis + V) / L::VEC);
-        const int per = (f1 - f0 + P.segs - 1) / P.segs;
-        v0 = f0 + seg * per;
-        v1 = min(f1, v0 + per);
-        head = mis > 0 ? min(V, L::VEC - mis) : 0;
-        tail = max(head, f1 * L::VEC - mis);
+        const RowCut cut = cut_row<L::VEC>(e0, V);
+        const int per = (cut.f1 - cut.f0 + P.segs - 1) / P.segs;
+        mis = cut.mis;  // elements of the row's first vector before it
+        v0 = cut.f0 + seg * per;
+        v1 = min(cut.f1, v0 + per);
+        head = cut.head;
+        tail = cut.tail;
         edges = seg == 0 ? head + V - tail : 0;
     }
     // (past L1, which holds no segment: 64 x 8 rows of 128256 bf16 40.4 -> 36.8 us, 32 x 5 of 151936
