@@ -36,6 +36,8 @@ extern "C" {
  *   norm      device float [B, K] or NULL (1)
  *   end_token in [0, V): the candidate of an ended beam
  *   out_tokens, out_beams  device int32 [B, n]; out_scores device float [B, n]: score(k, x)
+ *   No output shares memory with an input or another output (SPEC_EINVAL): where an order is open the
+ *   scores are read again after the outputs have been written.
  * 0 <= B <= 65535, 1 <= K, n <= SPEC_BEAM_MAX, 2 <= V <= SPEC_MAX_V.  The
  * workspace has spec_beam_workspace_size bytes (0 for sizes out of range),
  * 256-byte aligned, was zeroed once (spec_verify_workspace_reset does) and

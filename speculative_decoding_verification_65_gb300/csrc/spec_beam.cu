@@ -832,6 +832,33 @@ __global__ void __launch_bounds__(TH) reorder_kernel(const __grid_constant__ Reo
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
+// An output of a selection that shares a byte with an input or another output: CTAs read the scores
+// of sequences that others have finished with, and where an order is open a second time.
+bool outputs_apart(const spec_beam_select_args &a)
+{
+    struct Span {
+        const void *p;
+        uint64_t bytes;
+    };
+    const uint64_t rows = (uint64_t)a.B * a.K, each = (uint64_t)a.B * a.n * 4;
+    const Span in[] = {{a.logits, rows * a.V * (a.dtype == SPEC_F32 ? 4 : 2)}, {a.scores, rows * 4},
+                       {a.norm, rows * 4}, {a.finished, rows * 4}};
+    const Span out[] = {{a.out_tokens, each}, {a.out_beams, each}, {a.out_scores, each}};
+    auto apart = [](const Span &x, const Span &y) {
+        const uintptr_t i = reinterpret_cast<uintptr_t>(x.p), j = reinterpret_cast<uintptr_t>(y.p);
+        return !x.p || !y.p || i >= j + y.bytes || j >= i + x.bytes;
+    };
+    for (int o = 0; o < 3; ++o) {
+        for (const Span &x : in)
+            if (!apart(out[o], x))
+                return false;
+        for (int q = 0; q < o; ++q)
+            if (!apart(out[o], out[q]))
+                return false;
+    }
+    return true;
+}
+
 bool sizes_ok(int32_t B, int32_t K, int32_t V, int32_t n, int32_t dtype)
 {
     return B >= 0 && B <= 65535 && K >= 1 && K <= SPEC_BEAM_MAX && n >= 1 && n <= SPEC_BEAM_MAX &&
@@ -943,6 +970,8 @@ int32_t spec_beam_select(const spec_beam_select_args *args, void *workspace,
     const BeamLayout w = beam_layout(a.B, a.K, a.V, a.n, a.dtype);
     if (workspace_bytes < w.total)
         return SPEC_ENOSPACE;
+    if (!outputs_apart(a))
+        return SPEC_EINVAL;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     BeamParams P;
     P.a = a;
