@@ -73,7 +73,7 @@ def link_command(objs, out: str) -> list:
 def calls_command(out: str):
     """None without PyTorch (which is looked for, not imported)."""
     spec = importlib.util.find_spec("torch")
-    if spec is None:
+    if spec is None or not spec.submodule_search_locations:
         return None
     torch = spec.submodule_search_locations[0]
     lib = os.path.join(torch, "lib")
@@ -110,35 +110,54 @@ def _run(cmd, verbose):
     return res.returncode
 
 
-def build_calls(command, tag, verbose):
-    if _run(command, verbose):
-        raise RuntimeError("g++ failed compiling csrc/calls.cpp")
-    os.replace(CALLS + tag, CALLS)
+def build_calls(tag: str, verbose: bool) -> bool:
+    """Compile the binding's short way.  Where that does not work (a PyTorch without CUDA or without
+    headers, no Python.h, no g++) a line says so, an old one is taken away, and calls go through Python:
+    the library does not hang on it."""
+    tmp = CALLS + tag
+    try:
+        command = calls_command(tmp)
+        if command is None:
+            return False
+        res = subprocess.run(command, capture_output=True, text=True)
+        if verbose:
+            print(" ".join(command), res.stdout, res.stderr, sep="\n")
+        if res.returncode == 0:
+            os.replace(tmp, CALLS)
+            return True
+        errors = [x for x in res.stderr.splitlines() if "error" in x] or res.stderr.splitlines()
+        why = errors[0] if errors else f"g++ ended with {res.returncode}"
+    except OSError as error:  # no g++
+        why = str(error)
+    for path in (tmp, CALLS):
+        if os.path.exists(path):
+            os.remove(path)
+    print(f"_calls.so is left out, calls go through Python: {why}")
+    return False
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     """Compile the CUDA library if it is missing or older than its sources, and the binding's
     short way into it likewise."""
     tag = f".tmp{os.getpid()}"
-    calls = calls_command(CALLS + tag) if force or calls_stale() else None
+    calls = force or calls_stale()
     if not force and not stale() and not extra:
         if calls:
-            build_calls(calls, tag, verbose)
+            build_calls(tag, verbose)
         return LIB
     objs = [os.path.join(CSRC, os.path.basename(s) + tag + ".o") for s in SRCS]
     try:
         with ThreadPoolExecutor(len(SRCS) + 1) as ex:
-            short = ex.submit(build_calls, calls, tag, verbose) if calls else None
+            if calls:
+                ex.submit(build_calls, tag, verbose)
             rcs = list(ex.map(lambda so: _run(compile_command(so[0], so[1], extra), verbose),
                               zip(SRCS, objs)))
-        if any(rcs):
-            raise RuntimeError("nvcc failed compiling the CUDA sources")
-        if short:
-            short.result()
-        tmp = LIB + tag
-        if _run(link_command(objs, tmp), verbose):
-            raise RuntimeError("nvcc failed linking libspecverify.so")
-        os.replace(tmp, LIB)
+            if any(rcs):
+                raise RuntimeError("nvcc failed compiling the CUDA sources")
+            tmp = LIB + tag
+            if _run(link_command(objs, tmp), verbose):
+                raise RuntimeError("nvcc failed linking libspecverify.so")
+            os.replace(tmp, LIB)
     finally:
         for o in objs:
             if os.path.exists(o):
