@@ -1487,10 +1487,12 @@ _AS_ARGS, _WITH_WORKSPACE, _AS_REORDER, _AS_PLAN = range(4)
 
 
 def _load_calls():
-    """The module; without it every call goes the long way."""
+    """The module; without one that was compiled for this PyTorch every call goes the long way."""
     global _short, _run
     if _short is None:
         try:
+            if not importlib.import_module(".build", __name__).calls_match():
+                raise ImportError("_calls.so is none, or another PyTorch's")
             module = importlib.import_module("._calls", __name__)
         except ImportError:
             _short = False

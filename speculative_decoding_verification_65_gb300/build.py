@@ -46,7 +46,9 @@ DEPS = [os.path.join(CSRC, "device_common.cuh"), os.path.join(CSRC, "attn_plan.c
 SRC = SRCS[0]
 LIB = os.path.join(PKG, "libspecverify.so")
 CALLS_SRC = os.path.join(CSRC, "calls.cpp")
+CALLS_HEADER = os.path.join(ROOT, "include", "spec_verify.h")
 CALLS = os.path.join(PKG, "_calls.so")
+CALLS_FOR = CALLS + ".for"  # what it was compiled for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -94,11 +96,35 @@ def stale() -> bool:
     return any(os.path.getmtime(p) > t for p in (*SRCS, *DEPS, __file__))
 
 
-def calls_stale() -> bool:
-    if importlib.util.find_spec("torch") is None:
+def calls_made_for():
+    """What _calls.so depends on besides its sources: PyTorch (whose C++ headers it is compiled
+    against, inline functions and all) and this Python.  None without PyTorch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        return None
+    torch = spec.submodule_search_locations[0]
+    try:
+        with open(os.path.join(torch, "version.py")) as f:
+            version = f.read()
+    except OSError:
+        version = ""
+    return "\n".join((torch, version, sysconfig.get_config_var("SOABI") or "", ""))
+
+
+def calls_match() -> bool:
+    """Whether _calls.so was compiled for this PyTorch and Python."""
+    try:
+        with open(CALLS_FOR) as f:
+            return os.path.exists(CALLS) and f.read() == calls_made_for()
+    except OSError:
         return False
-    return not os.path.exists(CALLS) or any(os.path.getmtime(p) > os.path.getmtime(CALLS)
-                                            for p in (CALLS_SRC, __file__))
+
+
+def calls_stale() -> bool:
+    if calls_made_for() is None:
+        return False
+    return not calls_match() or any(os.path.getmtime(p) > os.path.getmtime(CALLS)
+                                    for p in (CALLS_SRC, CALLS_HEADER, __file__))
 
 
 def _run(cmd, verbose):
@@ -123,13 +149,19 @@ def build_calls(tag: str, verbose: bool) -> bool:
         if verbose:
             print(" ".join(command), res.stdout, res.stderr, sep="\n")
         if res.returncode == 0:
+            with open(tmp + ".for", "w") as f:
+                f.write(calls_made_for())
+            # (in this order: a build that is cut off between leaves none that passes for this one)
+            if os.path.exists(CALLS_FOR):
+                os.remove(CALLS_FOR)
             os.replace(tmp, CALLS)
+            os.replace(tmp + ".for", CALLS_FOR)
             return True
         errors = [x for x in res.stderr.splitlines() if "error" in x] or res.stderr.splitlines()
         why = errors[0] if errors else f"g++ ended with {res.returncode}"
     except OSError as error:  # no g++
         why = str(error)
-    for path in (tmp, CALLS):
+    for path in (tmp, tmp + ".for", CALLS_FOR, CALLS):
         if os.path.exists(path):
             os.remove(path)
     print(f"_calls.so is left out, calls go through Python: {why}")
