@@ -423,13 +423,15 @@ struct Segment {
         edges = seg == 0 ? head + V - tail : 0;
     }
     // (past L1, which holds no segment: 64 x 8 rows of 128256 bf16 40.4 -> 36.8 us, 32 x 5 of 151936
-    // fp32 32.5 -> 30.3, with inputs that L2 does not hold)
+    // fp32 32.5 -> 30.3, with inputs that L2 does not hold.  Volatile and with a clobber: without, the
+    // compiler may take it for arithmetic on the address and move it before the wait for the kernel that
+    // writes the logits.  That costs nothing: 37.4 us either way, and 30.6.)
     __device__ __forceinline__ uint4 fetch(int v) const
     {
         uint4 r = neg_inf_vec(L::NEG_INF_WORD);
         if (v < v1)
-            asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(src + v));
+            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(src + v) : "memory");
         return r;
     }
     __device__ __forceinline__ int col(int v, int j) const { return v * L::VEC + j - mis; }
