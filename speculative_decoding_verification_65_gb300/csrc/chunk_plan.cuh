@@ -50,4 +50,18 @@ __host__ __device__ inline ChunkLayout chunk_layout(int B, int rows, int group)
     return p;
 }
 
+// Where an item's tiles are those of more than one share, whole tiles are taken in an order by the
+// time: tile t of the item when the CTA has taken t more than a multiple of a share's tiles.  CTAs
+// that read the same keys for other rows then read them at one time, once from DRAM: from the first
+// tile on, each at a place of its own, 512 tokens behind 131072 positions read 11 times the cache, as
+// fast as DRAM gives it.  The first of them for a piece that begins at tile `tile` of `tiles` when
+// the CTA has taken `taken` units; `per` units are a share, none where no sequence has rows.
+__host__ __device__ inline int piece_turn(long long taken, int tile, int tiles, long long per)
+{
+    if (per <= 0 || tiles < per)
+        return 0;
+    const long long turn = (taken - tile) % per;
+    return (int)(turn < 0 ? turn + per : turn);
+}
+
 }  // namespace spec_attn

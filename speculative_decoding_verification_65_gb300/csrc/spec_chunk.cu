@@ -257,16 +257,7 @@ struct Walk {
         p.n = left <= 0 ? 0 : p.tiles - q.tile < left ? p.tiles - q.tile : (int)left;
         p.idle = q.x.bad | (q.status != 0);
         p.first = u - q.tile <= u0;
-        // Where an item's tiles are those of more than one share, whole tiles are taken in an order
-        // by the time: tile t of the item when the CTA has taken t more than a multiple of a share's
-        // tiles.  CTAs that read the same keys for other rows then read them at one time,
-        // once from DRAM: from the first tile on, each at a place of its own, 512 tokens
-        // behind 131072 positions read 11 times the cache, as fast as DRAM gives it.
-        p.turn = 0;
-        if (p.tiles >= per) {
-            const long long turn = (u - u0 - q.tile) % per;
-            p.turn = (int)(turn < 0 ? turn + per : turn);
-        }
+        p.turn = piece_turn(u - u0, q.tile, p.tiles, per);
         return p;
     }
     // to the piece behind this one of n tiles
