@@ -83,10 +83,13 @@ struct Cfg {
     static constexpr int DP = NP * PANEL;  // columns of O
 };
 // Stages are taken in the order of the CTA's tiles.  A wait for a phase of a barrier tells it from
-// the phase before only if that one is known to be over (parity), so whoever waits on a stage has
-// gone through its earlier phases: the loader and the issuer wait for all of them, and a softmax
-// group that looks at V waits for its tile's scores first, which the issuer's products of every
-// earlier tile precede.
+// the phase before only if that one is known to be over (parity).  The loader and the warp that waits
+// for the issuer's tiles wait for all phases of a stage.  A softmax group waits only for the V of masked
+// tiles, and before it waits for that tile's scores.  It has had the scores of tile c - 1 by then, which
+// the products with V of tile c - 2 precede, or, in a piece's first tile, the last products of the
+// piece before, with V of tile c - 1.  So V of tile c - 2 has landed, and a stage of V must not be
+// taken again sooner than two tiles later.
+static_assert(Cfg<1>::VST >= 2 && Cfg<2>::VST >= 2, "a group may wait for V two tiles ahead");
 
 // A run of one item's key tiles inside a CTA's share.
 struct Piece {
