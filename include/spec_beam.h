@@ -11,8 +11,8 @@
  * The comparison is that of 64 bits: where fp32 statistics of two beams leave an
  * order open, the beams' sums are taken again exactly.
  *
- * Candidates with a logit of -inf, and all of a beam at s_k = -inf (whose logits
- * are not read), do not count; where fewer than n are left, tokens and beams are
+ * Candidates with a logit of -inf, and all of a beam at s_k = -inf, do not count (logits
+ * of such a beam, and of one that has ended, are not read); where fewer than n are left, tokens and beams are
  * -1 and scores -inf.  A sequence with a NaN or +inf logit in a row that counts, a
  * NaN or +inf s_k or a norm that is not positive and finite is in error: tokens and beams -1,
  * scores NaN.

@@ -537,14 +537,16 @@ __global__ void __launch_bounds__(TH, 4) beam_kernel(const __grid_constant__ Bea
     const int b = row / A.K, n = A.n;
     allow_next_kernel();
     wait_previous_kernel();
-    // (the first group is on its way before it is known whether the beam counts)
     const Segment<DT> G(P, row, seg);
     uint4 raw[UN], ahead[UN];
-#pragma unroll
-    for (int u = 0; u < UN; ++u)
-        raw[u] = G.fetch(G.v0 + u * TH + tid);
+    // Logits of a beam that has ended or does not exist are not read.  (To have the first group on its way
+    // before that is known took 0.4 us less of 31 on 32 x 5 rows of 151936 fp32, 0.1 of 37.5 on
+    // 64 x 8 of 128256 bf16.)
     const bool counts = A.scores[row] > -INFINITY && !(A.finished && A.finished[row] != 0);
     if (counts) {
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+            raw[u] = G.fetch(G.v0 + u * TH + tid);
         float *maxima = reinterpret_cast<float *>(dyn) + tid;  // of the thread's groups
         float m = -INFINITY, top = -INFINITY, sum = 0.0f, low = 0.0f;  // sum + low in units of e^m
         bool bad = false;
