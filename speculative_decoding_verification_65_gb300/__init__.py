@@ -1887,6 +1887,11 @@ def spec_beam_reorder(state, beams, dim=0, out=None, stream=None):
         if got is not None:
             return got
     torch = _torch()
+    if state.dtype.is_complex:  # a view may stand for other numbers than its memory holds
+        with torch.cuda.stream(stream):
+            state = state.resolve_conj().resolve_neg()
+        if out is not None and (out.is_conj() or out.is_neg()):
+            raise ValueError("out must not be a conjugated or negated view")
 
     def check():
         if not 0 <= dim <= state.dim() - 2 or beams.dim() != 2:

@@ -158,7 +158,7 @@ bool make_key(PyObject *const *a, Py_ssize_t n)
         if (!THPVariable_CheckExact(a[i]))
             return false;
         const at::Tensor &t = THPVariable_Unpack(a[i]);
-        if (!t.is_cuda() || t.layout() != at::kStrided)
+        if (!t.is_cuda() || t.layout() != at::kStrided || t.is_conj() || t.is_neg())
             return false;
         key.push_back('t');
         key.push_back((char)t.scalar_type());
