@@ -90,6 +90,8 @@ int32_t spec_chunk_plan(const int32_t *row_start, const int32_t *kv_len, const i
  *   plan    spec_chunk_plan's, of the same B, rows, G and cache geometry
  *   out     [rows, Hq, D] contiguous, of q's dtype
  *   out_lse float [rows, Hq] or NULL: ln sum_j exp(scale * q . k_j)
+ * out may be q itself, where that is contiguous; otherwise the outputs share no memory with the
+ * inputs (by their extents, strides included) or each other (SPEC_EINVAL).
  * dtype SPEC_BF16 or SPEC_F16, one for all tensors.  D a multiple of 8 up to
  * SPEC_ATTN_MAX_HEAD_DIM, Hq a multiple of Hkv, Hq / Hkv <= 128, scale finite
  * and positive; page_size a multiple of 128, or a power of two from 8, or,

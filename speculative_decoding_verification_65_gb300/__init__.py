@@ -1742,9 +1742,9 @@ def spec_chunk_attention(q, k_cache, v_cache, plan, page_table=None, scale=None,
     float16, any strides with a contiguous last dimension; plan from
     spec_chunk_plan; page_table int32 [B, pages_per_seq] or None; scale
     1 / sqrt(D) by default; ws of one call at a time, by default this thread's.
-    Returns out [rows, Hq, D] and, with want_lse, the rows' log-sum-exp float32
-    [rows, Hq]; rows of no sequence are left as they are.  Asynchronous like
-    any CUDA op."""
+    Returns out [rows, Hq, D] (`out` may be a contiguous q, and shares no memory with other inputs)
+    and, with want_lse, the rows' log-sum-exp float32 [rows, Hq]; rows of no sequence are left as they
+    are.  Asynchronous like any CUDA op."""
     plain = scale is None and out is None and not want_lse and ws is None and stream is None
     if _run and plain:
         got = _run(_ATTEND, plan.code, 0, q, k_cache, v_cache, plan.data, page_table)

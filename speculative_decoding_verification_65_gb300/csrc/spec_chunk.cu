@@ -1244,6 +1244,39 @@ size_t spec_chunk_attention_workspace_size(int32_t Hq, int32_t Hkv, int32_t D)
     return heads_ok(Hq, Hkv, D) ? ws_layout(D).total : 0;
 }
 
+// Whether an output shares memory with an input, by their extents, or with the other.  (out may be q
+// itself: an item's queries are read by its own CTAs, which write its rows afterwards, the rows of split
+// items by the join behind them all; what a box reads past a group's rows has no effect.)
+static bool outputs_apart(const spec_chunk_attention_args &a, size_t plan_bytes)
+{
+    struct Span {
+        const void *p;
+        uint64_t bytes;
+    };
+    auto strided = [&](int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2, int64_t s2) {
+        return 2 * (uint64_t)((n0 - 1) * s0 + (n1 - 1) * s1 + (n2 - 1) * s2 + a.D);
+    };
+    auto cache = [&](const int64_t (&s)[3]) {
+        return a.num_pages < 1 ? 0 : strided(a.num_pages, s[0], a.page_size, s[1], a.Hkv, s[2]);
+    };
+    auto apart = [](const Span &x, const Span &y) {
+        const uintptr_t i = reinterpret_cast<uintptr_t>(x.p), j = reinterpret_cast<uintptr_t>(y.p);
+        return !x.p || !y.p || i >= j + y.bytes || j >= i + x.bytes;
+    };
+    const bool in_place = a.out == a.q && (a.rows == 1 || a.q_stride[0] == (int64_t)a.Hq * a.D) &&
+                          (a.Hq == 1 || a.q_stride[1] == a.D);
+    const Span in[] = {
+        {a.q, in_place ? 0 : strided(a.rows, a.q_stride[0], a.Hq, a.q_stride[1], 1, 0)},
+        {a.k_cache, cache(a.k_cache_stride)}, {a.v_cache, cache(a.v_cache_stride)},
+        {a.plan, plan_bytes}, {a.page_table, (uint64_t)a.B * a.pages_per_seq * 4}};
+    const uint64_t heads = (uint64_t)a.rows * a.Hq;
+    const Span out = {a.out, heads * a.D * 2}, lse = {a.out_lse, heads * 4};
+    for (const Span &x : in)
+        if (!apart(out, x) || !apart(lse, x))
+            return false;
+    return apart(out, lse);
+}
+
 static int32_t attend(const spec_chunk_attention_args *args, void *workspace,
                       size_t workspace_bytes, int lose, int lose_after, void *stream)
 {
@@ -1280,10 +1313,12 @@ static int32_t attend(const spec_chunk_attention_args *args, void *workspace,
     const WsLayout w = ws_layout(a.D);
     if (workspace_bytes < w.total)
         return SPEC_ENOSPACE;
+    const int32_t G = a.Hq / a.Hkv;
+    if (!outputs_apart(a, chunk_layout(a.B, a.rows, G).total))
+        return SPEC_EINVAL;
 
     KParams P;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const int32_t G = a.Hq / a.Hkv;
     P.plan = static_cast<const uint8_t *>(a.plan);
     P.lay = chunk_layout(a.B, a.rows, G);
     P.page_table = a.page_table;
