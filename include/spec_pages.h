@@ -48,7 +48,9 @@ extern "C" {
  * outside [0, num_pages)) keeps its references.  Where the free pages do not
  * suffice, every row is in error, and ref_out is ref_in.
  * 0 <= rows_in, rows_out <= 65535, 0 <= num_pages <= SPEC_PAGES_MAX, pages_per_seq * page_size <
- * 2^31.  The workspace has spec_pages_workspace_size bytes (0 for sizes out of range), 256-byte
+ * 2^31.  Rows look for one another in `parent`, so the time grows with the square of
+ * their number where there are many (512 rows: 19 us, 65535: 1.8 ms).  The
+ * workspace has spec_pages_workspace_size bytes (0 for sizes out of range), 256-byte
  * aligned, need not be cleared and belongs to one call at a time.  One or two kernels
  * on `stream`, no allocation.
  */

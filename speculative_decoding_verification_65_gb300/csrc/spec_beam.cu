@@ -871,7 +871,7 @@ bool sizes_ok(int32_t B, int32_t K, int32_t V, int32_t n, int32_t dtype)
 
 // Segments of a row: as many CTAs in all as run at a time (four per SM), each of which ends with some
 // us of choosing; no more groups than a thread has room for, and no fewer than one.  (64 x 8 rows of
-// 128256 bf16, before the reading was made faster: in one segment 50 us, in three 68 us.)
+// 128256 bf16 with the reordering: in one segment 37.4 us, in two 43.0, in three 47.9.)
 int segments(int32_t B, int32_t K, int32_t V, int32_t dtype)
 {
     const long long rows = (long long)B * K;
