@@ -1253,10 +1253,10 @@ static bool outputs_apart(const spec_chunk_attention_args &a, size_t plan_bytes)
         const void *p;
         uint64_t bytes;
     };
-    auto strided = [&](int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2, int64_t s2) {
-        return 2 * (uint64_t)((n0 - 1) * s0 + (n1 - 1) * s1 + (n2 - 1) * s2 + a.D);
+    auto strided = [&](uint64_t n0, uint64_t s0, uint64_t n1, uint64_t s1, uint64_t n2, uint64_t s2) {
+        return 2 * ((n0 - 1) * s0 + (n1 - 1) * s1 + (n2 - 1) * s2 + (uint64_t)a.D);
     };
-    auto cache = [&](const int64_t (&s)[3]) {
+    auto cache = [&](const int64_t (&s)[3]) -> uint64_t {
         return a.num_pages < 1 ? 0 : strided(a.num_pages, s[0], a.page_size, s[1], a.Hkv, s[2]);
     };
     auto apart = [](const Span &x, const Span &y) {
